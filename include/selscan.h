@@ -486,14 +486,157 @@ typedef struct {
 ss_status ss_step_layers(const ss_step_layer* layers, int64_t n_layers, int64_t batch, int64_t Dm, int64_t N,
                          const ss_step_strides* strides, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Serving a stack of multi-head state space layers: the scan with one decay per head and its
+ * short causal convolution in one call, for packed prompts (ss_heads_fwd) and for one token of
+ * every request (ss_heads_step), both on a pool of cached states; the residual norm before a
+ * layer with outputs in 8 bits (ss_add_rmsnorm, ss_add_rmsnorm_f8); and the choice of the next
+ * token (ss_sample).  The pages have no counterpart of these calls; the recurrence is theirs
+ * ("mamba-metal: Apple Silicon で Mamba を動かす", section "Selective scan の本質") with a decay
+ * shared by the P channels and N states of a head.
+ * ------------------------------------------------------------------------------------------ */
+
+/* Largest head width P and state count N of the multi-head scan. */
+#define SS_HEADS_MAX 256
+
+/*
+ * Element strides between tokens of the multi-head scan's tensors (channel stride 1).  NULL
+ * means io_dtype = SS_F32 and every tensor contiguous.  The strides let the call read z, xbc and
+ * dt_raw as column ranges of one projection's output.
+ */
+typedef struct {
+    int32_t io_dtype;
+    int64_t xbc_t;                          /* xbc    [tokens, C], C = H·P + 2·G·N */
+    int64_t dt_t;                           /* dt_raw [tokens, H]   */
+    int64_t z_t;                            /* z      [tokens, H·P] (ignored if z NULL) */
+    int64_t y_t;                            /* y      [tokens, H·P] */
+} ss_heads_strides;
+
+/*
+ * Multi-head selective scan with its causal convolution, over packed prompts.
+ * For every sequence, with e = its window ++ its rows of xbc, channel c, head h of group
+ * g = h / (H/G):
+ *   v_t[c]   = conv_b[c] + Σ_{k<4} conv_w[c,k] · e[t + k][c],   (x | B | C)_t = silu(v_t),
+ *              x [H,P] the first H·P channels, then B [G,N], then C [G,N]
+ *   Δ_t[h]   = softplus(dt_raw[t,h] + dt_bias[h])
+ *   S_t[h]   = exp(-Δ_t exp(A_log[h])) · S_{t-1}[h] + Δ_t · x_t[h] ⊗ B_t[g]      (P × N)
+ *   y_t[h,p] = (Σ_n S_t[h,p,n] C_t[g,n] + D[h] x_t[h,p]) · silu(z_t[h,p])
+ *   xbc, dt_raw, z, y   io_dtype, strides above; z NULL: no gate.  y must not overlap an input;
+ *                       its rows must not run into each other.  Rows that no sequence covers are
+ *                       left as they are.
+ *   conv_w [C,4], conv_b [C] or NULL (= 0), dt_bias [H] or NULL, A_log [H], D [H] or NULL: fp32
+ *   state  [n_slots, H, P, N] fp32 contiguous, window [n_slots, C, 3] fp32 contiguous (oldest
+ *                       sample first): the caches, updated in place
+ *   cu_seqlens [n_seq+1] int32, device: sequence i is rows cu_seqlens[i] .. cu_seqlens[i+1]-1
+ *                       (any length from 0; an empty sequence leaves its starting state)
+ *   slots  [n_seq] int32, device, or NULL (sequence i uses slot i): where the sequence's state
+ *                       and window are.  A negative slot: the sequence starts from zeros and
+ *                       leaves nothing.  No two sequences may share a slot.
+ *   fresh  [n_seq] int32, device, or NULL (= 0): non-zero starts the sequence from zeros instead
+ *                       of its slot's contents (which may then hold anything, NaN included)
+ *   A slot of n_slots or more, or rows outside 0 .. tokens, set bit 2 of the device error word
+ *   and that sequence is skipped.
+ *   P, N in 1..SS_HEADS_MAX, G divides H.  n_seq == 0 or tokens == 0 with n_seq == 0 is a no-op.
+ *   workspace           device memory, 256-byte aligned, ss_heads_workspace_size(...) bytes,
+ *                       zero-filled before its first use (never again).  Calls that share it must
+ *                       not run concurrently on the device.
+ * Arithmetic, sums and the state are fp32.  Errors as ss_fwd.
+ */
+ss_status ss_heads_fwd(const void* xbc, const void* dt_raw, const void* z, const float* conv_w,
+                       const float* conv_b, const float* dt_bias, const float* A_log, const float* D,
+                       void* y, float* state, float* window, const int32_t* cu_seqlens,
+                       const int32_t* slots, const int32_t* fresh, int64_t n_seq, int64_t tokens,
+                       int64_t H, int64_t P, int64_t G, int64_t N, int64_t n_slots,
+                       const ss_heads_strides* strides, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/* Workspace bytes ss_heads_fwd needs (0: sizes invalid or empty). */
+size_t ss_heads_workspace_size(int64_t n_seq, int64_t tokens, int64_t H, int64_t P, int64_t G,
+                               int64_t N, int32_t io_dtype);
+
+/*
+ * One token of every request: ss_heads_fwd on `batch` sequences of one token each, row b of xbc
+ * being request b's token, continuing from its slot.  A negative slot starts from zeros and
+ * leaves nothing (a padded row of a fixed-size batch); a slot of n_slots or more sets bit 2 of
+ * the device error word, and its y row is left as it is.  y and the window shift agree with
+ * ss_heads_fwd's up to rounding.  Workspace: ss_heads_step_workspace_size(batch, G) bytes, as above.
+ */
+ss_status ss_heads_step(float* state, float* window, const void* xbc, const void* dt_raw, const void* z,
+                        const float* conv_w, const float* conv_b, const float* dt_bias,
+                        const float* A_log, const float* D, void* y, const int32_t* slots,
+                        int64_t batch, int64_t H, int64_t P, int64_t G, int64_t N, int64_t n_slots,
+                        const ss_heads_strides* strides, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/* Workspace bytes ss_heads_step needs (0: sizes invalid or empty). */
+size_t ss_heads_step_workspace_size(int64_t batch, int64_t G);
+
+/* Widest row the norm takes. */
+#define SS_NORM_MAX 16384
+
+/* Element strides between rows of the norm's tensors (column stride 1) and their types. */
+typedef struct {
+    int32_t io_dtype;                       /* x, and y of ss_add_rmsnorm */
+    int32_t res_dtype;                      /* residual, residual_out */
+    int64_t x_r, res_r, res_out_r, y_r;
+} ss_norm_strides;
+
+/*
+ * Residual addition and root-mean-square norm over rows of D columns:
+ *   r = x + residual (x alone if residual is NULL),  residual_out = r (rounded once to its type)
+ *   y = r / sqrt(mean(r²) + eps) · weight            (from the unrounded r; sums in fp32)
+ *   residual_out may be residual itself (same stride) or NULL; outputs must not overlap otherwise.
+ *   weight [D] fp32.  D in 1..SS_NORM_MAX.  strides NULL: fp32, contiguous.
+ */
+ss_status ss_add_rmsnorm(const void* x, const void* residual, const float* weight, void* residual_out,
+                         void* y, int64_t rows, int64_t D, float eps, const ss_norm_strides* strides,
+                         void* stream);
+
+/*
+ * The same with y in 8 bits (e4m3) and fp32 scales, the input of an 8-bit projection:
+ *   scale[r, j] = max(max |y|, 1e-30) / 448 over columns j·block .. of row r,  y8 = e4m3(y / scale)
+ *   block           0 (one scale per row) or 32, 64, 128, 256 columns per scale; the last block of
+ *                   a row may be short
+ *   y8              [rows, D] bytes, row stride y_r;  scale [rows, ceil(D/block)] fp32 contiguous
+ * A block in which some y is NaN (a row with a NaN or an infinity) has a NaN scale and NaN codes.
+ */
+ss_status ss_add_rmsnorm_f8(const void* x, const void* residual, const float* weight, void* residual_out,
+                            uint8_t* y8, float* scale, int64_t rows, int64_t D, int64_t block, float eps,
+                            const ss_norm_strides* strides, void* stream);
+
+/* Largest vocabulary ss_sample takes. */
+#define SS_SAMPLE_MAX (1 << 20)
+
+/*
+ * Next tokens from logits and given random numbers.  Per row, with l = logits (NaN read as -inf,
+ * +inf as the largest finite number) in decreasing order, equal ones by increasing index, and
+ * w = exp((l - l_max) / temperature):
+ *   1. top_k:  the first top_k tokens stay (top_k <= 0: all)
+ *   2. top_p:  of those, the tokens before which less than top_p of their whole weight lies stay
+ *              (top_p >= 1: all)
+ *   3. min_p:  of those, the tokens with w >= min_p stay.  The first token always stays.
+ *   token = argmax over what stays of w / noise, the lowest index among equals: with noise drawn
+ *   from the exponential distribution of mean 1 a draw from the weights (an exponential race).
+ *   temperature <= 0: the largest logit, the lowest index among equals.
+ *   logits [rows, V] io_dtype, noise [rows, V] fp32, positive; row strides in elements
+ *   temperature, top_p, min_p [rows] fp32, top_k [rows] int32, device, each NULL for its default
+ *   (1, 1, 0, 0);  tokens [rows] int32: the row's token, -1 where every logit is -inf or NaN.
+ * V in 1..SS_SAMPLE_MAX.  Deterministic: equal inputs give equal tokens.  The weights' sums for
+ * top_p are taken in steps of 2^-31 of the largest weight.
+ */
+ss_status ss_sample(const void* logits, const float* noise, const float* temperature, const int32_t* top_k,
+                    const float* top_p, const float* min_p, int32_t* tokens, int64_t rows, int64_t V,
+                    int32_t io_dtype, int64_t logits_r, int64_t noise_r, void* stream);
+
 /* Static, human-readable name of a status code. */
 const char* ss_status_string(ss_status status);
 
 /*
  * Read (and, if `clear` is non-zero, reset) the device error word of the current
  * device: bit 0 = a kernel gave up waiting for a TMA tile; bit 1 = a kernel was launched
- * with a tile geometry other than its own and did nothing.  Either way that call's outputs
- * are invalid.
+ * with a tile geometry other than its own and did nothing; either way that call's outputs
+ * are invalid.  Bit 2 = a slot or a row range read from device memory was out of range, and the
+ * sequence or request it belongs to was skipped.
  * Synchronises with the device.  Returns SS_ERR_CUDA if the word cannot be read.
  */
 ss_status ss_device_error(uint32_t* bits, int clear);

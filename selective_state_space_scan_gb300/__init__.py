@@ -13,7 +13,9 @@ from typing import Optional
 from . import _build
 
 __all__ = ["ss_fwd", "ss_fwd_ckpt", "ss_fwd_dtproj", "ss_fwd_host", "ss_step", "ss_step_layers", "ss_fwd_summary", "ss_carry_compose", "ss_conv1d", "ss_bwd", "ss_fwd_workspace_size", "SelscanError", "lib", "device_error",
-           "version", "status_string", "SS_F32", "SS_BF16", "FwdStrides", "StepStrides", "ConvStrides"]
+           "version", "status_string", "SS_F32", "SS_BF16", "FwdStrides", "StepStrides", "ConvStrides",
+           "ss_heads_fwd", "ss_heads_step", "ss_add_rmsnorm", "ss_add_rmsnorm_f8", "ss_sample", "HeadsStrides",
+           "NormStrides"]
 
 SS_F32, SS_BF16 = 0, 1
 _STATUS = {0: "SS_OK", 1: "SS_ERR_INVALID_ARG", 2: "SS_ERR_UNSUPPORTED", 3: "SS_ERR_MISALIGNED",
@@ -38,6 +40,15 @@ class ConvStrides(ctypes.Structure):
 class StepStrides(ctypes.Structure):
     _fields_ = [("io_dtype", ctypes.c_int32)] + [(n, ctypes.c_int64) for n in (
         "x_b", "delta_b", "z_b", "y_b", "B_b", "C_b", "state_b", "state_d")]
+
+
+class HeadsStrides(ctypes.Structure):
+    _fields_ = [("io_dtype", ctypes.c_int32)] + [(n, ctypes.c_int64) for n in ("xbc_t", "dt_t", "z_t", "y_t")]
+
+
+class NormStrides(ctypes.Structure):
+    _fields_ = [("io_dtype", ctypes.c_int32), ("res_dtype", ctypes.c_int32)] + [
+        (n, ctypes.c_int64) for n in ("x_r", "res_r", "res_out_r", "y_r")]
 
 
 _LIB = None
@@ -84,6 +95,20 @@ def lib() -> ctypes.CDLL:
         L.ss_fwd_ckpt.restype = ctypes.c_int
         L.ss_fwd_ckpt_size.argtypes = [i64] * 4
         L.ss_fwd_ckpt_size.restype = ctypes.c_size_t
+        L.ss_heads_fwd.argtypes = [vp] * 14 + [i64] * 7 + [ctypes.POINTER(HeadsStrides), vp, ctypes.c_size_t, vp]
+        L.ss_heads_fwd.restype = ctypes.c_int
+        L.ss_heads_workspace_size.argtypes = [i64] * 6 + [ctypes.c_int32]
+        L.ss_heads_workspace_size.restype = ctypes.c_size_t
+        L.ss_heads_step.argtypes = [vp] * 12 + [i64] * 6 + [ctypes.POINTER(HeadsStrides), vp, ctypes.c_size_t, vp]
+        L.ss_heads_step.restype = ctypes.c_int
+        L.ss_heads_step_workspace_size.argtypes = [i64] * 2
+        L.ss_heads_step_workspace_size.restype = ctypes.c_size_t
+        L.ss_add_rmsnorm.argtypes = [vp] * 5 + [i64] * 2 + [ctypes.c_float, ctypes.POINTER(NormStrides), vp]
+        L.ss_add_rmsnorm.restype = ctypes.c_int
+        L.ss_add_rmsnorm_f8.argtypes = [vp] * 6 + [i64] * 3 + [ctypes.c_float, ctypes.POINTER(NormStrides), vp]
+        L.ss_add_rmsnorm_f8.restype = ctypes.c_int
+        L.ss_sample.argtypes = [vp] * 7 + [i64] * 2 + [ctypes.c_int32, i64, i64, vp]
+        L.ss_sample.restype = ctypes.c_int
         L.ss_status_string.argtypes = [ctypes.c_int]
         L.ss_status_string.restype = ctypes.c_char_p
         L.ss_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]
@@ -473,3 +498,6 @@ def ss_bwd(dy, u, delta_raw, delta_bias, A_log, B, C, D=None, z=None, h0=None, d
     if st != 0:
         raise SelscanError(st, where)
     return g
+
+
+from .serving import ss_add_rmsnorm, ss_add_rmsnorm_f8, ss_heads_fwd, ss_heads_step, ss_sample  # noqa: E402

@@ -1,0 +1,86 @@
+// Device helpers of the multi-head scan's kernels.
+#pragma once
+
+#include "device_common.cuh"
+#include "heads_params.h"
+
+namespace selscan {
+
+// Where a sequence's rows and its cached state are.
+struct HeadsSeq {
+    int64_t row0;       // first row of xbc
+    int len;            // rows
+    int slot;           // < 0: none
+    bool warm;          // starts from the slot's contents (else from zeros)
+    bool ok;            // indexes in range (else the sequence is skipped)
+};
+
+__device__ __forceinline__ HeadsSeq heads_seq(const HeadsParams& p, int seq) {
+    HeadsSeq s;
+    const int64_t a = p.cu[seq], b = p.cu[seq + 1];
+    s.slot = p.slots ? p.slots[seq] : seq;
+    s.ok = a >= 0 && b >= a && b <= p.tokens && s.slot < p.n_slots;
+    s.row0 = a;
+    s.len = static_cast<int>(b - a);
+    s.warm = s.slot >= 0 && !(p.fresh && p.fresh[seq] != 0);
+    return s;
+}
+
+// The three samples of channel c before a sequence's first row.
+struct HeadsWindow {
+    float v[kHeadsConv - 1];
+};
+__device__ __forceinline__ HeadsWindow heads_window(const HeadsParams& p, const HeadsSeq& s, int c) {
+    HeadsWindow w = {{0.f, 0.f, 0.f}};
+    if (s.warm) {
+        const float* q = p.window + (static_cast<int64_t>(s.slot) * p.C + c) * 3;
+        w.v[0] = q[0];
+        w.v[1] = q[1];
+        w.v[2] = q[2];
+    }
+    return w;
+}
+
+// Sample t (may be negative: from the window) of channel c of a sequence.
+template <typename TIO>
+__device__ __forceinline__ float heads_sample(const HeadsParams& p, const HeadsSeq& s, const HeadsWindow& w, int c, int t) {
+    if (t >= 0) return to_f32<TIO>(static_cast<const TIO*>(p.xbc)[(s.row0 + t) * p.xbc_t + c]);
+    return t == -1 ? w.v[2] : t == -2 ? w.v[1] : w.v[0];
+}
+
+// Leaves the last three samples of channel c in its slot's window: the slot's old ones are read
+// before any is written, so the thread that calls this owns the channel's window.
+template <typename TIO>
+__device__ __forceinline__ void heads_keep_window(const HeadsParams& p, const HeadsSeq& s, int c) {
+    const HeadsWindow w = heads_window(p, s, c);
+    const float a = heads_sample<TIO>(p, s, w, c, s.len - 3), b = heads_sample<TIO>(p, s, w, c, s.len - 2),
+                d = heads_sample<TIO>(p, s, w, c, s.len - 1);
+    float* q = p.window + (static_cast<int64_t>(s.slot) * p.C + c) * 3;
+    q[0] = a;
+    q[1] = b;
+    q[2] = d;
+}
+
+__device__ __forceinline__ float heads_conv(const float w[4], float b, float e0, float e1, float e2, float e3) {
+    return silu(fmaf(w[3], e3, fmaf(w[2], e2, fmaf(w[1], e1, fmaf(w[0], e0, b)))));
+}
+
+// The heads of a group share its B and C channels: each CTA that reads their windows says so here
+// when it has, and the last one to say so (it returns true there, for all its threads) may
+// overwrite them.  The counter is back at zero then.
+__device__ __forceinline__ bool heads_last_reader(unsigned int* counter, unsigned int readers) {
+    __shared__ int last;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        last = atomicAdd(counter, 1u) == readers - 1u;
+        if (last) {
+            *counter = 0u;
+            __threadfence();
+        }
+    }
+    __syncthreads();
+    return last != 0;
+}
+
+}  // namespace selscan
