@@ -538,8 +538,9 @@ typedef struct {
  *   and that sequence is skipped.
  *   P, N in 1..SS_HEADS_MAX, G divides H.  n_seq == 0 or tokens == 0 with n_seq == 0 is a no-op.
  *   workspace           device memory, 256-byte aligned, ss_heads_workspace_size(...) bytes,
- *                       zero-filled before its first use (never again).  Calls that share it must
- *                       not run concurrently on the device.
+ *                       zero-filled before its first use (never again, also between calls of
+ *                       different sizes and ss_heads_step's).  Calls that share it must not run
+ *                       concurrently on the device.
  * Arithmetic, sums and the state are fp32.  Errors as ss_fwd.
  */
 ss_status ss_heads_fwd(const void* xbc, const void* dt_raw, const void* z, const float* conv_w,

@@ -35,7 +35,25 @@ struct HeadsParams {
     int n_seq, H, P, G, N, C, n_slots;
 };
 
+// The counters of the B and C windows' readers (one per sequence and group) are at the front of every
+// workspace, in a part that nothing else uses, so that they are zero between calls of any sizes.
+// Calls with more of them than that part holds clear theirs, behind it.
+constexpr int64_t kHeadsCounters = 16384;
+constexpr size_t kHeadsCounterBytes = kHeadsCounters * 4;
+
 namespace host {
+
+inline size_t heads_counter_bytes(int64_t n_seq, int64_t G) {
+    const int64_t n = n_seq * G;
+    return kHeadsCounterBytes + (n > kHeadsCounters ? (static_cast<size_t>(n) * 4 + 255) / 256 * 256 : 0);
+}
+inline cudaError_t heads_counters(HeadsParams& p, void* workspace, cudaStream_t stream) {
+    const int64_t n = static_cast<int64_t>(p.n_seq) * p.G;
+    p.arrivals = static_cast<unsigned int*>(workspace);
+    if (n <= kHeadsCounters) return cudaSuccess;
+    p.arrivals += kHeadsCounters;
+    return cudaMemsetAsync(p.arrivals, 0, static_cast<size_t>(n) * 4, stream);
+}
 
 // Checks what ss_heads_fwd and ss_heads_step share and fills p (without cu, fresh, arrivals).
 // `idle` is set when there is nothing to do.

@@ -16,6 +16,7 @@
 #include "../../include/selscan.h"
 #include "heads_device.cuh"
 #include "heads_params.h"
+#include "heads_tc.h"
 #include "internal.h"
 
 namespace selscan {
@@ -152,8 +153,6 @@ cudaError_t launch_seq(const HeadsParams& p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-size_t arrivals_bytes(int64_t n_seq, int64_t G) { return ((static_cast<size_t>(n_seq * G) * 4 + 255) / 256) * 256; }
-
 }  // namespace
 
 namespace host {
@@ -249,7 +248,9 @@ extern "C" size_t ss_heads_workspace_size(int64_t n_seq, int64_t tokens, int64_t
     if (n_seq <= 0 || tokens < 0 || H <= 0 || G <= 0 || P < 1 || P > SS_HEADS_MAX || N < 1 || N > SS_HEADS_MAX ||
         H % G != 0 || n_seq > INT32_MAX || (io_dtype != SS_F32 && io_dtype != SS_BF16))
         return 0;
-    return arrivals_bytes(n_seq, G);
+    return heads_tc_takes(n_seq, tokens, H, P, G, N, io_dtype == SS_BF16)
+               ? kHeadsCounterBytes + heads_tc_plan(n_seq, tokens, H, P, G, N).bytes
+               : heads_counter_bytes(n_seq, G);
 }
 
 extern "C" ss_status ss_heads_fwd(const void* xbc, const void* dt_raw, const void* z, const float* conv_w,
@@ -267,8 +268,13 @@ extern "C" ss_status ss_heads_fwd(const void* xbc, const void* dt_raw, const voi
                                      cu_seqlens, slots, fresh, n_seq, tokens, H, P, G, N, n_slots, workspace,
                                      workspace_bytes, need, &bf16, &idle);
     if (st != SS_OK || idle) return st;
-    p.arrivals = static_cast<unsigned int*>(workspace);
     cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-    const cudaError_t e = bf16 ? launch_seq<__nv_bfloat16>(p, stream) : launch_seq<float>(p, stream);
+    cudaError_t e;
+    if (heads_tc_takes(n_seq, tokens, H, P, G, N, bf16)) {
+        e = launch_heads_tc(p, static_cast<uint8_t*>(workspace) + kHeadsCounterBytes, bf16, stream);
+    } else {
+        e = heads_counters(p, workspace, stream);
+        if (e == cudaSuccess) e = bf16 ? launch_seq<__nv_bfloat16>(p, stream) : launch_seq<float>(p, stream);
+    }
     return e == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }

@@ -161,8 +161,6 @@ cudaError_t launch_step_heads(const HeadsParams& p, cudaStream_t stream) {
     return launch_one<TIO, 32, 8, 1, 4>(p, stream);
 }
 
-size_t step_bytes(int64_t batch, int64_t G) { return ((static_cast<size_t>(batch * G) * 4 + 255) / 256) * 256; }
-
 }  // namespace
 }  // namespace selscan
 
@@ -170,7 +168,7 @@ using namespace selscan;
 using namespace selscan::host;
 
 extern "C" size_t ss_heads_step_workspace_size(int64_t batch, int64_t G) {
-    return (batch <= 0 || G <= 0 || batch > INT32_MAX || G > (1 << 20)) ? 0 : step_bytes(batch, G);
+    return (batch <= 0 || G <= 0 || batch > INT32_MAX || G > (1 << 20)) ? 0 : heads_counter_bytes(batch, G);
 }
 
 extern "C" ss_status ss_heads_step(float* state, float* window, const void* xbc, const void* dt_raw, const void* z,
@@ -184,8 +182,8 @@ extern "C" ss_status ss_heads_step(float* state, float* window, const void* xbc,
                                      nullptr, slots, nullptr, batch, batch, H, P, G, N, n_slots, workspace,
                                      workspace_bytes, ss_heads_step_workspace_size(batch, G), &bf16, &idle);
     if (st != SS_OK || idle) return st;
-    p.arrivals = static_cast<unsigned int*>(workspace);
     cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-    const cudaError_t e = bf16 ? launch_step_heads<__nv_bfloat16>(p, stream) : launch_step_heads<float>(p, stream);
+    cudaError_t e = heads_counters(p, workspace, stream);
+    if (e == cudaSuccess) e = bf16 ? launch_step_heads<__nv_bfloat16>(p, stream) : launch_step_heads<float>(p, stream);
     return e == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }

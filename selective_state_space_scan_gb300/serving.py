@@ -111,9 +111,10 @@ def ss_heads_step(state, window, xbc, dt_raw, conv_w, A_log, conv_b=None, dt_bia
     n = xbc.shape[0]
     io, y, T, H, P, G, N, n_slots, s = _heads_args(xbc, dt_raw, conv_w, conv_b, dt_bias, A_log, D, z, state, window, y,
                                                    (("slots", slots, n),), stream)
-    # 4 bytes per request and group: the same size ss_heads_step_workspace_size gives
-    nbytes = (n * G * 4 + 255) // 256 * 256
-    ws = _ss.workspace_for(xbc.device, stream, nbytes, purpose="heads_step") if nbytes else None
+    nbytes = _HEADS_WS.get((n, G))
+    if nbytes is None:
+        nbytes = _HEADS_WS[n, G] = int(_ss.lib().ss_heads_step_workspace_size(n, G))
+    ws = _ss.workspace_for(xbc.device, stream, nbytes, purpose="heads") if nbytes else None
     p = _ss._ptr
     st = _ss.lib().ss_heads_step(p(state), p(window), p(xbc), p(dt_raw), p(z), p(conv_w), p(conv_b), p(dt_bias), p(A_log),
                                  p(D), p(y), p(slots), n, H, P, G, N, n_slots, ctypes.byref(s), p(ws),
