@@ -23,7 +23,6 @@ struct HeadsTcParams {
     int pairs;                          // pairs of tiles, over all groups
     int gtiles;                         // tiles, over all heads
     int nb;                             // blocks of 64 states
-    bool vec_x, vec_bc, vec_z, vec_y;   // 4-channel accesses are aligned
 };
 
 struct HeadsTcPlan {

@@ -2,7 +2,7 @@
 //
 // With one decay per head the recurrence over a chunk of tokens is three matrix products.  Let a_t be
 // the log2 decay of token t, l_t its running sum within the chunk, and S the state that enters:
-//   Y   = exp2(l_t) (C_t · S) + Σ_{s<=t} exp2(l_t - l_s) Δ_s (C_t · B_s) x_s + D x_t
+//   Y   = exp2(l_t) (C_t · S) + Σ_{s<=t} exp2(l_t - l_s) Δ_s (C_t · B_s) x_s,   y = Y + D x
 //   S'  = exp2(l_end) S + Σ_s exp2(l_end - l_s) Δ_s B_s ⊗ x_s
 // heads_prep_kernel convolves B and C once per chunk and group and leaves them as shared-memory
 // images of bf16 operand tiles: B as a sum of two bf16 (hi + lo), C rounded.  heads_tc_kernel walks
@@ -10,13 +10,13 @@
 // as a rule), a warpgroup for each:
 //   scores C·Bᵀ, and C·S of both tiles        while the warpgroups convolve x, as tiles of x and of
 //                                             x scaled for the state (hi + lo)
-//   the state's products, hi·hi + hi·lo + lo·hi   while they turn scores into P (decay, Δ, mask, D)
+//   the state's products, hi·hi + hi·lo + lo·hi   while they turn scores into P (decay, Δ, mask)
 //   P·x on top of exp2(l)·(C·S), P read from tensor memory
 // The state itself stays in registers, fp32: what the chunk adds comes out of tensor memory.
 //
 // Rounding: the state's operands carry 16 bits each, so a state is off by about 1e-6 of what was added
-// to it.  y is rounded to bf16 in the end; its factors C, S, P and x are rounded to bf16 before the
-// products, each error as large as that last one.
+// to it.  y is rounded to bf16 in the end; the factors C, S, P and x of its sums are rounded to bf16
+// before the products, each error as large as that last one, and D·x is not.
 // A decay is only ever the exp2 of a sum of steps between its two tokens, never a quotient, and such
 // sums are taken over the steps themselves, so strong decays neither overflow nor cancel.
 #include <cuda_runtime.h>
@@ -73,24 +73,38 @@ __device__ __forceinline__ int block_prefix(int v, int* total, int* scratch) {
 
 // ---- B and C
 
-// Four channels of row t of a sequence, t >= 0; `n` of them exist.
-template <typename TIO>
-__device__ __forceinline__ float4 load4(const TIO* q, int n, bool vec) {
-    if (vec) {
-        if constexpr (sizeof(TIO) == 2) {
-            const uint2 u = *reinterpret_cast<const uint2*>(q);
-            return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+// Four channels as loaded: bf16 pairs, or floats.  `n` of them exist; VEC: all or none, one aligned access.
+template <typename TIO, bool VEC> struct Quad4;
+template <bool VEC> struct Quad4<__nv_bfloat16, VEC> {
+    uint2 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16* q, int n) {
+        u = make_uint2(0u, 0u);
+        if constexpr (VEC) {
+            if (n > 0) u = *reinterpret_cast<const uint2*>(q);
         } else {
-            return *reinterpret_cast<const float4*>(q);
+            const uint16_t* h = reinterpret_cast<const uint16_t*>(q);
+            if (n > 0) u.x = h[0];
+            if (n > 1) u.x |= static_cast<uint32_t>(h[1]) << 16;
+            if (n > 2) u.y = h[2];
+            if (n > 3) u.y |= static_cast<uint32_t>(h[3]) << 16;
         }
     }
-    return make_float4(n > 0 ? to_f32<TIO>(q[0]) : 0.f, n > 1 ? to_f32<TIO>(q[1]) : 0.f, n > 2 ? to_f32<TIO>(q[2]) : 0.f,
-                       n > 3 ? to_f32<TIO>(q[3]) : 0.f);
-}
+    __device__ __forceinline__ float4 get() const { return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y)); }
+    static __device__ __forceinline__ void store(__nv_bfloat16* q, int n, float4 v) {
+        if constexpr (VEC) {
+            if (n > 0) *reinterpret_cast<uint2*>(q) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+        } else {
+            if (n > 0) q[0] = from_f32<__nv_bfloat16>(v.x);
+            if (n > 1) q[1] = from_f32<__nv_bfloat16>(v.y);
+            if (n > 2) q[2] = from_f32<__nv_bfloat16>(v.z);
+            if (n > 3) q[3] = from_f32<__nv_bfloat16>(v.w);
+        }
+    }
+};
 
 // Grid (chunk, group, B or C).  Block (0, 0, 0) also writes the tables of where chunks and segments
 // begin, and reports indexes out of range.
-template <typename TIO>
+template <typename TIO, bool VEC>
 __global__ void __launch_bounds__(kPrepThreads) heads_prep_kernel(const HeadsTcParams q) {
     const HeadsParams& p = q.p;
     __shared__ int scratch[kPrepThreads / 32], found[2];
@@ -133,9 +147,19 @@ __global__ void __launch_bounds__(kPrepThreads) heads_prep_kernel(const HeadsTcP
     uint8_t* img = q.images + (static_cast<int64_t>(id) * p.G + g) * (3 * q.nb * static_cast<int64_t>(kBlock));
     uint8_t* hi = img + (which ? 2 * q.nb * kBlock : 0) + (qd / 16) * kBlock;
     uint8_t* lo = img + q.nb * kBlock + (qd / 16) * kBlock;            // B only
+    const TIO* x = static_cast<const TIO*>(p.xbc) + s.row0 * p.xbc_t + c0 + ch;
+    constexpr int kRows = 8;                                           // a round: its loads are issued together
+    Quad4<TIO, VEC> raw[kRows];
+    auto load_round = [&](int r) {
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+            const int t = t0 + r0 + r + j;
+            raw[j].load(x + t * p.xbc_t, t < s.len ? n : 0);
+        }
+    };
+    load_round(0);
     float w[4][4], b[4];
     float4 e[3];
-    const TIO* x = static_cast<const TIO*>(p.xbc) + s.row0 * p.xbc_t + c0 + ch;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
@@ -145,38 +169,41 @@ __global__ void __launch_bounds__(kPrepThreads) heads_prep_kernel(const HeadsTcP
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
         const int t = t0 + r0 + j - 3;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        Quad4<TIO, VEC> f;
+        f.load(x + static_cast<int64_t>(max(t, 0)) * p.xbc_t, (t >= 0 && t < s.len) ? n : 0);
+        e[j] = f.get();
         if (t < 0) {
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (i < n) v[i] = heads_window(p, s, c0 + ch + i).v[j];      // j: t = j - 3
+                if (i < n) v[i] = heads_window(p, s, c0 + ch + i).v[j];      // t = j - 3
             e[j] = make_float4(v[0], v[1], v[2], v[3]);
-        } else {
-            e[j] = (n > 0 && t < s.len) ? load4<TIO>(x + t * p.xbc_t, n, q.vec_bc) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
     }
-#pragma unroll 8
-    for (int r = 0; r < rows; ++r) {
-        const int t = t0 + r0 + r;
-        const bool on = n > 0 && t < s.len;
-        const float4 f = on ? load4<TIO>(x + t * p.xbc_t, n, q.vec_bc) : make_float4(0.f, 0.f, 0.f, 0.f);
-        float u[4];
-        u[0] = heads_conv(w[0], b[0], e[0].x, e[1].x, e[2].x, f.x);
-        u[1] = heads_conv(w[1], b[1], e[0].y, e[1].y, e[2].y, f.y);
-        u[2] = heads_conv(w[2], b[2], e[0].z, e[1].z, e[2].z, f.z);
-        u[3] = heads_conv(w[3], b[3], e[0].w, e[1].w, e[2].w, f.w);
+    for (int r = 0; r < rows; r += kRows) {
+        if (r > 0) load_round(r);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (!on || i >= n) u[i] = 0.f;
-        const uint32_t off = tc_chunk(r0 + r, (qd % 16) / 2) + (qd & 1) * 8;
-        const uint2 h = make_uint2(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]));
-        *reinterpret_cast<uint2*>(hi + off) = h;
-        if (which == 0)
-            *reinterpret_cast<uint2*>(lo + off) = make_uint2(pack_bf16(u[0] - bf16_lo(h.x), u[1] - bf16_hi(h.x)),
-                                                             pack_bf16(u[2] - bf16_lo(h.y), u[3] - bf16_hi(h.y)));
-        e[0] = e[1];
-        e[1] = e[2];
-        e[2] = f;
+        for (int j = 0; j < kRows; ++j) {
+            const bool on = t0 + r0 + r + j < s.len;
+            const float4 f = raw[j].get();
+            float u[4];
+            u[0] = heads_conv(w[0], b[0], e[0].x, e[1].x, e[2].x, f.x);
+            u[1] = heads_conv(w[1], b[1], e[0].y, e[1].y, e[2].y, f.y);
+            u[2] = heads_conv(w[2], b[2], e[0].z, e[1].z, e[2].z, f.z);
+            u[3] = heads_conv(w[3], b[3], e[0].w, e[1].w, e[2].w, f.w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (!on || i >= n) u[i] = 0.f;
+            const uint32_t off = tc_chunk(r0 + r + j, (qd % 16) / 2) + (qd & 1) * 8;
+            const uint2 h = make_uint2(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]));
+            *reinterpret_cast<uint2*>(hi + off) = h;
+            if (which == 0)
+                *reinterpret_cast<uint2*>(lo + off) = make_uint2(pack_bf16(u[0] - bf16_lo(h.x), u[1] - bf16_hi(h.x)),
+                                                                 pack_bf16(u[2] - bf16_lo(h.y), u[3] - bf16_hi(h.y)));
+            e[0] = e[1];
+            e[1] = e[2];
+            e[2] = f;
+        }
     }
     // the first chunk's block alone reads these channels' windows: it shifts them
     if (chunk == 0 && s.slot >= 0) {
@@ -213,7 +240,7 @@ __device__ __forceinline__ void wg_sync(int wg) { named_barrier(1 + wg, 128); }
 
 // STATE_ONLY: the first pass over a sequence cut in segments: the state that each segment but the last
 // leaves from zero, and its decay; no outputs.
-template <typename TIO, bool STATE_ONLY>
+template <typename TIO, bool VEC, bool STATE_ONLY>
 __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcParams q) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const HeadsParams& p = q.p;
@@ -222,7 +249,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
     const int tid = threadIdx.x, wg = tid / 128, t = tid % 128, warp = t / 32, lane = t % 32;
     uint8_t* tile = smem + 3 * kImage + wg * kTileBytes;
     uint8_t *sX = tile, *sXh = tile + kBlock, *sXl = tile + 2 * kBlock, *sS = tile + 3 * kBlock;
-    float* stage = reinterpret_cast<float*>(tile);                     // y, over x and x scaled hi
+    float* stage = reinterpret_cast<float*>(sXh);                      // y, over x scaled (hi and lo)
 
     const int unit = blockIdx.x / q.pairs, pair = blockIdx.x % q.pairs;
     if (unit >= q.seg_base[p.n_seq]) return;
@@ -335,10 +362,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
         for (int k = 0; k < 4; ++k) cw[i][k] = i < nq ? p.conv_w[static_cast<int64_t>(cx + 4 * qd + i) * 4 + k] : 0.f;
         cb[i] = (i < nq && p.conv_b) ? p.conv_b[cx + 4 * qd + i] : 0.f;
     }
+    const int row0 = tg * 16;
     const TIO* xg = static_cast<const TIO*>(p.xbc) + s.row0 * p.xbc_t + cx + 4 * qd;
     const TIO* zg = p.z ? static_cast<const TIO*>(p.z) + s.row0 * p.z_t + cx + 4 * qd : nullptr;
     TIO* yg = static_cast<TIO*>(p.y) + s.row0 * p.y_t + cx + 4 * qd;
+    Quad4<TIO, VEC> raw[19];                                           // samples row0 - 3 .. row0 + 15 of a chunk
+    auto load_x = [&](int c) {
+#pragma unroll
+        for (int j = 0; j < 19; ++j) {
+            const int tk = c * kQ + row0 + j - 3;
+            raw[j].load(xg + static_cast<int64_t>(max(tk, 0)) * p.xbc_t, (tk >= 0 && tk < s.len) ? nq : 0);
+        }
+    };
     const TIO* dg = static_cast<const TIO*>(p.dt_raw) + s.row0 * p.dt_t + h;
+    if (ch0 < ch1) load_x(ch0);
     float decay_sum = 0.f;
     volatile int* abort = &sh.abort;
     TcTables& tab = sh.tab[wg];
@@ -399,37 +436,45 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
         decay_sum += all;
         wg_sync(wg);
         // x, through the convolution
-        float4 raw[19];
-#pragma unroll
-        for (int j = 0; j < 19; ++j) {
-            const int tk = tok0 + tg * 16 + j - 3;
-            raw[j] = (nq > 0 && tk >= 0 && tk < s.len) ? load4<TIO>(xg + static_cast<int64_t>(tk) * p.xbc_t, nq, q.vec_x)
-                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+        uint2 xlo[16];                                                 // what bf16 leaves of it, for D·x
+        float4 e0 = raw[0].get(), e1 = raw[1].get(), e2 = raw[2].get();
         if (c == 0 && tg == 0 && s.warm) {
+            float v[3][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < nq) {
-                    const HeadsWindow w = heads_window(p, s, cx + 4 * qd + i);
-                    reinterpret_cast<float*>(&raw[0])[i] = w.v[0];
-                    reinterpret_cast<float*>(&raw[1])[i] = w.v[1];
-                    reinterpret_cast<float*>(&raw[2])[i] = w.v[2];
-                }
+            for (int i = 0; i < 4; ++i) {
+                HeadsWindow w = {{0.f, 0.f, 0.f}};
+                if (i < nq) w = heads_window(p, s, cx + 4 * qd + i);
+                v[0][i] = w.v[0];
+                v[1][i] = w.v[1];
+                v[2][i] = w.v[2];
+            }
+            e0 = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
+            e1 = make_float4(v[1][0], v[1][1], v[1][2], v[1][3]);
+            e2 = make_float4(v[2][0], v[2][1], v[2][2], v[2][3]);
         }
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-            const int row = tg * 16 + j;
+            const int row = row0 + j;
             const float m = tab.tail[row];
+            const float4 f = raw[j + 3].get();
             float u[4];
-            u[0] = heads_conv(cw[0], cb[0], raw[j].x, raw[j + 1].x, raw[j + 2].x, raw[j + 3].x);
-            u[1] = heads_conv(cw[1], cb[1], raw[j].y, raw[j + 1].y, raw[j + 2].y, raw[j + 3].y);
-            u[2] = heads_conv(cw[2], cb[2], raw[j].z, raw[j + 1].z, raw[j + 2].z, raw[j + 3].z);
-            u[3] = heads_conv(cw[3], cb[3], raw[j].w, raw[j + 1].w, raw[j + 2].w, raw[j + 3].w);
+            u[0] = heads_conv(cw[0], cb[0], e0.x, e1.x, e2.x, f.x);
+            u[1] = heads_conv(cw[1], cb[1], e0.y, e1.y, e2.y, f.y);
+            u[2] = heads_conv(cw[2], cb[2], e0.z, e1.z, e2.z, f.z);
+            u[3] = heads_conv(cw[3], cb[3], e0.w, e1.w, e2.w, f.w);
+            e0 = e1;
+            e1 = e2;
+            e2 = f;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (row >= nt || i >= nq) u[i] = 0.f;
             const uint32_t off = tc_chunk(row, qd / 2) + (qd & 1) * 8;
-            if (!STATE_ONLY) *reinterpret_cast<uint2*>(sX + off) = make_uint2(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]));
+            if (!STATE_ONLY) {
+                const uint2 x = make_uint2(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]));
+                *reinterpret_cast<uint2*>(sX + off) = x;
+                xlo[j] = make_uint2(pack_bf16(u[0] - bf16_lo(x.x), u[1] - bf16_hi(x.x)),
+                                    pack_bf16(u[2] - bf16_lo(x.y), u[3] - bf16_hi(x.y)));
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) u[i] *= m;
             const uint2 hi = make_uint2(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]));
@@ -437,6 +482,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
             *reinterpret_cast<uint2*>(sXl + off) = make_uint2(pack_bf16(u[0] - bf16_lo(hi.x), u[1] - bf16_hi(hi.x)),
                                                               pack_bf16(u[2] - bf16_lo(hi.y), u[3] - bf16_hi(hi.y)));
         }
+        if (c + 1 < ch1) load_x(c + 1);
         tma_store_fence();
         __syncthreads();
         // what the chunk adds to the state, both tiles side by side
@@ -487,8 +533,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
                             const float ls = __shfl_sync(0xffffffffu, l, i), ds = __shfl_sync(0xffffffffu, dt, i);
-                            float w = __uint_as_float(v[i]) * ds * ex2(l - ls);
-                            if (i == lane) w += Dh;
+                            const float w = __uint_as_float(v[i]) * ds * ex2(l - ls);
                             v[i] = i <= lane ? __float_as_uint(w) : 0u;
                         }
 #pragma unroll
@@ -513,6 +558,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
             }
             __syncwarp();
         }
+        Quad4<TIO, VEC> gate[16];
+        if (!STATE_ONLY && zg)
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                gate[j].load(zg + static_cast<int64_t>(tok0 + row0 + j) * p.z_t, row0 + j < nt ? nq : 0);
         // the state
         wait(&sh.bar_st, ph);
         if (tid == 0 && c + 1 < ch1 && !*abort) load_bc(c + 1);          // the products that read B and C are done
@@ -541,28 +591,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                         make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
             }
             wg_sync(wg);
-#pragma unroll 4
-            for (int i = 0; i < 16; ++i) {
-                const int row = tg + 8 * i;
-                if (row >= nt || nq <= 0) continue;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const int row = row0 + j;
                 float4 v = *reinterpret_cast<const float4*>(stage + row * kTile + ((qd ^ (row & 7)) << 2));
-                const int64_t tk = tok0 + row;
+                const uint2 x = *reinterpret_cast<const uint2*>(sX + tc_chunk(row, qd / 2) + (qd & 1) * 8);
+                v.x = fmaf(Dh, bf16_lo(x.x) + bf16_lo(xlo[j].x), v.x);
+                v.y = fmaf(Dh, bf16_hi(x.x) + bf16_hi(xlo[j].x), v.y);
+                v.z = fmaf(Dh, bf16_lo(x.y) + bf16_lo(xlo[j].y), v.z);
+                v.w = fmaf(Dh, bf16_hi(x.y) + bf16_hi(xlo[j].y), v.w);
                 if (zg) {
-                    const float4 z = load4<TIO>(zg + tk * p.z_t, nq, q.vec_z);
+                    const float4 z = gate[j].get();
                     v.x *= silu(z.x);
                     v.y *= silu(z.y);
                     v.z *= silu(z.z);
                     v.w *= silu(z.w);
                 }
-                TIO* o = yg + tk * p.y_t;
-                if (q.vec_y) {
-                    *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-                } else {
-                    o[0] = from_f32<TIO>(v.x);
-                    if (nq > 1) o[1] = from_f32<TIO>(v.y);
-                    if (nq > 2) o[2] = from_f32<TIO>(v.z);
-                    if (nq > 3) o[3] = from_f32<TIO>(v.w);
-                }
+                Quad4<TIO, VEC>::store(yg + static_cast<int64_t>(tok0 + row) * p.y_t, row < nt ? nq : 0, v);
             }
             tma_store_fence();
         }
@@ -624,23 +669,23 @@ int sm_count() {
 
 size_t padded(size_t n) { return (n + 255) / 256 * 256; }
 
-template <typename TIO>
+template <typename TIO, bool VEC>
 cudaError_t launch_typed(const HeadsTcParams& q, const HeadsTcPlan& plan, cudaStream_t stream) {
     static_assert(sizeof(TIO) == 2, "bf16 operands of the products carry bf16 inputs");
     const dim3 prep(static_cast<unsigned>(plan.chunks), static_cast<unsigned>(q.p.G), 2u);
-    heads_prep_kernel<TIO><<<prep, kPrepThreads, 0, stream>>>(q);
+    heads_prep_kernel<TIO, VEC><<<prep, kPrepThreads, 0, stream>>>(q);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const unsigned grid = static_cast<unsigned>(plan.segments * plan.pairs);
     if (plan.split) {
-        e = cudaFuncSetAttribute(heads_tc_kernel<TIO, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+        e = cudaFuncSetAttribute(heads_tc_kernel<TIO, VEC, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
         if (e != cudaSuccess) return e;
-        heads_tc_kernel<TIO, true><<<grid, kTcThreads, kTcSmem, stream>>>(q);
+        heads_tc_kernel<TIO, VEC, true><<<grid, kTcThreads, kTcSmem, stream>>>(q);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    e = cudaFuncSetAttribute(heads_tc_kernel<TIO, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+    e = cudaFuncSetAttribute(heads_tc_kernel<TIO, VEC, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
     if (e != cudaSuccess) return e;
-    heads_tc_kernel<TIO, false><<<grid, kTcThreads, kTcSmem, stream>>>(q);
+    heads_tc_kernel<TIO, VEC, false><<<grid, kTcThreads, kTcSmem, stream>>>(q);
     return cudaGetLastError();
 }
 
@@ -698,13 +743,10 @@ cudaError_t launch_heads_tc(const HeadsParams& p, void* workspace, bool bf16, cu
     q.pairs = plan.pairs;
     q.gtiles = plan.gtiles;
     q.nb = plan.nb;
-    const int64_t a = 4 * (bf16 ? 2 : 4);                    // bytes of four channels
-    auto wide = [&](const void* base, int64_t stride) { return host::is_aligned(base, a) && stride % 4 == 0; };
-    q.vec_x = p.P % 4 == 0 && wide(p.xbc, p.xbc_t);
-    q.vec_bc = q.vec_x && p.N % 4 == 0;
-    q.vec_z = p.P % 4 == 0 && wide(p.z, p.z_t);
-    q.vec_y = p.P % 4 == 0 && wide(p.y, p.y_t);
-    return launch_typed<__nv_bfloat16>(q, plan, stream);
+    // four channels in one access: z, x, B, C and y of every head and group on that boundary
+    auto wide = [&](const void* base, int64_t stride) { return host::is_aligned(base, 8) && stride % 4 == 0; };
+    const bool vec = p.P % 4 == 0 && p.N % 4 == 0 && wide(p.xbc, p.xbc_t) && wide(p.z, p.z_t) && wide(p.y, p.y_t);
+    return vec ? launch_typed<__nv_bfloat16, true>(q, plan, stream) : launch_typed<__nv_bfloat16, false>(q, plan, stream);
 }
 
 }  // namespace selscan
