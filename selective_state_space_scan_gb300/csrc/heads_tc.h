@@ -15,10 +15,14 @@ constexpr int kHeadsTile = 64;          // rows of the state per tile
 struct HeadsTcParams {
     HeadsParams p;
     uint8_t* images;                    // [chunks, G][B hi, B lo, C][nb] blocks of 128 × 64 bf16
-    int32_t* chunk_base;                // [n_seq] first chunk of a sequence
+    int32_t* chunk_base;                // [n_seq + 1] first chunk of a sequence
     int32_t* seg_base;                  // [n_seq + 1] first segment of a sequence
     float* seg_state;                   // [segments, gtiles][16][128][4]: what a segment leaves from zero
     float* seg_decay;                   // [segments, gtiles]: its log2 decay
+    int32_t* order;                     // [segments][sequence, segment], by the segment's number
+    float* handover;                    // [n_seq, pairs, 2][16][128][4]: the state between two segments
+    unsigned int* flags;                // [n_seq, pairs, 2]: segments done
+    int nflags;
     int seg_chunks;                     // chunks per segment
     int pairs;                          // pairs of tiles, over all groups
     int gtiles;                         // tiles, over all heads
@@ -27,8 +31,9 @@ struct HeadsTcParams {
 
 struct HeadsTcPlan {
     int64_t chunks, segments;           // upper bounds over all lengths that make up `tokens`
-    int seg_chunks, pairs, gtiles, nb;
-    size_t off_images, off_chunk_base, off_seg_base, off_state, off_decay, bytes;   // in the workspace
+    int seg_chunks, pairs, gtiles, nb, ctas, chains;
+    size_t off_images, off_chunk_base, off_seg_base, off_state, off_decay, off_handover, off_flags, off_order,
+        bytes;                          // in the workspace
     bool split;
 };
 

@@ -7,7 +7,7 @@
 // heads_prep_kernel convolves B and C once per chunk and group and leaves them as shared-memory
 // images of bf16 operand tiles: B as a sum of two bf16 (hi + lo), C rounded.  heads_tc_kernel walks
 // the chunks of one sequence (or of a segment of it) for two tiles of 64 rows of the state (two heads,
-// as a rule), a warpgroup for each:
+// as a rule), two warpgroups for each:
 //   scores C·Bᵀ, and C·S of both tiles        while the warpgroups convolve x, as tiles of x and of
 //                                             x scaled for the state (hi + lo)
 //   the state's products, hi·hi + hi·lo + lo·hi   while they turn scores into P (decay, Δ, mask)
@@ -38,7 +38,7 @@ constexpr int kQ = kHeadsChunk;                    // tokens per chunk (128: row
 constexpr int kTile = kHeadsTile;                  // rows of the state per tile (64)
 constexpr uint32_t kBlock = kQ * kTcRow;           // a tile's block: 128 rows of 64 bf16
 constexpr int kPrepThreads = 256;
-constexpr int kTcThreads = 256;                    // two warpgroups, one per tile
+constexpr int kTcThreads = 512;                    // two warpgroups per tile
 
 // ---- where the chunks and segments of the sequences are
 
@@ -136,10 +136,30 @@ __global__ void __launch_bounds__(kPrepThreads) heads_prep_kernel(const HeadsTcP
         __syncthreads();
         if (!first && found[0] >= 0) break;
     }
-    if (first && tid == 0) q.seg_base[p.n_seq] = sbase;
+    if (first && tid == 0) {
+        q.seg_base[p.n_seq] = sbase;
+        q.chunk_base[p.n_seq] = base;
+    }
+    if (first)
+        for (int i = tid; i < q.nflags; i += kPrepThreads) q.flags[i] = 0u;
     __syncthreads();
     if (found[0] < 0) return;
     const int seq = found[0], chunk = found[1], which = blockIdx.z;
+    if (g == 0 && which == 0 && chunk % q.seg_chunks == 0) {
+        // the segment's place among all: after those of lower number, and those of its number in sequences before
+        const int seg = chunk / q.seg_chunks;
+        int at = 0;
+        for (int s0 = 0; s0 < p.n_seq; s0 += kPrepThreads) {
+            const int n = (chunks_of(p, s0 + tid) + q.seg_chunks - 1) / q.seg_chunks;
+            int total;
+            block_prefix(min(n, seg) + (n > seg && s0 + tid < seq ? 1 : 0), &total, scratch);
+            at += total;
+        }
+        if (tid == 0) {
+            q.order[2 * at] = seq;
+            q.order[2 * at + 1] = seg;
+        }
+    }
     const HeadsSeq s = heads_seq(p, seq);
     const int c0 = p.H * p.P + (which ? p.G * p.N : 0) + g * p.N;      // first channel
     const int quads = q.nb * 16, qd = tid % quads, rows = kQ * quads / kPrepThreads, r0 = (tid / quads) * rows;
@@ -217,13 +237,16 @@ __global__ void __launch_bounds__(kPrepThreads) heads_prep_kernel(const HeadsTcP
 constexpr uint32_t kImage = 2 * kBlock;            // B hi, B lo or C in shared memory (N up to 128)
 constexpr uint32_t kTileBytes = 4 * kBlock;        // per tile: x, x scaled hi, x scaled lo, state
 constexpr int kFacs = 192;                         // decay factors of the blocks off the diagonal
+constexpr int kToks = 8;                           // tokens per thread in the convolution and the output
 struct TcTables {
     float tail[kQ];                                // Δ_s · decay from s to the chunk's end
     float fac[kFacs];                              // Δ_s · decay from s to the start of a later block of 32
     float total[4];                                // log2 decay of the blocks of 32
 };
 struct TcShared {
-    uint64_t bar_bc, bar_cs, bar_st, bar_pv[2];
+    uint64_t bc;                                   // B and C have arrived
+    uint64_t cs, st, pv[2];                        // products complete: scores and C·S; state; P·x of a tile
+    uint64_t x_ready, p_ready[2], y_free;          // operands written: x tiles; P; S (and the last y read)
     uint32_t tmem;
     int abort;
     TcTables tab[2];
@@ -235,86 +258,81 @@ static_assert(kTcSmem <= 232448, "227 KB of shared memory per CTA");
 // both tiles, P of both tiles (two bf16 a column).
 constexpr uint32_t kColScore = 0, kColY = 128, kColS = 256, kColP = 384, kTmemCols = 512;
 
-// Warpgroup-wide barrier (its four warps).
-__device__ __forceinline__ void wg_sync(int wg) { named_barrier(1 + wg, 128); }
+enum class Pass {
+    kWaves,       // one launch: the segments in the order of their place in their sequence, dealt out to
+                  // the CTAs; a segment takes the state that the one before it left
+    kStates,      // time split, first pass: the state that each segment but the last leaves; no outputs
+    kSegments     // time split, second pass: every segment from the state that enters it
+};
 
-// STATE_ONLY: the first pass over a sequence cut in segments: the state that each segment but the last
-// leaves from zero, and its decay; no outputs.
-template <typename TIO, bool VEC, bool STATE_ONLY>
+// Consecutive chunks of one sequence for one pair of tiles.
+struct Piece {
+    int seq, seg, pair, ch0, ch1, nchunks;   // nchunks: of the sequence, at least 1
+};
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// One arrival per warp, after the writes of all its lanes.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) mbar_arrive(bar);
+}
+
+// Waits (with a limit, longer than any chain of segments takes) until *flag has reached n.
+__device__ __forceinline__ void wait_flag(const unsigned int* flag, unsigned int n, volatile int* abort, unsigned int* err) {
+    const long long t0 = clock64();
+    for (;;) {
+        unsigned int v;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
+        if (v >= n || *abort) return;
+        if (clock64() - t0 > (1ll << 34)) {
+            *abort = 1;
+            if (err) atomicOr(err, kErrWaitTimeout);
+            return;
+        }
+    }
+}
+
+template <typename TIO, bool VEC, Pass PASS>
 __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcParams q) {
+    constexpr bool kOut = PASS != Pass::kStates;
     extern __shared__ __align__(1024) uint8_t smem[];
     const HeadsParams& p = q.p;
     uint8_t* img = smem;                                               // B hi, B lo, C
     TcShared& sh = *reinterpret_cast<TcShared*>(smem + 3 * kImage + 2 * kTileBytes);
-    const int tid = threadIdx.x, wg = tid / 128, t = tid % 128, warp = t / 32, lane = t % 32;
-    uint8_t* tile = smem + 3 * kImage + wg * kTileBytes;
-    uint8_t *sX = tile, *sXh = tile + kBlock, *sXl = tile + 2 * kBlock, *sS = tile + 3 * kBlock;
-    float* stage = reinterpret_cast<float*>(sXh);                      // y, over x scaled (hi and lo)
+    volatile int* abort = &sh.abort;
+    const int tid = threadIdx.x;
 
-    const int unit = blockIdx.x / q.pairs, pair = blockIdx.x % q.pairs;
-    if (unit >= q.seg_base[p.n_seq]) return;
-    int seq = 0;
-    for (int a = 0, b = p.n_seq; b - a > 1;) {                          // the sequence with seg_base <= unit
-        const int m = (a + b) / 2;
-        if (q.seg_base[m] <= unit) a = m;
-        else b = m;
-        seq = a;
-    }
-    // (a skipped sequence has no segments: the last of equal bases is the one that has them)
-    const HeadsSeq s = heads_seq(p, seq);
-    const int seg = unit - q.seg_base[seq], nchunks = (s.len + kQ - 1) / kQ;
-    const int ch0 = seg * q.seg_chunks, ch1 = min(nchunks, ch0 + q.seg_chunks);
-    const bool last = ch1 >= nchunks;
-    // the tile: tiles of a group are numbered head by head, two of them to a CTA
-    const int ppg = q.pairs / p.G, g = pair / ppg, tiles = (p.P + kTile - 1) / kTile, per_group = (p.H / p.G) * tiles;
-    const int tl = (pair % ppg) * 2 + wg;
-    const bool on = tl < per_group;
-    const int h = g * (p.H / p.G) + (on ? tl / tiles : 0), p0 = on ? (tl % tiles) * kTile : 0, np = on ? min(kTile, p.P - p0) : 0;
-    const int cx = h * p.P + p0, gtile = h * tiles + p0 / kTile;
-
-    // the state that enters: thread = state n, registers = rows of the tile.  A sequence in one segment
-    // takes its slot's state.  One in several must not read the slot here (the last segment's CTA may
-    // have written it already): the first pass runs segment 0 from it and puts a copy in the place of the
-    // last segment, which that pass does not run.
-    float S[kTile];
-    const float* slot_state =
-        p.state + (static_cast<int64_t>(max(s.slot, 0)) * p.H + h) * p.P * p.N + static_cast<int64_t>(p0) * p.N + t;
-    auto segment = [&](int j) { return static_cast<int64_t>(q.seg_base[seq] + j) * q.gtiles + gtile; };
-    auto segment_state = [&](int j) { return reinterpret_cast<float4*>(q.seg_state + segment(j) * (kQ * kTile)) + t; };
-    auto add_segment = [&](int j, float d) {
-        const float4* l = segment_state(j);
-#pragma unroll
-        for (int i = 0; i < kTile / 4; ++i) {
-            const float4 v = l[i * kQ];
-            S[4 * i] = fmaf(d, S[4 * i], v.x);
-            S[4 * i + 1] = fmaf(d, S[4 * i + 1], v.y);
-            S[4 * i + 2] = fmaf(d, S[4 * i + 2], v.z);
-            S[4 * i + 3] = fmaf(d, S[4 * i + 3], v.w);
+    // this CTA's pieces: a segment for a pair of tiles each.  Pairs run fastest, so that the CTAs at work
+    // read the same rows of the tokens (a tile's share of a row is 128 bytes).
+    const int64_t items = static_cast<int64_t>(q.seg_base[p.n_seq]) * q.pairs;
+    if (blockIdx.x >= items) return;
+    auto each_piece = [&](auto&& f) {
+        for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+            Piece c;
+            const int u = static_cast<int>(i / q.pairs);
+            c.pair = static_cast<int>(i - static_cast<int64_t>(u) * q.pairs);
+            c.seq = q.order[2 * u];
+            c.seg = q.order[2 * u + 1];
+            c.nchunks = q.chunk_base[c.seq + 1] - q.chunk_base[c.seq];
+            c.ch0 = c.seg * q.seg_chunks;
+            c.ch1 = min(c.nchunks, c.ch0 + q.seg_chunks);
+            if (PASS == Pass::kStates && c.nchunks <= q.seg_chunks) continue;      // one segment: nothing to prepare
+            f(c);
         }
     };
-    auto keep_segment = [&](int j) {
-        float4* l = segment_state(j);
-#pragma unroll
-        for (int i = 0; i < kTile / 4; ++i) l[i * kQ] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
-    };
-    const int nsegs = max(1, (nchunks + q.seg_chunks - 1) / q.seg_chunks);
-    const bool from_slot = s.warm && t < p.N && (STATE_ONLY ? seg == 0 || last : nsegs == 1);
-#pragma unroll
-    for (int i = 0; i < kTile; ++i) S[i] = (from_slot && i < np) ? slot_state[static_cast<int64_t>(i) * p.N] : 0.f;
-    if (STATE_ONLY && last) {
-        if (on && nsegs > 1) keep_segment(nsegs - 1);
-        return;
-    }
-    if (!STATE_ONLY && on && nsegs > 1) {
-        if (seg == 0) add_segment(nsegs - 1, 0.f);
-        for (int j = 0; j < seg; ++j) add_segment(j, ex2(q.seg_decay[segment(j)]));      // in order
-    }
+
     if (tid == 0) {
-        mbar_init(&sh.bar_bc, 1);
-        mbar_init(&sh.bar_cs, 1);
-        mbar_init(&sh.bar_st, 1);
-        mbar_init(&sh.bar_pv[0], 1);
-        mbar_init(&sh.bar_pv[1], 1);
+        mbar_init(&sh.bc, 1);
+        mbar_init(&sh.cs, 1);
+        mbar_init(&sh.st, 1);
+        mbar_init(&sh.pv[0], 1);
+        mbar_init(&sh.pv[1], 1);
+        mbar_init(&sh.x_ready, 16);
+        mbar_init(&sh.p_ready[0], 8);
+        mbar_init(&sh.p_ready[1], 8);
+        mbar_init(&sh.y_free, 16);
         mbar_fence_init();
         sh.abort = 0;
     }
@@ -325,331 +343,456 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
             *reinterpret_cast<uint4*>(img + kBlock + i * 16) = make_uint4(0u, 0u, 0u, 0u);
             *reinterpret_cast<uint4*>(img + kImage + kBlock + i * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
-    const uint8_t* src = q.images + (static_cast<int64_t>(q.chunk_base[seq]) * p.G + g) * (3 * q.nb * static_cast<int64_t>(kBlock));
-    const int64_t src_step = static_cast<int64_t>(p.G) * 3 * q.nb * kBlock;
-    const uint32_t part = q.nb * kBlock;
-    auto load_bc = [&](int c) {
-        mbar_expect_tx(&sh.bar_bc, (STATE_ONLY ? 2 : 3) * part);
-        const uint8_t* f = src + c * src_step;
-        bulk_load(img, f, part, &sh.bar_bc);
-        bulk_load(img + kImage, f + part, part, &sh.bar_bc);
-        if (!STATE_ONLY) bulk_load(img + 2 * kImage, f + 2 * part, part, &sh.bar_bc);
-    };
-
-    auto store_state_tile = [&]() {                                    // S rounded, for C·S
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            *reinterpret_cast<uint4*>(sS + tc_chunk(t, c)) =
-                make_uint4(pack_bf16(S[8 * c], S[8 * c + 1]), pack_bf16(S[8 * c + 2], S[8 * c + 3]),
-                           pack_bf16(S[8 * c + 4], S[8 * c + 5]), pack_bf16(S[8 * c + 6], S[8 * c + 7]));
-    };
-    if (!STATE_ONLY) store_state_tile();
     tma_store_fence();                                                 // (generic writes, for the tensor cores)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem, lanes = static_cast<uint32_t>(warp) << 21;      // this warp's lanes: 32·warp << 16
-    if (tid == 0 && ch0 < ch1) load_bc(ch0);
+    const uint32_t tmem = sh.tmem;
+    const int ppg = q.pairs / p.G, tiles = (p.P + kTile - 1) / kTile, per_group = (p.H / p.G) * tiles;
+    uint32_t it = 0;                                                   // chunks so far: the barriers' phases
 
-    const float A2 = on ? -expf(p.A_log[h]) * kLog2e : 0.f, dbias = (on && p.dt_bias) ? p.dt_bias[h] : 0.f;
-    const float Dh = (on && p.D) ? p.D[h] : 0.f;
-    // x: a thread has 4 channels of 16 tokens
-    const int qd = t % 16, tg = t / 16, nq = min(4, np - 4 * qd);
-    float cw[4][4], cb[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) cw[i][k] = i < nq ? p.conv_w[static_cast<int64_t>(cx + 4 * qd + i) * 4 + k] : 0.f;
-        cb[i] = (i < nq && p.conv_b) ? p.conv_b[cx + 4 * qd + i] : 0.f;
-    }
-    const int row0 = tg * 16;
-    const TIO* xg = static_cast<const TIO*>(p.xbc) + s.row0 * p.xbc_t + cx + 4 * qd;
-    const TIO* zg = p.z ? static_cast<const TIO*>(p.z) + s.row0 * p.z_t + cx + 4 * qd : nullptr;
-    TIO* yg = static_cast<TIO*>(p.y) + s.row0 * p.y_t + cx + 4 * qd;
-    Quad4<TIO, VEC> raw[19];                                           // samples row0 - 3 .. row0 + 15 of a chunk
-    auto load_x = [&](int c) {
-#pragma unroll
-        for (int j = 0; j < 19; ++j) {
-            const int tk = c * kQ + row0 + j - 3;
-            raw[j].load(xg + static_cast<int64_t>(max(tk, 0)) * p.xbc_t, (tk >= 0 && tk < s.len) ? nq : 0);
-        }
-    };
-    const TIO* dg = static_cast<const TIO*>(p.dt_raw) + s.row0 * p.dt_t + h;
-    if (ch0 < ch1) load_x(ch0);
-    float decay_sum = 0.f;
-    volatile int* abort = &sh.abort;
-    TcTables& tab = sh.tab[wg];
-
-    auto wait = [&](uint64_t* bar, uint32_t parity) {                  // for a product's completion
-        mbar_wait_bounded(bar, parity, abort, p.err);
-        __syncwarp();
-        tc_fence_after();
-    };
-
-    for (int c = ch0; c < ch1; ++c) {
-        const int tok0 = c * kQ, nt = min(kQ, s.len - tok0);
-        const uint32_t ph = (c - ch0) & 1;
-        // scores and C·S: the tiles are there, S was written before the last barrier
-        if (tid == 0) {
-            mbar_wait_bounded(&sh.bar_bc, ph, abort, p.err);
-            if (!STATE_ONLY) {
-                tc_fence_after();
-                const uint32_t b = smem_addr(img), cc = b + 2 * kImage, st = smem_addr(smem + 3 * kImage + 3 * kBlock);
-                for (int k = 0; k < 4 * q.nb; ++k) {
-                    const uint32_t at = (k / 4) * kBlock + (k % 4) * 32;
-                    tc_mma(tmem + kColScore, tc_desc(cc + at, 16, 1024), tc_desc(b + at, 16, 1024), tc_idesc(128, 128, false, false),
-                           k > 0);
-                }
-                for (int k = 0; k < 4 * q.nb; ++k)
-                    tc_mma(tmem + kColY, tc_desc(cc + (k / 4) * kBlock + (k % 4) * 32, 16, 1024),
-                           tc_desc(st + k * 2048, kTileBytes, 1024), tc_idesc(128, 128, false, true), k > 0);
-                tc_commit(&sh.bar_cs);
-            }
-        }
-        __syncwarp();
-        // time steps: thread = token
-        float dt = 0.f;
-        if (on && t < nt) dt = softplus(to_f32<TIO>(dg[static_cast<int64_t>(tok0 + t) * p.dt_t]) + dbias);
-        const float a = dt * A2;
-        float l = a, r = __shfl_down_sync(0xffffffffu, a, 1);          // sums up to t, and after t, in the block of 32
-        if (lane == 31) r = 0.f;
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-            const float u = __shfl_up_sync(0xffffffffu, l, o), d = __shfl_down_sync(0xffffffffu, r, o);
-            if (lane >= o) l += u;
-            if (lane + o < 32) r += d;
-        }
-        if (lane == 31) tab.total[warp] = l;
-        wg_sync(wg);
-        float before = 0.f, all = 0.f, after = r;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const float v = tab.total[w];
-            all += v;
-            if (w < warp) before += v;
-            if (w > warp) {
-                if (!STATE_ONLY) tab.fac[(w - 1) * w / 2 * 32 + t] = dt * ex2(after);   // blocks 1, 2, 3 at 0, 32, 96
-                after += v;
-            }
-        }
-        tab.tail[t] = dt * ex2(after);
-        decay_sum += all;
-        wg_sync(wg);
-        // x, through the convolution
-        uint2 xlo[16];                                                 // what bf16 leaves of it, for D·x
-        float4 e0 = raw[0].get(), e1 = raw[1].get(), e2 = raw[2].get();
-        if (c == 0 && tg == 0 && s.warm) {
-            float v[3][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                HeadsWindow w = {{0.f, 0.f, 0.f}};
-                if (i < nq) w = heads_window(p, s, cx + 4 * qd + i);
-                v[0][i] = w.v[0];
-                v[1][i] = w.v[1];
-                v[2][i] = w.v[2];
-            }
-            e0 = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
-            e1 = make_float4(v[1][0], v[1][1], v[1][2], v[1][3]);
-            e2 = make_float4(v[2][0], v[2][1], v[2][2], v[2][3]);
-        }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const int row = row0 + j;
-            const float m = tab.tail[row];
-            const float4 f = raw[j + 3].get();
-            float u[4];
-            u[0] = heads_conv(cw[0], cb[0], e0.x, e1.x, e2.x, f.x);
-            u[1] = heads_conv(cw[1], cb[1], e0.y, e1.y, e2.y, f.y);
-            u[2] = heads_conv(cw[2], cb[2], e0.z, e1.z, e2.z, f.z);
-            u[3] = heads_conv(cw[3], cb[3], e0.w, e1.w, e2.w, f.w);
-            e0 = e1;
-            e1 = e2;
-            e2 = f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (row >= nt || i >= nq) u[i] = 0.f;
-            const uint32_t off = tc_chunk(row, qd / 2) + (qd & 1) * 8;
-            if (!STATE_ONLY) {
-                const uint2 x = make_uint2(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]));
-                *reinterpret_cast<uint2*>(sX + off) = x;
-                xlo[j] = make_uint2(pack_bf16(u[0] - bf16_lo(x.x), u[1] - bf16_hi(x.x)),
-                                    pack_bf16(u[2] - bf16_lo(x.y), u[3] - bf16_hi(x.y)));
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) u[i] *= m;
-            const uint2 hi = make_uint2(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]));
-            *reinterpret_cast<uint2*>(sXh + off) = hi;
-            *reinterpret_cast<uint2*>(sXl + off) = make_uint2(pack_bf16(u[0] - bf16_lo(hi.x), u[1] - bf16_hi(hi.x)),
-                                                              pack_bf16(u[2] - bf16_lo(hi.y), u[3] - bf16_hi(hi.y)));
-        }
-        if (c + 1 < ch1) load_x(c + 1);
-        tma_store_fence();
-        __syncthreads();
-        // what the chunk adds to the state, both tiles side by side
-        if (tid == 0) {
-            tc_fence_after();
-            const uint32_t b = smem_addr(img), x = smem_addr(smem + 3 * kImage + kBlock);
-            for (int k = 0; k < 8; ++k) {
-                const uint64_t bh = tc_desc(b + k * 2048, kBlock, 1024), bl = tc_desc(b + kImage + k * 2048, kBlock, 1024);
-                const uint64_t xh = tc_desc(x + k * 2048, kTileBytes, 1024), xl = tc_desc(x + kBlock + k * 2048, kTileBytes, 1024);
-                constexpr uint32_t id = tc_idesc(128, 128, true, true);
-                tc_mma(tmem + kColS, bh, xl, id, k > 0);
-                tc_mma(tmem + kColS, bl, xh, id, true);
-                tc_mma(tmem + kColS, bh, xh, id, true);
-            }
-            tc_commit(&sh.bar_st);
-        }
-        __syncwarp();
-        if (!STATE_ONLY) {
-            wait(&sh.bar_cs, ph);
-            // exp2(l)·(C·S)
-            const float carry = ex2(before + l);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint32_t v[32];
-                tc_ld32(tmem + lanes + kColY + wg * 64 + k * 32, v);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * carry);
-                tc_st32(tmem + lanes + kColY + wg * 64 + k * 32, v);
-            }
-            // P: thread = row t; the blocks of 32 columns before its own by a product of two decays, its own
-            // by the decay itself, the ones after it zero
-            const float mine = ex2(l);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t o[16];
-                if (j <= warp) {
-                    uint32_t v[32];
-                    tc_ld32(tmem + lanes + kColScore + j * 32, v);
-                    if (j < warp) {
-                        const float4* f = reinterpret_cast<const float4*>(&tab.fac[(warp - 1) * warp / 2 * 32 + j * 32]);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float4 w = f[i];
-                            o[2 * i] = pack_bf16(__uint_as_float(v[4 * i]) * w.x * mine, __uint_as_float(v[4 * i + 1]) * w.y * mine);
-                            o[2 * i + 1] = pack_bf16(__uint_as_float(v[4 * i + 2]) * w.z * mine, __uint_as_float(v[4 * i + 3]) * w.w * mine);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float ls = __shfl_sync(0xffffffffu, l, i), ds = __shfl_sync(0xffffffffu, dt, i);
-                            const float w = __uint_as_float(v[i]) * ds * ex2(l - ls);
-                            v[i] = i <= lane ? __float_as_uint(w) : 0u;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = pack_bf16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = 0u;
-                }
-                tc_st16(tmem + lanes + kColP + wg * 64 + j * 16, o);
-            }
-            tc_wait_st();
-            tc_fence_before();
-            wg_sync(wg);
-            if (t == 0) {
-                tc_fence_after();
-                const uint32_t x = smem_addr(sX);
-                for (int k = 0; k < 8; ++k)
-                    tc_mma_ta(tmem + kColY + wg * 64, tmem + kColP + wg * 64 + k * 8, tc_desc(x + k * 2048, 16, 1024),
-                              tc_idesc(128, 64, false, true), true);
-                tc_commit(&sh.bar_pv[wg]);
-            }
+    {
+        // two warpgroups to a tile: both have all 128 tokens (or states) as their lanes, and half of the
+        // columns each
+        const int wg = tid / 256, hf = (tid / 128) & 1, t = tid % 128, warp = t / 32, lane = t % 32;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp) << 21);        // this warp's lanes: 32·warp << 16
+        uint8_t* tile = smem + 3 * kImage + wg * kTileBytes;
+        uint8_t *sX = tile, *sXh = tile + kBlock, *sXl = tile + 2 * kBlock, *sS = tile + 3 * kBlock;
+        float* stage = reinterpret_cast<float*>(sXh);                  // y, over x scaled (hi and lo)
+        TcTables& tab = sh.tab[wg];
+        auto tile_sync = [&]() { named_barrier(1 + wg, 256); };
+        auto wait = [&](uint64_t* bar, uint32_t parity) {              // for a product's completion
+            mbar_wait_bounded(bar, parity, abort, p.err);
             __syncwarp();
-        }
-        Quad4<TIO, VEC> gate[16];
-        if (!STATE_ONLY && zg)
+            tc_fence_after();
+        };
+        // The products are issued by threads of the warps that have no block of P on or below the diagonal:
+        // P·x of a tile by the tile's own, all others by the first tile's.
+        const bool issue_pv = hf == 1 && t == 0, issue = issue_pv && wg == 0;
+        const uint32_t b_at = smem_addr(img), c_at = b_at + 2 * kImage, x_at = smem_addr(smem + 3 * kImage);
+        // the convolution and the output: a thread has 4 channels of 8 tokens
+        const int qd = t % 16, row0 = (hf * 8 + t / 16) * kToks;
+
+        each_piece([&](const Piece& c) {
+            const HeadsSeq s = heads_seq(p, c.seq);
+            const int ch1 = min(c.ch1, (s.len + kQ - 1) / kQ);
+            const bool begins = c.ch0 == 0, ends = c.ch1 >= c.nchunks;
+            // the tile: tiles of a group are numbered head by head, two of them to a CTA
+            const int g = c.pair / ppg, tl = (c.pair % ppg) * 2 + wg;
+            const bool on = tl < per_group;
+            const int h = g * (p.H / p.G) + (on ? tl / tiles : 0), p0 = on ? (tl % tiles) * kTile : 0;
+            const int np = on ? min(kTile, p.P - p0) : 0, cx = h * p.P + p0, gtile = h * tiles + p0 / kTile;
+            const int nq = min(4, np - 4 * qd);
+
+            const uint8_t* src =
+                q.images + (static_cast<int64_t>(q.chunk_base[c.seq]) * p.G + g) * (3 * q.nb * static_cast<int64_t>(kBlock));
+            auto load_bc = [&](int ch) {
+                const uint32_t part = q.nb * kBlock;
+                const uint8_t* f = src + static_cast<int64_t>(ch) * p.G * 3 * part;
+                mbar_expect_tx(&sh.bc, (kOut ? 3 : 2) * part);
+                bulk_load(img, f, part, &sh.bc);
+                bulk_load(img + kImage, f + part, part, &sh.bc);
+                if (kOut) bulk_load(img + 2 * kImage, f + 2 * part, part, &sh.bc);
+            };
+            const TIO* xg = static_cast<const TIO*>(p.xbc) + s.row0 * p.xbc_t + cx + 4 * qd;
+            Quad4<TIO, VEC> raw[kToks + 3];                            // samples row0 - 3 .. of a chunk
+            auto load_x = [&](int ch) {
+                const int tk = ch * kQ + row0 - 3;
+                const TIO* f = xg + static_cast<int64_t>(tk) * p.xbc_t;
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                gate[j].load(zg + static_cast<int64_t>(tok0 + row0 + j) * p.z_t, row0 + j < nt ? nq : 0);
-        // the state
-        wait(&sh.bar_st, ph);
-        if (tid == 0 && c + 1 < ch1 && !*abort) load_bc(c + 1);          // the products that read B and C are done
-        __syncwarp();
-        {
-            const float d = ex2(all);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint32_t v[32];
-                tc_ld32(tmem + lanes + kColS + wg * 64 + k * 32, v);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) S[32 * k + i] = fmaf(d, S[32 * k + i], __uint_as_float(v[i]));
-            }
-        }
-        if (!STATE_ONLY) {
-            store_state_tile();
-            wait(&sh.bar_pv[wg], ph);
-            // y: rows out of tensor memory, through shared memory, so that 16 threads write a token's 64 channels
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint32_t v[32];
-                tc_ld32(tmem + lanes + kColY + wg * 64 + k * 32, v);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    *reinterpret_cast<uint4*>(stage + t * kTile + (((8 * k + i) ^ (t & 7)) << 2)) =
-                        make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-            }
-            wg_sync(wg);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const int row = row0 + j;
-                float4 v = *reinterpret_cast<const float4*>(stage + row * kTile + ((qd ^ (row & 7)) << 2));
-                const uint2 x = *reinterpret_cast<const uint2*>(sX + tc_chunk(row, qd / 2) + (qd & 1) * 8);
-                v.x = fmaf(Dh, bf16_lo(x.x) + bf16_lo(xlo[j].x), v.x);
-                v.y = fmaf(Dh, bf16_hi(x.x) + bf16_hi(xlo[j].x), v.y);
-                v.z = fmaf(Dh, bf16_lo(x.y) + bf16_lo(xlo[j].y), v.z);
-                v.w = fmaf(Dh, bf16_hi(x.y) + bf16_hi(xlo[j].y), v.w);
-                if (zg) {
-                    const float4 z = gate[j].get();
-                    v.x *= silu(z.x);
-                    v.y *= silu(z.y);
-                    v.z *= silu(z.z);
-                    v.w *= silu(z.w);
+                for (int j = 0; j < kToks + 3; ++j) {
+                    raw[j].load(f, (tk + j >= 0 && tk + j < s.len) ? nq : 0);
+                    f += p.xbc_t;
                 }
-                Quad4<TIO, VEC>::store(yg + static_cast<int64_t>(tok0 + row) * p.y_t, row < nt ? nq : 0, v);
+            };
+            const TIO* dg = static_cast<const TIO*>(p.dt_raw) + s.row0 * p.dt_t + h;
+            auto load_dt = [&](int ch) {
+                const int tk = ch * kQ + t;
+                return (on && tk < s.len) ? to_f32<TIO>(dg[static_cast<int64_t>(tk) * p.dt_t]) : 0.f;
+            };
+            float dt_next = 0.f;
+            // x and z of a chunk into L2, a chunk ahead of their loads: one thread per row of 128 bytes, half
+            // the threads for x and half for z
+            auto prefetch = [&](int ch) {
+                const int tk = ch * kQ + t;
+                if (np <= 0 || tk >= s.len) return;
+                const TIO* f = hf == 0 ? static_cast<const TIO*>(p.xbc) + (s.row0 + tk) * p.xbc_t + cx
+                                       : static_cast<const TIO*>(p.z) + (s.row0 + tk) * p.z_t + cx;
+                if (hf == 0 || (kOut && p.z)) asm volatile("prefetch.global.L2 [%0];" ::"l"(f));
+            };
+            if (c.ch0 < ch1) {
+                prefetch(c.ch0);
+                dt_next = load_dt(c.ch0);
+                // (the last piece's products are complete: this thread has waited for them)
+                if (issue && !(PASS == Pass::kStates && ends)) load_bc(c.ch0);
             }
-            tma_store_fence();
-        }
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-    }
-    if (*abort && tid == 0) {                                          // a copy in flight lands before the block ends
-        const long long t0 = clock64();
-        while (!mbar_try_wait(&sh.bar_bc, (ch1 - ch0 - 1) & 1) && clock64() - t0 < (1ll << 28)) {
-        }
-    }
-    if (STATE_ONLY) {
-        if (on) {
-            keep_segment(seg);
-            if (t == 0) q.seg_decay[segment(seg)] = decay_sum;
-        }
-    } else if (s.slot >= 0) {
-        if (last && on && t < p.N) {
-            float* f = const_cast<float*>(slot_state);
+
+            // The state that enters: thread = state n, registers = rows hf·32 .. of the tile.
+            // A time-split sequence must not read its slot in the second pass (the last segment's CTA may
+            // have written it already): the first pass runs segment 0 from it and puts a copy in the place
+            // of the last segment, which that pass does not run.
+            float S[32];
+            float* slot_state = p.state + ((static_cast<int64_t>(max(s.slot, 0)) * p.H + h) * p.P + p0 + hf * 32) * p.N + t;
+            const int my_rows = np - hf * 32;
+            auto segment = [&](int j) { return static_cast<int64_t>(q.seg_base[c.seq] + j) * q.gtiles + gtile; };
+            auto saved = [&](float* base, int64_t at) {                // [16][128][4] floats per tile
+                return reinterpret_cast<float4*>(base + at * (kQ * kTile)) + hf * 8 * kQ + t;
+            };
+            auto add_saved = [&](const float4* l, float d) {
 #pragma unroll
-            for (int i = 0; i < kTile; ++i)
-                if (i < np) f[static_cast<int64_t>(i) * p.N] = S[i];
+                for (int i = 0; i < 8; ++i) {
+                    const float4 v = __ldcg(l + i * kQ);
+                    S[4 * i] = fmaf(d, S[4 * i], v.x);
+                    S[4 * i + 1] = fmaf(d, S[4 * i + 1], v.y);
+                    S[4 * i + 2] = fmaf(d, S[4 * i + 2], v.z);
+                    S[4 * i + 3] = fmaf(d, S[4 * i + 3], v.w);
+                }
+            };
+            auto save = [&](float4* l) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) __stcg(l + i * kQ, make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]));
+            };
+            const int seg = c.seg, nsegs = (c.nchunks + q.seg_chunks - 1) / q.seg_chunks;
+            const int64_t chain = (static_cast<int64_t>(c.seq) * q.pairs + c.pair) * 2 + wg;
+            const bool from_slot = s.warm && t < p.N &&
+                                   (PASS == Pass::kStates ? begins || ends : PASS == Pass::kWaves ? begins : nsegs == 1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) S[i] = (from_slot && i < my_rows) ? slot_state[static_cast<int64_t>(i) * p.N] : 0.f;
+            if (PASS == Pass::kStates && ends) {
+                if (on) save(saved(q.seg_state, segment(nsegs - 1)));
+                return;
+            }
+            if (PASS == Pass::kSegments && on && nsegs > 1) {
+                if (seg == 0) add_saved(saved(q.seg_state, segment(nsegs - 1)), 0.f);
+                for (int j = 0; j < seg; ++j) add_saved(saved(q.seg_state, segment(j)), ex2(q.seg_decay[segment(j)]));
+            }
+            if (PASS == Pass::kWaves && !begins) {                      // what the segment before left
+                if (t == 0 && hf == 0) wait_flag(q.flags + chain, seg, abort, p.err);
+                tile_sync();
+                add_saved(saved(q.handover, chain), 0.f);
+            }
+            auto state_tile = [&]() {                                   // S rounded, for C·S
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    *reinterpret_cast<uint4*>(sS + tc_chunk(t, hf * 4 + k)) =
+                        make_uint4(pack_bf16(S[8 * k], S[8 * k + 1]), pack_bf16(S[8 * k + 2], S[8 * k + 3]),
+                                   pack_bf16(S[8 * k + 4], S[8 * k + 5]), pack_bf16(S[8 * k + 6], S[8 * k + 7]));
+            };
+            if (kOut && c.ch0 < ch1) {
+                state_tile();
+                tma_store_fence();
+                warp_arrive(&sh.y_free);
+            }
+
+            const float A2 = on ? -expf(p.A_log[h]) * kLog2e : 0.f, dbias = (on && p.dt_bias) ? p.dt_bias[h] : 0.f;
+            const float Dh = (on && p.D) ? p.D[h] : 0.f;
+            auto load_weights = [&](float2 (&wk)[2][4], float2 (&wb)[2]) {
+                float4 f[4];
+                float b[4];
+                const float* w = p.conv_w + static_cast<int64_t>(cx + 4 * qd) * 4;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (VEC)
+                        f[i] = i < nq ? *reinterpret_cast<const float4*>(w + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    else
+                        f[i] = i < nq ? make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3])
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+                    b[i] = (i < nq && p.conv_b) ? p.conv_b[cx + 4 * qd + i] : 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    wk[i][0] = make_float2(f[2 * i].x, f[2 * i + 1].x);
+                    wk[i][1] = make_float2(f[2 * i].y, f[2 * i + 1].y);
+                    wk[i][2] = make_float2(f[2 * i].z, f[2 * i + 1].z);
+                    wk[i][3] = make_float2(f[2 * i].w, f[2 * i + 1].w);
+                    wb[i] = make_float2(b[2 * i], b[2 * i + 1]);
+                }
+            };
+            float decay_sum = 0.f;
+
+            for (int ch = c.ch0; ch < ch1; ++ch, ++it) {
+                const uint32_t ph = it & 1;
+                const int tok0 = ch * kQ, nt = min(kQ, s.len - tok0);
+                if (kOut && issue) {                                    // scores, and C·S of both tiles
+                    mbar_wait_bounded(&sh.bc, ph, abort, p.err);
+                    for (int k = 0; k < 4 * q.nb; ++k) {
+                        const uint32_t at = (k / 4) * kBlock + (k % 4) * 32;
+                        tc_mma(tmem + kColScore, tc_desc(c_at + at, 16, 1024), tc_desc(b_at + at, 16, 1024),
+                               tc_idesc(128, 128, false, false), k > 0);
+                    }
+                    mbar_wait_bounded(&sh.y_free, ph, abort, p.err);
+                    tc_fence_after();
+                    for (int k = 0; k < 4 * q.nb; ++k)
+                        tc_mma(tmem + kColY, tc_desc(c_at + (k / 4) * kBlock + (k % 4) * 32, 16, 1024),
+                               tc_desc(x_at + 3 * kBlock + k * 2048, kTileBytes, 1024), tc_idesc(128, 128, false, true), k > 0);
+                    tc_commit(&sh.cs);
+                }
+                __syncwarp();
+                load_x(ch);
+                if (ch + 1 < ch1) prefetch(ch + 1);
+                float2 wk[2][4], wb[2];
+                load_weights(wk, wb);
+                // time steps: thread = token (both warpgroups of a tile compute them all)
+                const float dt = (on && t < nt) ? softplus(dt_next + dbias) : 0.f;
+                const float a = dt * A2;
+                float l = a, r = __shfl_down_sync(0xffffffffu, a, 1);   // sums up to t, and after t, in the block of 32
+                if (lane == 31) r = 0.f;
+#pragma unroll
+                for (int o = 1; o < 32; o *= 2) {
+                    const float u = __shfl_up_sync(0xffffffffu, l, o), d = __shfl_down_sync(0xffffffffu, r, o);
+                    if (lane >= o) l += u;
+                    if (lane + o < 32) r += d;
+                }
+                if (lane == 31 && hf == 0) tab.total[warp] = l;
+                tile_sync();                                            // (also: the last chunk's y is out of its stage)
+                float before = 0.f, all = 0.f, after = r;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const float v = tab.total[w];
+                    all += v;
+                    if (w < warp) before += v;
+                    if (w > warp) {
+                        if (kOut && hf == 0) tab.fac[(w - 1) * w / 2 * 32 + t] = dt * ex2(after);   // blocks 1, 2, 3 at 0, 32, 96
+                        after += v;
+                    }
+                }
+                if (hf == 0) tab.tail[t] = dt * ex2(after);
+                decay_sum += all;
+                // x, through the convolution
+                float4 e0 = raw[0].get(), e1 = raw[1].get(), e2 = raw[2].get();
+                if (ch == 0 && row0 == 0 && s.warm) {
+                    float v[3][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        HeadsWindow w = {{0.f, 0.f, 0.f}};
+                        if (i < nq) w = heads_window(p, s, cx + 4 * qd + i);
+                        v[0][i] = w.v[0];
+                        v[1][i] = w.v[1];
+                        v[2][i] = w.v[2];
+                    }
+                    e0 = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
+                    e1 = make_float4(v[1][0], v[1][1], v[1][2], v[1][3]);
+                    e2 = make_float4(v[2][0], v[2][1], v[2][2], v[2][3]);
+                }
+                tile_sync();
+                // (rows past the sequence's end hold silu(conv_b): their Δ is zero, so nothing reads them)
+                uint2 xlo[kToks];                                       // what bf16 leaves of x, for D·x
+#pragma unroll
+                for (int j = 0; j < kToks; ++j) {
+                    const int row = row0 + j;
+                    const float2 m = splat2(tab.tail[row]);
+                    const float4 f = raw[j + 3].get();
+                    const float2 u0 = heads_conv2(wk[0], wb[0], make_float2(e0.x, e0.y), make_float2(e1.x, e1.y),
+                                                  make_float2(e2.x, e2.y), make_float2(f.x, f.y));
+                    const float2 u1 = heads_conv2(wk[1], wb[1], make_float2(e0.z, e0.w), make_float2(e1.z, e1.w),
+                                                  make_float2(e2.z, e2.w), make_float2(f.z, f.w));
+                    e0 = e1;
+                    e1 = e2;
+                    e2 = f;
+                    const uint32_t off = tc_chunk(row, qd / 2) + (qd & 1) * 8;
+                    if (kOut) {
+                        const uint2 x = make_uint2(pack_bf16(u0.x, u0.y), pack_bf16(u1.x, u1.y));
+                        *reinterpret_cast<uint2*>(sX + off) = x;
+                        xlo[j] = make_uint2(pack_rest(u0, x.x), pack_rest(u1, x.y));
+                    }
+                    const float2 t0 = mul2(u0, m), t1 = mul2(u1, m);
+                    const uint2 x = make_uint2(pack_bf16(t0.x, t0.y), pack_bf16(t1.x, t1.y));
+                    *reinterpret_cast<uint2*>(sXh + off) = x;
+                    *reinterpret_cast<uint2*>(sXl + off) = make_uint2(pack_rest(t0, x.x), pack_rest(t1, x.y));
+                }
+                tma_store_fence();
+                warp_arrive(&sh.x_ready);
+                if (issue) {                                            // what the chunk adds to the state, both tiles side by side
+                    if (!kOut) mbar_wait_bounded(&sh.bc, ph, abort, p.err);
+                    mbar_wait_bounded(&sh.x_ready, ph, abort, p.err);
+                    tc_fence_after();
+                    for (int k = 0; k < 8; ++k) {
+                        const uint64_t bh = tc_desc(b_at + k * 2048, kBlock, 1024), bl = tc_desc(b_at + kImage + k * 2048, kBlock, 1024);
+                        const uint64_t xh = tc_desc(x_at + kBlock + k * 2048, kTileBytes, 1024),
+                                       xl = tc_desc(x_at + 2 * kBlock + k * 2048, kTileBytes, 1024);
+                        constexpr uint32_t id = tc_idesc(128, 128, true, true);
+                        tc_mma(tmem + kColS, bh, xl, id, k > 0);
+                        tc_mma(tmem + kColS, bl, xh, id, true);
+                        tc_mma(tmem + kColS, bh, xh, id, true);
+                    }
+                    tc_commit(&sh.st);
+                }
+                __syncwarp();
+                if (kOut) {
+                    wait(&sh.cs, ph);
+                    // exp2(l)·(C·S)
+                    {
+                        const float2 carry = splat2(ex2(before + l));
+                        uint32_t v[32];
+                        tc_ld32(lanes + kColY + wg * 64 + hf * 32, v);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 y = mul2(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), carry);
+                            v[i] = __float_as_uint(y.x);
+                            v[i + 1] = __float_as_uint(y.y);
+                        }
+                        tc_st32(lanes + kColY + wg * 64 + hf * 32, v);
+                    }
+                    // P: thread = row t; the blocks of 32 columns before its own by a product of two decays, its own
+                    // by the decay itself, the ones after it zero.  One warpgroup has blocks 0 and 3, the other 1 and 2.
+                    const float2 mine = splat2(ex2(l));
+                    const float back = l - lg2_approx(dt);              // exp2(l_t - back_s) = Δ_s · decay from s to t
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int j = hf == 0 ? 3 * k : 1 + k;
+                        uint32_t o[16];
+                        if (j <= warp) {
+                            uint32_t v[32];
+                            tc_ld32(lanes + kColScore + j * 32, v);
+                            if (j < warp) {
+                                const float4* f = reinterpret_cast<const float4*>(&tab.fac[(warp - 1) * warp / 2 * 32 + j * 32]);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const float4 w = f[i];
+                                    const float2 a0 = mul2(mul2(make_float2(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])),
+                                                                make_float2(w.x, w.y)), mine);
+                                    const float2 a1 = mul2(mul2(make_float2(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])),
+                                                                make_float2(w.z, w.w)), mine);
+                                    o[2 * i] = pack_bf16(a0.x, a0.y);
+                                    o[2 * i + 1] = pack_bf16(a1.x, a1.y);
+                                }
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) {
+                                    const float w = __uint_as_float(v[i]) * ex2(l - __shfl_sync(0xffffffffu, back, i));
+                                    v[i] = i <= lane ? __float_as_uint(w) : 0u;
+                                }
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[i] = pack_bf16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = 0u;
+                        }
+                        tc_st16(lanes + kColP + wg * 64 + j * 16, o);
+                    }
+                    tc_wait_st();
+                    tc_fence_before();
+                    warp_arrive(&sh.p_ready[wg]);
+                    if (issue_pv) {
+                        mbar_wait_bounded(&sh.p_ready[wg], ph, abort, p.err);
+                        tc_fence_after();
+                        for (int k = 0; k < 8; ++k)
+                            tc_mma_ta(tmem + kColY + wg * 64, tmem + kColP + wg * 64 + k * 8,
+                                      tc_desc(x_at + wg * kTileBytes + k * 2048, 16, 1024), tc_idesc(128, 64, false, true), true);
+                        tc_commit(&sh.pv[wg]);
+                    }
+                    __syncwarp();
+                }
+                // the state
+                wait(&sh.st, ph);
+                if (issue && ch + 1 < ch1 && !*abort) load_bc(ch + 1);   // the products that read B and C are complete
+                __syncwarp();
+                {
+                    const float2 d = splat2(ex2(all));
+                    uint32_t v[32];
+                    tc_ld32(lanes + kColS + wg * 64 + hf * 32, v);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 n = fma2(d, make_float2(S[i], S[i + 1]), make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+                        S[i] = n.x;
+                        S[i + 1] = n.y;
+                    }
+                }
+                if (ch + 1 < ch1) dt_next = load_dt(ch + 1);
+                if (kOut) {
+                    if (ch + 1 < ch1) state_tile();
+                    Quad4<TIO, VEC> gate[kToks];
+                    if (p.z) {
+                        const TIO* z = static_cast<const TIO*>(p.z) + (s.row0 + tok0 + row0) * p.z_t + cx + 4 * qd;
+#pragma unroll
+                        for (int j = 0; j < kToks; ++j) {
+                            gate[j].load(z, row0 + j < nt ? nq : 0);
+                            z += p.z_t;
+                        }
+                    }
+                    wait(&sh.pv[wg], ph);
+                    // y: rows out of tensor memory, through shared memory, so that 16 threads write a token's 64 channels
+                    {
+                        uint32_t v[32];
+                        tc_ld32(lanes + kColY + wg * 64 + hf * 32, v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<uint4*>(stage + t * kTile + (((8 * hf + i) ^ (t & 7)) << 2)) =
+                                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    }
+                    if (ch + 1 < ch1) {                                 // the next C·S may begin
+                        tma_store_fence();
+                        tc_fence_before();
+                        warp_arrive(&sh.y_free);
+                    }
+                    tile_sync();
+                    TIO* y = static_cast<TIO*>(p.y) + (s.row0 + tok0 + row0) * p.y_t + cx + 4 * qd;
+#pragma unroll
+                    for (int j = 0; j < kToks; ++j) {
+                        const int row = row0 + j;
+                        const float4 v = *reinterpret_cast<const float4*>(stage + row * kTile + ((qd ^ (row & 7)) << 2));
+                        const uint2 x = *reinterpret_cast<const uint2*>(sX + tc_chunk(row, qd / 2) + (qd & 1) * 8);
+                        const float2 Dd = splat2(Dh);
+                        float2 y0 = fma2(Dd, add2(unpack2(x.x), unpack2(xlo[j].x)), make_float2(v.x, v.y));
+                        float2 y1 = fma2(Dd, add2(unpack2(x.y), unpack2(xlo[j].y)), make_float2(v.z, v.w));
+                        if (p.z) {
+                            const float4 z = gate[j].get();
+                            y0 = mul2(y0, silu2_joint(make_float2(z.x, z.y)));
+                            y1 = mul2(y1, silu2_joint(make_float2(z.z, z.w)));
+                        }
+                        Quad4<TIO, VEC>::store(y, row < nt ? nq : 0, make_float4(y0.x, y0.y, y1.x, y1.y));
+                        y += p.y_t;
+                    }
+                }
+            }
+            if (PASS == Pass::kStates) {
+                if (on) {
+                    save(saved(q.seg_state, segment(seg)));
+                    if (t == 0 && hf == 0) q.seg_decay[segment(seg)] = decay_sum;
+                }
+                return;
+            }
+            if (!ends && PASS == Pass::kWaves) {                        // for the segment after this one
+                save(saved(q.handover, chain));
+                __threadfence();
+                tile_sync();
+                if (t == 0 && hf == 0)
+                    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(q.flags + chain), "r"(static_cast<unsigned>(seg) + 1u) : "memory");
+            }
+            if (s.slot < 0) return;
+            if (ends && on && t < p.N)
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (i < my_rows) slot_state[static_cast<int64_t>(i) * p.N] = S[i];
+            // the CTA that begins the sequence alone reads its x channels' windows: it shifts them
+            if (begins) {
+                tile_sync();
+                for (int k = hf * 128 + t; k < np; k += 256) heads_keep_window<TIO>(p, s, cx + k);
+            }
+        });
+        if (issue && *abort) {                                         // a copy in flight lands before the block ends
+            const long long t0 = clock64();
+            while (!mbar_try_wait(&sh.bc, (it - 1) & 1) && !mbar_try_wait(&sh.bc, it & 1) && clock64() - t0 < (1ll << 28)) {
+            }
         }
-        // the first segment's CTA alone reads its x channels' windows: it shifts them
-        if (seg == 0)
-            for (int k = t; k < np; k += 128) heads_keep_window<TIO>(p, s, cx + k);
     }
+    tc_fence_before();
     __syncthreads();
     if (tid / 32 == 0) tc_dealloc(tmem, kTmemCols);
 }
 
-// Segments per sequence, for sequences of equal length, in units of a chunk's time: a segment costs a
-// first pass of about 0.45 of a full one (no scores, no outputs) and a prologue, the whole call two
-// launches; what it buys is CTAs, one to an SM.
-int segments_for(int64_t n_seq, int64_t chunks, int64_t pairs, int64_t sms) {
+// Segments per sequence of the time split (1: none), for sequences of equal length, in units of a chunk's
+// time.  Without it no more CTAs run than there are chains (sequences times pairs of tiles).  With it a
+// segment costs a first pass of about 0.45 of a full one (no scores, no outputs) and a prologue, the
+// whole call one more launch.
+int segments_for(int64_t chains, int64_t chunks, int64_t sms) {
     auto waves = [&](int64_t ctas) { return (ctas + sms - 1) / sms; };
     int best = 1;
-    double cost = static_cast<double>(waves(n_seq * pairs)) * static_cast<double>(chunks + 1);
+    double cost = static_cast<double>(chains * chunks) / static_cast<double>(std::min(chains, sms)) + 1.0;
     for (int k = 2; k <= 64 && k <= chunks; ++k) {
         const double len = static_cast<double>((chunks + k - 1) / k);
-        const double c = waves(n_seq * pairs * k) * (len + 1.5) + waves(n_seq * pairs * (k - 1)) * (0.45 * len + 1.0) + 2.0;
+        const double c = waves(chains * k) * (len + 1.5) + waves(chains * (k - 1)) * (0.45 * len + 1.0) + 2.0;
         if (c < cost) {
             cost = c;
             best = k;
@@ -657,6 +800,11 @@ int segments_for(int64_t n_seq, int64_t chunks, int64_t pairs, int64_t sms) {
     }
     return best;
 }
+
+// Chunks per segment of the waves: short ones, so that the last wave leaves little idle, unless there
+// are so many chains that whole sequences do as well.
+constexpr int kWaveChunks = 4;
+constexpr int kManyChains = 8;           // per SM
 
 int sm_count() {
     int dev = 0, n = 0;
@@ -669,6 +817,19 @@ int sm_count() {
 
 size_t padded(size_t n) { return (n + 255) / 256 * 256; }
 
+template <typename TIO, bool VEC, Pass PASS>
+cudaError_t launch_pass(const HeadsTcParams& q, unsigned grid, cudaStream_t stream) {
+    void (*kern)(const HeadsTcParams) = heads_tc_kernel<TIO, VEC, PASS>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+    if (e != cudaSuccess) return e;
+    if (PASS == Pass::kWaves) {                       // CTAs wait for one another: all of them at once
+        void* args[] = {const_cast<HeadsTcParams*>(&q)};
+        return cudaLaunchCooperativeKernel(reinterpret_cast<void*>(kern), dim3(grid), dim3(kTcThreads), args, kTcSmem, stream);
+    }
+    kern<<<grid, kTcThreads, kTcSmem, stream>>>(q);
+    return cudaGetLastError();
+}
+
 template <typename TIO, bool VEC>
 cudaError_t launch_typed(const HeadsTcParams& q, const HeadsTcPlan& plan, cudaStream_t stream) {
     static_assert(sizeof(TIO) == 2, "bf16 operands of the products carry bf16 inputs");
@@ -676,17 +837,10 @@ cudaError_t launch_typed(const HeadsTcParams& q, const HeadsTcPlan& plan, cudaSt
     heads_prep_kernel<TIO, VEC><<<prep, kPrepThreads, 0, stream>>>(q);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    if (!plan.split) return launch_pass<TIO, VEC, Pass::kWaves>(q, static_cast<unsigned>(plan.ctas), stream);
     const unsigned grid = static_cast<unsigned>(plan.segments * plan.pairs);
-    if (plan.split) {
-        e = cudaFuncSetAttribute(heads_tc_kernel<TIO, VEC, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
-        if (e != cudaSuccess) return e;
-        heads_tc_kernel<TIO, VEC, true><<<grid, kTcThreads, kTcSmem, stream>>>(q);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    e = cudaFuncSetAttribute(heads_tc_kernel<TIO, VEC, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
-    if (e != cudaSuccess) return e;
-    heads_tc_kernel<TIO, VEC, false><<<grid, kTcThreads, kTcSmem, stream>>>(q);
-    return cudaGetLastError();
+    e = launch_pass<TIO, VEC, Pass::kStates>(q, grid, stream);
+    return e != cudaSuccess ? e : launch_pass<TIO, VEC, Pass::kSegments>(q, grid, stream);
 }
 
 }  // namespace
@@ -708,10 +862,13 @@ HeadsTcPlan heads_tc_plan(int64_t n_seq, int64_t tokens, int64_t H, int64_t P, i
     plan.pairs = static_cast<int>(G * ((H / G * tiles + 1) / 2));
     plan.chunks = tokens / kHeadsChunk + n_seq;
     const int64_t mean = (tokens / n_seq + kHeadsChunk - 1) / kHeadsChunk;
-    const int k = segments_for(n_seq, std::max<int64_t>(mean, 1), plan.pairs, sm_count());
+    const int sms = sm_count();
+    const int64_t chains = n_seq * plan.pairs;
+    const int k = segments_for(chains, std::max<int64_t>(mean, 1), sms);
     plan.split = k > 1;
-    plan.seg_chunks = plan.split ? static_cast<int>((mean + k - 1) / k) : INT32_MAX / 2;
-    plan.segments = (plan.split ? plan.chunks / plan.seg_chunks : 0) + n_seq;
+    const bool whole = !plan.split && chains > kManyChains * sms;
+    plan.seg_chunks = plan.split ? static_cast<int>((mean + k - 1) / k) : whole ? INT32_MAX / 2 : kWaveChunks;
+    plan.segments = plan.chunks / plan.seg_chunks + n_seq;
     size_t at = 0;
     auto take = [&](size_t n) {
         const size_t here = at;
@@ -719,11 +876,16 @@ HeadsTcPlan heads_tc_plan(int64_t n_seq, int64_t tokens, int64_t H, int64_t P, i
         return here;
     };
     plan.off_images = take(static_cast<size_t>(plan.chunks) * G * 3 * plan.nb * kBlock);
-    plan.off_chunk_base = take(static_cast<size_t>(n_seq) * 4);
+    plan.off_chunk_base = take(static_cast<size_t>(n_seq + 1) * 4);
     plan.off_seg_base = take(static_cast<size_t>(n_seq + 1) * 4);
     const size_t states = plan.split ? static_cast<size_t>(plan.segments) * plan.gtiles : 0;
     plan.off_state = take(states * kQ * kTile * 4);
     plan.off_decay = take(states * 4);
+    plan.ctas = static_cast<int>(std::min<int64_t>(chains, sms));
+    plan.chains = plan.split || whole ? 0 : static_cast<int>(chains);
+    plan.off_handover = take(static_cast<size_t>(plan.chains) * 2 * kQ * kTile * 4);
+    plan.off_flags = take(static_cast<size_t>(plan.chains) * 2 * 4);
+    plan.off_order = take(static_cast<size_t>(plan.segments) * 8);
     plan.bytes = at;
     return plan;
 }
@@ -739,13 +901,18 @@ cudaError_t launch_heads_tc(const HeadsParams& p, void* workspace, bool bf16, cu
     q.seg_base = reinterpret_cast<int32_t*>(w + plan.off_seg_base);
     q.seg_state = reinterpret_cast<float*>(w + plan.off_state);
     q.seg_decay = reinterpret_cast<float*>(w + plan.off_decay);
+    q.handover = reinterpret_cast<float*>(w + plan.off_handover);
+    q.flags = reinterpret_cast<unsigned int*>(w + plan.off_flags);
+    q.nflags = 2 * plan.chains;
+    q.order = reinterpret_cast<int32_t*>(w + plan.off_order);
     q.seg_chunks = plan.seg_chunks;
     q.pairs = plan.pairs;
     q.gtiles = plan.gtiles;
     q.nb = plan.nb;
     // four channels in one access: z, x, B, C and y of every head and group on that boundary
     auto wide = [&](const void* base, int64_t stride) { return host::is_aligned(base, 8) && stride % 4 == 0; };
-    const bool vec = p.P % 4 == 0 && p.N % 4 == 0 && wide(p.xbc, p.xbc_t) && wide(p.z, p.z_t) && wide(p.y, p.y_t);
+    const bool vec = p.P % 4 == 0 && p.N % 4 == 0 && host::is_aligned(p.conv_w, 16) && wide(p.xbc, p.xbc_t) &&
+                     wide(p.z, p.z_t) && wide(p.y, p.y_t);
     return vec ? launch_typed<__nv_bfloat16, true>(q, plan, stream) : launch_typed<__nv_bfloat16, false>(q, plan, stream);
 }
 

@@ -105,5 +105,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+__device__ __forceinline__ float2 unpack2(uint32_t u) { return make_float2(bf16_lo(u), bf16_hi(u)); }
+// What rounding to the pair `u` left of v, rounded in turn.
+__device__ __forceinline__ uint32_t pack_rest(float2 v, uint32_t u) {
+    const float2 r = add2(v, make_float2(-bf16_lo(u), -bf16_hi(u)));
+    return pack_bf16(r.x, r.y);
+}
 
 }  // namespace selscan
