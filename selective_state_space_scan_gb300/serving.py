@@ -10,68 +10,109 @@ import ctypes
 
 import selective_state_space_scan_gb300 as _ss
 
+_HEADS_BYTES = {}
 _HEADS_WS = {}
+_IO = {}
+_torch = None
+_lib = None
 
 
-def _tensor(t, name, shape=None, dtype=None, contiguous=False, device=None):
-    """Refuses what the C call cannot see: types, shapes, layouts and devices of tensors."""
-    if t is None:
-        return
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{name} must be a CUDA tensor" + ("" if device is None else f" on {device}"))
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if not contiguous:
-        _ss._check_inner(t, name)
+def _load():
+    """The torch module and the library, looked up once: the calls below are made once per layer and
+    token, where a few microseconds of marshalling are as long as the kernels."""
+    global _torch, _lib
+    if _torch is None:
+        import torch
+        _lib = _ss.lib()
+        _IO.update({torch.float32: _ss.SS_F32, torch.bfloat16: _ss.SS_BF16})
+        _torch = torch
+    return _torch
+
+
+def _io(dtype):
+    code = _IO.get(dtype)
+    return _ss._io_code(dtype) if code is None else code      # (which refuses other types)
+
+
+def _stream(t, stream):
+    """Handle of the stream that the call runs on."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _empty(shape, dtype, device, stream):
     """An output allocated on the stream that the call runs on, so that its memory is not handed to
     another stream's work while the call may still write it."""
-    import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _torch.empty(shape, dtype=dtype, device=device)
+    with _torch.cuda.stream(stream):
+        return _torch.empty(shape, dtype=dtype, device=device)
 
 
-def _row_stride(t):
-    return 0 if t is None else t.stride(0)
+def _workspace(t, stream, handle, nbytes):
+    """The heads calls' workspace: one buffer per device and stream, zero-filled when it is made."""
+    key = (t.get_device(), handle)
+    ws = _HEADS_WS.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = _HEADS_WS[key] = _ss.workspace_for(t.device, stream, nbytes, purpose="heads")
+    return ws
 
 
-def _heads_args(xbc, dt_raw, conv_w, conv_b, dt_bias, A_log, D, z, state, window, y, ints, stream):
-    import torch
-    io = _ss._io_code(xbc.dtype)
-    dev, f32 = xbc.device, torch.float32
-    if state.dim() != 4:
-        raise ValueError("state must be [slots, H, P, N]")
+def _param(t, name, dtype, shape):
+    """Refuses a contiguous operand of another type, shape or layout (None passes)."""
+    if t is None or (t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        return
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(t, name, dtype, shape):
+    """The same for a two-dimensional operand with any row stride: returns the stride (0 for None)."""
+    if t is None:
+        return 0
+    stride = t.stride()
+    if t.dtype is dtype and t.shape == shape and (stride[1] == 1 or shape[1] <= 1):
+        return stride[0]
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name}: the last axis must have stride 1")
+
+
+def _cuda(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+
+
+def _heads_args(xbc, dt_raw, conv_w, conv_b, dt_bias, A_log, D, z, state, window, y, stream):
+    torch = _load()
+    _cuda(xbc, "xbc")
+    dtype, f32 = xbc.dtype, torch.float32
+    if state.dim() != 4 or xbc.dim() != 2:
+        raise ValueError("state must be [slots, H, P, N] and xbc [rows, channels]")
     n_slots, H, P, N = state.shape
     T, C = xbc.shape
-    bc = C - H * P
-    if bc <= 0 or bc % (2 * N):
+    HP = H * P
+    G, rest = divmod(C - HP, 2 * N) if N else (0, 1)
+    if G <= 0 or rest:
         raise ValueError(f"xbc has {C} channels: H*P + 2*G*N are wanted (H, P, N = {H}, {P}, {N})")
-    G = bc // (2 * N)
     if y is None:
-        y = _empty((T, H * P), xbc.dtype, dev, stream)
-    _tensor(xbc, "xbc")
-    _tensor(dt_raw, "dt_raw", (T, H), xbc.dtype, device=dev)
-    _tensor(z, "z", (T, H * P), xbc.dtype, device=dev)
-    _tensor(y, "y", (T, H * P), xbc.dtype, device=dev)
-    _tensor(conv_w, "conv_w", (C, 4), f32, True, dev)
-    _tensor(conv_b, "conv_b", (C,), f32, True, dev)
-    _tensor(dt_bias, "dt_bias", (H,), f32, True, dev)
-    _tensor(A_log, "A_log", (H,), f32, True, dev)
-    _tensor(D, "D", (H,), f32, True, dev)
-    _tensor(state, "state", None, f32, True, dev)
-    _tensor(window, "window", (n_slots, C, 3), f32, True, dev)
-    for name, t, n in ints:
-        _tensor(t, name, (n,), torch.int32, True, dev)
-    s = _ss.HeadsStrides(io, _row_stride(xbc), _row_stride(dt_raw), _row_stride(z), _row_stride(y))
-    return io, y, T, H, P, G, N, n_slots, s
+        y = _empty((T, HP), dtype, xbc.device, stream)
+    s = _ss.HeadsStrides(_io(dtype), _rows(xbc, "xbc", dtype, (T, C)), _rows(dt_raw, "dt_raw", dtype, (T, H)),
+                         _rows(z, "z", dtype, (T, HP)), _rows(y, "y", dtype, (T, HP)))
+    _param(conv_w, "conv_w", f32, (C, 4))
+    _param(conv_b, "conv_b", f32, (C,))
+    _param(dt_bias, "dt_bias", f32, (H,))
+    _param(A_log, "A_log", f32, (H,))
+    _param(D, "D", f32, (H,))
+    _param(state, "state", f32, state.shape)
+    _param(window, "window", f32, (n_slots, C, 3))
+    return y, T, H, P, G, N, n_slots, s
 
 
 def ss_heads_fwd(xbc, dt_raw, conv_w, A_log, state, window, cu_seqlens, conv_b=None, dt_bias=None, D=None, z=None,
@@ -83,21 +124,23 @@ def ss_heads_fwd(xbc, dt_raw, conv_w, A_log, state, window, cu_seqlens, conv_b=N
     state [slots, H, P, N] and window [slots, C, 3] (float32) are the caches, updated in place.
     cu_seqlens [n+1] int32: sequence i is rows cu_seqlens[i] to cu_seqlens[i+1]; slots [n] int32 (None:
     slot i; negative: no slot); fresh [n] int32: non-zero starts from zeros.  Returns y [tokens, H*P]."""
+    y, T, H, P, G, N, n_slots, s = _heads_args(xbc, dt_raw, conv_w, conv_b, dt_bias, A_log, D, z, state, window, y, stream)
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must be [sequences + 1]")
-    n = cu_seqlens.shape[0] - 1
-    io, y, T, H, P, G, N, n_slots, s = _heads_args(
-        xbc, dt_raw, conv_w, conv_b, dt_bias, A_log, D, z, state, window, y,
-        (("cu_seqlens", cu_seqlens, n + 1), ("slots", slots, n), ("fresh", fresh, n)), stream)
-    key = (n, T, H, P, G, N, io)
-    nbytes = _HEADS_WS.get(key)
+    n, i32 = cu_seqlens.shape[0] - 1, _torch.int32
+    _param(cu_seqlens, "cu_seqlens", i32, (n + 1,))
+    _param(slots, "slots", i32, (n,))
+    _param(fresh, "fresh", i32, (n,))
+    key = (n, T, H, P, G, N, s.io_dtype)
+    nbytes = _HEADS_BYTES.get(key)
     if nbytes is None:
-        nbytes = _HEADS_WS[key] = int(_ss.lib().ss_heads_workspace_size(*key))
-    ws = _ss.workspace_for(xbc.device, stream, nbytes, purpose="heads") if nbytes else None
+        nbytes = _HEADS_BYTES[key] = int(_lib.ss_heads_workspace_size(*key))
+    handle = _stream(xbc, stream)
+    ws = _workspace(xbc, stream, handle, nbytes)
     p = _ss._ptr
-    st = _ss.lib().ss_heads_fwd(p(xbc), p(dt_raw), p(z), p(conv_w), p(conv_b), p(dt_bias), p(A_log), p(D), p(y), p(state),
-                                p(window), p(cu_seqlens), p(slots), p(fresh), n, T, H, P, G, N, n_slots, ctypes.byref(s),
-                                p(ws), 0 if ws is None else ws.numel(), _ss._stream_handle(stream))
+    st = _lib.ss_heads_fwd(xbc.data_ptr(), dt_raw.data_ptr(), p(z), conv_w.data_ptr(), p(conv_b), p(dt_bias), A_log.data_ptr(),
+                           p(D), y.data_ptr(), state.data_ptr(), window.data_ptr(), cu_seqlens.data_ptr(), p(slots), p(fresh),
+                           n, T, H, P, G, N, n_slots, ctypes.byref(s), ws.data_ptr(), ws.numel(), handle)
     if st != 0:
         raise _ss.SelscanError(st, "ss_heads_fwd")
     return y
@@ -108,35 +151,38 @@ def ss_heads_step(state, window, xbc, dt_raw, conv_w, A_log, conv_b=None, dt_bia
     """One token of every request (ss_heads_step): ss_heads_fwd's tensors with one row per request;
     slots [batch] int32 (None: slot b; negative: a padded row).  Updates state and window in place
     and returns y [batch, H*P]."""
-    n = xbc.shape[0]
-    io, y, T, H, P, G, N, n_slots, s = _heads_args(xbc, dt_raw, conv_w, conv_b, dt_bias, A_log, D, z, state, window, y,
-                                                   (("slots", slots, n),), stream)
-    nbytes = _HEADS_WS.get((n, G))
+    y, n, H, P, G, N, n_slots, s = _heads_args(xbc, dt_raw, conv_w, conv_b, dt_bias, A_log, D, z, state, window, y, stream)
+    _param(slots, "slots", _torch.int32, (n,))
+    key = (n, G)
+    nbytes = _HEADS_BYTES.get(key)
     if nbytes is None:
-        nbytes = _HEADS_WS[n, G] = int(_ss.lib().ss_heads_step_workspace_size(n, G))
-    ws = _ss.workspace_for(xbc.device, stream, nbytes, purpose="heads") if nbytes else None
+        nbytes = _HEADS_BYTES[key] = int(_lib.ss_heads_step_workspace_size(n, G))
+    handle = _stream(xbc, stream)
+    ws = _workspace(xbc, stream, handle, nbytes)
     p = _ss._ptr
-    st = _ss.lib().ss_heads_step(p(state), p(window), p(xbc), p(dt_raw), p(z), p(conv_w), p(conv_b), p(dt_bias), p(A_log),
-                                 p(D), p(y), p(slots), n, H, P, G, N, n_slots, ctypes.byref(s), p(ws),
-                                 0 if ws is None else ws.numel(), _ss._stream_handle(stream))
+    st = _lib.ss_heads_step(state.data_ptr(), window.data_ptr(), xbc.data_ptr(), dt_raw.data_ptr(), p(z), conv_w.data_ptr(),
+                            p(conv_b), p(dt_bias), A_log.data_ptr(), p(D), y.data_ptr(), p(slots), n, H, P, G, N, n_slots,
+                            ctypes.byref(s), ws.data_ptr(), ws.numel(), handle)
     if st != 0:
         raise _ss.SelscanError(st, "ss_heads_step")
     return y
 
 
-def _norm_args(x, weight, residual, residual_out, stream):
-    import torch
-    rows, D = x.shape
-    io = _ss._io_code(x.dtype)
-    rdt = x.dtype if residual is None else residual.dtype
-    res = _ss._io_code(rdt)
+def _norm_args(x, weight, residual, residual_out, y, ydtype, stream):
+    torch = _load()
+    _cuda(x, "x")
+    rows, D = shape = x.shape
+    dtype = x.dtype
+    rdt = dtype if residual is None else residual.dtype
     if residual_out is None:
-        residual_out = _empty((rows, D), rdt, x.device, stream)
-    _tensor(x, "x")
-    _tensor(weight, "weight", (D,), torch.float32, True, x.device)
-    _tensor(residual, "residual", (rows, D), rdt, device=x.device)
-    _tensor(residual_out, "residual_out", (rows, D), rdt, device=x.device)
-    return rows, D, io, res, residual_out
+        residual_out = _empty(shape, rdt, x.device, stream)
+    if y is None:
+        y = _empty(shape, ydtype or dtype, x.device, stream)
+    s = _ss.NormStrides(_io(dtype), _io(rdt), _rows(x, "x", dtype, shape),
+                        _rows(residual, "residual", rdt, shape), _rows(residual_out, "residual_out", rdt, shape),
+                        _rows(y, "y", ydtype or dtype, shape))
+    _param(weight, "weight", torch.float32, (D,))
+    return rows, D, residual_out, y, s
 
 
 def ss_add_rmsnorm(x, weight, residual=None, eps=1e-5, y=None, residual_out=None, stream=None):
@@ -144,15 +190,9 @@ def ss_add_rmsnorm(x, weight, residual=None, eps=1e-5, y=None, residual_out=None
 
     x [rows, D] and residual [rows, D]: float32 or bfloat16, each its own; weight [D] float32.
     Returns (y, residual_out): y like x, r in the residual's type (residual_out may be residual)."""
-    import torch
-    rows, D, io, res, residual_out = _norm_args(x, weight, residual, residual_out, stream)
-    if y is None:
-        y = _empty((rows, D), x.dtype, x.device, stream)
-    _tensor(y, "y", (rows, D), x.dtype, device=x.device)
-    s = _ss.NormStrides(io, res, x.stride(0), _row_stride(residual), residual_out.stride(0), y.stride(0))
-    p = _ss._ptr
-    st = _ss.lib().ss_add_rmsnorm(p(x), p(residual), p(weight), p(residual_out), p(y), rows, D, eps, ctypes.byref(s),
-                                  _ss._stream_handle(stream))
+    rows, D, residual_out, y, s = _norm_args(x, weight, residual, residual_out, y, None, stream)
+    st = _lib.ss_add_rmsnorm(x.data_ptr(), _ss._ptr(residual), weight.data_ptr(), residual_out.data_ptr(), y.data_ptr(), rows, D,
+                             eps, ctypes.byref(s), _stream(x, stream))
     if st != 0:
         raise _ss.SelscanError(st, "ss_add_rmsnorm")
     return y, residual_out
@@ -163,20 +203,15 @@ def ss_add_rmsnorm_f8(x, weight, residual=None, eps=1e-5, block=0, y=None, scale
 
     Returns (y, residual_out, scale): y[r, c] * scale[r, c // block] stands for the norm's output;
     scale is [rows, ceil(D / block)]."""
-    import torch
-    rows, D, io, res, residual_out = _norm_args(x, weight, residual, residual_out, stream)
-    f8 = torch.float8_e4m3fn
-    if y is None:
-        y = _empty((rows, D), f8, x.device, stream)
-    nb = -(-D // block) if block else 1
+    torch = _load()
+    rows, D, residual_out, y, s = _norm_args(x, weight, residual, residual_out, y, torch.float8_e4m3fn, stream)
+    nb = -(-D // block) if block > 0 else 1
     if scale is None:
         scale = _empty((rows, nb), torch.float32, x.device, stream)
-    _tensor(y, "y", (rows, D), f8, device=x.device)
-    _tensor(scale, "scale", (rows, nb), torch.float32, True, x.device)
-    s = _ss.NormStrides(io, res, x.stride(0), _row_stride(residual), residual_out.stride(0), y.stride(0))
-    p = _ss._ptr
-    st = _ss.lib().ss_add_rmsnorm_f8(p(x), p(residual), p(weight), p(residual_out), p(y), p(scale), rows, D, block, eps,
-                                     ctypes.byref(s), _ss._stream_handle(stream))
+    else:
+        _param(scale, "scale", torch.float32, (rows, nb))
+    st = _lib.ss_add_rmsnorm_f8(x.data_ptr(), _ss._ptr(residual), weight.data_ptr(), residual_out.data_ptr(), y.data_ptr(),
+                                scale.data_ptr(), rows, D, block, eps, ctypes.byref(s), _stream(x, stream))
     if st != 0:
         raise _ss.SelscanError(st, "ss_add_rmsnorm_f8")
     return y, residual_out, scale
@@ -189,21 +224,23 @@ def ss_sample(logits, noise, temperature=None, top_k=None, top_p=None, min_p=Non
     logits [rows, V] float32 or bfloat16; noise [rows, V] float32 draws of the exponential distribution;
     temperature, top_p, min_p [rows] float32 and top_k [rows] int32, each None for off.  Returns
     tokens [rows] int32 (-1 for a row without a finite logit)."""
-    import torch
-    rows, V = logits.shape
-    io, dev, f32 = _ss._io_code(logits.dtype), logits.device, torch.float32
+    torch = _load()
+    _cuda(logits, "logits")
+    shape, dtype, f32, i32 = logits.shape, logits.dtype, torch.float32, torch.int32
+    rows, V = shape
+    io, per_row = _io(dtype), (rows,)
     if tokens is None:
-        tokens = _empty((rows,), torch.int32, dev, stream)
-    _tensor(logits, "logits")
-    _tensor(noise, "noise", (rows, V), f32, device=dev)
-    _tensor(temperature, "temperature", (rows,), f32, True, dev)
-    _tensor(top_k, "top_k", (rows,), torch.int32, True, dev)
-    _tensor(top_p, "top_p", (rows,), f32, True, dev)
-    _tensor(min_p, "min_p", (rows,), f32, True, dev)
-    _tensor(tokens, "tokens", (rows,), torch.int32, True, dev)
+        tokens = _empty(per_row, i32, logits.device, stream)
+    else:
+        _param(tokens, "tokens", i32, per_row)
+    logits_r, noise_r = _rows(logits, "logits", dtype, shape), _rows(noise, "noise", f32, shape)
+    _param(temperature, "temperature", f32, per_row)
+    _param(top_k, "top_k", i32, per_row)
+    _param(top_p, "top_p", f32, per_row)
+    _param(min_p, "min_p", f32, per_row)
     p = _ss._ptr
-    st = _ss.lib().ss_sample(p(logits), p(noise), p(temperature), p(top_k), p(top_p), p(min_p), p(tokens), rows, V, io,
-                             logits.stride(0), noise.stride(0), _ss._stream_handle(stream))
+    st = _lib.ss_sample(logits.data_ptr(), noise.data_ptr(), p(temperature), p(top_k), p(top_p), p(min_p), tokens.data_ptr(),
+                        rows, V, io, logits_r, noise_r, _stream(logits, stream))
     if st != 0:
         raise _ss.SelscanError(st, "ss_sample")
     return tokens
