@@ -78,6 +78,27 @@ __device__ __forceinline__ float2 heads_conv2(const float2 w[4], float2 b, float
     return silu2_joint(fma2(w[3], e3, fma2(w[2], e2, fma2(w[1], e1, fma2(w[0], e0, b)))));
 }
 
+// Sum over the block's threads before this one, and over all of them.
+__device__ __forceinline__ int block_prefix(int v, int* total, int* scratch) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) scratch[warp] = x;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < warps; ++w) {
+        if (w < warp) before += scratch[w];
+        all += scratch[w];
+    }
+    *total = all;
+    return before + x - v;
+}
+
 // The heads of a group share its B and C channels: each CTA that reads their windows says so here
 // when it has, and the last one to say so (it returns true there, for all its threads) may
 // overwrite them.  The counter is back at zero then.

@@ -37,6 +37,7 @@ struct HeadsTcPlan {
     bool split;
 };
 
+int heads_sm_count();                   // of the current device
 // Whether the tensor-core path takes these sizes.
 bool heads_tc_takes(int64_t n_seq, int64_t tokens, int64_t H, int64_t P, int64_t G, int64_t N, bool bf16);
 HeadsTcPlan heads_tc_plan(int64_t n_seq, int64_t tokens, int64_t H, int64_t P, int64_t G, int64_t N);

@@ -3,10 +3,13 @@
 // Per head and token: S <- a·S + (Δ·x) ⊗ B (P × N), y = S·C + D·x, gated by silu(z), where x, B
 // and C come out of a width-4 causal convolution and a SiLU.
 //
-// heads_seq_kernel walks the tokens in order, the recurrence as it is written.  A CTA has 16 rows
-// of one head's state of one sequence, a warp 4 of them with its 32 lanes along N, all in
-// registers; 16 tokens at a time the CTA convolves its x channels and the group's B and C into
-// shared memory, then every warp takes the tokens one by one.
+// heads_seq_kernel walks the tokens in order, the recurrence as it is written, all of it in fp32.  A CTA
+// has 64 rows of one head's state of one sequence.  A thread has 16 states of two rows in registers,
+// LPR lanes share a row; 16 tokens at a time the CTA convolves its x channels and the group's B and C
+// into shared memory (their samples are loaded a round ahead), then every warp takes the tokens one by
+// one.  What bounds it is issue: per token and 64 x 128 states 8 warps of some 70 instructions.
+// Long sequences of few heads are cut in segments: a first pass leaves each segment's state from zero
+// and its decay, the second starts every segment from the state that enters it.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -22,135 +25,315 @@
 namespace selscan {
 namespace {
 
-constexpr int kSeqThreads = 128;
-constexpr int kSeqRowsWarp = 4;
-constexpr int kSeqRows = kSeqRowsWarp * kSeqThreads / 32;   // rows of the state per CTA
+constexpr int kSeqRows = 64;                                // rows of the state per CTA
 constexpr int kSeqT = 16;                                   // tokens per round
+constexpr int kSeqN = 16;                                   // states per thread and row
+constexpr int kSeqU = 4;                                    // tokens whose sums over lanes are taken together
 
-template <typename TIO, int NL>
-__global__ void __launch_bounds__(kSeqThreads) heads_seq_kernel(const HeadsParams p) {
-    constexpr int NP = 32 * NL;
-    __shared__ float sB[kSeqT][NP], sC[kSeqT][NP], sx[kSeqT][kSeqRows], sy[kSeqT][kSeqRows], sdt[kSeqT], sa[kSeqT];
-    const int tiles = (p.P + kSeqRows - 1) / kSeqRows;
-    int id = blockIdx.x;
-    const int pt = id % tiles;
-    id /= tiles;
-    const int h = id % p.H, seq = id / p.H;
+struct SeqParams {
+    HeadsParams p;
+    int seg;                // tokens per segment (a multiple of kSeqT)
+    int64_t units;          // upper bound of the segments
+    float* seg_state;       // [units, H, P, N]: what a segment leaves from zero
+    float* seg_decay;       // [units, H]: its log2 decay
+};
+
+enum class SeqPass { kWhole, kStates, kSegments };
+
+template <typename TIO, int LPR, SeqPass PASS>
+__global__ void __launch_bounds__(32 * LPR) heads_seq_kernel(const SeqParams q) {
+    constexpr int NT = 32 * LPR, NP = kSeqN * LPR, CH = kSeqRows + 2 * NP, CPT = (CH + NT - 1) / NT;
+    constexpr int OPT = kSeqT * kSeqRows / NT;              // outputs per thread and round
+    constexpr bool kOut = PASS != SeqPass::kStates;
+    __shared__ __align__(16) float sB[kSeqT][NP], sC[kSeqT][NP], sx[kSeqT][kSeqRows], sy[kSeqT][kSeqRows];
+    __shared__ float sdt[kSeqT], sa[kSeqT];
+    __shared__ int scratch[NT / 32], found[2];
+    const HeadsParams& p = q.p;
+    const int tid = threadIdx.x, tiles = (p.P + kSeqRows - 1) / kSeqRows;
+    const int64_t id = blockIdx.x;
+    const int pt = static_cast<int>(id % tiles), h = static_cast<int>(id / tiles % p.H);
+    int64_t unit = id / tiles / p.H;
+    int seq = static_cast<int>(unit), seg = 0, nsegs = 1;
+    if (PASS != SeqPass::kWhole) {                          // the sequence that this segment is of
+        if (tid == 0) found[0] = -1;
+        __syncthreads();
+        int base = 0;
+        for (int s0 = 0; s0 < p.n_seq && found[0] < 0; s0 += NT) {
+            int n = 0;
+            if (s0 + tid < p.n_seq) {
+                const HeadsSeq c = heads_seq(p, s0 + tid);
+                n = c.ok ? max(1, (c.len + q.seg - 1) / q.seg) : 0;
+                if (!c.ok && id == 0 && p.err) atomicOr(p.err, kErrIndex);
+            }
+            int total;
+            const int at = base + block_prefix(n, &total, scratch);
+            if (unit >= at && unit < at + n) {
+                found[0] = s0 + tid;
+                found[1] = static_cast<int>(unit) - at;
+            }
+            base += total;
+            __syncthreads();
+        }
+        if (found[0] < 0) return;
+        seq = found[0];
+        seg = found[1];
+    }
     const HeadsSeq s = heads_seq(p, seq);
     if (!s.ok) {
-        if (h == 0 && pt == 0 && threadIdx.x == 0 && p.err) atomicOr(p.err, kErrIndex);
+        if (h == 0 && pt == 0 && tid == 0 && p.err) atomicOr(p.err, kErrIndex);
         return;
     }
-    const int g = h / (p.H / p.G), warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (PASS != SeqPass::kWhole) nsegs = max(1, (s.len + q.seg - 1) / q.seg);
+    const int64_t unit0 = unit - seg;
+    const int first = PASS == SeqPass::kWhole ? 0 : seg * q.seg;
+    const int end = PASS == SeqPass::kWhole ? s.len : min(s.len, first + q.seg);
+    const bool last = seg == nsegs - 1;
+    if (PASS == SeqPass::kStates && nsegs == 1) return;
+
+    const int g = h / (p.H / p.G), lr = tid % LPR, rp = tid / LPR;       // rows rp and rp + 32
     const int p0 = pt * kSeqRows, np = min(kSeqRows, p.P - p0);
     const int cx = h * p.P + p0, cb = p.H * p.P + g * p.N, cc = cb + p.G * p.N;
     const float A2 = -expf(p.A_log[h]) * kLog2e, bias = p.dt_bias ? p.dt_bias[h] : 0.f, Dh = p.D ? p.D[h] : 0.f;
-    float* Sg = p.state + ((static_cast<int64_t>(max(s.slot, 0)) * p.H + h) * p.P + p0) * p.N;
 
-    float S[kSeqRowsWarp][NL];
+    // a channel's convolution: this thread's channels, their weights and their last samples
+    int chan[CPT];
+    float w[CPT][4], cbias[CPT], e0[CPT], e1[CPT], e2[CPT];
+    TIO raw[CPT][kSeqT];
+    const TIO* xg = static_cast<const TIO*>(p.xbc) + s.row0 * p.xbc_t;
 #pragma unroll
-    for (int r = 0; r < kSeqRowsWarp; ++r)
+    for (int k = 0; k < CPT; ++k) {
+        const int i = tid + k * NT;
+        const int j = i < kSeqRows ? i : i < kSeqRows + NP ? i - kSeqRows : i - kSeqRows - NP;
+        const bool on = i < CH && (i < kSeqRows ? j < np : j < p.N) && (kOut || i < kSeqRows + NP);
+        chan[k] = !on ? -1 : i < kSeqRows ? cx + j : i < kSeqRows + NP ? cb + j : cc + j;
+    }
+    auto load_round = [&](int t0) {
 #pragma unroll
-        for (int j = 0; j < NL; ++j) {
-            const int row = warp * kSeqRowsWarp + r, n = lane + 32 * j;
-            S[r][j] = (s.warm && row < np && n < p.N) ? Sg[static_cast<int64_t>(row) * p.N + n] : 0.f;
+        for (int k = 0; k < CPT; ++k)
+#pragma unroll
+            for (int t = 0; t < kSeqT; ++t)
+                raw[k][t] = (chan[k] >= 0 && t0 + t < end) ? xg[static_cast<int64_t>(t0 + t) * p.xbc_t + chan[k]] : from_f32<TIO>(0.f);
+    };
+    if (first < end) load_round(first);
+#pragma unroll
+    for (int k = 0; k < CPT; ++k) {
+        const int c = max(chan[k], 0);
+        HeadsWindow win = {{0.f, 0.f, 0.f}};
+        if (chan[k] >= 0 && first == 0) win = heads_window(p, s, c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[k][i] = chan[k] >= 0 ? p.conv_w[static_cast<int64_t>(c) * 4 + i] : 0.f;
+        cbias[k] = (chan[k] >= 0 && p.conv_b) ? p.conv_b[c] : 0.f;
+        const bool past = chan[k] >= 0 && first > 0 && first < end;
+        e0[k] = past ? to_f32<TIO>(xg[static_cast<int64_t>(first - 3) * p.xbc_t + c]) : win.v[0];
+        e1[k] = past ? to_f32<TIO>(xg[static_cast<int64_t>(first - 2) * p.xbc_t + c]) : win.v[1];
+        e2[k] = past ? to_f32<TIO>(xg[static_cast<int64_t>(first - 1) * p.xbc_t + c]) : win.v[2];
+    }
+
+    // The state that enters (see ss_heads_tc.cu: the second pass over a cut sequence must not read its
+    // slot, which the first pass puts in the place of the last segment).
+    float2 S[2][kSeqN / 2];
+    auto at_state = [&](float* base, int64_t k) { return base + ((k * p.H + h) * p.P + p0) * p.N; };
+    auto each_state = [&](float* base, auto&& f) {          // f(element, its address) for this thread's
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int j = 0; j < kSeqN / 2; ++j) {
+                const int row = rp + 32 * r, n = (j / 2 * LPR + lr) * 4 + (j & 1) * 2;
+                if (row < np && n < p.N) f(S[r][j].x, base + static_cast<int64_t>(row) * p.N + n);
+                if (row < np && n + 1 < p.N) f(S[r][j].y, base + static_cast<int64_t>(row) * p.N + n + 1);
+            }
+    };
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int j = 0; j < kSeqN / 2; ++j) S[r][j] = make_float2(0.f, 0.f);
+    float* slot_state = at_state(p.state, max(s.slot, 0));
+    if (s.warm && (PASS == SeqPass::kStates ? seg == 0 || last : nsegs == 1))
+        each_state(slot_state, [](float& v, const float* f) { v = *f; });
+    if (PASS == SeqPass::kStates && last) {
+        each_state(at_state(q.seg_state, unit), [](float& v, float* f) { *f = v; });
+        return;
+    }
+    if (PASS == SeqPass::kSegments && nsegs > 1) {
+        if (seg == 0) each_state(at_state(q.seg_state, unit0 + nsegs - 1), [](float& v, const float* f) { v = *f; });
+        for (int j = 0; j < seg; ++j) {
+            const float d = ex2(q.seg_decay[(unit0 + j) * p.H + h]);
+            each_state(at_state(q.seg_state, unit0 + j), [d](float& v, const float* f) { v = fmaf(d, v, *f); });
         }
+    }
+    float decay_sum = 0.f, dt_next = 0.f;
+    auto load_dt = [&](int t0) {
+        return (tid < kSeqT && t0 + tid < end)
+                   ? to_f32<TIO>(static_cast<const TIO*>(p.dt_raw)[(s.row0 + t0 + tid) * p.dt_t + h]) : 0.f;
+    };
+    if (first < end) dt_next = load_dt(first);
 
-    for (int t0 = 0; t0 < s.len; t0 += kSeqT) {
-        const int nt = min(kSeqT, s.len - t0);
-        // x, B and C of the round's tokens; lanes past np and N hold zeros
-        for (int i = threadIdx.x; i < kSeqRows + 2 * NP; i += kSeqThreads) {
+    for (int t0 = first; t0 < end; t0 += kSeqT) {
+        const int nt = min(kSeqT, end - t0);
+#pragma unroll
+        for (int k = 0; k < CPT; ++k) {
+            const int i = tid + k * NT;
             float* dst = i < kSeqRows ? &sx[0][i] : i < kSeqRows + NP ? &sB[0][i - kSeqRows] : &sC[0][i - kSeqRows - NP];
             const int pitch = i < kSeqRows ? kSeqRows : NP;
-            const int k = i < kSeqRows ? i : (i - kSeqRows) % NP;
-            const bool on = i < kSeqRows ? k < np : k < p.N;
-            const int c = i < kSeqRows ? cx + k : i < kSeqRows + NP ? cb + k : cc + k;
-            if (!on) {
-                for (int t = 0; t < nt; ++t) dst[t * pitch] = 0.f;
-                continue;
-            }
-            const float* w = p.conv_w + static_cast<int64_t>(c) * 4;
-            const float wk[4] = {w[0], w[1], w[2], w[3]}, b = p.conv_b ? p.conv_b[c] : 0.f;
-            HeadsWindow win = {{0.f, 0.f, 0.f}};
-            if (t0 < 3) win = heads_window(p, s, c);
-            float e0 = heads_sample<TIO>(p, s, win, c, t0 - 3), e1 = heads_sample<TIO>(p, s, win, c, t0 - 2),
-                  e2 = heads_sample<TIO>(p, s, win, c, t0 - 1);
-#pragma unroll 4
-            for (int t = 0; t < nt; ++t) {
-                const float e3 = heads_sample<TIO>(p, s, win, c, t0 + t);
-                dst[t * pitch] = heads_conv(wk, b, e0, e1, e2, e3);
-                e0 = e1;
-                e1 = e2;
-                e2 = e3;
-            }
+            if (i < CH)
+#pragma unroll
+                for (int t = 0; t < kSeqT; ++t) {
+                    const float e3 = to_f32<TIO>(raw[k][t]);
+                    dst[t * pitch] = heads_conv(w[k], cbias[k], e0[k], e1[k], e2[k], e3);
+                    e0[k] = e1[k];
+                    e1[k] = e2[k];
+                    e2[k] = e3;
+                }
         }
-        if (threadIdx.x < nt) {
-            const float r = to_f32<TIO>(static_cast<const TIO*>(p.dt_raw)[(s.row0 + t0 + threadIdx.x) * p.dt_t + h]);
-            const float dt = softplus(r + bias);
-            sdt[threadIdx.x] = dt;
-            sa[threadIdx.x] = ex2(dt * A2);
+        if (tid < kSeqT) {                                  // past the end: Δ = 0, which changes nothing
+            const float dt = tid < nt ? softplus(dt_next + bias) : 0.f;
+            sdt[tid] = dt;
+            sa[tid] = ex2(dt * A2);
+            decay_sum += dt * A2;
+        }
+        if (t0 + kSeqT < end) {
+            load_round(t0 + kSeqT);
+            dt_next = load_dt(t0 + kSeqT);
+        }
+        TIO gate[OPT];                                      // z of this round's outputs, loaded ahead of their use
+        if (kOut && p.z) {
+#pragma unroll
+            for (int k = 0; k < OPT; ++k) {
+                const int i = tid + k * NT, t = i / kSeqRows, c = i % kSeqRows;
+                gate[k] = (t < nt && c < np) ? static_cast<const TIO*>(p.z)[(s.row0 + t0 + t) * p.z_t + cx + c] : from_f32<TIO>(0.f);
+            }
         }
         __syncthreads();
-        for (int t = 0; t < nt; ++t) {
-            const float a = sa[t], dt = sdt[t];
-            float acc[kSeqRowsWarp];
+#pragma unroll 1
+        for (int t4 = 0; t4 < nt; t4 += kSeqU) {
+            float v[2 * kSeqU];                             // this thread's part of C·S, row by row
 #pragma unroll
-            for (int r = 0; r < kSeqRowsWarp; ++r) acc[r] = 0.f;
-            float dx[kSeqRowsWarp];
+            for (int u = 0; u < kSeqU; ++u) {
+                const int t = t4 + u;
+                const float2 a = splat2(sa[t]);
+                const float dt = sdt[t];
+                const float2 d0 = splat2(dt * sx[t][rp]), d1 = splat2(dt * sx[t][rp + 32]);
+                float2 y0 = make_float2(0.f, 0.f), y1 = y0;
 #pragma unroll
-            for (int r = 0; r < kSeqRowsWarp; ++r) dx[r] = dt * sx[t][warp * kSeqRowsWarp + r];
+                for (int j = 0; j < kSeqN / 4; ++j) {
+                    const float4 B = *reinterpret_cast<const float4*>(&sB[t][(j * LPR + lr) * 4]);
+                    const float2 b0 = make_float2(B.x, B.y), b1 = make_float2(B.z, B.w);
+                    S[0][2 * j] = fma2(a, S[0][2 * j], mul2(d0, b0));
+                    S[0][2 * j + 1] = fma2(a, S[0][2 * j + 1], mul2(d0, b1));
+                    S[1][2 * j] = fma2(a, S[1][2 * j], mul2(d1, b0));
+                    S[1][2 * j + 1] = fma2(a, S[1][2 * j + 1], mul2(d1, b1));
+                    if (kOut) {
+                        const float4 C = *reinterpret_cast<const float4*>(&sC[t][(j * LPR + lr) * 4]);
+                        const float2 c0 = make_float2(C.x, C.y), c1 = make_float2(C.z, C.w);
+                        y0 = fma2(S[0][2 * j + 1], c1, fma2(S[0][2 * j], c0, y0));
+                        y1 = fma2(S[1][2 * j + 1], c1, fma2(S[1][2 * j], c0, y1));
+                    }
+                }
+                v[u] = y0.x + y0.y;
+                v[kSeqU + u] = y1.x + y1.y;
+            }
+            if (kOut) {
+                // sums over the lanes of a row: at each exchange a lane keeps half of the values
+                int n = 2 * kSeqU, at = 0;
 #pragma unroll
-            for (int j = 0; j < NL; ++j) {
-                const float B = sB[t][lane + 32 * j], C = sC[t][lane + 32 * j];
+                for (int o = LPR / 2; o > 0; o /= 2) {
+                    if (n > 1) {
+                        n /= 2;
+                        const bool up = lr & o;
 #pragma unroll
-                for (int r = 0; r < kSeqRowsWarp; ++r) {
-                    S[r][j] = fmaf(a, S[r][j], dx[r] * B);
-                    acc[r] = fmaf(S[r][j], C, acc[r]);
+                        for (int i = 0; i < n; ++i) {
+                            const float give = up ? v[i] : v[i + n];
+                            v[i] = (up ? v[i + n] : v[i]) + __shfl_xor_sync(0xffffffffu, give, o);
+                        }
+                        at += up ? n : 0;
+                    } else {
+                        v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < n; ++i) sy[t4 + (at + i) % kSeqU][rp + 32 * ((at + i) / kSeqU)] = v[i];
+            }
+        }
+        __syncthreads();
+        if (kOut) {
+#pragma unroll
+            for (int k = 0; k < OPT; ++k) {
+                const int i = tid + k * NT, t = i / kSeqRows, c = i % kSeqRows;
+                if (t < nt && c < np) {
+                    float y = fmaf(Dh, sx[t][c], sy[t][c]);
+                    if (p.z) y *= silu(to_f32<TIO>(gate[k]));
+                    static_cast<TIO*>(p.y)[(s.row0 + t0 + t) * p.y_t + cx + c] = from_f32<TIO>(y);
                 }
             }
-#pragma unroll
-            for (int o = 16; o > 0; o /= 2)
-#pragma unroll
-                for (int r = 0; r < kSeqRowsWarp; ++r) acc[r] += __shfl_xor_sync(0xffffffffu, acc[r], o);
-            if (lane == 0)
-#pragma unroll
-                for (int r = 0; r < kSeqRowsWarp; ++r) sy[t][warp * kSeqRowsWarp + r] = acc[r];
+            __syncthreads();
         }
-        __syncthreads();
-        for (int i = threadIdx.x; i < nt * kSeqRows; i += kSeqThreads) {
-            const int t = i / kSeqRows, k = i % kSeqRows;
-            if (k < np) {
-                const int64_t row = s.row0 + t0 + t;
-                float v = fmaf(Dh, sx[t][k], sy[t][k]);
-                if (p.z) v *= silu(to_f32<TIO>(static_cast<const TIO*>(p.z)[row * p.z_t + cx + k]));
-                static_cast<TIO*>(p.y)[row * p.y_t + cx + k] = from_f32<TIO>(v);
-            }
-        }
-        __syncthreads();
+    }
+    if (PASS == SeqPass::kStates) {
+        each_state(at_state(q.seg_state, unit), [](float& v, float* f) { *f = v; });
+#pragma unroll
+        for (int o = 8; o > 0; o /= 2) decay_sum += __shfl_xor_sync(0xffffffffu, decay_sum, o);      // the first 16 lanes hold it
+        if (pt == 0 && tid == 0) q.seg_decay[unit * p.H + h] = decay_sum;
+        return;
     }
     if (s.slot < 0) return;
-#pragma unroll
-    for (int r = 0; r < kSeqRowsWarp; ++r)
-#pragma unroll
-        for (int j = 0; j < NL; ++j) {
-            const int row = warp * kSeqRowsWarp + r, n = lane + 32 * j;
-            if (row < np && n < p.N) Sg[static_cast<int64_t>(row) * p.N + n] = S[r][j];
-        }
-    for (int k = threadIdx.x; k < np; k += kSeqThreads) heads_keep_window<TIO>(p, s, cx + k);
+    if (last) each_state(slot_state, [](float& v, float* f) { *f = v; });
+    if (seg > 0) return;
+    // the CTAs of a sequence's first segment read its windows: the x channels' are this CTA's own, those of
+    // B and C the group's, whose last reader shifts them
+    __syncthreads();
+    for (int k = tid; k < np; k += NT) heads_keep_window<TIO>(p, s, cx + k);
     if (heads_last_reader(p.arrivals + static_cast<int64_t>(seq) * p.G + g, (p.H / p.G) * tiles))
-        for (int k = threadIdx.x; k < 2 * p.N; k += kSeqThreads)
-            heads_keep_window<TIO>(p, s, k < p.N ? cb + k : cc + k - p.N);
+        for (int k = tid; k < 2 * p.N; k += NT) heads_keep_window<TIO>(p, s, k < p.N ? cb + k : cc + k - p.N);
+}
+
+// Tokens per segment (0: whole sequences), for sequences of equal length: a segmented call does about 1.7
+// times the work and has one more launch (10 us, about 60 tokens' time), and pays where the CTAs of
+// whole sequences leave the SMs fewer than 16 warps.
+struct SeqPlan {
+    int seg;
+    int64_t units;
+    size_t state_bytes, bytes;
+};
+SeqPlan seq_plan(int64_t n_seq, int64_t tokens, int64_t H, int64_t P, int64_t N) {
+    SeqPlan plan{0, n_seq, 0, 0};
+    const int64_t ctas = n_seq * H * ((P + kSeqRows - 1) / kSeqRows), lpr = N <= 16 ? 1 : N <= 32 ? 2 : N <= 64 ? 4 : N <= 128 ? 8 : 16;
+    const int64_t room = heads_sm_count() * (16 / lpr);      // CTAs of lpr warps
+    const int64_t mean = tokens / std::max<int64_t>(n_seq, 1);
+    const int64_t k = std::min<int64_t>(room / std::max<int64_t>(ctas, 1), mean / 64);
+    if (k < 3) return plan;
+    plan.seg = static_cast<int>((mean / k + kSeqT - 1) / kSeqT * kSeqT);
+    plan.units = tokens / plan.seg + n_seq;
+    plan.state_bytes = (static_cast<size_t>(plan.units) * H * P * N * 4 + 255) / 256 * 256;
+    plan.bytes = plan.state_bytes + (static_cast<size_t>(plan.units) * H * 4 + 255) / 256 * 256;
+    return plan;
+}
+
+template <typename TIO, int LPR>
+cudaError_t launch_seq_lanes(const SeqParams& q, cudaStream_t stream) {
+    const int64_t per_unit = static_cast<int64_t>(q.p.H) * ((q.p.P + kSeqRows - 1) / kSeqRows);
+    const unsigned grid = static_cast<unsigned>(q.units * per_unit);
+    if (q.seg == 0) {
+        heads_seq_kernel<TIO, LPR, SeqPass::kWhole><<<grid, 32 * LPR, 0, stream>>>(q);
+        return cudaGetLastError();
+    }
+    heads_seq_kernel<TIO, LPR, SeqPass::kStates><<<grid, 32 * LPR, 0, stream>>>(q);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    heads_seq_kernel<TIO, LPR, SeqPass::kSegments><<<grid, 32 * LPR, 0, stream>>>(q);
+    return cudaGetLastError();
 }
 
 template <typename TIO>
-cudaError_t launch_seq(const HeadsParams& p, cudaStream_t stream) {
-    const int64_t blocks = static_cast<int64_t>(p.n_seq) * p.H * ((p.P + kSeqRows - 1) / kSeqRows);
-    const unsigned grid = static_cast<unsigned>(blocks);
-    if (p.N <= 32) heads_seq_kernel<TIO, 1><<<grid, kSeqThreads, 0, stream>>>(p);
-    else if (p.N <= 64) heads_seq_kernel<TIO, 2><<<grid, kSeqThreads, 0, stream>>>(p);
-    else if (p.N <= 128) heads_seq_kernel<TIO, 4><<<grid, kSeqThreads, 0, stream>>>(p);
-    else heads_seq_kernel<TIO, 8><<<grid, kSeqThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+cudaError_t launch_seq(const HeadsParams& p, uint8_t* workspace, cudaStream_t stream) {
+    const SeqPlan plan = seq_plan(p.n_seq, p.tokens, p.H, p.P, p.N);
+    const SeqParams q{p, plan.seg, plan.units, reinterpret_cast<float*>(workspace),
+                      reinterpret_cast<float*>(workspace + plan.state_bytes)};
+    if (plan.units * p.H * ((p.P + kSeqRows - 1) / kSeqRows) > INT32_MAX) return cudaErrorInvalidConfiguration;
+    if (p.N <= 16) return launch_seq_lanes<TIO, 1>(q, stream);
+    if (p.N <= 32) return launch_seq_lanes<TIO, 2>(q, stream);
+    if (p.N <= 64) return launch_seq_lanes<TIO, 4>(q, stream);
+    if (p.N <= 128) return launch_seq_lanes<TIO, 8>(q, stream);
+    return launch_seq_lanes<TIO, 16>(q, stream);
 }
 
 }  // namespace
@@ -250,7 +433,7 @@ extern "C" size_t ss_heads_workspace_size(int64_t n_seq, int64_t tokens, int64_t
         return 0;
     return heads_tc_takes(n_seq, tokens, H, P, G, N, io_dtype == SS_BF16)
                ? kHeadsCounterBytes + heads_tc_plan(n_seq, tokens, H, P, G, N).bytes
-               : heads_counter_bytes(n_seq, G);
+               : heads_counter_bytes(n_seq, G) + seq_plan(n_seq, tokens, H, P, N).bytes;
 }
 
 extern "C" ss_status ss_heads_fwd(const void* xbc, const void* dt_raw, const void* z, const float* conv_w,
@@ -274,7 +457,8 @@ extern "C" ss_status ss_heads_fwd(const void* xbc, const void* dt_raw, const voi
         e = launch_heads_tc(p, static_cast<uint8_t*>(workspace) + kHeadsCounterBytes, bf16, stream);
     } else {
         e = heads_counters(p, workspace, stream);
-        if (e == cudaSuccess) e = bf16 ? launch_seq<__nv_bfloat16>(p, stream) : launch_seq<float>(p, stream);
+        uint8_t* behind = static_cast<uint8_t*>(workspace) + heads_counter_bytes(n_seq, G);
+        if (e == cudaSuccess) e = bf16 ? launch_seq<__nv_bfloat16>(p, behind, stream) : launch_seq<float>(p, behind, stream);
     }
     return e == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }

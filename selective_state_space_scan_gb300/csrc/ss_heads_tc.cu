@@ -50,27 +50,6 @@ __device__ __forceinline__ int chunks_of(const HeadsParams& p, int seq) {
     return s.ok ? max(1, (s.len + kQ - 1) / kQ) : 0;
 }
 
-// Sum over the block's threads before this one, and over all of them.
-__device__ __forceinline__ int block_prefix(int v, int* total, int* scratch) {
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
-    int x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) scratch[warp] = x;
-    __syncthreads();
-    int before = 0, all = 0;
-    for (int w = 0; w < warps; ++w) {
-        if (w < warp) before += scratch[w];
-        all += scratch[w];
-    }
-    *total = all;
-    return before + x - v;
-}
-
 // ---- B and C
 
 // Four channels as loaded: bf16 pairs, or floats.  `n` of them exist; VEC: all or none, one aligned access.
@@ -806,15 +785,6 @@ int segments_for(int64_t chains, int64_t chunks, int64_t sms) {
 constexpr int kWaveChunks = 4;
 constexpr int kManyChains = 8;           // per SM
 
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return 152;
-    }
-    return n;
-}
-
 size_t padded(size_t n) { return (n + 255) / 256 * 256; }
 
 template <typename TIO, bool VEC, Pass PASS>
@@ -845,6 +815,15 @@ cudaError_t launch_typed(const HeadsTcParams& q, const HeadsTcPlan& plan, cudaSt
 
 }  // namespace
 
+int heads_sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 152;
+    }
+    return n;
+}
+
 // bf16 activations, up to 128 states, and more than 16 tokens a sequence on average: below that the
 // token-by-token kernel is faster (about 1 us a token against 5 us a chunk and a second launch).
 bool heads_tc_takes(int64_t n_seq, int64_t tokens, int64_t H, int64_t P, int64_t G, int64_t N, bool bf16) {
@@ -862,7 +841,7 @@ HeadsTcPlan heads_tc_plan(int64_t n_seq, int64_t tokens, int64_t H, int64_t P, i
     plan.pairs = static_cast<int>(G * ((H / G * tiles + 1) / 2));
     plan.chunks = tokens / kHeadsChunk + n_seq;
     const int64_t mean = (tokens / n_seq + kHeadsChunk - 1) / kHeadsChunk;
-    const int sms = sm_count();
+    const int sms = heads_sm_count();
     const int64_t chains = n_seq * plan.pairs;
     const int k = segments_for(chains, std::max<int64_t>(mean, 1), sms);
     plan.split = k > 1;
