@@ -606,7 +606,7 @@ ss_status ss_add_rmsnorm_f8(const void* x, const void* residual, const float* we
                             const ss_norm_strides* strides, void* stream);
 
 /* Largest vocabulary ss_sample takes. */
-#define SS_SAMPLE_MAX (1 << 20)
+#define SS_SAMPLE_MAX (1 << 19)
 
 /*
  * Next tokens from logits and given random numbers.  Per row, with l = logits (NaN read as -inf,

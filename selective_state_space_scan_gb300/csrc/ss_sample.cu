@@ -3,15 +3,19 @@
 //
 // With l_max the row's largest logit, w = exp((l - l_max)/T).  Tokens are ordered by one whole
 // number each, the logit's bits (made monotone) above the complement of the index, so there are no
-// ties and the top-k and top-p sets are "every token from some number up".  That number is found
-// without sorting the row: a histogram over d = (l_max - l)/T (counts, and weights in fixed point,
-// whose sums do not depend on the order of the atomics) names the bin it is in; the bin's tokens,
-// a few hundred as a rule, are collected in shared memory and ranked against each other.  A bin
-// with more tokens than that (equal logits, or the tail beyond exp(-22)) is narrowed by further
-// histograms over the ordering number itself.  The last pass runs the race over what stays and
-// reads the noise of those tokens alone.
+// ties and the top-k and top-p sets are "every token from some number up".  Weights are summed in
+// fixed point, so that no sum depends on the order of its terms.
 //
-// A CTA has a row; its passes after the first read the logits from L2.
+// A row is shared by the CTAs of a cluster (up to 8), each with a slice; they exchange what they find
+// through distributed shared memory.  The first pass takes the maximum, per thread and then of the row.
+//   - A small top_k: the k-th largest of the threads' maxima is a lower bound of the k-th largest
+//     logit, and only little more than k logits reach it.  They are collected, ranked against each
+//     other, and the race is among them: two passes over the logits, none over the noise.
+//   - Otherwise, with a top_k or top_p: a histogram over d = (l_max - l)/T (weights, and counts where
+//     they matter) names the bin that the last token to stay is in; the bin's tokens, a few hundred as
+//     a rule, are collected and ranked against each other.  A bin with more of them (equal logits, or the
+//     tail beyond exp(-22)) is narrowed by further histograms over the ordering number itself.
+//   - The last pass runs the race over what stays and reads the noise of those tokens alone.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -25,11 +29,14 @@
 namespace selscan {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048;
 constexpr int kCap = 1024;               // most tokens ranked against each other
-constexpr int kIndexBits = 20;           // SS_SAMPLE_MAX
+constexpr int kIndexBits = 19;           // SS_SAMPLE_MAX
+constexpr int kMaxSlice = 1 << 16;       // most tokens per CTA
+static_assert(SS_SAMPLE_MAX <= kMaxCluster * kMaxSlice, "the largest row fits a cluster");
 constexpr int kOrderBits = 32 + kIndexBits;
 constexpr float kReach = 22.1807098f;    // ln 2^32: a weight below exp(-kReach) has no mass in fixed point
 constexpr float kMassOne = 2147483648.f; // a weight of 1
@@ -46,6 +53,8 @@ struct SampleParams {
     int32_t* tokens;
     int64_t logits_r, noise_r;
     int V;
+    uint32_t cluster;        // CTAs per row
+    int slice;               // tokens per CTA (whole 16-byte runs)
 };
 
 __device__ __forceinline__ float tidy(float l) {           // NaN as -inf, +inf as the largest number
@@ -71,6 +80,11 @@ template <> struct Pack<float> {
         const float4 f = *reinterpret_cast<const float4*>(q);
         v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
     }
+    // (fmaxf passes over NaN)
+    static __device__ __forceinline__ float largest(const float* q) {
+        const float4 f = *reinterpret_cast<const float4*>(q);
+        return fmaxf(fmaxf(fmaxf(f.x, f.y), fmaxf(f.z, f.w)), -INFINITY);
+    }
 };
 template <> struct Pack<__nv_bfloat16> {
     static constexpr int n = 8;
@@ -83,10 +97,17 @@ template <> struct Pack<__nv_bfloat16> {
             v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
         }
     }
+    static __device__ __forceinline__ float largest(const __nv_bfloat16* q) {
+        const uint4 u = *reinterpret_cast<const uint4*>(q);
+        const __nv_bfloat162 m = __hmax2(__hmax2(*reinterpret_cast<const __nv_bfloat162*>(&u.x), *reinterpret_cast<const __nv_bfloat162*>(&u.y)),
+                                         __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&u.z), *reinterpret_cast<const __nv_bfloat162*>(&u.w)));
+        const float2 f = __bfloat1622float2(m);
+        return fmaxf(fmaxf(f.x, f.y), -INFINITY);
+    }
 };
 
 // f(index, logit) for every token of the row: 16-byte loads between the first and the last
-// 16-byte boundary of the row, single ones around them.
+// 16-byte boundary of the row, single ones around them.  A thread's indexes increase.
 template <typename T, typename F>
 __device__ __forceinline__ void each_token(const T* row, int V, F&& f) {
     constexpr int W = Pack<T>::n;
@@ -95,8 +116,6 @@ __device__ __forceinline__ void each_token(const T* row, int V, F&& f) {
     const int body = (V - head) / W;
     const int tail0 = head + body * W;
     if (static_cast<int>(threadIdx.x) < head) f(static_cast<int>(threadIdx.x), tidy(to_f32<T>(row[threadIdx.x])));
-    if (static_cast<int>(threadIdx.x) < V - tail0)
-        f(tail0 + static_cast<int>(threadIdx.x), tidy(to_f32<T>(row[tail0 + threadIdx.x])));
 #pragma unroll 2
     for (int b = threadIdx.x; b < body; b += kThreads) {
         float v[W];
@@ -104,20 +123,101 @@ __device__ __forceinline__ void each_token(const T* row, int V, F&& f) {
 #pragma unroll
         for (int j = 0; j < W; ++j) f(head + b * W + j, tidy(v[j]));
     }
+    if (static_cast<int>(threadIdx.x) < V - tail0)
+        f(tail0 + static_cast<int>(threadIdx.x), tidy(to_f32<T>(row[tail0 + threadIdx.x])));
+}
+
+// f(index, weight, noise) for every token that stays, in the order of each_token.  The noise of a pack is
+// read as a whole where its alignment allows and one of its tokens stays, else one by one.
+template <typename T, typename S, typename Wt, typename F>
+__device__ __forceinline__ void each_token_and_noise(const T* row, const float* noise, int V, S&& stays, Wt&& weight, F&& f) {
+    constexpr int W = Pack<T>::n;
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+    const int head = min(V, off ? W - off : 0);
+    const int body = (V - head) / W;
+    const int tail0 = head + body * W;
+    const bool wide = (reinterpret_cast<uintptr_t>(noise + head) & 15u) == 0;
+    auto one = [&](int i) {
+        const float l = tidy(to_f32<T>(row[i])), w = weight(l);
+        if (stays(i, l, w)) f(i, w, noise[i]);
+    };
+    if (static_cast<int>(threadIdx.x) < head) one(static_cast<int>(threadIdx.x));
+    for (int b = threadIdx.x; b < body; b += kThreads) {
+        const int i = head + b * W;
+        float v[W], e[W];
+        Pack<T>::load(row + i, v);
+        bool on[W], any = false;
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            const float l = tidy(v[j]);
+            v[j] = weight(l);
+            on[j] = stays(i + j, l, v[j]);
+            any = any || on[j];
+        }
+        if (!any) continue;
+        if (wide) {
+#pragma unroll
+            for (int j = 0; j < W; j += 4) Pack<float>::load(noise + i + j, e + j);
+        } else {
+#pragma unroll
+            for (int j = 0; j < W; ++j) e[j] = noise[i + j];
+        }
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            if (on[j]) f(i + j, v[j], e[j]);
+    }
+    if (static_cast<int>(threadIdx.x) < V - tail0) one(tail0 + static_cast<int>(threadIdx.x));
+}
+
+// f(index of the pack's first token, the pack's largest logit) for every pack: the same tokens by the same
+// threads as each_token's, in increasing order of the index for each of them but the tail.
+template <typename T, typename F>
+__device__ __forceinline__ void each_pack(const T* row, int V, F&& f) {
+    constexpr int W = Pack<T>::n;
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+    const int head = min(V, off ? W - off : 0);
+    const int body = (V - head) / W;
+    const int tail0 = head + body * W;
+    if (static_cast<int>(threadIdx.x) < head) f(static_cast<int>(threadIdx.x), tidy(to_f32<T>(row[threadIdx.x])));
+#pragma unroll 4
+    for (int b = threadIdx.x; b < body; b += kThreads) f(head + b * W, fminf(Pack<T>::largest(row + head + b * W), FLT_MAX));
+    if (static_cast<int>(threadIdx.x) < V - tail0)
+        f(tail0 + static_cast<int>(threadIdx.x), tidy(to_f32<T>(row[tail0 + threadIdx.x])));
+}
+// The ordering number of the first token from `at` on that has logit `best` (the pack at `at` has one).
+template <typename T>
+__device__ __forceinline__ uint64_t first_of_pack(const T* row, int V, int at, float best, int i0) {
+    for (int j = at; j < V && j < at + Pack<T>::n; ++j)
+        if (tidy(to_f32<T>(row[j])) == best) return order_of(best, i0 + j);
+    return 0;
 }
 
 struct Shared {
-    uint32_t count[kBins], lo[kBins], hi[kBins];   // a bin's tokens, and their mass as hi·2^32 + lo
-    uint64_t cand[kCap];
+    uint32_t count[kBins], lo[kBins], hi[kBins];   // a bin's tokens, and their mass as hi·2^16 + lo
+    uint64_t mine[kCap];                           // tokens that this CTA has collected
+    uint64_t cand[kCap];                           // those of the whole cluster, and their masses
     uint32_t cmass[kCap];
+    uint64_t slot[2][kMaxCluster];                 // a number from every CTA
     uint64_t warp64[kWarps];
     uint32_t warp32[kWarps];
-    uint64_t mass_above;      // of the bins before the found one
-    uint32_t count_above;
+    uint64_t mass_above;                           // of the bins before the found one
+    uint32_t count_above, share_count;
+    uint64_t share_mass;
     int bin;
-    uint32_t ncand;
+    uint32_t ncand;                                // collected here
     uint64_t cut;
 };
+
+__device__ __forceinline__ uint32_t ld_peer_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint64_t ld_peer_u64(uint32_t addr) {
+    uint64_t v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+    return v;
+}
 
 __device__ __forceinline__ uint64_t block_max(Shared& s, uint64_t v) {
 #pragma unroll
@@ -128,178 +228,411 @@ __device__ __forceinline__ uint64_t block_max(Shared& s, uint64_t v) {
     __syncthreads();
     if (threadIdx.x % 32 == 0) s.warp64[threadIdx.x / 32] = v;
     __syncthreads();
-    v = s.warp64[threadIdx.x % 32];
 #pragma unroll
-    for (int o = 16; o > 0; o /= 2) {
-        const uint64_t w = __shfl_xor_sync(0xffffffffu, v, o);
-        v = v > w ? v : w;
-    }
+    for (int w = 0; w < kWarps; ++w) v = s.warp64[w] > v ? s.warp64[w] : v;
     return v;
 }
+__device__ __forceinline__ uint64_t block_sum(Shared& s, uint64_t v) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) s.warp64[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v += s.warp64[w];
+    return v;
+}
+
+// The cluster that has a row.  Every thread of every CTA makes the same calls in the same order.
+struct Team {
+    Shared& s;
+    uint32_t rank, size;
+    int turn;                                      // alternates between the two sets of slots
+    __device__ __forceinline__ void sync() const {
+        if (size > 1) cluster_sync_all();
+        else __syncthreads();
+    }
+    // The largest of the CTAs' numbers (the same for all threads of a CTA).
+    __device__ __forceinline__ uint64_t max_over(uint64_t v) {
+        if (size == 1) return v;
+        turn ^= 1;
+        if (threadIdx.x == 0) s.slot[turn][rank] = v;
+        sync();
+        for (uint32_t r = 0; r < size; ++r) {
+            const uint64_t w = ld_peer_u64(peer_smem_addr(&s.slot[turn][r], r));
+            v = w > v ? w : v;
+        }
+        return v;                                  // (the next use of these slots is two syncs away)
+    }
+};
 
 __device__ __forceinline__ void clear_bins(Shared& s) {
     for (int i = threadIdx.x; i < kBins; i += kThreads) s.count[i] = s.lo[i] = s.hi[i] = 0u;
     __syncthreads();
 }
-__device__ __forceinline__ void add_to_bin(Shared& s, int bin, uint32_t mass) {
-    atomicAdd(&s.count[bin], 1u);
-    if (mass) {
-        const uint32_t old = atomicAdd(&s.lo[bin], mass);
-        if (old + mass < old) atomicAdd(&s.hi[bin], 1u);      // the carry
-    }
-}
-__device__ __forceinline__ uint64_t bin_mass(const Shared& s, int bin) {
-    return static_cast<uint64_t>(s.hi[bin]) << 32 | s.lo[bin];
+__device__ __forceinline__ void add_to_bin(Shared& s, int bin, uint32_t mass, bool counted) {
+    if (counted) atomicAdd(&s.count[bin], 1u);
+    // halves of 16 bits, which kMaxSlice tokens do not carry out of; most weights have no upper half
+    if (mass & 0xffffu) atomicAdd(&s.lo[bin], mass & 0xffffu);
+    if (mass >> 16) atomicAdd(&s.hi[bin], mass >> 16);
 }
 
-// The first bin at which the running count, begun at `count`, reaches `k` (by_mass false), or the
-// running mass, begun at `mass`, reaches `target` (by_mass true); the last bin if none does.  Leaves
-// it in s.bin, with the count and mass before it.
-__device__ void find_bin(Shared& s, bool by_mass, uint32_t k, double target, uint32_t count, uint64_t mass) {
-    static_assert(kBins == 2 * kThreads, "two bins a thread");
-    const int b = 2 * threadIdx.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    __syncthreads();
-    if (threadIdx.x == 0) s.bin = kBins;
-    const uint32_t c0 = s.count[b], c1 = s.count[b + 1];
-    const uint64_t m0 = bin_mass(s, b), m1 = bin_mass(s, b + 1);
-    uint32_t ci = c0 + c1;
-    uint64_t mi = m0 + m1;
+// A bin's count and mass over the cluster's histograms.
+__device__ __forceinline__ void whole_bin(const Team& team, int b, uint32_t& c, uint64_t& m) {
+    Shared& s = team.s;
+    c = 0;
+    m = 0;
+    for (uint32_t r = 0; r < team.size; ++r) {
+        const uint32_t pc = team.size > 1 ? peer_smem_addr(&s.count[b], r) : smem_addr(&s.count[b]);
+        c += ld_peer_u32(pc);
+        m += (static_cast<uint64_t>(ld_peer_u32(pc + sizeof(s.count) + sizeof(s.lo))) << 16) + ld_peer_u32(pc + sizeof(s.count));
+    }
+}
+
+// Sums over the bins: this CTA's share of them (kBins / size, in order of the ranks), and exchanged.
+// Histograms are complete when every CTA has called.  Returns the mass of all bins.
+__device__ uint64_t sum_bins(Team& team) {
+    Shared& s = team.s;
+    team.sync();
+    const int share = kBins / static_cast<int>(team.size), each = share / kThreads;
+    uint32_t c = 0;
+    uint64_t m = 0;
+    for (int j = 0; j < each; ++j) {
+        uint32_t cj;
+        uint64_t mj;
+        whole_bin(team, static_cast<int>(team.rank) * share + static_cast<int>(threadIdx.x) * each + j, cj, mj);
+        c += cj;
+        m += mj;
+    }
+    c = static_cast<uint32_t>(block_sum(s, c));
+    m = block_sum(s, m);
+    if (threadIdx.x == 0) {
+        s.share_count = c;
+        s.share_mass = m;
+    }
+    team.sync();
+    uint64_t all = 0;
+    for (uint32_t r = 0; r < team.size; ++r)
+        all += team.size > 1 ? ld_peer_u64(peer_smem_addr(&s.share_mass, r)) : s.share_mass;
+    return all;
+}
+
+// After sum_bins: the first bin at which the running count, begun at `count`, reaches `k` (by_mass false),
+// or the running mass, begun at `mass`, reaches `target` (by_mass true); the last bin if none does.  Leaves
+// it in s.bin, with what is before it, in every CTA.  Histograms may be cleared after it.
+__device__ void find_bin(Team& team, bool by_mass, uint32_t k, double target, uint32_t count, uint64_t mass) {
+    Shared& s = team.s;
+    // the CTA whose share it is in
+    uint32_t owner = 0;
+    for (; owner < team.size; ++owner) {
+        const uint32_t c = team.size > 1 ? ld_peer_u32(peer_smem_addr(&s.share_count, owner)) : s.share_count;
+        const uint64_t m = team.size > 1 ? ld_peer_u64(peer_smem_addr(&s.share_mass, owner)) : s.share_mass;
+        if (owner == team.size - 1 || (by_mass ? static_cast<double>(mass + m) >= target : count + c >= k)) break;
+        count += c;
+        mass += m;
+    }
+    if (owner == team.rank) {
+        const int share = kBins / static_cast<int>(team.size), each = share / kThreads;
+        const int b0 = static_cast<int>(team.rank) * share + static_cast<int>(threadIdx.x) * each, lane = threadIdx.x % 32,
+                  warp = threadIdx.x / 32;
+        uint32_t ci = 0;
+        uint64_t mi = 0;
+        for (int j = 0; j < each; ++j) {
+            uint32_t cj;
+            uint64_t mj;
+            whole_bin(team, b0 + j, cj, mj);
+            ci += cj;
+            mi += mj;
+        }
+        const uint32_t ct = ci;
+        const uint64_t mt = mi;
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-        const uint32_t cu = __shfl_up_sync(0xffffffffu, ci, o);
-        const uint64_t mu = __shfl_up_sync(0xffffffffu, mi, o);
-        if (lane >= o) {
-            ci += cu;
-            mi += mu;
+        for (int o = 1; o < 32; o *= 2) {
+            const uint32_t cu = __shfl_up_sync(0xffffffffu, ci, o);
+            const uint64_t mu = __shfl_up_sync(0xffffffffu, mi, o);
+            if (lane >= o) {
+                ci += cu;
+                mi += mu;
+            }
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) s.bin = kBins;
+        if (lane == 31) {
+            s.warp32[warp] = ci;
+            s.warp64[warp] = mi;
+        }
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) {
+            count += s.warp32[w];
+            mass += s.warp64[w];
+        }
+        uint32_t cb = count + ci - ct, c_at = 0;                 // before this thread's bins
+        uint64_t mb = mass + mi - mt, m_at = 0;
+        int mine = kBins;
+        for (int j = 0; j < each; ++j) {
+            uint32_t cj;
+            uint64_t mj;
+            whole_bin(team, b0 + j, cj, mj);
+            const bool end = threadIdx.x == kThreads - 1 && j == each - 1;
+            if (mine == kBins && (end || (by_mass ? static_cast<double>(mb + mj) >= target : cb + cj >= k))) {
+                mine = b0 + j;
+                c_at = cb;
+                m_at = mb;
+            }
+            cb += cj;
+            mb += mj;
+        }
+        if (mine < kBins) atomicMin(&s.bin, mine);
+        __syncthreads();
+        if (mine < kBins && s.bin == mine) {
+            s.count_above = c_at;
+            s.mass_above = m_at;
         }
     }
-    __syncthreads();
-    if (lane == 31) {
-        s.warp32[warp] = ci;
-        s.warp64[warp] = mi;
+    team.sync();
+    if (owner != team.rank && threadIdx.x == 0) {
+        s.bin = static_cast<int>(ld_peer_u32(peer_smem_addr(&s.bin, owner)));
+        s.count_above = ld_peer_u32(peer_smem_addr(&s.count_above, owner));
+        s.mass_above = ld_peer_u64(peer_smem_addr(&s.mass_above, owner));
+    }
+    team.sync();
+}
+
+// The number of tokens that the CTAs have collected, all of which are then in s.cand with their masses;
+// more than kCap: too many.  (The cluster syncs before it collects again, or ends.)
+template <typename M>
+__device__ uint32_t gather(Team& team, M&& mass_of) {
+    Shared& s = team.s;
+    team.sync();
+    uint32_t c[kMaxCluster], n = 0;
+    bool fits = true;
+#pragma unroll
+    for (uint32_t r = 0; r < kMaxCluster; ++r)
+        c[r] = r >= team.size ? 0u : team.size > 1 ? ld_peer_u32(peer_smem_addr(&s.ncand, r)) : s.ncand;
+#pragma unroll
+    for (uint32_t r = 0; r < kMaxCluster; ++r) {
+        fits = fits && c[r] <= kCap;
+        n += c[r];
+    }
+    if (!fits || n > kCap) return kCap + 1;
+    for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
+        uint32_t r = 0, at = i;
+#pragma unroll
+        for (uint32_t q = 0; q < kMaxCluster - 1; ++q)
+            if (r == q && at >= c[q]) {
+                at -= c[q];
+                r = q + 1;
+            }
+        const uint64_t o = ld_peer_u64(team.size > 1 ? peer_smem_addr(&s.mine[at], r) : smem_addr(&s.mine[at]));
+        s.cand[i] = o;
+        s.cmass[i] = mass_of(logit_of(o));
     }
     __syncthreads();
-    for (int w = 0; w < warp; ++w) {
-        count += s.warp32[w];
-        mass += s.warp64[w];
-    }
-    const uint32_t cb = count + ci - c0 - c1;               // before bin b
-    const uint64_t mb = mass + mi - m0 - m1;
-    const bool r0 = by_mass ? static_cast<double>(mb + m0) >= target : cb + c0 >= k;
-    const bool r1 = by_mass ? static_cast<double>(mb + m0 + m1) >= target : cb + c0 + c1 >= k;
-    if (r0) atomicMin(&s.bin, b);
-    else if (r1 || threadIdx.x == kThreads - 1) atomicMin(&s.bin, b + 1);
-    __syncthreads();
-    if (s.bin == b) {
-        s.count_above = cb;
-        s.mass_above = mb;
-    } else if (s.bin == b + 1) {
-        s.count_above = cb + c0;
-        s.mass_above = mb + m0;
-    }
-    __syncthreads();
+    return n;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) {
+__global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams p) {
     __shared__ Shared s;
-    const int64_t r = blockIdx.x;
-    const T* row = static_cast<const T*>(p.logits) + r * p.logits_r;
+    Team team{s, 0u, p.cluster, 0};
+    if (p.cluster > 1) team.rank = cluster_ctarank();
+    const int64_t r = blockIdx.x / p.cluster;
     const float* noise = p.noise + r * p.noise_r;
-    const int V = p.V;
+    const int V = p.V, i0 = min(V, static_cast<int>(team.rank) * p.slice), n_slice = min(V - i0, p.slice);
+    const T* slice = static_cast<const T*>(p.logits) + r * p.logits_r + i0;
 
-    uint64_t top = 0;
-    each_token(row, V, [&](int i, float l) {
-        const uint64_t o = order_of(l, i);
-        top = o > top ? o : top;
-    });
-    top = block_max(s, top);
-    const float lmax = logit_of(top);
+    // the row's largest logit, and the first of its indexes; each thread's own for the bound of top_k
+    uint64_t own = 0;
+    {
+        float best = -INFINITY;
+        int at = -1;
+        each_pack(slice, n_slice, [&](int i, float l) {
+            if (l > best) {
+                best = l;
+                at = i;
+            }
+        });
+        if (at >= 0) own = first_of_pack(slice, n_slice, at, best, i0);
+    }
+    const uint64_t top = team.max_over(block_max(s, own));
+    const float lmax = top ? logit_of(top) : -INFINITY;
     const float temp = p.temperature ? p.temperature[r] : 1.f;
-    if (lmax == -INFINITY || temp <= 0.f) {
-        if (threadIdx.x == 0) p.tokens[r] = lmax == -INFINITY ? -1 : index_of(top);
+    const float mp = p.min_p ? p.min_p[r] : 0.f;
+    if (top == 0 || temp <= 0.f || !(mp <= 1.f)) {             // nothing there; greedy; only the first token stays
+        if (team.rank == 0 && threadIdx.x == 0) p.tokens[r] = top == 0 ? -1 : index_of(top);
+        team.sync();                                           // (a peer may still read this CTA's slots)
         return;
     }
     const float inv_t = fminf(1.f / (temp > 0.f ? temp : 1.f), 1e35f);   // finite times any reach
     const float c2 = inv_t * kLog2e;
     const int k = p.top_k && p.top_k[r] > 0 && p.top_k[r] < V ? p.top_k[r] : V;
     const float tp = p.top_p && p.top_p[r] < 1.f ? p.top_p[r] : 2.f;
-    const float mp = p.min_p ? p.min_p[r] : 0.f;
+    const double all = 1e300;
 
     auto weight = [&](float l) { return l == -INFINITY ? 0.f : ex2((l - lmax) * c2); };
     const float per_bin = inv_t * (kBins / kReach);
     auto bin_of = [&](float l) { return static_cast<int>(fminf((lmax - l) * per_bin, kBins - 1.f)); };
     auto mass_of = [&](float l) { return __float2uint_rn(weight(l) * kMassOne); };
+    auto race = [&](float e, float w) {                        // the race's key, larger is better; NaN as 0
+        const float key = w * rcp_approx(e);
+        return key >= 0.f ? key : 0.f;
+    };
+    auto numbered = [&](float key, int i) {                    // the lower index among equals
+        return static_cast<uint64_t>(__float_as_uint(key)) << 32 | (0xffffffffu - static_cast<uint32_t>(i));
+    };
+    auto finish = [&](uint64_t best) {
+        best = team.max_over(block_max(s, best));
+        if (team.rank == 0 && threadIdx.x == 0) p.tokens[r] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(best));
+        team.sync();
+    };
+    auto keep = [&](float l, int i) {
+        const uint32_t at = atomicAdd(&s.ncand, 1u);
+        if (at < kCap) s.mine[at] = order_of(l, i);
+    };
+    auto start_collecting = [&](bool again) {                 // again: peers may still read the last list
+        if (again) team.sync();
+        __syncthreads();
+        if (threadIdx.x == 0) s.ncand = 0u;
+        __syncthreads();
+    };
+    // rank of collected token i: how many come before it, and their mass
+    auto rank = [&](int n, uint64_t o, uint32_t& c, uint64_t& m) {
+        for (int j = 0; j < n; ++j)
+            if (s.cand[j] > o) {
+                ++c;
+                m += s.cmass[j];
+            }
+    };
+
+    if (k <= static_cast<int>(team.size * kThreads) / 2 && k <= kCap / 2) {
+        // every thread's maximum, everywhere (in the place of the counts, which this path does not need)
+        static_assert(kMaxCluster * kThreads <= kBins, "a count's place for every thread");
+        uint32_t* tops = s.count;
+        if (team.size > 1) {
+            for (uint32_t q = 0; q < team.size; ++q)
+                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_smem_addr(&tops[team.rank * kThreads + threadIdx.x], q)),
+                             "r"(static_cast<uint32_t>(own >> kIndexBits)) : "memory");
+        } else {
+            tops[threadIdx.x] = static_cast<uint32_t>(own >> kIndexBits);
+        }
+        team.sync();
+        uint32_t mine[kMaxCluster];
+#pragma unroll
+        for (uint32_t q = 0; q < kMaxCluster; ++q) mine[q] = q < team.size ? tops[q * kThreads + threadIdx.x] : 0u;
+        // the largest number that at least k of them reach, bit by bit; a few too many do no harm
+        uint32_t bound = 0u;
+        for (int bit = 31; bit >= 0; --bit) {
+            const uint32_t t = bound | 1u << bit;
+            uint32_t c = 0;
+#pragma unroll
+            for (uint32_t q = 0; q < kMaxCluster; ++q) c += mine[q] >= t ? 1u : 0u;
+            c = __reduce_add_sync(0xffffffffu, c);
+            if (threadIdx.x % 32 == 0) s.warp32[threadIdx.x / 32] = c;
+            __syncthreads();
+            c = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) c += s.warp32[w];
+            if (c >= static_cast<uint32_t>(k)) {
+                bound = t;
+                if (c <= static_cast<uint32_t>(k + k / 16)) break;
+            }
+            __syncthreads();
+        }
+        start_collecting(false);
+        const float lbound = logit_of(static_cast<uint64_t>(bound) << kIndexBits);
+        each_token(slice, n_slice, [&](int i, float l) {
+            if (l >= lbound && l > -INFINITY) keep(l, i0 + i);
+        });
+        // (fewer than k logits above -inf: bound is 0, lbound a NaN)
+        if (bound == 0u) {
+            start_collecting(false);
+            each_token(slice, n_slice, [&](int i, float l) {
+                if (l > -INFINITY) keep(l, i0 + i);
+            });
+        }
+        const int n = static_cast<int>(gather(team, mass_of));
+        if (n <= kCap) {
+            // every CTA ranks a share of them
+            const int at = static_cast<int>(team.rank * kThreads + threadIdx.x), step = static_cast<int>(team.size * kThreads);
+            const int mine_n = (n + step - 1) / step;            // at most 4
+            uint32_t c[4];
+            uint64_t m[4], sum = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                c[q] = 0;
+                m[q] = 0;
+                const int i = at + q * step;
+                if (q < mine_n && i < n) rank(n, s.cand[i], c[q], m[q]);
+                if (q < mine_n && i < n && c[q] < static_cast<uint32_t>(k)) sum = max(sum, m[q] + s.cmass[i]);
+            }
+            // the mass of the first k: up to and with the last of them
+            double target = all;
+            if (tp < 2.f) target = fmax(static_cast<double>(tp) * static_cast<double>(team.max_over(block_max(s, sum))), 1.0);
+            uint64_t best = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int i = at + q * step;
+                if (q < mine_n && i < n && c[q] < static_cast<uint32_t>(k) && static_cast<double>(m[q]) < target) {
+                    const float w = weight(logit_of(s.cand[i]));
+                    const uint64_t v = numbered(race(noise[index_of(s.cand[i])], w), index_of(s.cand[i]));
+                    if (w >= mp) best = v > best ? v : best;
+                }
+            }
+            finish(best);
+            return;
+        }
+    }
 
     // What stays: bins before `bin`, and in it the tokens whose number is at least `cut`.
     int bin = kBins;
     uint64_t cut = 0;
     if (k < V || tp < 2.f) {
-        clear_bins(s);
-        each_token(row, V, [&](int, float l) { add_to_bin(s, bin_of(l), mass_of(l)); });
-        __syncthreads();
-
-        // Collects the tokens of bin `b` that hold the k-th token (by_mass false) or the one at which
-        // the mass reaches `target`, narrowing while there are more than kCap of them; `count` and
-        // `mass` become those of the tokens above the collected ones.
+        // Collects the tokens of bin `b` that hold the k-th token (by_mass false) or the one at which the mass
+        // reaches `target`, narrowing while there are more than kCap of them; `count` and `mass` become those
+        // of the tokens above the collected ones.  Returns how many there are.
         bool narrowed = false;
-        auto collect = [&](int b, bool by_mass, uint32_t kk, double target, uint32_t& count, uint64_t& mass, uint32_t n) {
+        auto collect = [&](int b, bool by_mass, uint32_t kk, double target, uint32_t& count, uint64_t& mass) {
             uint64_t lo = 0;
-            int bits = kOrderBits;                           // candidates: numbers lo .. lo + 2^bits - 1
-            while (n > kCap) {
+            int bits = kOrderBits;                             // candidates: numbers lo .. lo + 2^bits - 1
+            for (;;) {
+                start_collecting(true);
+                each_token(slice, n_slice, [&](int i, float l) {
+                    if (bin_of(l) == b && (order_of(l, i0 + i) - lo) >> bits == 0) keep(l, i0 + i);
+                });
+                const uint32_t n = gather(team, mass_of);
+                if (n <= kCap) return static_cast<int>(n);
                 const int shift = bits > 11 ? bits - 11 : 0;
                 narrowed = true;
-                __syncthreads();
                 clear_bins(s);
-                each_token(row, V, [&](int i, float l) {
+                each_token(slice, n_slice, [&](int i, float l) {
                     if (bin_of(l) != b) return;
-                    const uint64_t o = order_of(l, i) - lo;
+                    const uint64_t o = order_of(l, i0 + i) - lo;
                     if (o >> bits) return;
-                    add_to_bin(s, kBins - 1 - static_cast<int>(o >> shift), mass_of(l));
+                    add_to_bin(s, kBins - 1 - static_cast<int>(o >> shift), mass_of(l), true);
                 });
-                __syncthreads();
-                find_bin(s, by_mass, kk, target, count, mass);
+                sum_bins(team);
+                find_bin(team, by_mass, kk, target, count, mass);
                 count = s.count_above;
                 mass = s.mass_above;
-                n = s.count[s.bin];
                 lo += static_cast<uint64_t>(kBins - 1 - s.bin) << shift;
                 bits = shift;
             }
-            __syncthreads();
-            if (threadIdx.x == 0) s.ncand = 0u;
-            __syncthreads();
-            each_token(row, V, [&](int i, float l) {
-                if (bin_of(l) != b) return;
-                const uint64_t o = order_of(l, i);
-                if ((o - lo) >> bits) return;
-                const uint32_t at = atomicAdd(&s.ncand, 1u);
-                if (at < kCap) {
-                    s.cand[at] = o;
-                    s.cmass[at] = mass_of(l);
-                }
-            });
-            __syncthreads();
         };
-        // Over the collected tokens, with `count` and `mass` above them: the smallest number whose
-        // token is among the first kk and has less than `target` above it (or is the row's first).
-        auto smallest_kept = [&](uint32_t kk, double target, uint32_t count, uint64_t mass, uint64_t* kept_mass) {
+        // Over the n collected tokens, with `count` and `mass` above them: the smallest number whose token is
+        // among the first kk and has less than `target` above it.
+        auto smallest_kept = [&](int n, uint32_t kk, double target, uint32_t count, uint64_t mass, uint64_t* kept_mass) {
             __syncthreads();
             if (threadIdx.x == 0) s.cut = ~0ull;
             __syncthreads();
-            const int n = min(static_cast<int>(s.ncand), kCap);
             uint64_t sum = 0;
             for (int i = threadIdx.x; i < n; i += kThreads) {
-                const uint64_t o = s.cand[i];
                 uint32_t c = count;
                 uint64_t m = mass;
-                for (int j = 0; j < n; ++j)
-                    if (s.cand[j] > o) {
-                        ++c;
-                        m += s.cmass[j];
-                    }
-                if ((c < kk && static_cast<double>(m) < target) || o == top) {
-                    atomicMin(reinterpret_cast<unsigned long long*>(&s.cut), o);
-                    sum = m + s.cmass[i];                    // largest at the smallest number
+                rank(n, s.cand[i], c, m);
+                if (c < kk && static_cast<double>(m) < target) {
+                    atomicMin(reinterpret_cast<unsigned long long*>(&s.cut), s.cand[i]);
+                    sum = max(sum, m + s.cmass[i]);              // largest at the smallest number
                 }
             }
             sum = block_max(s, sum);
@@ -307,70 +640,86 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
             __syncthreads();
             return s.cut;
         };
+        auto histogram = [&](bool counted) {
+            clear_bins(s);
+            each_token(slice, n_slice, [&](int, float l) { add_to_bin(s, bin_of(l), mass_of(l), counted); });
+        };
 
         uint32_t count = 0;
         uint64_t mass = 0;
-        const double all = 1e300;
-        double target = all;                                 // never below 1: the first token stays
+        int n = 0;
+        double target = all;                                   // never below 1: the first token stays
+        team.sync();
+        histogram(k < V);
+        const uint64_t whole = sum_bins(team);
         if (k < V) {
-            find_bin(s, false, k, 0.0, 0u, 0ull);
+            find_bin(team, false, k, 0.0, 0u, 0ull);
             bin = s.bin;
             count = s.count_above;
             mass = s.mass_above;
             uint64_t kept = mass;
-            collect(bin, false, k, 0.0, count, mass, s.count[bin]);
-            cut = smallest_kept(k, all, count, mass, &kept);
+            n = collect(bin, false, k, 0.0, count, mass);
+            cut = smallest_kept(n, k, all, count, mass, &kept);
             if (tp < 2.f) target = fmax(static_cast<double>(tp) * static_cast<double>(kept), 1.0);
         } else {
-            // the whole mass: a target that no bin reaches leaves the last one
-            find_bin(s, true, 0u, all, 0u, 0ull);
-            target = fmax(static_cast<double>(tp) * static_cast<double>(s.mass_above + bin_mass(s, s.bin)), 1.0);
+            target = fmax(static_cast<double>(tp) * static_cast<double>(whole), 1.0);
         }
         if (tp < 2.f) {
             const int kbin = bin;
-            if (narrowed) {                                  // the bins hold something else by now
-                __syncthreads();
-                clear_bins(s);
-                each_token(row, V, [&](int, float l) { add_to_bin(s, bin_of(l), mass_of(l)); });
-                __syncthreads();
+            if (narrowed) {                                    // the bins hold something else by now
+                histogram(k < V);
+                sum_bins(team);
             }
-            find_bin(s, true, 0u, target, 0u, 0ull);
+            find_bin(team, true, 0u, target, 0u, 0ull);
             const int b = s.bin;
             if (b < kbin) {
                 bin = b;
                 count = s.count_above;
                 mass = s.mass_above;
-                collect(b, true, 0u, target, count, mass, s.count[b]);
-                cut = smallest_kept(V, target, count, mass, nullptr);
-            } else if (narrowed) {                           // the same bin, but elsewhere in it
-                bin = kbin;
-                find_bin(s, false, k, 0.0, 0u, 0ull);
+                n = collect(b, true, 0u, target, count, mass);
+                cut = smallest_kept(n, V, target, count, mass, nullptr);
+            } else if (narrowed) {                             // the same bin, but elsewhere in it
+                find_bin(team, false, k, 0.0, 0u, 0ull);
                 count = s.count_above;
                 mass = s.mass_above;
-                collect(kbin, true, 0u, target, count, mass, s.count[kbin]);
-                const uint64_t pcut = smallest_kept(V, target, count, mass, nullptr);
+                n = collect(kbin, true, 0u, target, count, mass);
+                const uint64_t pcut = smallest_kept(n, V, target, count, mass, nullptr);
                 cut = pcut > cut ? pcut : cut;
             } else {
-                cut = smallest_kept(k, target, count, mass, nullptr);
+                cut = smallest_kept(n, k, target, count, mass, nullptr);
             }
         }
     }
 
-    uint64_t best = 0;
-    each_token(row, V, [&](int i, float l) {
+    float best = -1.f;
+    int at = 0;
+    auto stays = [&](int i, float l, float w) {
         const int b = bin < kBins ? bin_of(l) : 0;
-        if (b > bin) return;
-        const uint64_t o = order_of(l, i);
-        if (b == bin && o < cut) return;
-        const float w = weight(l);
-        if (!(w >= mp) && o != top) return;
-        float key = w * rcp_approx(noise[i]);
-        if (!(key >= 0.f)) key = 0.f;
-        const uint64_t v = static_cast<uint64_t>(__float_as_uint(key)) << 32 | (0xffffffffu - static_cast<uint32_t>(i));
-        best = v > best ? v : best;
+        return !(b > bin || (b == bin && order_of(l, i0 + i) < cut)) && w >= mp;
+    };
+    each_token_and_noise(slice, noise + i0, n_slice, stays, weight, [&](int i, float w, float e) {
+        const float key = race(e, w);
+        if (key > best) {                                      // (a thread's indexes increase)
+            best = key;
+            at = i;
+        }
     });
-    best = block_max(s, best);
-    if (threadIdx.x == 0) p.tokens[r] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(best));
+    finish(best >= 0.f ? numbered(best, i0 + at) : 0ull);
+}
+
+template <typename T>
+cudaError_t launch_sample(const SampleParams& p, int64_t rows, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(rows * p.cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = p.cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, sample_kernel<T>, p);
 }
 
 }  // namespace
@@ -404,9 +753,19 @@ extern "C" ss_status ss_sample(const void* logits, const float* noise, const flo
                         range3(top_p, 1, 1, rows, 0, 0, 4), range3(min_p, 1, 1, rows, 0, 0, 4)};
     for (const Range& q : in)
         if (meet(out, q)) return SS_ERR_INVALID_ARG;
-    const SampleParams p{logits, noise, temperature, top_k, top_p, min_p, tokens, logits_r, noise_r, static_cast<int>(V)};
+    // as many CTAs to a row as keep at least 2048 tokens each, up to six to an SM over all rows: a row's
+    // passes take as long as its slices (one row of 50257: 38 us with one CTA of 1024 threads)
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return SS_ERR_CUDA;
+    int cluster = 1;
+    while (cluster < kMaxCluster && (V > cluster * static_cast<int64_t>(kMaxSlice) ||
+                                     (V / (2 * cluster) >= 2048 && rows * 2 * cluster <= 6 * static_cast<int64_t>(sms))))
+        cluster *= 2;
+    const int slice = static_cast<int>(((V + cluster - 1) / cluster + 7) / 8 * 8);
+    const SampleParams p{logits, noise, temperature, top_k, top_p, min_p, tokens, logits_r, noise_r, static_cast<int>(V),
+                         static_cast<uint32_t>(cluster), slice};
+    if (rows * cluster > INT32_MAX) return SS_ERR_UNSUPPORTED;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-    if (io_dtype == SS_BF16) sample_kernel<__nv_bfloat16><<<static_cast<unsigned>(rows), kThreads, 0, stream>>>(p);
-    else sample_kernel<float><<<static_cast<unsigned>(rows), kThreads, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+    const cudaError_t e = io_dtype == SS_BF16 ? launch_sample<__nv_bfloat16>(p, rows, stream) : launch_sample<float>(p, rows, stream);
+    return e == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
