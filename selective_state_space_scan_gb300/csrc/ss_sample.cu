@@ -128,9 +128,11 @@ __device__ __forceinline__ void each_token(const T* row, int V, F&& f) {
 }
 
 // f(index, weight, noise) for every token that stays, in the order of each_token.  The noise of a pack is
-// read as a whole where its alignment allows and one of its tokens stays, else one by one.
+// read as a whole where its alignment allows: with the logits, two packs at a time, where every token may
+// stay (`eager`), else if one of its tokens does.
 template <typename T, typename S, typename Wt, typename F>
-__device__ __forceinline__ void each_token_and_noise(const T* row, const float* noise, int V, S&& stays, Wt&& weight, F&& f) {
+__device__ __forceinline__ void each_token_and_noise(const T* row, const float* noise, int V, bool eager, S&& stays, Wt&& weight,
+                                                     F&& f) {
     constexpr int W = Pack<T>::n;
     const int off = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
     const int head = min(V, off ? W - off : 0);
@@ -141,8 +143,34 @@ __device__ __forceinline__ void each_token_and_noise(const T* row, const float* 
         const float l = tidy(to_f32<T>(row[i])), w = weight(l);
         if (stays(i, l, w)) f(i, w, noise[i]);
     };
+    auto load_noise = [&](int i, float (&e)[W]) {
+        if (wide) {
+#pragma unroll
+            for (int j = 0; j < W; j += 4) Pack<float>::load(noise + i + j, e + j);
+        } else {
+#pragma unroll
+            for (int j = 0; j < W; ++j) e[j] = noise[i + j];
+        }
+    };
     if (static_cast<int>(threadIdx.x) < head) one(static_cast<int>(threadIdx.x));
-    for (int b = threadIdx.x; b < body; b += kThreads) {
+    int b = threadIdx.x;
+    if (eager)
+        for (; b + kThreads < body; b += 2 * kThreads) {
+            float v[2][W], e[2][W];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) Pack<T>::load(row + head + (b + k * kThreads) * W, v[k]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) load_noise(head + (b + k * kThreads) * W, e[k]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    const int i = head + (b + k * kThreads) * W + j;
+                    const float l = tidy(v[k][j]), w = weight(l);
+                    if (stays(i, l, w)) f(i, w, e[k][j]);
+                }
+        }
+    for (; b < body; b += kThreads) {
         const int i = head + b * W;
         float v[W], e[W];
         Pack<T>::load(row + i, v);
@@ -155,18 +183,32 @@ __device__ __forceinline__ void each_token_and_noise(const T* row, const float* 
             any = any || on[j];
         }
         if (!any) continue;
-        if (wide) {
-#pragma unroll
-            for (int j = 0; j < W; j += 4) Pack<float>::load(noise + i + j, e + j);
-        } else {
-#pragma unroll
-            for (int j = 0; j < W; ++j) e[j] = noise[i + j];
-        }
+        load_noise(i, e);
 #pragma unroll
         for (int j = 0; j < W; ++j)
             if (on[j]) f(i + j, v[j], e[j]);
     }
     if (static_cast<int>(threadIdx.x) < V - tail0) one(tail0 + static_cast<int>(threadIdx.x));
+}
+
+// f(index, logit) for every token whose logit is `bound` or more (not NaN).
+template <typename T, typename F>
+__device__ __forceinline__ void each_token_from(const T* row, int V, float bound, F&& f) {
+    constexpr int W = Pack<T>::n;
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+    const int head = min(V, off ? W - off : 0);
+    const int body = (V - head) / W;
+    const int tail0 = head + body * W;
+    auto one = [&](int i) {
+        const float l = tidy(to_f32<T>(row[i]));
+        if (l >= bound) f(i, l);
+    };
+    if (static_cast<int>(threadIdx.x) < head) one(static_cast<int>(threadIdx.x));
+    if (static_cast<int>(threadIdx.x) < V - tail0) one(tail0 + static_cast<int>(threadIdx.x));
+#pragma unroll 4
+    for (int b = threadIdx.x; b < body; b += kThreads)
+        if (Pack<T>::largest(row + head + b * W) >= bound)
+            for (int j = 0; j < W; ++j) one(head + b * W + j);
 }
 
 // f(index of the pack's first token, the pack's largest logit) for every pack: the same tokens by the same
@@ -198,6 +240,7 @@ struct Shared {
     uint64_t cand[kCap];                           // those of the whole cluster, and their masses
     uint32_t cmass[kCap];
     uint64_t slot[2][kMaxCluster];                 // a number from every CTA
+    uint64_t last[kMaxCluster];                    // and the last one, at the first CTA
     uint64_t warp64[kWarps];
     uint32_t warp32[kWarps];
     uint64_t mass_above;                           // of the bins before the found one
@@ -455,24 +498,56 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
         });
         if (at >= 0) own = first_of_pack(slice, n_slice, at, best, i0);
     }
-    const uint64_t top = team.max_over(block_max(s, own));
-    const float lmax = top ? logit_of(top) : -INFINITY;
     const float temp = p.temperature ? p.temperature[r] : 1.f;
     const float mp = p.min_p ? p.min_p[r] : 0.f;
-    if (top == 0 || temp <= 0.f || !(mp <= 1.f)) {             // nothing there; greedy; only the first token stays
-        if (team.rank == 0 && threadIdx.x == 0) p.tokens[r] = top == 0 ? -1 : index_of(top);
-        team.sync();                                           // (a peer may still read this CTA's slots)
+    const int k = p.top_k && p.top_k[r] > 0 && p.top_k[r] < V ? p.top_k[r] : V;
+    const bool first_only = temp <= 0.f || !(mp <= 1.f);       // greedy, or no weight reaches min_p
+    const bool small_k = !first_only && k <= static_cast<int>(team.size * kThreads) / 2 && k <= kCap / 2;
+    float lmax;
+    float tops[kMaxCluster];                                   // maxima of this thread's namesakes in all CTAs
+    if (small_k) {
+        // every thread's maximum, everywhere (in the place of the counts, which this path does not need)
+        static_assert(kMaxCluster * kThreads <= kBins, "a count's place for every thread");
+        const float mine = own ? logit_of(own) : -INFINITY;
+        if (team.size > 1) {
+            for (uint32_t q = 0; q < team.size; ++q)
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer_smem_addr(&s.count[team.rank * kThreads + threadIdx.x], q)),
+                             "f"(mine) : "memory");
+        } else {
+            s.count[threadIdx.x] = __float_as_uint(mine);
+        }
+        team.sync();
+        lmax = -INFINITY;
+#pragma unroll
+        for (uint32_t q = 0; q < kMaxCluster; ++q) {
+            tops[q] = q < team.size ? __uint_as_float(s.count[q * kThreads + threadIdx.x]) : -INFINITY;
+            lmax = fmaxf(lmax, tops[q]);
+        }
+        const uint64_t top = block_max(s, lmax > -INFINITY ? order_of(lmax, 0) : 0ull);
+        lmax = top ? logit_of(top) : -INFINITY;
+    } else {
+        const uint64_t top = team.max_over(block_max(s, own));
+        lmax = top ? logit_of(top) : -INFINITY;
+        if (first_only && top != 0) {
+            if (team.rank == 0 && threadIdx.x == 0) p.tokens[r] = index_of(top);
+            team.sync();                                       // (a peer may still read this CTA's slots)
+            return;
+        }
+    }
+    if (lmax == -INFINITY) {                                   // nothing there
+        if (team.rank == 0 && threadIdx.x == 0) p.tokens[r] = -1;
+        team.sync();
         return;
     }
     const float inv_t = fminf(1.f / (temp > 0.f ? temp : 1.f), 1e35f);   // finite times any reach
     const float c2 = inv_t * kLog2e;
-    const int k = p.top_k && p.top_k[r] > 0 && p.top_k[r] < V ? p.top_k[r] : V;
     const float tp = p.top_p && p.top_p[r] < 1.f ? p.top_p[r] : 2.f;
     const double all = 1e300;
 
     auto weight = [&](float l) { return l == -INFINITY ? 0.f : ex2((l - lmax) * c2); };
     const float per_bin = inv_t * (kBins / kReach);
-    auto bin_of = [&](float l) { return static_cast<int>(fminf((lmax - l) * per_bin, kBins - 1.f)); };
+    // (rounded by adding 2^23: monotone in l, and cheaper than a conversion)
+    auto bin_of = [&](float l) { return __float_as_int(fminf((lmax - l) * per_bin, kBins - 1.f) + 8388608.f) & (kBins - 1); };
     auto mass_of = [&](float l) { return __float2uint_rn(weight(l) * kMassOne); };
     auto race = [&](float e, float w) {                        // the race's key, larger is better; NaN as 0
         const float key = w * rcp_approx(e);
@@ -481,10 +556,20 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
     auto numbered = [&](float key, int i) {                    // the lower index among equals
         return static_cast<uint64_t>(__float_as_uint(key)) << 32 | (0xffffffffu - static_cast<uint32_t>(i));
     };
+    // the best of the CTAs' best, at the first of them (peers may read this CTA's memory up to that sync)
     auto finish = [&](uint64_t best) {
-        best = team.max_over(block_max(s, best));
-        if (team.rank == 0 && threadIdx.x == 0) p.tokens[r] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(best));
+        best = block_max(s, best);
+        if (threadIdx.x == 0) {
+            if (team.size > 1)
+                asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(peer_smem_addr(&s.last[team.rank], 0)), "l"(best) : "memory");
+            else
+                s.last[0] = best;
+        }
         team.sync();
+        if (team.rank == 0 && threadIdx.x == 0) {
+            for (uint32_t q = 0; q < team.size; ++q) best = s.last[q] > best ? s.last[q] : best;
+            p.tokens[r] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(best));
+        }
     };
     auto keep = [&](float l, int i) {
         const uint32_t at = atomicAdd(&s.ncand, 1u);
@@ -505,52 +590,45 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
             }
     };
 
-    if (k <= static_cast<int>(team.size * kThreads) / 2 && k <= kCap / 2) {
-        // every thread's maximum, everywhere (in the place of the counts, which this path does not need)
-        static_assert(kMaxCluster * kThreads <= kBins, "a count's place for every thread");
-        uint32_t* tops = s.count;
-        if (team.size > 1) {
-            for (uint32_t q = 0; q < team.size; ++q)
-                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_smem_addr(&tops[team.rank * kThreads + threadIdx.x], q)),
-                             "r"(static_cast<uint32_t>(own >> kIndexBits)) : "memory");
-        } else {
-            tops[threadIdx.x] = static_cast<uint32_t>(own >> kIndexBits);
-        }
-        team.sync();
-        uint32_t mine[kMaxCluster];
-#pragma unroll
-        for (uint32_t q = 0; q < kMaxCluster; ++q) mine[q] = q < team.size ? tops[q * kThreads + threadIdx.x] : 0u;
-        // the largest number that at least k of them reach, bit by bit; a few too many do no harm
-        uint32_t bound = 0u;
-        for (int bit = 31; bit >= 0; --bit) {
-            const uint32_t t = bound | 1u << bit;
+    if (small_k) {
+        // A bound that at least k of the maxima reach, and not many more: down from the largest logit by
+        // doubled steps, then by halves.  Where that does not get there, all logits are collected.
+        auto reach = [&](float t) {
             uint32_t c = 0;
 #pragma unroll
-            for (uint32_t q = 0; q < kMaxCluster; ++q) c += mine[q] >= t ? 1u : 0u;
+            for (uint32_t q = 0; q < kMaxCluster; ++q) c += tops[q] >= t ? 1u : 0u;
             c = __reduce_add_sync(0xffffffffu, c);
+            __syncthreads();
             if (threadIdx.x % 32 == 0) s.warp32[threadIdx.x / 32] = c;
             __syncthreads();
             c = 0;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) c += s.warp32[w];
-            if (c >= static_cast<uint32_t>(k)) {
-                bound = t;
-                if (c <= static_cast<uint32_t>(k + k / 16)) break;
+            return static_cast<int>(c);
+        };
+        float bound = -FLT_MAX, near = 0.f, far = 1.f;         // distances from the largest: too few, enough
+        int c = 0;
+        for (; far < 1e30f; far *= 4.f) {
+            c = reach(lmax - far);
+            if (c >= k) break;
+            near = far;
+        }
+        if (c >= k) {
+            bound = lmax - far;
+            for (int i = 0; i < 24 && c > k + 64; ++i) {
+                const float mid = 0.5f * (near + far);
+                const int n = reach(lmax - mid);
+                if (n >= k) {
+                    far = mid;
+                    c = n;
+                    bound = lmax - mid;
+                } else {
+                    near = mid;
+                }
             }
-            __syncthreads();
         }
         start_collecting(false);
-        const float lbound = logit_of(static_cast<uint64_t>(bound) << kIndexBits);
-        each_token(slice, n_slice, [&](int i, float l) {
-            if (l >= lbound && l > -INFINITY) keep(l, i0 + i);
-        });
-        // (fewer than k logits above -inf: bound is 0, lbound a NaN)
-        if (bound == 0u) {
-            start_collecting(false);
-            each_token(slice, n_slice, [&](int i, float l) {
-                if (l > -INFINITY) keep(l, i0 + i);
-            });
-        }
+        each_token_from(slice, n_slice, bound, [&](int i, float l) { keep(l, i0 + i); });
         const int n = static_cast<int>(gather(team, mass_of));
         if (n <= kCap) {
             // every CTA ranks a share of them
@@ -697,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
         const int b = bin < kBins ? bin_of(l) : 0;
         return !(b > bin || (b == bin && order_of(l, i0 + i) < cut)) && w >= mp;
     };
-    each_token_and_noise(slice, noise + i0, n_slice, stays, weight, [&](int i, float w, float e) {
+    each_token_and_noise(slice, noise + i0, n_slice, bin == kBins && mp <= 0.f, stays, weight, [&](int i, float w, float e) {
         const float key = race(e, w);
         if (key > best) {                                      // (a thread's indexes increase)
             best = key;
