@@ -364,14 +364,14 @@ __device__ uint64_t sum_bins(Team& team) {
 // After sum_bins: the first bin at which the running count, begun at `count`, reaches `k` (by_mass false),
 // or the running mass, begun at `mass`, reaches `target` (by_mass true); the last bin if none does.  Leaves
 // it in s.bin, with what is before it, in every CTA.  Histograms may be cleared after it.
-__device__ void find_bin(Team& team, bool by_mass, uint32_t k, double target, uint32_t count, uint64_t mass) {
+__device__ void find_bin(Team& team, bool by_mass, uint32_t k, uint64_t target, uint32_t count, uint64_t mass) {
     Shared& s = team.s;
     // the CTA whose share it is in
     uint32_t owner = 0;
     for (; owner < team.size; ++owner) {
         const uint32_t c = team.size > 1 ? ld_peer_u32(peer_smem_addr(&s.share_count, owner)) : s.share_count;
         const uint64_t m = team.size > 1 ? ld_peer_u64(peer_smem_addr(&s.share_mass, owner)) : s.share_mass;
-        if (owner == team.size - 1 || (by_mass ? static_cast<double>(mass + m) >= target : count + c >= k)) break;
+        if (owner == team.size - 1 || (by_mass ? mass + m >= target : count + c >= k)) break;
         count += c;
         mass += m;
     }
@@ -418,7 +418,7 @@ __device__ void find_bin(Team& team, bool by_mass, uint32_t k, double target, ui
             uint64_t mj;
             whole_bin(team, b0 + j, cj, mj);
             const bool end = threadIdx.x == kThreads - 1 && j == each - 1;
-            if (mine == kBins && (end || (by_mass ? static_cast<double>(mb + mj) >= target : cb + cj >= k))) {
+            if (mine == kBins && (end || (by_mass ? mb + mj >= target : cb + cj >= k))) {
                 mine = b0 + j;
                 c_at = cb;
                 m_at = mb;
@@ -542,8 +542,14 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
     const float inv_t = fminf(1.f / (temp > 0.f ? temp : 1.f), 1e35f);   // finite times any reach
     const float c2 = inv_t * kLog2e;
     const float tp = p.top_p && p.top_p[r] < 1.f ? p.top_p[r] : 2.f;
-    const double all = 1e300;
+    const uint64_t all = ~0ull;
 
+    // top_p of a mass, rounded up and at least 1 (the first token stays), in whole numbers: doubles are slow here
+    const uint64_t tq = tp > 0.f && tp < 1.f ? static_cast<uint64_t>(tp * 18446744073709551616.f) : 0ull;      // exact
+    auto share_of = [&](uint64_t mass) {
+        const uint64_t v = __umul64hi(mass, tq) + (mass * tq != 0 ? 1 : 0);
+        return v > 0 ? v : static_cast<uint64_t>(1);
+    };
     auto weight = [&](float l) { return l == -INFINITY ? 0.f : ex2((l - lmax) * c2); };
     const float per_bin = inv_t * (kBins / kReach);
     // (rounded by adding 2^23: monotone in l, and cheaper than a conversion)
@@ -645,13 +651,13 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
                 if (q < mine_n && i < n && c[q] < static_cast<uint32_t>(k)) sum = max(sum, m[q] + s.cmass[i]);
             }
             // the mass of the first k: up to and with the last of them
-            double target = all;
-            if (tp < 2.f) target = fmax(static_cast<double>(tp) * static_cast<double>(team.max_over(block_max(s, sum))), 1.0);
+            uint64_t target = all;
+            if (tp < 2.f) target = share_of(team.max_over(block_max(s, sum)));
             uint64_t best = 0;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int i = at + q * step;
-                if (q < mine_n && i < n && c[q] < static_cast<uint32_t>(k) && static_cast<double>(m[q]) < target) {
+                if (q < mine_n && i < n && c[q] < static_cast<uint32_t>(k) && m[q] < target) {
                     const float w = weight(logit_of(s.cand[i]));
                     const uint64_t v = numbered(race(noise[index_of(s.cand[i])], w), index_of(s.cand[i]));
                     if (w >= mp) best = v > best ? v : best;
@@ -670,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
         // reaches `target`, narrowing while there are more than kCap of them; `count` and `mass` become those
         // of the tokens above the collected ones.  Returns how many there are.
         bool narrowed = false;
-        auto collect = [&](int b, bool by_mass, uint32_t kk, double target, uint32_t& count, uint64_t& mass) {
+        auto collect = [&](int b, bool by_mass, uint32_t kk, uint64_t target, uint32_t& count, uint64_t& mass) {
             uint64_t lo = 0;
             int bits = kOrderBits;                             // candidates: numbers lo .. lo + 2^bits - 1
             for (;;) {
@@ -699,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
         };
         // Over the n collected tokens, with `count` and `mass` above them: the smallest number whose token is
         // among the first kk and has less than `target` above it.
-        auto smallest_kept = [&](int n, uint32_t kk, double target, uint32_t count, uint64_t mass, uint64_t* kept_mass) {
+        auto smallest_kept = [&](int n, uint32_t kk, uint64_t target, uint32_t count, uint64_t mass, uint64_t* kept_mass) {
             __syncthreads();
             if (threadIdx.x == 0) s.cut = ~0ull;
             __syncthreads();
@@ -708,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
                 uint32_t c = count;
                 uint64_t m = mass;
                 rank(n, s.cand[i], c, m);
-                if (c < kk && static_cast<double>(m) < target) {
+                if (c < kk && m < target) {
                     atomicMin(reinterpret_cast<unsigned long long*>(&s.cut), s.cand[i]);
                     sum = max(sum, m + s.cmass[i]);              // largest at the smallest number
                 }
@@ -726,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
         uint32_t count = 0;
         uint64_t mass = 0;
         int n = 0;
-        double target = all;                                   // never below 1: the first token stays
+        uint64_t target = all;                                   // never below 1: the first token stays
         team.sync();
         histogram(k < V);
         const uint64_t whole = sum_bins(team);
@@ -738,9 +744,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
             uint64_t kept = mass;
             n = collect(bin, false, k, 0.0, count, mass);
             cut = smallest_kept(n, k, all, count, mass, &kept);
-            if (tp < 2.f) target = fmax(static_cast<double>(tp) * static_cast<double>(kept), 1.0);
+            if (tp < 2.f) target = share_of(kept);
         } else {
-            target = fmax(static_cast<double>(tp) * static_cast<double>(whole), 1.0);
+            target = share_of(whole);
         }
         if (tp < 2.f) {
             const int kbin = bin;
