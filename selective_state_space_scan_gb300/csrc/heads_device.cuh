@@ -65,17 +65,9 @@ __device__ __forceinline__ float heads_conv(const float w[4], float b, float e0,
     return silu(fmaf(w[3], e3, fmaf(w[2], e2, fmaf(w[1], e1, fmaf(w[0], e0, b)))));
 }
 
-// silu of two values with one reciprocal, 1/a = b·(1/(ab)): the SFU is what such streams run out of.
-// The exponent stops at 62, so that the product stays finite: below z = -43 the result is z·2^-62.
-__device__ __forceinline__ float2 silu2_joint(float2 z) {
-    const float2 n = mul2(z, splat2(-kLog2e));
-    const float2 d = add2(splat2(1.f), make_float2(ex2(fminf(n.x, 62.f)), ex2(fminf(n.y, 62.f))));
-    const float r = rcp_approx(d.x * d.y);
-    return mul2(z, make_float2(r * d.y, r * d.x));
-}
 // heads_conv of two channels; w[k] their weights of sample k.
 __device__ __forceinline__ float2 heads_conv2(const float2 w[4], float2 b, float2 e0, float2 e1, float2 e2, float2 e3) {
-    return silu2_joint(fma2(w[3], e3, fma2(w[2], e2, fma2(w[1], e1, fma2(w[0], e0, b)))));
+    return silu2(fma2(w[3], e3, fma2(w[2], e2, fma2(w[1], e1, fma2(w[0], e0, b)))));
 }
 
 // Sum over the block's threads before this one, and over all of them.

@@ -22,6 +22,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cstddef>
 #include <cstdint>
 
 #include "../../include/selscan.h"
@@ -217,7 +218,7 @@ constexpr uint32_t kImage = 2 * kBlock;            // B hi, B lo or C in shared 
 constexpr uint32_t kTileBytes = 4 * kBlock;        // per tile: x, x scaled hi, x scaled lo, state
 constexpr int kFacs = 192;                         // decay factors of the blocks off the diagonal
 constexpr int kToks = 8;                           // tokens per thread in the convolution and the output
-struct TcTables {
+struct alignas(16) TcTables {                      // (read in runs of four floats)
     float tail[kQ];                                // Δ_s · decay from s to the chunk's end
     float fac[kFacs];                              // Δ_s · decay from s to the start of a later block of 32
     float total[4];                                // log2 decay of the blocks of 32
@@ -231,6 +232,7 @@ struct TcShared {
     TcTables tab[2];
 };
 constexpr uint32_t kTcSmem = 3 * kImage + 2 * kTileBytes + sizeof(TcShared);
+static_assert(offsetof(TcTables, fac) % 16 == 0 && offsetof(TcShared, tab) % 16 == 0, "16-byte loads");
 static_assert(kTcSmem <= 232448, "227 KB of shared memory per CTA");
 
 // Columns of tensor memory: scores, C·S and then y of both tiles, what the chunk adds to the state of
@@ -717,8 +719,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                         float2 y1 = fma2(Dd, add2(unpack2(x.y), unpack2(xlo[j].y)), make_float2(v.z, v.w));
                         if (p.z) {
                             const float4 z = gate[j].get();
-                            y0 = mul2(y0, silu2_joint(make_float2(z.x, z.y)));
-                            y1 = mul2(y1, silu2_joint(make_float2(z.z, z.w)));
+                            y0 = mul2(y0, silu2(make_float2(z.x, z.y)));
+                            y1 = mul2(y1, silu2(make_float2(z.z, z.w)));
                         }
                         Quad4<TIO, VEC>::store(y, row < nt ? nq : 0, make_float4(y0.x, y0.y, y1.x, y1.y));
                         y += p.y_t;

@@ -108,7 +108,7 @@ __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u 
 __device__ __forceinline__ float2 unpack2(uint32_t u) { return make_float2(bf16_lo(u), bf16_hi(u)); }
 // What rounding to the pair `u` left of v, rounded in turn.
 __device__ __forceinline__ uint32_t pack_rest(float2 v, uint32_t u) {
-    const float2 r = add2(v, make_float2(-bf16_lo(u), -bf16_hi(u)));
+    const float2 r = fma2(unpack2(u), splat2(-1.f), v);
     return pack_bf16(r.x, r.y);
 }
 
