@@ -91,22 +91,13 @@ __device__ __forceinline__ int block_prefix(int v, int* total, int* scratch) {
     return before + x - v;
 }
 
-// The heads of a group share its B and C channels: each CTA that reads their windows says so here
-// when it has, and the last one to say so (it returns true there, for all its threads) may
-// overwrite them.  The counter is back at zero then.
-__device__ __forceinline__ bool heads_last_reader(unsigned int* counter, unsigned int readers) {
-    __shared__ int last;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        __threadfence();
-        last = atomicAdd(counter, 1u) == readers - 1u;
-        if (last) {
-            *counter = 0u;
-            __threadfence();
-        }
-    }
-    __syncthreads();
-    return last != 0;
+// The heads of a group share its B and C channels.  Each CTA that reads their windows says so on the
+// group's counter once all its threads have (behind a barrier), and the one that finds itself the last
+// may overwrite them; it puts the counter back to zero.
+__device__ __forceinline__ unsigned int heads_say_read(unsigned int* counter) {
+    unsigned int before;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+    return before;
 }
 
 }  // namespace selscan

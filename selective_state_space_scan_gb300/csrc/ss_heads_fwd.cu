@@ -282,7 +282,14 @@ __global__ void __launch_bounds__(32 * LPR) heads_seq_kernel(const SeqParams q) 
     // B and C the group's, whose last reader shifts them
     __syncthreads();
     for (int k = tid; k < np; k += NT) heads_keep_window<TIO>(p, s, cx + k);
-    if (heads_last_reader(p.arrivals + static_cast<int64_t>(seq) * p.G + g, (p.H / p.G) * tiles))
+    __shared__ int last_reader;
+    if (tid == 0) {
+        unsigned int* counter = p.arrivals + static_cast<int64_t>(seq) * p.G + g;
+        last_reader = heads_say_read(counter) == static_cast<unsigned int>((p.H / p.G) * tiles) - 1u;
+        if (last_reader) *counter = 0u;
+    }
+    __syncthreads();
+    if (last_reader)
         for (int k = tid; k < 2 * p.N; k += NT) heads_keep_window<TIO>(p, s, k < p.N ? cb + k : cc + k - p.N);
 }
 

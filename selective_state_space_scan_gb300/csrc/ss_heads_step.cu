@@ -12,13 +12,12 @@
 #include "../../include/selscan.h"
 #include "heads_device.cuh"
 #include "heads_params.h"
+#include "heads_tc.h"
 #include "internal.h"
 
 namespace selscan {
 namespace {
 
-constexpr int kStepThreads = 128;
-constexpr int kStepWarps = kStepThreads / 32;
 
 // One token of request b as a sequence.
 __device__ __forceinline__ HeadsSeq step_seq(const HeadsParams& p, int b) {
@@ -33,10 +32,11 @@ __device__ __forceinline__ HeadsSeq step_seq(const HeadsParams& p, int b) {
 
 // LPR lanes share a row of the state, each with NV runs of W adjacent states (W = 4: 16-byte
 // accesses, N = 4·LPR·NV; W = 1: any N up to 32·NV); a warp takes RPI = 32/LPR rows at once, U times.
-template <typename TIO, int LPR, int NV, int W, int U>
-__global__ void __launch_bounds__(kStepThreads) heads_step_kernel(const HeadsParams p) {
-    constexpr int RPI = 32 / LPR, RW = RPI * U, RC = RW * kStepWarps, NP = LPR * NV * W;
+template <typename TIO, int LPR, int NV, int W, int U, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, W == 4 ? 32 / WARPS : 1) heads_step_kernel(const HeadsParams p) {
+    constexpr int RPI = 32 / LPR, RW = RPI * U, RC = RW * WARPS, NP = LPR * NV * W, kStepThreads = 32 * WARPS;
     __shared__ float sB[NP], sC[NP], sx[RC];
+    __shared__ int last_reader;
     const int tiles = (p.P + RC - 1) / RC;
     int id = blockIdx.x;
     const int pt = id % tiles;
@@ -95,6 +95,10 @@ __global__ void __launch_bounds__(kStepThreads) heads_step_kernel(const HeadsPar
                               (p.dt_bias ? p.dt_bias[h] : 0.f));
     const float a = ex2(dt * (-expf(p.A_log[h]) * kLog2e)), Dh = p.D ? p.D[h] : 0.f;
     __syncthreads();
+    // the windows are read: said before the state's stores, which it would wait for, and looked at after them
+    unsigned int* counter = p.arrivals + static_cast<int64_t>(b) * p.G + g;
+    unsigned int said = 0u;
+    if (s.slot >= 0 && threadIdx.x == kStepThreads - 1) said = heads_say_read(counter);
     float B[NV][W], C[NV][W];
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -137,28 +141,38 @@ __global__ void __launch_bounds__(kStepThreads) heads_step_kernel(const HeadsPar
         }
     }
     if (s.slot < 0) return;
-    if (heads_last_reader(p.arrivals + static_cast<int64_t>(b) * p.G + g, (p.H / p.G) * tiles))
+    if (threadIdx.x == kStepThreads - 1) {
+        last_reader = said == static_cast<unsigned int>((p.H / p.G) * tiles) - 1u;
+        if (last_reader) *counter = 0u;
+    }
+    __syncthreads();
+    if (last_reader)
         for (int k = threadIdx.x; k < 2 * p.N; k += kStepThreads)
             heads_keep_window<TIO>(p, s, k < p.N ? cb + k : cc + k - p.N);
 }
 
-template <typename TIO, int LPR, int NV, int W, int U>
+template <typename TIO, int LPR, int NV, int W, int U, int WARPS>
 cudaError_t launch_one(const HeadsParams& p, cudaStream_t stream) {
-    constexpr int RC = (32 / LPR) * U * kStepWarps;
+    constexpr int RC = (32 / LPR) * U * WARPS;
     const int64_t blocks = static_cast<int64_t>(p.n_seq) * p.H * ((p.P + RC - 1) / RC);
-    heads_step_kernel<TIO, LPR, NV, W, U><<<static_cast<unsigned>(blocks), kStepThreads, 0, stream>>>(p);
+    heads_step_kernel<TIO, LPR, NV, W, U, WARPS><<<static_cast<unsigned>(blocks), 32 * WARPS, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
 template <typename TIO>
 cudaError_t launch_step_heads(const HeadsParams& p, cudaStream_t stream) {
     const bool vec = host::is_aligned(p.state, 16);
-    if (vec && p.N == 128) return launch_one<TIO, 32, 1, 4, 8>(p, stream);
-    if (vec && p.N == 64) return launch_one<TIO, 16, 1, 4, 8>(p, stream);
-    if (vec && p.N == 32) return launch_one<TIO, 8, 1, 4, 4>(p, stream);
-    if (vec && p.N == 16) return launch_one<TIO, 4, 1, 4, 2>(p, stream);
-    if (p.N <= 64) return launch_one<TIO, 32, 2, 1, 8>(p, stream);
-    return launch_one<TIO, 32, 8, 1, 4>(p, stream);
+    // a CTA's convolution of the group's B and C is shared by its rows, so it has 64 of them, unless that
+    // makes fewer CTAs than two to an SM: then 8 or 16
+    const bool few = static_cast<int64_t>(p.n_seq) * p.H * ((p.P + 63) / 64) < 2 * heads_sm_count();
+    if (vec && p.N == 128)
+        return few ? launch_one<TIO, 32, 1, 4, 2, 4>(p, stream) : launch_one<TIO, 32, 1, 4, 8, 8>(p, stream);
+    if (vec && p.N == 64)
+        return few ? launch_one<TIO, 16, 1, 4, 2, 4>(p, stream) : launch_one<TIO, 16, 1, 4, 8, 4>(p, stream);
+    if (vec && p.N == 32) return launch_one<TIO, 8, 1, 4, 4, 4>(p, stream);
+    if (vec && p.N == 16) return launch_one<TIO, 4, 1, 4, 2, 4>(p, stream);
+    if (p.N <= 64) return launch_one<TIO, 32, 2, 1, 8, 4>(p, stream);
+    return launch_one<TIO, 32, 8, 1, 4, 4>(p, stream);
 }
 
 }  // namespace

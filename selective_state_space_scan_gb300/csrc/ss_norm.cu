@@ -79,13 +79,20 @@ __device__ __forceinline__ void store_run(T* q, int n, const float v[kRun]) {
             if (i < n) q[i] = from_f32<T>(v[i]);
     }
 }
-// The codes of v / scale (round to nearest even; at most 448 by the choice of scale).
+// The codes of v / scale (round to nearest even; at most 448 by the choice of scale).  The quotient is
+// v·(1/scale) and one correction by its remainder: as good as rounded once, so that a value near the
+// middle of two codes goes where a division would put it.
 template <bool VEC>
-__device__ __forceinline__ void store_codes(uint8_t* q, int n, const float v[kRun], float inv) {
+__device__ __forceinline__ void store_codes(uint8_t* q, int n, const float v[kRun], float scale) {
+    const float inv = 1.f / scale;
     uint32_t lo[4];
+    auto quotient = [&](float x) {
+        const float f = x * inv;
+        return fmaf(fmaf(-f, scale, x), inv, f);
+    };
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        lo[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i] * inv, v[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+        lo[i] = __nv_cvt_float2_to_fp8x2(make_float2(quotient(v[2 * i]), quotient(v[2 * i + 1])), __NV_SATFINITE, __NV_E4M3);
     if constexpr (VEC) {
         __stcs(reinterpret_cast<uint2*>(q), make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16));
     } else {
@@ -204,7 +211,7 @@ __global__ void __launch_bounds__(512) norm_kernel(const NormParams p) {
         for (int k = 0; k < K; ++k) {
             const int c = (k * nt + tid) * kRun;
             const int n = min(kRun, p.D - c);
-            if (n > 0) store_codes<VEC>(y + c, n, r[k], 1.f / __uint_as_float(m[k]));
+            if (n > 0) store_codes<VEC>(y + c, n, r[k], __uint_as_float(m[k]));
         }
     }
 }
