@@ -53,6 +53,8 @@ __global__ void __launch_bounds__(32 * WARPS, W == 4 ? 32 / WARPS : 1) heads_ste
     const int lr = lane % LPR, rr = lane / LPR;
     float* Sg = p.state + ((static_cast<int64_t>(max(s.slot, 0)) * p.H + h) * p.P + p0) * p.N;
 
+    const int N = W == 4 ? NP : p.N;                                   // (whole rows of 16-byte runs)
+    float* mine = Sg + static_cast<int64_t>(warp * RW + rr) * N + lr * W;
     float S[U][NV][W];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -60,13 +62,13 @@ __global__ void __launch_bounds__(32 * WARPS, W == 4 ? 32 / WARPS : 1) heads_ste
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int n = (j * LPR + lr) * W;
-            const bool on = s.warm && row < np && n < p.N;
+            const bool on = s.warm && row < np && n < N;
+            const float* q = mine + u * RPI * N + j * LPR * W;
             if constexpr (W == 4) {
-                const float4 v = on ? __ldcs(reinterpret_cast<const float4*>(Sg + static_cast<int64_t>(row) * p.N + n))
-                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 v = on ? __ldcs(reinterpret_cast<const float4*>(q)) : make_float4(0.f, 0.f, 0.f, 0.f);
                 S[u][j][0] = v.x; S[u][j][1] = v.y; S[u][j][2] = v.z; S[u][j][3] = v.w;
             } else {
-                S[u][j][0] = on ? __ldcs(Sg + static_cast<int64_t>(row) * p.N + n) : 0.f;
+                S[u][j][0] = on ? __ldcs(q) : 0.f;
             }
         }
     }
@@ -107,39 +109,63 @@ __global__ void __launch_bounds__(32 * WARPS, W == 4 ? 32 / WARPS : 1) heads_ste
             B[j][i] = sB[(j * LPR + lr) * W + i];
             C[j][i] = sC[(j * LPR + lr) * W + i];
         }
+    float acc[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int row = warp * RW + u * RPI + rr;
-        const float x = sx[row], dx = dt * x;
-        float acc = 0.f;
+        const float dx = dt * sx[row];
+        acc[u] = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int i = 0; i < W; ++i) {
                 S[u][j][i] = fmaf(a, S[u][j][i], dx * B[j][i]);
-                acc = fmaf(S[u][j][i], C[j][i], acc);
+                acc[u] = fmaf(S[u][j][i], C[j][i], acc[u]);
             }
         if (s.slot >= 0 && row < np)
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int n = (j * LPR + lr) * W;
-                if (n < p.N) {
-                    float* q = Sg + static_cast<int64_t>(row) * p.N + n;
+                if (n < N) {
+                    float* q = mine + u * RPI * N + j * LPR * W;
                     if constexpr (W == 4)
                         __stcs(reinterpret_cast<float4*>(q), make_float4(S[u][j][0], S[u][j][1], S[u][j][2], S[u][j][3]));
                     else
                         __stcs(q, S[u][j][0]);
                 }
             }
+    }
+    // sums over the lanes of a row: at each exchange a lane keeps half of its rows, so that the outputs of
+    // the warp's rows end up in different lanes
+    constexpr int kLeft = U > LPR ? U / LPR : 1, kSame = LPR > U ? LPR / U : 1;      // rows per lane; lanes with the same row
+    int cnt = U, at = 0;
 #pragma unroll
-        for (int o = LPR / 2; o > 0; o /= 2) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-        if (lr == 0 && row < np) {
-            float v = fmaf(Dh, x, acc);
-            const int c = cx + row;
-            if (p.z) v *= silu(to_f32<TIO>(static_cast<const TIO*>(p.z)[s.row0 * p.z_t + c]));
-            static_cast<TIO*>(p.y)[s.row0 * p.y_t + c] = from_f32<TIO>(v);
+    for (int o = LPR / 2; o > 0; o /= 2) {
+        if (cnt > 1) {
+            cnt /= 2;
+            const bool up = lr & o;
+#pragma unroll
+            for (int i = 0; i < U / 2; ++i)
+                if (i < cnt) {
+                    const float give = up ? acc[i] : acc[i + cnt];
+                    acc[i] = (up ? acc[i + cnt] : acc[i]) + __shfl_xor_sync(0xffffffffu, give, o);
+                }
+            at += up ? cnt : 0;
+        } else {
+            acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
         }
     }
+    if (lr % kSame == 0)
+#pragma unroll
+        for (int i = 0; i < kLeft; ++i) {
+            const int row = warp * RW + (at + i) * RPI + rr;
+            if (row < np) {
+                const int c = cx + row;
+                float v = fmaf(Dh, sx[row], acc[i]);
+                if (p.z) v *= silu(to_f32<TIO>(static_cast<const TIO*>(p.z)[s.row0 * p.z_t + c]));
+                static_cast<TIO*>(p.y)[s.row0 * p.y_t + c] = from_f32<TIO>(v);
+            }
+        }
     if (s.slot < 0) return;
     if (threadIdx.x == kStepThreads - 1) {
         last_reader = said == static_cast<unsigned int>((p.H / p.G) * tiles) - 1u;
