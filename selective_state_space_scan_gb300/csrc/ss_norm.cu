@@ -9,6 +9,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <cstring>
 
@@ -33,32 +34,56 @@ struct NormParams {
     int64_t x_r, res_r, res_out_r, y_r;
     int D, block;           // block 0: the row
     int nblocks;
+    int64_t rows;
     float eps, inv_d;
 };
 
-// 8 adjacent elements; `n` of them exist.  VEC: n is 8 and the address 16-byte (fp32, bf16) or
-// 8-byte (e4m3) aligned.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_run(const T* q, int n, float v[kRun]) {
-    if constexpr (VEC && sizeof(T) == 2) {
-        const uint4 u = __ldcs(reinterpret_cast<const uint4*>(q));
-        const uint32_t a[4] = {u.x, u.y, u.z, u.w};
+// 8 adjacent elements as loaded; `n` of them exist.  VEC: n is 8 or none, and the address 16-byte aligned.
+template <typename T, bool VEC> struct Raw {
+    static constexpr int kWords = sizeof(T) == 2 ? 1 : 2;
+    uint4 u[kWords];
+    __device__ __forceinline__ void load(const T* q, int n) {
+        if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(a[i] << 16);
-            v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+            for (int i = 0; i < kWords; ++i)
+                u[i] = n > 0 ? __ldcs(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0u, 0u, 0u, 0u);
+        } else {
+            T v[kRun];
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) v[i] = i < n ? q[i] : from_f32<T>(0.f);
+            if constexpr (sizeof(T) == 2) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] = static_cast<uint32_t>(__bfloat16_as_ushort(v[2 * i])) | static_cast<uint32_t>(__bfloat16_as_ushort(v[2 * i + 1])) << 16;
+                u[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    u[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                                      __float_as_uint(v[4 * i + 3]));
+            }
         }
-    } else if constexpr (VEC) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float4 f = __ldcs(reinterpret_cast<const float4*>(q) + i);
-            v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) v[i] = i < n ? to_f32<T>(q[i]) : 0.f;
     }
-}
+    __device__ __forceinline__ void get(float v[kRun]) const {
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t a[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = __uint_as_float(a[i] << 16);
+                v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                v[4 * i] = __uint_as_float(u[i].x);
+                v[4 * i + 1] = __uint_as_float(u[i].y);
+                v[4 * i + 2] = __uint_as_float(u[i].z);
+                v[4 * i + 3] = __uint_as_float(u[i].w);
+            }
+        }
+    }
+};
 template <typename T, bool VEC>
 __device__ __forceinline__ void store_run(T* q, int n, const float v[kRun]) {
     if constexpr (VEC && sizeof(T) == 2) {
@@ -112,125 +137,156 @@ __device__ __forceinline__ float scale_of(uint32_t amax) {
 
 template <typename TIO, typename TR, bool F8, bool VEC, int K>
 __global__ void __launch_bounds__(512) norm_kernel(const NormParams p) {
-    __shared__ float part[16];
-    __shared__ uint32_t pmax[16];
-    const int64_t row = blockIdx.x;
+    __shared__ float part[2][16];
+    __shared__ uint32_t pmax[2][16];
     const int tid = threadIdx.x, nt = blockDim.x, warp = tid / 32, lane = tid % 32;
-    const TIO* x = static_cast<const TIO*>(p.x) + row * p.x_r;
-    const TR* res = p.res ? static_cast<const TR*>(p.res) + row * p.res_r : nullptr;
-    float r[K][kRun];
-    float sum = 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int c = (k * nt + tid) * kRun;
-        const int n = min(kRun, p.D - c);
-        float b[kRun];
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) r[k][i] = b[i] = 0.f;
-        if (n > 0) {
-            load_run<TIO, VEC>(x + c, n, r[k]);
-            if (res) load_run<TR, VEC>(res + c, n, b);
-        }
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) r[k][i] += b[i];
-    }
-    if (p.res_out) {
-        TR* ro = static_cast<TR*>(p.res_out) + row * p.res_out_r;
+    Raw<TIO, VEC> rx[K];
+    Raw<TR, VEC> rr[K];
+    auto load_row = [&](int64_t row) {
+        const TIO* x = static_cast<const TIO*>(p.x) + row * p.x_r;
+        const TR* res = p.res ? static_cast<const TR*>(p.res) + row * p.res_r : nullptr;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (k * nt + tid) * kRun;
-            const int n = min(kRun, p.D - c);
-            if (n > 0) store_run<TR, VEC>(ro + c, n, r[k]);
+            rx[k].load(x + c, p.D - c);
+            rr[k].load(res + c, res ? p.D - c : 0);
         }
-    }
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) sum = fmaf(r[k][i], r[k][i], sum);
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) part[warp] = sum;
-    __syncthreads();
-    sum = 0.f;
-    for (int i = 0; i < nt / 32; ++i) sum += part[i];
-    const float rstd = rsqrtf(fmaf(sum, p.inv_d, p.eps));
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int c = (k * nt + tid) * kRun;
-        const int n = min(kRun, p.D - c);
-        if (n > 0) {
-            float w[kRun];
-#pragma unroll
-            for (int i = 0; i < kRun; ++i) w[i] = i < n ? p.w[c + i] : 0.f;
-#pragma unroll
-            for (int i = 0; i < kRun; ++i) r[k][i] = i < n ? r[k][i] * rstd * w[i] : 0.f;
-        }
-    }
-    if constexpr (!F8) {
-        TIO* y = static_cast<TIO*>(p.y) + row * p.y_r;
+    };
+    load_row(blockIdx.x);
+    int turn = 0;                                  // rows take the two sets of partial results in turn
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+        float r[K][kRun];
+        float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (k * nt + tid) * kRun;
-            const int n = min(kRun, p.D - c);
-            if (n > 0) store_run<TIO, VEC>(y + c, n, r[k]);
+            float b[kRun];
+            rx[k].get(r[k]);
+            rr[k].get(b);
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) r[k][i] += b[i];
         }
-    } else {
-        uint8_t* y = static_cast<uint8_t*>(p.y) + row * p.y_r;
-        float* scale = p.scale + row * p.nblocks;
-        uint32_t m[K];
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            m[k] = 0u;
-#pragma unroll
-            for (int i = 0; i < kRun; ++i) m[k] = max(m[k], mag_bits(r[k][i]));
-        }
-        if (p.block == 0) {
-            uint32_t a = m[0];
-#pragma unroll
-            for (int k = 1; k < K; ++k) a = max(a, m[k]);
-            a = __reduce_max_sync(0xffffffffu, a);
-            if (lane == 0) pmax[warp] = a;
-            __syncthreads();
-            for (int i = 0; i < nt / 32; ++i) a = max(a, pmax[i]);
-            const float sc = scale_of(a);
-            if (tid == 0) scale[0] = sc;
-#pragma unroll
-            for (int k = 0; k < K; ++k) m[k] = __float_as_uint(sc);
-        } else {
-            const int lanes = p.block / kRun;
+        if (row + gridDim.x < p.rows) load_row(row + gridDim.x);          // on its way while this row is worked on
+        if (p.res_out) {
+            TR* ro = static_cast<TR*>(p.res_out) + row * p.res_out_r;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                for (int o = lanes / 2; o > 0; o /= 2) m[k] = max(m[k], __shfl_xor_sync(0xffffffffu, m[k], o));
-                const float sc = scale_of(m[k]);
                 const int c = (k * nt + tid) * kRun;
-                if (c < p.D && lane % lanes == 0) scale[c / p.block] = sc;
-                m[k] = __float_as_uint(sc);
+                const int n = min(kRun, p.D - c);
+                if (n > 0) store_run<TR, VEC>(ro + c, n, r[k]);
             }
         }
 #pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) sum = fmaf(r[k][i], r[k][i], sum);
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) part[turn][warp] = sum;
+        __syncthreads();
+        sum = lane < nt / 32 ? part[turn][lane] : 0.f;                   // (at most 16 warps)
+#pragma unroll
+        for (int o = 8; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        sum = __shfl_sync(0xffffffffu, sum, 0);
+        const float rstd = rsqrtf(fmaf(sum, p.inv_d, p.eps));
+#pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (k * nt + tid) * kRun;
             const int n = min(kRun, p.D - c);
-            if (n > 0) store_codes<VEC>(y + c, n, r[k], __uint_as_float(m[k]));
+            if (n > 0) {
+                float w[kRun];
+                if constexpr (VEC) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float4 f = __ldg(reinterpret_cast<const float4*>(p.w + c) + i);
+                        w[4 * i] = f.x; w[4 * i + 1] = f.y; w[4 * i + 2] = f.z; w[4 * i + 3] = f.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kRun; ++i) w[i] = i < n ? p.w[c + i] : 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < kRun; ++i) r[k][i] = i < n ? r[k][i] * rstd * w[i] : 0.f;
+            }
+        }
+        if constexpr (!F8) {
+            TIO* y = static_cast<TIO*>(p.y) + row * p.y_r;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int c = (k * nt + tid) * kRun;
+                const int n = min(kRun, p.D - c);
+                if (n > 0) store_run<TIO, VEC>(y + c, n, r[k]);
+            }
+        } else {
+            uint8_t* y = static_cast<uint8_t*>(p.y) + row * p.y_r;
+            float* scale = p.scale + row * p.nblocks;
+            uint32_t m[K];
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                m[k] = 0u;
+#pragma unroll
+                for (int i = 0; i < kRun; ++i) m[k] = max(m[k], mag_bits(r[k][i]));
+            }
+            if (p.block == 0) {
+                uint32_t a = m[0];
+#pragma unroll
+                for (int k = 1; k < K; ++k) a = max(a, m[k]);
+                a = __reduce_max_sync(0xffffffffu, a);
+                if (lane == 0) pmax[turn][warp] = a;
+                __syncthreads();
+                a = __reduce_max_sync(0xffffffffu, lane < nt / 32 ? pmax[turn][lane] : 0u);
+                const float sc = scale_of(a);
+                if (tid == 0) scale[0] = sc;
+#pragma unroll
+                for (int k = 0; k < K; ++k) m[k] = __float_as_uint(sc);
+            } else {
+                const int lanes = p.block / kRun;
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    for (int o = lanes / 2; o > 0; o /= 2) m[k] = max(m[k], __shfl_xor_sync(0xffffffffu, m[k], o));
+                    const float sc = scale_of(m[k]);
+                    const int c = (k * nt + tid) * kRun;
+                    if (c < p.D && lane % lanes == 0) scale[c / p.block] = sc;
+                    m[k] = __float_as_uint(sc);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int c = (k * nt + tid) * kRun;
+                const int n = min(kRun, p.D - c);
+                if (n > 0) store_codes<VEC>(y + c, n, r[k], __uint_as_float(m[k]));
+            }
         }
     }
 }
 
-template <typename TIO, typename TR, bool F8, bool VEC>
-cudaError_t launch_norm(const NormParams& p, int64_t rows, cudaStream_t stream) {
+template <typename TIO, typename TR, bool F8, bool VEC, int K>
+cudaError_t launch_norm_k(const NormParams& p, cudaStream_t stream) {
     const int runs = (p.D + kRun - 1) / kRun;
-    const unsigned grid = static_cast<unsigned>(rows);
-    auto threads = [&](int k) { return static_cast<unsigned>((((runs + k - 1) / k + 31) / 32) * 32); };
-    if (runs <= 512) norm_kernel<TIO, TR, F8, VEC, 1><<<grid, threads(1), 0, stream>>>(p);
-    else if (runs <= 1024) norm_kernel<TIO, TR, F8, VEC, 2><<<grid, threads(2), 0, stream>>>(p);
-    else norm_kernel<TIO, TR, F8, VEC, 4><<<grid, threads(4), 0, stream>>>(p);
+    const int threads = ((runs + K - 1) / K + 31) / 32 * 32;
+    void (*kern)(const NormParams) = norm_kernel<TIO, TR, F8, VEC, K>;
+    int dev = 0, sms = 0, per_sm = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0);
+    if (e != cudaSuccess) return e;
+    // as many CTAs as fit at once, each with its share of the rows
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(p.rows, static_cast<int64_t>(sms) * std::max(per_sm, 1)));
+    kern<<<grid, threads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
+template <typename TIO, typename TR, bool F8, bool VEC>
+cudaError_t launch_norm(const NormParams& p, cudaStream_t stream) {
+    const int runs = (p.D + kRun - 1) / kRun;
+    if (runs <= 512) return launch_norm_k<TIO, TR, F8, VEC, 1>(p, stream);
+    if (runs <= 1024) return launch_norm_k<TIO, TR, F8, VEC, 2>(p, stream);
+    return launch_norm_k<TIO, TR, F8, VEC, 4>(p, stream);
+}
+
 template <typename TIO, typename TR>
-cudaError_t launch_typed(const NormParams& p, bool f8, bool vec, int64_t rows, cudaStream_t s) {
-    if (f8) return vec ? launch_norm<TIO, TR, true, true>(p, rows, s) : launch_norm<TIO, TR, true, false>(p, rows, s);
-    return vec ? launch_norm<TIO, TR, false, true>(p, rows, s) : launch_norm<TIO, TR, false, false>(p, rows, s);
+cudaError_t launch_typed(const NormParams& p, bool f8, bool vec, cudaStream_t s) {
+    if (f8) return vec ? launch_norm<TIO, TR, true, true>(p, s) : launch_norm<TIO, TR, true, false>(p, s);
+    return vec ? launch_norm<TIO, TR, false, true>(p, s) : launch_norm<TIO, TR, false, false>(p, s);
 }
 
 using host::dev_ptr;
@@ -282,19 +338,19 @@ ss_status add_rmsnorm(const void* x, const void* residual, const float* weight, 
     p.x = x; p.res = residual; p.w = weight; p.res_out = residual_out; p.y = y; p.scale = scale;
     p.x_r = s.x_r; p.res_r = s.res_r; p.res_out_r = s.res_out_r; p.y_r = s.y_r;
     p.D = static_cast<int>(D); p.block = f8 ? static_cast<int>(block) : 0; p.nblocks = static_cast<int>(nb);
-    p.eps = eps; p.inv_d = 1.f / static_cast<float>(D);
+    p.rows = rows; p.eps = eps; p.inv_d = 1.f / static_cast<float>(D);
     // 16-byte accesses (8-byte ones for the codes): whole runs, rows and bases on that boundary
     auto wide = [&](const void* q, int64_t stride, int64_t es, int64_t a) {
         return !q || (is_aligned(q, a) && (rows == 1 || (stride * es) % a == 0));
     };
-    const bool vec = D % kRun == 0 && wide(x, s.x_r, xe, 16) && wide(residual, s.res_r, re, 16) &&
+    const bool vec = D % kRun == 0 && is_aligned(weight, 16) && wide(x, s.x_r, xe, 16) && wide(residual, s.res_r, re, 16) &&
                      wide(residual_out, s.res_out_r, re, 16) && wide(y, s.y_r, ye, f8 ? 8 : 16);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool xb = s.io_dtype == SS_BF16, rb = s.res_dtype == SS_BF16;
-    const cudaError_t e = xb ? (rb ? launch_typed<__nv_bfloat16, __nv_bfloat16>(p, f8, vec, rows, st)
-                                   : launch_typed<__nv_bfloat16, float>(p, f8, vec, rows, st))
-                             : (rb ? launch_typed<float, __nv_bfloat16>(p, f8, vec, rows, st)
-                                   : launch_typed<float, float>(p, f8, vec, rows, st));
+    const cudaError_t e = xb ? (rb ? launch_typed<__nv_bfloat16, __nv_bfloat16>(p, f8, vec, st)
+                                   : launch_typed<__nv_bfloat16, float>(p, f8, vec, st))
+                             : (rb ? launch_typed<float, __nv_bfloat16>(p, f8, vec, st)
+                                   : launch_typed<float, float>(p, f8, vec, st));
     return e == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
