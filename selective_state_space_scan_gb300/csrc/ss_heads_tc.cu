@@ -22,8 +22,11 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
+#include <cmath>
 #include <cstddef>
 #include <cstdint>
+#include <cstdlib>
 
 #include "../../include/selscan.h"
 #include "heads_device.cuh"
@@ -782,6 +785,8 @@ int segments_for(int64_t chains, int64_t chunks, int64_t sms) {
     return best;
 }
 
+std::atomic<int> g_force_path{0}, g_force_chunks{0};
+
 // Chunks per segment of the waves: short ones, so that the last wave leaves little idle, unless there
 // are so many chains that whole sequences do as well.
 constexpr int kWaveChunks = 4;
@@ -826,13 +831,19 @@ int heads_sm_count() {
     return n;
 }
 
-// bf16 activations, up to 128 states, and more than 16 tokens a sequence on average: below that the
-// token-by-token kernel is faster (about 1 us a token against 5 us a chunk and a second launch).
+// bf16 activations, up to 128 states, and sequences long enough (on average) that the products' fixed
+// costs pay, by what both paths measure, in us: token by token 7 + 0.28 a token as long as there are no
+// more CTAs than 170, in proportion beyond; here 12 + 10 a chunk up to 110 chains.  (One sequence of 45
+// tokens, 24 heads: 19 against 22; 8 of 32: 23 against 23; 16 of 24, 80 heads: 80 against 71.)
 bool heads_tc_takes(int64_t n_seq, int64_t tokens, int64_t H, int64_t P, int64_t G, int64_t N, bool bf16) {
-    (void)P;
-    if (!bf16 || N > 128 || tokens <= 16 * n_seq || G > 65535) return false;
+    if (!bf16 || N > 128 || G > 65535 || n_seq < 1 || tokens < 1) return false;
     const HeadsTcPlan plan = heads_tc_plan(n_seq, tokens, H, P, G, N);
-    return plan.segments * plan.pairs <= INT32_MAX && plan.chunks <= INT32_MAX;
+    if (plan.segments * plan.pairs > INT32_MAX || plan.chunks > INT32_MAX) return false;
+    if (const int forced = g_force_path.load()) return forced == 2;
+    const double mean = static_cast<double>(tokens) / static_cast<double>(n_seq), chunks = std::ceil(mean / kHeadsChunk);
+    const double seq = 7.0 + 0.28 * mean * std::max(1.0, static_cast<double>(n_seq) * plan.gtiles / 170.0);
+    const double tc = 12.0 + 10.0 * chunks * std::max(1.0, static_cast<double>(n_seq) * plan.pairs / 110.0);
+    return tc < seq;
 }
 
 HeadsTcPlan heads_tc_plan(int64_t n_seq, int64_t tokens, int64_t H, int64_t P, int64_t G, int64_t N) {
@@ -846,9 +857,11 @@ HeadsTcPlan heads_tc_plan(int64_t n_seq, int64_t tokens, int64_t H, int64_t P, i
     const int sms = heads_sm_count();
     const int64_t chains = n_seq * plan.pairs;
     const int k = segments_for(chains, std::max<int64_t>(mean, 1), sms);
-    plan.split = k > 1;
-    const bool whole = !plan.split && chains > kManyChains * sms;
+    const int forced = g_force_chunks.load();
+    plan.split = forced ? forced > 0 : k > 1;
+    const bool whole = !forced && !plan.split && chains > kManyChains * sms;
     plan.seg_chunks = plan.split ? static_cast<int>((mean + k - 1) / k) : whole ? INT32_MAX / 2 : kWaveChunks;
+    if (forced) plan.seg_chunks = std::abs(forced);
     plan.segments = plan.chunks / plan.seg_chunks + n_seq;
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -898,3 +911,8 @@ cudaError_t launch_heads_tc(const HeadsParams& p, void* workspace, bool bf16, cu
 }
 
 }  // namespace selscan
+
+// Test hooks.  The path of ss_heads_fwd: 1 token by token, 2 products (where it can), 0 by size.  Chunks per
+// segment of the products' path: n > 0 a time split, n < 0 waves of -n, 0 by size.  Return the previous value.
+extern "C" int ss__force_heads_path(int path) { return selscan::g_force_path.exchange(path); }
+extern "C" int ss__force_heads_chunks(int chunks) { return selscan::g_force_chunks.exchange(chunks); }

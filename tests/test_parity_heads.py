@@ -8,6 +8,7 @@ import pytest
 
 import selective_state_space_scan_gb300 as ss
 import serving_ref as ref
+from selective_state_space_scan_gb300 import serving
 
 from helpers import BF16_REL_L2, FP32_REL_L2, STATE_REL_L2, rel_l2, to_host
 
@@ -327,3 +328,61 @@ def test_overlaps_are_refused():
         c.fwd(state, window, y=c.z)                                         # y over z
     with pytest.raises(ss.SelscanError):
         c.fwd(state, state.view(-1)[:window.numel()].view_as(window))        # window inside state
+
+
+class Force:
+    """Takes the library's choice of path and of segments out of its hands for a while."""
+
+    def __init__(self, path=0, chunks=0):
+        self.path, self.chunks = path, chunks
+
+    def __enter__(self):
+        lib = ss.lib()
+        for f in (lib.ss__force_heads_path, lib.ss__force_heads_chunks):
+            f.argtypes = [ctypes.c_int]
+        lib.ss__force_heads_path(self.path)
+        lib.ss__force_heads_chunks(self.chunks)
+        serving._HEADS_BYTES.clear()
+
+    def __exit__(self, *a):
+        ss.lib().ss__force_heads_path(0)
+        ss.lib().ss__force_heads_chunks(0)
+        serving._HEADS_BYTES.clear()
+
+
+@pytest.mark.parametrize("L", [1, 2, 3, 4, 17, 31, 32, 33, 64, 96, 97, 127, 128, 129, 130, 131, 255, 257])
+def test_products_at_every_length(L):
+    """Chunks of every fill, from the slot's state and from zeros."""
+    with Force(path=2):
+        run_fwd(Case([L], H=3, seed=L), f"products L={L}")
+        run_fwd(Case([5, L, 0, L + 130, 1], H=2, N=48, P=40, seed=L), f"products packed L={L}")
+
+
+@pytest.mark.parametrize("io", IOS)
+@pytest.mark.parametrize("L", [70, 256, 1000])
+def test_token_by_token_at_long_lengths(io, L):
+    with Force(path=1):
+        run_fwd(Case([L, 3, L // 2], H=3, io=io, seed=L), f"tokens L={L} {io}")
+        run_fwd(Case([L], H=1, P=64, N=200, io=io, seed=L), f"tokens L={L} N=200 {io}")
+
+
+@pytest.mark.parametrize("chunks", [1, 2, 3, 7, -1, -2, -3, -100])
+def test_segments_of_any_length(chunks):
+    """The time split (two passes) and the waves (the state handed from CTA to CTA) at every cut, with
+    sequences that end inside, at and before a segment's end, fresh ones and slotless ones."""
+    lens = [700, 128, 0, 385, 256, 60, 512]
+    c = Case(lens, H=5, seed=40 + abs(chunks))
+    c.fresh = torch.tensor([0, 1, 0, 1, 0, 0, 0], dtype=torch.int32, device="cuda")
+    c.slots[4] = -1
+    with Force(path=2, chunks=chunks):
+        first = run_fwd(c, f"segments of {chunks}")
+        again = run_fwd(c, f"segments of {chunks}")
+    for a, b in zip(first, again):
+        assert torch.equal(a, b)
+
+
+def test_more_segments_than_ctas():
+    """Waves of many more segments than the device has SMs, of sequences of unlike lengths."""
+    lens = [1300, 40, 900, 640, 128, 129, 1, 500]
+    with Force(path=2, chunks=-1):
+        run_fwd(Case(lens, H=96, P=64, N=32, G=1, seed=50), "many segments")
