@@ -4,15 +4,18 @@
 // and C come out of a width-4 causal convolution and a SiLU.
 //
 // heads_seq_kernel walks the tokens in order, the recurrence as it is written, all of it in fp32.  A CTA
-// has 64 rows of one head's state of one sequence.  A thread has 16 states of two rows in registers,
+// has 64 rows of one head's state of one sequence.  A thread has 16 states of two or four rows in registers,
 // LPR lanes share a row; 16 tokens at a time the CTA convolves its x channels and the group's B and C
 // into shared memory (their samples are loaded a round ahead), then every warp takes the tokens one by
-// one.  What bounds it is issue: per token and 64 x 128 states 8 warps of some 70 instructions.
+// one.  For longer sequences heads_bc_kernel convolves B and C once for all heads of a group beforehand,
+// and the rounds come as bulk copies into two buffers.  What bounds it is the FMA pipe: three operations
+// per state and token, 195 cycles of an SM for 64 x 128 states.
 // Long sequences of few heads are cut in segments: a first pass leaves each segment's state from zero
 // and its decay, the second starts every segment from the state that enters it.
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 
@@ -28,7 +31,7 @@ namespace {
 constexpr int kSeqRows = 64;                                // rows of the state per CTA
 constexpr int kSeqT = 16;                                   // tokens per round
 constexpr int kSeqN = 16;                                   // states per thread and row
-constexpr int kSeqU = 4;                                    // tokens whose sums over lanes are taken together
+constexpr int kPreTokens = 96;                              // mean length from which B and C are convolved beforehand
 
 struct SeqParams {
     HeadsParams p;
@@ -36,17 +39,95 @@ struct SeqParams {
     int64_t units;          // upper bound of the segments
     float* seg_state;       // [units, H, P, N]: what a segment leaves from zero
     float* seg_decay;       // [units, H]: its log2 decay
+    float* bc;              // [G, tokens][B | C], each padded with zeros to whole runs of kSeqN states
 };
 
 enum class SeqPass { kWhole, kStates, kSegments };
 
-template <typename TIO, int LPR, SeqPass PASS>
-__global__ void __launch_bounds__(32 * LPR) heads_seq_kernel(const SeqParams q) {
-    constexpr int NT = 32 * LPR, NP = kSeqN * LPR, CH = kSeqRows + 2 * NP, CPT = (CH + NT - 1) / NT;
+constexpr int kBcThreads = 256, kBcToks = 32;               // tokens per block (and thread)
+
+// B and C of all tokens, convolved.  Grid (kBcToks tokens of a sequence, group).
+template <typename TIO>
+__global__ void __launch_bounds__(kBcThreads) heads_bc_kernel(const SeqParams q, int np) {
+    const HeadsParams& p = q.p;
+    __shared__ int scratch[kBcThreads / 32], found[2];
+    const int tid = threadIdx.x, id = blockIdx.x, g = blockIdx.y;
+    if (tid == 0) found[0] = -1;
+    __syncthreads();
+    int base = 0;
+    for (int s0 = 0; s0 < p.n_seq && found[0] < 0; s0 += kBcThreads) {
+        int n = 0;
+        if (s0 + tid < p.n_seq) {
+            const HeadsSeq c = heads_seq(p, s0 + tid);
+            n = c.ok ? max(1, (c.len + kBcToks - 1) / kBcToks) : 0;
+        }
+        int total;
+        const int at = base + block_prefix(n, &total, scratch);
+        if (id >= at && id < at + n) {
+            found[0] = s0 + tid;
+            found[1] = id - at;
+        }
+        base += total;
+        __syncthreads();
+    }
+    if (found[0] < 0) return;
+    const HeadsSeq s = heads_seq(p, found[0]);
+    const int first = found[1] * kBcToks;
+    const TIO* x = static_cast<const TIO*>(p.xbc) + s.row0 * p.xbc_t;
+    for (int k = tid; k < 2 * np && first < s.len; k += kBcThreads) {
+        const int n = k % np;
+        const bool on = n < p.N;
+        const int c = p.H * p.P + (k >= np ? p.G * p.N : 0) + g * p.N + (on ? n : 0);
+        const HeadsWindow win = first == 0 ? heads_window(p, s, c) : HeadsWindow{{0.f, 0.f, 0.f}};
+        const float* w = p.conv_w + static_cast<int64_t>(c) * 4;
+        const float wk[4] = {w[0], w[1], w[2], w[3]}, b = p.conv_b ? p.conv_b[c] : 0.f;
+        float e0 = heads_sample<TIO>(p, s, win, c, first - 3), e1 = heads_sample<TIO>(p, s, win, c, first - 2),
+              e2 = heads_sample<TIO>(p, s, win, c, first - 1);
+        float* out = q.bc + (g * p.tokens + s.row0 + first) * (2 * np) + k;
+        for (int j0 = 0; j0 < kBcToks && first + j0 < s.len; j0 += 8) {
+            TIO raw[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                raw[j] = first + j0 + j < s.len ? x[static_cast<int64_t>(first + j0 + j) * p.xbc_t + c] : from_f32<TIO>(0.f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float e3 = to_f32<TIO>(raw[j]);
+                const float v = heads_conv(wk, b, e0, e1, e2, e3);
+                if (first + j0 + j < s.len) out[static_cast<int64_t>(j0 + j) * (2 * np)] = on ? v : 0.f;
+                e0 = e1;
+                e1 = e2;
+                e2 = e3;
+            }
+        }
+    }
+    if (found[1] == 0 && s.slot >= 0) {                     // this block alone reads these channels' windows
+        __syncthreads();
+        const int cb = p.H * p.P + g * p.N, cc = cb + p.G * p.N;
+        for (int k = tid; k < 2 * p.N; k += kBcThreads) heads_keep_window<TIO>(p, s, k < p.N ? cb + k : cc + k - p.N);
+    }
+}
+
+// Rows per thread.  B and C of a token go to every thread that has a row, 128 bytes a cycle of an SM, which
+// is what bounds two rows a thread (290 cycles for 64 x 128 states); with four, and fewer threads, the FMA
+// pipe does.  Where B and C are convolved here the threads are needed for that.
+constexpr int seq_rows(int lpr, bool pre) { return pre && lpr >= 2 ? 4 : 2; }
+constexpr int seq_threads(int lpr, bool pre) { return kSeqRows / seq_rows(lpr, pre) * lpr; }
+
+// PRE: B and C come convolved from heads_bc_kernel.
+template <typename TIO, int LPR, SeqPass PASS, bool PRE>
+__global__ void __launch_bounds__(seq_threads(LPR, PRE)) heads_seq_kernel(const SeqParams q) {
+    constexpr int NT = seq_threads(LPR, PRE), RPT = seq_rows(LPR, PRE), RT = kSeqRows / RPT, NP = kSeqN * LPR;
+    constexpr int U = 8 / RPT;                              // tokens whose sums over lanes are taken together
+    constexpr int CH = PRE ? kSeqRows : kSeqRows + 2 * NP;  // channels convolved here
+    constexpr int XT = PRE && NT > kSeqRows ? kSeqT * kSeqRows / NT : kSeqT;      // tokens per thread and channel
+    constexpr int CPT = (CH * (kSeqT / XT) + NT - 1) / NT;  // channels per thread
     constexpr int OPT = kSeqT * kSeqRows / NT;              // outputs per thread and round
     constexpr bool kOut = PASS != SeqPass::kStates;
-    __shared__ __align__(16) float sB[kSeqT][NP], sC[kSeqT][NP], sx[kSeqT][kSeqRows], sy[kSeqT][kSeqRows];
+    __shared__ __align__(128) float sbc[PRE ? 2 : 1][kSeqT][2 * NP];
+    __shared__ float sx[kSeqT][kSeqRows], sy[kSeqT][kSeqRows];
     __shared__ float sdt[kSeqT], sa[kSeqT];
+    __shared__ uint64_t full[2];
+    __shared__ int abort_flag;
     __shared__ int scratch[NT / 32], found[2];
     const HeadsParams& p = q.p;
     const int tid = threadIdx.x, tiles = (p.P + kSeqRows - 1) / kSeqRows;
@@ -90,19 +171,45 @@ __global__ void __launch_bounds__(32 * LPR) heads_seq_kernel(const SeqParams q) 
     const bool last = seg == nsegs - 1;
     if (PASS == SeqPass::kStates && nsegs == 1) return;
 
-    const int g = h / (p.H / p.G), lr = tid % LPR, rp = tid / LPR;       // rows rp and rp + 32
+    const int g = h / (p.H / p.G), lr = tid % LPR, rp = tid / LPR;       // rows rp, rp + RT, ..
     const int p0 = pt * kSeqRows, np = min(kSeqRows, p.P - p0);
     const int cx = h * p.P + p0, cb = p.H * p.P + g * p.N, cc = cb + p.G * p.N;
     const float A2 = -expf(p.A_log[h]) * kLog2e, bias = p.dt_bias ? p.dt_bias[h] : 0.f, Dh = p.D ? p.D[h] : 0.f;
 
-    // a channel's convolution: this thread's channels, their weights and their last samples
+    const int rounds = (end - first + kSeqT - 1) / kSeqT;
+    auto load_bc = [&](int r) {                             // (one thread) round r into its buffer
+        const int t0 = first + r * kSeqT;
+        const uint32_t bytes = static_cast<uint32_t>(min(kSeqT, end - t0)) * (2 * NP * 4);
+        mbar_expect_tx(&full[r & 1], bytes);
+        bulk_load(&sbc[PRE ? r & 1 : 0][0][0], q.bc + (g * p.tokens + s.row0 + t0) * (2 * NP), bytes, &full[r & 1]);
+    };
+    if (PRE) {
+        if (tid == 0) {
+            mbar_init(&full[0], 1);
+            mbar_init(&full[1], 1);
+            mbar_fence_init();
+            abort_flag = 0;
+        }
+        // rows that no copy has reached yet meet Δ = 0: they have to be numbers
+        for (int i = tid; i < 2 * kSeqT * 2 * NP; i += NT) (&sbc[0][0][0])[i] = 0.f;
+        tma_store_fence();
+        __syncthreads();
+        if (tid == 0) {
+            if (rounds > 0) load_bc(0);
+            if (rounds > 1) load_bc(1);
+        }
+    }
+
+    // this thread's channels (the tokens of a round shared among the threads of a channel), their weights
+    // and their samples from three before on
     int chan[CPT];
-    float w[CPT][4], cbias[CPT], e0[CPT], e1[CPT], e2[CPT];
-    TIO raw[CPT][kSeqT];
+    float w[CPT][4], cbias[CPT], win[CPT][3];
+    TIO raw[CPT][XT + 3];
+    const int my_t = PRE && NT > kSeqRows ? tid / kSeqRows * XT : 0;
     const TIO* xg = static_cast<const TIO*>(p.xbc) + s.row0 * p.xbc_t;
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
-        const int i = tid + k * NT;
+        const int i = PRE && NT > kSeqRows ? tid % kSeqRows : tid + k * NT;
         const int j = i < kSeqRows ? i : i < kSeqRows + NP ? i - kSeqRows : i - kSeqRows - NP;
         const bool on = i < CH && (i < kSeqRows ? j < np : j < p.N) && (kOut || i < kSeqRows + NP);
         chan[k] = !on ? -1 : i < kSeqRows ? cx + j : i < kSeqRows + NP ? cb + j : cc + j;
@@ -111,40 +218,40 @@ __global__ void __launch_bounds__(32 * LPR) heads_seq_kernel(const SeqParams q) 
 #pragma unroll
         for (int k = 0; k < CPT; ++k)
 #pragma unroll
-            for (int t = 0; t < kSeqT; ++t)
-                raw[k][t] = (chan[k] >= 0 && t0 + t < end) ? xg[static_cast<int64_t>(t0 + t) * p.xbc_t + chan[k]] : from_f32<TIO>(0.f);
+            for (int t = 0; t < XT + 3; ++t) {
+                const int at = t0 + my_t + t - 3;
+                raw[k][t] = (chan[k] >= 0 && at >= 0 && at < end) ? xg[static_cast<int64_t>(at) * p.xbc_t + chan[k]] : from_f32<TIO>(0.f);
+            }
     };
     if (first < end) load_round(first);
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
         const int c = max(chan[k], 0);
-        HeadsWindow win = {{0.f, 0.f, 0.f}};
-        if (chan[k] >= 0 && first == 0) win = heads_window(p, s, c);
+        HeadsWindow v = {{0.f, 0.f, 0.f}};
+        if (chan[k] >= 0 && first == 0) v = heads_window(p, s, c);
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[k][i] = chan[k] >= 0 ? p.conv_w[static_cast<int64_t>(c) * 4 + i] : 0.f;
         cbias[k] = (chan[k] >= 0 && p.conv_b) ? p.conv_b[c] : 0.f;
-        const bool past = chan[k] >= 0 && first > 0 && first < end;
-        e0[k] = past ? to_f32<TIO>(xg[static_cast<int64_t>(first - 3) * p.xbc_t + c]) : win.v[0];
-        e1[k] = past ? to_f32<TIO>(xg[static_cast<int64_t>(first - 2) * p.xbc_t + c]) : win.v[1];
-        e2[k] = past ? to_f32<TIO>(xg[static_cast<int64_t>(first - 1) * p.xbc_t + c]) : win.v[2];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) win[k][i] = v.v[i];
     }
 
     // The state that enters (see ss_heads_tc.cu: the second pass over a cut sequence must not read its
     // slot, which the first pass puts in the place of the last segment).
-    float2 S[2][kSeqN / 2];
+    float2 S[RPT][kSeqN / 2];
     auto at_state = [&](float* base, int64_t k) { return base + ((k * p.H + h) * p.P + p0) * p.N; };
     auto each_state = [&](float* base, auto&& f) {          // f(element, its address) for this thread's
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int r = 0; r < RPT; ++r)
 #pragma unroll
             for (int j = 0; j < kSeqN / 2; ++j) {
-                const int row = rp + 32 * r, n = (j / 2 * LPR + lr) * 4 + (j & 1) * 2;
+                const int row = rp + RT * r, n = (j / 2 * LPR + lr) * 4 + (j & 1) * 2;
                 if (row < np && n < p.N) f(S[r][j].x, base + static_cast<int64_t>(row) * p.N + n);
                 if (row < np && n + 1 < p.N) f(S[r][j].y, base + static_cast<int64_t>(row) * p.N + n + 1);
             }
     };
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < RPT; ++r)
 #pragma unroll
         for (int j = 0; j < kSeqN / 2; ++j) S[r][j] = make_float2(0.f, 0.f);
     float* slot_state = at_state(p.state, max(s.slot, 0));
@@ -170,20 +277,29 @@ __global__ void __launch_bounds__(32 * LPR) heads_seq_kernel(const SeqParams q) 
 
     for (int t0 = first; t0 < end; t0 += kSeqT) {
         const int nt = min(kSeqT, end - t0);
+        const int round = (t0 - first) / kSeqT;
+        float (*bc)[2 * NP] = sbc[PRE ? round & 1 : 0];
 #pragma unroll
         for (int k = 0; k < CPT; ++k) {
-            const int i = tid + k * NT;
-            float* dst = i < kSeqRows ? &sx[0][i] : i < kSeqRows + NP ? &sB[0][i - kSeqRows] : &sC[0][i - kSeqRows - NP];
-            const int pitch = i < kSeqRows ? kSeqRows : NP;
-            if (i < CH)
+            const int i = PRE && NT > kSeqRows ? tid % kSeqRows : tid + k * NT;
+            float* dst = i < kSeqRows ? &sx[0][i] : &bc[0][i - kSeqRows];          // (B, then C)
+            const int pitch = i < kSeqRows ? kSeqRows : 2 * NP;
+            if (i < CH) {
+                float e[3];
 #pragma unroll
-                for (int t = 0; t < kSeqT; ++t) {
-                    const float e3 = to_f32<TIO>(raw[k][t]);
-                    dst[t * pitch] = heads_conv(w[k], cbias[k], e0[k], e1[k], e2[k], e3);
-                    e0[k] = e1[k];
-                    e1[k] = e2[k];
-                    e2[k] = e3;
+                for (int j = 0; j < 3; ++j) {
+                    const int at = t0 + my_t + j - 3;
+                    e[j] = at >= 0 ? to_f32<TIO>(raw[k][j]) : at == -1 ? win[k][2] : at == -2 ? win[k][1] : win[k][0];
                 }
+#pragma unroll
+                for (int t = 0; t < XT; ++t) {
+                    const float e3 = to_f32<TIO>(raw[k][t + 3]);
+                    dst[(my_t + t) * pitch] = heads_conv(w[k], cbias[k], e[0], e[1], e[2], e3);
+                    e[0] = e[1];
+                    e[1] = e[2];
+                    e[2] = e3;
+                }
+            }
         }
         if (tid < kSeqT) {                                  // past the end: Δ = 0, which changes nothing
             const float dt = tid < nt ? softplus(dt_next + bias) : 0.f;
@@ -203,38 +319,53 @@ __global__ void __launch_bounds__(32 * LPR) heads_seq_kernel(const SeqParams q) 
                 gate[k] = (t < nt && c < np) ? static_cast<const TIO*>(p.z)[(s.row0 + t0 + t) * p.z_t + cx + c] : from_f32<TIO>(0.f);
             }
         }
+        if (PRE) mbar_wait_bounded(&full[round & 1], (round >> 1) & 1, &abort_flag, p.err);
         __syncthreads();
 #pragma unroll 1
-        for (int t4 = 0; t4 < nt; t4 += kSeqU) {
-            float v[2 * kSeqU];                             // this thread's part of C·S, row by row
+        for (int t4 = 0; t4 < nt; t4 += U) {
+            float2 a[U], d[RPT][U], y[RPT][U];
 #pragma unroll
-            for (int u = 0; u < kSeqU; ++u) {
+            for (int u = 0; u < U; ++u) {
                 const int t = t4 + u;
-                const float2 a = splat2(sa[t]);
                 const float dt = sdt[t];
-                const float2 d0 = splat2(dt * sx[t][rp]), d1 = splat2(dt * sx[t][rp + 32]);
-                float2 y0 = make_float2(0.f, 0.f), y1 = y0;
+                a[u] = splat2(sa[t]);
 #pragma unroll
-                for (int j = 0; j < kSeqN / 4; ++j) {
-                    const float4 B = *reinterpret_cast<const float4*>(&sB[t][(j * LPR + lr) * 4]);
-                    const float2 b0 = make_float2(B.x, B.y), b1 = make_float2(B.z, B.w);
-                    S[0][2 * j] = fma2(a, S[0][2 * j], mul2(d0, b0));
-                    S[0][2 * j + 1] = fma2(a, S[0][2 * j + 1], mul2(d0, b1));
-                    S[1][2 * j] = fma2(a, S[1][2 * j], mul2(d1, b0));
-                    S[1][2 * j + 1] = fma2(a, S[1][2 * j + 1], mul2(d1, b1));
-                    if (kOut) {
-                        const float4 C = *reinterpret_cast<const float4*>(&sC[t][(j * LPR + lr) * 4]);
-                        const float2 c0 = make_float2(C.x, C.y), c1 = make_float2(C.z, C.w);
-                        y0 = fma2(S[0][2 * j + 1], c1, fma2(S[0][2 * j], c0, y0));
-                        y1 = fma2(S[1][2 * j + 1], c1, fma2(S[1][2 * j], c0, y1));
+                for (int r = 0; r < RPT; ++r) {
+                    d[r][u] = splat2(dt * sx[t][rp + RT * r]);
+                    y[r][u] = make_float2(0.f, 0.f);
+                }
+            }
+            // four states at a time through all of the tokens, so that their loads are together
+#pragma unroll
+            for (int j = 0; j < kSeqN / 4; ++j) {
+                float4 B[U], C[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    B[u] = *reinterpret_cast<const float4*>(&bc[t4 + u][(j * LPR + lr) * 4]);
+                    if (kOut) C[u] = *reinterpret_cast<const float4*>(&bc[t4 + u][NP + (j * LPR + lr) * 4]);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const float2 b0 = make_float2(B[u].x, B[u].y), b1 = make_float2(B[u].z, B[u].w);
+#pragma unroll
+                    for (int r = 0; r < RPT; ++r) {
+                        S[r][2 * j] = fma2(a[u], S[r][2 * j], mul2(d[r][u], b0));
+                        S[r][2 * j + 1] = fma2(a[u], S[r][2 * j + 1], mul2(d[r][u], b1));
+                        if (kOut) {
+                            const float2 c0 = make_float2(C[u].x, C[u].y), c1 = make_float2(C[u].z, C[u].w);
+                            y[r][u] = fma2(S[r][2 * j + 1], c1, fma2(S[r][2 * j], c0, y[r][u]));
+                        }
                     }
                 }
-                v[u] = y0.x + y0.y;
-                v[kSeqU + u] = y1.x + y1.y;
             }
             if (kOut) {
                 // sums over the lanes of a row: at each exchange a lane keeps half of the values
-                int n = 2 * kSeqU, at = 0;
+                float v[RPT * U];
+#pragma unroll
+                for (int r = 0; r < RPT; ++r)
+#pragma unroll
+                    for (int u = 0; u < U; ++u) v[r * U + u] = y[r][u].x + y[r][u].y;
+                int n = RPT * U, at = 0;
 #pragma unroll
                 for (int o = LPR / 2; o > 0; o /= 2) {
                     if (n > 1) {
@@ -251,10 +382,11 @@ __global__ void __launch_bounds__(32 * LPR) heads_seq_kernel(const SeqParams q) 
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < n; ++i) sy[t4 + (at + i) % kSeqU][rp + 32 * ((at + i) / kSeqU)] = v[i];
+                for (int i = 0; i < n; ++i) sy[t4 + (at + i) % U][rp + RT * ((at + i) / U)] = v[i];
             }
         }
         __syncthreads();
+        if (PRE && tid == 0 && round + 2 < rounds && !abort_flag) load_bc(round + 2);
         if (kOut) {
 #pragma unroll
             for (int k = 0; k < OPT; ++k) {
@@ -266,6 +398,12 @@ __global__ void __launch_bounds__(32 * LPR) heads_seq_kernel(const SeqParams q) 
                 }
             }
             __syncthreads();
+        }
+    }
+    if (PRE && abort_flag && tid == 0) {                    // copies in flight land before the block ends
+        const long long c0 = clock64();
+        while (!(mbar_try_wait(&full[0], ((rounds - 1) >> 1) & 1) && mbar_try_wait(&full[1], ((rounds - 1) >> 1) & 1)) &&
+               clock64() - c0 < (1ll << 26)) {
         }
     }
     if (PASS == SeqPass::kStates) {
@@ -282,6 +420,7 @@ __global__ void __launch_bounds__(32 * LPR) heads_seq_kernel(const SeqParams q) 
     // B and C the group's, whose last reader shifts them
     __syncthreads();
     for (int k = tid; k < np; k += NT) heads_keep_window<TIO>(p, s, cx + k);
+    if (PRE) return;
     __shared__ int last_reader;
     if (tid == 0) {
         unsigned int* counter = p.arrivals + static_cast<int64_t>(seq) * p.G + g;
@@ -295,52 +434,84 @@ __global__ void __launch_bounds__(32 * LPR) heads_seq_kernel(const SeqParams q) 
 
 // Tokens per segment (0: whole sequences), for sequences of equal length: a segmented call does about 1.7
 // times the work and has one more launch (10 us, about 60 tokens' time), and pays where the CTAs of
-// whole sequences leave the SMs fewer than 16 warps.
+// whole sequences leave the SMs fewer than 16 warps; past a
+// dozen segments what a segment gathers of those before it costs more than that brings.
 struct SeqPlan {
-    int seg;
-    int64_t units;
-    size_t state_bytes, bytes;
+    int seg, np;            // np: states padded
+    bool pre;               // B and C convolved beforehand
+    int64_t units, chunks;  // upper bounds
+    size_t off_state, off_decay, off_bc, bytes;
 };
-SeqPlan seq_plan(int64_t n_seq, int64_t tokens, int64_t H, int64_t P, int64_t N) {
-    SeqPlan plan{0, n_seq, 0, 0};
-    const int64_t ctas = n_seq * H * ((P + kSeqRows - 1) / kSeqRows), lpr = N <= 16 ? 1 : N <= 32 ? 2 : N <= 64 ? 4 : N <= 128 ? 8 : 16;
-    const int64_t room = heads_sm_count() * (16 / lpr);      // CTAs of lpr warps
+std::atomic<int> g_force_pre{0};
+
+SeqPlan seq_plan(int64_t n_seq, int64_t tokens, int64_t H, int64_t P, int64_t G, int64_t N) {
+    SeqPlan plan{};
+    const int64_t ctas = n_seq * H * ((P + kSeqRows - 1) / kSeqRows);
+    const int64_t lpr = N <= 16 ? 1 : N <= 32 ? 2 : N <= 64 ? 4 : N <= 128 ? 8 : 16;
     const int64_t mean = tokens / std::max<int64_t>(n_seq, 1);
-    const int64_t k = std::min<int64_t>(room / std::max<int64_t>(ctas, 1), mean / 64);
-    if (k < 3) return plan;
-    plan.seg = static_cast<int>((mean / k + kSeqT - 1) / kSeqT * kSeqT);
-    plan.units = tokens / plan.seg + n_seq;
-    plan.state_bytes = (static_cast<size_t>(plan.units) * H * P * N * 4 + 255) / 256 * 256;
-    plan.bytes = plan.state_bytes + (static_cast<size_t>(plan.units) * H * 4 + 255) / 256 * 256;
+    const int forced = g_force_pre.load();
+    plan.pre = N <= 128 && G <= 65535 && (forced ? forced == 2 : mean >= kPreTokens);
+    const int64_t room = heads_sm_count() * 16 / std::max(seq_threads(static_cast<int>(lpr), plan.pre) / 32, 1);
+    const int64_t k = std::min({room / std::max<int64_t>(ctas, 1), mean / 64, static_cast<int64_t>(12)});
+    plan.units = n_seq;
+    plan.np = static_cast<int>(kSeqN * lpr);
+    plan.chunks = tokens / kBcToks + n_seq;
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t here = at;
+        at += (n + 255) / 256 * 256;
+        return here;
+    };
+    if (k >= 3) {
+        plan.seg = static_cast<int>((mean / k + kSeqT - 1) / kSeqT * kSeqT);
+        plan.units = tokens / plan.seg + n_seq;
+        plan.off_state = take(static_cast<size_t>(plan.units) * H * P * N * 4);
+        plan.off_decay = take(static_cast<size_t>(plan.units) * H * 4);
+    }
+    if (plan.pre) plan.off_bc = take(static_cast<size_t>(tokens) * G * 2 * plan.np * 4);
+    plan.bytes = at;
     return plan;
 }
 
-template <typename TIO, int LPR>
-cudaError_t launch_seq_lanes(const SeqParams& q, cudaStream_t stream) {
-    const int64_t per_unit = static_cast<int64_t>(q.p.H) * ((q.p.P + kSeqRows - 1) / kSeqRows);
-    const unsigned grid = static_cast<unsigned>(q.units * per_unit);
+template <typename TIO, int LPR, bool PRE>
+cudaError_t launch_seq_pre(const SeqParams& q, unsigned grid, cudaStream_t stream) {
     if (q.seg == 0) {
-        heads_seq_kernel<TIO, LPR, SeqPass::kWhole><<<grid, 32 * LPR, 0, stream>>>(q);
+        heads_seq_kernel<TIO, LPR, SeqPass::kWhole, PRE><<<grid, seq_threads(LPR, PRE), 0, stream>>>(q);
         return cudaGetLastError();
     }
-    heads_seq_kernel<TIO, LPR, SeqPass::kStates><<<grid, 32 * LPR, 0, stream>>>(q);
+    heads_seq_kernel<TIO, LPR, SeqPass::kStates, PRE><<<grid, seq_threads(LPR, PRE), 0, stream>>>(q);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    heads_seq_kernel<TIO, LPR, SeqPass::kSegments><<<grid, 32 * LPR, 0, stream>>>(q);
+    heads_seq_kernel<TIO, LPR, SeqPass::kSegments, PRE><<<grid, seq_threads(LPR, PRE), 0, stream>>>(q);
     return cudaGetLastError();
+}
+
+template <typename TIO, int LPR>
+cudaError_t launch_seq_lanes(const SeqParams& q, const SeqPlan& plan, cudaStream_t stream) {
+    const int64_t per_unit = static_cast<int64_t>(q.p.H) * ((q.p.P + kSeqRows - 1) / kSeqRows);
+    const unsigned grid = static_cast<unsigned>(q.units * per_unit);
+    if constexpr (LPR <= 8) {                               // (two buffers of more states do not fit)
+        if (plan.pre) {
+            const dim3 bc(static_cast<unsigned>(plan.chunks), static_cast<unsigned>(q.p.G));
+            heads_bc_kernel<TIO><<<bc, kBcThreads, 0, stream>>>(q, plan.np);
+            const cudaError_t e = cudaGetLastError();
+            return e != cudaSuccess ? e : launch_seq_pre<TIO, LPR, true>(q, grid, stream);
+        }
+    }
+    return launch_seq_pre<TIO, LPR, false>(q, grid, stream);
 }
 
 template <typename TIO>
 cudaError_t launch_seq(const HeadsParams& p, uint8_t* workspace, cudaStream_t stream) {
-    const SeqPlan plan = seq_plan(p.n_seq, p.tokens, p.H, p.P, p.N);
-    const SeqParams q{p, plan.seg, plan.units, reinterpret_cast<float*>(workspace),
-                      reinterpret_cast<float*>(workspace + plan.state_bytes)};
+    const SeqPlan plan = seq_plan(p.n_seq, p.tokens, p.H, p.P, p.G, p.N);
+    const SeqParams q{p, plan.seg, plan.units, reinterpret_cast<float*>(workspace + plan.off_state),
+                      reinterpret_cast<float*>(workspace + plan.off_decay), reinterpret_cast<float*>(workspace + plan.off_bc)};
     if (plan.units * p.H * ((p.P + kSeqRows - 1) / kSeqRows) > INT32_MAX) return cudaErrorInvalidConfiguration;
-    if (p.N <= 16) return launch_seq_lanes<TIO, 1>(q, stream);
-    if (p.N <= 32) return launch_seq_lanes<TIO, 2>(q, stream);
-    if (p.N <= 64) return launch_seq_lanes<TIO, 4>(q, stream);
-    if (p.N <= 128) return launch_seq_lanes<TIO, 8>(q, stream);
-    return launch_seq_lanes<TIO, 16>(q, stream);
+    if (p.N <= 16) return launch_seq_lanes<TIO, 1>(q, plan, stream);
+    if (p.N <= 32) return launch_seq_lanes<TIO, 2>(q, plan, stream);
+    if (p.N <= 64) return launch_seq_lanes<TIO, 4>(q, plan, stream);
+    if (p.N <= 128) return launch_seq_lanes<TIO, 8>(q, plan, stream);
+    return launch_seq_lanes<TIO, 16>(q, plan, stream);
 }
 
 }  // namespace
@@ -440,7 +611,7 @@ extern "C" size_t ss_heads_workspace_size(int64_t n_seq, int64_t tokens, int64_t
         return 0;
     return heads_tc_takes(n_seq, tokens, H, P, G, N, io_dtype == SS_BF16)
                ? kHeadsCounterBytes + heads_tc_plan(n_seq, tokens, H, P, G, N).bytes
-               : heads_counter_bytes(n_seq, G) + seq_plan(n_seq, tokens, H, P, N).bytes;
+               : heads_counter_bytes(n_seq, G) + seq_plan(n_seq, tokens, H, P, G, N).bytes;
 }
 
 extern "C" ss_status ss_heads_fwd(const void* xbc, const void* dt_raw, const void* z, const float* conv_w,
@@ -469,3 +640,7 @@ extern "C" ss_status ss_heads_fwd(const void* xbc, const void* dt_raw, const voi
     }
     return e == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
+
+// Test hook: whether the token-by-token path convolves B and C beforehand (1 no, 2 yes, 0 by length).  Returns
+// the previous value.
+extern "C" int ss__force_heads_pre(int pre) { return selscan::g_force_pre.exchange(pre); }

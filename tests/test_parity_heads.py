@@ -333,20 +333,22 @@ def test_overlaps_are_refused():
 class Force:
     """Takes the library's choice of path and of segments out of its hands for a while."""
 
-    def __init__(self, path=0, chunks=0):
-        self.path, self.chunks = path, chunks
+    def __init__(self, path=0, chunks=0, pre=0):
+        self.path, self.chunks, self.pre = path, chunks, pre
 
     def __enter__(self):
         lib = ss.lib()
-        for f in (lib.ss__force_heads_path, lib.ss__force_heads_chunks):
+        for f in (lib.ss__force_heads_path, lib.ss__force_heads_chunks, lib.ss__force_heads_pre):
             f.argtypes = [ctypes.c_int]
         lib.ss__force_heads_path(self.path)
         lib.ss__force_heads_chunks(self.chunks)
+        lib.ss__force_heads_pre(self.pre)
         serving._HEADS_BYTES.clear()
 
     def __exit__(self, *a):
         ss.lib().ss__force_heads_path(0)
         ss.lib().ss__force_heads_chunks(0)
+        ss.lib().ss__force_heads_pre(0)
         serving._HEADS_BYTES.clear()
 
 
@@ -364,6 +366,15 @@ def test_token_by_token_at_long_lengths(io, L):
     with Force(path=1):
         run_fwd(Case([L, 3, L // 2], H=3, io=io, seed=L), f"tokens L={L} {io}")
         run_fwd(Case([L], H=1, P=64, N=200, io=io, seed=L), f"tokens L={L} N=200 {io}")
+
+
+@pytest.mark.parametrize("pre", [1, 2])
+@pytest.mark.parametrize("io", IOS)
+@pytest.mark.parametrize("H,P,G,N", [(2, 64, 1, 128), (3, 20, 3, 7), (4, 72, 2, 64), (2, 100, 1, 32), (1, 64, 1, 16)])
+def test_token_by_token_with_b_and_c_beforehand(io, pre, H, P, G, N):
+    with Force(path=1, pre=pre):
+        run_fwd(Case([1, 0, 15, 16, 17, 200, 33, 130, 2], H=H, P=P, G=G, N=N, io=io, seed=H + N), f"{(H, P, G, N)} {io} {pre}")
+        run_fwd(Case([900], H=H, P=P, G=G, N=N, io=io, seed=N), f"long {(H, P, G, N)} {io} {pre}")
 
 
 @pytest.mark.parametrize("chunks", [1, 2, 3, 7, -1, -2, -3, -100])
