@@ -492,10 +492,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                     wb[i] = make_float2(b[2 * i], b[2 * i + 1]);
                 }
             };
-            float decay_sum = 0.f;
+            float decay_sum = 0.f, last_all = 0.f;
+            // S <- decay · S + what a chunk added, from its place in tensor memory
+            auto update = [&](float all, uint32_t col) {
+                const float2 d = splat2(ex2(all));
+                uint32_t v[32];
+                tc_ld32(lanes + col + wg * 64 + hf * 32, v);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    const float2 n = fma2(d, make_float2(S[i], S[i + 1]), make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+                    S[i] = n.x;
+                    S[i + 1] = n.y;
+                }
+            };
 
             for (int ch = c.ch0; ch < ch1; ++ch, ++it) {
                 const uint32_t ph = it & 1;
+                // The first pass has two sets of scaled tiles, accumulators and barriers, and takes a chunk's
+                // products in while it convolves the next.  (A tile is at most one chunk ahead of the other: it
+                // reaches a set again only behind the products of the set's last chunk.)
+                const uint32_t set = kOut ? 0u : ph, set_ph = kOut ? ph : (it >> 1) & 1;
+                uint8_t *th = set ? sX : sXh, *tl = set ? sS : sXl;
+                uint64_t *st = set ? &sh.cs : &sh.st, *x_ready = set ? &sh.y_free : &sh.x_ready;
                 const int tok0 = ch * kQ, nt = min(kQ, s.len - tok0);
                 if (kOut && issue) {                                    // scores, and C·S of both tiles
                     mbar_wait_bounded(&sh.bc, ph, abort, p.err);
@@ -559,6 +577,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                     e2 = make_float4(v[2][0], v[2][1], v[2][2], v[2][3]);
                 }
                 tile_sync();
+                if (!kOut && issue && ch > c.ch0) {                     // B of this chunk, once the last one's products are complete
+                    mbar_wait_bounded(set ? &sh.st : &sh.cs, ((it - 1) >> 1) & 1, abort, p.err);
+                    if (!*abort) load_bc(ch);
+                }
+                __syncwarp();
                 // (rows past the sequence's end hold silu(conv_b): their Δ is zero, so nothing reads them)
                 uint2 xlo[kToks];                                       // what bf16 leaves of x, for D·x
 #pragma unroll
@@ -581,25 +604,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                     }
                     const float2 t0 = mul2(u0, m), t1 = mul2(u1, m);
                     const uint2 x = make_uint2(pack_bf16(t0.x, t0.y), pack_bf16(t1.x, t1.y));
-                    *reinterpret_cast<uint2*>(sXh + off) = x;
-                    *reinterpret_cast<uint2*>(sXl + off) = make_uint2(pack_rest(t0, x.x), pack_rest(t1, x.y));
+                    *reinterpret_cast<uint2*>(th + off) = x;
+                    *reinterpret_cast<uint2*>(tl + off) = make_uint2(pack_rest(t0, x.x), pack_rest(t1, x.y));
                 }
                 tma_store_fence();
-                warp_arrive(&sh.x_ready);
+                warp_arrive(x_ready);
                 if (issue) {                                            // what the chunk adds to the state, both tiles side by side
                     if (!kOut) mbar_wait_bounded(&sh.bc, ph, abort, p.err);
-                    mbar_wait_bounded(&sh.x_ready, ph, abort, p.err);
+                    mbar_wait_bounded(x_ready, set_ph, abort, p.err);
                     tc_fence_after();
+                    const uint32_t xh_at = x_at + (set ? 0 : kBlock), xl_at = x_at + (set ? 3 : 2) * kBlock;
+                    const uint32_t to = tmem + (set ? kColY : kColS);
                     for (int k = 0; k < 8; ++k) {
                         const uint64_t bh = tc_desc(b_at + k * 2048, kBlock, 1024), bl = tc_desc(b_at + kImage + k * 2048, kBlock, 1024);
-                        const uint64_t xh = tc_desc(x_at + kBlock + k * 2048, kTileBytes, 1024),
-                                       xl = tc_desc(x_at + 2 * kBlock + k * 2048, kTileBytes, 1024);
+                        const uint64_t xh = tc_desc(xh_at + k * 2048, kTileBytes, 1024), xl = tc_desc(xl_at + k * 2048, kTileBytes, 1024);
                         constexpr uint32_t id = tc_idesc(128, 128, true, true);
-                        tc_mma(tmem + kColS, bh, xl, id, k > 0);
-                        tc_mma(tmem + kColS, bl, xh, id, true);
-                        tc_mma(tmem + kColS, bh, xh, id, true);
+                        tc_mma(to, bh, xl, id, k > 0);
+                        tc_mma(to, bl, xh, id, true);
+                        tc_mma(to, bh, xh, id, true);
                     }
-                    tc_commit(&sh.st);
+                    tc_commit(st);
                 }
                 __syncwarp();
                 if (kOut) {
@@ -669,19 +693,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                     __syncwarp();
                 }
                 // the state
-                wait(&sh.st, ph);
-                if (issue && ch + 1 < ch1 && !*abort) load_bc(ch + 1);   // the products that read B and C are complete
-                __syncwarp();
-                {
-                    const float2 d = splat2(ex2(all));
-                    uint32_t v[32];
-                    tc_ld32(lanes + kColS + wg * 64 + hf * 32, v);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float2 n = fma2(d, make_float2(S[i], S[i + 1]), make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
-                        S[i] = n.x;
-                        S[i + 1] = n.y;
+                if (kOut) {
+                    wait(st, set_ph);
+                    if (issue && ch + 1 < ch1 && !*abort) load_bc(ch + 1);   // the products that read B and C are complete
+                    __syncwarp();
+                    update(all, kColS);
+                } else {
+                    if (ch > c.ch0) {
+                        wait(set ? &sh.st : &sh.cs, ((it - 1) >> 1) & 1);
+                        update(last_all, set ? kColS : kColY);
                     }
+                    last_all = all;
                 }
                 if (ch + 1 < ch1) dt_next = load_dt(ch + 1);
                 if (kOut) {
@@ -731,6 +753,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                 }
             }
             if (PASS == Pass::kStates) {
+                if (c.ch0 < ch1) {
+                    const uint32_t set = (it - 1) & 1;
+                    wait(set ? &sh.cs : &sh.st, ((it - 1) >> 1) & 1);
+                    update(last_all, set ? kColY : kColS);
+                }
                 if (on) {
                     save(saved(q.seg_state, segment(seg)));
                     if (t == 0 && hf == 0) q.seg_decay[segment(seg)] = decay_sum;
