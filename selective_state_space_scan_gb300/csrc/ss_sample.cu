@@ -262,6 +262,7 @@ __device__ __forceinline__ uint64_t ld_peer_u64(uint32_t addr) {
     return v;
 }
 
+// The largest of the block's numbers, for all its threads.
 __device__ __forceinline__ uint64_t block_max(Shared& s, uint64_t v) {
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) {
@@ -275,18 +276,6 @@ __device__ __forceinline__ uint64_t block_max(Shared& s, uint64_t v) {
     for (int w = 0; w < kWarps; ++w) v = s.warp64[w] > v ? s.warp64[w] : v;
     return v;
 }
-__device__ __forceinline__ uint64_t block_sum(Shared& s, uint64_t v) {
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) s.warp64[threadIdx.x / 32] = v;
-    __syncthreads();
-    v = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += s.warp64[w];
-    return v;
-}
-
 // The cluster that has a row.  Every thread of every CTA makes the same calls in the same order.
 struct Team {
     Shared& s;
@@ -321,35 +310,78 @@ __device__ __forceinline__ void add_to_bin(Shared& s, int bin, uint32_t mass, bo
     if (mass >> 16) atomicAdd(&s.hi[bin], mass >> 16);
 }
 
-// A bin's count and mass over the cluster's histograms.
-__device__ __forceinline__ void whole_bin(const Team& team, int b, uint32_t& c, uint64_t& m) {
+// A thread's share of the bins over the cluster's histograms: kBins / size of them belong to each CTA, in
+// order of the ranks, and EACH = 8 / size adjacent ones to a thread.  All loads are issued before the first
+// sum: each is a trip to another SM.
+constexpr int kBinsThread = kBins / kThreads;
+struct Bins {
+    uint32_t c[kBinsThread];
+    uint64_t m[kBinsThread];
+    int n, first;                                              // how many, and the first's number
+};
+template <int EACH>
+__device__ __forceinline__ void load_share(const Team& team, Bins& h) {
+    constexpr int SIZE = kBinsThread / EACH;
     Shared& s = team.s;
-    c = 0;
-    m = 0;
-    for (uint32_t r = 0; r < team.size; ++r) {
-        const uint32_t pc = team.size > 1 ? peer_smem_addr(&s.count[b], r) : smem_addr(&s.count[b]);
-        c += ld_peer_u32(pc);
-        m += (static_cast<uint64_t>(ld_peer_u32(pc + sizeof(s.count) + sizeof(s.lo))) << 16) + ld_peer_u32(pc + sizeof(s.count));
+    h.n = EACH;
+    h.first = (static_cast<int>(team.rank) * kThreads + static_cast<int>(threadIdx.x)) * EACH;
+    uint32_t v[SIZE][EACH][3];
+#pragma unroll
+    for (int r = 0; r < SIZE; ++r) {
+        const uint32_t pc = SIZE > 1 ? peer_smem_addr(&s.count[h.first], r) : smem_addr(&s.count[h.first]);
+#pragma unroll
+        for (int j = 0; j < EACH; ++j)
+#pragma unroll
+            for (int k = 0; k < 3; ++k) v[r][j][k] = ld_peer_u32(pc + 4 * j + k * static_cast<uint32_t>(sizeof(s.count)));
+    }
+#pragma unroll
+    for (int j = 0; j < kBinsThread; ++j) {
+        h.c[j] = 0u;
+        h.m[j] = 0ull;
+        if (j < EACH)
+#pragma unroll
+            for (int r = 0; r < SIZE; ++r) {
+                h.c[j] += v[r][j < EACH ? j : 0][0];
+                h.m[j] += (static_cast<uint64_t>(v[r][j < EACH ? j : 0][2]) << 16) + v[r][j < EACH ? j : 0][1];
+            }
     }
 }
+__device__ __forceinline__ void load_bins(const Team& team, Bins& h) {
+    if (team.size == 1) load_share<8>(team, h);
+    else if (team.size == 2) load_share<4>(team, h);
+    else if (team.size == 4) load_share<2>(team, h);
+    else load_share<1>(team, h);
+}
 
-// Sums over the bins: this CTA's share of them (kBins / size, in order of the ranks), and exchanged.
-// Histograms are complete when every CTA has called.  Returns the mass of all bins.
-__device__ uint64_t sum_bins(Team& team) {
+// Sums of the CTAs' shares, exchanged.  Histograms are complete when every CTA has called.  Returns the mass
+// of all bins; `h` is this thread's share.
+__device__ uint64_t sum_bins(Team& team, Bins& h) {
     Shared& s = team.s;
     team.sync();
-    const int share = kBins / static_cast<int>(team.size), each = share / kThreads;
+    load_bins(team, h);
     uint32_t c = 0;
     uint64_t m = 0;
-    for (int j = 0; j < each; ++j) {
-        uint32_t cj;
-        uint64_t mj;
-        whole_bin(team, static_cast<int>(team.rank) * share + static_cast<int>(threadIdx.x) * each + j, cj, mj);
-        c += cj;
-        m += mj;
+#pragma unroll
+    for (int j = 0; j < kBinsThread; ++j) {
+        c += h.c[j];
+        m += h.m[j];
     }
-    c = static_cast<uint32_t>(block_sum(s, c));
-    m = block_sum(s, m);
+    c = __reduce_add_sync(0xffffffffu, c);
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) m += __shfl_xor_sync(0xffffffffu, m, o);
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) {
+        s.warp32[threadIdx.x / 32] = c;
+        s.warp64[threadIdx.x / 32] = m;
+    }
+    __syncthreads();
+    c = 0;
+    m = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        c += s.warp32[w];
+        m += s.warp64[w];
+    }
     if (threadIdx.x == 0) {
         s.share_count = c;
         s.share_mass = m;
@@ -364,7 +396,7 @@ __device__ uint64_t sum_bins(Team& team) {
 // After sum_bins: the first bin at which the running count, begun at `count`, reaches `k` (by_mass false),
 // or the running mass, begun at `mass`, reaches `target` (by_mass true); the last bin if none does.  Leaves
 // it in s.bin, with what is before it, in every CTA.  Histograms may be cleared after it.
-__device__ void find_bin(Team& team, bool by_mass, uint32_t k, uint64_t target, uint32_t count, uint64_t mass) {
+__device__ void find_bin(Team& team, const Bins& h, bool by_mass, uint32_t k, uint64_t target, uint32_t count, uint64_t mass) {
     Shared& s = team.s;
     // the CTA whose share it is in
     uint32_t owner = 0;
@@ -376,17 +408,13 @@ __device__ void find_bin(Team& team, bool by_mass, uint32_t k, uint64_t target, 
         mass += m;
     }
     if (owner == team.rank) {
-        const int share = kBins / static_cast<int>(team.size), each = share / kThreads;
-        const int b0 = static_cast<int>(team.rank) * share + static_cast<int>(threadIdx.x) * each, lane = threadIdx.x % 32,
-                  warp = threadIdx.x / 32;
+        const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
         uint32_t ci = 0;
         uint64_t mi = 0;
-        for (int j = 0; j < each; ++j) {
-            uint32_t cj;
-            uint64_t mj;
-            whole_bin(team, b0 + j, cj, mj);
-            ci += cj;
-            mi += mj;
+#pragma unroll
+        for (int j = 0; j < kBinsThread; ++j) {
+            ci += h.c[j];
+            mi += h.m[j];
         }
         const uint32_t ct = ci;
         const uint64_t mt = mi;
@@ -413,18 +441,16 @@ __device__ void find_bin(Team& team, bool by_mass, uint32_t k, uint64_t target, 
         uint32_t cb = count + ci - ct, c_at = 0;                 // before this thread's bins
         uint64_t mb = mass + mi - mt, m_at = 0;
         int mine = kBins;
-        for (int j = 0; j < each; ++j) {
-            uint32_t cj;
-            uint64_t mj;
-            whole_bin(team, b0 + j, cj, mj);
-            const bool end = threadIdx.x == kThreads - 1 && j == each - 1;
-            if (mine == kBins && (end || (by_mass ? mb + mj >= target : cb + cj >= k))) {
-                mine = b0 + j;
+#pragma unroll
+        for (int j = 0; j < kBinsThread; ++j) {
+            const bool end = threadIdx.x == kThreads - 1 && j == h.n - 1;
+            if (mine == kBins && j < h.n && (end || (by_mass ? mb + h.m[j] >= target : cb + h.c[j] >= k))) {
+                mine = h.first + j;
                 c_at = cb;
                 m_at = mb;
             }
-            cb += cj;
-            mb += mj;
+            cb += h.c[j];
+            mb += h.m[j];
         }
         if (mine < kBins) atomicMin(&s.bin, mine);
         __syncthreads();
@@ -695,8 +721,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
                     if (o >> bits) return;
                     add_to_bin(s, kBins - 1 - static_cast<int>(o >> shift), mass_of(l), true);
                 });
-                sum_bins(team);
-                find_bin(team, by_mass, kk, target, count, mass);
+                Bins h;
+                sum_bins(team, h);
+                find_bin(team, h, by_mass, kk, target, count, mass);
                 count = s.count_above;
                 mass = s.mass_above;
                 lo += static_cast<uint64_t>(kBins - 1 - s.bin) << shift;
@@ -735,14 +762,15 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
         uint64_t target = all;                                   // never below 1: the first token stays
         team.sync();
         histogram(k < V);
-        const uint64_t whole = sum_bins(team);
+        Bins h;
+        const uint64_t whole = sum_bins(team, h);
         if (k < V) {
-            find_bin(team, false, k, 0.0, 0u, 0ull);
+            find_bin(team, h, false, k, 0ull, 0u, 0ull);
             bin = s.bin;
             count = s.count_above;
             mass = s.mass_above;
             uint64_t kept = mass;
-            n = collect(bin, false, k, 0.0, count, mass);
+            n = collect(bin, false, k, 0ull, count, mass);
             cut = smallest_kept(n, k, all, count, mass, &kept);
             if (tp < 2.f) target = share_of(kept);
         } else {
@@ -752,9 +780,11 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
             const int kbin = bin;
             if (narrowed) {                                    // the bins hold something else by now
                 histogram(k < V);
-                sum_bins(team);
+                sum_bins(team, h);
+            } else if (k < V) {
+                load_bins(team, h);
             }
-            find_bin(team, true, 0u, target, 0u, 0ull);
+            find_bin(team, h, true, 0u, target, 0u, 0ull);
             const int b = s.bin;
             if (b < kbin) {
                 bin = b;
@@ -763,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
                 n = collect(b, true, 0u, target, count, mass);
                 cut = smallest_kept(n, V, target, count, mass, nullptr);
             } else if (narrowed) {                             // the same bin, but elsewhere in it
-                find_bin(team, false, k, 0.0, 0u, 0ull);
+                find_bin(team, h, false, k, 0ull, 0u, 0ull);
                 count = s.count_above;
                 mass = s.mass_above;
                 n = collect(kbin, true, 0u, target, count, mass);
