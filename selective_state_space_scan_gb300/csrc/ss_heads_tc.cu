@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
         TcTables& tab = sh.tab[wg];
         auto tile_sync = [&]() { named_barrier(1 + wg, 256); };
         auto wait = [&](uint64_t* bar, uint32_t parity) {              // for a product's completion
-            mbar_wait_bounded(bar, parity, abort, p.err);
+            mbar_sleep_bounded(bar, parity, abort, p.err);
             __syncwarp();
             tc_fence_after();
         };
@@ -516,13 +516,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                 uint64_t *st = set ? &sh.cs : &sh.st, *x_ready = set ? &sh.y_free : &sh.x_ready;
                 const int tok0 = ch * kQ, nt = min(kQ, s.len - tok0);
                 if (kOut && issue) {                                    // scores, and C·S of both tiles
-                    mbar_wait_bounded(&sh.bc, ph, abort, p.err);
+                    mbar_sleep_bounded(&sh.bc, ph, abort, p.err);
                     for (int k = 0; k < 4 * q.nb; ++k) {
                         const uint32_t at = (k / 4) * kBlock + (k % 4) * 32;
                         tc_mma(tmem + kColScore, tc_desc(c_at + at, 16, 1024), tc_desc(b_at + at, 16, 1024),
                                tc_idesc(128, 128, false, false), k > 0);
                     }
-                    mbar_wait_bounded(&sh.y_free, ph, abort, p.err);
+                    mbar_sleep_bounded(&sh.y_free, ph, abort, p.err);
                     tc_fence_after();
                     for (int k = 0; k < 4 * q.nb; ++k)
                         tc_mma(tmem + kColY, tc_desc(c_at + (k / 4) * kBlock + (k % 4) * 32, 16, 1024),
@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                 }
                 tile_sync();
                 if (!kOut && issue && ch > c.ch0) {                     // B of this chunk, once the last one's products are complete
-                    mbar_wait_bounded(set ? &sh.st : &sh.cs, ((it - 1) >> 1) & 1, abort, p.err);
+                    mbar_sleep_bounded(set ? &sh.st : &sh.cs, ((it - 1) >> 1) & 1, abort, p.err);
                     if (!*abort) load_bc(ch);
                 }
                 __syncwarp();
@@ -610,8 +610,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                 tma_store_fence();
                 warp_arrive(x_ready);
                 if (issue) {                                            // what the chunk adds to the state, both tiles side by side
-                    if (!kOut) mbar_wait_bounded(&sh.bc, ph, abort, p.err);
-                    mbar_wait_bounded(x_ready, set_ph, abort, p.err);
+                    if (!kOut) mbar_sleep_bounded(&sh.bc, ph, abort, p.err);
+                    mbar_sleep_bounded(x_ready, set_ph, abort, p.err);
                     tc_fence_after();
                     const uint32_t xh_at = x_at + (set ? 0 : kBlock), xl_at = x_at + (set ? 3 : 2) * kBlock;
                     const uint32_t to = tmem + (set ? kColY : kColS);
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                     tc_fence_before();
                     warp_arrive(&sh.p_ready[wg]);
                     if (issue_pv) {
-                        mbar_wait_bounded(&sh.p_ready[wg], ph, abort, p.err);
+                        mbar_sleep_bounded(&sh.p_ready[wg], ph, abort, p.err);
                         tc_fence_after();
                         for (int k = 0; k < 8; ++k)
                             tc_mma_ta(tmem + kColY + wg * 64, tmem + kColP + wg * 64 + k * 8,

@@ -31,6 +31,26 @@ constexpr uint32_t tc_idesc(int m, int n, bool a_mn, bool b_mn) {
            static_cast<uint32_t>(n >> 3) << 17 | static_cast<uint32_t>(m >> 4) << 24;
 }
 
+// Waits for the barrier phase with the given parity with the warp put to sleep in between (up to 0.2 ms at a
+// time): warps that spin take issue slots from the others, a fifth of all instructions of the scan before
+// this.  Gives up after about a second: see mbar_wait_bounded.
+__device__ __forceinline__ bool mbar_sleep_bounded(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned int* err_word) {
+    for (int i = 0; i < 5000; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(smem_addr(bar)), "r"(parity), "r"(200000u)
+            : "memory");
+        if (ok) return true;
+        if (*abort_flag) return false;
+    }
+    *abort_flag = 1;
+    if (err_word) atomicOr(err_word, kErrWaitTimeout);
+    return false;
+}
+
 // D (+)= A·B over 16 of K; one thread issues it.
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
     asm volatile(
