@@ -56,34 +56,96 @@ __device__ __forceinline__ int chunks_of(const HeadsParams& p, int seq) {
 
 // ---- B and C
 
-// Four channels as loaded: bf16 pairs, or floats.  `n` of them exist; VEC: all or none, one aligned access.
-template <typename TIO, bool VEC> struct Quad4;
-template <bool VEC> struct Quad4<__nv_bfloat16, VEC> {
+// Four channels of a row as loaded, `n` of them existing, and where they begin in their first word.
+// VEC: all or none, in one aligned access of 8 bytes.  Otherwise rows begin anywhere: the aligned words
+// that hold the channels are loaded (a third one only where the row begins inside a word) and shifted into
+// place at use.  A word that holds a channel that exists is readable as a whole; what else it holds belongs
+// to channels past the last, whose columns reach no result.
+template <bool VEC> struct Quad4;
+template <> struct Quad4<true> {
     uint2 u;
-    __device__ __forceinline__ void load(const __nv_bfloat16* q, int n) {
+    static __device__ __forceinline__ uint32_t shift(const __nv_bfloat16*) { return 0u; }
+    __device__ __forceinline__ void load(const __nv_bfloat16* q, int n, uint32_t) {
         u = make_uint2(0u, 0u);
-        if constexpr (VEC) {
-            if (n > 0) u = *reinterpret_cast<const uint2*>(q);
-        } else {
-            const uint16_t* h = reinterpret_cast<const uint16_t*>(q);
-            if (n > 0) u.x = h[0];
-            if (n > 1) u.x |= static_cast<uint32_t>(h[1]) << 16;
-            if (n > 2) u.y = h[2];
-            if (n > 3) u.y |= static_cast<uint32_t>(h[3]) << 16;
+        if (n > 0) u = *reinterpret_cast<const uint2*>(q);
+    }
+    __device__ __forceinline__ uint2 bits(uint32_t) const { return u; }
+};
+template <> struct Quad4<false> {
+    uint32_t w[3];
+    static __device__ __forceinline__ uint32_t shift(const __nv_bfloat16* q) {
+        return (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(q)) & 2u) * 8u;
+    }
+    __device__ __forceinline__ void load(const __nv_bfloat16* q, int n, uint32_t sh) {
+        const uint32_t* f = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(q) & ~static_cast<uintptr_t>(3));
+        w[0] = w[1] = w[2] = 0u;
+        if (n > 0) {
+            const int words = (n + (sh ? 1 : 0) + 1) / 2;
+            w[0] = f[0];
+            if (words > 1) w[1] = f[1];
+            if (words > 2) w[2] = f[2];
         }
     }
-    __device__ __forceinline__ float4 get() const { return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y)); }
-    static __device__ __forceinline__ void store(__nv_bfloat16* q, int n, float4 v) {
-        if constexpr (VEC) {
-            if (n > 0) *reinterpret_cast<uint2*>(q) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-        } else {
-            if (n > 0) q[0] = from_f32<__nv_bfloat16>(v.x);
-            if (n > 1) q[1] = from_f32<__nv_bfloat16>(v.y);
-            if (n > 2) q[2] = from_f32<__nv_bfloat16>(v.z);
-            if (n > 3) q[3] = from_f32<__nv_bfloat16>(v.w);
-        }
+    __device__ __forceinline__ uint2 bits(uint32_t sh) const {
+        return make_uint2(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh));
     }
 };
+__device__ __forceinline__ float4 quad_floats(uint2 u) { return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y)); }
+
+// The same in the scan, where 16 lanes of a warp hold a row of a tile's 64 channels and a thread holds many
+// rows: without VEC a lane loads the two words at its channels and takes the third from the lane after it;
+// the last lane's third words of all rows (up to 16) are spread over the lanes of the row (load_tail).
+// Four sequences of 8192 tokens, 128 states, a chunk of a pair of tiles per SM: 11.0 us with VEC (76 heads),
+// 14.7 at rows of 4-byte boundaries (38 heads), 15.2 at any (77 heads); 16.7 and 18.3 with three words a row and
+// thread (276 bytes of spills), 22.6 with one access per channel.
+template <bool VEC> struct Row4 : Quad4<true> {
+    __device__ __forceinline__ uint2 bits(uint32_t, uint32_t, int, int) const { return u; }
+};
+template <> struct Row4<false> {
+    uint32_t w0, w1;
+    __device__ __forceinline__ void load(const __nv_bfloat16* q, int n, uint32_t sh) {
+        const uint32_t* f = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(q) & ~static_cast<uintptr_t>(3));
+        const int m = n + (sh ? 1 : 0);            // channels from the first word's beginning (n < 0: no such row)
+        w0 = m > 0 ? f[0] : 0u;
+        w1 = m > 2 ? f[1] : 0u;
+    }
+    // all lanes at once; qd: the lane's place in its row, j: the row's number
+    __device__ __forceinline__ uint2 bits(uint32_t sh, uint32_t tails, int qd, int j) const {
+        const uint32_t next = __shfl_down_sync(0xffffffffu, w0, 1, 16), tail = __shfl_sync(0xffffffffu, tails, j, 16);
+        return make_uint2(__funnelshift_r(w0, w1, sh), __funnelshift_r(w1, qd == 15 ? tail : next, sh));
+    }
+};
+// The word that begins with channel 63 of row j, for lane j; q: channel 0 of row 0.  (Where rows begin at words it
+// is not used.)
+template <bool VEC>
+__device__ __forceinline__ uint32_t load_tail(const __nv_bfloat16* q, int64_t stride, bool on, int j) {
+    if (VEC || !on) return 0u;
+    const __nv_bfloat16* f = q + j * stride + 63;
+    return Quad4<false>::shift(f) == 0 ? *reinterpret_cast<const uint32_t*>(f) : 0u;
+}
+
+// Stores the first n of four channels; wide: y's rows are on boundaries of 8 bytes.
+template <bool VEC>
+__device__ __forceinline__ void quad_store(__nv_bfloat16* q, int n, bool wide, float2 a, float2 b) {
+    const uint2 u = make_uint2(pack_bf16(a.x, a.y), pack_bf16(b.x, b.y));
+    if (VEC || (wide && (n & 3) == 0)) {
+        if (n > 0) *reinterpret_cast<uint2*>(q) = u;
+        return;
+    }
+    uint16_t* h = reinterpret_cast<uint16_t*>(q);
+    if (n >= 4 && Quad4<false>::shift(q) == 0) {
+        reinterpret_cast<uint32_t*>(q)[0] = u.x;
+        reinterpret_cast<uint32_t*>(q)[1] = u.y;
+    } else if (n >= 4) {
+        h[0] = static_cast<uint16_t>(u.x);
+        *reinterpret_cast<uint32_t*>(h + 1) = __funnelshift_r(u.x, u.y, 16);
+        h[3] = static_cast<uint16_t>(u.y >> 16);
+    } else {
+        if (n > 0) h[0] = static_cast<uint16_t>(u.x);
+        if (n > 1) h[1] = static_cast<uint16_t>(u.x >> 16);
+        if (n > 2) h[2] = static_cast<uint16_t>(u.y);
+    }
+}
 
 // Grid (chunk, group, B or C).  Block (0, 0, 0) also writes the tables of where chunks and segments
 // begin, and reports indexes out of range.
@@ -152,12 +214,13 @@ __global__ void __launch_bounds__(kPrepThreads) heads_prep_kernel(const HeadsTcP
     uint8_t* lo = img + q.nb * kBlock + (qd / 16) * kBlock;            // B only
     const TIO* x = static_cast<const TIO*>(p.xbc) + s.row0 * p.xbc_t + c0 + ch;
     constexpr int kRows = 8;                                           // a round: its loads are issued together
-    Quad4<TIO, VEC> raw[kRows];
+    Quad4<VEC> raw[kRows];
+    const uint32_t sh0 = Quad4<VEC>::shift(x), sh1 = Quad4<VEC>::shift(x + p.xbc_t);    // of even rows, and of odd ones
     auto load_round = [&](int r) {
 #pragma unroll
         for (int j = 0; j < kRows; ++j) {
             const int t = t0 + r0 + r + j;
-            raw[j].load(x + t * p.xbc_t, t < s.len ? n : 0);
+            raw[j].load(x + t * p.xbc_t, t < s.len ? n : 0, t & 1 ? sh1 : sh0);
         }
     };
     load_round(0);
@@ -172,9 +235,10 @@ __global__ void __launch_bounds__(kPrepThreads) heads_prep_kernel(const HeadsTcP
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
         const int t = t0 + r0 + j - 3;
-        Quad4<TIO, VEC> f;
-        f.load(x + static_cast<int64_t>(max(t, 0)) * p.xbc_t, (t >= 0 && t < s.len) ? n : 0);
-        e[j] = f.get();
+        Quad4<VEC> f;
+        const uint32_t sh = t & 1 ? sh1 : sh0;
+        f.load(x + static_cast<int64_t>(max(t, 0)) * p.xbc_t, (t >= 0 && t < s.len) ? n : 0, sh);
+        e[j] = quad_floats(f.bits(sh));
         if (t < 0) {
             float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -188,7 +252,7 @@ __global__ void __launch_bounds__(kPrepThreads) heads_prep_kernel(const HeadsTcP
 #pragma unroll
         for (int j = 0; j < kRows; ++j) {
             const bool on = t0 + r0 + r + j < s.len;
-            const float4 f = raw[j].get();
+            const float4 f = quad_floats(raw[j].bits(j & 1 ? sh1 : sh0));      // (a round begins at an even row)
             float u[4];
             u[0] = heads_conv(w[0], b[0], e[0].x, e[1].x, e[2].x, f.x);
             u[1] = heads_conv(w[1], b[1], e[0].y, e[1].y, e[2].y, f.y);
@@ -366,7 +430,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
             const bool on = tl < per_group;
             const int h = g * (p.H / p.G) + (on ? tl / tiles : 0), p0 = on ? (tl % tiles) * kTile : 0;
             const int np = on ? min(kTile, p.P - p0) : 0, cx = h * p.P + p0, gtile = h * tiles + p0 / kTile;
-            const int nq = min(4, np - 4 * qd);
+            const int nq = np > 0 ? min(4, np - 4 * qd) : -1;
 
             const uint8_t* src =
                 q.images + (static_cast<int64_t>(q.chunk_base[c.seq]) * p.G + g) * (3 * q.nb * static_cast<int64_t>(kBlock));
@@ -379,13 +443,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                 if (kOut) bulk_load(img + 2 * kImage, f + 2 * part, part, &sh.bc);
             };
             const TIO* xg = static_cast<const TIO*>(p.xbc) + s.row0 * p.xbc_t + cx + 4 * qd;
-            Quad4<TIO, VEC> raw[kToks + 3];                            // samples row0 - 3 .. of a chunk
+            Row4<VEC> raw[kToks + 3];                                  // samples row0 - 3 .. of a chunk
+            // where they begin in a word: row0 - 3 and every second row, and the others
+            const uint32_t sh0 = Quad4<VEC>::shift(xg - p.xbc_t), sh1 = Quad4<VEC>::shift(xg);
+            uint32_t raw_tail = 0u;
             auto load_x = [&](int ch) {
                 const int tk = ch * kQ + row0 - 3;
                 const TIO* f = xg + static_cast<int64_t>(tk) * p.xbc_t;
+                raw_tail = load_tail<VEC>(f - 4 * qd, p.xbc_t, np >= kTile && qd < kToks + 3 && tk + qd >= 0 && tk + qd < s.len, qd);
 #pragma unroll
                 for (int j = 0; j < kToks + 3; ++j) {
-                    raw[j].load(f, (tk + j >= 0 && tk + j < s.len) ? nq : 0);
+                    raw[j].load(f, (tk + j >= 0 && tk + j < s.len) ? nq : -1, j & 1 ? sh1 : sh0);
                     f += p.xbc_t;
                 }
             };
@@ -476,7 +544,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                 const float* w = p.conv_w + static_cast<int64_t>(cx + 4 * qd) * 4;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    if constexpr (VEC)
+                    if (VEC || q.wide_w)
                         f[i] = i < nq ? *reinterpret_cast<const float4*>(w + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
                     else
                         f[i] = i < nq ? make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3])
@@ -561,7 +629,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                 if (hf == 0) tab.tail[t] = dt * ex2(after);
                 decay_sum += all;
                 // x, through the convolution
-                float4 e0 = raw[0].get(), e1 = raw[1].get(), e2 = raw[2].get();
+                float4 e0 = quad_floats(raw[0].bits(sh0, raw_tail, qd, 0)), e1 = quad_floats(raw[1].bits(sh1, raw_tail, qd, 1)),
+                       e2 = quad_floats(raw[2].bits(sh0, raw_tail, qd, 2));
                 if (ch == 0 && row0 == 0 && s.warm) {
                     float v[3][4];
 #pragma unroll
@@ -588,7 +657,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                 for (int j = 0; j < kToks; ++j) {
                     const int row = row0 + j;
                     const float2 m = splat2(tab.tail[row]);
-                    const float4 f = raw[j + 3].get();
+                    const float4 f = quad_floats(raw[j + 3].bits(j & 1 ? sh0 : sh1, raw_tail, qd, j + 3));
                     const float2 u0 = heads_conv2(wk[0], wb[0], make_float2(e0.x, e0.y), make_float2(e1.x, e1.y),
                                                   make_float2(e2.x, e2.y), make_float2(f.x, f.y));
                     const float2 u1 = heads_conv2(wk[1], wb[1], make_float2(e0.z, e0.w), make_float2(e1.z, e1.w),
@@ -708,12 +777,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                 if (ch + 1 < ch1) dt_next = load_dt(ch + 1);
                 if (kOut) {
                     if (ch + 1 < ch1) state_tile();
-                    Quad4<TIO, VEC> gate[kToks];
+                    Row4<VEC> gate[kToks];
+                    uint32_t zsh0 = 0u, zsh1 = 0u, gate_tail = 0u;
                     if (p.z) {
                         const TIO* z = static_cast<const TIO*>(p.z) + (s.row0 + tok0 + row0) * p.z_t + cx + 4 * qd;
+                        zsh0 = Quad4<VEC>::shift(z);
+                        zsh1 = Quad4<VEC>::shift(z + p.z_t);
+                        gate_tail = load_tail<VEC>(z - 4 * qd, p.z_t, np >= kTile && qd < kToks && row0 + qd < nt, qd);
 #pragma unroll
                         for (int j = 0; j < kToks; ++j) {
-                            gate[j].load(z, row0 + j < nt ? nq : 0);
+                            gate[j].load(z, row0 + j < nt ? nq : -1, j & 1 ? zsh1 : zsh0);
                             z += p.z_t;
                         }
                     }
@@ -743,11 +816,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                         float2 y0 = fma2(Dd, add2(unpack2(x.x), unpack2(xlo[j].x)), make_float2(v.x, v.y));
                         float2 y1 = fma2(Dd, add2(unpack2(x.y), unpack2(xlo[j].y)), make_float2(v.z, v.w));
                         if (p.z) {
-                            const float4 z = gate[j].get();
+                            const float4 z = quad_floats(gate[j].bits(j & 1 ? zsh1 : zsh0, gate_tail, qd, j));
                             y0 = mul2(y0, silu2(make_float2(z.x, z.y)));
                             y1 = mul2(y1, silu2(make_float2(z.z, z.w)));
                         }
-                        Quad4<TIO, VEC>::store(y, row < nt ? nq : 0, make_float4(y0.x, y0.y, y1.x, y1.y));
+                        quad_store<VEC>(y, row < nt ? nq : 0, q.wide_y, y0, y1);
                         y += p.y_t;
                     }
                 }
@@ -932,8 +1005,9 @@ cudaError_t launch_heads_tc(const HeadsParams& p, void* workspace, bool bf16, cu
     q.nb = plan.nb;
     // four channels in one access: z, x, B, C and y of every head and group on that boundary
     auto wide = [&](const void* base, int64_t stride) { return host::is_aligned(base, 8) && stride % 4 == 0; };
-    const bool vec = p.P % 4 == 0 && p.N % 4 == 0 && host::is_aligned(p.conv_w, 16) && wide(p.xbc, p.xbc_t) &&
-                     wide(p.z, p.z_t) && wide(p.y, p.y_t);
+    q.wide_w = host::is_aligned(p.conv_w, 16);
+    q.wide_y = wide(p.y, p.y_t);
+    const bool vec = p.P % 4 == 0 && p.N % 4 == 0 && q.wide_w && wide(p.xbc, p.xbc_t) && wide(p.z, p.z_t) && q.wide_y;
     return vec ? launch_typed<__nv_bfloat16, true>(q, plan, stream) : launch_typed<__nv_bfloat16, false>(q, plan, stream);
 }
 
