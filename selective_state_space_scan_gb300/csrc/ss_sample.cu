@@ -18,8 +18,8 @@
 //   - The last pass runs the race over what stays and reads the noise of those tokens alone.
 //
 // 192 rows of 128000 bf16 logits (147 MB with the noise, 22 us at the copy rate), GPU time: greedy 13.5 us; top_k
-// 50 34 us; no filter 50 us (the race: an exp2 and a reciprocal a token); top_p 0.9 146 us, which the atomic adds of
-// the histogram bound; every row with settings of its own 74 us.  One row of 50257: 4.1, 9.4, 7.8 and 23 us, the
+// 50 34 us; no filter 50 us (the race: an exp2 and a reciprocal a token); top_p 0.9 146 us (a pass
+// with two atomic adds a token, and one that collects); every row with settings of its own 74 us.  One row of 50257: 4.1, 9.4, 7.8 and 23 us, the
 // chain of syncs over the cluster.
 #include <cuda_runtime.h>
 
