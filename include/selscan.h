@@ -543,7 +543,7 @@ typedef struct {
  *                       concurrently on the device.
  * Sums and the state are fp32.  So are all factors, but for longer bf16 sequences, which take the
  * tensor cores: there B and Δ·x go into the state as sums of two bf16 (a state is off by some
- * 1e-6 of what was added to it), and C, S, x and the decays into y as one (2e-3 of y, as its own
+ * 4e-6 of its norm), and C, S, x and the decays into y as one (2e-3 of y, as its own
  * rounding is).  An infinite or NaN input reaches what the formulas take it to and nothing else
  * (there every output that should be infinite may be NaN).  Errors as ss_fwd.
  */

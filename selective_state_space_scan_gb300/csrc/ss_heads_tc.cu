@@ -14,8 +14,8 @@
 //   P·x on top of exp2(l)·(C·S), P read from tensor memory
 // The state itself stays in registers, fp32: what the chunk adds comes out of tensor memory.
 //
-// Rounding: the state's operands carry 16 bits each, so a state is off by about 1e-6 of what was added
-// to it.  y is rounded to bf16 in the end; the factors C, S, P and x of its sums are rounded to bf16
+// Rounding: the state's operands carry 16 bits each and the product of their low parts is left out, so a state
+// is off by about 4e-6 of its norm (in fp32: 1e-6).  y is rounded to bf16 in the end; the factors C, S, P and x of its sums are rounded to bf16
 // before the products, each error as large as that last one, and D·x is not.
 // A decay is only ever the exp2 of a sum of steps between its two tokens, never a quotient, and such
 // sums are taken over the steps themselves, so strong decays neither overflow nor cancel.  P is zero above
@@ -24,9 +24,9 @@
 //
 // What bounds it is the chain within a chunk (loads, convolution, products, P, products, outputs), with one
 // CTA of 16 warps on an SM: two tiles' operands and accumulators fill its shared and tensor memory.  Four
-// sequences of 8192 tokens, 80 heads of 64 x 128 states, bf16, gated: 713 us, 10.9 us a chunk and SM, at 43% of
+// sequences of 8192 tokens, 80 heads of 64 x 128 states, bf16, gated: 735 us, 11.2 us a chunk and SM, at 43% of
 // the issue slots, 15% of the tensor pipe and 15% of the memory's peak (156 us are the copy rate's).  One
-// document of 32768 tokens, 24 heads: 380 us in two passes (48 at the copy rate).  Token by token (see
+// document of 32768 tokens, 24 heads: 385 us in two passes (48 at the copy rate).  Token by token (see
 // ss_heads_fwd.cu) the FMA pipe alone would take 1.7 and 0.5 ms.
 // Measured and not taken: one tile per product (N = 64), which shared memory's bandwidth bounds (940 us), a warp
 // for issuing alone (96 registers a thread, spills), x or z a chunk ahead in registers (841), waves of 2 or 8
