@@ -27,7 +27,7 @@ struct HeadsTcParams {
     int pairs;                          // pairs of tiles, over all groups
     int gtiles;                         // tiles, over all heads
     int nb;                             // blocks of 64 states
-    bool wide_w, wide_y;                // conv_w on a boundary of 16 bytes; y's rows on boundaries of 8
+    bool wide_w, wide_y;                // conv_w on a boundary of 16 bytes; the quads of y on boundaries of 8
 };
 
 struct HeadsTcPlan {

@@ -136,7 +136,7 @@ __device__ __forceinline__ uint32_t load_tail(const __nv_bfloat16* q, int64_t st
     return Quad4<false>::shift(f) == 0 ? *reinterpret_cast<const uint32_t*>(f) : 0u;
 }
 
-// Stores the first n of four channels; wide: y's rows are on boundaries of 8 bytes.
+// Stores the first n of four channels; wide: every head's quads of y are on boundaries of 8 bytes.
 template <bool VEC>
 __device__ __forceinline__ void quad_store(__nv_bfloat16* q, int n, bool wide, float2 a, float2 b) {
     const uint2 u = make_uint2(pack_bf16(a.x, a.y), pack_bf16(b.x, b.y));
@@ -986,9 +986,11 @@ int heads_sm_count() {
 // bf16 activations, up to 128 states, and sequences long enough (on average) that the products' fixed
 // costs pay, by what both paths measure, in us: token by token 7 + 0.28 a token as long as there are no
 // more CTAs than 170, in proportion beyond; here 12 + 10 a chunk up to 110 chains.  (One sequence of 45
-// tokens, 24 heads: 19 against 22; 8 of 32: 23 against 23; 16 of 24, 80 heads: 80 against 71.)
+// tokens, 24 heads: 19 against 22; 8 of 32: 23 against 23; 16 of 24, 80 heads: 80 against 71.)  Not for heads of
+// fewer than 256 states: the operands' error is one of the terms, and in so few sums one may cancel (1.1e-5 of a
+// state of 1 x 1, 4e-6 of one of 64 x 128; fp32 has neither), while a tile has 64 x 128 whatever the head has.
 bool heads_tc_takes(int64_t n_seq, int64_t tokens, int64_t H, int64_t P, int64_t G, int64_t N, bool bf16) {
-    if (!bf16 || N > 128 || G > 65535 || n_seq < 1 || tokens < 1) return false;
+    if (!bf16 || N > 128 || P * N < 256 || G > 65535 || n_seq < 1 || tokens < 1) return false;
     const HeadsTcPlan plan = heads_tc_plan(n_seq, tokens, H, P, G, N);
     if (plan.segments * plan.pairs > INT32_MAX || plan.chunks > INT32_MAX) return false;
     if (const int forced = g_force_path.load()) return forced == 2;
@@ -1058,8 +1060,8 @@ cudaError_t launch_heads_tc(const HeadsParams& p, void* workspace, bool bf16, cu
     // four channels in one access: z, x, B, C and y of every head and group on that boundary
     auto wide = [&](const void* base, int64_t stride) { return host::is_aligned(base, 8) && stride % 4 == 0; };
     q.wide_w = host::is_aligned(p.conv_w, 16);
-    q.wide_y = wide(p.y, p.y_t);
-    const bool vec = p.P % 4 == 0 && p.N % 4 == 0 && q.wide_w && wide(p.xbc, p.xbc_t) && wide(p.z, p.z_t) && q.wide_y;
+    q.wide_y = p.P % 4 == 0 && wide(p.y, p.y_t);
+    const bool vec = p.N % 4 == 0 && q.wide_w && wide(p.xbc, p.xbc_t) && wide(p.z, p.z_t) && q.wide_y;
     return vec ? launch_typed<__nv_bfloat16, true>(q, plan, stream) : launch_typed<__nv_bfloat16, false>(q, plan, stream);
 }
 

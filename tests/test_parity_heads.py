@@ -423,3 +423,20 @@ def test_what_is_not_finite_stays_in_its_place(io, path, what, value, at):
         np.testing.assert_array_equal(np.isfinite(got), on)
         assert rel_l2(got[on], want[on]) <= tol
     np.testing.assert_array_equal(to_host(window), rw.astype(np.float32).astype(np.float64))
+
+
+@pytest.mark.parametrize("pad", [0, 1, 2])
+@pytest.mark.parametrize("H,P,G,N", [(3, 20, 1, 7), (1, 1, 1, 1), (5, 37, 5, 33), (4, 63, 2, 128), (2, 127, 1, 61), (3, 66, 1, 16)])
+def test_products_at_any_alignment(H, P, G, N, pad):
+    """Rows of the products' path that begin anywhere, tiles that end anywhere; what lies between the rows
+    is NaN."""
+    c = Case([150, 37, 0, 129], H=H, P=P, G=G, N=N, pad=pad, seed=70 + pad)
+    wide = torch.full((316, c.C + 2 + pad), float("nan"), dtype=c.dt, device="cuda")
+    gate = torch.full((316, H * P + 1 + 2 * pad), float("nan"), dtype=c.dt, device="cuda")
+    wide[:, 1:1 + c.C], gate[:, :H * P] = c.xbc, c.z
+    out = torch.full((316, H * P + 2 + pad), float("nan"), dtype=c.dt, device="cuda")
+    with Force(path=2):
+        run_fwd(c, f"{(H, P, G, N)} pad {pad}")
+        c.xbc, c.z = wide[:, 1:1 + c.C], gate[:, :H * P]
+        run_fwd(c, f"{(H, P, G, N)} pad {pad}, apart", y=out[:, 1:1 + H * P])
+    assert torch.isnan(out[:, 0]).all() and torch.isnan(out[:, 1 + H * P:]).all()
