@@ -4,7 +4,7 @@
 // and C come out of a width-4 causal convolution and a SiLU.
 //
 // heads_seq_kernel walks the tokens in order, the recurrence as it is written, all of it in fp32.  A CTA
-// has 64 rows of one head's state of one sequence.  A thread has 16 states of two or four rows in registers,
+// has 64 rows of one head's state of one sequence.  A thread has 8 or 16 states of two or four rows in registers,
 // LPR lanes share a row; 16 tokens at a time the CTA convolves its x channels and the group's B and C
 // into shared memory (their samples are loaded a round ahead), then every warp takes the tokens one by
 // one.  For longer sequences heads_bc_kernel convolves B and C once for all heads of a group beforehand,
@@ -34,7 +34,6 @@ namespace {
 
 constexpr int kSeqRows = 64;                                // rows of the state per CTA
 constexpr int kSeqT = 16;                                   // tokens per round
-constexpr int kSeqN = 16;                                   // states per thread and row
 constexpr int kPreTokens = 96;                              // mean length from which B and C are convolved beforehand
 
 struct SeqParams {
@@ -43,7 +42,7 @@ struct SeqParams {
     int64_t units;          // upper bound of the segments
     float* seg_state;       // [units, H, P, N]: what a segment leaves from zero
     float* seg_decay;       // [units, H]: its log2 decay
-    float* bc;              // [G, tokens][B | C], each padded with zeros to whole runs of kSeqN states
+    float* bc;              // [G, tokens][B | C], each padded with zeros to all lanes' states
 };
 
 enum class SeqPass { kWhole, kStates, kSegments };
@@ -114,13 +113,23 @@ __global__ void __launch_bounds__(kBcThreads) heads_bc_kernel(const SeqParams q,
 // Rows per thread.  B and C of a token go to every thread that has a row, 128 bytes a cycle of an SM, which
 // is what bounds two rows a thread (290 cycles for 64 x 128 states); with four, and fewer threads, the FMA
 // pipe does.  Where B and C are convolved here the threads are needed for that.
-constexpr int seq_rows(int lpr, bool pre) { return pre && lpr >= 2 ? 4 : 2; }
-constexpr int seq_threads(int lpr, bool pre) { return kSeqRows / seq_rows(lpr, pre) * lpr; }
+constexpr int seq_rows(int lpr, int ns, bool pre) { return pre && lpr * ns >= 32 ? 4 : 2; }
+constexpr int seq_threads(int lpr, int ns, bool pre) { return kSeqRows / seq_rows(lpr, ns, pre) * lpr; }
+
+// Lanes that share a row and states of a lane, for N up to 16, 32, 64, 128 and 256.  16 states to a lane make the
+// fewest loads of B and C, but up to 32 states they leave a CTA one warp, which also has to convolve and write:
+// 16 prompts of 512 tokens, 40 heads of 64 rows, fp32: 16 states 247 us with 1 x 16, 158 with 2 x 8, 157 with
+// 4 x 4 (4 prompts of 2048: 284, 194, 243); 32 states 324 with 2 x 16, 216 with 4 x 8; 64 states 301 with 4 x 16, 302
+// with 8 x 8, 366 with 16 x 4; 128 states 456 with 8 x 16, 531 with 16 x 8.
+struct SeqLanes {
+    int lpr, ns;
+};
+constexpr SeqLanes kSeqLanes[] = {{2, 8}, {4, 8}, {4, 16}, {8, 16}, {16, 16}};
 
 // PRE: B and C come convolved from heads_bc_kernel.
-template <typename TIO, int LPR, SeqPass PASS, bool PRE>
-__global__ void __launch_bounds__(seq_threads(LPR, PRE)) heads_seq_kernel(const SeqParams q) {
-    constexpr int NT = seq_threads(LPR, PRE), RPT = seq_rows(LPR, PRE), RT = kSeqRows / RPT, NP = kSeqN * LPR;
+template <typename TIO, int LPR, int NS, SeqPass PASS, bool PRE>
+__global__ void __launch_bounds__(seq_threads(LPR, NS, PRE)) heads_seq_kernel(const SeqParams q) {
+    constexpr int NT = seq_threads(LPR, NS, PRE), RPT = seq_rows(LPR, NS, PRE), RT = kSeqRows / RPT, NP = NS * LPR;
     constexpr int U = 8 / RPT;                              // tokens whose sums over lanes are taken together
     constexpr int CH = PRE ? kSeqRows : kSeqRows + 2 * NP;  // channels convolved here
     constexpr int XT = PRE && NT > kSeqRows ? kSeqT * kSeqRows / NT : kSeqT;      // tokens per thread and channel
@@ -242,13 +251,13 @@ __global__ void __launch_bounds__(seq_threads(LPR, PRE)) heads_seq_kernel(const 
 
     // The state that enters (see ss_heads_tc.cu: the second pass over a cut sequence must not read its
     // slot, which the first pass puts in the place of the last segment).
-    float2 S[RPT][kSeqN / 2];
+    float2 S[RPT][NS / 2];
     auto at_state = [&](float* base, int64_t k) { return base + ((k * p.H + h) * p.P + p0) * p.N; };
     auto each_state = [&](float* base, auto&& f) {          // f(element, its address) for this thread's
 #pragma unroll
         for (int r = 0; r < RPT; ++r)
 #pragma unroll
-            for (int j = 0; j < kSeqN / 2; ++j) {
+            for (int j = 0; j < NS / 2; ++j) {
                 const int row = rp + RT * r, n = (j / 2 * LPR + lr) * 4 + (j & 1) * 2;
                 if (row < np && n < p.N) f(S[r][j].x, base + static_cast<int64_t>(row) * p.N + n);
                 if (row < np && n + 1 < p.N) f(S[r][j].y, base + static_cast<int64_t>(row) * p.N + n + 1);
@@ -257,7 +266,7 @@ __global__ void __launch_bounds__(seq_threads(LPR, PRE)) heads_seq_kernel(const 
 #pragma unroll
     for (int r = 0; r < RPT; ++r)
 #pragma unroll
-        for (int j = 0; j < kSeqN / 2; ++j) S[r][j] = make_float2(0.f, 0.f);
+        for (int j = 0; j < NS / 2; ++j) S[r][j] = make_float2(0.f, 0.f);
     float* slot_state = at_state(p.state, max(s.slot, 0));
     if (s.warm && (PASS == SeqPass::kStates ? seg == 0 || last : nsegs == 1))
         each_state(slot_state, [](float& v, const float* f) { v = *f; });
@@ -341,7 +350,7 @@ __global__ void __launch_bounds__(seq_threads(LPR, PRE)) heads_seq_kernel(const 
             }
             // four states at a time through all of the tokens, so that their loads are together
 #pragma unroll
-            for (int j = 0; j < kSeqN / 4; ++j) {
+            for (int j = 0; j < NS / 4; ++j) {
                 float4 B[U], C[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
@@ -451,14 +460,14 @@ std::atomic<int> g_force_pre{0};
 SeqPlan seq_plan(int64_t n_seq, int64_t tokens, int64_t H, int64_t P, int64_t G, int64_t N) {
     SeqPlan plan{};
     const int64_t ctas = n_seq * H * ((P + kSeqRows - 1) / kSeqRows);
-    const int64_t lpr = N <= 16 ? 1 : N <= 32 ? 2 : N <= 64 ? 4 : N <= 128 ? 8 : 16;
+    const SeqLanes lanes = kSeqLanes[N <= 16 ? 0 : N <= 32 ? 1 : N <= 64 ? 2 : N <= 128 ? 3 : 4];
     const int64_t mean = tokens / std::max<int64_t>(n_seq, 1);
     const int forced = g_force_pre.load();
     plan.pre = N <= 128 && G <= 65535 && (forced ? forced == 2 : mean >= kPreTokens);
-    const int64_t room = heads_sm_count() * 16 / std::max(seq_threads(static_cast<int>(lpr), plan.pre) / 32, 1);
+    const int64_t room = heads_sm_count() * 16 / std::max(seq_threads(lanes.lpr, lanes.ns, plan.pre) / 32, 1);
     const int64_t k = std::min({room / std::max<int64_t>(ctas, 1), mean / 64, static_cast<int64_t>(12)});
     plan.units = n_seq;
-    plan.np = static_cast<int>(kSeqN * lpr);
+    plan.np = lanes.lpr * lanes.ns;
     plan.chunks = tokens / kBcToks + n_seq;
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -477,32 +486,32 @@ SeqPlan seq_plan(int64_t n_seq, int64_t tokens, int64_t H, int64_t P, int64_t G,
     return plan;
 }
 
-template <typename TIO, int LPR, bool PRE>
+template <typename TIO, int LPR, int NS, bool PRE>
 cudaError_t launch_seq_pre(const SeqParams& q, unsigned grid, cudaStream_t stream) {
     if (q.seg == 0) {
-        heads_seq_kernel<TIO, LPR, SeqPass::kWhole, PRE><<<grid, seq_threads(LPR, PRE), 0, stream>>>(q);
+        heads_seq_kernel<TIO, LPR, NS, SeqPass::kWhole, PRE><<<grid, seq_threads(LPR, NS, PRE), 0, stream>>>(q);
         return cudaGetLastError();
     }
-    heads_seq_kernel<TIO, LPR, SeqPass::kStates, PRE><<<grid, seq_threads(LPR, PRE), 0, stream>>>(q);
+    heads_seq_kernel<TIO, LPR, NS, SeqPass::kStates, PRE><<<grid, seq_threads(LPR, NS, PRE), 0, stream>>>(q);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    heads_seq_kernel<TIO, LPR, SeqPass::kSegments, PRE><<<grid, seq_threads(LPR, PRE), 0, stream>>>(q);
+    heads_seq_kernel<TIO, LPR, NS, SeqPass::kSegments, PRE><<<grid, seq_threads(LPR, NS, PRE), 0, stream>>>(q);
     return cudaGetLastError();
 }
 
-template <typename TIO, int LPR>
+template <typename TIO, int LPR, int NS>
 cudaError_t launch_seq_lanes(const SeqParams& q, const SeqPlan& plan, cudaStream_t stream) {
     const int64_t per_unit = static_cast<int64_t>(q.p.H) * ((q.p.P + kSeqRows - 1) / kSeqRows);
     const unsigned grid = static_cast<unsigned>(q.units * per_unit);
-    if constexpr (LPR <= 8) {                               // (two buffers of more states do not fit)
+    if constexpr (LPR * NS <= 128) {                               // (two buffers of more states do not fit)
         if (plan.pre) {
             const dim3 bc(static_cast<unsigned>(plan.chunks), static_cast<unsigned>(q.p.G));
             heads_bc_kernel<TIO><<<bc, kBcThreads, 0, stream>>>(q, plan.np);
             const cudaError_t e = cudaGetLastError();
-            return e != cudaSuccess ? e : launch_seq_pre<TIO, LPR, true>(q, grid, stream);
+            return e != cudaSuccess ? e : launch_seq_pre<TIO, LPR, NS, true>(q, grid, stream);
         }
     }
-    return launch_seq_pre<TIO, LPR, false>(q, grid, stream);
+    return launch_seq_pre<TIO, LPR, NS, false>(q, grid, stream);
 }
 
 template <typename TIO>
@@ -511,11 +520,12 @@ cudaError_t launch_seq(const HeadsParams& p, uint8_t* workspace, cudaStream_t st
     const SeqParams q{p, plan.seg, plan.units, reinterpret_cast<float*>(workspace + plan.off_state),
                       reinterpret_cast<float*>(workspace + plan.off_decay), reinterpret_cast<float*>(workspace + plan.off_bc)};
     if (plan.units * p.H * ((p.P + kSeqRows - 1) / kSeqRows) > INT32_MAX) return cudaErrorInvalidConfiguration;
-    if (p.N <= 16) return launch_seq_lanes<TIO, 1>(q, plan, stream);
-    if (p.N <= 32) return launch_seq_lanes<TIO, 2>(q, plan, stream);
-    if (p.N <= 64) return launch_seq_lanes<TIO, 4>(q, plan, stream);
-    if (p.N <= 128) return launch_seq_lanes<TIO, 8>(q, plan, stream);
-    return launch_seq_lanes<TIO, 16>(q, plan, stream);
+    constexpr const SeqLanes* w = kSeqLanes;
+    if (p.N <= 16) return launch_seq_lanes<TIO, w[0].lpr, w[0].ns>(q, plan, stream);
+    if (p.N <= 32) return launch_seq_lanes<TIO, w[1].lpr, w[1].ns>(q, plan, stream);
+    if (p.N <= 64) return launch_seq_lanes<TIO, w[2].lpr, w[2].ns>(q, plan, stream);
+    if (p.N <= 128) return launch_seq_lanes<TIO, w[3].lpr, w[3].ns>(q, plan, stream);
+    return launch_seq_lanes<TIO, w[4].lpr, w[4].ns>(q, plan, stream);
 }
 
 }  // namespace

@@ -984,18 +984,21 @@ int heads_sm_count() {
 }
 
 // bf16 activations, up to 128 states, and sequences long enough (on average) that the products' fixed
-// costs pay, by what both paths measure, in us: token by token 7 + 0.28 a token as long as there are no
-// more CTAs than 170, in proportion beyond; here 12 + 10 a chunk up to 110 chains.  (One sequence of 45
-// tokens, 24 heads: 19 against 22; 8 of 32: 23 against 23; 16 of 24, 80 heads: 80 against 71.)  Not for heads of
-// fewer than 256 states: the operands' error is one of the terms, and in so few sums one may cancel (1.1e-5 of a
-// state of 1 x 1, 4e-6 of one of 64 x 128; fp32 has neither), while a tile has 64 x 128 whatever the head has.
+// costs pay, by what both paths measure, in us: token by token 7 + 0.28 a token of 128 states (0.18 of 16) as
+// long as the CTAs are few, and 0.28 (0.1 of 16) per 170 CTAs beyond; here 12 + 10 a chunk up to 110 chains,
+// whatever the states.  (128 states: one sequence of 45 tokens, 24 heads: 19 against 22; 8 of 32: 23 against 23;
+// 16 of 24, 80 heads: 80 against 71.  40 sequences of 60 tokens, 40 heads: 16 states 51 against 81, 128 states 251
+// against 89.)  Not for heads of fewer than 256 states: the operands' error is one of the terms, and in so few
+// sums one may cancel (1.1e-5 of a state of 1 x 1, 4e-6 of one of 64 x 128; fp32 has neither), while a tile has
+// 64 x 128 whatever the head has.
 bool heads_tc_takes(int64_t n_seq, int64_t tokens, int64_t H, int64_t P, int64_t G, int64_t N, bool bf16) {
     if (!bf16 || N > 128 || P * N < 256 || G > 65535 || n_seq < 1 || tokens < 1) return false;
     const HeadsTcPlan plan = heads_tc_plan(n_seq, tokens, H, P, G, N);
     if (plan.segments * plan.pairs > INT32_MAX || plan.chunks > INT32_MAX) return false;
     if (const int forced = g_force_path.load()) return forced == 2;
     const double mean = static_cast<double>(tokens) / static_cast<double>(n_seq), chunks = std::ceil(mean / kHeadsChunk);
-    const double seq = 7.0 + 0.28 * mean * std::max(1.0, static_cast<double>(n_seq) * plan.gtiles / 170.0);
+    const double part = static_cast<double>(N) / 128.0, ctas = static_cast<double>(n_seq) * plan.gtiles;
+    const double seq = 7.0 + mean * std::max(0.16 + 0.12 * part, (0.07 + 0.21 * part) * ctas / 170.0);
     const double tc = 12.0 + 10.0 * chunks * std::max(1.0, static_cast<double>(n_seq) * plan.pairs / 110.0);
     return tc < seq;
 }
