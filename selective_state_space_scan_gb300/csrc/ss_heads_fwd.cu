@@ -196,7 +196,10 @@ __global__ void __launch_bounds__(seq_threads(LPR, NS, PRE)) heads_seq_kernel(co
         mbar_expect_tx(&full[r & 1], bytes);
         bulk_load(&sbc[PRE ? r & 1 : 0][0][0], q.bc + (g * p.tokens + s.row0 + t0) * (2 * NP), bytes, &full[r & 1]);
     };
-    if (PRE) {
+    // (the first pass only passes on the last segment's starting state: no rounds, and no copies that the
+    // block would leave in flight)
+    const bool runs = !(PASS == SeqPass::kStates && last);
+    if (PRE && runs) {
         if (tid == 0) {
             mbar_init(&full[0], 1);
             mbar_init(&full[1], 1);
@@ -236,7 +239,7 @@ __global__ void __launch_bounds__(seq_threads(LPR, NS, PRE)) heads_seq_kernel(co
                 raw[k][t] = (chan[k] >= 0 && at >= 0 && at < end) ? xg[static_cast<int64_t>(at) * p.xbc_t + chan[k]] : from_f32<TIO>(0.f);
             }
     };
-    if (first < end) load_round(first);
+    if (runs && first < end) load_round(first);
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
         const int c = max(chan[k], 0);
@@ -270,7 +273,7 @@ __global__ void __launch_bounds__(seq_threads(LPR, NS, PRE)) heads_seq_kernel(co
     float* slot_state = at_state(p.state, max(s.slot, 0));
     if (s.warm && (PASS == SeqPass::kStates ? seg == 0 || last : nsegs == 1))
         each_state(slot_state, [](float& v, const float* f) { v = *f; });
-    if (PASS == SeqPass::kStates && last) {
+    if (!runs) {
         each_state(at_state(q.seg_state, unit), [](float& v, float* f) { *f = v; });
         return;
     }
