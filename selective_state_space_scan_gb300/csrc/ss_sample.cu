@@ -293,6 +293,14 @@ struct Team {
         if (size > 1) cluster_sync_all();
         else __syncthreads();
     }
+    // A CTA's shared memory may be touched by its peers once it is known to run: each says so as it begins
+    // and waits for the others after its first pass, by when they have.
+    __device__ __forceinline__ void begin() const {
+        if (size > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    }
+    __device__ __forceinline__ void begun() const {
+        if (size > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
     // The largest of the CTAs' numbers (the same for all threads of a CTA).
     __device__ __forceinline__ uint64_t max_over(uint64_t v) {
         if (size == 1) return v;
@@ -514,6 +522,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
     __shared__ Shared s;
     Team team{s, 0u, p.cluster, 0};
     if (p.cluster > 1) team.rank = cluster_ctarank();
+    team.begin();
     const int64_t r = blockIdx.x / p.cluster;
     const float* noise = p.noise + r * p.noise_r;
     const int V = p.V, i0 = min(V, static_cast<int>(team.rank) * p.slice), n_slice = min(V - i0, p.slice);
@@ -532,6 +541,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
         });
         if (at >= 0) own = first_of_pack(slice, n_slice, at, best, i0);
     }
+    __syncwarp();                                              // (the barrier takes whole warps)
+    team.begun();
     const float temp = p.temperature ? p.temperature[r] : 1.f;
     const float mp = p.min_p ? p.min_p[r] : 0.f;
     const int k = p.top_k && p.top_k[r] > 0 && p.top_k[r] < V ? p.top_k[r] : V;
