@@ -528,14 +528,16 @@ typedef struct {
  *   state  [n_slots, H, P, N] fp32 contiguous, window [n_slots, C, 3] fp32 contiguous (oldest
  *                       sample first): the caches, updated in place
  *   cu_seqlens [n_seq+1] int32, device: sequence i is rows cu_seqlens[i] .. cu_seqlens[i+1]-1
- *                       (any length from 0; an empty sequence leaves its starting state)
+ *                       (any length from 0; an empty sequence leaves its starting state).  The
+ *                       entries must not decrease
  *   slots  [n_seq] int32, device, or NULL (sequence i uses slot i): where the sequence's state
  *                       and window are.  A negative slot: the sequence starts from zeros and
  *                       leaves nothing.  No two sequences may share a slot.
  *   fresh  [n_seq] int32, device, or NULL (= 0): non-zero starts the sequence from zeros instead
  *                       of its slot's contents (which may then hold anything, NaN included)
- *   A slot of n_slots or more, or rows outside 0 .. tokens, set bit 2 of the device error word
- *   and that sequence is skipped.
+ *   A slot of n_slots or more, rows outside 0 .. tokens, an end before the start, or a start
+ *   below an earlier entry of cu_seqlens set bit 2 of the device error word and that sequence is
+ *   skipped.
  *   P, N in 1..SS_HEADS_MAX, G divides H.  n_seq == 0 or tokens == 0 with n_seq == 0 is a no-op.
  *   workspace           device memory, 256-byte aligned, ss_heads_workspace_size(...) bytes,
  *                       zero-filled before its first use (never again, also between calls of

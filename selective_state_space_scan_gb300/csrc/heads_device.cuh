@@ -91,6 +91,31 @@ __device__ __forceinline__ int block_prefix(int v, int* total, int* scratch) {
     return before + x - v;
 }
 
+// Sequences lie one behind the other: one that starts below an earlier entry of cu_seqlens is skipped.  So no
+// row belongs to two of them, and there are no more chunks and segments than the workspace was planned for.
+// For blockDim.x adjacent sequences at a time, from the first on, by all threads: whether this thread's
+// sequence starts at or behind every entry before its own; `largest` (0 at first) is what carries over.
+__device__ __forceinline__ bool heads_in_order(const HeadsParams& p, int seq, int& largest, int* scratch) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+    const int start = seq < p.n_seq ? p.cu[seq] : 0;
+    int x = start;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x = max(x, y);
+    }
+    int before = __shfl_up_sync(0xffffffffu, x, 1);
+    before = lane == 0 ? largest : max(before, largest);
+    __syncthreads();
+    if (lane == 31) scratch[warp] = x;
+    __syncthreads();
+    for (int w = 0; w < warps; ++w) {
+        if (w < warp) before = max(before, scratch[w]);
+        largest = max(largest, scratch[w]);
+    }
+    return start >= before;
+}
+
 // The heads of a group share its B and C channels.  Each CTA that reads their windows says so on the
 // group's counter once all its threads have (behind a barrier), and the one that finds itself the last
 // may overwrite them; it puts the counter back to zero.

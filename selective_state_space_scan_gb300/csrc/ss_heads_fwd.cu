@@ -57,10 +57,11 @@ __global__ void __launch_bounds__(kBcThreads) heads_bc_kernel(const SeqParams q,
     const int tid = threadIdx.x, id = blockIdx.x, g = blockIdx.y;
     if (tid == 0) found[0] = -1;
     __syncthreads();
-    int base = 0;
+    int base = 0, largest = 0;
     for (int s0 = 0; s0 < p.n_seq && found[0] < 0; s0 += kBcThreads) {
+        const bool in_order = heads_in_order(p, s0 + tid, largest, scratch);
         int n = 0;
-        if (s0 + tid < p.n_seq) {
+        if (s0 + tid < p.n_seq && in_order) {
             const HeadsSeq c = heads_seq(p, s0 + tid);
             n = c.ok ? max(1, (c.len + kBcToks - 1) / kBcToks) : 0;
         }
@@ -151,13 +152,16 @@ __global__ void __launch_bounds__(seq_threads(LPR, NS, PRE)) heads_seq_kernel(co
     if (PASS != SeqPass::kWhole) {                          // the sequence that this segment is of
         if (tid == 0) found[0] = -1;
         __syncthreads();
-        int base = 0;
-        for (int s0 = 0; s0 < p.n_seq && found[0] < 0; s0 += NT) {
+        int base = 0, largest = 0;
+        const bool reports = id == 0;                       // (and looks at all sequences)
+        for (int s0 = 0; s0 < p.n_seq && (reports || found[0] < 0); s0 += NT) {
+            const bool in_order = heads_in_order(p, s0 + tid, largest, scratch);
             int n = 0;
             if (s0 + tid < p.n_seq) {
                 const HeadsSeq c = heads_seq(p, s0 + tid);
-                n = c.ok ? max(1, (c.len + q.seg - 1) / q.seg) : 0;
-                if (!c.ok && id == 0 && p.err) atomicOr(p.err, kErrIndex);
+                const bool ok = c.ok && in_order;
+                n = ok ? max(1, (c.len + q.seg - 1) / q.seg) : 0;
+                if (!ok && reports && p.err) atomicOr(p.err, kErrIndex);
             }
             int total;
             const int at = base + block_prefix(n, &total, scratch);
@@ -173,7 +177,13 @@ __global__ void __launch_bounds__(seq_threads(LPR, NS, PRE)) heads_seq_kernel(co
         seg = found[1];
     }
     const HeadsSeq s = heads_seq(p, seq);
-    if (!s.ok) {
+    bool ok = s.ok;
+    if (PASS == SeqPass::kWhole) {                          // (see heads_in_order)
+        bool below = false;
+        for (int j = tid; j < seq; j += NT) below = below || p.cu[j] > s.row0;
+        ok = !__syncthreads_or(below) && ok;
+    }
+    if (!ok) {
         if (h == 0 && pt == 0 && tid == 0 && p.err) atomicOr(p.err, kErrIndex);
         return;
     }

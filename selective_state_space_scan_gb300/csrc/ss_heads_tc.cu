@@ -59,9 +59,9 @@ constexpr int kTcThreads = 512;                    // two warpgroups per tile
 // ---- where the chunks and segments of the sequences are
 
 // Chunks of sequence `seq`: at least one, so that an empty sequence is visited too; none if its
-// indexes are out of range.
-__device__ __forceinline__ int chunks_of(const HeadsParams& p, int seq) {
-    if (seq >= p.n_seq) return 0;
+// indexes are out of range or out of order.
+__device__ __forceinline__ int chunks_of(const HeadsParams& p, int seq, bool in_order) {
+    if (seq >= p.n_seq || !in_order) return 0;
     const HeadsSeq s = heads_seq(p, seq);
     return s.ok ? max(1, (s.len + kQ - 1) / kQ) : 0;
 }
@@ -169,9 +169,9 @@ __global__ void __launch_bounds__(kPrepThreads) heads_prep_kernel(const HeadsTcP
     const bool first = id == 0 && g == 0 && blockIdx.z == 0;
     if (tid == 0) found[0] = -1;
     __syncthreads();
-    int base = 0, sbase = 0;
+    int base = 0, sbase = 0, largest = 0;
     for (int s0 = 0; s0 < p.n_seq; s0 += kPrepThreads) {
-        const int seq = s0 + tid, n = chunks_of(p, seq);
+        const int seq = s0 + tid, n = chunks_of(p, seq, heads_in_order(p, seq, largest, scratch));
         int total;
         const int at = base + block_prefix(n, &total, scratch);
         if (id >= at && id < at + n) {
@@ -205,9 +205,10 @@ __global__ void __launch_bounds__(kPrepThreads) heads_prep_kernel(const HeadsTcP
     if (g == 0 && which == 0 && chunk % q.seg_chunks == 0) {
         // the segment's place among all: after those of lower number, and those of its number in sequences before
         const int seg = chunk / q.seg_chunks;
-        int at = 0;
+        int at = 0, up_to = 0;
         for (int s0 = 0; s0 < p.n_seq; s0 += kPrepThreads) {
-            const int n = (chunks_of(p, s0 + tid) + q.seg_chunks - 1) / q.seg_chunks;
+            const bool in_order = heads_in_order(p, s0 + tid, up_to, scratch);
+            const int n = (chunks_of(p, s0 + tid, in_order) + q.seg_chunks - 1) / q.seg_chunks;
             int total;
             block_prefix(min(n, seg) + (n > seg && s0 + tid < seq ? 1 : 0), &total, scratch);
             at += total;
