@@ -613,6 +613,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                 const int tok0 = ch * kQ, nt = min(kQ, s.len - tok0);
                 if (kOut && issue) {                                    // scores, and C·S of both tiles
                     mbar_sleep_bounded(&sh.bc, ph, abort, p.err);
+                    // (both tiles read one set of scores: the other's P says that it has read the last ones)
+                    if (it > 0) mbar_sleep_bounded(&sh.p_ready[1], ph ^ 1, abort, p.err);
+                    tc_fence_after();
                     for (int k = 0; k < 4 * q.nb; ++k) {
                         const uint32_t at = (k / 4) * kBlock + (k % 4) * 32;
                         tc_mma(tmem + kColScore, tc_desc(c_at + at, 16, 1024), tc_desc(b_at + at, 16, 1024),
