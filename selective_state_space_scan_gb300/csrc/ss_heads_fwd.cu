@@ -47,6 +47,11 @@ struct SeqParams {
 
 enum class SeqPass { kWhole, kStates, kSegments };
 
+// Parity of the last phase of buffer `b` of two, after `loads` copies into them in turn (more than b).
+constexpr uint32_t last_parity(int loads, int b) { return ((loads - 1 - b) >> 1) & 1; }
+static_assert(last_parity(1, 0) == 0 && last_parity(2, 1) == 0 && last_parity(3, 0) == 1 && last_parity(3, 1) == 0 &&
+              last_parity(4, 0) == 1 && last_parity(4, 1) == 1 && last_parity(5, 0) == 0 && last_parity(5, 1) == 1, "copies 0, 2, 4 and 1, 3, 5");
+
 constexpr int kBcThreads = 256, kBcToks = 32;               // tokens per block (and thread)
 
 // B and C of all tokens, convolved.  Grid (kBcToks tokens of a sequence, group).
@@ -200,8 +205,10 @@ __global__ void __launch_bounds__(seq_threads(LPR, NS, PRE)) heads_seq_kernel(co
     const float A2 = -expf(p.A_log[h]) * kLog2e, bias = p.dt_bias ? p.dt_bias[h] : 0.f, Dh = p.D ? p.D[h] : 0.f;
 
     const int rounds = (end - first + kSeqT - 1) / kSeqT;
-    auto load_bc = [&](int r) {                             // (one thread) round r into its buffer
+    int loads = 0;
+    auto load_bc = [&](int r) {                             // (one thread, in order) round r into its buffer
         const int t0 = first + r * kSeqT;
+        ++loads;
         const uint32_t bytes = static_cast<uint32_t>(min(kSeqT, end - t0)) * (2 * NP * 4);
         mbar_expect_tx(&full[r & 1], bytes);
         bulk_load(&sbc[PRE ? r & 1 : 0][0][0], q.bc + (g * p.tokens + s.row0 + t0) * (2 * NP), bytes, &full[r & 1]);
@@ -428,8 +435,8 @@ __global__ void __launch_bounds__(seq_threads(LPR, NS, PRE)) heads_seq_kernel(co
     }
     if (PRE && abort_flag && tid == 0) {                    // copies in flight land before the block ends
         const long long c0 = clock64();
-        while (!(mbar_try_wait(&full[0], ((rounds - 1) >> 1) & 1) && mbar_try_wait(&full[1], ((rounds - 1) >> 1) & 1)) &&
-               clock64() - c0 < (1ll << 26)) {
+        auto landed = [&](int b) { return loads <= b || mbar_try_wait(&full[b], last_parity(loads, b)); };
+        while (!(landed(0) && landed(1)) && clock64() - c0 < (1ll << 28)) {
         }
     }
     if (PASS == SeqPass::kStates) {

@@ -309,8 +309,10 @@ struct TcShared {
     uint64_t bc;                                   // B and C have arrived
     uint64_t cs, st, pv[2];                        // products complete: scores and C·S; state; P·x of a tile
     uint64_t x_ready, p_ready[2], y_free;          // operands written: x tiles; P; S (and the last y read)
+    uint64_t drain[2];                             // everything a tile's issuer has issued (after a wait that ran out)
     uint32_t tmem;
     int abort;
+    uint32_t loads;                                // of B and C so far (its issuer's alone)
     TcTables tab[2];
 };
 constexpr uint32_t kTcSmem = 3 * kImage + 2 * kTileBytes + sizeof(TcShared);
@@ -409,6 +411,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
         mbar_init(&sh.p_ready[0], 8);
         mbar_init(&sh.p_ready[1], 8);
         mbar_init(&sh.y_free, 16);
+        mbar_init(&sh.drain[0], 1);
+        mbar_init(&sh.drain[1], 1);
+        sh.loads = 0u;
         mbar_fence_init();
         sh.abort = 0;
     }
@@ -465,6 +470,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
             auto load_bc = [&](int ch) {
                 const uint32_t part = q.nb * kBlock;
                 const uint8_t* f = src + static_cast<int64_t>(ch) * p.G * 3 * part;
+                ++sh.loads;
                 mbar_expect_tx(&sh.bc, (kOut ? 3 : 2) * part);
                 bulk_load(img, f, part, &sh.bc);
                 bulk_load(img + kImage, f + part, part, &sh.bc);
@@ -504,7 +510,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                 prefetch(c.ch0);
                 dt_next = load_dt(c.ch0);
                 // (the last piece's products are complete: this thread has waited for them)
-                if (issue && !(PASS == Pass::kStates && ends)) load_bc(c.ch0);
+                if (issue && !(PASS == Pass::kStates && ends) && !*abort) load_bc(c.ch0);
             }
 
             // The state that enters: thread = state n, registers = rows hf·32 .. of the tile.
@@ -911,9 +917,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                 for (int k = hf * 128 + t; k < np; k += 256) heads_keep_window<TIO>(p, s, cx + k);
             }
         });
-        if (issue && *abort) {                                         // a copy in flight lands before the block ends
+        if (issue_pv && *abort) {                // products and copies in flight are over before the block ends (or a limit)
+            tc_commit(&sh.drain[wg]);
             const long long t0 = clock64();
-            while (!mbar_try_wait(&sh.bc, (it - 1) & 1) && !mbar_try_wait(&sh.bc, it & 1) && clock64() - t0 < (1ll << 28)) {
+            while (!(mbar_try_wait(&sh.drain[wg], 0u) &&
+                     (wg > 0 || sh.loads == 0u || mbar_try_wait(&sh.bc, (sh.loads - 1u) & 1u))) &&
+                   clock64() - t0 < (1ll << 28)) {
             }
         }
     }
