@@ -542,7 +542,9 @@ typedef struct {
  *   workspace           device memory, 256-byte aligned, ss_heads_workspace_size(...) bytes,
  *                       zero-filled before its first use (never again, also between calls of
  *                       different sizes and ss_heads_step's).  Calls that share it must not run
- *                       concurrently on the device.
+ *                       concurrently on the device.  A call that is captured in a graph reads and
+ *                       writes it at every launch of the graph: it has to live as long, and be
+ *                       filled before the first launch (or by the graph)
  * Sums and the state are fp32.  So are all factors, but for longer bf16 sequences, which take the
  * tensor cores: there B and Δ·x go into the state as sums of two bf16 (a state is off by some
  * 4e-6 of its norm), and C, S, x and the decays into y as one (2e-3 of y, as its own

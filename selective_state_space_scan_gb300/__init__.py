@@ -109,6 +109,8 @@ def lib() -> ctypes.CDLL:
         L.ss_add_rmsnorm_f8.restype = ctypes.c_int
         L.ss_sample.argtypes = [vp] * 7 + [i64] * 2 + [ctypes.c_int32, i64, i64, vp]
         L.ss_sample.restype = ctypes.c_int
+        L.ss__capture_id.argtypes = [vp]
+        L.ss__capture_id.restype = ctypes.c_uint64
         L.ss_status_string.argtypes = [ctypes.c_int]
         L.ss_status_string.restype = ctypes.c_char_p
         L.ss_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]
@@ -163,6 +165,7 @@ def _check_inner(t, name):
 
 
 _WORKSPACES = {}
+_CAPTURED = {}
 _WS_SIZES = {}
 
 
@@ -174,10 +177,22 @@ def workspace_for(device, stream, nbytes: int, purpose: str = "fwd"):
     ``stream`` is the torch stream the calls run on (None: the device's current stream).  The
     buffer is allocated and zero-filled on that stream, so the fill is ordered before its first
     use, and when a larger buffer replaces it the caching allocator hands the old memory only to
-    later work on the same stream."""
+    later work on the same stream.
+
+    While the stream is being captured the buffer is one of that capture's alone: its memory belongs to
+    the graph and its fill is a node of it, so that the graph needs neither another one's launch nor a
+    buffer that calls outside of graphs may replace.  It is kept until the stream's next capture."""
     import torch
     s = torch.cuda.current_stream(device) if stream is None else stream
     key = (str(device), s.cuda_stream, purpose)
+    capture = lib().ss__capture_id(s.cuda_stream)
+    if capture:
+        made_in, ws = _CAPTURED.get(key, (0, None))
+        if made_in != capture or ws.numel() < nbytes:
+            with torch.cuda.stream(s):
+                ws = torch.zeros(max(nbytes, 1), dtype=torch.uint8, device=device)
+            _CAPTURED[key] = (capture, ws)
+        return ws
     ws = _WORKSPACES.get(key)
     if ws is None or ws.numel() < nbytes:
         with torch.cuda.stream(s):

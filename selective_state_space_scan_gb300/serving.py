@@ -51,7 +51,10 @@ def _empty(shape, dtype, device, stream):
 
 
 def _workspace(t, stream, handle, nbytes):
-    """The heads calls' workspace: one buffer per device and stream, zero-filled when it is made."""
+    """The heads calls' workspace: one buffer per device and stream, zero-filled when it is made (one of its own
+    for every capture: see workspace_for)."""
+    if _lib.ss__capture_id(handle):
+        return _ss.workspace_for(t.device, stream, nbytes, purpose="heads")
     key = (t.get_device(), handle)
     ws = _HEADS_WS.get(key)
     if ws is None or ws.numel() < nbytes:
