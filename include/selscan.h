@@ -135,9 +135,10 @@ ss_status ss_fwd(const void* u, const void* delta_raw, const float* delta_bias,
  *   workspace        device memory, 256-byte aligned, at least workspace_bytes =
  *                    ss_fwd_workspace_size(...) bytes, zero-filled before its first use (the
  *                    library never needs it cleared again).  Calls that share a workspace must
- *                    not run concurrently on the device.  A workspace smaller than the size
- *                    query asks for gives the time-split schedule fewer segments (none, i.e.
- *                    ss_fwd's schedule, below two); for the balanced schedule it returns
+ *                    not run concurrently on the device, nor be made by two threads at once.
+ *                    A workspace smaller than the size query asks for gives the time-split
+ *                    schedule fewer segments (none, i.e. ss_fwd's schedule, below two); for the
+ *                    balanced schedule it returns
  *                    SS_ERR_INVALID_ARG.
  *   workspace NULL   behaves exactly like ss_fwd.
  * A misaligned workspace returns SS_ERR_MISALIGNED.  When the arguments cannot use TMA-fed
@@ -322,7 +323,8 @@ ss_status ss_fwd_static(const void* u, const void* delta_raw, const float* delta
  *   workspace          device memory, 256-byte aligned, ss_bwd_workspace_size(...) bytes (the
  *                      state at every 16th step and, for few channel tiles, the time split's
  *                      per-segment entering states, adjoints and Σ Δ); contents need no
- *                      initialisation.  Calls that share it must not overlap on the device.
+ *                      initialisation.  Calls that share it must not overlap on the device, nor be
+ *                      made by two threads at once.
  * Schedule: one CTA per 32-channel tile over the whole sequence, or, when the tiles alone cannot
  * fill the GPU (e.g. one long sequence), the sequence cut into segments that run side by side:
  * each segment is folded and its adjoint swept from zero, the entering states are composed left
@@ -542,9 +544,11 @@ typedef struct {
  *   workspace           device memory, 256-byte aligned, ss_heads_workspace_size(...) bytes,
  *                       zero-filled before its first use (never again, also between calls of
  *                       different sizes and ss_heads_step's).  Calls that share it must not run
- *                       concurrently on the device.  A call that is captured in a graph reads and
- *                       writes it at every launch of the graph: it has to live as long, and be
- *                       filled before the first launch (or by the graph)
+ *                       concurrently on the device, nor be made by two threads at once (a call is
+ *                       up to three launches that pass data through it).  A call that is
+ *                       captured in a graph reads and writes it at every launch of the graph: it
+ *                       has to live as long, and be filled before the first launch (or by the
+ *                       graph)
  * Sums and the state are fp32.  So are all factors, but for longer bf16 sequences, which take the
  * tensor cores: there B and Δ·x go into the state as sums of two bf16 (a state is off by some
  * 4e-6 of its norm), and C, S, x and the decays into y as one (2e-3 of y, as its own

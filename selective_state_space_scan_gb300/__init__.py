@@ -7,6 +7,7 @@ There is no CPU path: if the library cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import threading
 import os
 from typing import Optional
 
@@ -169,6 +170,16 @@ _CAPTURED = {}
 _WS_SIZES = {}
 
 
+_STREAM_LOCKS = {}
+
+
+def _stream_lock(handle):
+    """Held by a call from the lookup of its stream's workspace until all of its launches are on the stream:
+    they pass data through that buffer, so another thread's must not come between them, nor replace it."""
+    lock = _STREAM_LOCKS.get(handle)
+    return _STREAM_LOCKS.setdefault(handle, threading.Lock()) if lock is None else lock
+
+
 def workspace_for(device, stream, nbytes: int, purpose: str = "fwd"):
     """A zero-filled, 256-byte aligned device buffer of at least nbytes, cached per (device,
     stream, purpose) and grown when needed; calls on one stream are ordered, so they never
@@ -245,18 +256,19 @@ def ss_fwd(u, delta_raw, delta_bias, A_log, B, C, D=None, z=None, y=None, last_s
     nbytes = ss_fwd_workspace_size(batch, L, Dm, N, io) if workspace and batch * L * Dm > 0 else 0
     sh = _stream_handle(stream)
     ws_ptr, ws_len = None, 0
-    if nbytes:
-        ws = workspace_for(u.device, stream, nbytes)
-        ws_ptr, ws_len = ws.data_ptr(), ws.numel()
-    if h0 is not None:
-        st = lib().ss_fwd_h0(*head, _ptr(h0), *dims, ws_ptr, ws_len, sh)
-        where = "ss_fwd_h0"
-    elif nbytes:
-        st = lib().ss_fwd_ws(*head, *dims, ws_ptr, ws_len, sh)
-        where = "ss_fwd_ws"
-    else:
-        st = lib().ss_fwd(*head, *dims, sh)
-        where = "ss_fwd"
+    with _stream_lock(sh):
+        if nbytes:
+            ws = workspace_for(u.device, stream, nbytes)
+            ws_ptr, ws_len = ws.data_ptr(), ws.numel()
+        if h0 is not None:
+            st = lib().ss_fwd_h0(*head, _ptr(h0), *dims, ws_ptr, ws_len, sh)
+            where = "ss_fwd_h0"
+        elif nbytes:
+            st = lib().ss_fwd_ws(*head, *dims, ws_ptr, ws_len, sh)
+            where = "ss_fwd_ws"
+        else:
+            st = lib().ss_fwd(*head, *dims, sh)
+            where = "ss_fwd"
     if st != 0:
         raise SelscanError(st, where)
     return y
@@ -314,10 +326,11 @@ def ss_fwd_host(u, delta_raw, delta_bias, A_log, B, C, D=None, z=None, y=None, l
     with torch.cuda.device(dev):          # the library runs on the current device
         sh = _stream_handle(stream)
         nbytes = int(lib().ss_fwd_host_workspace_size(batch, L, Dm, N, io))
-        ws = workspace_for(dev, stream, nbytes, purpose="host") if nbytes else None
-        st = lib().ss_fwd_host(_ptr(u), _ptr(delta_raw), _ptr(delta_bias), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D),
-                               _ptr(z), _ptr(y), _ptr(last_state), batch, L, Dm, N, io,
-                               None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), sh)
+        with _stream_lock(sh):
+            ws = workspace_for(dev, stream, nbytes, purpose="host") if nbytes else None
+            st = lib().ss_fwd_host(_ptr(u), _ptr(delta_raw), _ptr(delta_bias), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D),
+                                   _ptr(z), _ptr(y), _ptr(last_state), batch, L, Dm, N, io,
+                                   None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), sh)
     if st != 0:
         raise SelscanError(st, "ss_fwd_host")
     return y
@@ -462,12 +475,14 @@ def ss_fwd_ckpt(u, delta_raw, delta_bias, A_log, B, C, D=None, z=None, y=None, l
                    y.stride(0), y.stride(1), B.stride(0), B.stride(1), C.stride(0), C.stride(1))
     ws_ptr, ws_len = None, 0
     wbytes = ss_fwd_workspace_size(batch, L, Dm, N, io) if workspace and batch * L * Dm > 0 else 0
-    if wbytes:
-        ws = workspace_for(u.device, stream, wbytes)
-        ws_ptr, ws_len = ws.data_ptr(), ws.numel()
-    st = lib().ss_fwd_ckpt(_ptr(u), _ptr(delta_raw), _ptr(delta_bias), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D),
-                           _ptr(z), _ptr(y), _ptr(last_state), _ptr(h0), _ptr(ckpt), batch, L, Dm, N, ctypes.byref(s),
-                           ws_ptr, ws_len, _stream_handle(stream))
+    sh = _stream_handle(stream)
+    with _stream_lock(sh):
+        if wbytes:
+            ws = workspace_for(u.device, stream, wbytes)
+            ws_ptr, ws_len = ws.data_ptr(), ws.numel()
+        st = lib().ss_fwd_ckpt(_ptr(u), _ptr(delta_raw), _ptr(delta_bias), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D),
+                               _ptr(z), _ptr(y), _ptr(last_state), _ptr(h0), _ptr(ckpt), batch, L, Dm, N, ctypes.byref(s),
+                               ws_ptr, ws_len, sh)
     if st != 0:
         raise SelscanError(st, "ss_fwd_ckpt")
     return y, ckpt
@@ -499,17 +514,18 @@ def ss_bwd(dy, u, delta_raw, delta_bias, A_log, B, C, D=None, z=None, h0=None, d
                    0, 0, B.stride(0), B.stride(1), C.stride(0), C.stride(1))
     sh = _stream_handle(stream)
     nbytes = int(lib().ss_bwd_workspace_size(batch, L, Dm, N))
-    ws = workspace_for(u.device, stream, nbytes, purpose="bwd") if nbytes else None
     head = (_ptr(u), _ptr(delta_raw), _ptr(delta_bias), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(h0))
     tail = (_ptr(dy), _ptr(dlast), _ptr(g["du"]), _ptr(g["ddelta_raw"]), _ptr(g["dz"]), _ptr(g["dB"]), _ptr(g["dC"]),
-            _ptr(g["dA_log"]), _ptr(g["dD"]), _ptr(g["ddelta_bias"]), _ptr(g["dh0"]), batch, L, Dm, N, ctypes.byref(s),
-            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), sh)
-    if ckpt is not None:
-        st = lib().ss_bwd_ckpt(*head, _ptr(ckpt), *tail)
-        where = "ss_bwd_ckpt"
-    else:
-        st = lib().ss_bwd(*head, *tail)
-        where = "ss_bwd"
+            _ptr(g["dA_log"]), _ptr(g["dD"]), _ptr(g["ddelta_bias"]), _ptr(g["dh0"]), batch, L, Dm, N, ctypes.byref(s))
+    with _stream_lock(sh):
+        ws = workspace_for(u.device, stream, nbytes, purpose="bwd") if nbytes else None
+        tail += (None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), sh)
+        if ckpt is not None:
+            st = lib().ss_bwd_ckpt(*head, _ptr(ckpt), *tail)
+            where = "ss_bwd_ckpt"
+        else:
+            st = lib().ss_bwd(*head, *tail)
+            where = "ss_bwd"
     if st != 0:
         raise SelscanError(st, where)
     return g

@@ -139,11 +139,12 @@ def ss_heads_fwd(xbc, dt_raw, conv_w, A_log, state, window, cu_seqlens, conv_b=N
     if nbytes is None:
         nbytes = _HEADS_BYTES[key] = int(_lib.ss_heads_workspace_size(*key))
     handle = _stream(xbc, stream)
-    ws = _workspace(xbc, stream, handle, nbytes)
     p = _ss._ptr
-    st = _lib.ss_heads_fwd(xbc.data_ptr(), dt_raw.data_ptr(), p(z), conv_w.data_ptr(), p(conv_b), p(dt_bias), A_log.data_ptr(),
-                           p(D), y.data_ptr(), state.data_ptr(), window.data_ptr(), cu_seqlens.data_ptr(), p(slots), p(fresh),
-                           n, T, H, P, G, N, n_slots, ctypes.byref(s), ws.data_ptr(), ws.numel(), handle)
+    with _ss._stream_lock(handle):
+        ws = _workspace(xbc, stream, handle, nbytes)
+        st = _lib.ss_heads_fwd(xbc.data_ptr(), dt_raw.data_ptr(), p(z), conv_w.data_ptr(), p(conv_b), p(dt_bias),
+                               A_log.data_ptr(), p(D), y.data_ptr(), state.data_ptr(), window.data_ptr(), cu_seqlens.data_ptr(),
+                               p(slots), p(fresh), n, T, H, P, G, N, n_slots, ctypes.byref(s), ws.data_ptr(), ws.numel(), handle)
     if st != 0:
         raise _ss.SelscanError(st, "ss_heads_fwd")
     return y
@@ -161,11 +162,12 @@ def ss_heads_step(state, window, xbc, dt_raw, conv_w, A_log, conv_b=None, dt_bia
     if nbytes is None:
         nbytes = _HEADS_BYTES[key] = int(_lib.ss_heads_step_workspace_size(n, G))
     handle = _stream(xbc, stream)
-    ws = _workspace(xbc, stream, handle, nbytes)
     p = _ss._ptr
-    st = _lib.ss_heads_step(state.data_ptr(), window.data_ptr(), xbc.data_ptr(), dt_raw.data_ptr(), p(z), conv_w.data_ptr(),
-                            p(conv_b), p(dt_bias), A_log.data_ptr(), p(D), y.data_ptr(), p(slots), n, H, P, G, N, n_slots,
-                            ctypes.byref(s), ws.data_ptr(), ws.numel(), handle)
+    with _ss._stream_lock(handle):
+        ws = _workspace(xbc, stream, handle, nbytes)
+        st = _lib.ss_heads_step(state.data_ptr(), window.data_ptr(), xbc.data_ptr(), dt_raw.data_ptr(), p(z), conv_w.data_ptr(),
+                                p(conv_b), p(dt_bias), A_log.data_ptr(), p(D), y.data_ptr(), p(slots), n, H, P, G, N, n_slots,
+                                ctypes.byref(s), ws.data_ptr(), ws.numel(), handle)
     if st != 0:
         raise _ss.SelscanError(st, "ss_heads_step")
     return y
