@@ -8,7 +8,7 @@
 // images of bf16 operand tiles: B as a sum of two bf16 (hi + lo), C rounded.  heads_tc_kernel walks
 // the chunks of one sequence (or of a segment of it) for two tiles of 64 rows of the state (two heads,
 // as a rule), two warpgroups for each:
-//   scores C·Bᵀ, and C·S of both tiles        while the warpgroups convolve x, as tiles of x and of
+//   scores C·Bᵀ (C·hi + C·lo), and C·S        while the warpgroups convolve x, as tiles of x and of
 //                                             x scaled for the state (hi + lo)
 //   the state's products, hi·hi + hi·lo + lo·hi   while they turn scores into P (decay, Δ, mask)
 //   P·x on top of exp2(l)·(C·S), P read from tensor memory
@@ -16,7 +16,10 @@
 //
 // Rounding: the state's operands carry 16 bits each and the product of their low parts is left out, so a state
 // is off by about 4e-6 of its norm (in fp32: 1e-6).  y is rounded to bf16 in the end; the factors C, S, P and x of its sums are rounded to bf16
-// before the products, each error as large as that last one, and D·x is not.
+// before the products, each error as large as that last one, and D·x is not.  B is not either (hi + lo in the scores
+// too): where one token's step outweighs all others', its score's error is that of every output, and C·B
+// cancels.  y of such prompts is off by 3e-3 to 4.5e-3 (with one bf16 of B by 3.3e-3 to 5.1e-3, and a quarter of a chunk's
+// microsecond less), of others by 2e-3, 1.7e-3 of which are its own rounding.
 // A decay is only ever the exp2 of a sum of steps between its two tokens, never a quotient, and such
 // sums are taken over the steps themselves, so strong decays neither overflow nor cancel.  P is zero above
 // the diagonal, and zero times an infinity or NaN is NaN: such x are zeros in P·x, and their channel's
@@ -624,8 +627,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                     tc_fence_after();
                     for (int k = 0; k < 4 * q.nb; ++k) {
                         const uint32_t at = (k / 4) * kBlock + (k % 4) * 32;
-                        tc_mma(tmem + kColScore, tc_desc(c_at + at, 16, 1024), tc_desc(b_at + at, 16, 1024),
+                        tc_mma(tmem + kColScore, tc_desc(c_at + at, 16, 1024), tc_desc(b_at + kImage + at, 16, 1024),
                                tc_idesc(128, 128, false, false), k > 0);
+                        tc_mma(tmem + kColScore, tc_desc(c_at + at, 16, 1024), tc_desc(b_at + at, 16, 1024),
+                               tc_idesc(128, 128, false, false), true);
                     }
                     mbar_sleep_bounded(&sh.y_free, ph, abort, p.err);
                     tc_fence_after();
