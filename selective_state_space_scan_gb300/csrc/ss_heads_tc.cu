@@ -20,9 +20,11 @@
 // too): where one token's step outweighs all others', its score's error is that of every output, and C·B
 // cancels.  y of such prompts is off by 3e-3 to 4.5e-3 (with one bf16 of B by 3.3e-3 to 5.1e-3, and a quarter of a chunk's
 // microsecond less), of others by 2e-3, 1.7e-3 of which are its own rounding.
-// A decay is only ever the exp2 of a sum of steps between its two tokens, never a quotient, and such
-// sums are taken over the steps themselves, so strong decays neither overflow nor cancel.  P is zero above
-// the diagonal, and zero times an infinity or NaN is NaN: such x are zeros in P·x, and their channel's
+// A decay is the exp2 of the sum of the steps between its two tokens, never a quotient.  From one block of 32
+// tokens to another, and to the chunk's end, these sums are taken over the steps themselves; within a block (P's
+// diagonal) as the difference of two running sums, whose steps are cut at 2^-128, where a decay is zero whatever else
+// it meets: the sums stay above -4096, whose ten roundings leave a decay behind strong steps off by less than 1e-3
+// (not cut, a single step of 1e5 leaves y off by 4e-2, one of 1e6 by 0.35).  P is zero above the diagonal, and zero times an infinity or NaN is NaN: such x are zeros in P·x, and their channel's
 // outputs from that token on are set to NaN (as the recurrence leaves them) after it.
 //
 // What bounds it is the chain within a chunk (loads, convolution, products, P, products, outputs), with one
@@ -299,6 +301,7 @@ __global__ void __launch_bounds__(kPrepThreads) heads_prep_kernel(const HeadsTcP
 
 constexpr uint32_t kImage = 2 * kBlock;            // B hi, B lo or C in shared memory (N up to 128)
 constexpr uint32_t kTileBytes = 4 * kBlock;        // per tile: x, x scaled hi, x scaled lo, state
+constexpr float kLeastDecay = -128.f;              // log2 of a step's decay at least: ex2 of it is zero, as of all below
 constexpr int kFacs = 192;                         // decay factors of the blocks off the diagonal
 constexpr uint32_t kNoBad = 0x01010101u * kQ;
 constexpr int kToks = 8;                           // tokens per thread in the convolution and the output
@@ -646,7 +649,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
                 load_weights(wk, wb);
                 // time steps: thread = token (both warpgroups of a tile compute them all)
                 const float dt = (on && t < nt) ? softplus(dt_next + dbias) : 0.f;
-                const float a = dt * A2;
+                const float a = dt * A2 < kLeastDecay ? kLeastDecay : dt * A2;
                 float l = a, r = __shfl_down_sync(0xffffffffu, a, 1);   // sums up to t, and after t, in the block of 32
                 if (lane == 31) r = 0.f;
 #pragma unroll
