@@ -212,13 +212,22 @@ def workspace_for(device, stream, nbytes: int, purpose: str = "fwd"):
     return ws
 
 
+def _remember(cache, key, value):
+    """value, kept under key; a full cache starts over (lengths that never come back would fill it for good)."""
+    if len(cache) >= 1024:
+        cache.clear()
+    cache[key] = value
+    return value
+
+
 def ss_fwd_workspace_size(batch, L, Dm, N, io_dtype=SS_F32) -> int:
     """Bytes of workspace ss_fwd_ws / ss_fwd_h0 need on the current device (0: none)."""
     import torch
     key = (torch.cuda.current_device() if torch.cuda.is_available() else -1, batch, L, Dm, N, io_dtype)
-    if key not in _WS_SIZES:
-        _WS_SIZES[key] = int(lib().ss_fwd_workspace_size(batch, L, Dm, N, io_dtype))
-    return _WS_SIZES[key]
+    nbytes = _WS_SIZES.get(key)
+    if nbytes is None:
+        nbytes = _remember(_WS_SIZES, key, int(lib().ss_fwd_workspace_size(batch, L, Dm, N, io_dtype)))
+    return nbytes
 
 
 def ss_fwd(u, delta_raw, delta_bias, A_log, B, C, D=None, z=None, y=None, last_state=None,

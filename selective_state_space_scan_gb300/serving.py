@@ -134,10 +134,11 @@ def ss_heads_fwd(xbc, dt_raw, conv_w, A_log, state, window, cu_seqlens, conv_b=N
     _param(cu_seqlens, "cu_seqlens", i32, (n + 1,))
     _param(slots, "slots", i32, (n,))
     _param(fresh, "fresh", i32, (n,))
-    key = (n, T, H, P, G, N, s.io_dtype)
+    sizes = (n, T, H, P, G, N, s.io_dtype)
+    key = (xbc.get_device(), sizes)                            # (the plan depends on the device's SM count)
     nbytes = _HEADS_BYTES.get(key)
     if nbytes is None:
-        nbytes = _HEADS_BYTES[key] = int(_lib.ss_heads_workspace_size(*key))
+        nbytes = _ss._remember(_HEADS_BYTES, key, int(_lib.ss_heads_workspace_size(*sizes)))
     handle = _stream(xbc, stream)
     p = _ss._ptr
     with _ss._stream_lock(handle):
@@ -157,10 +158,10 @@ def ss_heads_step(state, window, xbc, dt_raw, conv_w, A_log, conv_b=None, dt_bia
     and returns y [batch, H*P]."""
     y, n, H, P, G, N, n_slots, s = _heads_args(xbc, dt_raw, conv_w, conv_b, dt_bias, A_log, D, z, state, window, y, stream)
     _param(slots, "slots", _torch.int32, (n,))
-    key = (n, G)
+    key = (n, G)                                               # (the same on every device)
     nbytes = _HEADS_BYTES.get(key)
     if nbytes is None:
-        nbytes = _HEADS_BYTES[key] = int(_lib.ss_heads_step_workspace_size(n, G))
+        nbytes = _ss._remember(_HEADS_BYTES, key, int(_lib.ss_heads_step_workspace_size(n, G)))
     handle = _stream(xbc, stream)
     p = _ss._ptr
     with _ss._stream_lock(handle):
