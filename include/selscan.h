@@ -611,7 +611,8 @@ ss_status ss_add_rmsnorm(const void* x, const void* residual, const float* weigh
  *   block           0 (one scale per row) or 32, 64, 128, 256 columns per scale; the last block of
  *                   a row may be short
  *   y8              [rows, D] bytes, row stride y_r;  scale [rows, ceil(D/block)] fp32 contiguous
- * A block in which some y is NaN (a row with a NaN or an infinity) has a NaN scale and NaN codes.
+ * A block in which some y is NaN (a row with a NaN or an infinity) has a NaN scale and NaN codes; one
+ * in which some y is infinite (by the weights) an infinite scale, codes of 0 and, there, NaN.
  */
 ss_status ss_add_rmsnorm_f8(const void* x, const void* residual, const float* weight, void* residual_out,
                             uint8_t* y8, float* scale, int64_t rows, int64_t D, int64_t block, float eps,

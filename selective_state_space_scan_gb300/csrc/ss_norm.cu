@@ -109,14 +109,15 @@ __device__ __forceinline__ void store_run(T* q, int n, const float v[kRun]) {
 }
 // The codes of v / scale (round to nearest even; at most 448 by the choice of scale).  The quotient is
 // v·(1/scale) and one correction by its remainder: as good as rounded once, so that a value near the
-// middle of two codes goes where a division would put it.
+// middle of two codes goes where a division would put it.  (An infinite scale has no remainder: v / scale is 0,
+// NaN for an infinite v.)
 template <bool VEC>
 __device__ __forceinline__ void store_codes(uint8_t* q, int n, const float v[kRun], float scale) {
-    const float inv = 1.f / scale;
+    const float inv = 1.f / scale, back = scale == INFINITY ? 0.f : scale;
     uint32_t lo[4];
     auto quotient = [&](float x) {
         const float f = x * inv;
-        return fmaf(fmaf(-f, scale, x), inv, f);
+        return fmaf(fmaf(-f, back, x), inv, f);
     };
 #pragma unroll
     for (int i = 0; i < 4; ++i)
