@@ -50,6 +50,7 @@ class Layer:
 class Stack:
     def __init__(self, layers=2, width=768, H=24, P=64, G=1, N=128, vocab=1000, slots=8, seed=0):
         g = torch.Generator("cuda").manual_seed(seed)
+        self.slots = slots
         self.table = (torch.randn(vocab, width, generator=g, device="cuda")).to(torch.bfloat16)
         self.layers = [Layer(g, width, H, P, G, N, slots) for _ in range(layers)]
         self.norm = torch.ones(width, device="cuda")
@@ -67,6 +68,8 @@ class Stack:
     def generate(self, prompts, new_tokens, seed=0, temperature=0.8, top_k=50, top_p=0.95, min_p=0.0):
         """prompts: lists of tokens, each on a slot of its own.  Returns [prompts, new_tokens] int32."""
         n, dev = len(prompts), "cuda"
+        if not 0 < n <= self.slots or not all(prompts):
+            raise ValueError(f"1 to {self.slots} prompts of a token or more are wanted")
         g = torch.Generator(dev).manual_seed(seed)
         lens = torch.tensor([0] + [len(p) for p in prompts])
         cu = torch.cumsum(lens, 0).to(torch.int32).to(dev)
