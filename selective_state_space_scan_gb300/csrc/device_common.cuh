@@ -15,7 +15,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 enum : unsigned int {
     kErrWaitTimeout = 1u,   // an mbarrier wait for a TMA tile exceeded its limit
     kErrGeometry = 2u,      // launch geometry disagrees with the kernel's tile shape
-    kErrIndex = 4u,         // a slot or row range in device memory is out of range (its sequence is skipped)
 };
 
 // 2^x on the SFU (ex2.approx.ftz: inputs below -126 flush to 0).

@@ -6,6 +6,10 @@
 
 namespace selscan {
 
+// Error bit beside those of device_common.cuh: a slot or row range in device memory is out of range (its
+// sequence is skipped).
+constexpr unsigned int kErrIndex = 4u;
+
 // Where a sequence's rows and its cached state are.
 struct HeadsSeq {
     int64_t row0;       // first row of xbc
