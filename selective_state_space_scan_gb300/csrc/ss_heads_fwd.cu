@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(seq_threads(LPR, NS, PRE)) heads_seq_kernel(co
     __shared__ float sx[kSeqT][kSeqRows], sy[kSeqT][kSeqRows];
     __shared__ float sdt[kSeqT], sa[kSeqT];
     __shared__ uint64_t full[2];
-    __shared__ int abort_flag;
+    __shared__ int abort_flag, loads;                       // loads: thread 0's copies so far
     __shared__ int scratch[NT / 32], found[2];
     const HeadsParams& p = q.p;
     const int tid = threadIdx.x, tiles = (p.P + kSeqRows - 1) / kSeqRows;
@@ -205,10 +205,9 @@ __global__ void __launch_bounds__(seq_threads(LPR, NS, PRE)) heads_seq_kernel(co
     const float A2 = -expf(p.A_log[h]) * kLog2e, bias = p.dt_bias ? p.dt_bias[h] : 0.f, Dh = p.D ? p.D[h] : 0.f;
 
     const int rounds = (end - first + kSeqT - 1) / kSeqT;
-    int loads = 0;
     auto load_bc = [&](int r) {                             // (one thread, in order) round r into its buffer
         const int t0 = first + r * kSeqT;
-        ++loads;
+        loads = r + 1;
         const uint32_t bytes = static_cast<uint32_t>(min(kSeqT, end - t0)) * (2 * NP * 4);
         mbar_expect_tx(&full[r & 1], bytes);
         bulk_load(&sbc[PRE ? r & 1 : 0][0][0], q.bc + (g * p.tokens + s.row0 + t0) * (2 * NP), bytes, &full[r & 1]);
@@ -221,7 +220,7 @@ __global__ void __launch_bounds__(seq_threads(LPR, NS, PRE)) heads_seq_kernel(co
             mbar_init(&full[0], 1);
             mbar_init(&full[1], 1);
             mbar_fence_init();
-            abort_flag = 0;
+            abort_flag = loads = 0;
         }
         // rows that no copy has reached yet meet Δ = 0: they have to be numbers
         for (int i = tid; i < 2 * kSeqT * 2 * NP; i += NT) (&sbc[0][0][0])[i] = 0.f;
