@@ -12,10 +12,13 @@
 // per state and token, 195 cycles of an SM for 64 x 128 states.
 // Long sequences of few heads are cut in segments: a first pass leaves each segment's state from zero
 // and its decay, the second starts every segment from the state that enters it.
-// 8 prompts of up to 1024 tokens, 24 heads of 64 x 64 states, fp32: 151 us (8.8 us of memory traffic); one of
-// 32768 tokens, 24 heads of 64 x 128: 1565 us.  Eight prompts of 512 tokens, 48 heads of 64 x 128: 273 us, the FMA
-// pipe at 62%.  bf16 prompts take the tensor cores (ss_heads_tc.cu) from where a cost rule there says so.
-// fp32 ones do not: three bf16 products leave 4e-6 of a state and 2e-3 of an output.
+// 8 prompts of up to 1024 tokens, 24 heads of 64 x 64 states, fp32: 154 us (8.7 us of memory traffic; cut in
+// segments, 1.7 times the recurrence's work); one of 32768 tokens, 24 heads of 64 x 128: 1605 us.  Eight prompts of
+// 512 tokens, 48 heads of 64 x 128: 274 us, the FMA pipe at 62%.  bf16, 4 prompts of 2048 tokens, 24 heads of 64 x 256,
+// which come here whatever their length: 1058 us (13 of traffic; 64 x 128 on the tensor cores 122).  One of 45 tokens,
+// 24 heads: 20 us, 24 CTAs on 152 SMs with one chain of 45 steps each.  bf16 prompts take the tensor cores (ss_heads_tc.cu) from where a cost rule there says so.
+// fp32 ones do not: operands of two bf16 (three products) leave 4e-6 of a state.  (Three parts and six products have
+// not been tried.)
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -5,9 +5,11 @@
 // rows of one head's state; its warps issue the state's loads first, convolve the CTA's x rows and
 // the group's B and C (into shared memory) while those are in flight, then update and reduce in
 // registers.  The heads of a group all read its B and C windows; the last of them shifts those.
-// 61 requests of 64 heads of 64 x 128 states: 45.9 us, 5.75 TB/s (39.5 us at the copy rate); 256 of 80 heads of
-// 64 x 64: 118 us (106); with 16 states, where the convolution's work per byte is largest, 45.7 us (31).  One request of
-// 24 heads: 5.5 us, the launch and one dependent chain of loads.
+// bf16, 61 requests of 64 heads of 64 x 128 states: 48 us, 5.5 TB/s (38.8 us at the copy rate); 256 of 80 heads of
+// 64 x 64: 123 us (105), in fp32 with 8 groups 125 (107); 488 of 64 heads of 64 x 16, where the convolution's work per
+// byte is largest, 75 (47).  Other state counts take 4-byte accesses: 64 heads of 64 x 24, 305 requests: 134 us (41); x 96,
+// 81 requests: 116 (39); x 256, 30 requests: 65 (38).  One request of 24 heads: 4.6 us, the launch and one dependent
+// chain of loads.
 #include <cuda_runtime.h>
 
 #include <cstdint>

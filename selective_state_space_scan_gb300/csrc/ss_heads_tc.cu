@@ -15,11 +15,11 @@
 // The state itself stays in registers, fp32: what the chunk adds comes out of tensor memory.
 //
 // Rounding: the state's operands carry 16 bits each and the product of their low parts is left out, so a state
-// is off by about 4e-6 of its norm (in fp32: 1e-6).  y is rounded to bf16 in the end; the factors C, S, P and x of its sums are rounded to bf16
-// before the products, each error as large as that last one, and D·x is not.  B is not either (hi + lo in the scores
-// too): where one token's step outweighs all others', its score's error is that of every output, and C·B
-// cancels.  y of such prompts is off by 3e-3 to 4.5e-3 (with one bf16 of B by 3.3e-3 to 5.1e-3, and a quarter of a chunk's
-// microsecond less), of others by 2e-3, 1.7e-3 of which are its own rounding.
+// is off by about 4e-6 of its norm (in fp32: 1e-6).  y is rounded to bf16 in the end; the factors C, S, P and x of
+// its sums are rounded to bf16 before the products, each error as large as that last one, and D·x is not.  B is
+// not either (hi + lo in the scores too): where one token's step outweighs all others', the error of its score is that
+// of every output behind it, and C·B cancels.  y of such prompts is off by 3e-3 to 4.8e-3 (with B in one bf16 by
+// up to 5.7e-3; the second product costs 0.15 us a chunk), of others by 2e-3, 1.7e-3 of which are its own rounding.
 // A decay is the exp2 of the sum of the steps between its two tokens, never a quotient.  From one block of 32
 // tokens to another, and to the chunk's end, these sums are taken over the steps themselves; within a block (P's
 // diagonal) as the difference of two running sums, whose steps are cut at 2^-128, where a decay is zero whatever else
@@ -29,11 +29,12 @@
 //
 // What bounds it is the chain within a chunk (loads, convolution, products, P, products, outputs), with one
 // CTA of 16 warps on an SM: two tiles' operands and accumulators fill its shared and tensor memory.  Four
-// sequences of 8192 tokens, 80 heads of 64 x 128 states, bf16, gated: 735 us, 11.2 us a chunk and SM, at 43% of
-// the issue slots, 15% of the tensor pipe and 15% of the memory's peak (156 us are the copy rate's).  One
-// document of 32768 tokens, 24 heads: 385 us in two passes (48 at the copy rate).  Token by token (see
+// sequences of 8192 tokens, 80 heads of 64 x 128 states, bf16, gated: 770 us, 11.4 us a chunk and SM, at 42% of
+// the issue slots, 17% of the tensor pipe and 15% of the memory's peak (153 us are the copy rate's): no unit is full,
+// and global loads in the middle of the chain are the longest stall.  One document of 32768 tokens, 24 heads: 397 us
+// in two passes (47 at the copy rate).  Token by token (see
 // ss_heads_fwd.cu) the FMA pipe alone would take 1.7 and 0.5 ms.
-// Measured and not taken: one tile per product (N = 64), which shared memory's bandwidth bounds (940 us), a warp
+// Measured (against 715 to 735 us then) and not taken: one tile per product (N = 64), which shared memory's bandwidth bounds (940 us), a warp
 // for issuing alone (96 registers a thread, spills), x or z a chunk ahead in registers (841), waves of 2 or 8
 // chunks (no gain), equal ranges of chunks for every CTA (three times as long).
 #include <cuda_runtime.h>
@@ -112,9 +113,9 @@ __device__ __forceinline__ float4 quad_floats(uint2 u) { return make_float4(bf16
 // The same in the scan, where 16 lanes of a warp hold a row of a tile's 64 channels and a thread holds many
 // rows: without VEC a lane loads the two words at its channels and takes the third from the lane after it;
 // the last lane's third words of all rows (up to 16) are spread over the lanes of the row (load_tail).
-// Four sequences of 8192 tokens, 128 states, a chunk of a pair of tiles per SM: 11.0 us with VEC (76 heads),
-// 14.7 at rows of 4-byte boundaries (38 heads), 15.2 at any (77 heads); 16.7 and 18.3 with three words a row and
-// thread (276 bytes of spills), 22.6 with one access per channel.
+// Sequences of 8192 tokens, 128 states, time over chunks per SM: 11.6 us with VEC (4, 76 heads), 15.9 at rows of
+// 4-byte boundaries (8, 38 heads), 17.9 at any (4, 77 heads).  At 4-byte boundaries three words a row and thread (276
+// bytes of spills) took 16.7 where this took 14.7 then, and one access per channel 22.6.
 template <bool VEC> struct Row4 : Quad4<true> {
     __device__ __forceinline__ uint2 bits(uint32_t, uint32_t, int, int) const { return u; }
 };
@@ -939,8 +940,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) heads_tc_kernel(const HeadsTcPa
     if (tid / 32 == 0) tc_dealloc(tmem, kTmemCols);
 }
 
-// Segments per sequence of the time split (1: none), for sequences of equal length, in units of a chunk's
-// time.  Without it no more CTAs run than there are chains (sequences times pairs of tiles).  With it a
+// Segments per sequence of the time split (1: none), for sequences of equal length (the host does not know them:
+// one of 32768 tokens among fifteen of 100, 24 heads, is not cut and takes 2.66 ms, alone 0.41), in units of a
+// chunk's time.  Without it no more CTAs run than there are chains (sequences times pairs of tiles).  With it a
 // segment costs a first pass of about 0.45 of a full one (no scores, no outputs) and a prologue, the
 // whole call one more launch.
 int segments_for(int64_t chains, int64_t chunks, int64_t sms) {
@@ -1009,7 +1011,7 @@ int heads_sm_count() {
 // long as the CTAs are few, and 0.28 (0.1 of 16) per 170 CTAs beyond; here 12 + 10 a chunk up to 110 chains,
 // whatever the states.  (128 states: one sequence of 45 tokens, 24 heads: 19 against 22; 8 of 32: 23 against 23;
 // 16 of 24, 80 heads: 80 against 71.  40 sequences of 60 tokens, 40 heads: 16 states 51 against 81, 128 states 251
-// against 89.)  Not for heads of fewer than 256 states: the operands' error is one of the terms, and in so few
+// against 89.)  It knows the mean length alone: the lengths themselves are in device memory.  Not for heads of fewer than 256 states: the operands' error is one of the terms, and in so few
 // sums one may cancel (1.1e-5 of a state of 1 x 1, 4e-6 of one of 64 x 128; fp32 has neither), while a tile has
 // 64 x 128 whatever the head has.
 bool heads_tc_takes(int64_t n_seq, int64_t tokens, int64_t H, int64_t P, int64_t G, int64_t N, bool bf16) {

@@ -17,11 +17,12 @@
 //     tail beyond exp(-22)) is narrowed by further histograms over the ordering number itself.
 //   - The last pass runs the race over what stays and reads the noise of those tokens alone.
 //
-// 192 rows of 128000 bf16 logits (147 MB with the noise, 22 us at the copy rate), GPU time: greedy 13.5 us; top_k
-// 50 34 us; no filter 50 us (the race: an exp2 and a reciprocal a token); top_p 0.9 146 us (three more
-// passes, each waiting for L2 more than for its arithmetic); every row with settings of its own 74 us.  One row of
-// 50257: 4.1, 9.4, 7.8 and 23 us, the passes' latency and the cluster's syncs.
-// Measured and not taken: light tokens summed in registers instead of the histogram (146 to 161 us: the atomic
+// 192 rows of 128000 bf16 logits (147 MB with the noise, 22 us at the copy rate), GPU time with nothing in L2
+// from the call before: greedy 20 us; top_k 50 43 us; no filter 54 us (the race: an exp2 and a reciprocal a token);
+// top_p 0.9 152 us (three more passes, each waiting for L2 more than for its arithmetic); every row with settings of
+// its own 86 us (greedy and top_k rows need little of the noise).  One row of 50257: 4.3, 9.8, 8.0 and 24 us, the
+// passes' latency and the cluster's syncs.
+// Measured (the same inputs call after call: top_p 146, settings of its own 74) and not taken: light tokens summed in registers instead of the histogram (146 to 161 us: the atomic
 // adds are not what bounds the pass), numbers stored to the peers instead of loaded from them (top_p 2% faster,
 // top_k 3% slower), the race over single tokens that pass the cut instead of whole packs (146 to 190 us).
 #include <cuda_runtime.h>
@@ -888,7 +889,7 @@ extern "C" ss_status ss_sample(const void* logits, const float* noise, const flo
         if (meet(out, q)) return SS_ERR_INVALID_ARG;
     // as many CTAs to a row as keep at least 2048 tokens each, up to six to an SM over all rows: a row's
     // passes take as long as its slices (one row of 50257: 38 us with one CTA of 1024 threads).  Four to an SM run
-    // at once; with no more than those 192 rows of 128000 take 135 instead of 146 us if all have a top_p, but 96
+    // at once; with no more than those (the same inputs call after call) 192 rows of 128000 take 135 instead of 146 us if all have a top_p, but 96
     // instead of 74 if every row has settings of its own, when the longest rows are what the call waits for.
     int sms = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return SS_ERR_CUDA;
