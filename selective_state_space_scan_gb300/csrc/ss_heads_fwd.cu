@@ -46,7 +46,31 @@ struct SeqParams {
     float* seg_state;       // [units, H, P, N]: what a segment leaves from zero
     float* seg_decay;       // [units, H]: its log2 decay
     float* bc;              // [G, tokens][B | C], each padded with zeros to all lanes' states
+    uint8_t* in_order;      // [n_seq] whether a sequence lies behind all before it; nullptr: every CTA looks itself
 };
+
+// Sequences from which on one small launch looks at their order for all CTAs, each of which would read all entries
+// before its own.  24 heads, looked at by every CTA and beforehand: 64 sequences of 8 tokens (64 x 128, bf16) 93 and
+// 94 us, 256 of 4 300 and 300, 400 of 4 465 and 455; 2048 of 2 (64 x 64, fp32) 1306 and 1192.
+constexpr int kOrderFrom = 256;
+constexpr int kOrderThreads = 1024;
+
+// The same by all threads of a CTA for one sequence.  (Not inlined: the recurrence is scheduled worse with it.)
+__device__ __noinline__ bool heads_behind_all(const int32_t* cu, int seq) {
+    bool below = false;
+    for (int j = threadIdx.x; j < seq; j += blockDim.x) below |= cu[j] > cu[seq];
+    return !__syncthreads_or(below);
+}
+
+__global__ void __launch_bounds__(kOrderThreads) heads_order_kernel(const SeqParams q) {
+    __shared__ int scratch[kOrderThreads / 32];
+    int largest = 0;
+    for (int s0 = 0; s0 < q.p.n_seq; s0 += blockDim.x) {
+        const int seq = s0 + static_cast<int>(threadIdx.x);
+        const bool ok = heads_in_order(q.p, seq, largest, scratch);
+        if (seq < q.p.n_seq) q.in_order[seq] = ok;
+    }
+}
 
 enum class SeqPass { kWhole, kStates, kSegments };
 
@@ -184,14 +208,9 @@ __global__ void __launch_bounds__(seq_threads(LPR, NS, PRE)) heads_seq_kernel(co
         seq = found[0];
         seg = found[1];
     }
+    const bool in_order = PASS != SeqPass::kWhole || (q.in_order ? q.in_order[seq] != 0 : heads_behind_all(p.cu, seq));
     const HeadsSeq s = heads_seq(p, seq);
-    bool ok = s.ok;
-    if (PASS == SeqPass::kWhole) {                          // (see heads_in_order)
-        bool below = false;
-        for (int j = tid; j < seq; j += NT) below = below || p.cu[j] > s.row0;
-        ok = !__syncthreads_or(below) && ok;
-    }
-    if (!ok) {
+    if (!s.ok || !in_order) {
         if (h == 0 && pt == 0 && tid == 0 && p.err) atomicOr(p.err, kErrIndex);
         return;
     }
@@ -475,7 +494,8 @@ struct SeqPlan {
     int seg, np;            // np: states padded
     bool pre;               // B and C convolved beforehand
     int64_t units, chunks;  // upper bounds
-    size_t off_state, off_decay, off_bc, bytes;
+    size_t off_state, off_decay, off_bc, off_order, bytes;
+    bool order;             // the sequences' order is looked at beforehand
 };
 std::atomic<int> g_force_pre{0};
 
@@ -504,6 +524,8 @@ SeqPlan seq_plan(int64_t n_seq, int64_t tokens, int64_t H, int64_t P, int64_t G,
         plan.off_decay = take(static_cast<size_t>(plan.units) * H * 4);
     }
     if (plan.pre) plan.off_bc = take(static_cast<size_t>(tokens) * G * 2 * plan.np * 4);
+    plan.order = plan.seg == 0 && n_seq >= kOrderFrom;
+    if (plan.order) plan.off_order = take(static_cast<size_t>(n_seq));
     plan.bytes = at;
     return plan;
 }
@@ -540,8 +562,14 @@ template <typename TIO>
 cudaError_t launch_seq(const HeadsParams& p, uint8_t* workspace, cudaStream_t stream) {
     const SeqPlan plan = seq_plan(p.n_seq, p.tokens, p.H, p.P, p.G, p.N);
     const SeqParams q{p, plan.seg, plan.units, reinterpret_cast<float*>(workspace + plan.off_state),
-                      reinterpret_cast<float*>(workspace + plan.off_decay), reinterpret_cast<float*>(workspace + plan.off_bc)};
+                      reinterpret_cast<float*>(workspace + plan.off_decay), reinterpret_cast<float*>(workspace + plan.off_bc),
+                      plan.order ? workspace + plan.off_order : nullptr};
     if (plan.units * p.H * ((p.P + kSeqRows - 1) / kSeqRows) > INT32_MAX) return cudaErrorInvalidConfiguration;
+    if (plan.order) {
+        heads_order_kernel<<<1, std::min(kOrderThreads, (p.n_seq + 31) / 32 * 32), 0, stream>>>(q);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
     constexpr const SeqLanes* w = kSeqLanes;
     if (p.N <= 16) return launch_seq_lanes<TIO, w[0].lpr, w[0].ns>(q, plan, stream);
     if (p.N <= 32) return launch_seq_lanes<TIO, w[1].lpr, w[1].ns>(q, plan, stream);

@@ -98,3 +98,16 @@ def test_short_sequences_and_whole_passes():
     for io in ("bf16", "f32"):
         run([0, 20, 10, 30, 25, 40], 40, io, seed=1)
         run([0, 0, 0, 40, 0, 40], 40, io, path=1, pre=1, H=40, seed=2)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [64, 255, 256, 1100])
+def test_faults_among_many_short_sequences(io, n):
+    """Sequences of a token or two, many of them out of order, around the number from which one launch looks at
+    their order for all, and past what that looks at in one go."""
+    rng = np.random.default_rng(n)
+    cu = np.concatenate([[0], np.cumsum(rng.integers(0, 3, n))]).tolist()
+    T = cu[-1]
+    for i in rng.choice(n, 9, replace=False).tolist() + [n - 1]:
+        cu[i] = int(rng.integers(-1, T + 2))
+    run(cu, T, io, path=1, pre=1, H=9 if n < 100 else 40, N=16, seed=n)
