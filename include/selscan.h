@@ -552,10 +552,11 @@ typedef struct {
  * Sums and the state are fp32.  So are all factors, but for longer bf16 sequences, which take the
  * tensor cores: there B and Δ·x go into the state as sums of two bf16 (a state is off by some
  * 4e-6 of its norm), and C, S, x and the decays into y as one (y is off by 2e-3 of its norm, 1.7e-3
- * of which are its own rounding; by up to 5e-3 where one token's step outweighs all others').  Which
- * way a call takes follows from its sizes (sequences, tokens, H, P, G, N) and the device: the same
- * prompt may come out with other bits, within these errors, in another batch.  An infinite or NaN input reaches what the formulas take it to and nothing else
- * (there every output that should be infinite may be NaN).  Errors as ss_fwd.
+ * of which are its own rounding; by 3e-3 to 5e-3, in a head of few states alone up to 6e-3, where one
+ * token's step outweighs all others').  Which way a call takes follows from its sizes (sequences,
+ * tokens, H, P, G, N) and the device: the same prompt may come out with other bits, within these
+ * errors, in another batch.  An infinite or NaN input reaches what the formulas take it to and
+ * nothing else (there every output that should be infinite may be NaN).  Errors as ss_fwd.
  */
 ss_status ss_heads_fwd(const void* xbc, const void* dt_raw, const void* z, const float* conv_w,
                        const float* conv_b, const float* dt_bias, const float* A_log, const float* D,

@@ -16,7 +16,8 @@
 // segments, 1.7 times the recurrence's work); one of 32768 tokens, 24 heads of 64 x 128: 1605 us.  Eight prompts of
 // 512 tokens, 48 heads of 64 x 128: 274 us, the FMA pipe at 62%.  bf16, 4 prompts of 2048 tokens, 24 heads of 64 x 256,
 // which come here whatever their length: 1058 us (13 of traffic; 64 x 128 on the tensor cores 122).  One of 45 tokens,
-// 24 heads: 20 us, 24 CTAs on 152 SMs with one chain of 45 steps each.  bf16 prompts take the tensor cores (ss_heads_tc.cu) from where a cost rule there says so.
+// 24 heads: 20 us, 24 CTAs on 152 SMs with one chain of 45 steps each.  bf16 prompts take the tensor cores
+// (ss_heads_tc.cu) from where a cost rule there says so.
 // fp32 ones do not: operands of two bf16 (three products) leave 4e-6 of a state.  (Three parts and six products have
 // not been tried.)
 #include <cuda_runtime.h>

@@ -24,7 +24,8 @@
 // tokens to another, and to the chunk's end, these sums are taken over the steps themselves; within a block (P's
 // diagonal) as the difference of two running sums, whose steps are cut at 2^-128, where a decay is zero whatever else
 // it meets: the sums stay above -4096, whose ten roundings leave a decay behind strong steps off by less than 1e-3
-// (not cut, a single step of 1e5 leaves y off by 4e-2, one of 1e6 by 0.35).  P is zero above the diagonal, and zero times an infinity or NaN is NaN: such x are zeros in P·x, and their channel's
+// (not cut, a single step of 1e5 leaves y off by 4e-2, one of 1e6 by 0.35).
+// P is zero above the diagonal, and zero times an infinity or NaN is NaN: such x are zeros in P·x, and their channel's
 // outputs from that token on are set to NaN (as the recurrence leaves them) after it.
 //
 // What bounds it is the chain within a chunk (loads, convolution, products, P, products, outputs), with one
@@ -32,11 +33,11 @@
 // sequences of 8192 tokens, 80 heads of 64 x 128 states, bf16, gated: 770 us, 11.4 us a chunk and SM, at 42% of
 // the issue slots, 17% of the tensor pipe and 15% of the memory's peak (153 us are the copy rate's): no unit is full,
 // and global loads in the middle of the chain are the longest stall.  One document of 32768 tokens, 24 heads: 397 us
-// in two passes (47 at the copy rate).  Token by token (see
-// ss_heads_fwd.cu) the FMA pipe alone would take 1.7 and 0.5 ms.
-// Measured (against 715 to 735 us then) and not taken: one tile per product (N = 64), which shared memory's bandwidth bounds (940 us), a warp
-// for issuing alone (96 registers a thread, spills), x or z a chunk ahead in registers (841), waves of 2 or 8
-// chunks (no gain), equal ranges of chunks for every CTA (three times as long).
+// in two passes (47 at the copy rate).  Token by token (see ss_heads_fwd.cu) the FMA pipe alone would take 1.7 and
+// 0.5 ms.
+// Measured (against 715 to 735 us then) and not taken: one tile per product (N = 64), which shared memory's bandwidth
+// bounds (940 us), a warp for issuing alone (96 registers a thread, spills), x or z a chunk ahead in registers
+// (841), waves of 2 or 8 chunks (no gain), equal ranges of chunks for every CTA (three times as long).
 #include <cuda_runtime.h>
 
 #include <algorithm>
