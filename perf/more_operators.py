@@ -41,17 +41,18 @@ def listed():
         # the large model's training batch
         dict(name="conv of 4 x 8192", op="conv", batch=4, L=8192, Dm=5120, io="bf16", silu=True, window=False),
         # scoring one short text: the output embedding is read for few tokens
-        dict(name="loss of 45 tokens", op="xent", tokens=45, D=768, V=50257, io="bf16", grad=False),
+        dict(name="loss of 45 tokens", op="xent", tokens=45, D=768, V=50257, io="bf16", ignored=0.0, grad=False),
         # a training step of the small model in 32 bits
-        dict(name="step of 2048 tokens", op="xent", tokens=2048, D=768, V=50257, io="f32", grad=True),
-        # a training step on a large vocabulary: the largest call
-        dict(name="step of 4096 tokens", op="xent", tokens=4096, D=2048, V=128000, io="bf16", grad=True),
+        dict(name="step of 2048 tokens", op="xent", tokens=2048, D=768, V=50257, io="f32", ignored=0.0, grad=True),
+        # a fine-tuning step on a large vocabulary, the prompts' tokens without a target: the largest call
+        dict(name="step of 4096 tokens", op="xent", tokens=4096, D=2048, V=128000, io="bf16", ignored=0.15, grad=True),
         # scoring a long document, an odd number of tokens
-        dict(name="loss of 8191 tokens", op="xent", tokens=8191, D=2560, V=50257, io="bf16", grad=False),
+        dict(name="loss of 8191 tokens", op="xent", tokens=8191, D=2560, V=50257, io="bf16", ignored=0.0, grad=False),
         # a short answer distilled from a teacher's 16 likeliest tokens
-        dict(name="distill 37 tokens", op="distill", rows=37, V=50257, K=16, io="f32", temperature=1.0, grad=True),
-        # a training batch distilled on a large vocabulary
-        dict(name="distill 4096 tokens", op="distill", rows=4096, V=128000, K=64, io="bf16", temperature=2.0, grad=True),
+        dict(name="distill 37 tokens", op="distill", rows=37, V=50257, K=16, io="f32", temperature=1.0, empty=0.0, grad=True),
+        # a training batch distilled on a large vocabulary, the prompts' tokens without a teacher
+        dict(name="distill 4096 tokens", op="distill", rows=4096, V=128000, K=64, io="bf16", temperature=2.0, empty=0.1,
+             grad=True),
     ]
 
 
@@ -84,9 +85,17 @@ def draw(rng):
             D = -(-D // 64) * 64
         # 32 bits cost more: fewer tokens there
         most = 4096 * 2048 * 128000 // (D * V * (8 if io == "f32" else 1))
-        return dict(op=op, tokens=_log_int(rng, 1, min(8192, most)), D=D, V=V, io=io, grad=grad)
+        return dict(op=op, tokens=_log_int(rng, 1, min(8192, most)), D=D, V=V, io=io, ignored=rng.choice((0.0, 0.15, 0.5)),
+                    grad=grad)
     rows = _log_int(rng, 1, 2048 if io == "f32" else 4096)
-    return dict(op=op, rows=rows, V=V, K=_log_int(rng, 1, 128), io=io, temperature=rng.choice((1.0, 2.0, 4.0)), grad=grad)
+    return dict(op=op, rows=rows, V=V, K=_log_int(rng, 1, 128), io=io, temperature=rng.choice((1.0, 2.0, 4.0)),
+                empty=rng.choice((0.0, 0.1, 0.4)), grad=grad)
+
+
+def _trained(case):
+    """Rows that have a target (or a teacher): the others have a loss and gradients of zero."""
+    n = case["tokens"] if case["op"] == "xent" else case["rows"]
+    return n - int(n * case["ignored" if case["op"] == "xent" else "empty"])
 
 
 # ----------------------------------------------------------------------------------- the inputs
@@ -123,10 +132,10 @@ def prepare(case, seed):
         targets = torch.randint(V, (T,), generator=g, device="cuda")
         # rows that point toward their target's embedding, as a trained model's do
         hidden = (rn(T, D) + 3.0 * weight[targets].float()).to(io)
-        # prompt tokens are not trained on: every seventh or so
-        targets = torch.where(ru(T) < 0.15, -1, targets).to(torch.int32)
-        n = torch.clamp((targets >= 0).sum(), min=1).float()
-        s.update(hidden=hidden, weight=weight, targets=targets, dloss=torch.ones(T, device="cuda") / n)
+        without = torch.randperm(T, generator=g, device="cuda")[_trained(case):]
+        targets = targets.to(torch.int32)
+        targets[without] = -1
+        s.update(hidden=hidden, weight=weight, targets=targets, dloss=torch.full((T,), 1.0 / max(1, _trained(case)), device="cuda"))
         return s
     rows, V, K = case["rows"], case["V"], case["K"]
     logits = _by_rows(lambda n: (2.5 * rn(n, V)).to(io), rows, V)
@@ -134,12 +143,11 @@ def prepare(case, seed):
     step = max(1, (1 << 27) // V)
     top = [torch.topk(part.float() + rn(part.shape[0], V), K) for part in logits.split(step)]
     teacher, ids = torch.cat([t.values for t in top]), torch.cat([t.indices for t in top])
-    # some rows have fewer entries, some (prompt tokens) none
-    have = torch.where(ru(rows) < 0.2, (ru(rows) * (K + 1)).long(), K)
-    have = torch.where(ru(rows) < 0.1, 0, have)
+    # some rows have fewer entries, some none
+    have = torch.where(ru(rows) < 0.2, 1 + (ru(rows) * K).long().clamp(max=K - 1), K)
+    have[torch.randperm(rows, generator=g, device="cuda")[_trained(case):]] = 0
     ids = torch.where(torch.arange(K, device="cuda")[None] < have[:, None], ids, -1).to(torch.int32)
-    n = torch.clamp((have > 0).sum(), min=1).float()
-    s.update(logits=logits, ids=ids, teacher=teacher, dloss=torch.ones(rows, device="cuda") / n)
+    s.update(logits=logits, ids=ids, teacher=teacher, dloss=torch.full((rows,), 1.0 / max(1, _trained(case)), device="cuda"))
     return s
 
 
@@ -202,7 +210,7 @@ def _plain_xent(s):
     l = torch.exp(l - m)
     total = l.sum(-1, keepdim=True)
     lse = (m + torch.log(total))[:, 0]
-    out = dict(loss=torch.where(valid, lse - lt, 0.0), lse=lse)
+    out = dict(loss=torch.where(valid, lse - lt, 0.0), lse=torch.where(valid, lse, 0.0))
     if s["case"]["grad"]:
         l = l / total
         l.scatter_add_(1, at, torch.full_like(lse, -1.0)[:, None])
@@ -226,7 +234,7 @@ def _plain_distill(s):
     total = z.sum(-1, keepdim=True)
     lq = (zi - m) / T - torch.log(total)
     lp = (t - mt) / T - torch.log(torch.where(pt > 0, pt, 1.0))
-    out = dict(loss=torch.where(p > 0, p * (lp - lq), 0.0).sum(-1), stats=torch.cat([m, total], 1))
+    out = dict(loss=torch.where(p > 0, p * (lp - lq), 0.0).sum(-1), stats=torch.where(row[:, None], torch.cat([m, total], 1), 0.0))
     if s["case"]["grad"]:
         g = torch.where(row, s["dloss"], 0.0)[:, None] / T
         z = z / total
@@ -282,11 +290,12 @@ def work(case):
         window = 24 * case["batch"] * case["Dm"] if case["window"] else 0
         return dict(bytes=3 * n * es + 40 * case["Dm"] + window, flops=(34 if case["silu"] else 18) * n)
     if op == "xent":
-        T, D, V = case["tokens"], case["D"], case["V"]
-        both = 2 if case["grad"] else 1
-        return dict(bytes=both * es * D * (T + V) + 16 * T, flops=2 * T * D * V * (3 if case["grad"] else 1))
-    n = case["rows"] * case["V"]
-    return dict(bytes=n * es * (2 if case["grad"] else 1) + case["rows"] * (8 * case["K"] + 16), flops=n * (8 if case["grad"] else 4))
+        T, D, V, n = case["tokens"], case["D"], case["V"], _trained(case)
+        out = es * D * (T + V) if case["grad"] else 0
+        return dict(bytes=es * D * (n + V) + out + 16 * T, flops=2 * n * D * V * (3 if case["grad"] else 1))
+    n, V = _trained(case), case["V"]
+    out = es * V * case["rows"] if case["grad"] else 0
+    return dict(bytes=n * V * es + out + case["rows"] * (8 * case["K"] + 16), flops=n * V * (8 if case["grad"] else 4))
 
 
 # --------------------------------------------------------------------- the definitions in 64 bits
@@ -332,7 +341,7 @@ def exact(case, seed):
             h, w, t = _leaf(s["hidden"]), _leaf(s["weight"]), s["targets"].long()
             l = h @ w.t()
             loss = F.cross_entropy(l, t, ignore_index=-1, reduction="none")
-            out = dict(loss=loss.detach(), lse=torch.logsumexp(l.detach(), 1))
+            out = dict(loss=loss.detach(), lse=torch.logsumexp(l.detach(), 1) * (t >= 0))
             if case["grad"]:
                 dh, dw = torch.autograd.grad(loss, (h, w), s["dloss"].double())
                 out.update(dhidden=dh, dweight=dw)
@@ -348,7 +357,8 @@ def exact(case, seed):
             some = ids >= 0
             loss = torch.where(some, torch.where(some, lp.exp() * lp, 0.0) - torch.where(some, lp.exp(), 0.0) * lq, 0.0).sum(1)
             m = z.detach().amax(1)
-            part = [loss.detach(), torch.stack([m, torch.exp((z.detach() - m[:, None]) / T).sum(1)], 1)]
+            stats = torch.stack([m, torch.exp((z.detach() - m[:, None]) / T).sum(1)], 1)
+            part = [loss.detach(), stats * some.any(1)[:, None]]
             if case["grad"]:
                 part.append(torch.autograd.grad(loss, z, s["dloss"][i:i + step].double())[0])
             parts.append(part)
