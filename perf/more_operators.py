@@ -234,7 +234,7 @@ def _plain_distill(s):
     total = z.sum(-1, keepdim=True)
     lq = (zi - m) / T - torch.log(total)
     lp = (t - mt) / T - torch.log(torch.where(pt > 0, pt, 1.0))
-    out = dict(loss=torch.where(p > 0, p * (lp - lq), 0.0).sum(-1), stats=torch.where(row[:, None], torch.cat([m, total], 1), 0.0))
+    out = dict(loss=torch.where(p > 0, p * (lp - lq), 0.0).sum(-1))
     if s["case"]["grad"]:
         g = torch.where(row, s["dloss"], 0.0)[:, None] / T
         z = z / total
@@ -268,11 +268,10 @@ def run(s):
         if c["grad"]:
             out.update(ss.ss_linear_xent_bwd(s["dloss"], s["hidden"], s["weight"], s["targets"], lse))
         return out
-    loss, stats = ss.ss_distill(s["logits"], s["ids"], s["teacher"], temperature=c["temperature"])
-    out = dict(loss=loss, stats=stats)
     if c["grad"]:
-        out["dlogits"] = ss.ss_distill_bwd(s["dloss"], s["logits"], s["ids"], s["teacher"], stats, temperature=c["temperature"])
-    return out
+        loss, dlogits = ss.ss_distill_grad(s["dloss"], s["logits"], s["ids"], s["teacher"], temperature=c["temperature"])
+        return dict(loss=loss, dlogits=dlogits)
+    return dict(loss=ss.ss_distill(s["logits"], s["ids"], s["teacher"], temperature=c["temperature"]))
 
 
 # -------------------------------------------------------------------------- bytes and operations
@@ -356,10 +355,8 @@ def exact(case, seed):
             lq = torch.gather(torch.log_softmax(z / T, 1), 1, ids.clamp(min=0))
             some = ids >= 0
             loss = torch.where(some, torch.where(some, lp.exp() * lp, 0.0) - torch.where(some, lp.exp(), 0.0) * lq, 0.0).sum(1)
-            m = z.detach().amax(1)
-            stats = torch.stack([m, torch.exp((z.detach() - m[:, None]) / T).sum(1)], 1)
-            part = [loss.detach(), stats * some.any(1)[:, None]]
+            part = [loss.detach()]
             if case["grad"]:
                 part.append(torch.autograd.grad(loss, z, s["dloss"][i:i + step].double())[0])
             parts.append(part)
-        return dict(zip(("loss", "stats", "dlogits"), (torch.cat(p) for p in zip(*parts))))
+        return dict(zip(("loss", "dlogits"), (torch.cat(p) for p in zip(*parts))))
