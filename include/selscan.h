@@ -645,6 +645,123 @@ ss_status ss_sample(const void* logits, const float* noise, const float* tempera
                     const float* top_p, const float* min_p, int32_t* tokens, int64_t rows, int64_t V,
                     int32_t io_dtype, int64_t logits_r, int64_t noise_r, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Training a stack of layers around the scan's forward and backward calls: the residual layer norm
+ * with its backward pass (ss_add_layernorm, ss_add_layernorm_bwd), the backward pass of the
+ * convolution (ss_conv1d_bwd), and the losses over the vocabulary with their gradients: cross
+ * entropy from the last layer's rows (ss_linear_xent, ss_linear_xent_bwd) and distillation from a
+ * teacher's top logits (ss_distill, ss_distill_grad).  The pages have no counterpart but for the
+ * convolution.  Every workspace here is scratch: its contents need not be set before a call nor
+ * kept after it, and calls that run at the same time need one each.
+ * ------------------------------------------------------------------------------------------ */
+
+/*
+ * Residual addition and layer norm over rows of D columns:
+ *   r = x + residual (x alone if residual is NULL),  residual_out = r (rounded once to its type)
+ *   mean = Σ r / D,  rstd = 1 / sqrt(Σ (r - mean)² / D + eps)       (from the unrounded r, in fp32)
+ *   y = (r - mean) · rstd · weight + bias
+ *   residual_out may be residual itself (same stride) or NULL; outputs must not overlap otherwise.
+ *   weight [D], bias [D] or NULL (= 0): fp32.  mean, rstd [rows] fp32, what the backward pass reads;
+ *   each may be NULL.  Types and strides as ss_add_rmsnorm.  D in 1..SS_NORM_MAX.
+ */
+ss_status ss_add_layernorm(const void* x, const void* residual, const float* weight, const float* bias,
+                           void* residual_out, void* y, float* mean, float* rstd, int64_t rows,
+                           int64_t D, float eps, const ss_norm_strides* strides, void* stream);
+
+/* Element strides between rows of the norm's backward tensors (column stride 1) and their types. */
+typedef struct {
+    int32_t io_dtype;                       /* dy, dx */
+    int32_t res_dtype;                      /* r, dr, dresidual */
+    int64_t dy_r, dr_r, r_r, dx_r, dres_r;
+} ss_norm_grad_strides;
+
+/*
+ * Backward of ss_add_layernorm: with xh = (r - mean) · rstd and a = dy · weight,
+ *   d = rstd · (a - Σ a / D - xh · Σ (a · xh) / D) + dr,   dx = dresidual = d
+ *   dweight = Σ_rows dy · xh,  dbias = Σ_rows dy           [D] fp32
+ *   r                   the forward call's residual_out (or x, if that call had no residual)
+ *   dr                  gradient of residual_out from the layers behind, or NULL (= 0)
+ *   dx, dresidual       d in io_dtype and in res_dtype, each or NULL.  dresidual may be dr itself
+ *                       (same stride); outputs must not overlap otherwise
+ *   workspace           256-byte aligned, ss_add_layernorm_bwd_workspace_size(rows, D) bytes
+ * Deterministic.  rows == 0 sets dweight and dbias to zero.  strides NULL: fp32, contiguous.
+ */
+ss_status ss_add_layernorm_bwd(const void* dy, const void* dr, const void* r, const float* weight,
+                               const float* mean, const float* rstd, void* dx, void* dresidual,
+                               float* dweight, float* dbias, int64_t rows, int64_t D,
+                               const ss_norm_grad_strides* strides, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Workspace bytes ss_add_layernorm_bwd needs on the current device (0: sizes invalid or empty). */
+size_t ss_add_layernorm_bwd_workspace_size(int64_t rows, int64_t D);
+
+/* Element strides of the convolution's backward tensors ([batch, L, Dm], channel stride 1). */
+typedef struct {
+    int32_t io_dtype;
+    int64_t dout_b, dout_l, x_b, x_l, dx_b, dx_l;
+} ss_conv_grad_strides;
+
+/*
+ * Backward of ss_conv1d: with e = window_in ++ x, v_t = bias + Σ_k weight_k · e_{t+k} and
+ * g_t = dout_t · silu'(v_t) (dout_t without SiLU),
+ *   de_j = Σ_k weight_k · g_{j-k}:  dx_t = de_{t+3},  dwindow_in = de_0..2
+ *   dweight[d,k] = Σ_{b,t} g_t · e_{t+k}  [Dm,4],   dbias = Σ_{b,t} g_t  [Dm]      (fp32)
+ *   x, weight, bias, window_in, silu    as in the forward call
+ *   dwindow_out         [batch, Dm, 3] fp32, gradient of the window the forward call left, or NULL
+ *   dwindow_in          [batch, Dm, 3] fp32 or NULL (not wanted)
+ *   workspace           256-byte aligned, ss_conv1d_bwd_workspace_size(batch, L, Dm) bytes
+ * Outputs must not overlap each other nor any input.  Deterministic.  Sums are fp32.  batch == 0 or L == 0 sets
+ * dweight and dbias to zero (and dwindow_in to dwindow_out).  strides NULL: fp32, contiguous.
+ */
+ss_status ss_conv1d_bwd(const void* dout, const void* x, const float* weight, const float* bias,
+                        const float* window_in, const float* dwindow_out, void* dx, float* dweight,
+                        float* dbias, float* dwindow_in, int64_t batch, int64_t L, int64_t Dm,
+                        int32_t silu, const ss_conv_grad_strides* strides, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Workspace bytes ss_conv1d_bwd needs on the current device (0: sizes invalid or empty). */
+size_t ss_conv1d_bwd_workspace_size(int64_t batch, int64_t L, int64_t Dm);
+
+/* Largest vocabulary and most entries per row of the distillation calls. */
+#define SS_DISTILL_MAX_V (1 << 24)
+#define SS_DISTILL_MAX_K 1024
+
+/* Element strides between rows of the distillation tensors (inner stride 1) and their types. */
+typedef struct {
+    int32_t io_dtype;                       /* logits, dlogits */
+    int32_t teacher_dtype;
+    int64_t logits_r, ids_r, teacher_r, dlogits_r, dloss_r;
+} ss_distill_strides;
+
+/*
+ * Divergence from a teacher's distribution over its top logits, per row:
+ *   p = softmax(teacher / temperature) over the row's K entries,
+ *   q = softmax(logits / temperature) over the V columns,
+ *   loss = Σ_k p_k · (log p_k - log q[ids_k])
+ *   logits [rows, V] io_dtype;  ids [rows, K] int32, teacher [rows, K] teacher_dtype;  loss [rows] fp32
+ *   A negative id: no entry there (a row with fewer than K).  An id of V or more sets bit 2 of the
+ *   device error word and is no entry either.  An entry of -inf has no weight.  Entries may name a
+ *   column twice: their p add up.  A row without weight has a loss of 0 and its logits are not read.
+ *   A row with a NaN, or with a logit or entry of +inf, or with logits of -inf alone, has a NaN loss; a
+ *   logit of -inf under an entry of some weight an infinite one.
+ *   V in 1..SS_DISTILL_MAX_V, K in 0..SS_DISTILL_MAX_K, temperature > 0 and finite.  Sums are fp32.
+ */
+ss_status ss_distill(const void* logits, const int32_t* ids, const void* teacher, float* loss,
+                     int64_t rows, int64_t V, int64_t K, float temperature,
+                     const ss_distill_strides* strides, void* stream);
+
+/*
+ * ss_distill and the gradient of the logits in one call, for given gradients dloss [rows] fp32 of the
+ * losses (row stride dloss_r, 0 for one value):
+ *   dlogits[v] = dloss / temperature · (q_v - Σ_{k: ids_k = v} p_k)       [rows, V] io_dtype
+ * dlogits may be logits itself (same stride).  A row without weight has gradients of zero, whatever its
+ * dloss.  Outputs must not overlap anything else.  Deterministic.
+ */
+ss_status ss_distill_grad(const float* dloss, const void* logits, const int32_t* ids,
+                          const void* teacher, float* loss, void* dlogits, int64_t rows, int64_t V,
+                          int64_t K, float temperature, const ss_distill_strides* strides,
+                          void* stream);
+
 /* Static, human-readable name of a status code. */
 const char* ss_status_string(ss_status status);
 

@@ -16,7 +16,9 @@ from . import _build
 __all__ = ["ss_fwd", "ss_fwd_ckpt", "ss_fwd_dtproj", "ss_fwd_host", "ss_step", "ss_step_layers", "ss_fwd_summary", "ss_carry_compose", "ss_conv1d", "ss_bwd", "ss_fwd_workspace_size", "SelscanError", "lib", "device_error",
            "version", "status_string", "SS_F32", "SS_BF16", "FwdStrides", "StepStrides", "ConvStrides",
            "ss_heads_fwd", "ss_heads_step", "ss_add_rmsnorm", "ss_add_rmsnorm_f8", "ss_sample", "HeadsStrides",
-           "NormStrides"]
+           "NormStrides",
+           "ss_add_layernorm", "ss_add_layernorm_bwd", "ss_conv1d_bwd", "ss_distill", "ss_distill_grad", "NormGradStrides",
+           "ConvGradStrides", "DistillStrides"]
 
 SS_F32, SS_BF16 = 0, 1
 _STATUS = {0: "SS_OK", 1: "SS_ERR_INVALID_ARG", 2: "SS_ERR_UNSUPPORTED", 3: "SS_ERR_MISALIGNED",
@@ -50,6 +52,20 @@ class HeadsStrides(ctypes.Structure):
 class NormStrides(ctypes.Structure):
     _fields_ = [("io_dtype", ctypes.c_int32), ("res_dtype", ctypes.c_int32)] + [
         (n, ctypes.c_int64) for n in ("x_r", "res_r", "res_out_r", "y_r")]
+
+
+class NormGradStrides(ctypes.Structure):
+    _fields_ = [("io_dtype", ctypes.c_int32), ("res_dtype", ctypes.c_int32)] + [
+        (n, ctypes.c_int64) for n in ("dy_r", "dr_r", "r_r", "dx_r", "dres_r")]
+
+
+class ConvGradStrides(ctypes.Structure):
+    _fields_ = [("io_dtype", ctypes.c_int32)] + [(n, ctypes.c_int64) for n in ("dout_b", "dout_l", "x_b", "x_l", "dx_b", "dx_l")]
+
+
+class DistillStrides(ctypes.Structure):
+    _fields_ = [("io_dtype", ctypes.c_int32), ("teacher_dtype", ctypes.c_int32)] + [
+        (n, ctypes.c_int64) for n in ("logits_r", "ids_r", "teacher_r", "dlogits_r", "dloss_r")]
 
 
 _LIB = None
@@ -110,6 +126,20 @@ def lib() -> ctypes.CDLL:
         L.ss_add_rmsnorm_f8.restype = ctypes.c_int
         L.ss_sample.argtypes = [vp] * 7 + [i64] * 2 + [ctypes.c_int32, i64, i64, vp]
         L.ss_sample.restype = ctypes.c_int
+        L.ss_add_layernorm.argtypes = [vp] * 8 + [i64] * 2 + [ctypes.c_float, ctypes.POINTER(NormStrides), vp]
+        L.ss_add_layernorm.restype = ctypes.c_int
+        L.ss_add_layernorm_bwd.argtypes = [vp] * 10 + [i64] * 2 + [ctypes.POINTER(NormGradStrides), vp, ctypes.c_size_t, vp]
+        L.ss_add_layernorm_bwd.restype = ctypes.c_int
+        L.ss_add_layernorm_bwd_workspace_size.argtypes = [i64] * 2
+        L.ss_add_layernorm_bwd_workspace_size.restype = ctypes.c_size_t
+        L.ss_conv1d_bwd.argtypes = [vp] * 10 + [i64] * 3 + [ctypes.c_int32, ctypes.POINTER(ConvGradStrides), vp, ctypes.c_size_t, vp]
+        L.ss_conv1d_bwd.restype = ctypes.c_int
+        L.ss_conv1d_bwd_workspace_size.argtypes = [i64] * 3
+        L.ss_conv1d_bwd_workspace_size.restype = ctypes.c_size_t
+        L.ss_distill.argtypes = [vp] * 4 + [i64] * 3 + [ctypes.c_float, ctypes.POINTER(DistillStrides), vp]
+        L.ss_distill.restype = ctypes.c_int
+        L.ss_distill_grad.argtypes = [vp] * 6 + [i64] * 3 + [ctypes.c_float, ctypes.POINTER(DistillStrides), vp]
+        L.ss_distill_grad.restype = ctypes.c_int
         L.ss__capture_id.argtypes = [vp]
         L.ss__capture_id.restype = ctypes.c_uint64
         L.ss_status_string.argtypes = [ctypes.c_int]
@@ -541,3 +571,4 @@ def ss_bwd(dy, u, delta_raw, delta_bias, A_log, B, C, D=None, z=None, h0=None, d
 
 
 from .serving import ss_add_rmsnorm, ss_add_rmsnorm_f8, ss_heads_fwd, ss_heads_step, ss_sample  # noqa: E402
+from .training import ss_add_layernorm, ss_add_layernorm_bwd, ss_conv1d_bwd, ss_distill, ss_distill_grad  # noqa: E402

@@ -1,0 +1,405 @@
+// Divergence from a teacher's distribution over its top logits, and its gradient.  Per row, with student logits
+// z [V], teacher logits t_k at ids_k (k < K) and a temperature τ:
+//   p = softmax_k(t / τ),  q = softmax_v(z / τ),  loss = Σ_k p_k (log p_k - log q_{ids_k})
+//   dz_v = dloss / τ · (q_v - Σ_{k: ids_k = v} p_k)
+//
+// The vocabulary is the traffic: a row is read once for the running maximum and sum, and, for the gradient, again
+// from L2 as soon as both are known, by the CTAs that have just read it (a cluster for a row where there are few
+// rows or where the rows at work would not stay in L2).  An entry's K values lie in shared memory; their
+// columns get their gradient after the row's stream, rounded once, duplicates summed.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/selscan.h"
+#include "device_common.cuh"
+#include "heads_device.cuh"
+#include "host_util.h"
+#include "internal.h"
+
+namespace selscan {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxK = SS_DISTILL_MAX_K;
+constexpr int kPer = kMaxK / kThreads;             // entries of a thread at most
+constexpr int kMaxCluster = 8;
+
+struct DistillParams {
+    const void* logits;
+    const int32_t* ids;
+    const void* teacher;
+    const float* dloss;
+    float* loss;
+    void* dlogits;
+    int64_t logits_r, ids_r, teacher_r, dlogits_r, dloss_r;
+    int64_t rows;
+    int V, K, slice;                               // slice: columns of a CTA (a multiple of 8)
+    bool teacher_bf16;
+    float inv_t;                                   // 1 / τ
+    unsigned int* err;
+};
+
+struct DistillShared {
+    float p[kMaxK], z[kMaxK], t[kMaxK];
+    int32_t id[kMaxK];
+    float part[2][kWarps];
+    float2 stat[kWarps];
+    float2 mine;                                   // (max, sum) of this CTA's slice: read by the cluster's others
+};
+
+template <typename T> struct Vec16;                // 16 bytes of a row
+template <> struct Vec16<float> {
+    static constexpr int n = 4;
+    static __device__ __forceinline__ void get(const uint4& u, float (&v)[4]) {
+        v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y); v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
+    }
+    static __device__ __forceinline__ uint4 put(const float (&v)[4]) {
+        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    }
+};
+template <> struct Vec16<__nv_bfloat16> {
+    static constexpr int n = 8;
+    static __device__ __forceinline__ void get(const uint4& u, float (&v)[8]) {
+        const uint32_t a[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(a[i] << 16);
+            v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 put(const float (&v)[8]) {
+        uint32_t a[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            a[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        return make_uint4(a[0], a[1], a[2], a[3]);
+    }
+};
+
+// A running maximum m and the sum s of exp2((z - m) c).
+struct Running {
+    float m = -INFINITY, s = 0.f;
+    // (-inf as the maximum so far: nothing but -inf seen, whose weights are zero)
+    static __device__ __forceinline__ float base(float m) { return m == -INFINITY ? 0.f : m; }
+    template <int N> __device__ __forceinline__ void take(const float (&v)[N], float c) {
+        float b = v[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i) b = fmaxf(b, v[i]);
+        if (b > m) {
+            s *= ex2((m - b) * c);
+            m = b;
+        }
+        const float2 off = splat2(-base(m)), c2 = splat2(c);
+        float2 a = splat2(0.f);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) a = add2(a, ex2x2(mul2(add2(make_float2(v[i], v[i + 1]), off), c2)));
+        s += a.x + a.y;
+    }
+    __device__ __forceinline__ void one(float v, float c) {
+        if (v > m) {
+            s *= ex2((m - v) * c);
+            m = v;
+        }
+        s += ex2((v - base(m)) * c);
+    }
+    __device__ __forceinline__ void join(float m2, float s2, float c) {
+        const float n = fmaxf(m, m2), b = base(n);
+        s = s * ex2((m - b) * c) + s2 * ex2((m2 - b) * c);
+        m = n;
+    }
+};
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+// The sum (MAX: maximum) over the block in every thread; `slot` is this use's place in shared memory.
+template <bool MAX>
+__device__ __forceinline__ float block_all(float v, float* slot) {
+    v = MAX ? warp_max(v) : warp_sum(v);
+    if (threadIdx.x % 32 == 0) slot[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = slot[threadIdx.x % kWarps];
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o /= 2) {
+        const float w = __shfl_xor_sync(0xffffffffu, v, o);
+        v = MAX ? fmaxf(v, w) : v + w;
+    }
+    return v;
+}
+
+template <typename T, bool GRAD>
+__global__ void __launch_bounds__(kThreads) distill_kernel(const DistillParams p) {
+    constexpr int N = Vec16<T>::n, U = 4;
+    __shared__ DistillShared sh;
+    uint32_t rank = 0, size = 1;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
+    const int tid = threadIdx.x;
+    // the last rows first: in a row of calls these are what L2 still holds
+    const int64_t row = p.rows - 1 - blockIdx.x / size;
+    const T* z = static_cast<const T*>(p.logits) + row * p.logits_r;
+    const int32_t* ids = p.ids + row * p.ids_r;
+    const float c = kLog2e * p.inv_t;
+
+    // the teacher's entries, in every CTA of the row
+    float mt = -INFINITY;
+    for (int k = tid; k < p.K; k += kThreads) {
+        const int id = ids[k];
+        const bool ok = id >= 0 && id < p.V;
+        if (id >= p.V && rank == 0 && p.err) atomicOr(p.err, kErrIndex);
+        float t = -INFINITY;
+        if (ok)
+            t = p.teacher_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.teacher)[row * p.teacher_r + k])
+                               : static_cast<const float*>(p.teacher)[row * p.teacher_r + k];
+        sh.t[k] = t;
+        sh.id[k] = ok ? id : -1;
+        sh.z[k] = ok ? to_f32<T>(z[id]) : 0.f;
+        mt = fmaxf(mt, t);
+    }
+    mt = Running::base(block_all<true>(mt, sh.part[0]));
+    float pt = 0.f;
+    for (int k = tid; k < p.K; k += kThreads) {
+        const float e = ex2((sh.t[k] - mt) * c);   // (0 for an entry that is not there)
+        sh.p[k] = e;
+        pt += e;
+    }
+    pt = block_all<false>(pt, sh.part[1]);
+    const bool some = pt != 0.f;                   // (NaN: a row with a NaN)
+    const float inv_pt = some ? 1.f / pt : 0.f;
+
+    const int lo = static_cast<int>(rank) * p.slice, hi = min(lo + p.slice, p.V);
+    // columns up to the first 16-byte boundary, whole vectors, and what is left
+    const int head = min(hi, lo + static_cast<int>(((16 - reinterpret_cast<uintptr_t>(z + lo) % 16) % 16) / sizeof(T)));
+    const int vecs = hi > head ? (hi - head) / N : 0, tail = head + vecs * N;
+    const uint4* zv = reinterpret_cast<const uint4*>(z + head);
+
+    Running r;
+    if (some) {
+        for (int i = tid; i < vecs; i += kThreads * U) {
+            uint4 u[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (i + j * kThreads < vecs) u[j] = zv[i + j * kThreads];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                if (i + j * kThreads >= vecs) break;
+                float v[N];
+                Vec16<T>::get(u[j], v);
+                r.take(v, c);
+            }
+        }
+        if (lo + tid < head) r.one(to_f32<T>(z[lo + tid]), c);
+        if (tail + tid < hi) r.one(to_f32<T>(z[tail + tid]), c);
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) r.join(__shfl_xor_sync(0xffffffffu, r.m, o), __shfl_xor_sync(0xffffffffu, r.s, o), c);
+        if (tid % 32 == 0) sh.stat[tid / 32] = make_float2(r.m, r.s);
+    }
+    __syncthreads();
+    if (some) {
+        const float2 q = sh.stat[tid % kWarps];
+        r.m = q.x;
+        r.s = q.y;
+#pragma unroll
+        for (int o = kWarps / 2; o > 0; o /= 2) r.join(__shfl_xor_sync(0xffffffffu, r.m, o), __shfl_xor_sync(0xffffffffu, r.s, o), c);
+        if (tid == 0) sh.mine = make_float2(r.m, r.s);
+    }
+    if (size > 1) {
+        cluster_sync_all();
+        if (some) {
+            Running all;
+            for (uint32_t k = 0; k < size; ++k) {
+                const uint32_t a = peer_smem_addr(&sh.mine, k);
+                all.join(ld_peer_f32(a), ld_peer_f32(a + 4), c);
+            }
+            r = all;
+        }
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");    // (waited for at the end)
+    }
+    const float m = Running::base(r.m), inv_s = 1.f / r.s;
+
+    if (rank == 0) {
+        float sum = 0.f;
+        if (some)
+            for (int k = tid; k < p.K; k += kThreads) {
+                const float w = sh.p[k] * inv_pt;
+                if (w != 0.f) sum += w * ((sh.t[k] - mt) - (sh.z[k] - m)) * p.inv_t;
+            }
+        sum = block_all<false>(sum, sh.part[0]);
+        if (tid == 0) p.loss[row] = some ? sum + (logf(r.s) - logf(pt)) : 0.f;
+    }
+    if constexpr (GRAD) {
+        T* d = static_cast<T*>(p.dlogits) + row * p.dlogits_r;
+        const float g = some ? p.dloss[row * p.dloss_r] * p.inv_t : 0.f;
+        // the entries' own columns in this slice: the first of equal ones has them all
+        float val[kPer];
+        int col[kPer];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const int k = tid + j * kThreads, id = k < p.K ? sh.id[k] : -1;
+            col[j] = -1;
+            if (!some || id < lo || id >= hi) continue;
+            float w = 0.f;
+            bool first = true;
+            for (int i = 0; i < p.K; ++i)
+                if (sh.id[i] == id) {
+                    first = first && i >= k;
+                    w += sh.p[i];
+                }
+            if (!first) continue;
+            col[j] = id;
+            val[j] = g * (ex2((sh.z[k] - m) * c) * inv_s - w * inv_pt);
+        }
+        const float gs = g * inv_s;
+        const float2 off = splat2(-m), c2 = splat2(c), gs2 = splat2(gs);
+        auto grad = [&](float v) { return some ? ex2((v - m) * c) * gs : 0.f; };
+        // (a row of dlogits that lies otherwise against the 16 bytes is written element by element)
+        const bool same = reinterpret_cast<uintptr_t>(d + head) % 16 == 0;
+        for (int i = tid; i < vecs; i += kThreads * U) {
+            uint4 u[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (i + j * kThreads < vecs && some) u[j] = __ldcs(zv + i + j * kThreads);
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int at = i + j * kThreads;
+                if (at >= vecs) break;
+                float v[N];
+                if (some) {
+                    Vec16<T>::get(u[j], v);
+#pragma unroll
+                    for (int e = 0; e < N; e += 2) {
+                        const float2 o = mul2(ex2x2(mul2(add2(make_float2(v[e], v[e + 1]), off), c2)), gs2);
+                        v[e] = o.x;
+                        v[e + 1] = o.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < N; ++e) v[e] = 0.f;
+                }
+                if (same) {
+                    __stcs(reinterpret_cast<uint4*>(d + head) + at, Vec16<T>::put(v));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < N; ++e) d[head + at * N + e] = from_f32<T>(v[e]);
+                }
+            }
+        }
+        if (lo + tid < head) d[lo + tid] = from_f32<T>(grad(some ? to_f32<T>(z[lo + tid]) : 0.f));
+        if (tail + tid < hi) d[tail + tid] = from_f32<T>(grad(some ? to_f32<T>(z[tail + tid]) : 0.f));
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            if (col[j] >= 0) d[col[j]] = from_f32<T>(val[j]);
+    }
+    if (size > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// CTAs for a row.  Enough to fill the SMs where rows are few, as long as each keeps some 16 KB; for the
+// gradient also enough that the rows at work (4 CTAs to an SM) stay in half of L2.
+constexpr int64_t kL2Rows = 64 << 20;
+int cluster_of(int64_t rows, int64_t row_bytes, int sms, bool grad) {
+    int n = 1;
+    while (n < kMaxCluster && rows * n < 3 * static_cast<int64_t>(sms) && row_bytes / (2 * n) >= 16384) n *= 2;
+    if (grad)
+        while (n < kMaxCluster && 4 * static_cast<int64_t>(sms) / n * row_bytes > kL2Rows) n *= 2;
+    return n;
+}
+
+using host::dev_ptr;
+using host::is_aligned;
+using host::meet;
+using host::Range;
+using host::range3;
+
+template <typename T, bool GRAD>
+cudaError_t launch(const DistillParams& p, int cluster, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.rows * cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, distill_kernel<T, GRAD>, p);
+}
+
+ss_status distill(const float* dloss, const void* logits, const int32_t* ids, const void* teacher, float* loss, void* dlogits, bool grad,
+                  int64_t rows, int64_t V, int64_t K, float temperature, const ss_distill_strides* strides, void* stream) {
+    if (rows < 0 || V < 1 || K < 0 || !(temperature > 0.f) || !(temperature < INFINITY)) return SS_ERR_INVALID_ARG;
+    if (V > SS_DISTILL_MAX_V || K > SS_DISTILL_MAX_K || rows > INT32_MAX / kMaxCluster) return SS_ERR_UNSUPPORTED;
+    ss_distill_strides s;
+    if (strides) {
+        s = *strides;
+    } else {
+        std::memset(&s, 0, sizeof(s));
+        s.io_dtype = s.teacher_dtype = SS_F32;
+        s.logits_r = s.dlogits_r = V;
+        s.ids_r = s.teacher_r = K;
+        s.dloss_r = 1;
+    }
+    if ((s.io_dtype != SS_F32 && s.io_dtype != SS_BF16) || (s.teacher_dtype != SS_F32 && s.teacher_dtype != SS_BF16)) return SS_ERR_INVALID_ARG;
+    if (rows == 0) return SS_OK;
+    if (!logits || !loss || (K > 0 && (!ids || !teacher)) || (grad && (!dloss || !dlogits))) return SS_ERR_INVALID_ARG;
+    if (s.logits_r < 0 || s.ids_r < 0 || s.teacher_r < 0 || (grad && s.dloss_r < 0)) return SS_ERR_INVALID_ARG;
+    if (grad && rows > 1 && s.dlogits_r < V) return SS_ERR_INVALID_ARG;
+    const int64_t es = s.io_dtype == SS_BF16 ? 2 : 4, te = s.teacher_dtype == SS_BF16 ? 2 : 4;
+    if (!is_aligned(logits, es) || !is_aligned(loss, 4) || (K > 0 && (!is_aligned(ids, 4) || !is_aligned(teacher, te))) ||
+        (grad && (!is_aligned(dloss, 4) || !is_aligned(dlogits, es))))
+        return SS_ERR_MISALIGNED;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return SS_ERR_CUDA;
+    const void* all[] = {logits, K > 0 ? ids : nullptr, K > 0 ? teacher : nullptr, loss, grad ? dloss : nullptr, grad ? dlogits : nullptr};
+    for (const void* q : all)
+        if (q && !dev_ptr(q, dev)) return SS_ERR_INVALID_ARG;
+    const Range rl = range3(logits, 1, rows, V, 0, s.logits_r, es), ri = range3(ids, 1, rows, K, 0, s.ids_r, 4),
+                rt = range3(teacher, 1, rows, K, 0, s.teacher_r, te), ro = range3(loss, 1, 1, rows, 0, 0, 4),
+                rg = range3(grad ? dloss : nullptr, 1, rows, 1, 0, s.dloss_r, 4), rd = range3(grad ? dlogits : nullptr, 1, rows, V, 0, s.dlogits_r, es);
+    if (meet(ro, rl) || meet(ro, ri) || meet(ro, rt) || meet(ro, rg) || meet(ro, rd)) return SS_ERR_INVALID_ARG;
+    if (meet(rd, ri) || meet(rd, rt) || meet(rd, rg)) return SS_ERR_INVALID_ARG;
+    if (meet(rd, rl) && !(dlogits == logits && (s.dlogits_r == s.logits_r || rows == 1))) return SS_ERR_INVALID_ARG;
+
+    DistillParams p;
+    p.logits = logits; p.ids = ids; p.teacher = teacher; p.dloss = dloss; p.loss = loss; p.dlogits = dlogits;
+    p.logits_r = s.logits_r; p.ids_r = s.ids_r; p.teacher_r = s.teacher_r; p.dlogits_r = s.dlogits_r; p.dloss_r = s.dloss_r;
+    p.rows = rows; p.V = static_cast<int>(V); p.K = static_cast<int>(K);
+    p.teacher_bf16 = s.teacher_dtype == SS_BF16;
+    p.inv_t = 1.f / temperature;
+    p.err = device_error_word();
+    const int cluster = cluster_of(rows, V * es, sms, grad);
+    p.slice = static_cast<int>(((V + cluster - 1) / cluster + 7) / 8 * 8);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool b = s.io_dtype == SS_BF16;
+    const cudaError_t e = grad ? (b ? launch<__nv_bfloat16, true>(p, cluster, st) : launch<float, true>(p, cluster, st))
+                               : (b ? launch<__nv_bfloat16, false>(p, cluster, st) : launch<float, false>(p, cluster, st));
+    return e == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace selscan
+
+extern "C" ss_status ss_distill(const void* logits, const int32_t* ids, const void* teacher, float* loss, int64_t rows, int64_t V,
+                                int64_t K, float temperature, const ss_distill_strides* strides, void* stream) {
+    return selscan::distill(nullptr, logits, ids, teacher, loss, nullptr, false, rows, V, K, temperature, strides, stream);
+}
+
+extern "C" ss_status ss_distill_grad(const float* dloss, const void* logits, const int32_t* ids, const void* teacher, float* loss,
+                                     void* dlogits, int64_t rows, int64_t V, int64_t K, float temperature,
+                                     const ss_distill_strides* strides, void* stream) {
+    return selscan::distill(dloss, logits, ids, teacher, loss, dlogits, true, rows, V, K, temperature, strides, stream);
+}
