@@ -722,6 +722,55 @@ ss_status ss_conv1d_bwd(const void* dout, const void* x, const float* weight, co
 /* Workspace bytes ss_conv1d_bwd needs on the current device (0: sizes invalid or empty). */
 size_t ss_conv1d_bwd_workspace_size(int64_t batch, int64_t L, int64_t Dm);
 
+/* Most tokens, largest vocabulary and width of the cross entropy calls. */
+#define SS_XENT_MAX_TOKENS (1 << 22)
+#define SS_XENT_MAX_V (1 << 22)
+#define SS_XENT_MAX_D (1 << 16)
+
+/* Element strides between rows of the cross entropy's tensors (column stride 1) and their type. */
+typedef struct {
+    int32_t io_dtype;                       /* hidden, weight, dhidden, dweight */
+    int64_t hidden_t, weight_v, dhidden_t, dweight_v, dloss_t;
+} ss_xent_strides;
+
+/*
+ * Softmax cross entropy over the vocabulary from the last layer's rows, without keeping the logits:
+ *   l_v = Σ_d hidden[t,d] · weight[v,d],   lse[t] = log Σ_v exp(l_v),   loss[t] = lse[t] - l_{targets[t]}
+ *   hidden [tokens, D], weight [V, D] io_dtype (the output embedding);  targets [tokens] int32
+ *   loss, lse           [tokens] fp32.  A row with a negative target has none: its loss and lse are 0 and its
+ *                       hidden values are not read.  A target of V or more sets bit 2 of the device error
+ *                       word and is none either.
+ *   workspace           256-byte aligned, ss_linear_xent_workspace_size(tokens, V, D, io_dtype, 0) bytes
+ * Sums are fp32.  Products take bf16 operands as they are and fp32 ones as sums of three bf16, which are 24
+ * bits together.  A row with a NaN or an infinity has a NaN or infinite loss, without effect on others.
+ * tokens, V and D up to SS_XENT_MAX_*.  strides NULL: fp32, contiguous.
+ */
+ss_status ss_linear_xent(const void* hidden, const void* weight, const int32_t* targets, float* loss,
+                         float* lse, int64_t tokens, int64_t V, int64_t D,
+                         const ss_xent_strides* strides, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/*
+ * Its gradients for given gradients dloss [tokens] fp32 of the losses (stride dloss_t, 0 for one value):
+ *   dl_v = (exp(l_v - lse) - [v = target]) · dloss,   dhidden = Σ_v dl_v · weight[v]  [tokens, D],
+ *   dweight[v] = Σ_t dl_v · hidden[t]  [V, D]           (io_dtype, from sums in fp32)
+ *   lse                 from the forward call on the same hidden, weight and targets
+ *   workspace           256-byte aligned, ss_linear_xent_workspace_size(tokens, V, D, io_dtype, 1) bytes
+ * Rows without a target have a dhidden of zero and no part in dweight, whatever their hidden, lse and dloss.
+ * The logits are computed again, a piece of the vocabulary at a time; dl is an operand in bf16 for bf16
+ * tensors (half a step, 2^-9 of its value) and in three for fp32 ones.  Deterministic.  tokens == 0 sets
+ * dweight to zero.  Outputs must not overlap anything else.
+ */
+ss_status ss_linear_xent_bwd(const float* dloss, const void* hidden, const void* weight,
+                             const int32_t* targets, const float* lse, void* dhidden, void* dweight,
+                             int64_t tokens, int64_t V, int64_t D, const ss_xent_strides* strides,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of ss_linear_xent (backward 0) or ss_linear_xent_bwd (1) on the current device (0: sizes
+ * invalid or empty). */
+size_t ss_linear_xent_workspace_size(int64_t tokens, int64_t V, int64_t D, int32_t io_dtype,
+                                     int32_t backward);
+
 /* Largest vocabulary and most entries per row of the distillation calls. */
 #define SS_DISTILL_MAX_V (1 << 24)
 #define SS_DISTILL_MAX_K 1024

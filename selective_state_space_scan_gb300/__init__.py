@@ -18,7 +18,7 @@ __all__ = ["ss_fwd", "ss_fwd_ckpt", "ss_fwd_dtproj", "ss_fwd_host", "ss_step", "
            "ss_heads_fwd", "ss_heads_step", "ss_add_rmsnorm", "ss_add_rmsnorm_f8", "ss_sample", "HeadsStrides",
            "NormStrides",
            "ss_add_layernorm", "ss_add_layernorm_bwd", "ss_conv1d_bwd", "ss_distill", "ss_distill_grad", "NormGradStrides",
-           "ConvGradStrides", "DistillStrides"]
+           "ConvGradStrides", "DistillStrides", "ss_linear_xent", "ss_linear_xent_bwd", "XentStrides"]
 
 SS_F32, SS_BF16 = 0, 1
 _STATUS = {0: "SS_OK", 1: "SS_ERR_INVALID_ARG", 2: "SS_ERR_UNSUPPORTED", 3: "SS_ERR_MISALIGNED",
@@ -61,6 +61,10 @@ class NormGradStrides(ctypes.Structure):
 
 class ConvGradStrides(ctypes.Structure):
     _fields_ = [("io_dtype", ctypes.c_int32)] + [(n, ctypes.c_int64) for n in ("dout_b", "dout_l", "x_b", "x_l", "dx_b", "dx_l")]
+
+
+class XentStrides(ctypes.Structure):
+    _fields_ = [("io_dtype", ctypes.c_int32)] + [(n, ctypes.c_int64) for n in ("hidden_t", "weight_v", "dhidden_t", "dweight_v", "dloss_t")]
 
 
 class DistillStrides(ctypes.Structure):
@@ -140,6 +144,12 @@ def lib() -> ctypes.CDLL:
         L.ss_distill.restype = ctypes.c_int
         L.ss_distill_grad.argtypes = [vp] * 6 + [i64] * 3 + [ctypes.c_float, ctypes.POINTER(DistillStrides), vp]
         L.ss_distill_grad.restype = ctypes.c_int
+        L.ss_linear_xent.argtypes = [vp] * 5 + [i64] * 3 + [ctypes.POINTER(XentStrides), vp, ctypes.c_size_t, vp]
+        L.ss_linear_xent.restype = ctypes.c_int
+        L.ss_linear_xent_bwd.argtypes = [vp] * 7 + [i64] * 3 + [ctypes.POINTER(XentStrides), vp, ctypes.c_size_t, vp]
+        L.ss_linear_xent_bwd.restype = ctypes.c_int
+        L.ss_linear_xent_workspace_size.argtypes = [i64] * 3 + [ctypes.c_int32] * 2
+        L.ss_linear_xent_workspace_size.restype = ctypes.c_size_t
         L.ss__capture_id.argtypes = [vp]
         L.ss__capture_id.restype = ctypes.c_uint64
         L.ss_status_string.argtypes = [ctypes.c_int]
@@ -571,4 +581,5 @@ def ss_bwd(dy, u, delta_raw, delta_bias, A_log, B, C, D=None, z=None, h0=None, d
 
 
 from .serving import ss_add_rmsnorm, ss_add_rmsnorm_f8, ss_heads_fwd, ss_heads_step, ss_sample  # noqa: E402
-from .training import ss_add_layernorm, ss_add_layernorm_bwd, ss_conv1d_bwd, ss_distill, ss_distill_grad  # noqa: E402
+from .training import ss_add_layernorm, ss_add_layernorm_bwd, ss_conv1d_bwd, ss_distill, ss_distill_grad, \
+    ss_linear_xent, ss_linear_xent_bwd  # noqa: E402

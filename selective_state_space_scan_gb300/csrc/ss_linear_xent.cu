@@ -1,0 +1,924 @@
+// Softmax cross entropy over a vocabulary, from the rows of the last layer and the output embedding, and its
+// gradients, without keeping the logits:
+//   l_tv = hidden_t · weight_v,  lse_t = log Σ_v exp(l_tv),  loss_t = lse_t - l_{t,target_t}
+//   dl_tv = (exp(l_tv - lse_t) - [v = target_t]) · dloss_t,  dhidden = dl · weight,  dweight = dlᵀ · hidden
+//
+// Four matrix products of tokens x D x V, and those are the bound: hand-written tcgen05 products of 256 x 256
+// tiles by pairs of CTAs (tc_pair.cuh).  Rows without a target are left out before the first product: the others
+// are gathered into rows of their own, and the products' sizes come from their count in device memory.
+//   forward    the logits' tiles go from tensor memory into a maximum and a sum per row and half tile
+//   backward   the logits again, piece by piece of the vocabulary; a piece's dl is kept in bf16 (in the workspace,
+//              not the logits: kPieceBytes of it), then both products over it in one launch: dweight's rows of
+//              the piece, whole, and dhidden as sums in fp32 that grow from piece to piece
+// float32 operands are taken as sums of three bf16 (24 bits) and a product as the six products of them that
+// count: the same kernel with six times the K.
+//
+// One persistent CTA pair per two SMs: a warp that loads (TMA, six stages of 2 x 16 KB), one that issues, eight
+// that empty the other of two accumulators meanwhile.
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+#include <type_traits>
+
+#include "../../include/selscan.h"
+#include "heads_device.cuh"
+#include "host_util.h"
+#include "internal.h"
+#include "tc_pair.cuh"
+#include "xent_params.h"
+
+namespace selscan {
+namespace {
+
+constexpr int kTile = 256;                        // rows and columns of a pair's tile
+constexpr int kHalf = kTile / 2;                  // rows of a CTA's operand tiles
+constexpr int kStep = 64;                         // of K per stage
+constexpr int kStages = 6;
+constexpr uint32_t kOperand = kHalf * kStep * 2;  // bytes of one operand's tile
+constexpr uint32_t kStageBytes = 2 * kOperand;
+constexpr int kEpiWarps = 8;
+constexpr int kGemmThreads = (kEpiWarps + 2) * 32;
+constexpr int kGroup = 16;                        // tiles of rows that share a sweep over the vocabulary
+constexpr uint32_t kAccCols = 256;
+// Steps of K that one accumulator takes before its sums go into registers.  The tensor core cuts each addition of
+// 16 products off at 2^-23 of the sum instead of rounding it, so a long chain is off by its length times half of
+// that, to one side: 560 additions gave a dhidden off by 1e-5.  64 in a row leave 1e-6, and the registers' own
+// additions round.
+constexpr int kChain = 16;
+
+// The products of three-part operands that count, small ones first (the largest alone has the long chain).
+__constant__ int8_t kPartA[6] = {0, 2, 1, 0, 1, 0};
+__constant__ int8_t kPartB[6] = {2, 0, 1, 1, 0, 0};
+
+struct GemmShared {
+    uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+    uint32_t tmem;
+    int abort;
+};
+constexpr size_t kGemmSmem = kStages * kStageBytes + sizeof(GemmShared) + 1024;
+
+// A unit of work: a tile and a range of steps of K (each of them p.segs products of parts).
+struct Unit {
+    int job, m, n, k0, k1, split;
+};
+
+// How a kernel's units are numbered.  kOut has two products: 0 dweight (rows: the piece's tokens of the vocabulary),
+// 1 dhidden.
+struct Work {
+    int mt[2], nt[2], steps[2], per, splits, first;
+    int64_t n0, total;
+};
+template <Product P>
+__device__ __forceinline__ Work make_work(const XentParams& p, int rows) {
+    Work w;
+    const int dt = (p.D + kTile - 1) / kTile, vt = (p.Vp + kTile - 1) / kTile, rt = (rows + kTile - 1) / kTile;
+    if (P != Product::kOut) {
+        w.mt[0] = rt;
+        w.nt[0] = vt;
+        w.steps[0] = (p.D + kStep - 1) / kStep;
+        w.n0 = w.total = static_cast<int64_t>(rt) * vt;
+        w.splits = 1;
+        return w;
+    }
+    w.mt[0] = vt;
+    w.nt[0] = w.nt[1] = dt;
+    w.steps[0] = (rows + kStep - 1) / kStep;
+    w.mt[1] = rt;
+    w.steps[1] = (p.Vp + kStep - 1) / kStep;
+    w.splits = p.splits;
+    w.per = (w.steps[1] + p.splits - 1) / p.splits;
+    w.first = w.per > w.steps[0] ? 1 : 0;         // the longer units first, so that the shorter ones fill up
+    const int64_t a = static_cast<int64_t>(vt) * dt, b = static_cast<int64_t>(rt) * dt * p.splits;
+    w.n0 = w.first ? b : a;
+    w.total = a + b;
+    return w;
+}
+template <Product P>
+__device__ __forceinline__ Unit unit_of(const Work& w, int64_t i) {
+    Unit u;
+    if (P != Product::kOut) {
+        // the row tiles of a group take each tile of the vocabulary at the same time: it is read once
+        const int64_t per_group = static_cast<int64_t>(kGroup) * w.nt[0];
+        const int g = static_cast<int>(i / per_group), r = static_cast<int>(i - g * per_group);
+        const int size = min(kGroup, w.mt[0] - g * kGroup);
+        u.job = 0;
+        u.m = g * kGroup + r % size;
+        u.n = r / size;
+        u.k0 = 0;
+        u.k1 = w.steps[0];
+        u.split = 0;
+        return u;
+    }
+    u.job = i < w.n0 ? w.first : 1 - w.first;
+    const int64_t at = i < w.n0 ? i : i - w.n0;
+    u.n = static_cast<int>(at % w.nt[u.job]);
+    const int r = static_cast<int>(at / w.nt[u.job]);
+    u.m = r % w.mt[u.job];
+    u.split = r / w.mt[u.job];
+    u.k0 = u.job ? u.split * w.per : 0;
+    u.k1 = u.job ? min(u.k0 + w.per, w.steps[1]) : w.steps[0];
+    return u;
+}
+
+__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
+
+__device__ __forceinline__ void store16(void* q, uint4 v) { *reinterpret_cast<uint4*>(q) = v; }
+
+// 32 values of a row to bf16 (parts: what is left, and what is left of that); n of them exist.  The addresses are
+// 16-byte aligned and groups of 8 whole or not there (a row's padding may be written).
+template <bool F32>
+__device__ __forceinline__ void store_parts(__nv_bfloat16* q, int64_t part, int n, const float (&v)[32]) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        if (g * 8 >= n) break;
+        float2 f[4];
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[i] = make_float2(v[g * 8 + 2 * i], v[g * 8 + 2 * i + 1]);
+            h[i] = pack_bf16(f[i].x, f[i].y);
+        }
+        store16(q + g * 8, make_uint4(h[0], h[1], h[2], h[3]));
+        if constexpr (F32) {
+#pragma unroll
+            for (int part_i = 1; part_i < 3; ++part_i) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f[i] = fma2(unpack2(h[i]), splat2(-1.f), f[i]);
+                    h[i] = pack_bf16(f[i].x, f[i].y);
+                }
+                store16(q + part_i * part + g * 8, make_uint4(h[0], h[1], h[2], h[3]));
+            }
+        }
+    }
+}
+
+template <Product P, bool F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xent_gemm_kernel(const __grid_constant__ XentParams p) {
+    extern __shared__ uint8_t raw[];
+    uint8_t* tiles = raw + (1024 - smem_addr(raw) % 1024) % 1024;
+    GemmShared& sh = *reinterpret_cast<GemmShared*>(tiles + kStages * kStageBytes);
+    volatile int* abort = &sh.abort;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_ctarank();
+    const int64_t cluster = blockIdx.x / 2, clusters = gridDim.x / 2;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.acc_full[i], 1);
+            mbar_init(&sh.acc_empty[i], 2 * kEpiWarps);
+        }
+        sh.abort = 0;
+        mbar_fence_init();
+    }
+    if (warp == 0) pair_alloc(&sh.tmem, 2 * kAccCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    cluster_sync_all();                            // the peer's barriers exist
+    const uint32_t tmem = sh.tmem;
+    const int rows = *p.count;
+    const Work work = make_work<P>(p, rows);
+
+    if (warp == kEpiWarps) {
+        // ---------------------------------------------------------------- loads, by one thread of each CTA
+        if (lane == 0) {
+            uint32_t full0[kStages];
+#pragma unroll
+            for (int i = 0; i < kStages; ++i) full0[i] = peer_smem_addr(&sh.full[i], 0);
+            int st = 0;
+            uint32_t ph = 0;
+            for (int64_t i = cluster; i < work.total && !*abort; i += clusters) {
+                const Unit u = unit_of<P>(work, i);
+                const CUtensorMap* ma = u.job ? &p.a1 : &p.a0;
+                const CUtensorMap* mb = u.job ? &p.b1 : &p.b0;
+                // dweight: both operands have K (the tokens) along rows; dhidden: weight has K (the vocabulary) along rows
+                const bool a_mn = P == Product::kOut && u.job == 0, b_mn = P == Product::kOut;
+                const int am = u.m * kTile + static_cast<int>(rank) * kHalf, bn = u.n * kTile + static_cast<int>(rank) * kHalf;
+                bool go = true;
+                for (int kc = u.k0; kc < u.k1 && go; kc += kChain)
+                    for (int seg = 0; seg < (F32 ? 6 : 1) && go; ++seg) {
+                        const int pa = F32 ? kPartA[seg] : 0, pb = F32 ? kPartB[seg] : 0;
+                        for (int k = kc; k < min(kc + kChain, u.k1); ++k) {
+                            go = mbar_sleep_bounded(&sh.empty[st], ph ^ 1, abort, p.err);
+                            if (!go) break;
+                            if (rank == 0) mbar_expect_tx(&sh.full[st], 2 * kStageBytes);
+                            uint8_t* sa = tiles + st * kStageBytes;
+                            uint8_t* sb = sa + kOperand;
+                            const int kk = k * kStep;
+                            if (a_mn) {
+                                pair_tma_load(sa, ma, full0[st], am, kk, pa);
+                                pair_tma_load(sa + kOperand / 2, ma, full0[st], am + 64, kk, pa);
+                            } else {
+                                pair_tma_load(sa, ma, full0[st], kk, am, pa);
+                            }
+                            if (b_mn) {
+                                pair_tma_load(sb, mb, full0[st], bn, kk, pb);
+                                pair_tma_load(sb + kOperand / 2, mb, full0[st], bn + 64, kk, pb);
+                            } else {
+                                pair_tma_load(sb, mb, full0[st], kk, bn, pb);
+                            }
+                            if (++st == kStages) {
+                                st = 0;
+                                ph ^= 1;
+                            }
+                        }
+                    }
+            }
+            // the products' last arrivals on this CTA's barriers are in before it ends
+            for (int i = 0; i < kStages; ++i) {
+                if (!mbar_sleep_bounded(&sh.empty[st], ph ^ 1, abort, p.err)) break;
+                if (++st == kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+    } else if (warp == kEpiWarps + 1) {
+        // ---------------------------------------------------------------- products, by one thread of CTA 0
+        if (lane == 0 && rank == 0) {
+            const uint32_t at = smem_addr(tiles);
+            int st = 0;
+            uint32_t ph = 0;
+            int turn = 0;
+            bool go = true;
+            for (int64_t i = cluster; i < work.total && go; i += clusters) {
+                const Unit u = unit_of<P>(work, i);
+                const bool a_mn = P == Product::kOut && u.job == 0, b_mn = P == Product::kOut;
+                const uint32_t idesc = tc_idesc(256, 256, a_mn, b_mn);
+                const uint32_t la = a_mn ? kOperand / 2 : 16, lb = b_mn ? kOperand / 2 : 16, ka = a_mn ? 2048 : 32, kb = b_mn ? 2048 : 32;
+                for (int kc = u.k0; kc < u.k1 && go; kc += kChain, ++turn) {
+                    const uint32_t d = tmem + (turn & 1) * kAccCols;
+                    const int n = (min(kc + kChain, u.k1) - kc) * (F32 ? 6 : 1);
+                    go = mbar_sleep_bounded(&sh.acc_empty[turn & 1], ((turn >> 1) & 1) ^ 1, abort, p.err);
+                    tc_fence_after();
+                    for (int k = 0; k < n && go; ++k) {
+                        go = mbar_sleep_bounded(&sh.full[st], ph, abort, p.err);
+                        if (!go) break;
+                        tc_fence_after();
+                        const uint32_t a = at + st * kStageBytes, b = a + kOperand;
+#pragma unroll
+                        for (int j = 0; j < kStep / 16; ++j)
+                            pair_mma(d, tc_desc(a + j * ka, la, 1024), tc_desc(b + j * kb, lb, 1024), idesc, k > 0 || j > 0);
+                        pair_commit(&sh.empty[st]);
+                        if (++st == kStages) {
+                            st = 0;
+                            ph ^= 1;
+                        }
+                    }
+                    pair_commit(&sh.acc_full[turn & 1]);
+                }
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- accumulators, by eight warps of each CTA
+        const int quarter = warp % 4, half = warp / 4;
+        const uint32_t empty0 = peer_smem_addr(&sh.acc_empty[0], 0), empty1 = peer_smem_addr(&sh.acc_empty[1], 0);
+        int turn = 0;
+        bool go = true;
+        for (int64_t i = cluster; i < work.total; i += clusters) {
+            const Unit u = unit_of<P>(work, i);
+            float acc[kHalf];                      // a thread has half a row of the tile
+#pragma unroll
+            for (int j = 0; j < kHalf; ++j) acc[j] = 0.f;
+#pragma unroll 1
+            for (int kc = u.k0; kc < u.k1; kc += kChain, ++turn) {
+                go = __all_sync(0xffffffffu, mbar_sleep_bounded(&sh.acc_full[turn & 1], (turn >> 1) & 1, abort, p.err));
+                if (!go) break;
+                tc_fence_after();
+                const uint32_t at = tmem + (turn & 1) * kAccCols + half * kHalf + (static_cast<uint32_t>(quarter * 32) << 16);
+#pragma unroll
+                for (int c = 0; c < kHalf; c += 32) {
+                    uint32_t r[32];
+                    tc_ld32(at + c, r);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float2 v = add2(make_float2(acc[c + j], acc[c + j + 1]), make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])));
+                        acc[c + j] = v.x;
+                        acc[c + j + 1] = v.y;
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_peer(turn & 1 ? empty1 : empty0);
+            }
+            if (!go) break;
+            const int row = u.m * kTile + static_cast<int>(rank) * kHalf + quarter * 32 + lane;
+            const int col0 = u.n * kTile + half * kHalf;
+            if constexpr (P == Product::kLoss) {
+                float m = -INFINITY, s = 0.f;
+                const int tgt = row < rows ? p.tgt[row] - p.v0 - col0 : -1;
+#pragma unroll
+                for (int c = 0; c < kHalf; c += 32) {
+                    const int n = p.Vp - col0 - c;
+                    if (n <= 0) break;
+                    float b = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        acc[c + j] = j < n ? acc[c + j] : -INFINITY;
+                        b = fmaxf(b, acc[c + j]);
+                    }
+                    if (b > m) {
+                        s *= ex2((m - b) * kLog2e);
+                        m = b;
+                    }
+                    const float2 off = splat2(-base_of(m)), l2e = splat2(kLog2e);
+                    float2 a = splat2(0.f);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) a = add2(a, ex2x2(mul2(add2(make_float2(acc[c + j], acc[c + j + 1]), off), l2e)));
+                    s += a.x + a.y;
+                    if (tgt >= c && tgt < c + 32) {
+                        float l = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) l = tgt - c == j ? acc[c + j] : l;
+                        p.tl[row] = l;
+                    }
+                }
+                if (row < rows) p.part[(static_cast<int64_t>(p.tile0 + u.n) * 2 + half) * p.ld_part + row] = make_float2(m, s);
+            } else if constexpr (P == Product::kGrad) {
+                const bool ok = row < rows;
+                const float lse = ok ? p.lse[row] : 0.f, g = ok ? p.g[row] : 0.f;
+                const int tgt = ok ? p.tgt[row] - p.v0 - col0 : -1;
+                __nv_bfloat16* out = p.dl + static_cast<int64_t>(row) * p.ld_dl + col0;
+                const float2 off = splat2(-lse), l2e = splat2(kLog2e), g2 = splat2(g);
+#pragma unroll
+                for (int c = 0; c < kHalf; c += 32) {
+                    const int n = p.Vp - col0 - c;
+                    if (n <= 0) break;
+                    float v[32];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float2 e = ex2x2(mul2(add2(make_float2(acc[c + j], acc[c + j + 1]), off), l2e));
+                        v[j] = e.x;
+                        v[j + 1] = e.y;
+                    }
+                    if (tgt >= c && tgt < c + 32) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] -= tgt - c == j ? 1.f : 0.f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float2 e = mul2(make_float2(v[j], v[j + 1]), g2);
+                        v[j] = ok ? e.x : 0.f;
+                        v[j + 1] = ok ? e.y : 0.f;
+                    }
+                    store_parts<F32>(out + c, p.dl_part, n, v);
+                }
+            } else if (u.job) {
+                if (row < rows) {
+                    float* out = p.dx + u.split * p.dx_split + static_cast<int64_t>(row) * p.ld_dx + col0;
+                    const int n = p.D - col0;
+#pragma unroll
+                    for (int j = 0; j < kHalf; j += 4) {
+                        if (j >= n) break;
+                        float4* q = reinterpret_cast<float4*>(out + j);
+                        float4 v = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+                        if (p.add) {
+                            const float4 o = *q;
+                            v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+                        }
+                        *q = v;
+                    }
+                }
+            } else if (row < p.Vp) {
+                using T = std::conditional_t<F32, float, __nv_bfloat16>;
+                T* out = static_cast<T*>(p.dw) + static_cast<int64_t>(p.v0 + row) * p.ld_dw + col0;
+                const int n = p.D - col0;
+                if (p.dw_wide) {
+#pragma unroll
+                    for (int j = 0; j < kHalf; j += 8) {
+                        if (j >= n) break;
+                        if constexpr (F32) {
+                            *reinterpret_cast<float4*>(out + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+                            *reinterpret_cast<float4*>(out + j + 4) = make_float4(acc[j + 4], acc[j + 5], acc[j + 6], acc[j + 7]);
+                        } else {
+                            store16(out + j, make_uint4(pack_bf16(acc[j], acc[j + 1]), pack_bf16(acc[j + 2], acc[j + 3]),
+                                                        pack_bf16(acc[j + 4], acc[j + 5]), pack_bf16(acc[j + 6], acc[j + 7])));
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kHalf; ++j)
+                        if (j < n) out[j] = from_f32<T>(acc[j]);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    // (after a wait that ran out: copies and products in flight are over long before this)
+    if (*abort)
+        for (int i = 0; i < 20; ++i) __nanosleep(1000000);
+    tc_fence_before();
+    cluster_sync_all();                            // nobody reads or signals the peer's memory any more
+    tc_fence_after();
+    if (warp == 0) pair_dealloc(tmem, 2 * kAccCols);
+}
+
+// ------------------------------------------------------------------------------------------ before and after
+
+constexpr int kPrepThreads = 256;
+
+template <typename T> __device__ __forceinline__ float load_f32(const T* q) { return to_f32<T>(*q); }
+
+// Columns [c, c + 8) of a row to one or three bf16 parts; columns of D and more are zero.
+template <typename T, bool F32>
+__device__ __forceinline__ void pack8(const T* row, __nv_bfloat16* out, int64_t part, int c, int D, bool wide) {
+    float v[8];
+    if (wide && c + 8 <= D) {
+        if constexpr (sizeof(T) == 2) {
+            store16(out + c, *reinterpret_cast<const uint4*>(row + c));
+            return;
+        } else {
+            const float4 a = *reinterpret_cast<const float4*>(row + c), b = *reinterpret_cast<const float4*>(row + c + 4);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < D ? load_f32<T>(row + c + i) : 0.f;
+    }
+    float2 f[4];
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[i] = make_float2(v[2 * i], v[2 * i + 1]);
+        h[i] = pack_bf16(f[i].x, f[i].y);
+    }
+    store16(out + c, make_uint4(h[0], h[1], h[2], h[3]));
+    if constexpr (F32) {
+#pragma unroll
+        for (int q = 1; q < 3; ++q) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[i] = fma2(unpack2(h[i]), splat2(-1.f), f[i]);
+                h[i] = pack_bf16(f[i].x, f[i].y);
+            }
+            store16(out + q * part + c, make_uint4(h[0], h[1], h[2], h[3]));
+        }
+    }
+}
+
+// Sum over the block, in every thread.
+__device__ __forceinline__ int block_sum(int v, int* slot) {
+    v = __reduce_add_sync(0xffffffffu, v);
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) slot[threadIdx.x / 32] = v;
+    __syncthreads();
+    int s = 0;
+    for (int i = 0; i < kPrepThreads / 32; ++i) s += slot[i];
+    return s;
+}
+
+// The rows that have a target, gathered in order: row i of x is row rows[i] of hidden.  A block has `per` rows of
+// hidden and counts the targets before them itself.
+template <typename T, bool BWD>
+__global__ void __launch_bounds__(kPrepThreads) xent_gather_kernel(const PrepParams p) {
+    constexpr bool F32 = sizeof(T) == 4;
+    __shared__ int slot[kPrepThreads / 32];
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * p.per, last = min(first + p.per, p.T);
+    int before = 0;
+    for (int64_t t = threadIdx.x; t < first; t += kPrepThreads) {
+        const int v = p.targets[t];
+        before += v >= 0 && v < p.V;
+    }
+    int at = block_sum(before, slot);
+    for (int64_t t = first; t < last; ++t) {
+        const int v = p.targets[t];
+        if (v >= 0 && v < p.V) {
+            const T* src = static_cast<const T*>(p.hidden) + t * p.hidden_t;
+            __nv_bfloat16* dst = p.x + static_cast<int64_t>(at) * p.ld_x;
+            for (int c = threadIdx.x * 8; c < p.D; c += kPrepThreads * 8) pack8<T, F32>(src, dst, p.x_part, c, p.D, p.wide);
+            if (threadIdx.x == 0) {
+                p.rows[at] = static_cast<int>(t);
+                p.tgt[at] = v;
+                if constexpr (BWD) {
+                    p.lse_c[at] = p.lse[t];
+                    p.g_c[at] = p.dloss[t * p.dloss_t];
+                }
+            }
+            ++at;
+        } else if constexpr (BWD) {
+            T* d = static_cast<T*>(p.dhidden) + t * p.dhidden_t;
+            for (int c = threadIdx.x; c < p.D; c += kPrepThreads) d[c] = from_f32<T>(0.f);
+        } else if (threadIdx.x == 0) {
+            p.loss_out[t] = p.lse_out[t] = 0.f;
+            if (v >= p.V && p.err) atomicOr(p.err, kErrIndex);
+        }
+    }
+    if (last == p.T) {
+        if (threadIdx.x == 0) *p.count = at;
+        // the rest of the last step of K over the tokens counts for nothing, but must be finite
+        const int end = (at + kStep - 1) / kStep * kStep, vecs = static_cast<int>(p.ld_x / 8);
+        for (int q = 0; q < (F32 ? 3 : 1); ++q)
+            for (int i = threadIdx.x; i < (end - at) * vecs; i += kPrepThreads)
+                store16(p.x + q * p.x_part + (at + i / vecs) * p.ld_x + i % vecs * 8, make_uint4(0u, 0u, 0u, 0u));
+    }
+}
+
+// Rows of weight as operands of the products (where they cannot be loaded as they lie).
+template <typename T>
+__global__ void __launch_bounds__(kPrepThreads) xent_pack_kernel(const T* w, int64_t stride, __nv_bfloat16* out, int64_t ld, int64_t part,
+                                                                 int64_t n, int D, bool wide) {
+    const int vecs = static_cast<int>(ld / 8);
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPrepThreads + threadIdx.x; i < n * vecs; i += static_cast<int64_t>(gridDim.x) * kPrepThreads) {
+        const int64_t r = i / vecs;
+        pack8<T, sizeof(T) == 4>(w + r * stride, out + r * ld, part, static_cast<int>(i - r * vecs) * 8, D, wide);
+    }
+}
+
+// lse and loss from the maxima and sums of the half tiles; a block has 32 rows, a warp a share of the tiles.
+__global__ void __launch_bounds__(kPrepThreads) xent_join_kernel(const float2* part, int64_t ld, int halves, const int* count, const int* rows,
+                                                                 const float* tl, float* loss, float* lse) {
+    __shared__ float2 s[kPrepThreads / 32][32];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, n = *count;
+    const int row = blockIdx.x * 32 + lane;
+    float m = -INFINITY, sum = 0.f;
+    auto join = [&](float2 q) {
+        const float b = fmaxf(m, q.x), o = base_of(b);
+        sum = sum * ex2((m - o) * kLog2e) + q.y * ex2((q.x - o) * kLog2e);
+        m = b;
+    };
+    if (blockIdx.x * 32 >= n) return;
+    if (row < n)
+        for (int i = warp; i < halves; i += kPrepThreads / 32) join(part[i * ld + row]);
+    s[warp][lane] = make_float2(m, sum);
+    __syncthreads();
+    if (warp == 0 && row < n) {
+        for (int i = 1; i < kPrepThreads / 32; ++i) join(s[i][lane]);
+        const float v = m + logf(sum);
+        const int t = rows[row];
+        lse[t] = v;
+        loss[t] = v - tl[row];
+    }
+}
+
+// dhidden's rows from their sums.
+template <typename T>
+__global__ void __launch_bounds__(kPrepThreads) xent_scatter_kernel(const float* dx, int64_t split_stride, int splits, int64_t ld, const int* count,
+                                                                    const int* rows, T* dhidden, int64_t stride, int D) {
+    const int n = *count;
+    for (int i = blockIdx.x; i < n; i += gridDim.x) {
+        T* out = dhidden + static_cast<int64_t>(rows[i]) * stride;
+        for (int c = threadIdx.x; c < D; c += kPrepThreads) {
+            float v = 0.f;
+            for (int s = 0; s < splits; ++s) v += dx[s * split_stride + i * ld + c];
+            out[c] = from_f32<T>(v);
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------------------ host
+
+using host::dev_ptr;
+using host::is_aligned;
+using host::meet;
+using host::Range;
+using host::range3;
+
+constexpr int64_t kPieceBytes = 256 << 20;        // of dl (and of a packed piece of weight)
+constexpr int64_t kMinPiece = 4096;               // columns: below, the sums of dhidden cost as much as the products
+constexpr int64_t kMaxSplits = 32;
+
+int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
+
+int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 152;
+    }
+    return sms;
+}
+
+// Where everything lies in the workspace.
+struct Layout {
+    int64_t parts, segs, ld_x, tpad, piece, pieces, splits, ld_dl, ld_dx, halves;
+    size_t count, rows, tgt, lse, g, tl, part, x, w, dl, dx, total;
+};
+
+// Time of one launch of both products over a piece, in steps of K, when dhidden's are cut in `splits`: units in
+// turn over the pairs of CTAs, each some steps longer for its end.
+int64_t out_cost(int64_t T, int64_t D, int64_t Vp, int64_t segs, int64_t splits, int64_t pairs) {
+    constexpr int64_t kEnd = 6;
+    const int64_t dt = (D + kTile - 1) / kTile;
+    const int64_t len[2] = {(T + kStep - 1) / kStep * segs, ((Vp + kStep - 1) / kStep + splits - 1) / splits * segs};
+    const int64_t n[2] = {(Vp + kTile - 1) / kTile * dt, (T + kTile - 1) / kTile * dt * splits};
+    const int first = len[1] > len[0] ? 1 : 0;
+    const int64_t a = n[first], b = n[1 - first];
+    int64_t worst = 0;
+    for (int64_t c = 0; c < pairs; ++c) {
+        const int64_t ca = (a - c + pairs - 1) / pairs, all = (a + b - c + pairs - 1) / pairs;
+        worst = std::max(worst, std::max<int64_t>(ca, 0) * (len[first] + kEnd) + (std::max<int64_t>(all, 0) - std::max<int64_t>(ca, 0)) * (len[1 - first] + kEnd));
+    }
+    // a slice of sums more: its bytes out and in again, some 2 MB of them to a step's time (0.3 us at 6.8 TB/s)
+    return worst + splits * T * D * 8 / (2 << 20);
+}
+
+Layout layout(int64_t T, int64_t V, int64_t D, bool f32, bool packed, bool bwd) {
+    Layout q;
+    std::memset(&q, 0, sizeof(q));
+    q.parts = f32 ? 3 : 1;
+    q.segs = f32 ? 6 : 1;
+    q.ld_x = round_up(D, 8);
+    q.tpad = round_up(T, kTile);
+    const int64_t per_col = std::max(bwd ? q.tpad * 2 * q.parts : 0, packed ? q.ld_x * 2 * q.parts : 0);
+    q.piece = V;
+    if (per_col > 0) {
+        const int64_t most = std::max(kPieceBytes / per_col / kTile * kTile, kMinPiece);
+        const int64_t n = (V + most - 1) / most;               // pieces of like widths
+        q.piece = std::min(V, round_up((V + n - 1) / n, kTile));
+    }
+    q.pieces = (V + q.piece - 1) / q.piece;
+    q.halves = 0;
+    for (int64_t v = 0; v < V; v += q.piece) q.halves += 2 * ((std::min(q.piece, V - v) + kTile - 1) / kTile);
+    q.ld_dl = round_up(q.piece, 8);
+    q.ld_dx = round_up(D, 4);
+    q.splits = 1;
+    if (bwd) {
+        const int64_t pairs = sm_count() / 2;
+        int64_t best = -1;
+        for (int64_t s = 1; s <= kMaxSplits && (s == 1 || (q.piece / kStep / s >= kChain && s * q.tpad * q.ld_dx * 4 <= 2 * kPieceBytes)); ++s) {
+            const int64_t c = out_cost(T, D, q.piece, q.segs, s, pairs);
+            if (best < 0 || c < best) {
+                best = c;
+                q.splits = s;
+            }
+        }
+    }
+    size_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const size_t o = at;
+        at += static_cast<size_t>(round_up(bytes, 1024));
+        return o;
+    };
+    q.count = take(4);
+    q.rows = take(4 * q.tpad);
+    q.tgt = take(4 * q.tpad);
+    if (bwd) {
+        q.lse = take(4 * q.tpad);
+        q.g = take(4 * q.tpad);
+    } else {
+        q.tl = take(4 * q.tpad);
+        q.part = take(8 * q.tpad * q.halves);
+    }
+    q.x = take(2 * q.parts * q.tpad * q.ld_x);
+    if (packed) q.w = take(2 * q.parts * q.piece * q.ld_x);
+    if (bwd) {
+        q.dl = take(2 * q.parts * q.tpad * q.ld_dl);
+        q.dx = take(4 * q.splits * q.tpad * q.ld_dx);
+    }
+    q.total = at;
+    return q;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* q = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &q, 12000, cudaEnableDefault, &r) == cudaSuccess &&
+            r == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(q);
+    });
+    return fn;
+}
+
+// [parts][rows][cols] of bf16, boxes of 64 columns and `box_rows` rows, 128-byte swizzle, zeros outside.
+bool make_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t parts, int64_t ld, int64_t part, int box_rows) {
+    auto enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(parts)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * 2), static_cast<cuuint64_t>((parts > 1 ? part : rows * ld) * 2)};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1}, one[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Pairs of CTAs that fit on the device at once.
+template <Product P, bool F32>
+cudaError_t launch_gemm_as(const XentParams& p, int64_t units, cudaStream_t stream) {
+    static std::atomic<int> known[64] = {};
+    auto* kern = xent_gemm_kernel<P, F32>;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    int pairs = dev < 64 ? known[dev].load() : 0;
+    if (pairs == 0) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kGemmSmem));
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * sm_count());
+        cfg.blockDim = dim3(kGemmThreads);
+        cfg.dynamicSmemBytes = kGemmSmem;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 2;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg);
+        if (e != cudaSuccess) return e;
+        if (pairs < 1) return cudaErrorInvalidConfiguration;
+        if (dev < 64) known[dev].store(pairs);
+    }
+    const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(pairs, std::max<int64_t>(units, 1)));
+    kern<<<grid, kGemmThreads, kGemmSmem, stream>>>(p);
+    return cudaGetLastError();
+}
+template <Product P>
+cudaError_t launch_gemm(const XentParams& p, bool f32, int64_t units, cudaStream_t stream) {
+    return f32 ? launch_gemm_as<P, true>(p, units, stream) : launch_gemm_as<P, false>(p, units, stream);
+}
+
+struct Call {
+    const void* hidden;
+    const void* weight;
+    const int32_t* targets;
+    const float* dloss;
+    const float* lse_in;
+    float* loss;
+    float* lse;
+    void* dhidden;
+    void* dweight;
+    bool bwd;
+};
+
+bool loads_in_place(const void* weight, int64_t stride, int32_t io) {
+    return io == SS_BF16 && is_aligned(weight, 16) && stride % 8 == 0 && stride * 2 < (int64_t(1) << 40);
+}
+
+ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_strides* strides, void* workspace, size_t workspace_bytes,
+               void* stream_ptr) {
+    if (T < 0 || V < 1 || D < 1) return SS_ERR_INVALID_ARG;
+    if (T > SS_XENT_MAX_TOKENS || V > SS_XENT_MAX_V || D > SS_XENT_MAX_D) return SS_ERR_UNSUPPORTED;
+    ss_xent_strides s;
+    if (strides) {
+        s = *strides;
+    } else {
+        std::memset(&s, 0, sizeof(s));
+        s.io_dtype = SS_F32;
+        s.hidden_t = s.weight_v = s.dhidden_t = s.dweight_v = D;
+        s.dloss_t = 1;
+    }
+    if (s.io_dtype != SS_F32 && s.io_dtype != SS_BF16) return SS_ERR_INVALID_ARG;
+    const bool f32 = s.io_dtype == SS_F32;
+    const int64_t es = f32 ? 4 : 2;
+    if (!c.bwd && T == 0) return SS_OK;
+    if (s.hidden_t < 0 || s.weight_v < D) return SS_ERR_INVALID_ARG;
+    if (T > 0 && (!c.hidden || !c.weight || !c.targets)) return SS_ERR_INVALID_ARG;
+    if (c.bwd) {
+        if (!c.dweight || s.dweight_v < D || s.dloss_t < 0 || (T > 1 && s.dhidden_t < D)) return SS_ERR_INVALID_ARG;
+        if (T > 0 && (!c.dloss || !c.lse_in || !c.dhidden)) return SS_ERR_INVALID_ARG;
+    } else if (!c.loss || !c.lse) {
+        return SS_ERR_INVALID_ARG;
+    }
+    const bool in_place = loads_in_place(c.weight, s.weight_v, s.io_dtype);
+    const Layout q = layout(std::max<int64_t>(T, 1), V, D, f32, !in_place, c.bwd);
+    if (T > 0 && (!workspace || workspace_bytes < q.total)) return SS_ERR_INVALID_ARG;
+    const void* words[] = {c.targets, c.dloss, c.lse_in, c.loss, c.lse};
+    for (const void* a : words)
+        if (a && !is_aligned(a, 4)) return SS_ERR_MISALIGNED;
+    const void* elems[] = {c.hidden, c.weight, c.dhidden, c.dweight};
+    for (const void* a : elems)
+        if (a && !is_aligned(a, es)) return SS_ERR_MISALIGNED;
+    if (T > 0 && !is_aligned(workspace, 256)) return SS_ERR_MISALIGNED;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return SS_ERR_CUDA;
+    for (const void* a : words)
+        if (a && T > 0 && !dev_ptr(a, dev)) return SS_ERR_INVALID_ARG;
+    for (const void* a : elems)
+        if (a && (T > 0 || a == c.dweight) && !dev_ptr(a, dev)) return SS_ERR_INVALID_ARG;
+    if (T > 0 && !dev_ptr(workspace, dev)) return SS_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream_ptr);
+    if (T == 0)                                    // sums over no tokens
+        return cudaMemset2DAsync(c.dweight, static_cast<size_t>(s.dweight_v * es), 0, static_cast<size_t>(D * es), static_cast<size_t>(V), st) ==
+                       cudaSuccess
+                   ? SS_OK
+                   : SS_ERR_CUDA;
+    const Range in[] = {range3(c.hidden, 1, T, D, 0, s.hidden_t, es), range3(c.weight, 1, V, D, 0, s.weight_v, es), range3(c.targets, 1, 1, T, 0, 0, 4),
+                        range3(c.dloss, 1, T, 1, 0, s.dloss_t, 4), range3(c.lse_in, 1, 1, T, 0, 0, 4)};
+    const Range out[] = {range3(c.loss, 1, 1, T, 0, 0, 4), range3(c.lse, 1, 1, T, 0, 0, 4), range3(c.dhidden, 1, T, D, 0, s.dhidden_t, es),
+                         range3(c.dweight, 1, V, D, 0, s.dweight_v, es), range3(workspace, 1, 1, static_cast<int64_t>(q.total), 0, 0, 1)};
+    for (int i = 0; i < 5; ++i) {
+        for (const Range& r : in)
+            if (meet(out[i], r)) return SS_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (meet(out[i], out[j])) return SS_ERR_INVALID_ARG;
+    }
+
+    char* ws = static_cast<char*>(workspace);
+    auto f32_at = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
+    __nv_bfloat16* x = reinterpret_cast<__nv_bfloat16*>(ws + q.x);
+    __nv_bfloat16* w = reinterpret_cast<__nv_bfloat16*>(ws + q.w);
+    __nv_bfloat16* dl = reinterpret_cast<__nv_bfloat16*>(ws + q.dl);
+    const int64_t x_part = q.tpad * q.ld_x, w_part = q.piece * q.ld_x, dl_part = q.tpad * q.ld_dl;
+    auto wide = [&](const void* a, int64_t stride) { return is_aligned(a, 16) && (stride * es) % 16 == 0; };
+
+    PrepParams g;
+    std::memset(&g, 0, sizeof(g));
+    g.hidden = c.hidden; g.hidden_t = s.hidden_t; g.targets = c.targets; g.T = T; g.V = V; g.D = static_cast<int>(D);
+    g.per = static_cast<int>(std::max<int64_t>(8, T / 1024));
+    g.x = x; g.ld_x = q.ld_x; g.x_part = x_part; g.wide = wide(c.hidden, T > 1 ? s.hidden_t : 0);
+    g.count = reinterpret_cast<int*>(ws + q.count); g.rows = reinterpret_cast<int*>(ws + q.rows); g.tgt = reinterpret_cast<int*>(ws + q.tgt);
+    g.lse = c.lse_in; g.dloss = c.dloss; g.dloss_t = s.dloss_t; g.lse_c = f32_at(q.lse); g.g_c = f32_at(q.g);
+    g.dhidden = c.dhidden; g.dhidden_t = s.dhidden_t; g.loss_out = c.loss; g.lse_out = c.lse;
+    g.err = device_error_word();
+    void (*gather)(PrepParams) = f32 ? (c.bwd ? xent_gather_kernel<float, true> : xent_gather_kernel<float, false>)
+                                     : (c.bwd ? xent_gather_kernel<__nv_bfloat16, true> : xent_gather_kernel<__nv_bfloat16, false>);
+    gather<<<static_cast<unsigned>((T + g.per - 1) / g.per), kPrepThreads, 0, st>>>(g);
+    if (cudaGetLastError() != cudaSuccess) return SS_ERR_CUDA;
+
+    XentParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.count = g.count; p.tgt = g.tgt; p.D = static_cast<int>(D); p.segs = static_cast<int>(q.segs); p.err = g.err;
+    p.part = reinterpret_cast<float2*>(ws + q.part); p.ld_part = q.tpad; p.tl = f32_at(q.tl);
+    p.lse = g.lse_c; p.g = g.g_c; p.dl = dl; p.ld_dl = q.ld_dl; p.dl_part = dl_part;
+    p.dw = c.dweight; p.ld_dw = s.dweight_v; p.dw_wide = c.bwd && D % 8 == 0 && wide(c.dweight, s.dweight_v);
+    p.dx = f32_at(q.dx); p.ld_dx = q.ld_dx; p.dx_split = q.tpad * q.ld_dx; p.splits = static_cast<int>(q.splits);
+    const int64_t mt = (T + kTile - 1) / kTile, dt = (D + kTile - 1) / kTile;
+    for (int64_t v0 = 0; v0 < V; v0 += q.piece) {
+        const int64_t Vp = std::min(q.piece, V - v0), vt = (Vp + kTile - 1) / kTile;
+        const void* wp = static_cast<const char*>(c.weight) + v0 * s.weight_v * es;
+        int64_t ld_w = s.weight_v;
+        if (!in_place) {
+            const unsigned grid = static_cast<unsigned>(std::min<int64_t>((Vp * q.ld_x / 8 + kPrepThreads - 1) / kPrepThreads, 8 * sm_count()));
+            if (f32)
+                xent_pack_kernel<float><<<grid, kPrepThreads, 0, st>>>(static_cast<const float*>(wp), s.weight_v, w, q.ld_x, w_part, Vp, p.D,
+                                                                       wide(wp, s.weight_v));
+            else
+                xent_pack_kernel<__nv_bfloat16><<<grid, kPrepThreads, 0, st>>>(static_cast<const __nv_bfloat16*>(wp), s.weight_v, w, q.ld_x, w_part,
+                                                                               Vp, p.D, wide(wp, s.weight_v));
+            if (cudaGetLastError() != cudaSuccess) return SS_ERR_CUDA;
+            wp = w;
+            ld_w = q.ld_x;
+        }
+        p.v0 = static_cast<int>(v0);
+        p.Vp = static_cast<int>(Vp);
+        // logits: rows of x and of weight, K along the columns
+        if (!make_map(&p.a0, x, D, q.tpad, q.parts, q.ld_x, x_part, kHalf) || !make_map(&p.b0, wp, D, Vp, q.parts, ld_w, w_part, kHalf))
+            return SS_ERR_CUDA;
+        if (!c.bwd) {
+            if (launch_gemm<Product::kLoss>(p, f32, mt * vt, st) != cudaSuccess) return SS_ERR_CUDA;
+            p.tile0 += static_cast<int>(vt);
+            continue;
+        }
+        if (launch_gemm<Product::kGrad>(p, f32, mt * vt, st) != cudaSuccess) return SS_ERR_CUDA;
+        // dweight: dl and x with the tokens along rows; dhidden: dl with K along columns, weight with K along rows
+        if (!make_map(&p.a0, dl, Vp, q.tpad, q.parts, q.ld_dl, dl_part, kStep) || !make_map(&p.b0, x, D, q.tpad, q.parts, q.ld_x, x_part, kStep) ||
+            !make_map(&p.a1, dl, Vp, q.tpad, q.parts, q.ld_dl, dl_part, kHalf) || !make_map(&p.b1, wp, D, Vp, q.parts, ld_w, w_part, kStep))
+            return SS_ERR_CUDA;
+        p.add = v0 > 0;
+        if (launch_gemm<Product::kOut>(p, f32, vt * dt + mt * dt * q.splits, st) != cudaSuccess) return SS_ERR_CUDA;
+    }
+    if (!c.bwd) {
+        xent_join_kernel<<<static_cast<unsigned>((T + 31) / 32), kPrepThreads, 0, st>>>(p.part, q.tpad, static_cast<int>(q.halves), g.count, g.rows, p.tl,
+                                                                                     c.loss, c.lse);
+    } else {
+        const unsigned grid = static_cast<unsigned>(std::min<int64_t>(T, 8 * sm_count()));
+        if (f32)
+            xent_scatter_kernel<float><<<grid, kPrepThreads, 0, st>>>(p.dx, p.dx_split, p.splits, p.ld_dx, g.count, g.rows, static_cast<float*>(c.dhidden),
+                                                                      s.dhidden_t, p.D);
+        else
+            xent_scatter_kernel<__nv_bfloat16><<<grid, kPrepThreads, 0, st>>>(p.dx, p.dx_split, p.splits, p.ld_dx, g.count, g.rows,
+                                                                              static_cast<__nv_bfloat16*>(c.dhidden), s.dhidden_t, p.D);
+    }
+    return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace selscan
+
+using namespace selscan;
+
+extern "C" size_t ss_linear_xent_workspace_size(int64_t tokens, int64_t V, int64_t D, int32_t io_dtype, int32_t backward) {
+    if (tokens <= 0 || V < 1 || D < 1 || tokens > SS_XENT_MAX_TOKENS || V > SS_XENT_MAX_V || D > SS_XENT_MAX_D ||
+        (io_dtype != SS_F32 && io_dtype != SS_BF16))
+        return 0;
+    const bool f32 = io_dtype == SS_F32;
+    return std::max(layout(tokens, V, D, f32, true, backward != 0).total, layout(tokens, V, D, f32, f32, backward != 0).total);
+}
+
+extern "C" ss_status ss_linear_xent(const void* hidden, const void* weight, const int32_t* targets, float* loss, float* lse, int64_t tokens,
+                                    int64_t V, int64_t D, const ss_xent_strides* strides, void* workspace, size_t workspace_bytes, void* stream) {
+    Call c = {};
+    c.hidden = hidden; c.weight = weight; c.targets = targets; c.loss = loss; c.lse = lse;
+    return xent(c, tokens, V, D, strides, workspace, workspace_bytes, stream);
+}
+
+extern "C" ss_status ss_linear_xent_bwd(const float* dloss, const void* hidden, const void* weight, const int32_t* targets, const float* lse,
+                                        void* dhidden, void* dweight, int64_t tokens, int64_t V, int64_t D, const ss_xent_strides* strides,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+    Call c = {};
+    c.hidden = hidden; c.weight = weight; c.targets = targets; c.dloss = dloss; c.lse_in = lse; c.dhidden = dhidden; c.dweight = dweight;
+    c.bwd = true;
+    return xent(c, tokens, V, D, strides, workspace, workspace_bytes, stream);
+}

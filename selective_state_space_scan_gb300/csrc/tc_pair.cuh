@@ -1,0 +1,43 @@
+// Tensor-core helpers for pairs of CTAs (clusters of two): one tcgen05.mma of M = 256 and N = 256 works on both
+// CTAs' tiles.  Each CTA holds 128 rows of A and 128 of B in its shared memory and the products of its rows in
+// its tensor memory; CTA 0 issues.  Operand tiles are those of tc_device.cuh.  Hand-written inline PTX for sm_103a.
+#pragma once
+
+#include "tc_device.cuh"
+
+namespace selscan {
+
+// D (+)= A·B over 16 of K, D 256 x 256; one thread of CTA 0 issues it.
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+// One arrival on the barrier at this address in both CTAs once every product this thread has issued is complete.
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_addr(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+__device__ __forceinline__ void pair_alloc(uint32_t* out, uint32_t cols) {    // one whole warp of each CTA
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(out)), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_dealloc(uint32_t addr, uint32_t cols) {  // one whole warp of each CTA
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+
+// TMA tile into this CTA's shared memory, completing on a barrier of either CTA (`bar`: its address in the
+// cluster's window, from peer_smem_addr).
+__device__ __forceinline__ void pair_tma_load(void* dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+
+}  // namespace selscan

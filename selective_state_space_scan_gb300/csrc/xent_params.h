@@ -1,0 +1,65 @@
+// Parameters of the cross entropy's kernels (ss_linear_xent.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace selscan {
+
+enum class Product { kLoss, kGrad, kOut };
+
+struct XentParams {
+    // operands of the products as [part][row][col]; kOut's second product has the maps a1 and b1
+    CUtensorMap a0, b0, a1, b1;
+    const int* count;           // rows that have a target
+    const int* tgt;             // [count] their targets
+    int D, v0, Vp;              // the piece: columns v0 .. v0 + Vp of the vocabulary
+    int segs;                   // products of parts
+    unsigned int* err;
+    // kLoss
+    float2* part;               // [half tile][ld_part] maximum and sum of a row
+    float* tl;                  // [count] logit of the target
+    int64_t ld_part;
+    int tile0;                  // tiles of the pieces before
+    // kGrad
+    const float* lse;           // [count]
+    const float* g;             // [count] gradient of the loss
+    __nv_bfloat16* dl;          // [part][row][ld_dl]
+    int64_t ld_dl, dl_part;
+    // kOut
+    void* dw;
+    int64_t ld_dw;
+    bool dw_wide;               // 16-byte stores
+    float* dx;                  // [split][row][ld_dx]
+    int64_t ld_dx, dx_split;
+    int splits;
+    bool add;                   // dx has the earlier pieces' sums
+};
+
+struct PrepParams {
+    const void* hidden;
+    const int32_t* targets;
+    int64_t hidden_t, T, V;
+    int D, per;
+    bool wide;                  // rows of hidden begin on 16-byte boundaries
+    __nv_bfloat16* x;           // [part][row][ld_x]
+    int64_t ld_x, x_part;
+    int* count;
+    int* rows;                  // [count] row of hidden
+    int* tgt;
+    unsigned int* err;
+    float* loss_out;            // forward: zeros in rows without a target
+    float* lse_out;
+    const float* lse;           // backward
+    const float* dloss;
+    int64_t dloss_t;
+    float* lse_c;
+    float* g_c;
+    void* dhidden;
+    int64_t dhidden_t;
+};
+
+}  // namespace selscan

@@ -173,3 +173,60 @@ def ss_distill_grad(dloss, logits, ids, teacher, temperature=1.0, dlogits=None, 
     if st != 0:
         raise _ss.SelscanError(st, "ss_distill_grad")
     return loss, dlogits
+
+
+def _xent_args(hidden, weight, targets):
+    torch = _load()
+    _cuda(hidden, "hidden")
+    if hidden.dim() != 2 or weight.dim() != 2:
+        raise ValueError("hidden must be [tokens, D] and weight [V, D]")
+    T, D = hidden.shape
+    V = weight.shape[0]
+    io = hidden.dtype
+    s = _ss.XentStrides(_io(io), _rows(hidden, "hidden", io, (T, D)), _rows(weight, "weight", io, (V, D)), D, D, 1)
+    _param(targets, "targets", torch.int32, (T,))
+    return T, V, D, s
+
+
+def _xent_scratch(hidden, stream, T, V, D, s, backward):
+    return _scratch(hidden, stream, _ws_bytes("ss_linear_xent_workspace_size", hidden.get_device(), T, V, D, s.io_dtype, backward))
+
+
+def ss_linear_xent(hidden, weight, targets, stream=None):
+    """Softmax cross entropy over the vocabulary from the last layer's rows (ss_linear_xent): the logits
+    hidden @ weight.T are not kept.
+
+    hidden [tokens, D], weight [V, D] (float32 or bfloat16, the same); targets [tokens] int32, negative for a
+    row without one.  Returns (loss, lse), both [tokens] float32 and zero in rows without a target; lse is for
+    ss_linear_xent_bwd."""
+    T, V, D, s = _xent_args(hidden, weight, targets)
+    loss, lse = _empty((2, T), _load().float32, hidden.device, stream).unbind()
+    ws = _xent_scratch(hidden, stream, T, V, D, s, 0)
+    st = _ss.lib().ss_linear_xent(hidden.data_ptr(), weight.data_ptr(), targets.data_ptr(), loss.data_ptr(), lse.data_ptr(), T, V, D,
+                                  ctypes.byref(s), ws.data_ptr(), ws.numel(), _stream(hidden, stream))
+    if st != 0:
+        raise _ss.SelscanError(st, "ss_linear_xent")
+    return loss, lse
+
+
+def ss_linear_xent_bwd(dloss, hidden, weight, targets, lse, stream=None):
+    """Gradients of ss_linear_xent for given gradients of the losses (ss_linear_xent_bwd): dloss [tokens]
+    float32 (any stride, so an expanded value too), lse from the forward call.
+
+    Returns a dict: dhidden like hidden and dweight like weight."""
+    T, V, D, s = _xent_args(hidden, weight, targets)
+    f32, io, dev = _load().float32, hidden.dtype, hidden.device
+    if dloss.dtype is not f32:
+        raise TypeError(f"dloss must be float32, got {dloss.dtype}")
+    if dloss.shape != (T,):
+        raise ValueError(f"dloss must have shape ({T},), got {tuple(dloss.shape)}")
+    s.dloss_t = dloss.stride(0)
+    _param(lse, "lse", f32, (T,))
+    dhidden, dweight = _empty((T, D), io, dev, stream), _empty((V, D), io, dev, stream)
+    ws = _xent_scratch(hidden, stream, T, V, D, s, 1)
+    st = _ss.lib().ss_linear_xent_bwd(dloss.data_ptr(), hidden.data_ptr(), weight.data_ptr(), targets.data_ptr(), lse.data_ptr(),
+                                      dhidden.data_ptr(), dweight.data_ptr(), T, V, D, ctypes.byref(s), ws.data_ptr(), ws.numel(),
+                                      _stream(hidden, stream))
+    if st != 0:
+        raise _ss.SelscanError(st, "ss_linear_xent_bwd")
+    return dict(dhidden=dhidden, dweight=dweight)

@@ -92,6 +92,37 @@ def test_distill_refuses_on_host():
         assert call() == 4 and call(K=0, ids=None, t=None) == 4 and grad() == 4
 
 
+def test_linear_xent_refuses_on_host():
+    size = ss.lib().ss_linear_xent_workspace_size
+
+    def fwd(h=FAKE, w=FAKE, t=FAKE, loss=FAKE, lse=FAKE, T=4, V=10, D=8, s=None, ws=FAKE, nws=1 << 40):
+        return ss.lib().ss_linear_xent(h, w, t, loss, lse, T, V, D, s, ws, nws, None)
+
+    def bwd(g=FAKE, h=FAKE, w=FAKE, t=FAKE, lse=FAKE, dh=FAKE, dw=FAKE, T=4, V=10, D=8, s=None, ws=FAKE, nws=1 << 40):
+        return ss.lib().ss_linear_xent_bwd(g, h, w, t, lse, dh, dw, T, V, D, s, ws, nws, None)
+    for f, back in ((fwd, 0), (bwd, 1)):
+        assert f(T=-1) == 1 and f(V=0) == 1 and f(D=0) == 1 and f(V=-3) == 1
+        assert f(T=1 << 30) == 2 and f(V=1 << 30) == 2 and f(D=1 << 20) == 2
+        for k in ("h", "w", "t", "lse", "ws"):
+            assert f(**{k: None}) == 1, k
+        for k in ("h", "w", "t", "lse"):
+            assert f(**{k: FAKE + 1}) == 3, k
+        assert f(ws=FAKE + 128) == 3 and f(nws=1000) == 1 and f(nws=size(4, 10, 8, 0, back)) in (4, 1)
+        assert f(s=ctypes.byref(ss.XentStrides(5, 8, 8, 8, 8, 1))) == 1
+        assert f(s=ctypes.byref(ss.XentStrides(0, -8, 8, 8, 8, 1))) == 1
+        assert f(s=ctypes.byref(ss.XentStrides(0, 8, 7, 8, 8, 1))) == 1                          # rows of weight run into each other
+        if _no_gpu():
+            assert f() == 4
+    assert fwd(T=0) == 0 and fwd(loss=None) == 1
+    for k in ("g", "dh", "dw"):
+        assert bwd(**{k: None}) == 1 and bwd(**{k: FAKE + 1}) == 3, k
+    assert bwd(s=ctypes.byref(ss.XentStrides(0, 8, 8, 7, 8, 1))) == 1 and bwd(s=ctypes.byref(ss.XentStrides(0, 8, 8, 8, 7, 1))) == 1
+    assert bwd(s=ctypes.byref(ss.XentStrides(0, 8, 8, 8, 8, -1))) == 1
+    assert size(0, 10, 8, 0, 0) == 0 and size(4, 0, 8, 0, 0) == 0 and size(4, 10, 8, 9, 0) == 0
+    # the workspace does not grow with the vocabulary beyond a piece of it
+    assert size(4096, 1 << 20, 2048, ss.SS_BF16, 1) < (1 << 30) < 4096 * (1 << 20) * 2
+
+
 def test_binding_refuses_cpu_tensors():
     torch = pytest.importorskip("torch")
     x, w = torch.zeros(2, 64), torch.ones(64)
@@ -99,7 +130,9 @@ def test_binding_refuses_cpu_tensors():
     for f in (lambda: ss.ss_add_layernorm(x, w), lambda: ss.ss_add_layernorm(x, w, residual=x),
               lambda: ss.ss_add_layernorm_bwd(x, x, w, one, one), lambda: ss.ss_conv1d_bwd(x[None], x[None], torch.zeros(64, 4)),
               lambda: ss.ss_distill(x, torch.zeros(2, 1, dtype=torch.int32), x[:, :1]),
-              lambda: ss.ss_distill_grad(one, x, torch.zeros(2, 1, dtype=torch.int32), x[:, :1])):
+              lambda: ss.ss_distill_grad(one, x, torch.zeros(2, 1, dtype=torch.int32), x[:, :1]),
+              lambda: ss.ss_linear_xent(x, x, torch.zeros(2, dtype=torch.int32)),
+              lambda: ss.ss_linear_xent_bwd(one, x, x, torch.zeros(2, dtype=torch.int32), one)):
         with pytest.raises(ValueError):
             f()
 
