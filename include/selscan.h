@@ -741,8 +741,8 @@ typedef struct {
  *                       hidden values are not read.  A target of V or more sets bit 2 of the device error
  *                       word and is none either.
  *   workspace           256-byte aligned, ss_linear_xent_workspace_size(tokens, V, D, io_dtype, 0) bytes
- * Sums are fp32.  Products take bf16 operands as they are and fp32 ones as sums of three bf16, which are 24
- * bits together.  A row with a NaN or an infinity has a NaN or infinite loss, without effect on others.
+ * Sums are fp32.  Products take bf16 operands as they are and fp32 ones as sums of two fp16, scaled by a power
+ * of two per tensor (22 bits, and 2^-39 of the tensor's largest finite value at least).  A row with a NaN or an infinity has a NaN or infinite loss, without effect on others.
  * tokens, V and D up to SS_XENT_MAX_*.  strides NULL: fp32, contiguous.
  */
 ss_status ss_linear_xent(const void* hidden, const void* weight, const int32_t* targets, float* loss,
@@ -757,8 +757,8 @@ ss_status ss_linear_xent(const void* hidden, const void* weight, const int32_t* 
  *   lse                 from the forward call on the same hidden, weight and targets
  *   workspace           256-byte aligned, ss_linear_xent_workspace_size(tokens, V, D, io_dtype, 1) bytes
  * Rows without a target have a dhidden of zero and no part in dweight, whatever their hidden, lse and dloss.
- * The logits are computed again, a piece of the vocabulary at a time; dl is an operand in bf16 for bf16
- * tensors (half a step, 2^-9 of its value) and in three for fp32 ones.  Deterministic.  tokens == 0 sets
+ * The logits are computed again, a piece of the vocabulary at a time.  Operands, dl among them, are fp16 scaled by a
+ * power of two per tensor, one for bf16 tensors (dl to 11 bits) and two for fp32 ones.  Deterministic.  tokens == 0 sets
  * dweight to zero.  Outputs must not overlap anything else.
  */
 ss_status ss_linear_xent_bwd(const float* dloss, const void* hidden, const void* weight,

@@ -7,14 +7,18 @@
 // tiles by pairs of CTAs (tc_pair.cuh).  Rows without a target are left out before the first product: the others
 // are gathered into rows of their own, and the products' sizes come from their count in device memory.
 //   forward    the logits' tiles go from tensor memory into a maximum and a sum per row and half tile
-//   backward   the logits again, piece by piece of the vocabulary; a piece's dl is kept in bf16 (in the workspace,
-//              not the logits: kPieceBytes of it), then both products over it in one launch: dweight's rows of
-//              the piece, whole, and dhidden as sums in fp32 that grow from piece to piece
-// float32 operands are taken as sums of three bf16 (24 bits) and a product as the six products of them that
-// count: the same kernel with six times the K.
+//   backward   the logits again, piece by piece of the vocabulary; a piece's dl is kept in fp16 (in the workspace:
+//              kPieceBytes of it), then both products over it in one launch: dweight's rows of the piece, whole, and
+//              dhidden as sums in fp32 that grow from piece to piece
+// Operands.  bf16 logits of the forward pass: as they are.  Everything else is taken in fp16, scaled by one power of
+// two per tensor so that its largest value lies below 2^15: a bf16 value is exact there down to 2^-31 of the
+// largest, and dl has 11 bits instead of bf16's 8 (in bf16 its rounding would add to the gradients' error as much as
+// their own does: 2.9e-3 instead of 1.7e-3).  A float32 value is the sum of two fp16 (22 bits), and a product the
+// three products of these that count (K three times as long; three parts of bf16 would take six).
 //
 // One persistent CTA pair per two SMs: a warp that loads (TMA, six stages of 2 x 16 KB), one that issues, eight
 // that empty the other of two accumulators meanwhile.
+#include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
@@ -47,13 +51,28 @@ constexpr int kGroup = 16;                        // tiles of rows that share a 
 constexpr uint32_t kAccCols = 256;
 // Steps of K that one accumulator takes before its sums go into registers.  The tensor core cuts each addition of
 // 16 products off at 2^-23 of the sum instead of rounding it, so a long chain is off by its length times half of
-// that, to one side: 560 additions gave a dhidden off by 1e-5.  64 in a row leave 1e-6, and the registers' own
-// additions round.
-constexpr int kChain = 16;
+// that, to one side: 560 additions gave a dhidden off by 1e-5, 64 in a row 1e-6.  The registers' own additions
+// round.  Results in fp32 take 16 (32 the loss) in a row, those that end in bf16 64.
+template <Product P, bool F32> constexpr int kChain = F32 ? 4 : P == Product::kLoss ? 8 : 16;
 
-// The products of three-part operands that count, small ones first (the largest alone has the long chain).
-__constant__ int8_t kPartA[6] = {0, 2, 1, 0, 1, 0};
-__constant__ int8_t kPartB[6] = {2, 0, 1, 1, 0, 0};
+// The products of two-part operands that count, small ones first.
+constexpr int kSegs = 3;
+__constant__ int8_t kPartA[kSegs] = {0, 1, 0};
+__constant__ int8_t kPartB[kSegs] = {1, 0, 0};
+
+// Exponent n of the power of two that a tensor's values are divided by, from the bits of its largest finite one: what
+// is left is below 2^15.  2^n and 2^-n are normal floats.
+__device__ __forceinline__ int scale_exp(unsigned int bits) { return min(max(static_cast<int>(bits >> 23) - 127 - 14, -126), 126); }
+__device__ __forceinline__ float pow2(int n) { return __int_as_float((n + 127) << 23); }
+// 2^n for n of -252 to 252 as a product of two floats (the second 1 where one is enough).
+struct Pow2x2 {
+    float a, b;
+    __device__ __forceinline__ explicit Pow2x2(int n) {
+        const int h = min(max(n, -126), 126);
+        a = pow2(h);
+        b = pow2(n - h);
+    }
+};
 
 struct GemmShared {
     uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
@@ -62,7 +81,10 @@ struct GemmShared {
 };
 constexpr size_t kGemmSmem = kStages * kStageBytes + sizeof(GemmShared) + 1024;
 
-// A unit of work: a tile and a range of steps of K (each of them p.segs products of parts).
+// Whether the operands are bf16 as they are (else scaled fp16).
+template <Product P, bool F32> constexpr bool kRaw = P == Product::kLoss && !F32;
+
+// A unit of work: a tile and a range of steps of K (each of them kSegs products of parts for F32).
 struct Unit {
     int job, m, n, k0, k1, split;
 };
@@ -129,32 +151,19 @@ __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f 
 
 __device__ __forceinline__ void store16(void* q, uint4 v) { *reinterpret_cast<uint4*>(q) = v; }
 
-// 32 values of a row to bf16 (parts: what is left, and what is left of that); n of them exist.  The addresses are
-// 16-byte aligned and groups of 8 whole or not there (a row's padding may be written).
+__device__ __forceinline__ uint32_t half_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+
+// 8 values to fp16, and (F32) what is left of them to the second part.
 template <bool F32>
-__device__ __forceinline__ void store_parts(__nv_bfloat16* q, int64_t part, int n, const float (&v)[32]) {
+__device__ __forceinline__ void store_half8(__half* q, int64_t part, const float2 (&f)[4]) {
+    __half2 h[4];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        if (g * 8 >= n) break;
-        float2 f[4];
-        uint32_t h[4];
+    for (int i = 0; i < 4; ++i) h[i] = __float22half2_rn(f[i]);
+    store16(q, make_uint4(half_bits(h[0]), half_bits(h[1]), half_bits(h[2]), half_bits(h[3])));
+    if constexpr (F32) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[i] = make_float2(v[g * 8 + 2 * i], v[g * 8 + 2 * i + 1]);
-            h[i] = pack_bf16(f[i].x, f[i].y);
-        }
-        store16(q + g * 8, make_uint4(h[0], h[1], h[2], h[3]));
-        if constexpr (F32) {
-#pragma unroll
-            for (int part_i = 1; part_i < 3; ++part_i) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    f[i] = fma2(unpack2(h[i]), splat2(-1.f), f[i]);
-                    h[i] = pack_bf16(f[i].x, f[i].y);
-                }
-                store16(q + part_i * part + g * 8, make_uint4(h[0], h[1], h[2], h[3]));
-            }
-        }
+        for (int i = 0; i < 4; ++i) h[i] = __float22half2_rn(fma2(__half22float2(h[i]), splat2(-1.f), f[i]));
+        store16(q + part, make_uint4(half_bits(h[0]), half_bits(h[1]), half_bits(h[2]), half_bits(h[3])));
     }
 }
 
@@ -188,6 +197,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
     const uint32_t tmem = sh.tmem;
     const int rows = *p.count;
     const Work work = make_work<P>(p, rows);
+    int ex = 0, ew = 0, eg = 0;
+    if constexpr (!kRaw<P, F32>) {
+        ex = scale_exp(p.range[kRangeX]);
+        ew = scale_exp(p.range[kRangeW]);
+        if constexpr (P != Product::kLoss) eg = scale_exp(p.range[kRangeG]);
+    }
 
     if (warp == kEpiWarps) {
         // ---------------------------------------------------------------- loads, by one thread of each CTA
@@ -205,10 +220,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                 const bool a_mn = P == Product::kOut && u.job == 0, b_mn = P == Product::kOut;
                 const int am = u.m * kTile + static_cast<int>(rank) * kHalf, bn = u.n * kTile + static_cast<int>(rank) * kHalf;
                 bool go = true;
-                for (int kc = u.k0; kc < u.k1 && go; kc += kChain)
-                    for (int seg = 0; seg < (F32 ? 6 : 1) && go; ++seg) {
+                for (int kc = u.k0; kc < u.k1 && go; kc += kChain<P, F32>)
+                    for (int seg = 0; seg < (F32 ? kSegs : 1) && go; ++seg) {
                         const int pa = F32 ? kPartA[seg] : 0, pb = F32 ? kPartB[seg] : 0;
-                        for (int k = kc; k < min(kc + kChain, u.k1); ++k) {
+                        for (int k = kc; k < min(kc + kChain<P, F32>, u.k1); ++k) {
                             go = mbar_sleep_bounded(&sh.empty[st], ph ^ 1, abort, p.err);
                             if (!go) break;
                             if (rank == 0) mbar_expect_tx(&sh.full[st], 2 * kStageBytes);
@@ -254,11 +269,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
             for (int64_t i = cluster; i < work.total && go; i += clusters) {
                 const Unit u = unit_of<P>(work, i);
                 const bool a_mn = P == Product::kOut && u.job == 0, b_mn = P == Product::kOut;
-                const uint32_t idesc = tc_idesc(256, 256, a_mn, b_mn);
+                constexpr uint32_t kBf16 = 1u << 7 | 1u << 10;                          // operand types (else fp16)
+                const uint32_t idesc = tc_idesc(256, 256, a_mn, b_mn) & ~(kRaw<P, F32> ? 0u : kBf16);
                 const uint32_t la = a_mn ? kOperand / 2 : 16, lb = b_mn ? kOperand / 2 : 16, ka = a_mn ? 2048 : 32, kb = b_mn ? 2048 : 32;
-                for (int kc = u.k0; kc < u.k1 && go; kc += kChain, ++turn) {
+                for (int kc = u.k0; kc < u.k1 && go; kc += kChain<P, F32>, ++turn) {
                     const uint32_t d = tmem + (turn & 1) * kAccCols;
-                    const int n = (min(kc + kChain, u.k1) - kc) * (F32 ? 6 : 1);
+                    const int n = (min(kc + kChain<P, F32>, u.k1) - kc) * (F32 ? kSegs : 1);
                     go = mbar_sleep_bounded(&sh.acc_empty[turn & 1], ((turn >> 1) & 1) ^ 1, abort, p.err);
                     tc_fence_after();
                     for (int k = 0; k < n && go; ++k) {
@@ -291,7 +307,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
 #pragma unroll
             for (int j = 0; j < kHalf; ++j) acc[j] = 0.f;
 #pragma unroll 1
-            for (int kc = u.k0; kc < u.k1; kc += kChain, ++turn) {
+            for (int kc = u.k0; kc < u.k1; kc += kChain<P, F32>, ++turn) {
                 go = __all_sync(0xffffffffu, mbar_sleep_bounded(&sh.acc_full[turn & 1], (turn >> 1) & 1, abort, p.err));
                 if (!go) break;
                 tc_fence_after();
@@ -315,6 +331,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
             const int row = u.m * kTile + static_cast<int>(rank) * kHalf + quarter * 32 + lane;
             const int col0 = u.n * kTile + half * kHalf;
             if constexpr (P == Product::kLoss) {
+                if constexpr (F32) {
+                    const Pow2x2 f(ex + ew);
+#pragma unroll
+                    for (int j = 0; j < kHalf; ++j) acc[j] = acc[j] * f.a * f.b;
+                }
                 float m = -INFINITY, s = 0.f;
                 const int tgt = row < rows ? p.tgt[row] - p.v0 - col0 : -1;
 #pragma unroll
@@ -346,34 +367,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                 if (row < rows) p.part[(static_cast<int64_t>(p.tile0 + u.n) * 2 + half) * p.ld_part + row] = make_float2(m, s);
             } else if constexpr (P == Product::kGrad) {
                 const bool ok = row < rows;
-                const float lse = ok ? p.lse[row] : 0.f, g = ok ? p.g[row] : 0.f;
+                const float lse = ok ? p.lse[row] : 0.f, g = ok ? p.g[row] * pow2(-eg) : 0.f;
                 const int tgt = ok ? p.tgt[row] - p.v0 - col0 : -1;
-                __nv_bfloat16* out = p.dl + static_cast<int64_t>(row) * p.ld_dl + col0;
-                const float2 off = splat2(-lse), l2e = splat2(kLog2e), g2 = splat2(g);
+                __half* out = p.dl + static_cast<int64_t>(row) * p.ld_dl + col0;
+                const Pow2x2 f(ex + ew);
+                const float2 off = splat2(-lse), f2 = splat2(f.a), l2e = splat2(kLog2e), g2 = splat2(g);
+                if (f.b != 1.f) {
 #pragma unroll
-                for (int c = 0; c < kHalf; c += 32) {
-                    const int n = p.Vp - col0 - c;
-                    if (n <= 0) break;
-                    float v[32];
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float2 e = ex2x2(mul2(add2(make_float2(acc[c + j], acc[c + j + 1]), off), l2e));
-                        v[j] = e.x;
-                        v[j + 1] = e.y;
-                    }
-                    if (tgt >= c && tgt < c + 32) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] -= tgt - c == j ? 1.f : 0.f;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float2 e = mul2(make_float2(v[j], v[j + 1]), g2);
-                        v[j] = ok ? e.x : 0.f;
-                        v[j + 1] = ok ? e.y : 0.f;
-                    }
-                    store_parts<F32>(out + c, p.dl_part, n, v);
+                    for (int j = 0; j < kHalf; ++j) acc[j] *= f.b;
                 }
-            } else if (u.job) {
+#pragma unroll
+                for (int c = 0; c < kHalf; c += 8) {
+                    if (c >= p.Vp - col0) break;                          // (a row's padding to 8 columns may be written)
+                    float2 e[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        e[j] = ex2x2(mul2(fma2(make_float2(acc[c + 2 * j], acc[c + 2 * j + 1]), f2, off), l2e));
+                    if (tgt >= c && tgt < c + 8) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            e[j].x -= tgt - c == 2 * j ? 1.f : 0.f;
+                            e[j].y -= tgt - c == 2 * j + 1 ? 1.f : 0.f;
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        e[j] = mul2(e[j], g2);
+                        if (!ok) e[j] = splat2(0.f);
+                    }
+                    store_half8<F32>(out + c, p.dl_part, e);
+                }
+            } else {
+              const Pow2x2 f(eg + (u.job ? ew : ex));
+#pragma unroll
+              for (int j = 0; j < kHalf; ++j) acc[j] = acc[j] * f.a * f.b;
+              if (u.job) {
                 if (row < rows) {
                     float* out = p.dx + u.split * p.dx_split + static_cast<int64_t>(row) * p.ld_dx + col0;
                     const int n = p.D - col0;
@@ -389,7 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                         *q = v;
                     }
                 }
-            } else if (row < p.Vp) {
+              } else if (row < p.Vp) {
                 using T = std::conditional_t<F32, float, __nv_bfloat16>;
                 T* out = static_cast<T*>(p.dw) + static_cast<int64_t>(p.v0 + row) * p.ld_dw + col0;
                 const int n = p.D - col0;
@@ -410,6 +438,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                     for (int j = 0; j < kHalf; ++j)
                         if (j < n) out[j] = from_f32<T>(acc[j]);
                 }
+              }
             }
         }
     }
@@ -427,43 +456,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
 
 constexpr int kPrepThreads = 256;
 
-template <typename T> __device__ __forceinline__ float load_f32(const T* q) { return to_f32<T>(*q); }
-
-// Columns [c, c + 8) of a row to one or three bf16 parts; columns of D and more are zero.
-template <typename T, bool F32>
-__device__ __forceinline__ void pack8(const T* row, __nv_bfloat16* out, int64_t part, int c, int D, bool wide) {
+// Columns [c, c + 8) of a row as an operand: bf16 as it is (RAW), or fp16 times `scale`, in two parts for fp32.
+// Columns of D and more are zero.
+template <typename T, bool RAW>
+__device__ __forceinline__ void pack8(const T* row, __half* out, int64_t part, int c, int D, bool wide, float scale) {
     float v[8];
     if (wide && c + 8 <= D) {
         if constexpr (sizeof(T) == 2) {
-            store16(out + c, *reinterpret_cast<const uint4*>(row + c));
-            return;
+            const uint4 u = *reinterpret_cast<const uint4*>(row + c);
+            if constexpr (RAW) {
+                store16(out + c, u);
+                return;
+            }
+            const uint32_t a[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = bf16_lo(a[i]);
+                v[2 * i + 1] = bf16_hi(a[i]);
+            }
         } else {
             const float4 a = *reinterpret_cast<const float4*>(row + c), b = *reinterpret_cast<const float4*>(row + c + 4);
             v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c + i < D ? load_f32<T>(row + c + i) : 0.f;
+        for (int i = 0; i < 8; ++i) v[i] = c + i < D ? to_f32<T>(row[c + i]) : 0.f;
     }
-    float2 f[4];
-    uint32_t h[4];
+    if constexpr (RAW) {
+        store16(out + c, make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])));
+    } else {
+        float2 f[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[i] = make_float2(v[2 * i], v[2 * i + 1]);
-        h[i] = pack_bf16(f[i].x, f[i].y);
+        for (int i = 0; i < 4; ++i) f[i] = make_float2(v[2 * i] * scale, v[2 * i + 1] * scale);
+        store_half8<sizeof(T) == 4>(out + c, part, f);
     }
-    store16(out + c, make_uint4(h[0], h[1], h[2], h[3]));
-    if constexpr (F32) {
+}
+
+// Largest finite magnitudes (as bits, whose order is the floats') of hidden's rows with a target, of weight and
+// of dloss: blocks of rows of hidden, then of weight.
+template <typename T>
+__device__ __forceinline__ unsigned int row_range(const T* row, int D, bool wide, unsigned int m) {
+    auto take = [&](unsigned int bits) {
+        bits &= 0x7fffffffu;
+        m = max(m, bits < 0x7f800000u ? bits : 0u);
+    };
+    constexpr int N = 16 / sizeof(T);
+    const int vecs = wide ? D / N : 0;
+    for (int i = threadIdx.x % 32; i < vecs; i += 32) {
+        const uint4 u = reinterpret_cast<const uint4*>(row)[i];
+        const uint32_t a[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int q = 1; q < 3; ++q) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f[i] = fma2(unpack2(h[i]), splat2(-1.f), f[i]);
-                h[i] = pack_bf16(f[i].x, f[i].y);
-            }
-            store16(out + q * part + c, make_uint4(h[0], h[1], h[2], h[3]));
+        for (int j = 0; j < 4; ++j) {
+            take(sizeof(T) == 2 ? a[j] << 16 : a[j]);
+            if constexpr (sizeof(T) == 2) take(a[j] & 0xffff0000u);
         }
     }
+    for (int c = vecs * N + threadIdx.x % 32; c < D; c += 32) take(__float_as_uint(to_f32<T>(row[c])));
+    return m;
+}
+template <typename T>
+__global__ void __launch_bounds__(kPrepThreads) xent_range_kernel(const PrepParams p, const T* w, int64_t w_v, bool w_wide, int x_blocks) {
+    __shared__ unsigned int part[3];
+    if (threadIdx.x < 3) part[threadIdx.x] = 0u;
+    __syncthreads();
+    constexpr int kWarps = kPrepThreads / 32;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    unsigned int m = 0u, g = 0u;
+    const bool x = static_cast<int>(blockIdx.x) < x_blocks;
+    if (x) {
+        for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.T; t += static_cast<int64_t>(x_blocks) * kWarps) {
+            const int v = p.targets[t];
+            if (v < 0 || v >= p.V) continue;
+            m = row_range<T>(static_cast<const T*>(p.hidden) + t * p.hidden_t, p.D, p.wide, m);
+            if (p.dloss && lane == 0) {
+                const unsigned int bits = __float_as_uint(p.dloss[t * p.dloss_t]) & 0x7fffffffu;
+                g = max(g, bits < 0x7f800000u ? bits : 0u);
+            }
+        }
+    } else {
+        const int64_t first = static_cast<int64_t>(blockIdx.x - x_blocks) * kWarps + warp, step = static_cast<int64_t>(gridDim.x - x_blocks) * kWarps;
+        for (int64_t v = first; v < p.V; v += step) m = row_range<T>(w + v * w_v, p.D, w_wide, m);
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    g = __reduce_max_sync(0xffffffffu, g);
+    if (lane == 0) {
+        atomicMax(&part[x ? kRangeX : kRangeW], m);
+        atomicMax(&part[kRangeG], g);
+    }
+    __syncthreads();
+    if (threadIdx.x < 3 && part[threadIdx.x]) atomicMax(&p.range[threadIdx.x], part[threadIdx.x]);
 }
 
 // Sum over the block, in every thread.
@@ -481,7 +562,8 @@ __device__ __forceinline__ int block_sum(int v, int* slot) {
 // hidden and counts the targets before them itself.
 template <typename T, bool BWD>
 __global__ void __launch_bounds__(kPrepThreads) xent_gather_kernel(const PrepParams p) {
-    constexpr bool F32 = sizeof(T) == 4;
+    constexpr bool F32 = sizeof(T) == 4, RAW = !F32 && !BWD;
+    const float scale = RAW ? 1.f : pow2(-scale_exp(p.range[kRangeX]));
     __shared__ int slot[kPrepThreads / 32];
     const int64_t first = static_cast<int64_t>(blockIdx.x) * p.per, last = min(first + p.per, p.T);
     int before = 0;
@@ -494,8 +576,8 @@ __global__ void __launch_bounds__(kPrepThreads) xent_gather_kernel(const PrepPar
         const int v = p.targets[t];
         if (v >= 0 && v < p.V) {
             const T* src = static_cast<const T*>(p.hidden) + t * p.hidden_t;
-            __nv_bfloat16* dst = p.x + static_cast<int64_t>(at) * p.ld_x;
-            for (int c = threadIdx.x * 8; c < p.D; c += kPrepThreads * 8) pack8<T, F32>(src, dst, p.x_part, c, p.D, p.wide);
+            __half* dst = p.x + static_cast<int64_t>(at) * p.ld_x;
+            for (int c = threadIdx.x * 8; c < p.D; c += kPrepThreads * 8) pack8<T, RAW>(src, dst, p.x_part, c, p.D, p.wide, scale);
             if (threadIdx.x == 0) {
                 p.rows[at] = static_cast<int>(t);
                 p.tgt[at] = v;
@@ -517,20 +599,21 @@ __global__ void __launch_bounds__(kPrepThreads) xent_gather_kernel(const PrepPar
         if (threadIdx.x == 0) *p.count = at;
         // the rest of the last step of K over the tokens counts for nothing, but must be finite
         const int end = (at + kStep - 1) / kStep * kStep, vecs = static_cast<int>(p.ld_x / 8);
-        for (int q = 0; q < (F32 ? 3 : 1); ++q)
+        for (int q = 0; q < (F32 ? 2 : 1); ++q)
             for (int i = threadIdx.x; i < (end - at) * vecs; i += kPrepThreads)
                 store16(p.x + q * p.x_part + (at + i / vecs) * p.ld_x + i % vecs * 8, make_uint4(0u, 0u, 0u, 0u));
     }
 }
 
-// Rows of weight as operands of the products (where they cannot be loaded as they lie).
-template <typename T>
-__global__ void __launch_bounds__(kPrepThreads) xent_pack_kernel(const T* w, int64_t stride, __nv_bfloat16* out, int64_t ld, int64_t part,
-                                                                 int64_t n, int D, bool wide) {
+// Rows of weight as operands of the products.
+template <typename T, bool RAW>
+__global__ void __launch_bounds__(kPrepThreads) xent_pack_kernel(const T* w, int64_t stride, __half* out, int64_t ld, int64_t part, int64_t n, int D,
+                                                                 bool wide, const unsigned int* range) {
     const int vecs = static_cast<int>(ld / 8);
+    const float scale = RAW ? 1.f : pow2(-scale_exp(range[kRangeW]));
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPrepThreads + threadIdx.x; i < n * vecs; i += static_cast<int64_t>(gridDim.x) * kPrepThreads) {
         const int64_t r = i / vecs;
-        pack8<T, sizeof(T) == 4>(w + r * stride, out + r * ld, part, static_cast<int>(i - r * vecs) * 8, D, wide);
+        pack8<T, RAW>(w + r * stride, out + r * ld, part, static_cast<int>(i - r * vecs) * 8, D, wide, scale);
     }
 }
 
@@ -586,6 +669,7 @@ using host::range3;
 constexpr int64_t kPieceBytes = 256 << 20;        // of dl (and of a packed piece of weight)
 constexpr int64_t kMinPiece = 4096;               // columns: below, the sums of dhidden cost as much as the products
 constexpr int64_t kMaxSplits = 32;
+constexpr int64_t kMinSteps = 16;                 // of K to a slice of dhidden's sums
 
 int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
@@ -601,7 +685,7 @@ int sm_count() {
 // Where everything lies in the workspace.
 struct Layout {
     int64_t parts, segs, ld_x, tpad, piece, pieces, splits, ld_dl, ld_dx, halves;
-    size_t count, rows, tgt, lse, g, tl, part, x, w, dl, dx, total;
+    size_t count, range, rows, tgt, lse, g, tl, part, x, w, dl, dx, total;
 };
 
 // Time of one launch of both products over a piece, in steps of K, when dhidden's are cut in `splits`: units in
@@ -622,11 +706,12 @@ int64_t out_cost(int64_t T, int64_t D, int64_t Vp, int64_t segs, int64_t splits,
     return worst + splits * T * D * 8 / (2 << 20);
 }
 
-Layout layout(int64_t T, int64_t V, int64_t D, bool f32, bool packed, bool bwd) {
+Layout layout(int64_t T, int64_t V, int64_t D, bool f32, bool in_place, bool bwd) {
+    const bool packed = f32 || bwd || !in_place;
     Layout q;
     std::memset(&q, 0, sizeof(q));
-    q.parts = f32 ? 3 : 1;
-    q.segs = f32 ? 6 : 1;
+    q.parts = f32 ? 2 : 1;
+    q.segs = f32 ? kSegs : 1;
     q.ld_x = round_up(D, 8);
     q.tpad = round_up(T, kTile);
     const int64_t per_col = std::max(bwd ? q.tpad * 2 * q.parts : 0, packed ? q.ld_x * 2 * q.parts : 0);
@@ -645,7 +730,7 @@ Layout layout(int64_t T, int64_t V, int64_t D, bool f32, bool packed, bool bwd) 
     if (bwd) {
         const int64_t pairs = sm_count() / 2;
         int64_t best = -1;
-        for (int64_t s = 1; s <= kMaxSplits && (s == 1 || (q.piece / kStep / s >= kChain && s * q.tpad * q.ld_dx * 4 <= 2 * kPieceBytes)); ++s) {
+        for (int64_t s = 1; s <= kMaxSplits && (s == 1 || (q.piece / kStep / s >= kMinSteps && s * q.tpad * q.ld_dx * 4 <= 2 * kPieceBytes)); ++s) {
             const int64_t c = out_cost(T, D, q.piece, q.segs, s, pairs);
             if (best < 0 || c < best) {
                 best = c;
@@ -660,6 +745,7 @@ Layout layout(int64_t T, int64_t V, int64_t D, bool f32, bool packed, bool bwd) 
         return o;
     };
     q.count = take(4);
+    q.range = take(12);
     q.rows = take(4 * q.tpad);
     q.tgt = take(4 * q.tpad);
     if (bwd) {
@@ -692,7 +778,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// [parts][rows][cols] of bf16, boxes of 64 columns and `box_rows` rows, 128-byte swizzle, zeros outside.
+// [parts][rows][cols] of 16 bits, boxes of 64 columns and `box_rows` rows, 128-byte swizzle, zeros outside.
 bool make_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t parts, int64_t ld, int64_t part, int box_rows) {
     auto enc = encode_fn();
     if (!enc) return false;
@@ -782,7 +868,7 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
         return SS_ERR_INVALID_ARG;
     }
     const bool in_place = loads_in_place(c.weight, s.weight_v, s.io_dtype);
-    const Layout q = layout(std::max<int64_t>(T, 1), V, D, f32, !in_place, c.bwd);
+    const Layout q = layout(std::max<int64_t>(T, 1), V, D, f32, in_place, c.bwd);
     if (T > 0 && (!workspace || workspace_bytes < q.total)) return SS_ERR_INVALID_ARG;
     const void* words[] = {c.targets, c.dloss, c.lse_in, c.loss, c.lse};
     for (const void* a : words)
@@ -817,9 +903,9 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
 
     char* ws = static_cast<char*>(workspace);
     auto f32_at = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
-    __nv_bfloat16* x = reinterpret_cast<__nv_bfloat16*>(ws + q.x);
-    __nv_bfloat16* w = reinterpret_cast<__nv_bfloat16*>(ws + q.w);
-    __nv_bfloat16* dl = reinterpret_cast<__nv_bfloat16*>(ws + q.dl);
+    __half* x = reinterpret_cast<__half*>(ws + q.x);
+    __half* w = reinterpret_cast<__half*>(ws + q.w);
+    __half* dl = reinterpret_cast<__half*>(ws + q.dl);
     const int64_t x_part = q.tpad * q.ld_x, w_part = q.piece * q.ld_x, dl_part = q.tpad * q.ld_dl;
     auto wide = [&](const void* a, int64_t stride) { return is_aligned(a, 16) && (stride * es) % 16 == 0; };
 
@@ -832,6 +918,19 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
     g.lse = c.lse_in; g.dloss = c.dloss; g.dloss_t = s.dloss_t; g.lse_c = f32_at(q.lse); g.g_c = f32_at(q.g);
     g.dhidden = c.dhidden; g.dhidden_t = s.dhidden_t; g.loss_out = c.loss; g.lse_out = c.lse;
     g.err = device_error_word();
+    g.range = reinterpret_cast<unsigned int*>(ws + q.range);
+    const bool raw = !f32 && !c.bwd;
+    if (!raw) {
+        if (cudaMemsetAsync(g.range, 0, 12, st) != cudaSuccess) return SS_ERR_CUDA;
+        const int64_t warps = kPrepThreads / 32, most = 4 * sm_count();
+        const int xb = static_cast<int>(std::min((T + warps - 1) / warps, most)), wb = static_cast<int>(std::min((V + warps - 1) / warps, most));
+        const bool ww = wide(c.weight, s.weight_v);
+        if (f32)
+            xent_range_kernel<float><<<xb + wb, kPrepThreads, 0, st>>>(g, static_cast<const float*>(c.weight), s.weight_v, ww, xb);
+        else
+            xent_range_kernel<__nv_bfloat16><<<xb + wb, kPrepThreads, 0, st>>>(g, static_cast<const __nv_bfloat16*>(c.weight), s.weight_v, ww, xb);
+        if (cudaGetLastError() != cudaSuccess) return SS_ERR_CUDA;
+    }
     void (*gather)(PrepParams) = f32 ? (c.bwd ? xent_gather_kernel<float, true> : xent_gather_kernel<float, false>)
                                      : (c.bwd ? xent_gather_kernel<__nv_bfloat16, true> : xent_gather_kernel<__nv_bfloat16, false>);
     gather<<<static_cast<unsigned>((T + g.per - 1) / g.per), kPrepThreads, 0, st>>>(g);
@@ -839,7 +938,7 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
 
     XentParams p;
     std::memset(&p, 0, sizeof(p));
-    p.count = g.count; p.tgt = g.tgt; p.D = static_cast<int>(D); p.segs = static_cast<int>(q.segs); p.err = g.err;
+    p.count = g.count; p.tgt = g.tgt; p.D = static_cast<int>(D); p.range = g.range; p.err = g.err;
     p.part = reinterpret_cast<float2*>(ws + q.part); p.ld_part = q.tpad; p.tl = f32_at(q.tl);
     p.lse = g.lse_c; p.g = g.g_c; p.dl = dl; p.ld_dl = q.ld_dl; p.dl_part = dl_part;
     p.dw = c.dweight; p.ld_dw = s.dweight_v; p.dw_wide = c.bwd && D % 8 == 0 && wide(c.dweight, s.dweight_v);
@@ -849,14 +948,17 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
         const int64_t Vp = std::min(q.piece, V - v0), vt = (Vp + kTile - 1) / kTile;
         const void* wp = static_cast<const char*>(c.weight) + v0 * s.weight_v * es;
         int64_t ld_w = s.weight_v;
-        if (!in_place) {
-            const unsigned grid = static_cast<unsigned>(std::min<int64_t>((Vp * q.ld_x / 8 + kPrepThreads - 1) / kPrepThreads, 8 * sm_count()));
+        if (!raw || !in_place) {
+            const unsigned grid = static_cast<unsigned>(std::min<int64_t>((Vp * q.ld_x / 8 + kPrepThreads - 1) / kPrepThreads, 16 * sm_count()));
+            const bool ww = wide(wp, s.weight_v);
+            const __nv_bfloat16* wb = static_cast<const __nv_bfloat16*>(wp);
             if (f32)
-                xent_pack_kernel<float><<<grid, kPrepThreads, 0, st>>>(static_cast<const float*>(wp), s.weight_v, w, q.ld_x, w_part, Vp, p.D,
-                                                                       wide(wp, s.weight_v));
+                xent_pack_kernel<float, false><<<grid, kPrepThreads, 0, st>>>(static_cast<const float*>(wp), s.weight_v, w, q.ld_x, w_part, Vp, p.D, ww,
+                                                                              g.range);
+            else if (raw)
+                xent_pack_kernel<__nv_bfloat16, true><<<grid, kPrepThreads, 0, st>>>(wb, s.weight_v, w, q.ld_x, w_part, Vp, p.D, ww, g.range);
             else
-                xent_pack_kernel<__nv_bfloat16><<<grid, kPrepThreads, 0, st>>>(static_cast<const __nv_bfloat16*>(wp), s.weight_v, w, q.ld_x, w_part,
-                                                                               Vp, p.D, wide(wp, s.weight_v));
+                xent_pack_kernel<__nv_bfloat16, false><<<grid, kPrepThreads, 0, st>>>(wb, s.weight_v, w, q.ld_x, w_part, Vp, p.D, ww, g.range);
             if (cudaGetLastError() != cudaSuccess) return SS_ERR_CUDA;
             wp = w;
             ld_w = q.ld_x;
@@ -904,7 +1006,7 @@ extern "C" size_t ss_linear_xent_workspace_size(int64_t tokens, int64_t V, int64
         (io_dtype != SS_F32 && io_dtype != SS_BF16))
         return 0;
     const bool f32 = io_dtype == SS_F32;
-    return std::max(layout(tokens, V, D, f32, true, backward != 0).total, layout(tokens, V, D, f32, f32, backward != 0).total);
+    return std::max(layout(tokens, V, D, f32, false, backward != 0).total, layout(tokens, V, D, f32, true, backward != 0).total);
 }
 
 extern "C" ss_status ss_linear_xent(const void* hidden, const void* weight, const int32_t* targets, float* loss, float* lse, int64_t tokens,

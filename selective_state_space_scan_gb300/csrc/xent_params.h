@@ -2,7 +2,7 @@
 #pragma once
 
 #include <cuda.h>
-#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -11,13 +11,16 @@ namespace selscan {
 
 enum class Product { kLoss, kGrad, kOut };
 
+// Largest finite magnitudes that the operands' scales follow from.
+enum { kRangeX = 0, kRangeW = 1, kRangeG = 2 };
+
 struct XentParams {
     // operands of the products as [part][row][col]; kOut's second product has the maps a1 and b1
     CUtensorMap a0, b0, a1, b1;
     const int* count;           // rows that have a target
     const int* tgt;             // [count] their targets
     int D, v0, Vp;              // the piece: columns v0 .. v0 + Vp of the vocabulary
-    int segs;                   // products of parts
+    const unsigned int* range;  // [3] bits of the largest magnitudes (scaled operands)
     unsigned int* err;
     // kLoss
     float2* part;               // [half tile][ld_part] maximum and sum of a row
@@ -27,7 +30,7 @@ struct XentParams {
     // kGrad
     const float* lse;           // [count]
     const float* g;             // [count] gradient of the loss
-    __nv_bfloat16* dl;          // [part][row][ld_dl]
+    __half* dl;                 // [part][row][ld_dl]
     int64_t ld_dl, dl_part;
     // kOut
     void* dw;
@@ -45,12 +48,13 @@ struct PrepParams {
     int64_t hidden_t, T, V;
     int D, per;
     bool wide;                  // rows of hidden begin on 16-byte boundaries
-    __nv_bfloat16* x;           // [part][row][ld_x]
+    __half* x;                  // [part][row][ld_x] (bf16 where the operands are raw)
     int64_t ld_x, x_part;
     int* count;
     int* rows;                  // [count] row of hidden
     int* tgt;
     unsigned int* err;
+    unsigned int* range;        // [3], zero before xent_range_kernel
     float* loss_out;            // forward: zeros in rows without a target
     float* lse_out;
     const float* lse;           // backward
