@@ -89,32 +89,30 @@ struct Unit {
     int job, m, n, k0, k1, split;
 };
 
-// How a kernel's units are numbered.  kOut has two products: 0 dweight (rows: the piece's tokens of the vocabulary),
-// 1 dhidden.
+// How a kernel's units are numbered.  kOut has two products: job 0 dweight (rows: the piece of the vocabulary), job 1
+// dhidden (rows: the tokens) in slices of K.
 struct Work {
-    int mt[2], nt[2], steps[2], per, splits, first;
-    int64_t n0, total;
+    int mt0, mt1, nt, steps0, steps1, per, first;
+    int64_t n0, total;                            // units of the job that is first, and of both
 };
 template <Product P>
 __device__ __forceinline__ Work make_work(const XentParams& p, int rows) {
-    Work w;
+    Work w = {};
     const int dt = (p.D + kTile - 1) / kTile, vt = (p.Vp + kTile - 1) / kTile, rt = (rows + kTile - 1) / kTile;
     if (P != Product::kOut) {
-        w.mt[0] = rt;
-        w.nt[0] = vt;
-        w.steps[0] = (p.D + kStep - 1) / kStep;
+        w.mt0 = rt;
+        w.nt = vt;
+        w.steps0 = (p.D + kStep - 1) / kStep;
         w.n0 = w.total = static_cast<int64_t>(rt) * vt;
-        w.splits = 1;
         return w;
     }
-    w.mt[0] = vt;
-    w.nt[0] = w.nt[1] = dt;
-    w.steps[0] = (rows + kStep - 1) / kStep;
-    w.mt[1] = rt;
-    w.steps[1] = (p.Vp + kStep - 1) / kStep;
-    w.splits = p.splits;
-    w.per = (w.steps[1] + p.splits - 1) / p.splits;
-    w.first = w.per > w.steps[0] ? 1 : 0;         // the longer units first, so that the shorter ones fill up
+    w.mt0 = vt;
+    w.mt1 = rt;
+    w.nt = dt;
+    w.steps0 = (rows + kStep - 1) / kStep;
+    w.steps1 = (p.Vp + kStep - 1) / kStep;
+    w.per = (w.steps1 + p.splits - 1) / p.splits;
+    w.first = w.per > w.steps0 ? 1 : 0;           // the longer units first, so that the shorter ones fill up
     const int64_t a = static_cast<int64_t>(vt) * dt, b = static_cast<int64_t>(rt) * dt * p.splits;
     w.n0 = w.first ? b : a;
     w.total = a + b;
@@ -125,25 +123,26 @@ __device__ __forceinline__ Unit unit_of(const Work& w, int64_t i) {
     Unit u;
     if (P != Product::kOut) {
         // the row tiles of a group take each tile of the vocabulary at the same time: it is read once
-        const int64_t per_group = static_cast<int64_t>(kGroup) * w.nt[0];
+        const int64_t per_group = static_cast<int64_t>(kGroup) * w.nt;
         const int g = static_cast<int>(i / per_group), r = static_cast<int>(i - g * per_group);
-        const int size = min(kGroup, w.mt[0] - g * kGroup);
+        const int size = min(kGroup, w.mt0 - g * kGroup);
         u.job = 0;
         u.m = g * kGroup + r % size;
         u.n = r / size;
         u.k0 = 0;
-        u.k1 = w.steps[0];
+        u.k1 = w.steps0;
         u.split = 0;
         return u;
     }
     u.job = i < w.n0 ? w.first : 1 - w.first;
     const int64_t at = i < w.n0 ? i : i - w.n0;
-    u.n = static_cast<int>(at % w.nt[u.job]);
-    const int r = static_cast<int>(at / w.nt[u.job]);
-    u.m = r % w.mt[u.job];
-    u.split = r / w.mt[u.job];
+    const int64_t r = at / w.nt;
+    u.n = static_cast<int>(at - r * w.nt);
+    const int mt = u.job ? w.mt1 : w.mt0;
+    u.split = u.job ? static_cast<int>(r / mt) : 0;
+    u.m = static_cast<int>(r - static_cast<int64_t>(u.split) * mt);
     u.k0 = u.job ? u.split * w.per : 0;
-    u.k1 = u.job ? min(u.k0 + w.per, w.steps[1]) : w.steps[0];
+    u.k1 = u.job ? min(u.k0 + w.per, w.steps1) : w.steps0;
     return u;
 }
 
@@ -224,7 +223,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                     for (int seg = 0; seg < (F32 ? kSegs : 1) && go; ++seg) {
                         const int pa = F32 ? kPartA[seg] : 0, pb = F32 ? kPartB[seg] : 0;
                         for (int k = kc; k < min(kc + kChain<P, F32>, u.k1); ++k) {
-                            go = mbar_sleep_bounded(&sh.empty[st], ph ^ 1, abort, p.err);
+                            go = mbar_wait_bounded(&sh.empty[st], ph ^ 1, abort, p.err);
                             if (!go) break;
                             if (rank == 0) mbar_expect_tx(&sh.full[st], 2 * kStageBytes);
                             uint8_t* sa = tiles + st * kStageBytes;
@@ -251,7 +250,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
             }
             // the products' last arrivals on this CTA's barriers are in before it ends
             for (int i = 0; i < kStages; ++i) {
-                if (!mbar_sleep_bounded(&sh.empty[st], ph ^ 1, abort, p.err)) break;
+                if (!mbar_wait_bounded(&sh.empty[st], ph ^ 1, abort, p.err)) break;
                 if (++st == kStages) {
                     st = 0;
                     ph ^= 1;
@@ -275,10 +274,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                 for (int kc = u.k0; kc < u.k1 && go; kc += kChain<P, F32>, ++turn) {
                     const uint32_t d = tmem + (turn & 1) * kAccCols;
                     const int n = (min(kc + kChain<P, F32>, u.k1) - kc) * (F32 ? kSegs : 1);
-                    go = mbar_sleep_bounded(&sh.acc_empty[turn & 1], ((turn >> 1) & 1) ^ 1, abort, p.err);
+                    go = mbar_wait_bounded(&sh.acc_empty[turn & 1], ((turn >> 1) & 1) ^ 1, abort, p.err);
                     tc_fence_after();
                     for (int k = 0; k < n && go; ++k) {
-                        go = mbar_sleep_bounded(&sh.full[st], ph, abort, p.err);
+                        go = mbar_wait_bounded(&sh.full[st], ph, abort, p.err);
                         if (!go) break;
                         tc_fence_after();
                         const uint32_t a = at + st * kStageBytes, b = a + kOperand;
@@ -308,7 +307,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
             for (int j = 0; j < kHalf; ++j) acc[j] = 0.f;
 #pragma unroll 1
             for (int kc = u.k0; kc < u.k1; kc += kChain<P, F32>, ++turn) {
-                go = __all_sync(0xffffffffu, mbar_sleep_bounded(&sh.acc_full[turn & 1], (turn >> 1) & 1, abort, p.err));
+                go = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.acc_full[turn & 1], (turn >> 1) & 1, abort, p.err));
                 if (!go) break;
                 tc_fence_after();
                 const uint32_t at = tmem + (turn & 1) * kAccCols + half * kHalf + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -358,9 +357,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                     for (int j = 0; j < 32; j += 2) a = add2(a, ex2x2(mul2(add2(make_float2(acc[c + j], acc[c + j + 1]), off), l2e)));
                     s += a.x + a.y;
                     if (tgt >= c && tgt < c + 32) {
+                        // (a choice written in C++ becomes an indexed array, and the accumulator with it local memory)
                         float l = 0.f;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) l = tgt - c == j ? acc[c + j] : l;
+                        for (int j = 0; j < 32; ++j)
+                            asm("{\n .reg .pred q;\n setp.eq.s32 q, %1, %2;\n @q mov.f32 %0, %3;\n}" : "+f"(l) : "r"(tgt - c), "r"(j), "f"(acc[c + j]));
                         p.tl[row] = l;
                     }
                 }
@@ -502,13 +503,19 @@ __device__ __forceinline__ unsigned int row_range(const T* row, int D, bool wide
     };
     constexpr int N = 16 / sizeof(T);
     const int vecs = wide ? D / N : 0;
-    for (int i = threadIdx.x % 32; i < vecs; i += 32) {
-        const uint4 u = reinterpret_cast<const uint4*>(row)[i];
-        const uint32_t a[4] = {u.x, u.y, u.z, u.w};
+    constexpr int U = 4;
+    for (int i = threadIdx.x % 32; i < vecs; i += 32 * U) {
+        uint4 u[U];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            take(sizeof(T) == 2 ? a[j] << 16 : a[j]);
-            if constexpr (sizeof(T) == 2) take(a[j] & 0xffff0000u);
+        for (int k = 0; k < U; ++k) u[k] = i + 32 * k < vecs ? reinterpret_cast<const uint4*>(row)[i + 32 * k] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const uint32_t a[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                take(sizeof(T) == 2 ? a[j] << 16 : a[j]);
+                if constexpr (sizeof(T) == 2) take(a[j] & 0xffff0000u);
+            }
         }
     }
     for (int c = vecs * N + threadIdx.x % 32; c < D; c += 32) take(__float_as_uint(to_f32<T>(row[c])));
@@ -547,61 +554,73 @@ __global__ void __launch_bounds__(kPrepThreads) xent_range_kernel(const PrepPara
     if (threadIdx.x < 3 && part[threadIdx.x]) atomicMax(&p.range[threadIdx.x], part[threadIdx.x]);
 }
 
-// Sum over the block, in every thread.
-__device__ __forceinline__ int block_sum(int v, int* slot) {
-    v = __reduce_add_sync(0xffffffffu, v);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) slot[threadIdx.x / 32] = v;
-    __syncthreads();
-    int s = 0;
-    for (int i = 0; i < kPrepThreads / 32; ++i) s += slot[i];
-    return s;
-}
-
 // The rows that have a target, gathered in order: row i of x is row rows[i] of hidden.  A block has `per` rows of
-// hidden and counts the targets before them itself.
+// hidden, at most one to a thread, and counts the targets before them itself; a warp packs a row at a time.
 template <typename T, bool BWD>
 __global__ void __launch_bounds__(kPrepThreads) xent_gather_kernel(const PrepParams p) {
     constexpr bool F32 = sizeof(T) == 4, RAW = !F32 && !BWD;
+    constexpr int kWarps = kPrepThreads / 32;
+    __shared__ int before[kWarps], own[kWarps], to[kPrepThreads];
     const float scale = RAW ? 1.f : pow2(-scale_exp(p.range[kRangeX]));
-    __shared__ int slot[kPrepThreads / 32];
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * p.per, last = min(first + p.per, p.T);
-    int before = 0;
-    for (int64_t t = threadIdx.x; t < first; t += kPrepThreads) {
-        const int v = p.targets[t];
-        before += v >= 0 && v < p.V;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * p.per;
+    const int n = static_cast<int>(min(static_cast<int64_t>(p.per), p.T - first));
+    auto has = [&](int v) { return v >= 0 && v < p.V; };
+    int count = 0;
+#pragma unroll 4
+    for (int64_t t = threadIdx.x; t < first; t += kPrepThreads) count += has(p.targets[t]);
+    count = __reduce_add_sync(0xffffffffu, count);
+    const int mine = static_cast<int>(threadIdx.x) < n ? p.targets[first + threadIdx.x] : -1;
+    const unsigned int some = __ballot_sync(0xffffffffu, has(mine));
+    if (lane == 0) {
+        before[warp] = count;
+        own[warp] = __popc(some);
     }
-    int at = block_sum(before, slot);
-    for (int64_t t = first; t < last; ++t) {
-        const int v = p.targets[t];
-        if (v >= 0 && v < p.V) {
-            const T* src = static_cast<const T*>(p.hidden) + t * p.hidden_t;
-            __half* dst = p.x + static_cast<int64_t>(at) * p.ld_x;
-            for (int c = threadIdx.x * 8; c < p.D; c += kPrepThreads * 8) pack8<T, RAW>(src, dst, p.x_part, c, p.D, p.wide, scale);
-            if (threadIdx.x == 0) {
-                p.rows[at] = static_cast<int>(t);
-                p.tgt[at] = v;
-                if constexpr (BWD) {
-                    p.lse_c[at] = p.lse[t];
-                    p.g_c[at] = p.dloss[t * p.dloss_t];
-                }
-            }
-            ++at;
-        } else if constexpr (BWD) {
-            T* d = static_cast<T*>(p.dhidden) + t * p.dhidden_t;
-            for (int c = threadIdx.x; c < p.D; c += kPrepThreads) d[c] = from_f32<T>(0.f);
-        } else if (threadIdx.x == 0) {
-            p.loss_out[t] = p.lse_out[t] = 0.f;
-            if (v >= p.V && p.err) atomicOr(p.err, kErrIndex);
+    __syncthreads();
+    int at = 0, total = 0;
+    for (int i = 0; i < kWarps; ++i) {
+        total += before[i] + own[i];
+        at += before[i] + (i < warp ? own[i] : 0);
+    }
+    at += __popc(some & ((1u << lane) - 1u));
+    if (has(mine)) {
+        const int64_t t = first + threadIdx.x;
+        to[threadIdx.x] = at;
+        p.rows[at] = static_cast<int>(t);
+        p.tgt[at] = mine;
+        if constexpr (BWD) {
+            p.lse_c[at] = p.lse[t];
+            p.g_c[at] = p.dloss[t * p.dloss_t];
+        }
+    } else if (static_cast<int>(threadIdx.x) < n) {
+        to[threadIdx.x] = -1;
+        if constexpr (!BWD) {
+            p.loss_out[first + threadIdx.x] = p.lse_out[first + threadIdx.x] = 0.f;
+            if (mine >= p.V && p.err) atomicOr(p.err, kErrIndex);
         }
     }
-    if (last == p.T) {
-        if (threadIdx.x == 0) *p.count = at;
+    __syncthreads();
+    for (int r = warp; r < n; r += kWarps) {
+        const int64_t t = first + r;
+        const int i = to[r];
+        if (i >= 0) {
+            const T* src = static_cast<const T*>(p.hidden) + t * p.hidden_t;
+            __half* dst = p.x + static_cast<int64_t>(i) * p.ld_x;
+#pragma unroll 2
+            for (int c = lane * 8; c < p.D; c += 256) pack8<T, RAW>(src, dst, p.x_part, c, p.D, p.wide, scale);
+        } else if constexpr (BWD) {
+            T* d = static_cast<T*>(p.dhidden) + t * p.dhidden_t;
+            for (int c = lane; c < p.D; c += 32) d[c] = from_f32<T>(0.f);
+        }
+    }
+    if (first + n == p.T) {
+        if (threadIdx.x == 0) *p.count = total;
         // the rest of the last step of K over the tokens counts for nothing, but must be finite
-        const int end = (at + kStep - 1) / kStep * kStep, vecs = static_cast<int>(p.ld_x / 8);
-        for (int q = 0; q < (F32 ? 2 : 1); ++q)
-            for (int i = threadIdx.x; i < (end - at) * vecs; i += kPrepThreads)
-                store16(p.x + q * p.x_part + (at + i / vecs) * p.ld_x + i % vecs * 8, make_uint4(0u, 0u, 0u, 0u));
+        const int end = (total + kStep - 1) / kStep * kStep, vecs = static_cast<int>(p.ld_x / 8);
+        if (BWD)
+            for (int q = 0; q < (F32 ? 2 : 1); ++q)
+                for (int i = threadIdx.x; i < (end - total) * vecs; i += kPrepThreads)
+                    store16(p.x + q * p.x_part + (total + i / vecs) * p.ld_x + i % vecs * 8, make_uint4(0u, 0u, 0u, 0u));
     }
 }
 
@@ -618,9 +637,11 @@ __global__ void __launch_bounds__(kPrepThreads) xent_pack_kernel(const T* w, int
 }
 
 // lse and loss from the maxima and sums of the half tiles; a block has 32 rows, a warp a share of the tiles.
-__global__ void __launch_bounds__(kPrepThreads) xent_join_kernel(const float2* part, int64_t ld, int halves, const int* count, const int* rows,
+constexpr int kJoinThreads = 1024;
+__global__ void __launch_bounds__(kJoinThreads) xent_join_kernel(const float2* part, int64_t ld, int halves, const int* count, const int* rows,
                                                                  const float* tl, float* loss, float* lse) {
-    __shared__ float2 s[kPrepThreads / 32][32];
+    constexpr int kWarps = kJoinThreads / 32, U = 8;
+    __shared__ float2 s[kWarps][33];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, n = *count;
     const int row = blockIdx.x * 32 + lane;
     float m = -INFINITY, sum = 0.f;
@@ -631,15 +652,27 @@ __global__ void __launch_bounds__(kPrepThreads) xent_join_kernel(const float2* p
     };
     if (blockIdx.x * 32 >= n) return;
     if (row < n)
-        for (int i = warp; i < halves; i += kPrepThreads / 32) join(part[i * ld + row]);
+        for (int i = warp; i < halves; i += kWarps * U) {
+            float2 q[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) q[u] = i + u * kWarps < halves ? part[(i + u * kWarps) * ld + row] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int u = 0; u < U; ++u) join(q[u]);
+        }
     s[warp][lane] = make_float2(m, sum);
     __syncthreads();
-    if (warp == 0 && row < n) {
-        for (int i = 1; i < kPrepThreads / 32; ++i) join(s[i][lane]);
+    // a warp has a row now, a lane a share
+    const float2 q = s[lane][warp];
+    m = q.x;
+    sum = q.y;
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) join(make_float2(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, sum, o)));
+    const int mine = blockIdx.x * 32 + warp;
+    if (lane == 0 && mine < n) {
         const float v = m + logf(sum);
-        const int t = rows[row];
+        const int t = rows[mine];
         lse[t] = v;
-        loss[t] = v - tl[row];
+        loss[t] = v - tl[mine];
     }
 }
 
@@ -912,7 +945,7 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
     PrepParams g;
     std::memset(&g, 0, sizeof(g));
     g.hidden = c.hidden; g.hidden_t = s.hidden_t; g.targets = c.targets; g.T = T; g.V = V; g.D = static_cast<int>(D);
-    g.per = static_cast<int>(std::max<int64_t>(8, T / 1024));
+    g.per = static_cast<int>(std::min<int64_t>(kPrepThreads, std::max<int64_t>(8, T / 1024)));
     g.x = x; g.ld_x = q.ld_x; g.x_part = x_part; g.wide = wide(c.hidden, T > 1 ? s.hidden_t : 0);
     g.count = reinterpret_cast<int*>(ws + q.count); g.rows = reinterpret_cast<int*>(ws + q.rows); g.tgt = reinterpret_cast<int*>(ws + q.tgt);
     g.lse = c.lse_in; g.dloss = c.dloss; g.dloss_t = s.dloss_t; g.lse_c = f32_at(q.lse); g.g_c = f32_at(q.g);
@@ -922,7 +955,7 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
     const bool raw = !f32 && !c.bwd;
     if (!raw) {
         if (cudaMemsetAsync(g.range, 0, 12, st) != cudaSuccess) return SS_ERR_CUDA;
-        const int64_t warps = kPrepThreads / 32, most = 4 * sm_count();
+        const int64_t warps = kPrepThreads / 32, most = 8 * sm_count();
         const int xb = static_cast<int>(std::min((T + warps - 1) / warps, most)), wb = static_cast<int>(std::min((V + warps - 1) / warps, most));
         const bool ww = wide(c.weight, s.weight_v);
         if (f32)
@@ -982,7 +1015,7 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
         if (launch_gemm<Product::kOut>(p, f32, vt * dt + mt * dt * q.splits, st) != cudaSuccess) return SS_ERR_CUDA;
     }
     if (!c.bwd) {
-        xent_join_kernel<<<static_cast<unsigned>((T + 31) / 32), kPrepThreads, 0, st>>>(p.part, q.tpad, static_cast<int>(q.halves), g.count, g.rows, p.tl,
+        xent_join_kernel<<<static_cast<unsigned>((T + 31) / 32), kJoinThreads, 0, st>>>(p.part, q.tpad, static_cast<int>(q.halves), g.count, g.rows, p.tl,
                                                                                      c.loss, c.lse);
     } else {
         const unsigned grid = static_cast<unsigned>(std::min<int64_t>(T, 8 * sm_count()));
