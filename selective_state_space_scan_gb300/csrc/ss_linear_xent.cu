@@ -79,7 +79,8 @@ struct GemmShared {
     uint32_t tmem;
     int abort;
 };
-constexpr size_t kGemmSmem = kStages * kStageBytes + sizeof(GemmShared) + 1024;
+constexpr uint32_t kBox = 32 * 128;                // bytes of a warp's store: 32 rows of 128
+constexpr size_t kGemmSmem = kStages * kStageBytes + kEpiWarps * kBox + sizeof(GemmShared) + 1024;
 
 // Whether the operands are bf16 as they are (else scaled fp16).
 template <Product P, bool F32> constexpr bool kRaw = P == Product::kLoss && !F32;
@@ -94,9 +95,11 @@ struct Unit {
 struct Work {
     int mt0, mt1, nt, steps0, steps1, per, first;
     int64_t n0, total;                            // units of the job that is first, and of both
+    int64_t extra;                                // pairs that have one unit of the first job more than the others
+    int64_t fill;                                 // units of the second job that each of the others has meanwhile
 };
 template <Product P>
-__device__ __forceinline__ Work make_work(const XentParams& p, int rows) {
+__device__ __forceinline__ Work make_work(const XentParams& p, int rows, int64_t pairs) {
     Work w = {};
     const int dt = (p.D + kTile - 1) / kTile, vt = (p.Vp + kTile - 1) / kTile, rt = (rows + kTile - 1) / kTile;
     if (P != Product::kOut) {
@@ -104,6 +107,7 @@ __device__ __forceinline__ Work make_work(const XentParams& p, int rows) {
         w.nt = vt;
         w.steps0 = (p.D + kStep - 1) / kStep;
         w.n0 = w.total = static_cast<int64_t>(rt) * vt;
+        w.extra = w.n0 % pairs;
         return w;
     }
     w.mt0 = vt;
@@ -116,7 +120,26 @@ __device__ __forceinline__ Work make_work(const XentParams& p, int rows) {
     const int64_t a = static_cast<int64_t>(vt) * dt, b = static_cast<int64_t>(rt) * dt * p.splits;
     w.n0 = w.first ? b : a;
     w.total = a + b;
+    w.extra = w.n0 % pairs;
+    const int short_one = w.first ? w.steps0 : w.per, long_one = w.first ? w.per : w.steps0;
+    w.fill = w.extra > 0 ? long_one / max(short_one, 1) : 0;
     return w;
+}
+// The i-th unit of a pair of CTAs, or -1: units of the first job in turn, then those of the second, of which the
+// pairs that have one of the first less get as many more as that one's length allows.
+__device__ __forceinline__ int64_t nth_unit(const Work& w, int64_t pair, int64_t pairs, int64_t i) {
+    const int64_t full = w.n0 / pairs, n = full + (pair < w.extra ? 1 : 0);
+    if (i < n) return pair + i * pairs;
+    i -= n;
+    const int64_t others = pairs - w.extra, filled = min(w.fill * others, w.total - w.n0);
+    int64_t at;
+    if (pair >= w.extra && i < w.fill && (pair - w.extra) + i * others < filled) {
+        at = (pair - w.extra) + i * others;
+    } else {
+        if (pair >= w.extra) i -= (filled - (pair - w.extra) + others - 1) / others;
+        at = filled + (pair >= w.extra ? pair - w.extra : others + pair) + i * pairs;
+    }
+    return at < w.total - w.n0 ? w.n0 + at : -1;
 }
 template <Product P>
 __device__ __forceinline__ Unit unit_of(const Work& w, int64_t i) {
@@ -166,11 +189,31 @@ __device__ __forceinline__ void store_half8(__half* q, int64_t part, const float
     }
 }
 
+// A warp's 32 rows of 128 bytes (a lane has a row) to a tensor, by way of its own part of shared memory: as rows of
+// their own they would be stores of 16 bytes to 32 lines at a time, which took the L1 half of its time beside the
+// operands.  What lies outside the tensor is not written.  ADD: onto what is there.
+template <bool ADD>
+__device__ __forceinline__ void store_box(const CUtensorMap* map, uint8_t* box, const uint32_t (&w)[32], int col, int row, int part) {
+    const int lane = threadIdx.x % 32;
+    if (lane == 0) tma_store_wait_read();          // the store before has left this memory
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        store16(box + tc_chunk(lane, j), make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
+    tma_store_fence();
+    __syncwarp();
+    if (lane == 0) {
+        if constexpr (ADD) pair_tma_add(map, box, col, row, part);
+        else tma_store_3d(map, box, col, row, part);
+        tma_store_commit();
+    }
+}
+
 template <Product P, bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xent_gemm_kernel(const __grid_constant__ XentParams p) {
     extern __shared__ uint8_t raw[];
     uint8_t* tiles = raw + (1024 - smem_addr(raw) % 1024) % 1024;
-    GemmShared& sh = *reinterpret_cast<GemmShared*>(tiles + kStages * kStageBytes);
+    GemmShared& sh = *reinterpret_cast<GemmShared*>(tiles + kStages * kStageBytes + kEpiWarps * kBox);
     volatile int* abort = &sh.abort;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_ctarank();
@@ -195,7 +238,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
     cluster_sync_all();                            // the peer's barriers exist
     const uint32_t tmem = sh.tmem;
     const int rows = *p.count;
-    const Work work = make_work<P>(p, rows);
+    const Work work = make_work<P>(p, rows, clusters);
     int ex = 0, ew = 0, eg = 0;
     if constexpr (!kRaw<P, F32>) {
         ex = scale_exp(p.range[kRangeX]);
@@ -211,7 +254,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
             for (int i = 0; i < kStages; ++i) full0[i] = peer_smem_addr(&sh.full[i], 0);
             int st = 0;
             uint32_t ph = 0;
-            for (int64_t i = cluster; i < work.total && !*abort; i += clusters) {
+            for (int64_t t = 0, i; (i = nth_unit(work, cluster, clusters, t)) >= 0 && !*abort; ++t) {
                 const Unit u = unit_of<P>(work, i);
                 const CUtensorMap* ma = u.job ? &p.a1 : &p.a0;
                 const CUtensorMap* mb = u.job ? &p.b1 : &p.b0;
@@ -265,7 +308,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
             uint32_t ph = 0;
             int turn = 0;
             bool go = true;
-            for (int64_t i = cluster; i < work.total && go; i += clusters) {
+            for (int64_t t = 0, i; go && (i = nth_unit(work, cluster, clusters, t)) >= 0; ++t) {
                 const Unit u = unit_of<P>(work, i);
                 const bool a_mn = P == Product::kOut && u.job == 0, b_mn = P == Product::kOut;
                 constexpr uint32_t kBf16 = 1u << 7 | 1u << 10;                          // operand types (else fp16)
@@ -298,9 +341,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
         // ---------------------------------------------------------------- accumulators, by eight warps of each CTA
         const int quarter = warp % 4, half = warp / 4;
         const uint32_t empty0 = peer_smem_addr(&sh.acc_empty[0], 0), empty1 = peer_smem_addr(&sh.acc_empty[1], 0);
+        uint8_t* box = tiles + kStages * kStageBytes + warp * kBox;
         int turn = 0;
         bool go = true;
-        for (int64_t i = cluster; i < work.total; i += clusters) {
+        for (int64_t t = 0, i; (i = nth_unit(work, cluster, clusters, t)) >= 0; ++t) {
             const Unit u = unit_of<P>(work, i);
             float acc[kHalf];                      // a thread has half a row of the tile
 #pragma unroll
@@ -370,7 +414,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                 const bool ok = row < rows;
                 const float lse = ok ? p.lse[row] : 0.f, g = ok ? p.g[row] * pow2(-eg) : 0.f;
                 const int tgt = ok ? p.tgt[row] - p.v0 - col0 : -1;
-                __half* out = p.dl + static_cast<int64_t>(row) * p.ld_dl + col0;
                 const Pow2x2 f(ex + ew);
                 const float2 off = splat2(-lse), f2 = splat2(f.a), l2e = splat2(kLog2e), g2 = splat2(g);
                 if (f.b != 1.f) {
@@ -378,70 +421,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                     for (int j = 0; j < kHalf; ++j) acc[j] *= f.b;
                 }
 #pragma unroll
-                for (int c = 0; c < kHalf; c += 8) {
-                    if (c >= p.Vp - col0) break;                          // (a row's padding to 8 columns may be written)
-                    float2 e[4];
+                for (int c = 0; c < kHalf; c += 64) {
+                    if (col0 + c >= p.Vp) break;
+                    uint32_t hi[32], lo[F32 ? 32 : 1];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        e[j] = ex2x2(mul2(fma2(make_float2(acc[c + 2 * j], acc[c + 2 * j + 1]), f2, off), l2e));
-                    if (tgt >= c && tgt < c + 8) {
+                    for (int q = 0; q < 64; q += 8) {
+                        float2 e[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            e[j] = ex2x2(mul2(fma2(make_float2(acc[c + q + 2 * j], acc[c + q + 2 * j + 1]), f2, off), l2e));
+                        if (tgt >= c + q && tgt < c + q + 8) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                e[j].x -= tgt - c - q == 2 * j ? 1.f : 0.f;
+                                e[j].y -= tgt - c - q == 2 * j + 1 ? 1.f : 0.f;
+                            }
+                        }
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            e[j].x -= tgt - c == 2 * j ? 1.f : 0.f;
-                            e[j].y -= tgt - c == 2 * j + 1 ? 1.f : 0.f;
+                            e[j] = mul2(e[j], g2);
+                            if (!ok) e[j] = splat2(0.f);
+                            const __half2 h = __float22half2_rn(e[j]);
+                            hi[q / 2 + j] = half_bits(h);
+                            if constexpr (F32) lo[q / 2 + j] = half_bits(__float22half2_rn(fma2(__half22float2(h), splat2(-1.f), e[j])));
                         }
                     }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        e[j] = mul2(e[j], g2);
-                        if (!ok) e[j] = splat2(0.f);
-                    }
-                    store_half8<F32>(out + c, p.dl_part, e);
+                    store_box<false>(&p.s0, box, hi, col0 + c, row - lane, 0);
+                    if constexpr (F32) store_box<false>(&p.s0, box, lo, col0 + c, row - lane, 1);
                 }
             } else {
-              const Pow2x2 f(eg + (u.job ? ew : ex));
+                const Pow2x2 f(eg + (u.job ? ew : ex));
 #pragma unroll
-              for (int j = 0; j < kHalf; ++j) acc[j] = acc[j] * f.a * f.b;
-              if (u.job) {
-                if (row < rows) {
-                    float* out = p.dx + u.split * p.dx_split + static_cast<int64_t>(row) * p.ld_dx + col0;
-                    const int n = p.D - col0;
+                for (int j = 0; j < kHalf; ++j) acc[j] = acc[j] * f.a * f.b;
+                if (u.job || (F32 && p.dw_wide)) {
+                    // rows of 32 floats
 #pragma unroll
-                    for (int j = 0; j < kHalf; j += 4) {
-                        if (j >= n) break;
-                        float4* q = reinterpret_cast<float4*>(out + j);
-                        float4 v = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-                        if (p.add) {
-                            const float4 o = *q;
-                            v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
-                        }
-                        *q = v;
+                    for (int c = 0; c < kHalf; c += 32) {
+                        if (col0 + c >= p.D) break;
+                        uint32_t w[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(acc[c + j]);
+                        if (!u.job) store_box<false>(&p.s0, box, w, col0 + c, row - lane, 0);
+                        else if (p.add) store_box<true>(&p.s1, box, w, col0 + c, row - lane, u.split);
+                        else store_box<false>(&p.s1, box, w, col0 + c, row - lane, u.split);
                     }
-                }
-              } else if (row < p.Vp) {
-                using T = std::conditional_t<F32, float, __nv_bfloat16>;
-                T* out = static_cast<T*>(p.dw) + static_cast<int64_t>(p.v0 + row) * p.ld_dw + col0;
-                const int n = p.D - col0;
-                if (p.dw_wide) {
+                } else if (!F32 && p.dw_wide) {
 #pragma unroll
-                    for (int j = 0; j < kHalf; j += 8) {
-                        if (j >= n) break;
-                        if constexpr (F32) {
-                            *reinterpret_cast<float4*>(out + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-                            *reinterpret_cast<float4*>(out + j + 4) = make_float4(acc[j + 4], acc[j + 5], acc[j + 6], acc[j + 7]);
-                        } else {
-                            store16(out + j, make_uint4(pack_bf16(acc[j], acc[j + 1]), pack_bf16(acc[j + 2], acc[j + 3]),
-                                                        pack_bf16(acc[j + 4], acc[j + 5]), pack_bf16(acc[j + 6], acc[j + 7])));
-                        }
+                    for (int c = 0; c < kHalf; c += 64) {
+                        if (col0 + c >= p.D) break;
+                        uint32_t w[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) w[j] = pack_bf16(acc[c + 2 * j], acc[c + 2 * j + 1]);
+                        store_box<false>(&p.s0, box, w, col0 + c, row - lane, 0);
                     }
-                } else {
+                } else if (row < p.Vp) {
+                    using T = std::conditional_t<F32, float, __nv_bfloat16>;
+                    T* out = static_cast<T*>(p.dw) + static_cast<int64_t>(p.v0 + row) * p.ld_dw + col0;
 #pragma unroll
                     for (int j = 0; j < kHalf; ++j)
-                        if (j < n) out[j] = from_f32<T>(acc[j]);
+                        if (j < p.D - col0) out[j] = from_f32<T>(acc[j]);
                 }
-              }
             }
         }
+        if (lane == 0) tma_store_wait_all();
     }
     __syncthreads();
     // (after a wait that ran out: copies and products in flight are over long before this)
@@ -699,7 +741,7 @@ using host::meet;
 using host::Range;
 using host::range3;
 
-constexpr int64_t kPieceBytes = 256 << 20;        // of dl (and of a packed piece of weight)
+constexpr int64_t kPieceBytes = 512 << 20;        // of dl (and of a packed piece of weight)
 constexpr int64_t kMinPiece = 4096;               // columns: below, the sums of dhidden cost as much as the products
 constexpr int64_t kMaxSplits = 32;
 constexpr int64_t kMinSteps = 16;                 // of K to a slice of dhidden's sums
@@ -763,7 +805,7 @@ Layout layout(int64_t T, int64_t V, int64_t D, bool f32, bool in_place, bool bwd
     if (bwd) {
         const int64_t pairs = sm_count() / 2;
         int64_t best = -1;
-        for (int64_t s = 1; s <= kMaxSplits && (s == 1 || (q.piece / kStep / s >= kMinSteps && s * q.tpad * q.ld_dx * 4 <= 2 * kPieceBytes)); ++s) {
+        for (int64_t s = 1; s <= kMaxSplits && (s == 1 || (q.piece / kStep / s >= kMinSteps && s * q.tpad * q.ld_dx * 4 <= kPieceBytes)); ++s) {
             const int64_t c = out_cost(T, D, q.piece, q.segs, s, pairs);
             if (best < 0 || c < best) {
                 best = c;
@@ -811,15 +853,17 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// [parts][rows][cols] of 16 bits, boxes of 64 columns and `box_rows` rows, 128-byte swizzle, zeros outside.
-bool make_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t parts, int64_t ld, int64_t part, int box_rows) {
+// [parts][rows][cols], boxes of 128 bytes by `box_rows` rows, 128-byte swizzle, zeros outside.  (Which 16-bit type it
+// is does not matter to a copy; fp32 is added in its type.)
+bool make_map(CUtensorMap* m, const void* base, int64_t es, int64_t cols, int64_t rows, int64_t parts, int64_t ld, int64_t part, int box_rows) {
     auto enc = encode_fn();
     if (!enc) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(parts)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * 2), static_cast<cuuint64_t>((parts > 1 ? part : rows * ld) * 2)};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1}, one[3] = {1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * es), static_cast<cuuint64_t>((parts > 1 ? part : rows * ld) * es)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(box_rows), 1}, one[3] = {1, 1, 1};
+    return enc(m, es == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Pairs of CTAs that fit on the device at once.
@@ -973,8 +1017,8 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
     std::memset(&p, 0, sizeof(p));
     p.count = g.count; p.tgt = g.tgt; p.D = static_cast<int>(D); p.range = g.range; p.err = g.err;
     p.part = reinterpret_cast<float2*>(ws + q.part); p.ld_part = q.tpad; p.tl = f32_at(q.tl);
-    p.lse = g.lse_c; p.g = g.g_c; p.dl = dl; p.ld_dl = q.ld_dl; p.dl_part = dl_part;
-    p.dw = c.dweight; p.ld_dw = s.dweight_v; p.dw_wide = c.bwd && D % 8 == 0 && wide(c.dweight, s.dweight_v);
+    p.lse = g.lse_c; p.g = g.g_c;
+    p.dw = c.dweight; p.ld_dw = s.dweight_v; p.dw_wide = c.bwd && wide(c.dweight, s.dweight_v);
     p.dx = f32_at(q.dx); p.ld_dx = q.ld_dx; p.dx_split = q.tpad * q.ld_dx; p.splits = static_cast<int>(q.splits);
     const int64_t mt = (T + kTile - 1) / kTile, dt = (D + kTile - 1) / kTile;
     for (int64_t v0 = 0; v0 < V; v0 += q.piece) {
@@ -999,17 +1043,21 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
         p.v0 = static_cast<int>(v0);
         p.Vp = static_cast<int>(Vp);
         // logits: rows of x and of weight, K along the columns
-        if (!make_map(&p.a0, x, D, q.tpad, q.parts, q.ld_x, x_part, kHalf) || !make_map(&p.b0, wp, D, Vp, q.parts, ld_w, w_part, kHalf))
+        if (!make_map(&p.a0, x, 2, D, q.tpad, q.parts, q.ld_x, x_part, kHalf) || !make_map(&p.b0, wp, 2, D, Vp, q.parts, ld_w, w_part, kHalf))
             return SS_ERR_CUDA;
         if (!c.bwd) {
             if (launch_gemm<Product::kLoss>(p, f32, mt * vt, st) != cudaSuccess) return SS_ERR_CUDA;
             p.tile0 += static_cast<int>(vt);
             continue;
         }
+        if (!make_map(&p.s0, dl, 2, Vp, q.tpad, q.parts, q.ld_dl, dl_part, 32)) return SS_ERR_CUDA;
         if (launch_gemm<Product::kGrad>(p, f32, mt * vt, st) != cudaSuccess) return SS_ERR_CUDA;
         // dweight: dl and x with the tokens along rows; dhidden: dl with K along columns, weight with K along rows
-        if (!make_map(&p.a0, dl, Vp, q.tpad, q.parts, q.ld_dl, dl_part, kStep) || !make_map(&p.b0, x, D, q.tpad, q.parts, q.ld_x, x_part, kStep) ||
-            !make_map(&p.a1, dl, Vp, q.tpad, q.parts, q.ld_dl, dl_part, kHalf) || !make_map(&p.b1, wp, D, Vp, q.parts, ld_w, w_part, kStep))
+        char* dw = static_cast<char*>(c.dweight) + v0 * s.dweight_v * es;
+        if (!make_map(&p.a0, dl, 2, Vp, q.tpad, q.parts, q.ld_dl, dl_part, kStep) || !make_map(&p.b0, x, 2, D, q.tpad, q.parts, q.ld_x, x_part, kStep) ||
+            !make_map(&p.a1, dl, 2, Vp, q.tpad, q.parts, q.ld_dl, dl_part, kHalf) || !make_map(&p.b1, wp, 2, D, Vp, q.parts, ld_w, w_part, kStep) ||
+            !make_map(&p.s1, p.dx, 4, D, q.tpad, q.splits, q.ld_dx, p.dx_split, 32) ||
+            (p.dw_wide && !make_map(&p.s0, dw, es, D, Vp, 1, s.dweight_v, 0, 32)))
             return SS_ERR_CUDA;
         p.add = v0 > 0;
         if (launch_gemm<Product::kOut>(p, f32, vt * dt + mt * dt * q.splits, st) != cudaSuccess) return SS_ERR_CUDA;

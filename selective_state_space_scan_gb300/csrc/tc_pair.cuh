@@ -40,4 +40,12 @@ __device__ __forceinline__ void pair_tma_load(void* dst, const CUtensorMap* map,
         : "memory");
 }
 
+// Adds a tile of floats in shared memory to a tensor (bulk async-group completion).
+__device__ __forceinline__ void pair_tma_add(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+        ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(src))
+        : "memory");
+}
+
 }  // namespace selscan

@@ -17,6 +17,7 @@ enum { kRangeX = 0, kRangeW = 1, kRangeG = 2 };
 struct XentParams {
     // operands of the products as [part][row][col]; kOut's second product has the maps a1 and b1
     CUtensorMap a0, b0, a1, b1;
+    CUtensorMap s0, s1;         // where results go: dl (kGrad), dweight's rows of the piece and dhidden's sums (kOut)
     const int* count;           // rows that have a target
     const int* tgt;             // [count] their targets
     int D, v0, Vp;              // the piece: columns v0 .. v0 + Vp of the vocabulary
@@ -30,12 +31,10 @@ struct XentParams {
     // kGrad
     const float* lse;           // [count]
     const float* g;             // [count] gradient of the loss
-    __half* dl;                 // [part][row][ld_dl]
-    int64_t ld_dl, dl_part;
     // kOut
     void* dw;
     int64_t ld_dw;
-    bool dw_wide;               // 16-byte stores
+    bool dw_wide;               // rows begin on 16-byte boundaries: stored by s0
     float* dx;                  // [split][row][ld_dx]
     int64_t ld_dx, dx_split;
     int splits;
