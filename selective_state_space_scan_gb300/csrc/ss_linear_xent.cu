@@ -763,22 +763,22 @@ struct Layout {
     size_t count, range, rows, tgt, lse, g, tl, part, x, w, dl, dx, total;
 };
 
-// Time of one launch of both products over a piece, in steps of K, when dhidden's are cut in `splits`: units in
-// turn over the pairs of CTAs, each some steps longer for its end.
+// Time of one launch of both products over a piece, in steps of K, when dhidden's are cut in `splits`: units as
+// nth_unit hands them out, each some steps longer for its end.
 int64_t out_cost(int64_t T, int64_t D, int64_t Vp, int64_t segs, int64_t splits, int64_t pairs) {
     constexpr int64_t kEnd = 6;
     const int64_t dt = (D + kTile - 1) / kTile;
     const int64_t len[2] = {(T + kStep - 1) / kStep * segs, ((Vp + kStep - 1) / kStep + splits - 1) / splits * segs};
     const int64_t n[2] = {(Vp + kTile - 1) / kTile * dt, (T + kTile - 1) / kTile * dt * splits};
     const int first = len[1] > len[0] ? 1 : 0;
-    const int64_t a = n[first], b = n[1 - first];
-    int64_t worst = 0;
-    for (int64_t c = 0; c < pairs; ++c) {
-        const int64_t ca = (a - c + pairs - 1) / pairs, all = (a + b - c + pairs - 1) / pairs;
-        worst = std::max(worst, std::max<int64_t>(ca, 0) * (len[first] + kEnd) + (std::max<int64_t>(all, 0) - std::max<int64_t>(ca, 0)) * (len[1 - first] + kEnd));
-    }
+    const int64_t a = n[first], b = n[1 - first], la = len[first] + kEnd, lb = len[1 - first] + kEnd;
+    const int64_t extra = a % pairs, others = pairs - extra, filled = extra ? std::min(len[first] / std::max<int64_t>(len[1 - first], 1) * others, b) : 0;
+    // the pair that is last with each kind of load
+    const int64_t rounds = (b - filled + pairs - 1) / pairs, rest = (b - filled) - (rounds - 1) * pairs;
+    const int64_t with_extra = (a / pairs + (extra ? 1 : 0)) * la + (rounds - (extra && rest <= others ? 1 : 0)) * lb;
+    const int64_t without = a / pairs * la + ((filled + others - 1) / others + rounds) * lb;
     // a slice of sums more: its bytes out and in again, some 2 MB of them to a step's time (0.3 us at 6.8 TB/s)
-    return worst + splits * T * D * 8 / (2 << 20);
+    return std::max(with_extra, without) + splits * T * D * 8 / (2 << 20);
 }
 
 Layout layout(int64_t T, int64_t V, int64_t D, bool f32, bool in_place, bool bwd) {
