@@ -4,11 +4,11 @@
 //   de_j = Σ_k w_k g_{j-k}  (dx_t = de_{t+3}; de_0..2 is the window's gradient),
 //   dw_k = Σ_{b,t} g_t e_{t+k},  dbias = Σ_{b,t} g_t
 //
-// A stream of three elements per step and channel.  As in the forward kernel, a thread has 4 channels (as two
-// packed pairs) and a segment of steps, with several steps' loads in flight; it runs three steps past its
-// segment, whose g belong to its last outputs.  The weight's gradients are sums in registers; every thread
-// leaves its own in the workspace (a row of it per segment) and a second kernel adds the rows up in the same
-// order every time.
+// A stream of three elements per step and channel.  A thread has 2 channels (a packed pair) and a segment of steps;
+// the next steps' loads are in flight while it works on some, and a warp covers 64 channels of a step.  It runs
+// three steps past its segment, whose g belong to its last outputs.  The weight's gradients are sums in registers;
+// every thread leaves its own in the workspace (a row of it per segment) and a second kernel adds the rows up in
+// the same order every time.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -25,8 +25,9 @@ namespace {
 
 constexpr int kConvK = SS_CONV_WIDTH;   // 4
 constexpr int kSegMin = 8;
-constexpr int kThreads = 128;
-constexpr int kBlockChannels = 4 * kThreads;
+constexpr int kThreads = 256;
+constexpr int kBlockChannels = 2 * kThreads;
+constexpr int kBlocksPerSm = 3;
 
 struct ConvBwdParams {
     const void* dout;
@@ -42,48 +43,39 @@ struct ConvBwdParams {
     int L, Dm, seg, nbd;
 };
 
-// 4 channels of one step as loaded.  VEC: adjacent ones; else kThreads apart, so that a warp's are adjacent.
-template <typename T, bool VEC> struct Chan4;
-template <> struct Chan4<float, true> {
-    float4 v;
-    __device__ __forceinline__ void load(const float* q, int) { v = __ldcs(reinterpret_cast<const float4*>(q)); }
-    __device__ __forceinline__ float2 lo() const { return make_float2(v.x, v.y); }
-    __device__ __forceinline__ float2 hi() const { return make_float2(v.z, v.w); }
-    __device__ __forceinline__ void zero() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
+// 2 channels of one step as loaded.  VEC: adjacent ones; else kThreads apart, so that a warp's are adjacent.
+template <typename T, bool VEC> struct Chan2;
+template <> struct Chan2<float, true> {
+    float2 v;
+    __device__ __forceinline__ void load(const float* q, bool) { v = __ldcs(reinterpret_cast<const float2*>(q)); }
+    __device__ __forceinline__ float2 get() const { return v; }
+    __device__ __forceinline__ void zero() { v = make_float2(0.f, 0.f); }
 };
-template <> struct Chan4<__nv_bfloat16, true> {
-    uint2 v;
-    __device__ __forceinline__ void load(const __nv_bfloat16* q, int) { v = __ldcs(reinterpret_cast<const uint2*>(q)); }
-    static __device__ __forceinline__ float2 pair(uint32_t u) { return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); }
-    __device__ __forceinline__ float2 lo() const { return pair(v.x); }
-    __device__ __forceinline__ float2 hi() const { return pair(v.y); }
-    __device__ __forceinline__ void zero() { v = make_uint2(0u, 0u); }
+template <> struct Chan2<__nv_bfloat16, true> {
+    uint32_t v;
+    __device__ __forceinline__ void load(const __nv_bfloat16* q, bool) { v = __ldcs(reinterpret_cast<const uint32_t*>(q)); }
+    __device__ __forceinline__ float2 get() const { return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)); }
+    __device__ __forceinline__ void zero() { v = 0u; }
 };
-template <typename T> struct Chan4<T, false> {
-    T v[4];
-    __device__ __forceinline__ void load(const T* q, int n) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] = c < n ? q[c * kThreads] : from_f32<T>(0.f);
+template <typename T> struct Chan2<T, false> {
+    T v[2];
+    __device__ __forceinline__ void load(const T* q, bool two) {
+        v[0] = q[0];
+        v[1] = two ? q[kThreads] : from_f32<T>(0.f);
     }
-    __device__ __forceinline__ float2 lo() const { return make_float2(to_f32<T>(v[0]), to_f32<T>(v[1])); }
-    __device__ __forceinline__ float2 hi() const { return make_float2(to_f32<T>(v[2]), to_f32<T>(v[3])); }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] = from_f32<T>(0.f);
-    }
+    __device__ __forceinline__ float2 get() const { return make_float2(to_f32<T>(v[0]), to_f32<T>(v[1])); }
+    __device__ __forceinline__ void zero() { v[0] = v[1] = from_f32<T>(0.f); }
 };
 template <typename T, bool VEC>
-__device__ __forceinline__ void store4(T* q, int n, float2 lo, float2 hi) {
+__device__ __forceinline__ void store2(T* q, bool two, float2 v) {
     if constexpr (VEC && sizeof(T) == 4) {
-        __stcs(reinterpret_cast<float4*>(q), make_float4(lo.x, lo.y, hi.x, hi.y));
+        __stcs(reinterpret_cast<float2*>(q), v);
     } else if constexpr (VEC) {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(lo.x, lo.y), b = __floats2bfloat162_rn(hi.x, hi.y);
-        __stcs(reinterpret_cast<uint2*>(q), make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b)));
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+        __stcs(reinterpret_cast<uint32_t*>(q), *reinterpret_cast<const uint32_t*>(&h));
     } else {
-        const float v[4] = {lo.x, lo.y, hi.x, hi.y};
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (c < n) q[c * kThreads] = from_f32<T>(v[c]);
+        q[0] = from_f32<T>(v.x);
+        if (two) q[kThreads] = from_f32<T>(v.y);
     }
 }
 
@@ -93,129 +85,123 @@ __device__ __forceinline__ float2 silu_slope(float2 v) {
 }
 
 template <typename T, bool VEC, bool SILU>
-__global__ void __launch_bounds__(kThreads, 4) ss_conv1d_bwd_kernel(const ConvBwdParams p) {
-    constexpr int U = sizeof(T) == 2 ? 8 : 4;      // steps whose loads are issued together
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) ss_conv1d_bwd_kernel(const ConvBwdParams p) {
+    constexpr int U = VEC && sizeof(T) == 2 ? 8 : 4;      // steps whose loads are issued together
     const int seg = static_cast<int>(blockIdx.x) / p.nbd, b = blockIdx.y;
     const int base = (static_cast<int>(blockIdx.x) - seg * p.nbd) * kBlockChannels;
-    const int d0 = base + (VEC ? 4 * threadIdx.x : threadIdx.x);
-    constexpr int kStep = VEC ? 1 : kThreads;      // from one of the thread's channels to the next
+    const int d0 = base + (VEC ? 2 * threadIdx.x : threadIdx.x);
     if (d0 >= p.Dm) return;
-    const int nc = VEC ? 4 : min(4, (p.Dm - d0 + kThreads - 1) / kThreads);
+    const int d1 = d0 + (VEC ? 1 : kThreads);
+    const bool two = VEC || d1 < p.Dm;
     const int t0 = seg * p.seg, t1 = min(t0 + p.seg, p.L);
     const T* x = static_cast<const T*>(p.x) + b * p.x_b + d0;
     const T* dout = static_cast<const T*>(p.dout) + b * p.do_b + d0;
     T* dx = static_cast<T*>(p.dx) + b * p.dx_b + d0;
 
-    auto chan = [&](int c) { return d0 + c * kStep; };
-    float2 w[2][kConvK], bs[2];
-    auto each = [&](auto&& f) {                    // f(channel) for the two pairs
-        float2 r[2];
-        r[0].x = f(0);
-        r[0].y = nc > 1 ? f(1) : 0.f;
-        r[1].x = nc > 2 ? f(2) : 0.f;
-        r[1].y = nc > 3 ? f(3) : 0.f;
-        return make_float4(r[0].x, r[0].y, r[1].x, r[1].y);
+    auto each = [&](auto&& f) { return make_float2(f(d0), two ? f(d1) : 0.f); };            // f(channel)
+    auto window = [&](const float* w, int k) {
+        return each([&](int d) { return w[(static_cast<int64_t>(b) * p.Dm + d) * 3 + k]; });
     };
+    float2 w[kConvK];
 #pragma unroll
-    for (int k = 0; k < kConvK; ++k) {
-        const float4 f = each([&](int c) { return p.w[static_cast<int64_t>(chan(c)) * kConvK + k]; });
-        w[0][k] = make_float2(f.x, f.y);
-        w[1][k] = make_float2(f.z, f.w);
-    }
-    {
-        const float4 f = each([&](int c) { return p.bias ? p.bias[chan(c)] : 0.f; });
-        bs[0] = make_float2(f.x, f.y);
-        bs[1] = make_float2(f.z, f.w);
-    }
-    // the three samples before the segment
-    float2 e[3][2];
+    for (int k = 0; k < kConvK; ++k) w[k] = each([&](int d) { return p.w[static_cast<int64_t>(d) * kConvK + k]; });
+    const float2 bs = each([&](int d) { return p.bias ? p.bias[d] : 0.f; });
+    // the three samples before the segment, and g of the three steps before
+    float2 e[3], g[3], dw[kConvK], db = splat2(0.f);
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
         const int t = t0 - 3 + j;
+        e[j] = g[j] = splat2(0.f);
         if (t >= 0) {
-            Chan4<T, VEC> q;
-            q.load(x + t * p.x_l, nc);
-            e[j][0] = q.lo();
-            e[j][1] = q.hi();
-        } else {
-            const float4 f = each([&](int c) { return p.win_in ? p.win_in[(static_cast<int64_t>(b) * p.Dm + chan(c)) * 3 + 3 + t] : 0.f; });
-            e[j][0] = make_float2(f.x, f.y);
-            e[j][1] = make_float2(f.z, f.w);
+            Chan2<T, VEC> q;
+            q.load(x + t * p.x_l, two);
+            e[j] = q.get();
+        } else if (p.win_in) {
+            e[j] = window(p.win_in, 3 + t);
         }
     }
-    float2 g[3][2], dw[2][kConvK], db[2];          // g of the three steps before
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        db[h] = g[0][h] = g[1][h] = g[2][h] = splat2(0.f);
-#pragma unroll
-        for (int k = 0; k < kConvK; ++k) dw[h][k] = splat2(0.f);
-    }
-    const int end = t1 + 3;                        // the steps whose g reach the segment's outputs
-    for (int tb = t0; tb < end; tb += U) {
-        Chan4<T, VEC> xs[U], ds[U];
+    for (int k = 0; k < kConvK; ++k) dw[k] = splat2(0.f);
+
+    const int end = t1 + 3, have = min(end, p.L);  // the steps whose g reach the segment's outputs; those there are
+    const T* xq = x + t0 * p.x_l;
+    const T* dq = dout + t0 * p.do_l;
+    auto load = [&](int tb, Chan2<T, VEC> (&xs)[U], Chan2<T, VEC> (&ds)[U]) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int t = tb + u;
-            if (t < min(end, p.L)) {
-                xs[u].load(x + t * p.x_l, nc);
-                ds[u].load(dout + t * p.do_l, nc);
+            if (tb + u < have) {
+                xs[u].load(xq, two);
+                ds[u].load(dq, two);
             } else {
                 xs[u].zero();
                 ds[u].zero();
             }
+            xq += p.x_l;
+            dq += p.do_l;
+        }
+    };
+    // Step t: g_t (live: of a step that there is), its part in the weight's gradients (own: of the segment), and de of
+    // three steps before.
+    auto step = [&](float2 xv, float2 gt, bool own, bool live) {
+        if constexpr (SILU) gt = mul2(gt, silu_slope(fma2(w[3], xv, fma2(w[2], e[2], fma2(w[1], e[1], fma2(w[0], e[0], bs))))));
+        if (!live) gt = splat2(0.f);
+        if (own) {
+            dw[0] = fma2(gt, e[0], dw[0]);
+            dw[1] = fma2(gt, e[1], dw[1]);
+            dw[2] = fma2(gt, e[2], dw[2]);
+            dw[3] = fma2(gt, xv, dw[3]);
+            db = add2(db, gt);
+        }
+        const float2 de = fma2(w[0], gt, fma2(w[1], g[2], fma2(w[2], g[1], mul2(w[3], g[0]))));
+        g[0] = g[1];
+        g[1] = g[2];
+        g[2] = gt;
+        e[0] = e[1];
+        e[1] = e[2];
+        e[2] = xv;
+        return de;
+    };
+    T* out = dx + t0 * p.dx_l;
+    Chan2<T, VEC> xs[U], ds[U];
+    load(t0, xs, ds);
+    for (int tb = t0; tb < end; tb += U) {
+        Chan2<T, VEC> xn[U], dn[U];
+        load(tb + U, xn, dn);
+        if (tb >= t0 + 3 && tb + U <= t1) {        // steps inside the segment, as all but its ends are
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                store2<T, VEC>(out, two, step(xs[u].get(), ds[u].get(), true, true));
+                out += p.dx_l;
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int t = tb + u, j = t - 3;   // j: the step (below 0: the window's entry) that de belongs to
+                if (t >= end) break;
+                float2 de = step(xs[u].get(), ds[u].get(), t < t1, t < p.L);
+                if (p.dwin_out && j >= p.L - 3) de = add2(de, window(p.dwin_out, j - (p.L - 3)));
+                if (j >= t0) {
+                    store2<T, VEC>(out, two, de);
+                    out += p.dx_l;
+                } else if (j < 0 && p.dwin_in) {
+                    float* q = p.dwin_in + static_cast<int64_t>(b) * p.Dm * 3 + 3 + j;
+                    q[static_cast<int64_t>(d0) * 3] = de.x;
+                    if (two) q[static_cast<int64_t>(d1) * 3] = de.y;
+                }
+            }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int t = tb + u;
-            if (t >= end) break;
-            const float2 xv[2] = {xs[u].lo(), xs[u].hi()}, dv[2] = {ds[u].lo(), ds[u].hi()};
-            float2 de[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float2 gt = dv[h];
-                if constexpr (SILU) {
-                    const float2 v = fma2(w[h][3], xv[h], fma2(w[h][2], e[2][h], fma2(w[h][1], e[1][h], fma2(w[h][0], e[0][h], bs[h]))));
-                    gt = mul2(gt, silu_slope(v));
-                }
-                if (t >= p.L) gt = splat2(0.f);
-                if (t < t1) {
-                    dw[h][0] = fma2(gt, e[0][h], dw[h][0]);
-                    dw[h][1] = fma2(gt, e[1][h], dw[h][1]);
-                    dw[h][2] = fma2(gt, e[2][h], dw[h][2]);
-                    dw[h][3] = fma2(gt, xv[h], dw[h][3]);
-                    db[h] = add2(db[h], gt);
-                }
-                de[h] = fma2(w[h][0], gt, fma2(w[h][1], g[2][h], fma2(w[h][2], g[1][h], mul2(w[h][3], g[0][h]))));
-                g[0][h] = g[1][h];
-                g[1][h] = g[2][h];
-                g[2][h] = gt;
-                e[0][h] = e[1][h];
-                e[1][h] = e[2][h];
-                e[2][h] = xv[h];
-            }
-            const int j = t - 3;                   // the step (below 0: the window's entry) that de belongs to
-            if (p.dwin_out && j >= p.L - 3) {
-                const float4 f = each([&](int c) { return p.dwin_out[(static_cast<int64_t>(b) * p.Dm + chan(c)) * 3 + j - (p.L - 3)]; });
-                de[0] = add2(de[0], make_float2(f.x, f.y));
-                de[1] = add2(de[1], make_float2(f.z, f.w));
-            }
-            if (j >= t0) {
-                store4<T, VEC>(dx + j * p.dx_l, nc, de[0], de[1]);
-            } else if (j < 0 && p.dwin_in) {
-                const float v[4] = {de[0].x, de[0].y, de[1].x, de[1].y};
-                for (int c = 0; c < nc; ++c) p.dwin_in[(static_cast<int64_t>(b) * p.Dm + chan(c)) * 3 + 3 + j] = v[c];
-            }
+            xs[u] = xn[u];
+            ds[u] = dn[u];
         }
     }
     float* mine = p.part + (static_cast<int64_t>(b) * (gridDim.x / p.nbd) + seg) * p.ld;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        if (c >= nc) break;
-        const int h = c / 2;
-        const bool y = c & 1;
-        float4 f = y ? make_float4(dw[h][0].y, dw[h][1].y, dw[h][2].y, dw[h][3].y) : make_float4(dw[h][0].x, dw[h][1].x, dw[h][2].x, dw[h][3].x);
-        *reinterpret_cast<float4*>(mine + 4 * static_cast<int64_t>(chan(c))) = f;
-        mine[4 * static_cast<int64_t>(p.Dm) + chan(c)] = y ? db[h].y : db[h].x;
+    *reinterpret_cast<float4*>(mine + 4 * static_cast<int64_t>(d0)) = make_float4(dw[0].x, dw[1].x, dw[2].x, dw[3].x);
+    mine[4 * static_cast<int64_t>(p.Dm) + d0] = db.x;
+    if (two) {
+        *reinterpret_cast<float4*>(mine + 4 * static_cast<int64_t>(d1)) = make_float4(dw[0].y, dw[1].y, dw[2].y, dw[3].y);
+        mine[4 * static_cast<int64_t>(p.Dm) + d1] = db.y;
     }
 }
 
@@ -244,7 +230,7 @@ int64_t plan_slots() {
         cudaGetLastError();
         sms = 152;
     }
-    return 4 * static_cast<int64_t>(sms);
+    return kBlocksPerSm * static_cast<int64_t>(sms);
 }
 
 int64_t row_floats(int64_t Dm) { return (5 * Dm + 3) / 4 * 4; }
@@ -356,11 +342,11 @@ extern "C" ss_status ss_conv1d_bwd(const void* dout, const void* x, const float*
     p.dwin_in = dwindow_in; p.part = static_cast<float*>(workspace);
     p.do_b = s.dout_b; p.do_l = s.dout_l; p.x_b = s.x_b; p.x_l = s.x_l; p.dx_b = s.dx_b; p.dx_l = s.dx_l; p.ld = row_floats(Dm);
     p.L = static_cast<int>(L); p.Dm = static_cast<int>(Dm); p.seg = static_cast<int>(q.seg); p.nbd = static_cast<int>(q.nbd);
-    const int64_t va = 4 * es;                     // bytes of 4 channels
+    const int64_t va = 2 * es;                     // bytes of 2 channels
     auto wide = [&](const void* a, int64_t sb, int64_t sl) {
         return is_aligned(a, va) && (sl * es) % va == 0 && (batch == 1 || (sb * es) % va == 0);
     };
-    const bool vec = Dm % 4 == 0 && wide(dout, s.dout_b, s.dout_l) && wide(x, s.x_b, s.x_l) && wide(dx, s.dx_b, s.dx_l);
+    const bool vec = Dm % 2 == 0 && wide(dout, s.dout_b, s.dout_l) && wide(x, s.x_b, s.x_l) && wide(dx, s.dx_b, s.dx_l);
     void (*kern)(ConvBwdParams) = bf16 ? kernel_of<__nv_bfloat16>(vec, silu != 0) : kernel_of<float>(vec, silu != 0);
     kern<<<dim3(static_cast<unsigned>(q.segs * q.nbd), static_cast<unsigned>(batch)), kThreads, 0, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return SS_ERR_CUDA;
