@@ -4,11 +4,12 @@
 //   de_j = Σ_k w_k g_{j-k}  (dx_t = de_{t+3}; de_0..2 is the window's gradient),
 //   dw_k = Σ_{b,t} g_t e_{t+k},  dbias = Σ_{b,t} g_t
 //
-// A stream of three elements per step and channel.  A thread has 2 channels (a packed pair) and a segment of steps;
-// the next steps' loads are in flight while it works on some, and a warp covers 64 channels of a step.  It runs
-// three steps past its segment, whose g belong to its last outputs.  The weight's gradients are sums in registers;
-// every thread leaves its own in the workspace (a row of it per segment) and a second kernel adds the rows up in
-// the same order every time.
+// A stream of three elements per step and channel: what counts is how much of it is on its way.  A thread has 2
+// channels (a packed pair) and a segment of steps; TMA brings the steps into a ring in shared memory (four stages of
+// 8 KB a CTA, 7 CTAs an SM), as loads into registers stayed behind at a third of that (4 x 8192 x 5120 bf16: 315 us).
+// It runs three steps past its segment, whose g belong to its last outputs.  The weight's gradients are sums in
+// registers; every thread leaves its own in the workspace (a row of it per segment) and a second kernel adds the
+// rows up in the same order every time.  Layouts that TMA does not take go by plain loads.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -19,15 +20,18 @@
 #include "column_sum.h"
 #include "device_common.cuh"
 #include "host_util.h"
+#include "internal.h"
 
 namespace selscan {
 namespace {
 
 constexpr int kConvK = SS_CONV_WIDTH;   // 4
 constexpr int kSegMin = 8;
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kBlockChannels = 2 * kThreads;
-constexpr int kBlocksPerSm = 3;
+constexpr int kBlocksPerSm = 6;
+constexpr int kStages = 4;
+template <typename T> constexpr int kSteps = 16 / sizeof(T);          // steps of a stage: 4 KB of x and of dout
 
 struct ConvBwdParams {
     const void* dout;
@@ -41,42 +45,21 @@ struct ConvBwdParams {
     float* part;            // [batch · segs][ld]: dw [Dm, 4], then dbias [Dm]
     int64_t do_b, do_l, x_b, x_l, dx_b, dx_l, ld;
     int L, Dm, seg, nbd;
+    unsigned int* err;
+};
+struct ConvBwdMaps {
+    CUtensorMap x, dout;    // [batch, L, Dm], boxes of kSteps by kBlockChannels
 };
 
-// 2 channels of one step as loaded.  VEC: adjacent ones; else kThreads apart, so that a warp's are adjacent.
-template <typename T, bool VEC> struct Chan2;
-template <> struct Chan2<float, true> {
-    float2 v;
-    __device__ __forceinline__ void load(const float* q, bool) { v = __ldcs(reinterpret_cast<const float2*>(q)); }
-    __device__ __forceinline__ float2 get() const { return v; }
-    __device__ __forceinline__ void zero() { v = make_float2(0.f, 0.f); }
-};
-template <> struct Chan2<__nv_bfloat16, true> {
-    uint32_t v;
-    __device__ __forceinline__ void load(const __nv_bfloat16* q, bool) { v = __ldcs(reinterpret_cast<const uint32_t*>(q)); }
-    __device__ __forceinline__ float2 get() const { return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)); }
-    __device__ __forceinline__ void zero() { v = 0u; }
-};
-template <typename T> struct Chan2<T, false> {
-    T v[2];
-    __device__ __forceinline__ void load(const T* q, bool two) {
-        v[0] = q[0];
-        v[1] = two ? q[kThreads] : from_f32<T>(0.f);
-    }
-    __device__ __forceinline__ float2 get() const { return make_float2(to_f32<T>(v[0]), to_f32<T>(v[1])); }
-    __device__ __forceinline__ void zero() { v[0] = v[1] = from_f32<T>(0.f); }
-};
-template <typename T, bool VEC>
-__device__ __forceinline__ void store2(T* q, bool two, float2 v) {
-    if constexpr (VEC && sizeof(T) == 4) {
-        __stcs(reinterpret_cast<float2*>(q), v);
-    } else if constexpr (VEC) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
-        __stcs(reinterpret_cast<uint32_t*>(q), *reinterpret_cast<const uint32_t*>(&h));
-    } else {
-        q[0] = from_f32<T>(v.x);
-        if (two) q[kThreads] = from_f32<T>(v.y);
-    }
+__device__ __forceinline__ float2 load2(const float* q) { return *reinterpret_cast<const float2*>(q); }
+__device__ __forceinline__ float2 load2(const __nv_bfloat16* q) {
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(q);
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+__device__ __forceinline__ void store2(float* q, float2 v) { __stcs(reinterpret_cast<float2*>(q), v); }
+__device__ __forceinline__ void store2(__nv_bfloat16* q, float2 v) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+    __stcs(reinterpret_cast<uint32_t*>(q), *reinterpret_cast<const uint32_t*>(&h));
 }
 
 __device__ __forceinline__ float2 silu_slope(float2 v) {
@@ -84,65 +67,53 @@ __device__ __forceinline__ float2 silu_slope(float2 v) {
     return mul2(s, fma2(v, fma2(s, splat2(-1.f), splat2(1.f)), splat2(1.f)));
 }
 
-template <typename T, bool VEC, bool SILU>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) ss_conv1d_bwd_kernel(const ConvBwdParams p) {
-    constexpr int U = VEC && sizeof(T) == 2 ? 8 : 4;      // steps whose loads are issued together
-    const int seg = static_cast<int>(blockIdx.x) / p.nbd, b = blockIdx.y;
-    const int base = (static_cast<int>(blockIdx.x) - seg * p.nbd) * kBlockChannels;
-    const int d0 = base + (VEC ? 2 * threadIdx.x : threadIdx.x);
-    if (d0 >= p.Dm) return;
-    const int d1 = d0 + (VEC ? 1 : kThreads);
-    const bool two = VEC || d1 < p.Dm;
-    const int t0 = seg * p.seg, t1 = min(t0 + p.seg, p.L);
-    const T* x = static_cast<const T*>(p.x) + b * p.x_b + d0;
-    const T* dout = static_cast<const T*>(p.dout) + b * p.do_b + d0;
-    T* dx = static_cast<T*>(p.dx) + b * p.dx_b + d0;
+// A thread's place: two channels (adjacent ones, or kThreads apart, so that a warp's are adjacent) and a segment.
+struct Place {
+    int seg, b, d0, d1, t0, t1, end;               // end: behind the steps whose g reach the segment's outputs
+    bool one, two;                                 // channels that there are
+};
+__device__ __forceinline__ Place place_of(const ConvBwdParams& p, bool adjacent) {
+    Place q;
+    q.seg = static_cast<int>(blockIdx.x) / p.nbd;
+    q.b = blockIdx.y;
+    q.d0 = (static_cast<int>(blockIdx.x) - q.seg * p.nbd) * kBlockChannels + (adjacent ? 2 : 1) * static_cast<int>(threadIdx.x);
+    q.d1 = q.d0 + (adjacent ? 1 : kThreads);
+    q.one = q.d0 < p.Dm;
+    q.two = q.d1 < p.Dm;
+    q.t0 = q.seg * p.seg;
+    q.t1 = min(q.t0 + p.seg, p.L);
+    q.end = q.t1 + 3;
+    return q;
+}
 
-    auto each = [&](auto&& f) { return make_float2(f(d0), two ? f(d1) : 0.f); };            // f(channel)
-    auto window = [&](const float* w, int k) {
-        return each([&](int d) { return w[(static_cast<int64_t>(b) * p.Dm + d) * 3 + k]; });
-    };
-    float2 w[kConvK];
+// What a thread carries from step to step.
+template <typename T, bool SILU> struct Pair {
+    float2 w[kConvK], bs, e[3], g[3], dw[kConvK], db;      // e: the three samples before, g: of the three steps before
+    template <typename F> static __device__ __forceinline__ float2 each(const Place& q, F&& f) {
+        return make_float2(q.one ? f(q.d0) : 0.f, q.two ? f(q.d1) : 0.f);
+    }
+    static __device__ __forceinline__ float2 window(const ConvBwdParams& p, const Place& q, const float* w, int k) {
+        return each(q, [&](int d) { return w[(static_cast<int64_t>(q.b) * p.Dm + d) * 3 + k]; });
+    }
+    __device__ __forceinline__ void start(const ConvBwdParams& p, const Place& q) {
 #pragma unroll
-    for (int k = 0; k < kConvK; ++k) w[k] = each([&](int d) { return p.w[static_cast<int64_t>(d) * kConvK + k]; });
-    const float2 bs = each([&](int d) { return p.bias ? p.bias[d] : 0.f; });
-    // the three samples before the segment, and g of the three steps before
-    float2 e[3], g[3], dw[kConvK], db = splat2(0.f);
+        for (int k = 0; k < kConvK; ++k) {
+            w[k] = each(q, [&](int d) { return p.w[static_cast<int64_t>(d) * kConvK + k]; });
+            dw[k] = splat2(0.f);
+        }
+        bs = each(q, [&](int d) { return p.bias ? p.bias[d] : 0.f; });
+        db = splat2(0.f);
 #pragma unroll
-    for (int j = 0; j < 3; ++j) {
-        const int t = t0 - 3 + j;
-        e[j] = g[j] = splat2(0.f);
-        if (t >= 0) {
-            Chan2<T, VEC> q;
-            q.load(x + t * p.x_l, two);
-            e[j] = q.get();
-        } else if (p.win_in) {
-            e[j] = window(p.win_in, 3 + t);
+        for (int j = 0; j < 3; ++j) {
+            const int t = q.t0 - 3 + j;
+            e[j] = g[j] = splat2(0.f);
+            if (t >= 0) e[j] = each(q, [&](int d) { return to_f32<T>(static_cast<const T*>(p.x)[q.b * p.x_b + t * p.x_l + d]); });
+            else if (p.win_in) e[j] = window(p, q, p.win_in, 3 + t);
         }
     }
-#pragma unroll
-    for (int k = 0; k < kConvK; ++k) dw[k] = splat2(0.f);
-
-    const int end = t1 + 3, have = min(end, p.L);  // the steps whose g reach the segment's outputs; those there are
-    const T* xq = x + t0 * p.x_l;
-    const T* dq = dout + t0 * p.do_l;
-    auto load = [&](int tb, Chan2<T, VEC> (&xs)[U], Chan2<T, VEC> (&ds)[U]) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (tb + u < have) {
-                xs[u].load(xq, two);
-                ds[u].load(dq, two);
-            } else {
-                xs[u].zero();
-                ds[u].zero();
-            }
-            xq += p.x_l;
-            dq += p.do_l;
-        }
-    };
-    // Step t: g_t (live: of a step that there is), its part in the weight's gradients (own: of the segment), and de of
-    // three steps before.
-    auto step = [&](float2 xv, float2 gt, bool own, bool live) {
+    // Step t: g_t (live: of a step that there is), its part in the weight's gradients (own: of the segment), and de
+    // of three steps before.
+    __device__ __forceinline__ float2 step(float2 xv, float2 gt, bool own, bool live) {
         if constexpr (SILU) gt = mul2(gt, silu_slope(fma2(w[3], xv, fma2(w[2], e[2], fma2(w[1], e[1], fma2(w[0], e[0], bs))))));
         if (!live) gt = splat2(0.f);
         if (own) {
@@ -160,49 +131,122 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) ss_conv1d_bwd_kernel(c
         e[1] = e[2];
         e[2] = xv;
         return de;
+    }
+    // The same at a segment's ends: returns whether de is a step's of the segment; the window's goes where it belongs.
+    __device__ __forceinline__ bool end_step(const ConvBwdParams& p, const Place& q, int t, float2 xv, float2 gt, float2* de) {
+        *de = step(xv, gt, t < q.t1, t < p.L);
+        const int j = t - 3;                       // the step (below 0: the window's entry) that de belongs to
+        if (p.dwin_out && j >= p.L - 3) *de = add2(*de, window(p, q, p.dwin_out, j - (p.L - 3)));
+        if (j >= q.t0) return true;
+        if (j < 0 && p.dwin_in) {
+            float* o = p.dwin_in + static_cast<int64_t>(q.b) * p.Dm * 3 + 3 + j;
+            if (q.one) o[static_cast<int64_t>(q.d0) * 3] = de->x;
+            if (q.two) o[static_cast<int64_t>(q.d1) * 3] = de->y;
+        }
+        return false;
+    }
+    __device__ __forceinline__ void leave(const ConvBwdParams& p, const Place& q) const {
+        float* mine = p.part + (static_cast<int64_t>(q.b) * (gridDim.x / p.nbd) + q.seg) * p.ld;
+        if (q.one) {
+            *reinterpret_cast<float4*>(mine + 4 * static_cast<int64_t>(q.d0)) = make_float4(dw[0].x, dw[1].x, dw[2].x, dw[3].x);
+            mine[4 * static_cast<int64_t>(p.Dm) + q.d0] = db.x;
+        }
+        if (q.two) {
+            *reinterpret_cast<float4*>(mine + 4 * static_cast<int64_t>(q.d1)) = make_float4(dw[0].y, dw[1].y, dw[2].y, dw[3].y);
+            mine[4 * static_cast<int64_t>(p.Dm) + q.d1] = db.y;
+        }
+    }
+};
+
+template <typename T, bool SILU>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) ss_conv1d_bwd_kernel(const ConvBwdParams p, const __grid_constant__ ConvBwdMaps m) {
+    constexpr int U = kSteps<T>, kTile = U * kBlockChannels;
+    __shared__ __align__(128) T tile[kStages][2][kTile];
+    __shared__ uint64_t full[kStages];
+    __shared__ int abort_flag;
+    const Place q = place_of(p, true);
+    const int tid = threadIdx.x, c0 = q.d0 - 2 * tid, n = (q.end - q.t0 + U - 1) / U;
+    auto issue = [&](int i) {                      // (steps and channels outside the tensor are zeros)
+        const int s = i % kStages;
+        mbar_expect_tx(&full[s], 2 * kTile * sizeof(T));
+        tma_load_3d(tile[s][0], &m.x, &full[s], c0, q.t0 + i * U, q.b);
+        tma_load_3d(tile[s][1], &m.dout, &full[s], c0, q.t0 + i * U, q.b);
     };
-    T* out = dx + t0 * p.dx_l;
-    Chan2<T, VEC> xs[U], ds[U];
-    load(t0, xs, ds);
-    for (int tb = t0; tb < end; tb += U) {
-        Chan2<T, VEC> xn[U], dn[U];
-        load(tb + U, xn, dn);
-        if (tb >= t0 + 3 && tb + U <= t1) {        // steps inside the segment, as all but its ends are
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1);
+        abort_flag = 0;
+        mbar_fence_init();
+        for (int i = 0; i < min(n, kStages); ++i) issue(i);
+    }
+    Pair<T, SILU> c;
+    c.start(p, q);
+    __syncthreads();
+    T* out = static_cast<T*>(p.dx) + q.b * p.dx_b + q.t0 * p.dx_l + q.d0;
+    for (int i = 0; i < n; ++i) {
+        const int s = i % kStages, tb = q.t0 + i * U;
+        const bool ok = mbar_wait_bounded(&full[s], (i / kStages) & 1, &abort_flag, p.err);
+        const T* xs = tile[s][0] + 2 * tid;
+        const T* ds = tile[s][1] + 2 * tid;
+        if (tb >= q.t0 + 3 && tb + U <= q.t1) {    // steps inside the segment, as all but its ends are
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                store2<T, VEC>(out, two, step(xs[u].get(), ds[u].get(), true, true));
+                const float2 de = c.step(load2(xs + u * kBlockChannels), load2(ds + u * kBlockChannels), true, true);
+                if (q.one) store2(out, de);
                 out += p.dx_l;
             }
         } else {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int t = tb + u, j = t - 3;   // j: the step (below 0: the window's entry) that de belongs to
-                if (t >= end) break;
-                float2 de = step(xs[u].get(), ds[u].get(), t < t1, t < p.L);
-                if (p.dwin_out && j >= p.L - 3) de = add2(de, window(p.dwin_out, j - (p.L - 3)));
-                if (j >= t0) {
-                    store2<T, VEC>(out, two, de);
+            for (int u = 0; u < U && tb + u < q.end; ++u) {
+                float2 de;
+                if (c.end_step(p, q, tb + u, load2(xs + u * kBlockChannels), load2(ds + u * kBlockChannels), &de)) {
+                    if (q.one) store2(out, de);
                     out += p.dx_l;
-                } else if (j < 0 && p.dwin_in) {
-                    float* q = p.dwin_in + static_cast<int64_t>(b) * p.Dm * 3 + 3 + j;
-                    q[static_cast<int64_t>(d0) * 3] = de.x;
-                    if (two) q[static_cast<int64_t>(d1) * 3] = de.y;
                 }
             }
         }
+        if (__syncthreads_or(!ok)) {               // a wait that ran out: copies in flight are over long before this
+            for (int k = 0; k < 20; ++k) __nanosleep(1000000);
+            break;
+        }
+        if (tid == 0 && i + kStages < n) issue(i + kStages);
+    }
+    c.leave(p, q);
+}
+
+template <typename T, bool SILU>
+__global__ void __launch_bounds__(kThreads) ss_conv1d_bwd_plain_kernel(const ConvBwdParams p) {
+    constexpr int U = 4;                           // steps whose loads are issued together
+    const Place q = place_of(p, false);
+    if (!q.one) return;
+    Pair<T, SILU> c;
+    c.start(p, q);
+    const T* x = static_cast<const T*>(p.x) + q.b * p.x_b + q.t0 * p.x_l + q.d0;
+    const T* dout = static_cast<const T*>(p.dout) + q.b * p.do_b + q.t0 * p.do_l + q.d0;
+    T* out = static_cast<T*>(p.dx) + q.b * p.dx_b + q.t0 * p.dx_l + q.d0;
+    for (int tb = q.t0; tb < q.end; tb += U) {
+        T xs[U][2], ds[U][2];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            xs[u] = xn[u];
-            ds[u] = dn[u];
+            const bool ok = tb + u < min(q.end, p.L);
+            xs[u][0] = ok ? x[0] : from_f32<T>(0.f);
+            xs[u][1] = ok && q.two ? x[kThreads] : from_f32<T>(0.f);
+            ds[u][0] = ok ? dout[0] : from_f32<T>(0.f);
+            ds[u][1] = ok && q.two ? dout[kThreads] : from_f32<T>(0.f);
+            x += p.x_l;
+            dout += p.do_l;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (tb + u >= q.end) break;
+            float2 de;
+            if (c.end_step(p, q, tb + u, make_float2(to_f32<T>(xs[u][0]), to_f32<T>(xs[u][1])),
+                           make_float2(to_f32<T>(ds[u][0]), to_f32<T>(ds[u][1])), &de)) {
+                out[0] = from_f32<T>(de.x);
+                if (q.two) out[kThreads] = from_f32<T>(de.y);
+                out += p.dx_l;
+            }
         }
     }
-    float* mine = p.part + (static_cast<int64_t>(b) * (gridDim.x / p.nbd) + seg) * p.ld;
-    *reinterpret_cast<float4*>(mine + 4 * static_cast<int64_t>(d0)) = make_float4(dw[0].x, dw[1].x, dw[2].x, dw[3].x);
-    mine[4 * static_cast<int64_t>(p.Dm) + d0] = db.x;
-    if (two) {
-        *reinterpret_cast<float4*>(mine + 4 * static_cast<int64_t>(d1)) = make_float4(dw[0].y, dw[1].y, dw[2].y, dw[3].y);
-        mine[4 * static_cast<int64_t>(p.Dm) + d1] = db.y;
-    }
+    c.leave(p, q);
 }
 
 // Steps per thread for batch · ceil(L / seg) · nbd blocks when `slots` are resident at once: the length whose
@@ -252,10 +296,11 @@ __global__ void window_grad_copy(const float* dwin_out, float* dwin_in, int64_t 
     if (i < n) dwin_in[i] = dwin_out ? dwin_out[i] : 0.f;
 }
 
-template <typename T>
-void (*kernel_of(bool vec, bool silu))(ConvBwdParams) {
-    if (vec) return silu ? ss_conv1d_bwd_kernel<T, true, true> : ss_conv1d_bwd_kernel<T, true, false>;
-    return silu ? ss_conv1d_bwd_kernel<T, false, true> : ss_conv1d_bwd_kernel<T, false, false>;
+template <typename T, bool SILU>
+cudaError_t launch(const ConvBwdParams& p, const ConvBwdMaps* m, dim3 grid, cudaStream_t stream) {
+    if (m) ss_conv1d_bwd_kernel<T, SILU><<<grid, kThreads, 0, stream>>>(p, *m);
+    else ss_conv1d_bwd_plain_kernel<T, SILU><<<grid, kThreads, 0, stream>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -342,14 +387,18 @@ extern "C" ss_status ss_conv1d_bwd(const void* dout, const void* x, const float*
     p.dwin_in = dwindow_in; p.part = static_cast<float*>(workspace);
     p.do_b = s.dout_b; p.do_l = s.dout_l; p.x_b = s.x_b; p.x_l = s.x_l; p.dx_b = s.dx_b; p.dx_l = s.dx_l; p.ld = row_floats(Dm);
     p.L = static_cast<int>(L); p.Dm = static_cast<int>(Dm); p.seg = static_cast<int>(q.seg); p.nbd = static_cast<int>(q.nbd);
-    const int64_t va = 2 * es;                     // bytes of 2 channels
-    auto wide = [&](const void* a, int64_t sb, int64_t sl) {
-        return is_aligned(a, va) && (sl * es) % va == 0 && (batch == 1 || (sb * es) % va == 0);
-    };
-    const bool vec = Dm % 2 == 0 && wide(dout, s.dout_b, s.dout_l) && wide(x, s.x_b, s.x_l) && wide(dx, s.dx_b, s.dx_l);
-    void (*kern)(ConvBwdParams) = bf16 ? kernel_of<__nv_bfloat16>(vec, silu != 0) : kernel_of<float>(vec, silu != 0);
-    kern<<<dim3(static_cast<unsigned>(q.segs * q.nbd), static_cast<unsigned>(batch)), kThreads, 0, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return SS_ERR_CUDA;
+    p.err = device_error_word();
+    // TMA: rows and bases on 16-byte boundaries; a pair of outputs is one store
+    ConvBwdMaps m;
+    const int steps = 16 / static_cast<int>(es);
+    const bool tma = Dm % 2 == 0 && is_aligned(dx, 2 * es) && s.dx_l % 2 == 0 && (batch == 1 || s.dx_b % 2 == 0) &&
+                     make_tile_map(&m.x, x, bf16, Dm, L, batch, s.x_l, s.x_b, kBlockChannels, steps) &&
+                     make_tile_map(&m.dout, dout, bf16, Dm, L, batch, s.dout_l, s.dout_b, kBlockChannels, steps);
+    const dim3 grid(static_cast<unsigned>(q.segs * q.nbd), static_cast<unsigned>(batch));
+    const ConvBwdMaps* maps = tma ? &m : nullptr;
+    const cudaError_t k = bf16 ? (silu ? launch<__nv_bfloat16, true>(p, maps, grid, stream) : launch<__nv_bfloat16, false>(p, maps, grid, stream))
+                               : (silu ? launch<float, true>(p, maps, grid, stream) : launch<float, false>(p, maps, grid, stream));
+    if (k != cudaSuccess) return SS_ERR_CUDA;
     const cudaError_t e = launch_column_sum(p.part, static_cast<int>(batch * q.segs), p.ld, 5 * p.Dm, 4 * p.Dm, dweight, dbias, stream);
     return e == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
