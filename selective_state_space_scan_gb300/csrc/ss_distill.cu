@@ -3,9 +3,11 @@
 //   p = softmax_k(t / τ),  q = softmax_v(z / τ),  loss = Σ_k p_k (log p_k - log q_{ids_k})
 //   dz_v = dloss / τ · (q_v - Σ_{k: ids_k = v} p_k)
 //
-// The vocabulary is the traffic: a row is read once for the running maximum and sum, and, for the gradient, again
-// from L2 as soon as both are known, by the CTAs that have just read it (a cluster for a row where there are few
-// rows or where the rows at work would not stay in L2).  An entry's K values lie in shared memory; their
+// The vocabulary is the traffic, and it is read once: a row is shared out to the CTAs of a cluster so that each
+// keeps its slice (64 KB) in shared memory from the running maximum and sum to the gradient.  Bulk copies bring it,
+// three CTAs to an SM, so that an SM has some 190 KB under way or in use: a CTA's chain (entries, row, the cluster's
+// exchange, stores) is some 5 us long, and slices of 32 KB in registers left it at 0.44 of the copy rate.  (What
+// of a longer row does not fit is read again from L2.)  An entry's values lie in shared memory as well; their
 // columns get their gradient after the row's stream, rounded once, duplicates summed.
 #include <cuda_runtime.h>
 
@@ -22,10 +24,11 @@
 namespace selscan {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kHeld = 64 * 1024 + 512;             // bytes of a slice that a CTA holds at most
+constexpr int kParts = 4;                          // copies that they come in
 constexpr int kMaxK = SS_DISTILL_MAX_K;
-constexpr int kPer = kMaxK / kThreads;             // entries of a thread at most
 constexpr int kMaxCluster = 8;
 
 struct DistillParams {
@@ -37,18 +40,20 @@ struct DistillParams {
     void* dlogits;
     int64_t logits_r, ids_r, teacher_r, dlogits_r, dloss_r;
     int64_t rows;
-    int V, K, slice;                               // slice: columns of a CTA (a multiple of 8)
+    int V, K, slice, cap;                          // slice: columns of a CTA (a multiple of 8); cap: vectors it holds
     bool teacher_bf16;
     float inv_t;                                   // 1 / τ
     unsigned int* err;
 };
 
 struct DistillShared {
-    float p[kMaxK], z[kMaxK], t[kMaxK];
-    int32_t id[kMaxK];
-    float part[2][kWarps];
-    float2 stat[kWarps];
+    float t[kMaxK], z[kMaxK];                      // the entries' logits: teacher's, student's
+    int32_t id[kMaxK];                             // -1: not there
+    float4 stat[kWarps];
+    float part[kWarps];
     float2 mine;                                   // (max, sum) of this CTA's slice: read by the cluster's others
+    uint64_t full[kParts];
+    int abort;
 };
 
 template <typename T> struct Vec16;                // 16 bytes of a row
@@ -115,49 +120,28 @@ struct Running {
     }
 };
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
-}
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-// The sum (MAX: maximum) over the block in every thread; `slot` is this use's place in shared memory.
-template <bool MAX>
-__device__ __forceinline__ float block_all(float v, float* slot) {
-    v = MAX ? warp_max(v) : warp_sum(v);
-    if (threadIdx.x % 32 == 0) slot[threadIdx.x / 32] = v;
-    __syncthreads();
-    v = slot[threadIdx.x % kWarps];
-#pragma unroll
-    for (int o = kWarps / 2; o > 0; o /= 2) {
-        const float w = __shfl_xor_sync(0xffffffffu, v, o);
-        v = MAX ? fmaxf(v, w) : v + w;
-    }
-    return v;
-}
-
 template <typename T, bool GRAD>
 __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillParams p) {
-    constexpr int N = Vec16<T>::n, U = 4;
+    constexpr int N = Vec16<T>::n;
+    extern __shared__ __align__(128) uint4 held[];
     __shared__ DistillShared sh;
     uint32_t rank = 0, size = 1;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
     const int tid = threadIdx.x;
-    // the last rows first: in a row of calls these are what L2 still holds
-    const int64_t row = p.rows - 1 - blockIdx.x / size;
+    const int64_t row = blockIdx.x / size;
     const T* z = static_cast<const T*>(p.logits) + row * p.logits_r;
-    const int32_t* ids = p.ids + row * p.ids_r;
     const float c = kLog2e * p.inv_t;
 
+    if (tid == 0) {
+        for (int i = 0; i < kParts; ++i) mbar_init(&sh.full[i], 1);
+        sh.abort = 0;
+        mbar_fence_init();
+    }
     // the teacher's entries, in every CTA of the row
-    float mt = -INFINITY;
+    Running e;
     for (int k = tid; k < p.K; k += kThreads) {
-        const int id = ids[k];
+        const int id = p.ids[row * p.ids_r + k];
         const bool ok = id >= 0 && id < p.V;
         if (id >= p.V && rank == 0 && p.err) atomicOr(p.err, kErrIndex);
         float t = -INFINITY;
@@ -166,155 +150,154 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillParams p
                                : static_cast<const float*>(p.teacher)[row * p.teacher_r + k];
         sh.t[k] = t;
         sh.id[k] = ok ? id : -1;
-        sh.z[k] = ok ? to_f32<T>(z[id]) : 0.f;
-        mt = fmaxf(mt, t);
+        e.one(t, c);                               // (-inf and what is not there: no weight)
     }
-    mt = Running::base(block_all<true>(mt, sh.part[0]));
-    float pt = 0.f;
-    for (int k = tid; k < p.K; k += kThreads) {
-        const float e = ex2((sh.t[k] - mt) * c);   // (0 for an entry that is not there)
-        sh.p[k] = e;
-        pt += e;
-    }
-    pt = block_all<false>(pt, sh.part[1]);
-    const bool some = pt != 0.f;                   // (NaN: a row with a NaN)
-    const float inv_pt = some ? 1.f / pt : 0.f;
+    const bool some = __syncthreads_or(e.s != 0.f);        // (NaN: a row with a NaN)
 
     const int lo = static_cast<int>(rank) * p.slice, hi = min(lo + p.slice, p.V);
     // columns up to the first 16-byte boundary, whole vectors, and what is left
     const int head = min(hi, lo + static_cast<int>(((16 - reinterpret_cast<uintptr_t>(z + lo) % 16) % 16) / sizeof(T)));
     const int vecs = hi > head ? (hi - head) / N : 0, tail = head + vecs * N;
     const uint4* zv = reinterpret_cast<const uint4*>(z + head);
-
+    const int mine = min(vecs, p.cap), part = (mine + kParts - 1) / kParts;
+    bool ok = true;
     Running r;
     if (some) {
-        for (int i = tid; i < vecs; i += kThreads * U) {
-            uint4 u[U];
-#pragma unroll
-            for (int j = 0; j < U; ++j)
-                if (i + j * kThreads < vecs) u[j] = zv[i + j * kThreads];
-#pragma unroll
-            for (int j = 0; j < U; ++j) {
-                if (i + j * kThreads >= vecs) break;
+        if (tid == 0)
+            for (int i = 0; i < kParts && i * part < mine; ++i) {
+                const uint32_t bytes = static_cast<uint32_t>(min(part, mine - i * part)) * 16u;
+                mbar_expect_tx(&sh.full[i], bytes);
+                bulk_load(held + i * part, zv + i * part, bytes, &sh.full[i]);
+            }
+        for (int k = tid; k < p.K; k += kThreads) sh.z[k] = sh.id[k] >= 0 ? to_f32<T>(z[sh.id[k]]) : 0.f;
+        if (lo + tid < head) r.one(to_f32<T>(z[lo + tid]), c);
+        if (tail + tid < hi) r.one(to_f32<T>(z[tail + tid]), c);
+        for (int i = 0; i < kParts && i * part < mine; ++i) {
+            ok = mbar_wait_bounded(&sh.full[i], 0, &sh.abort, p.err) && ok;
+            const int end = min((i + 1) * part, mine);
+#pragma unroll 2
+            for (int k = i * part + tid; k < end; k += kThreads) {
                 float v[N];
-                Vec16<T>::get(u[j], v);
+                Vec16<T>::get(held[k], v);
                 r.take(v, c);
             }
         }
-        if (lo + tid < head) r.one(to_f32<T>(z[lo + tid]), c);
-        if (tail + tid < hi) r.one(to_f32<T>(z[tail + tid]), c);
+#pragma unroll 4
+        for (int k = mine + tid; k < vecs; k += kThreads) {
+            float v[N];
+            Vec16<T>::get(zv[k], v);
+            r.take(v, c);
+        }
 #pragma unroll
-        for (int o = 16; o > 0; o /= 2) r.join(__shfl_xor_sync(0xffffffffu, r.m, o), __shfl_xor_sync(0xffffffffu, r.s, o), c);
-        if (tid % 32 == 0) sh.stat[tid / 32] = make_float2(r.m, r.s);
-    }
-    __syncthreads();
-    if (some) {
-        const float2 q = sh.stat[tid % kWarps];
-        r.m = q.x;
-        r.s = q.y;
+        for (int o = 16; o > 0; o /= 2) {
+            r.join(__shfl_xor_sync(0xffffffffu, r.m, o), __shfl_xor_sync(0xffffffffu, r.s, o), c);
+            e.join(__shfl_xor_sync(0xffffffffu, e.m, o), __shfl_xor_sync(0xffffffffu, e.s, o), c);
+        }
+        if (tid % 32 == 0) sh.stat[tid / 32] = make_float4(r.m, r.s, e.m, e.s);
+        __syncthreads();
+        const float4 q = sh.stat[tid % kWarps];
+        r.m = q.x; r.s = q.y; e.m = q.z; e.s = q.w;
 #pragma unroll
-        for (int o = kWarps / 2; o > 0; o /= 2) r.join(__shfl_xor_sync(0xffffffffu, r.m, o), __shfl_xor_sync(0xffffffffu, r.s, o), c);
-        if (tid == 0) sh.mine = make_float2(r.m, r.s);
-    }
-    if (size > 1) {
-        cluster_sync_all();
-        if (some) {
+        for (int o = kWarps / 2; o > 0; o /= 2) {
+            r.join(__shfl_xor_sync(0xffffffffu, r.m, o), __shfl_xor_sync(0xffffffffu, r.s, o), c);
+            e.join(__shfl_xor_sync(0xffffffffu, e.m, o), __shfl_xor_sync(0xffffffffu, e.s, o), c);
+        }
+        if (size > 1) {                            // (a row's CTAs agree on whether it has any weight)
+            if (tid == 0) sh.mine = make_float2(r.m, r.s);
+            cluster_sync_all();
             Running all;
             for (uint32_t k = 0; k < size; ++k) {
                 const uint32_t a = peer_smem_addr(&sh.mine, k);
                 all.join(ld_peer_f32(a), ld_peer_f32(a + 4), c);
             }
             r = all;
+            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");            // (waited for at the end)
         }
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");    // (waited for at the end)
     }
     const float m = Running::base(r.m), inv_s = 1.f / r.s;
+    const float mt = Running::base(e.m), inv_pt = 1.f / e.s;
 
     if (rank == 0) {
         float sum = 0.f;
-        if (some)
+        if (some) {
             for (int k = tid; k < p.K; k += kThreads) {
-                const float w = sh.p[k] * inv_pt;
+                const float w = ex2((sh.t[k] - mt) * c) * inv_pt;
                 if (w != 0.f) sum += w * ((sh.t[k] - mt) - (sh.z[k] - m)) * p.inv_t;
             }
-        sum = block_all<false>(sum, sh.part[0]);
-        if (tid == 0) p.loss[row] = some ? sum + (logf(r.s) - logf(pt)) : 0.f;
+#pragma unroll
+            for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (tid % 32 == 0) sh.part[tid / 32] = sum;
+            __syncthreads();
+        }
+        if (tid == 0) {
+            sum = 0.f;
+            if (some) {
+                for (int i = 0; i < kWarps; ++i) sum += sh.part[i];
+                sum += logf(r.s) - logf(e.s);
+            }
+            p.loss[row] = sum;
+        }
     }
     if constexpr (GRAD) {
         T* d = static_cast<T*>(p.dlogits) + row * p.dlogits_r;
         const float g = some ? p.dloss[row * p.dloss_r] * p.inv_t : 0.f;
-        // the entries' own columns in this slice: the first of equal ones has them all
-        float val[kPer];
-        int col[kPer];
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const int k = tid + j * kThreads, id = k < p.K ? sh.id[k] : -1;
-            col[j] = -1;
-            if (!some || id < lo || id >= hi) continue;
-            float w = 0.f;
-            bool first = true;
-            for (int i = 0; i < p.K; ++i)
-                if (sh.id[i] == id) {
-                    first = first && i >= k;
-                    w += sh.p[i];
-                }
-            if (!first) continue;
-            col[j] = id;
-            val[j] = g * (ex2((sh.z[k] - m) * c) * inv_s - w * inv_pt);
-        }
         const float gs = g * inv_s;
         const float2 off = splat2(-m), c2 = splat2(c), gs2 = splat2(gs);
         auto grad = [&](float v) { return some ? ex2((v - m) * c) * gs : 0.f; };
         // (a row of dlogits that lies otherwise against the 16 bytes is written element by element)
         const bool same = reinterpret_cast<uintptr_t>(d + head) % 16 == 0;
-        for (int i = tid; i < vecs; i += kThreads * U) {
-            uint4 u[U];
+        const T first_z = some && lo + tid < head ? z[lo + tid] : from_f32<T>(0.f), last_z = some && tail + tid < hi ? z[tail + tid] : from_f32<T>(0.f);
+#pragma unroll 4
+        for (int k = tid; k < vecs; k += kThreads) {
+            float v[N];
 #pragma unroll
-            for (int j = 0; j < U; ++j)
-                if (i + j * kThreads < vecs && some) u[j] = __ldcs(zv + i + j * kThreads);
+            for (int i = 0; i < N; ++i) v[i] = 0.f;
+            if (some) {
+                Vec16<T>::get(k < mine ? held[k] : __ldcs(zv + k), v);
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
-                const int at = i + j * kThreads;
-                if (at >= vecs) break;
-                float v[N];
-                if (some) {
-                    Vec16<T>::get(u[j], v);
-#pragma unroll
-                    for (int e = 0; e < N; e += 2) {
-                        const float2 o = mul2(ex2x2(mul2(add2(make_float2(v[e], v[e + 1]), off), c2)), gs2);
-                        v[e] = o.x;
-                        v[e + 1] = o.y;
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < N; ++e) v[e] = 0.f;
-                }
-                if (same) {
-                    __stcs(reinterpret_cast<uint4*>(d + head) + at, Vec16<T>::put(v));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < N; ++e) d[head + at * N + e] = from_f32<T>(v[e]);
+                for (int i = 0; i < N; i += 2) {
+                    const float2 o = mul2(ex2x2(mul2(add2(make_float2(v[i], v[i + 1]), off), c2)), gs2);
+                    v[i] = o.x;
+                    v[i + 1] = o.y;
                 }
             }
-        }
-        if (lo + tid < head) d[lo + tid] = from_f32<T>(grad(some ? to_f32<T>(z[lo + tid]) : 0.f));
-        if (tail + tid < hi) d[tail + tid] = from_f32<T>(grad(some ? to_f32<T>(z[tail + tid]) : 0.f));
-        __syncthreads();
+            if (same) {
+                __stcs(reinterpret_cast<uint4*>(d + head) + k, Vec16<T>::put(v));
+            } else {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j)
-            if (col[j] >= 0) d[col[j]] = from_f32<T>(val[j]);
+                for (int i = 0; i < N; ++i) d[head + k * N + i] = from_f32<T>(v[i]);
+            }
+        }
+        if (lo + tid < head) d[lo + tid] = from_f32<T>(grad(to_f32<T>(first_z)));
+        if (tail + tid < hi) d[tail + tid] = from_f32<T>(grad(to_f32<T>(last_z)));
+        if (some) {
+            // the entries' own columns in this slice, after all others: the first of equal ones has them all
+            __syncthreads();
+            for (int k = tid; k < p.K; k += kThreads) {
+                const int id = sh.id[k];
+                if (id < lo || id >= hi) continue;
+                float w = 0.f;
+                bool first = true;
+                for (int i = 0; i < p.K; ++i)
+                    if (sh.id[i] == id) {
+                        first = first && i >= k;
+                        w += ex2((sh.t[i] - mt) * c);
+                    }
+                if (first) d[id] = from_f32<T>(g * (ex2((sh.z[k] - m) * c) * inv_s - w * inv_pt));
+            }
+        }
     }
-    if (size > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (!ok)                                       // a wait that ran out: copies in flight are over long before this
+        for (int i = 0; i < 20; ++i) __nanosleep(1000000);
+    if (some && size > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// CTAs for a row.  Enough to fill the SMs where rows are few, as long as each keeps some 16 KB; for the
-// gradient also enough that the rows at work (4 CTAs to an SM) stay in half of L2.
-constexpr int64_t kL2Rows = 64 << 20;
-int cluster_of(int64_t rows, int64_t row_bytes, int sms, bool grad) {
+// CTAs for a row: so many that each holds its slice, and more where rows are few, as long as each keeps some 8 KB.
+int cluster_of(int64_t rows, int64_t row_bytes, int sms) {
     int n = 1;
-    while (n < kMaxCluster && rows * n < 3 * static_cast<int64_t>(sms) && row_bytes / (2 * n) >= 16384) n *= 2;
-    if (grad)
-        while (n < kMaxCluster && 4 * static_cast<int64_t>(sms) / n * row_bytes > kL2Rows) n *= 2;
+    while (n < kMaxCluster && (row_bytes > n * static_cast<int64_t>(kHeld) ||
+                               (rows * n < 2 * static_cast<int64_t>(sms) && row_bytes / (2 * n) >= 8192)))
+        n *= 2;
     return n;
 }
 
@@ -329,7 +312,11 @@ cudaError_t launch(const DistillParams& p, int cluster, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.rows * cluster));
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(p.cap) * 16;
     cfg.stream = stream;
+    // (cheap, and the same from every thread that calls)
+    const cudaError_t e = cudaFuncSetAttribute(distill_kernel<T, GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeld);
+    if (e != cudaSuccess) return e;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = static_cast<unsigned>(cluster);
@@ -381,8 +368,9 @@ ss_status distill(const float* dloss, const void* logits, const int32_t* ids, co
     p.teacher_bf16 = s.teacher_dtype == SS_BF16;
     p.inv_t = 1.f / temperature;
     p.err = device_error_word();
-    const int cluster = cluster_of(rows, V * es, sms, grad);
+    const int cluster = cluster_of(rows, V * es, sms);
     p.slice = static_cast<int>(((V + cluster - 1) / cluster + 7) / 8 * 8);
+    p.cap = static_cast<int>(std::min<int64_t>(p.slice * es, kHeld) / 16);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool b = s.io_dtype == SS_BF16;
     const cudaError_t e = grad ? (b ? launch<__nv_bfloat16, true>(p, cluster, st) : launch<float, true>(p, cluster, st))
