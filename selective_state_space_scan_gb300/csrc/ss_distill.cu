@@ -27,7 +27,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kHeld = 64 * 1024 + 512;             // bytes of a slice that a CTA holds at most
-constexpr int kParts = 4;                          // copies that they come in
+constexpr int kBatch = 4;                          // vectors that a thread works on at a time
 constexpr int kMaxK = SS_DISTILL_MAX_K;
 constexpr int kMaxCluster = 8;
 
@@ -47,18 +47,26 @@ struct DistillParams {
 };
 
 struct DistillShared {
-    float t[kMaxK], z[kMaxK];                      // the entries' logits: teacher's, student's
-    int32_t id[kMaxK];                             // -1: not there
-    float4 stat[kWarps];
+    int4 id[kMaxK / 4];                            // the entries' columns, -1: not there
+    float t[kMaxK], z[kMaxK];                      // their logits: teacher's, student's
+    float2 stat[kWarps], entry[kWarps];
     float part[kWarps];
     float2 mine;                                   // (max, sum) of this CTA's slice: read by the cluster's others
-    uint64_t full[kParts];
+    uint64_t full;
     int abort;
 };
 
 template <typename T> struct Vec16;                // 16 bytes of a row
 template <> struct Vec16<float> {
     static constexpr int n = 4;
+    // The largest value (of a NaN and a number the number).
+    template <int B> static __device__ __forceinline__ float max(const uint4 (&u)[B]) {
+        float b = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < B; ++k)
+            b = fmaxf(b, fmaxf(fmaxf(__uint_as_float(u[k].x), __uint_as_float(u[k].y)), fmaxf(__uint_as_float(u[k].z), __uint_as_float(u[k].w))));
+        return b;
+    }
     static __device__ __forceinline__ void get(const uint4& u, float (&v)[4]) {
         v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y); v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
     }
@@ -68,6 +76,13 @@ template <> struct Vec16<float> {
 };
 template <> struct Vec16<__nv_bfloat16> {
     static constexpr int n = 8;
+    template <int B> static __device__ __forceinline__ float max(const uint4 (&u)[B]) {
+        auto h = [](uint32_t v) { return *reinterpret_cast<const __nv_bfloat162*>(&v); };
+        __nv_bfloat162 b = h(u[0].x);
+#pragma unroll
+        for (int k = 0; k < B; ++k) b = __hmax2(b, __hmax2(__hmax2(h(u[k].x), h(u[k].y)), __hmax2(h(u[k].z), h(u[k].w))));
+        return fmaxf(__low2float(b), __high2float(b));
+    }
     static __device__ __forceinline__ void get(const uint4& u, float (&v)[8]) {
         const uint32_t a[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -92,18 +107,27 @@ struct Running {
     float m = -INFINITY, s = 0.f;
     // (-inf as the maximum so far: nothing but -inf seen, whose weights are zero)
     static __device__ __forceinline__ float base(float m) { return m == -INFINITY ? 0.f : m; }
-    template <int N> __device__ __forceinline__ void take(const float (&v)[N], float c) {
-        float b = v[0];
-#pragma unroll
-        for (int i = 1; i < N; ++i) b = fmaxf(b, v[i]);
+    // n vectors (of the type T, what is behind them is not read)
+    template <typename T, int B> __device__ __forceinline__ void take(const uint4 (&u)[B], float c) {
+        constexpr int N = Vec16<T>::n;
+        const float b = Vec16<T>::max(u);
         if (b > m) {
             s *= ex2((m - b) * c);
             m = b;
         }
         const float2 off = splat2(-base(m)), c2 = splat2(c);
-        float2 a = splat2(0.f);
+        float2 a = splat2(0.f), a2 = a;
 #pragma unroll
-        for (int i = 0; i < N; i += 2) a = add2(a, ex2x2(mul2(add2(make_float2(v[i], v[i + 1]), off), c2)));
+        for (int k = 0; k < B; ++k) {
+            float v[N];
+            Vec16<T>::get(u[k], v);
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                a = add2(a, ex2x2(mul2(add2(make_float2(v[i], v[i + 1]), off), c2)));
+                a2 = add2(a2, ex2x2(mul2(add2(make_float2(v[i + 2], v[i + 3]), off), c2)));
+            }
+        }
+        a = add2(a, a2);
         s += a.x + a.y;
     }
     __device__ __forceinline__ void one(float v, float c) {
@@ -117,6 +141,16 @@ struct Running {
         const float n = fmaxf(m, m2), b = base(n);
         s = s * ex2((m - b) * c) + s2 * ex2((m2 - b) * c);
         m = n;
+    }
+    // Over groups of LANES lanes.
+    template <int LANES> __device__ __forceinline__ void join_lanes(float c) {
+        float n = m;
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o /= 2) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, o));
+        s *= ex2((m - base(n)) * c);
+        m = n;
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
     }
 };
 
@@ -134,12 +168,15 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillParams p
     const float c = kLog2e * p.inv_t;
 
     if (tid == 0) {
-        for (int i = 0; i < kParts; ++i) mbar_init(&sh.full[i], 1);
+        mbar_init(&sh.full, 1);
         sh.abort = 0;
         mbar_fence_init();
     }
     // the teacher's entries, in every CTA of the row
     Running e;
+    int32_t* sid = reinterpret_cast<int32_t*>(sh.id);
+    if (tid < 4 && p.K % 4 != 0) sid[p.K / 4 * 4 + tid] = -1;           // behind the last
+    __syncthreads();
     for (int k = tid; k < p.K; k += kThreads) {
         const int id = p.ids[row * p.ids_r + k];
         const bool ok = id >= 0 && id < p.V;
@@ -149,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillParams p
             t = p.teacher_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.teacher)[row * p.teacher_r + k])
                                : static_cast<const float*>(p.teacher)[row * p.teacher_r + k];
         sh.t[k] = t;
-        sh.id[k] = ok ? id : -1;
+        sid[k] = ok ? id : -1;
         e.one(t, c);                               // (-inf and what is not there: no weight)
     }
     const bool some = __syncthreads_or(e.s != 0.f);        // (NaN: a row with a NaN)
@@ -159,49 +196,46 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillParams p
     const int head = min(hi, lo + static_cast<int>(((16 - reinterpret_cast<uintptr_t>(z + lo) % 16) % 16) / sizeof(T)));
     const int vecs = hi > head ? (hi - head) / N : 0, tail = head + vecs * N;
     const uint4* zv = reinterpret_cast<const uint4*>(z + head);
-    const int mine = min(vecs, p.cap), part = (mine + kParts - 1) / kParts;
+    const int mine = min(vecs, p.cap);
     bool ok = true;
     Running r;
     if (some) {
-        if (tid == 0)
-            for (int i = 0; i < kParts && i * part < mine; ++i) {
-                const uint32_t bytes = static_cast<uint32_t>(min(part, mine - i * part)) * 16u;
-                mbar_expect_tx(&sh.full[i], bytes);
-                bulk_load(held + i * part, zv + i * part, bytes, &sh.full[i]);
-            }
-        for (int k = tid; k < p.K; k += kThreads) sh.z[k] = sh.id[k] >= 0 ? to_f32<T>(z[sh.id[k]]) : 0.f;
+        if (tid == 0 && mine > 0) {
+            mbar_expect_tx(&sh.full, static_cast<uint32_t>(mine) * 16u);
+            bulk_load(held, zv, static_cast<uint32_t>(mine) * 16u, &sh.full);
+        }
+        for (int k = tid; k < p.K; k += kThreads) sh.z[k] = sid[k] >= 0 ? to_f32<T>(z[sid[k]]) : 0.f;
+        if (tid / 32 * 32 < p.K) {                 // (a warp that has entries)
+            e.join_lanes<32>(c);
+            if (tid % 32 == 0) sh.entry[tid / 32] = make_float2(e.m, e.s);
+        }
         if (lo + tid < head) r.one(to_f32<T>(z[lo + tid]), c);
         if (tail + tid < hi) r.one(to_f32<T>(z[tail + tid]), c);
-        for (int i = 0; i < kParts && i * part < mine; ++i) {
-            ok = mbar_wait_bounded(&sh.full[i], 0, &sh.abort, p.err) && ok;
-            const int end = min((i + 1) * part, mine);
-#pragma unroll 2
-            for (int k = i * part + tid; k < end; k += kThreads) {
-                float v[N];
-                Vec16<T>::get(held[k], v);
-                r.take(v, c);
-            }
+        if (mine > 0) ok = mbar_wait_bounded(&sh.full, 0, &sh.abort, p.err);
+        constexpr int kAll = kBatch * kThreads;
+        int k = tid;
+        for (; k + kAll - kThreads < mine; k += kAll) {
+            uint4 u[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) u[j] = held[k + j * kThreads];
+            r.take<T>(u, c);
+        }
+        for (; k < mine; k += kThreads) {
+            const uint4 u[1] = {held[k]};
+            r.take<T>(u, c);
         }
 #pragma unroll 4
-        for (int k = mine + tid; k < vecs; k += kThreads) {
-            float v[N];
-            Vec16<T>::get(zv[k], v);
-            r.take(v, c);
+        for (k = mine + tid; k < vecs; k += kThreads) {
+            const uint4 u[1] = {zv[k]};
+            r.take<T>(u, c);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o /= 2) {
-            r.join(__shfl_xor_sync(0xffffffffu, r.m, o), __shfl_xor_sync(0xffffffffu, r.s, o), c);
-            e.join(__shfl_xor_sync(0xffffffffu, e.m, o), __shfl_xor_sync(0xffffffffu, e.s, o), c);
-        }
-        if (tid % 32 == 0) sh.stat[tid / 32] = make_float4(r.m, r.s, e.m, e.s);
+        r.join_lanes<32>(c);
+        if (tid % 32 == 0) sh.stat[tid / 32] = make_float2(r.m, r.s);
         __syncthreads();
-        const float4 q = sh.stat[tid % kWarps];
-        r.m = q.x; r.s = q.y; e.m = q.z; e.s = q.w;
-#pragma unroll
-        for (int o = kWarps / 2; o > 0; o /= 2) {
-            r.join(__shfl_xor_sync(0xffffffffu, r.m, o), __shfl_xor_sync(0xffffffffu, r.s, o), c);
-            e.join(__shfl_xor_sync(0xffffffffu, e.m, o), __shfl_xor_sync(0xffffffffu, e.s, o), c);
-        }
+        const float2 q = sh.stat[tid % kWarps], qe = tid % kWarps * 32 < p.K ? sh.entry[tid % kWarps] : make_float2(-INFINITY, 0.f);
+        r.m = q.x; r.s = q.y; e.m = qe.x; e.s = qe.y;
+        r.join_lanes<kWarps>(c);
+        e.join_lanes<kWarps>(c);
         if (size > 1) {                            // (a row's CTAs agree on whether it has any weight)
             if (tid == 0) sh.mine = make_float2(r.m, r.s);
             cluster_sync_all();
@@ -274,15 +308,21 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillParams p
             // the entries' own columns in this slice, after all others: the first of equal ones has them all
             __syncthreads();
             for (int k = tid; k < p.K; k += kThreads) {
-                const int id = sh.id[k];
+                const int id = sid[k];
                 if (id < lo || id >= hi) continue;
                 float w = 0.f;
                 bool first = true;
-                for (int i = 0; i < p.K; ++i)
-                    if (sh.id[i] == id) {
-                        first = first && i >= k;
-                        w += ex2((sh.t[i] - mt) * c);
-                    }
+                for (int i = 0; i < p.K; i += 4) {
+                    const int4 o = sh.id[i / 4];
+                    if (o.x != id && o.y != id && o.z != id && o.w != id) continue;
+                    const int at[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (at[j] == id) {
+                            first = first && i + j >= k;
+                            w += ex2((sh.t[i + j] - mt) * c);
+                        }
+                }
                 if (first) d[id] = from_f32<T>(g * (ex2((sh.z[k] - m) * c) * inv_s - w * inv_pt));
             }
         }
