@@ -3,6 +3,8 @@
 // shared memory.
 #include "column_sum.h"
 
+#include "chained.cuh"
+
 namespace selscan {
 namespace {
 
@@ -11,6 +13,7 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restric
     __shared__ float s[32][33];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, j = blockIdx.x * 32 + lane;
     float v = 0.f;
+    wait_for_earlier();
     if (j < cols) {
 #pragma unroll 4
         for (int i = warp; i < n; i += 32) v += part[i * ld + j];
@@ -30,8 +33,7 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restric
 }  // namespace
 
 cudaError_t launch_column_sum(const float* part, int n, int64_t ld, int cols, int split, float* out0, float* out1, cudaStream_t stream) {
-    column_sum_kernel<<<static_cast<unsigned>((cols + 31) / 32), 1024, 0, stream>>>(part, n, ld, cols, split, out0, out1);
-    return cudaGetLastError();
+    return launch_chained(column_sum_kernel, dim3(static_cast<unsigned>((cols + 31) / 32)), dim3(1024), 0, stream, part, n, ld, cols, split, out0, out1);
 }
 
 }  // namespace selscan

@@ -17,6 +17,7 @@
 #include <cstring>
 
 #include "../../include/selscan.h"
+#include "chained.cuh"
 #include "column_sum.h"
 #include "device_common.cuh"
 #include "host_util.h"
@@ -209,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) ss_conv1d_bwd_kernel(c
         }
         if (tid == 0 && i + kStages < n) issue(i + kStages);
     }
+    let_next_start();
     c.leave(p, q);
 }
 
@@ -216,7 +218,7 @@ template <typename T, bool SILU>
 __global__ void __launch_bounds__(kThreads) ss_conv1d_bwd_plain_kernel(const ConvBwdParams p) {
     constexpr int U = 4;                           // steps whose loads are issued together
     const Place q = place_of(p, false);
-    if (!q.one) return;
+    if (!q.one) return;                            // (an ended thread lets the next kernel start as well)
     Pair<T, SILU> c;
     c.start(p, q);
     const T* x = static_cast<const T*>(p.x) + q.b * p.x_b + q.t0 * p.x_l + q.d0;
@@ -246,6 +248,7 @@ __global__ void __launch_bounds__(kThreads) ss_conv1d_bwd_plain_kernel(const Con
             }
         }
     }
+    let_next_start();
     c.leave(p, q);
 }
 

@@ -16,6 +16,7 @@
 #include <cstring>
 
 #include "../../include/selscan.h"
+#include "chained.cuh"
 #include "column_sum.h"
 #include "device_common.cuh"
 #include "host_util.h"
@@ -256,6 +257,7 @@ __global__ void __launch_bounds__(512) layernorm_bwd_kernel(const LnParams p) {
             if (dres) store_cols<TR, VEC>(dres, c, k, a[k]);
         }
     }
+    let_next_start();
     float* mine = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.D;
 #pragma unroll
     for (int k = 0; k < K; ++k)

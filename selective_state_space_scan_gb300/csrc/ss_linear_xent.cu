@@ -30,6 +30,7 @@
 #include <type_traits>
 
 #include "../../include/selscan.h"
+#include "chained.cuh"
 #include "heads_device.cuh"
 #include "host_util.h"
 #include "internal.h"
@@ -237,6 +238,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
     tc_fence_after();
     cluster_sync_all();                            // the peer's barriers exist
     const uint32_t tmem = sh.tmem;
+    wait_for_earlier();
     const int rows = *p.count;
     const Work work = make_work<P>(p, rows, clusters);
     int ex = 0, ew = 0, eg = 0;
@@ -603,6 +605,8 @@ __global__ void __launch_bounds__(kPrepThreads) xent_gather_kernel(const PrepPar
     constexpr bool F32 = sizeof(T) == 4, RAW = !F32 && !BWD;
     constexpr int kWarps = kPrepThreads / 32;
     __shared__ int before[kWarps], own[kWarps], to[kPrepThreads];
+    let_next_start();
+    if constexpr (!RAW) wait_for_earlier();        // (else it is the call's first)
     const float scale = RAW ? 1.f : pow2(-scale_exp(p.range[kRangeX]));
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * p.per;
@@ -671,6 +675,8 @@ template <typename T, bool RAW>
 __global__ void __launch_bounds__(kPrepThreads) xent_pack_kernel(const T* w, int64_t stride, __half* out, int64_t ld, int64_t part, int64_t n, int D,
                                                                  bool wide, const unsigned int* range) {
     const int vecs = static_cast<int>(ld / 8);
+    let_next_start();
+    wait_for_earlier();
     const float scale = RAW ? 1.f : pow2(-scale_exp(range[kRangeW]));
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPrepThreads + threadIdx.x; i < n * vecs; i += static_cast<int64_t>(gridDim.x) * kPrepThreads) {
         const int64_t r = i / vecs;
@@ -682,8 +688,9 @@ __global__ void __launch_bounds__(kPrepThreads) xent_pack_kernel(const T* w, int
 constexpr int kJoinThreads = 1024;
 __global__ void __launch_bounds__(kJoinThreads) xent_join_kernel(const float2* part, int64_t ld, int halves, const int* count, const int* rows,
                                                                  const float* tl, float* loss, float* lse) {
-    constexpr int kWarps = kJoinThreads / 32, U = 8;
+    constexpr int kWarps = kJoinThreads / 32, U = 16;
     __shared__ float2 s[kWarps][33];
+    wait_for_earlier();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, n = *count;
     const int row = blockIdx.x * 32 + lane;
     float m = -INFINITY, sum = 0.f;
@@ -722,6 +729,7 @@ __global__ void __launch_bounds__(kJoinThreads) xent_join_kernel(const float2* p
 template <typename T>
 __global__ void __launch_bounds__(kPrepThreads) xent_scatter_kernel(const float* dx, int64_t split_stride, int splits, int64_t ld, const int* count,
                                                                     const int* rows, T* dhidden, int64_t stride, int D) {
+    wait_for_earlier();
     const int n = *count;
     for (int i = blockIdx.x; i < n; i += gridDim.x) {
         T* out = dhidden + static_cast<int64_t>(rows[i]) * stride;
@@ -894,8 +902,7 @@ cudaError_t launch_gemm_as(const XentParams& p, int64_t units, cudaStream_t stre
         if (dev < 64) known[dev].store(pairs);
     }
     const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(pairs, std::max<int64_t>(units, 1)));
-    kern<<<grid, kGemmThreads, kGemmSmem, stream>>>(p);
-    return cudaGetLastError();
+    return launch_chained(kern, dim3(grid), dim3(kGemmThreads), kGemmSmem, stream, p);
 }
 template <Product P>
 cudaError_t launch_gemm(const XentParams& p, bool f32, int64_t units, cudaStream_t stream) {
@@ -1010,8 +1017,10 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
     }
     void (*gather)(PrepParams) = f32 ? (c.bwd ? xent_gather_kernel<float, true> : xent_gather_kernel<float, false>)
                                      : (c.bwd ? xent_gather_kernel<__nv_bfloat16, true> : xent_gather_kernel<__nv_bfloat16, false>);
-    gather<<<static_cast<unsigned>((T + g.per - 1) / g.per), kPrepThreads, 0, st>>>(g);
-    if (cudaGetLastError() != cudaSuccess) return SS_ERR_CUDA;
+    const dim3 gather_grid(static_cast<unsigned>((T + g.per - 1) / g.per)), prep(kPrepThreads);
+    if (raw) gather<<<gather_grid, prep, 0, st>>>(g);
+    const cudaError_t ge = raw ? cudaGetLastError() : launch_chained(gather, gather_grid, prep, 0, st, g);
+    if (ge != cudaSuccess) return SS_ERR_CUDA;
 
     XentParams p;
     std::memset(&p, 0, sizeof(p));
@@ -1029,14 +1038,13 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
             const unsigned grid = static_cast<unsigned>(std::min<int64_t>((Vp * q.ld_x / 8 + kPrepThreads - 1) / kPrepThreads, 16 * sm_count()));
             const bool ww = wide(wp, s.weight_v);
             const __nv_bfloat16* wb = static_cast<const __nv_bfloat16*>(wp);
-            if (f32)
-                xent_pack_kernel<float, false><<<grid, kPrepThreads, 0, st>>>(static_cast<const float*>(wp), s.weight_v, w, q.ld_x, w_part, Vp, p.D, ww,
-                                                                              g.range);
-            else if (raw)
-                xent_pack_kernel<__nv_bfloat16, true><<<grid, kPrepThreads, 0, st>>>(wb, s.weight_v, w, q.ld_x, w_part, Vp, p.D, ww, g.range);
-            else
-                xent_pack_kernel<__nv_bfloat16, false><<<grid, kPrepThreads, 0, st>>>(wb, s.weight_v, w, q.ld_x, w_part, Vp, p.D, ww, g.range);
-            if (cudaGetLastError() != cudaSuccess) return SS_ERR_CUDA;
+            auto pack = [&](auto* kern, auto* from) {
+                return launch_chained(kern, dim3(grid), prep, 0, st, from, s.weight_v, w, q.ld_x, w_part, Vp, p.D, ww, g.range);
+            };
+            const cudaError_t e = f32   ? pack(xent_pack_kernel<float, false>, static_cast<const float*>(wp))
+                                  : raw ? pack(xent_pack_kernel<__nv_bfloat16, true>, wb)
+                                        : pack(xent_pack_kernel<__nv_bfloat16, false>, wb);
+            if (e != cudaSuccess) return SS_ERR_CUDA;
             wp = w;
             ld_w = q.ld_x;
         }
@@ -1062,19 +1070,18 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
         p.add = v0 > 0;
         if (launch_gemm<Product::kOut>(p, f32, vt * dt + mt * dt * q.splits, st) != cudaSuccess) return SS_ERR_CUDA;
     }
-    if (!c.bwd) {
-        xent_join_kernel<<<static_cast<unsigned>((T + 31) / 32), kJoinThreads, 0, st>>>(p.part, q.tpad, static_cast<int>(q.halves), g.count, g.rows, p.tl,
-                                                                                     c.loss, c.lse);
-    } else {
-        const unsigned grid = static_cast<unsigned>(std::min<int64_t>(T, 8 * sm_count()));
-        if (f32)
-            xent_scatter_kernel<float><<<grid, kPrepThreads, 0, st>>>(p.dx, p.dx_split, p.splits, p.ld_dx, g.count, g.rows, static_cast<float*>(c.dhidden),
-                                                                      s.dhidden_t, p.D);
-        else
-            xent_scatter_kernel<__nv_bfloat16><<<grid, kPrepThreads, 0, st>>>(p.dx, p.dx_split, p.splits, p.ld_dx, g.count, g.rows,
-                                                                              static_cast<__nv_bfloat16*>(c.dhidden), s.dhidden_t, p.D);
-    }
-    return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+    const unsigned rows_grid = static_cast<unsigned>(std::min<int64_t>(T, 8 * sm_count()));
+    cudaError_t e;
+    if (!c.bwd)
+        e = launch_chained(xent_join_kernel, dim3(static_cast<unsigned>((T + 31) / 32)), dim3(kJoinThreads), 0, st, p.part, q.tpad,
+                           static_cast<int>(q.halves), g.count, g.rows, p.tl, c.loss, c.lse);
+    else if (f32)
+        e = launch_chained(xent_scatter_kernel<float>, dim3(rows_grid), prep, 0, st, p.dx, p.dx_split, p.splits, p.ld_dx, g.count, g.rows,
+                           static_cast<float*>(c.dhidden), s.dhidden_t, p.D);
+    else
+        e = launch_chained(xent_scatter_kernel<__nv_bfloat16>, dim3(rows_grid), prep, 0, st, p.dx, p.dx_split, p.splits, p.ld_dx, g.count, g.rows,
+                           static_cast<__nv_bfloat16*>(c.dhidden), s.dhidden_t, p.D);
+    return e == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
 }  // namespace

@@ -16,19 +16,14 @@ from .serving import _cuda, _empty, _io, _load, _norm_args, _param, _rows, _stre
 _WS_BYTES = {}
 
 
-def _scratch(t, stream, nbytes):
-    """Workspace of one call (its memory may be handed on as soon as the call's work is on the stream)."""
-    import torch
-    return _empty((max(nbytes, 1),), torch.uint8, t.device, stream)
-
-
-def _ws_bytes(call, device, *sizes):
-    """Workspace bytes of a call of these sizes, asked for once (the plan depends on the device's SM count)."""
-    key = (call, device, sizes)
+def _scratch(t, stream, call, *sizes):
+    """Workspace of one call (its memory may be handed on as soon as the call's work is on the stream).  Its bytes are
+    asked for once for every device and sizes (the plan depends on the device's SM count)."""
+    key = (call, t.get_device(), sizes)
     n = _WS_BYTES.get(key)
     if n is None:
-        n = _ss._remember(_WS_BYTES, key, int(getattr(_ss.lib(), call)(*sizes)))
-    return n
+        n = _ss._remember(_WS_BYTES, key, max(1, int(getattr(_ss.lib(), call)(*sizes))))
+    return _empty((n,), _load().uint8, t.device, stream), n
 
 
 def ss_add_layernorm(x, weight, bias=None, residual=None, eps=1e-5, y=None, residual_out=None, stream=None):
@@ -52,7 +47,7 @@ def ss_add_layernorm(x, weight, bias=None, residual=None, eps=1e-5, y=None, resi
         rows, D, out, y, s = _norm_args(x, weight, residual, residual_out, y, None, stream)
         r = out
     _param(bias, "bias", torch.float32, (D,))
-    mean, rstd = _empty((2, rows), torch.float32, x.device, stream).unbind()
+    mean, rstd = _empty((rows,), torch.float32, x.device, stream), _empty((rows,), torch.float32, x.device, stream)
     st = _ss.lib().ss_add_layernorm(x.data_ptr(), _ss._ptr(residual), weight.data_ptr(), _ss._ptr(bias), _ss._ptr(out), y.data_ptr(),
                                     mean.data_ptr(), rstd.data_ptr(), rows, D, eps, ctypes.byref(s), _stream(x, stream))
     if st != 0:
@@ -77,11 +72,11 @@ def ss_add_layernorm_bwd(dy, r, weight, mean, rstd, dr=None, stream=None):
     dev = dy.device
     dx = _empty(shape, io, dev, stream)
     dres = dx if rdt is io else _empty(shape, rdt, dev, stream)
-    dweight, dbias = _empty((2, D), f32, dev, stream).unbind()
-    ws = _scratch(dy, stream, _ws_bytes("ss_add_layernorm_bwd_workspace_size", dy.get_device(), rows, D))
+    dweight, dbias = _empty((D,), f32, dev, stream), _empty((D,), f32, dev, stream)
+    ws, nbytes = _scratch(dy, stream, "ss_add_layernorm_bwd_workspace_size", rows, D)
     st = _ss.lib().ss_add_layernorm_bwd(dy.data_ptr(), _ss._ptr(dr), r.data_ptr(), weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
                                         dx.data_ptr(), None if dres is dx else dres.data_ptr(), dweight.data_ptr(), dbias.data_ptr(),
-                                        rows, D, ctypes.byref(s), ws.data_ptr(), ws.numel(), _stream(dy, stream))
+                                        rows, D, ctypes.byref(s), ws.data_ptr(), nbytes, _stream(dy, stream))
     if st != 0:
         raise _ss.SelscanError(st, "ss_add_layernorm_bwd")
     return dict(dx=dx, dresidual=dres, dweight=dweight, dbias=dbias)
@@ -118,11 +113,11 @@ def ss_conv1d_bwd(dout, x, weight, bias=None, window_in=None, dwindow_out=None, 
     _param(dwindow_out, "dwindow_out", f32, (batch, Dm, 3))
     dweight, dbias = _empty((Dm, 4), f32, dev, stream), _empty((Dm,), f32, dev, stream)
     dwin = None if window_in is None else _empty((batch, Dm, 3), f32, dev, stream)
-    ws = _scratch(x, stream, _ws_bytes("ss_conv1d_bwd_workspace_size", x.get_device(), batch, L, Dm))
+    ws, nbytes = _scratch(x, stream, "ss_conv1d_bwd_workspace_size", batch, L, Dm)
     p = _ss._ptr
     st = _ss.lib().ss_conv1d_bwd(dout.data_ptr(), x.data_ptr(), weight.data_ptr(), p(bias), p(window_in), p(dwindow_out), dx.data_ptr(),
                                  dweight.data_ptr(), dbias.data_ptr(), p(dwin), batch, L, Dm, int(bool(silu)), ctypes.byref(s),
-                                 ws.data_ptr(), ws.numel(), _stream(x, stream))
+                                 ws.data_ptr(), nbytes, _stream(x, stream))
     if st != 0:
         raise _ss.SelscanError(st, "ss_conv1d_bwd")
     return dict(dx=dx, dweight=dweight, dbias=dbias, dwindow_in=dwin)
@@ -188,10 +183,6 @@ def _xent_args(hidden, weight, targets):
     return T, V, D, s
 
 
-def _xent_scratch(hidden, stream, T, V, D, s, backward):
-    return _scratch(hidden, stream, _ws_bytes("ss_linear_xent_workspace_size", hidden.get_device(), T, V, D, s.io_dtype, backward))
-
-
 def ss_linear_xent(hidden, weight, targets, stream=None):
     """Softmax cross entropy over the vocabulary from the last layer's rows (ss_linear_xent): the logits
     hidden @ weight.T are not kept.
@@ -200,10 +191,11 @@ def ss_linear_xent(hidden, weight, targets, stream=None):
     row without one.  Returns (loss, lse), both [tokens] float32 and zero in rows without a target; lse is for
     ss_linear_xent_bwd."""
     T, V, D, s = _xent_args(hidden, weight, targets)
-    loss, lse = _empty((2, T), _load().float32, hidden.device, stream).unbind()
-    ws = _xent_scratch(hidden, stream, T, V, D, s, 0)
+    f32, dev = _load().float32, hidden.device
+    loss, lse = _empty((T,), f32, dev, stream), _empty((T,), f32, dev, stream)
+    ws, nbytes = _scratch(hidden, stream, "ss_linear_xent_workspace_size", T, V, D, s.io_dtype, 0)
     st = _ss.lib().ss_linear_xent(hidden.data_ptr(), weight.data_ptr(), targets.data_ptr(), loss.data_ptr(), lse.data_ptr(), T, V, D,
-                                  ctypes.byref(s), ws.data_ptr(), ws.numel(), _stream(hidden, stream))
+                                  ctypes.byref(s), ws.data_ptr(), nbytes, _stream(hidden, stream))
     if st != 0:
         raise _ss.SelscanError(st, "ss_linear_xent")
     return loss, lse
@@ -223,9 +215,9 @@ def ss_linear_xent_bwd(dloss, hidden, weight, targets, lse, stream=None):
     s.dloss_t = dloss.stride(0)
     _param(lse, "lse", f32, (T,))
     dhidden, dweight = _empty((T, D), io, dev, stream), _empty((V, D), io, dev, stream)
-    ws = _xent_scratch(hidden, stream, T, V, D, s, 1)
+    ws, nbytes = _scratch(hidden, stream, "ss_linear_xent_workspace_size", T, V, D, s.io_dtype, 1)
     st = _ss.lib().ss_linear_xent_bwd(dloss.data_ptr(), hidden.data_ptr(), weight.data_ptr(), targets.data_ptr(), lse.data_ptr(),
-                                      dhidden.data_ptr(), dweight.data_ptr(), T, V, D, ctypes.byref(s), ws.data_ptr(), ws.numel(),
+                                      dhidden.data_ptr(), dweight.data_ptr(), T, V, D, ctypes.byref(s), ws.data_ptr(), nbytes,
                                       _stream(hidden, stream))
     if st != 0:
         raise _ss.SelscanError(st, "ss_linear_xent_bwd")
