@@ -51,8 +51,8 @@ struct DistillShared {
     float t[kMaxK], z[kMaxK];                      // their logits: teacher's, student's
     float2 stat[kWarps], entry[kWarps];
     float part[kWarps];
-    float2 mine;                                   // (max, sum) of this CTA's slice: read by the cluster's others
-    uint64_t full;
+    float2 sums[kMaxCluster];                      // (max, sum) of the slices of the cluster's CTAs, which they send here
+    uint64_t full, sent;
     int abort;
 };
 
@@ -137,11 +137,6 @@ struct Running {
         }
         s += ex2((v - base(m)) * c);
     }
-    __device__ __forceinline__ void join(float m2, float s2, float c) {
-        const float n = fmaxf(m, m2), b = base(n);
-        s = s * ex2((m - b) * c) + s2 * ex2((m2 - b) * c);
-        m = n;
-    }
     // Over groups of LANES lanes.
     template <int LANES> __device__ __forceinline__ void join_lanes(float c) {
         float n = m;
@@ -153,6 +148,12 @@ struct Running {
         for (int o = LANES / 2; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
     }
 };
+
+// Two floats into a CTA's shared memory, which its barrier counts (addresses of the cluster's window).
+__device__ __forceinline__ void send_f32x2(uint32_t to, float2 v, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to), "f"(v.x), "f"(v.y), "r"(bar)
+                 : "memory");
+}
 
 template <typename T, bool GRAD>
 __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillParams p) {
@@ -169,9 +170,13 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillParams p
 
     if (tid == 0) {
         mbar_init(&sh.full, 1);
+        mbar_init(&sh.sent, 1);
         sh.abort = 0;
         mbar_fence_init();
     }
+    // (after thread 0's part: what it sets up is there for the cluster once all have arrived)
+    __syncwarp();
+    if (size > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     // the teacher's entries, in every CTA of the row
     Running e;
     int32_t* sid = reinterpret_cast<int32_t*>(sh.id);
@@ -237,15 +242,17 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillParams p
         r.join_lanes<kWarps>(c);
         e.join_lanes<kWarps>(c);
         if (size > 1) {                            // (a row's CTAs agree on whether it has any weight)
-            if (tid == 0) sh.mine = make_float2(r.m, r.s);
-            cluster_sync_all();
-            Running all;
-            for (uint32_t k = 0; k < size; ++k) {
-                const uint32_t a = peer_smem_addr(&sh.mine, k);
-                all.join(ld_peer_f32(a), ld_peer_f32(a + 4), c);
-            }
-            r = all;
-            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");            // (waited for at the end)
+            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");              // the others' barriers exist
+            if (tid == 0) mbar_expect_tx(&sh.sent, size * 8u);
+            if (tid < static_cast<int>(size))
+                send_f32x2(peer_smem_addr(&sh.sums[rank], tid), make_float2(r.m, r.s), peer_smem_addr(&sh.sent, tid));
+            ok = mbar_wait_bounded<true>(&sh.sent, 0, &sh.abort, p.err) && ok;
+            const float2 v = tid % 32 < static_cast<int>(size) ? sh.sums[tid % 32] : make_float2(-INFINITY, 0.f);
+            r.m = v.x;
+            r.s = v.y;
+            r.join_lanes<kMaxCluster>(c);
+            r.m = __shfl_sync(0xffffffffu, r.m, 0);
+            r.s = __shfl_sync(0xffffffffu, r.s, 0);
         }
     }
     const float m = Running::base(r.m), inv_s = 1.f / r.s;
@@ -281,23 +288,45 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillParams p
         // (a row of dlogits that lies otherwise against the 16 bytes is written element by element)
         const bool same = reinterpret_cast<uintptr_t>(d + head) % 16 == 0;
         const T first_z = some && lo + tid < head ? z[lo + tid] : from_f32<T>(0.f), last_z = some && tail + tid < hi ? z[tail + tid] : from_f32<T>(0.f);
-#pragma unroll 4
-        for (int k = tid; k < vecs; k += kThreads) {
+        uint4* dv = reinterpret_cast<uint4*>(d + head);
+        auto value = [&](const uint4& u, float (&v)[N]) {
+            Vec16<T>::get(u, v);
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const float2 o = mul2(ex2x2(mul2(add2(make_float2(v[i], v[i + 1]), off), c2)), gs2);
+                v[i] = o.x;
+                v[i + 1] = o.y;
+            }
+        };
+        if (!some) {
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            if (same)
+                for (int k = tid; k < vecs; k += kThreads) __stcs(dv + k, zero);
+            else
+                for (int k = head + tid; k < tail; k += kThreads) d[k] = from_f32<T>(0.f);
+        } else if (same) {
             float v[N];
+            int k = tid;
+            for (; k + (kBatch - 1) * kThreads < mine; k += kBatch * kThreads) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = 0.f;
-            if (some) {
-                Vec16<T>::get(k < mine ? held[k] : __ldcs(zv + k), v);
-#pragma unroll
-                for (int i = 0; i < N; i += 2) {
-                    const float2 o = mul2(ex2x2(mul2(add2(make_float2(v[i], v[i + 1]), off), c2)), gs2);
-                    v[i] = o.x;
-                    v[i + 1] = o.y;
+                for (int j = 0; j < kBatch; ++j) {
+                    value(held[k + j * kThreads], v);
+                    __stcs(dv + k + j * kThreads, Vec16<T>::put(v));
                 }
             }
-            if (same) {
-                __stcs(reinterpret_cast<uint4*>(d + head) + k, Vec16<T>::put(v));
-            } else {
+            for (; k < mine; k += kThreads) {
+                value(held[k], v);
+                __stcs(dv + k, Vec16<T>::put(v));
+            }
+#pragma unroll 4
+            for (k = mine + tid; k < vecs; k += kThreads) {
+                value(__ldcs(zv + k), v);
+                __stcs(dv + k, Vec16<T>::put(v));
+            }
+        } else {
+            for (int k = tid; k < vecs; k += kThreads) {
+                float v[N];
+                value(k < mine ? held[k] : __ldcs(zv + k), v);
 #pragma unroll
                 for (int i = 0; i < N; ++i) d[head + k * N + i] = from_f32<T>(v[i]);
             }
@@ -329,7 +358,8 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillParams p
     }
     if (!ok)                                       // a wait that ran out: copies in flight are over long before this
         for (int i = 0; i < 20; ++i) __nanosleep(1000000);
-    if (some && size > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    // (a CTA ends when it has everyone's sums, and its own have reached everyone: nobody ends before)
+    if (!some && size > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // CTAs for a row: so many that each holds its slice, and more where rows are few, as long as each keeps some 8 KB.
