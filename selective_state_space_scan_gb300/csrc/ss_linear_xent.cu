@@ -10,11 +10,13 @@
 //   backward   the logits again, piece by piece of the vocabulary; a piece's dl is kept in fp16 (in the workspace:
 //              kPieceBytes of it), then both products over it in one launch: dweight's rows of the piece, whole, and
 //              dhidden as sums in fp32 that grow from piece to piece
-// Operands.  bf16 logits of the forward pass: as they are.  Everything else is taken in fp16, scaled by one power of
-// two per tensor so that its largest value lies below 2^15: a bf16 value is exact there down to 2^-31 of the
-// largest, and dl has 11 bits instead of bf16's 8 (in bf16 its rounding would add to the gradients' error as much as
-// their own does: 2.9e-3 instead of 1.7e-3).  A float32 value is the sum of two fp16 (22 bits), and a product the
-// three products of these that count (K three times as long; three parts of bf16 would take six).
+// Operands.  bf16 logits of the forward pass: as they are.  The backward pass takes bf16 tensors in fp16 as a rule, scaled
+// by one power of two per tensor so that the largest value lies below 2^15: a bf16 value is exact there down to 2^-31 of
+// the largest, and dl has 11 bits instead of bf16's 8 (in bf16 its rounding would add to the gradients' error as much as
+// their own does: 2.9e-3 instead of 1.7e-3).  With few tokens, where the traffic is the bound, it takes them as they
+// are and dl as the sum of two bf16: half more products, but weight is not copied.  A float32 value is the sum of two
+// scaled fp16 (22 bits), and a product the three products of these that count (K three times as long; three parts of
+// bf16 would take six).
 //
 // One persistent CTA pair per two SMs: a warp that loads (TMA, six stages of 2 x 16 KB), one that issues, eight
 // that empty the other of two accumulators meanwhile.
@@ -54,17 +56,25 @@ constexpr uint32_t kAccCols = 256;
 // 16 products off at 2^-23 of the sum instead of rounding it, so a long chain is off by its length times half of
 // that, to one side: 560 additions gave a dhidden off by 1e-5, 64 in a row 1e-6.  The registers' own additions
 // round.  Results in fp32 take 16 (32 the loss) in a row, those that end in bf16 64.
-template <Product P, bool F32> constexpr int kChain = F32 ? 4 : P == Product::kLoss ? 8 : 16;
+template <Product P, Form F> constexpr int kChain = F == Form::kSplit ? 4 : P == Product::kLoss ? 8 : 16;
 
-// The products of two-part operands that count, small ones first.
-constexpr int kSegs = 3;
-__constant__ int8_t kPartA[kSegs] = {0, 1, 0};
-__constant__ int8_t kPartB[kSegs] = {1, 0, 0};
+// The products of parts that a product takes, small ones first: kSplit's, then kOut's of kRaw (dl's low part, its high one).
+template <Product P, Form F> constexpr int kSegs = F == Form::kSplit ? 3 : F == Form::kRaw && P == Product::kOut ? 2 : 1;
+__constant__ int8_t kPartA[2][3] = {{0, 1, 0}, {1, 0, 0}};
+__constant__ int8_t kPartB[2][3] = {{1, 0, 0}, {0, 0, 0}};
+constexpr int kDlParts(Form f) { return f == Form::kHalf ? 1 : 2; }
 
 // Exponent n of the power of two that a tensor's values are divided by, from the bits of its largest finite one: what
 // is left is below 2^15.  2^n and 2^-n are normal floats.
 __device__ __forceinline__ int scale_exp(unsigned int bits) { return min(max(static_cast<int>(bits >> 23) - 127 - 14, -126), 126); }
 __device__ __forceinline__ float pow2(int n) { return __int_as_float((n + 127) << 23); }
+// weight's, which is packed before its largest value is known: that of values below 2^7, unless they turn out larger or
+// all below 2^-4 (they are packed again then).
+constexpr int kGuess = -7;
+__device__ __forceinline__ int weight_exp(unsigned int bits) {
+    const int e = static_cast<int>(bits >> 23) - 127;
+    return e >= -4 && e < 7 ? kGuess : scale_exp(bits);
+}
 // 2^n for n of -252 to 252 as a product of two floats (the second 1 where one is enough).
 struct Pow2x2 {
     float a, b;
@@ -83,10 +93,7 @@ struct GemmShared {
 constexpr uint32_t kBox = 32 * 128;                // bytes of a warp's store: 32 rows of 128
 constexpr size_t kGemmSmem = kStages * kStageBytes + kEpiWarps * kBox + sizeof(GemmShared) + 1024;
 
-// Whether the operands are bf16 as they are (else scaled fp16).
-template <Product P, bool F32> constexpr bool kRaw = P == Product::kLoss && !F32;
-
-// A unit of work: a tile and a range of steps of K (each of them kSegs products of parts for F32).
+// A unit of work: a tile and a range of steps of K (each of them kSegs products of parts).
 struct Unit {
     int job, m, n, k0, k1, split;
 };
@@ -176,14 +183,14 @@ __device__ __forceinline__ void store16(void* q, uint4 v) { *reinterpret_cast<ui
 
 __device__ __forceinline__ uint32_t half_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
-// 8 values to fp16, and (F32) what is left of them to the second part.
-template <bool F32>
+// 8 values to fp16, and (SPLIT) what is left of them to the second part.
+template <bool SPLIT>
 __device__ __forceinline__ void store_half8(__half* q, int64_t part, const float2 (&f)[4]) {
     __half2 h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) h[i] = __float22half2_rn(f[i]);
     store16(q, make_uint4(half_bits(h[0]), half_bits(h[1]), half_bits(h[2]), half_bits(h[3])));
-    if constexpr (F32) {
+    if constexpr (SPLIT) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) h[i] = __float22half2_rn(fma2(__half22float2(h[i]), splat2(-1.f), f[i]));
         store16(q + part, make_uint4(half_bits(h[0]), half_bits(h[1]), half_bits(h[2]), half_bits(h[3])));
@@ -210,7 +217,7 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint8_t* box, 
     }
 }
 
-template <Product P, bool F32>
+template <Product P, Form F>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xent_gemm_kernel(const __grid_constant__ XentParams p) {
     extern __shared__ uint8_t raw[];
     uint8_t* tiles = raw + (1024 - smem_addr(raw) % 1024) % 1024;
@@ -242,9 +249,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
     const int rows = *p.count;
     const Work work = make_work<P>(p, rows, clusters);
     int ex = 0, ew = 0, eg = 0;
-    if constexpr (!kRaw<P, F32>) {
+    constexpr int kTable = F == Form::kSplit ? 0 : 1, kSegsHere = kSegs<P, F>;
+    if constexpr (F != Form::kRaw) {
         ex = scale_exp(p.range[kRangeX]);
-        ew = scale_exp(p.range[kRangeW]);
+        ew = weight_exp(p.range[kRangeW + p.piece]);
         if constexpr (P != Product::kLoss) eg = scale_exp(p.range[kRangeG]);
     }
 
@@ -264,10 +272,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                 const bool a_mn = P == Product::kOut && u.job == 0, b_mn = P == Product::kOut;
                 const int am = u.m * kTile + static_cast<int>(rank) * kHalf, bn = u.n * kTile + static_cast<int>(rank) * kHalf;
                 bool go = true;
-                for (int kc = u.k0; kc < u.k1 && go; kc += kChain<P, F32>)
-                    for (int seg = 0; seg < (F32 ? kSegs : 1) && go; ++seg) {
-                        const int pa = F32 ? kPartA[seg] : 0, pb = F32 ? kPartB[seg] : 0;
-                        for (int k = kc; k < min(kc + kChain<P, F32>, u.k1); ++k) {
+                for (int kc = u.k0; kc < u.k1 && go; kc += kChain<P, F>)
+                    for (int seg = 0; seg < kSegsHere && go; ++seg) {
+                        const int pa = kSegsHere > 1 ? kPartA[kTable][seg] : 0, pb = kSegsHere > 1 ? kPartB[kTable][seg] : 0;
+                        for (int k = kc; k < min(kc + kChain<P, F>, u.k1); ++k) {
                             go = mbar_wait_bounded(&sh.empty[st], ph ^ 1, abort, p.err);
                             if (!go) break;
                             if (rank == 0) mbar_expect_tx(&sh.full[st], 2 * kStageBytes);
@@ -314,11 +322,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                 const Unit u = unit_of<P>(work, i);
                 const bool a_mn = P == Product::kOut && u.job == 0, b_mn = P == Product::kOut;
                 constexpr uint32_t kBf16 = 1u << 7 | 1u << 10;                          // operand types (else fp16)
-                const uint32_t idesc = tc_idesc(256, 256, a_mn, b_mn) & ~(kRaw<P, F32> ? 0u : kBf16);
+                const uint32_t idesc = tc_idesc(256, 256, a_mn, b_mn) & ~(F == Form::kRaw ? 0u : kBf16);
                 const uint32_t la = a_mn ? kOperand / 2 : 16, lb = b_mn ? kOperand / 2 : 16, ka = a_mn ? 2048 : 32, kb = b_mn ? 2048 : 32;
-                for (int kc = u.k0; kc < u.k1 && go; kc += kChain<P, F32>, ++turn) {
+                for (int kc = u.k0; kc < u.k1 && go; kc += kChain<P, F>, ++turn) {
                     const uint32_t d = tmem + (turn & 1) * kAccCols;
-                    const int n = (min(kc + kChain<P, F32>, u.k1) - kc) * (F32 ? kSegs : 1);
+                    const int n = (min(kc + kChain<P, F>, u.k1) - kc) * kSegsHere;
                     go = mbar_wait_bounded(&sh.acc_empty[turn & 1], ((turn >> 1) & 1) ^ 1, abort, p.err);
                     tc_fence_after();
                     for (int k = 0; k < n && go; ++k) {
@@ -352,7 +360,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
 #pragma unroll
             for (int j = 0; j < kHalf; ++j) acc[j] = 0.f;
 #pragma unroll 1
-            for (int kc = u.k0; kc < u.k1; kc += kChain<P, F32>, ++turn) {
+            for (int kc = u.k0; kc < u.k1; kc += kChain<P, F>, ++turn) {
                 go = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.acc_full[turn & 1], (turn >> 1) & 1, abort, p.err));
                 if (!go) break;
                 tc_fence_after();
@@ -376,7 +384,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
             const int row = u.m * kTile + static_cast<int>(rank) * kHalf + quarter * 32 + lane;
             const int col0 = u.n * kTile + half * kHalf;
             if constexpr (P == Product::kLoss) {
-                if constexpr (F32) {
+                if constexpr (F == Form::kSplit) {
                     const Pow2x2 f(ex + ew);
 #pragma unroll
                     for (int j = 0; j < kHalf; ++j) acc[j] = acc[j] * f.a * f.b;
@@ -414,7 +422,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                 if (row < rows) p.part[(static_cast<int64_t>(p.tile0 + u.n) * 2 + half) * p.ld_part + row] = make_float2(m, s);
             } else if constexpr (P == Product::kGrad) {
                 const bool ok = row < rows;
-                const float lse = ok ? p.lse[row] : 0.f, g = ok ? p.g[row] * pow2(-eg) : 0.f;
+                const float lse = ok ? p.lse[row] : 0.f, g = ok ? (F == Form::kRaw ? p.g[row] : p.g[row] * pow2(-eg)) : 0.f;
                 const int tgt = ok ? p.tgt[row] - p.v0 - col0 : -1;
                 const Pow2x2 f(ex + ew);
                 const float2 off = splat2(-lse), f2 = splat2(f.a), l2e = splat2(kLog2e), g2 = splat2(g);
@@ -425,7 +433,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
 #pragma unroll
                 for (int c = 0; c < kHalf; c += 64) {
                     if (col0 + c >= p.Vp) break;
-                    uint32_t hi[32], lo[F32 ? 32 : 1];
+                    uint32_t hi[32], lo[kDlParts(F) > 1 ? 32 : 1];
 #pragma unroll
                     for (int q = 0; q < 64; q += 8) {
                         float2 e[4];
@@ -443,18 +451,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                         for (int j = 0; j < 4; ++j) {
                             e[j] = mul2(e[j], g2);
                             if (!ok) e[j] = splat2(0.f);
-                            const __half2 h = __float22half2_rn(e[j]);
-                            hi[q / 2 + j] = half_bits(h);
-                            if constexpr (F32) lo[q / 2 + j] = half_bits(__float22half2_rn(fma2(__half22float2(h), splat2(-1.f), e[j])));
+                            if constexpr (F == Form::kRaw) {
+                                hi[q / 2 + j] = pack_bf16(e[j].x, e[j].y);
+                                lo[q / 2 + j] = pack_rest(e[j], hi[q / 2 + j]);
+                            } else {
+                                const __half2 h = __float22half2_rn(e[j]);
+                                hi[q / 2 + j] = half_bits(h);
+                                if constexpr (F == Form::kSplit) lo[q / 2 + j] = half_bits(__float22half2_rn(fma2(__half22float2(h), splat2(-1.f), e[j])));
+                            }
                         }
                     }
                     store_box<false>(&p.s0, box, hi, col0 + c, row - lane, 0);
-                    if constexpr (F32) store_box<false>(&p.s0, box, lo, col0 + c, row - lane, 1);
+                    if constexpr (kDlParts(F) > 1) store_box<false>(&p.s0, box, lo, col0 + c, row - lane, 1);
                 }
             } else {
-                const Pow2x2 f(eg + (u.job ? ew : ex));
+                constexpr bool F32 = F == Form::kSplit;
+                if constexpr (F != Form::kRaw) {
+                    const Pow2x2 f(eg + (u.job ? ew : ex));
 #pragma unroll
-                for (int j = 0; j < kHalf; ++j) acc[j] = acc[j] * f.a * f.b;
+                    for (int j = 0; j < kHalf; ++j) acc[j] = acc[j] * f.a * f.b;
+                }
                 if (u.job || (F32 && p.dw_wide)) {
                     // rows of 32 floats
 #pragma unroll
@@ -504,7 +520,7 @@ constexpr int kPrepThreads = 256;
 // Columns [c, c + 8) of a row as an operand: bf16 as it is (RAW), or fp16 times `scale`, in two parts for fp32.
 // Columns of D and more are zero.
 template <typename T, bool RAW>
-__device__ __forceinline__ void pack8(const T* row, __half* out, int64_t part, int c, int D, bool wide, float scale) {
+__device__ __forceinline__ void pack8(const T* row, __half* out, int64_t part, int c, int D, bool wide, float scale, unsigned int* most = nullptr) {
     float v[8];
     if (wide && c + 8 <= D) {
         if constexpr (sizeof(T) == 2) {
@@ -530,6 +546,13 @@ __device__ __forceinline__ void pack8(const T* row, __half* out, int64_t part, i
     if constexpr (RAW) {
         store16(out + c, make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])));
     } else {
+        if (most) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const unsigned int bits = __float_as_uint(v[i]) & 0x7fffffffu;
+                *most = max(*most, bits < 0x7f800000u ? bits : 0u);
+            }
+        }
         float2 f[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[i] = make_float2(v[2 * i] * scale, v[2 * i + 1] * scale);
@@ -537,72 +560,61 @@ __device__ __forceinline__ void pack8(const T* row, __half* out, int64_t part, i
     }
 }
 
-// Largest finite magnitudes (as bits, whose order is the floats') of hidden's rows with a target, of weight and
-// of dloss: blocks of rows of hidden, then of weight.
-template <typename T>
-__device__ __forceinline__ unsigned int row_range(const T* row, int D, bool wide, unsigned int m) {
-    auto take = [&](unsigned int bits) {
-        bits &= 0x7fffffffu;
-        m = max(m, bits < 0x7f800000u ? bits : 0u);
-    };
-    constexpr int N = 16 / sizeof(T);
-    const int vecs = wide ? D / N : 0;
-    constexpr int U = 4;
-    for (int i = threadIdx.x % 32; i < vecs; i += 32 * U) {
-        uint4 u[U];
-#pragma unroll
-        for (int k = 0; k < U; ++k) u[k] = i + 32 * k < vecs ? reinterpret_cast<const uint4*>(row)[i + 32 * k] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const uint32_t a[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                take(sizeof(T) == 2 ? a[j] << 16 : a[j]);
-                if constexpr (sizeof(T) == 2) take(a[j] & 0xffff0000u);
-            }
-        }
-    }
-    for (int c = vecs * N + threadIdx.x % 32; c < D; c += 32) take(__float_as_uint(to_f32<T>(row[c])));
-    return m;
+// Magnitudes as bits, whose order is the floats': the larger of m and v's, if that is finite.
+__device__ __forceinline__ unsigned int max_finite(unsigned int m, float v) {
+    const unsigned int bits = __float_as_uint(v) & 0x7fffffffu;
+    return max(m, bits < 0x7f800000u ? bits : 0u);
 }
-template <typename T>
-__global__ void __launch_bounds__(kPrepThreads) xent_range_kernel(const PrepParams p, const T* w, int64_t w_v, bool w_wide, int x_blocks) {
-    __shared__ unsigned int part[3];
-    if (threadIdx.x < 3) part[threadIdx.x] = 0u;
+// The block's largest to *out.
+__device__ __forceinline__ void block_max(unsigned int m, unsigned int* part, unsigned int* out) {
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = m;
     __syncthreads();
-    constexpr int kWarps = kPrepThreads / 32;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x < 32) {
+        m = __reduce_max_sync(0xffffffffu, threadIdx.x < kPrepThreads / 32 ? part[threadIdx.x] : 0u);
+        if (threadIdx.x == 0 && m) atomicMax(out, m);
+    }
+    __syncthreads();
+}
+
+// Largest finite magnitudes of hidden's rows with a target and of their dloss; a warp has a row at a time.
+template <typename T>
+__global__ void __launch_bounds__(kPrepThreads) xent_range_kernel(const PrepParams p) {
+    __shared__ unsigned int part[kPrepThreads / 32];
+    constexpr int kWarps = kPrepThreads / 32, N = 16 / sizeof(T), U = 4;
+    const int lane = threadIdx.x % 32, vecs = p.wide ? p.D / N : 0;
     unsigned int m = 0u, g = 0u;
-    const bool x = static_cast<int>(blockIdx.x) < x_blocks;
-    if (x) {
-        for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.T; t += static_cast<int64_t>(x_blocks) * kWarps) {
-            const int v = p.targets[t];
-            if (v < 0 || v >= p.V) continue;
-            m = row_range<T>(static_cast<const T*>(p.hidden) + t * p.hidden_t, p.D, p.wide, m);
-            if (p.dloss && lane == 0) {
-                const unsigned int bits = __float_as_uint(p.dloss[t * p.dloss_t]) & 0x7fffffffu;
-                g = max(g, bits < 0x7f800000u ? bits : 0u);
+    let_next_start();
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32; t < p.T; t += static_cast<int64_t>(gridDim.x) * kWarps) {
+        const int v = p.targets[t];
+        if (v < 0 || v >= p.V) continue;
+        const T* row = static_cast<const T*>(p.hidden) + t * p.hidden_t;
+        for (int i = lane; i < vecs; i += 32 * U) {
+            uint4 u[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) u[k] = i + 32 * k < vecs ? reinterpret_cast<const uint4*>(row)[i + 32 * k] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const uint32_t a[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    m = max_finite(m, sizeof(T) == 2 ? bf16_lo(a[j]) : __uint_as_float(a[j]));
+                    if constexpr (sizeof(T) == 2) m = max_finite(m, bf16_hi(a[j]));
+                }
             }
         }
-    } else {
-        const int64_t first = static_cast<int64_t>(blockIdx.x - x_blocks) * kWarps + warp, step = static_cast<int64_t>(gridDim.x - x_blocks) * kWarps;
-        for (int64_t v = first; v < p.V; v += step) m = row_range<T>(w + v * w_v, p.D, w_wide, m);
+        for (int c = vecs * N + lane; c < p.D; c += 32) m = max_finite(m, to_f32<T>(row[c]));
+        if (p.dloss && lane == 0) g = max_finite(g, p.dloss[t * p.dloss_t]);
     }
-    m = __reduce_max_sync(0xffffffffu, m);
-    g = __reduce_max_sync(0xffffffffu, g);
-    if (lane == 0) {
-        atomicMax(&part[x ? kRangeX : kRangeW], m);
-        atomicMax(&part[kRangeG], g);
-    }
-    __syncthreads();
-    if (threadIdx.x < 3 && part[threadIdx.x]) atomicMax(&p.range[threadIdx.x], part[threadIdx.x]);
+    block_max(m, part, &p.range[kRangeX]);
+    block_max(g, part, &p.range[kRangeG]);
 }
 
 // The rows that have a target, gathered in order: row i of x is row rows[i] of hidden.  A block has `per` rows of
 // hidden, at most one to a thread, and counts the targets before them itself; a warp packs a row at a time.
-template <typename T, bool BWD>
+template <typename T, bool BWD, bool RAW>
 __global__ void __launch_bounds__(kPrepThreads) xent_gather_kernel(const PrepParams p) {
-    constexpr bool F32 = sizeof(T) == 4, RAW = !F32 && !BWD;
+    constexpr bool F32 = sizeof(T) == 4;
     constexpr int kWarps = kPrepThreads / 32;
     __shared__ int before[kWarps], own[kWarps], to[kPrepThreads];
     let_next_start();
@@ -670,18 +682,27 @@ __global__ void __launch_bounds__(kPrepThreads) xent_gather_kernel(const PrepPar
     }
 }
 
-// Rows of weight as operands of the products.
-template <typename T, bool RAW>
+// Rows of weight as operands of the products.  The scale is a guess, and *range gets the largest finite magnitude;
+// AGAIN: the same with the scale that this asks for, if the guess was wrong.
+template <typename T, bool RAW, bool AGAIN>
 __global__ void __launch_bounds__(kPrepThreads) xent_pack_kernel(const T* w, int64_t stride, __half* out, int64_t ld, int64_t part, int64_t n, int D,
-                                                                 bool wide, const unsigned int* range) {
+                                                                 bool wide, unsigned int* range) {
+    __shared__ unsigned int most[kPrepThreads / 32];
     const int vecs = static_cast<int>(ld / 8);
     let_next_start();
     wait_for_earlier();
-    const float scale = RAW ? 1.f : pow2(-scale_exp(range[kRangeW]));
+    int e = kGuess;
+    if constexpr (AGAIN) {
+        e = weight_exp(*range);
+        if (e == kGuess) return;
+    }
+    const float scale = RAW ? 1.f : pow2(-e);
+    unsigned int m = 0u;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPrepThreads + threadIdx.x; i < n * vecs; i += static_cast<int64_t>(gridDim.x) * kPrepThreads) {
         const int64_t r = i / vecs;
-        pack8<T, RAW>(w + r * stride, out + r * ld, part, static_cast<int>(i - r * vecs) * 8, D, wide, scale);
+        pack8<T, RAW>(w + r * stride, out + r * ld, part, static_cast<int>(i - r * vecs) * 8, D, wide, scale, RAW || AGAIN ? nullptr : &m);
     }
+    if constexpr (!RAW && !AGAIN) block_max(m, most, range);
 }
 
 // lse and loss from the maxima and sums of the half tiles; a block has 32 rows, a warp a share of the tiles.
@@ -752,6 +773,7 @@ using host::range3;
 constexpr int64_t kPieceBytes = 512 << 20;        // of dl (and of a packed piece of weight)
 constexpr int64_t kMinPiece = 4096;               // columns: below, the sums of dhidden cost as much as the products
 constexpr int64_t kMaxSplits = 32;
+constexpr int64_t kRawTokens = 256;               // tokens up to which the backward pass takes bf16 operands as they are
 constexpr int64_t kMinSteps = 16;                 // of K to a slice of dhidden's sums
 
 int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
@@ -767,7 +789,9 @@ int sm_count() {
 
 // Where everything lies in the workspace.
 struct Layout {
-    int64_t parts, segs, ld_x, tpad, piece, pieces, splits, ld_dl, ld_dx, halves;
+    int64_t parts, dl_parts, segs, ld_x, tpad, piece, pieces, splits, ld_dl, ld_dx, halves;
+    Form form;
+    bool packed;                                  // weight, piece by piece
     size_t count, range, rows, tgt, lse, g, tl, part, x, w, dl, dx, total;
 };
 
@@ -790,14 +814,16 @@ int64_t out_cost(int64_t T, int64_t D, int64_t Vp, int64_t segs, int64_t splits,
 }
 
 Layout layout(int64_t T, int64_t V, int64_t D, bool f32, bool in_place, bool bwd) {
-    const bool packed = f32 || bwd || !in_place;
     Layout q;
     std::memset(&q, 0, sizeof(q));
+    q.form = f32 ? Form::kSplit : bwd && T > kRawTokens ? Form::kHalf : Form::kRaw;
+    const bool packed = q.packed = q.form != Form::kRaw || !in_place;
     q.parts = f32 ? 2 : 1;
-    q.segs = f32 ? kSegs : 1;
+    q.dl_parts = kDlParts(q.form);
+    q.segs = f32 ? kSegs<Product::kOut, Form::kSplit> : q.form == Form::kRaw ? kSegs<Product::kOut, Form::kRaw> : 1;
     q.ld_x = round_up(D, 8);
     q.tpad = round_up(T, kTile);
-    const int64_t per_col = std::max(bwd ? q.tpad * 2 * q.parts : 0, packed ? q.ld_x * 2 * q.parts : 0);
+    const int64_t per_col = std::max(bwd ? q.tpad * 2 * q.dl_parts : 0, packed ? q.ld_x * 2 * q.parts : 0);
     q.piece = V;
     if (per_col > 0) {
         const int64_t most = std::max(kPieceBytes / per_col / kTile * kTile, kMinPiece);
@@ -828,7 +854,7 @@ Layout layout(int64_t T, int64_t V, int64_t D, bool f32, bool in_place, bool bwd
         return o;
     };
     q.count = take(4);
-    q.range = take(12);
+    q.range = take(4 * (kRangeW + q.pieces));
     q.rows = take(4 * q.tpad);
     q.tgt = take(4 * q.tpad);
     if (bwd) {
@@ -841,7 +867,7 @@ Layout layout(int64_t T, int64_t V, int64_t D, bool f32, bool in_place, bool bwd
     q.x = take(2 * q.parts * q.tpad * q.ld_x);
     if (packed) q.w = take(2 * q.parts * q.piece * q.ld_x);
     if (bwd) {
-        q.dl = take(2 * q.parts * q.tpad * q.ld_dl);
+        q.dl = take(2 * q.dl_parts * q.tpad * q.ld_dl);
         q.dx = take(4 * q.splits * q.tpad * q.ld_dx);
     }
     q.total = at;
@@ -875,10 +901,10 @@ bool make_map(CUtensorMap* m, const void* base, int64_t es, int64_t cols, int64_
 }
 
 // Pairs of CTAs that fit on the device at once.
-template <Product P, bool F32>
+template <Product P, Form F>
 cudaError_t launch_gemm_as(const XentParams& p, int64_t units, cudaStream_t stream) {
     static std::atomic<int> known[64] = {};
-    auto* kern = xent_gemm_kernel<P, F32>;
+    auto* kern = xent_gemm_kernel<P, F>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -905,8 +931,11 @@ cudaError_t launch_gemm_as(const XentParams& p, int64_t units, cudaStream_t stre
     return launch_chained(kern, dim3(grid), dim3(kGemmThreads), kGemmSmem, stream, p);
 }
 template <Product P>
-cudaError_t launch_gemm(const XentParams& p, bool f32, int64_t units, cudaStream_t stream) {
-    return f32 ? launch_gemm_as<P, true>(p, units, stream) : launch_gemm_as<P, false>(p, units, stream);
+cudaError_t launch_gemm(const XentParams& p, Form form, int64_t units, cudaStream_t stream) {
+    if (form == Form::kSplit) return launch_gemm_as<P, Form::kSplit>(p, units, stream);
+    if constexpr (P != Product::kLoss)
+        if (form == Form::kHalf) return launch_gemm_as<P, Form::kHalf>(p, units, stream);
+    return launch_gemm_as<P, Form::kRaw>(p, units, stream);
 }
 
 struct Call {
@@ -1003,20 +1032,18 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
     g.dhidden = c.dhidden; g.dhidden_t = s.dhidden_t; g.loss_out = c.loss; g.lse_out = c.lse;
     g.err = device_error_word();
     g.range = reinterpret_cast<unsigned int*>(ws + q.range);
-    const bool raw = !f32 && !c.bwd;
+    const bool raw = q.form == Form::kRaw;
     if (!raw) {
-        if (cudaMemsetAsync(g.range, 0, 12, st) != cudaSuccess) return SS_ERR_CUDA;
-        const int64_t warps = kPrepThreads / 32, most = 8 * sm_count();
-        const int xb = static_cast<int>(std::min((T + warps - 1) / warps, most)), wb = static_cast<int>(std::min((V + warps - 1) / warps, most));
-        const bool ww = wide(c.weight, s.weight_v);
-        if (f32)
-            xent_range_kernel<float><<<xb + wb, kPrepThreads, 0, st>>>(g, static_cast<const float*>(c.weight), s.weight_v, ww, xb);
-        else
-            xent_range_kernel<__nv_bfloat16><<<xb + wb, kPrepThreads, 0, st>>>(g, static_cast<const __nv_bfloat16*>(c.weight), s.weight_v, ww, xb);
+        if (cudaMemsetAsync(g.range, 0, 4 * (kRangeW + q.pieces), st) != cudaSuccess) return SS_ERR_CUDA;
+        const unsigned grid = static_cast<unsigned>(std::min<int64_t>((T + kPrepThreads / 32 - 1) / (kPrepThreads / 32), 8 * sm_count()));
+        if (f32) xent_range_kernel<float><<<grid, kPrepThreads, 0, st>>>(g);
+        else xent_range_kernel<__nv_bfloat16><<<grid, kPrepThreads, 0, st>>>(g);
         if (cudaGetLastError() != cudaSuccess) return SS_ERR_CUDA;
     }
-    void (*gather)(PrepParams) = f32 ? (c.bwd ? xent_gather_kernel<float, true> : xent_gather_kernel<float, false>)
-                                     : (c.bwd ? xent_gather_kernel<__nv_bfloat16, true> : xent_gather_kernel<__nv_bfloat16, false>);
+    using B = __nv_bfloat16;
+    void (*gather)(PrepParams) = f32   ? (c.bwd ? xent_gather_kernel<float, true, false> : xent_gather_kernel<float, false, false>)
+                                 : raw ? (c.bwd ? xent_gather_kernel<B, true, true> : xent_gather_kernel<B, false, true>)
+                                       : xent_gather_kernel<B, true, false>;
     const dim3 gather_grid(static_cast<unsigned>((T + g.per - 1) / g.per)), prep(kPrepThreads);
     if (raw) gather<<<gather_grid, prep, 0, st>>>(g);
     const cudaError_t ge = raw ? cudaGetLastError() : launch_chained(gather, gather_grid, prep, 0, st, g);
@@ -1034,16 +1061,17 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
         const int64_t Vp = std::min(q.piece, V - v0), vt = (Vp + kTile - 1) / kTile;
         const void* wp = static_cast<const char*>(c.weight) + v0 * s.weight_v * es;
         int64_t ld_w = s.weight_v;
-        if (!raw || !in_place) {
+        if (q.packed) {
             const unsigned grid = static_cast<unsigned>(std::min<int64_t>((Vp * q.ld_x / 8 + kPrepThreads - 1) / kPrepThreads, 16 * sm_count()));
             const bool ww = wide(wp, s.weight_v);
-            const __nv_bfloat16* wb = static_cast<const __nv_bfloat16*>(wp);
             auto pack = [&](auto* kern, auto* from) {
-                return launch_chained(kern, dim3(grid), prep, 0, st, from, s.weight_v, w, q.ld_x, w_part, Vp, p.D, ww, g.range);
+                return launch_chained(kern, dim3(grid), prep, 0, st, from, s.weight_v, w, q.ld_x, w_part, Vp, p.D, ww, g.range + kRangeW + p.piece);
             };
-            const cudaError_t e = f32   ? pack(xent_pack_kernel<float, false>, static_cast<const float*>(wp))
-                                  : raw ? pack(xent_pack_kernel<__nv_bfloat16, true>, wb)
-                                        : pack(xent_pack_kernel<__nv_bfloat16, false>, wb);
+            const B* wb = static_cast<const B*>(wp);
+            const float* wf = static_cast<const float*>(wp);
+            cudaError_t e = f32 ? pack(xent_pack_kernel<float, false, false>, wf)
+                                : raw ? pack(xent_pack_kernel<B, true, false>, wb) : pack(xent_pack_kernel<B, false, false>, wb);
+            if (e == cudaSuccess && !raw) e = f32 ? pack(xent_pack_kernel<float, false, true>, wf) : pack(xent_pack_kernel<B, false, true>, wb);
             if (e != cudaSuccess) return SS_ERR_CUDA;
             wp = w;
             ld_w = q.ld_x;
@@ -1054,21 +1082,23 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
         if (!make_map(&p.a0, x, 2, D, q.tpad, q.parts, q.ld_x, x_part, kHalf) || !make_map(&p.b0, wp, 2, D, Vp, q.parts, ld_w, w_part, kHalf))
             return SS_ERR_CUDA;
         if (!c.bwd) {
-            if (launch_gemm<Product::kLoss>(p, f32, mt * vt, st) != cudaSuccess) return SS_ERR_CUDA;
+            if (launch_gemm<Product::kLoss>(p, q.form, mt * vt, st) != cudaSuccess) return SS_ERR_CUDA;
             p.tile0 += static_cast<int>(vt);
+            ++p.piece;
             continue;
         }
-        if (!make_map(&p.s0, dl, 2, Vp, q.tpad, q.parts, q.ld_dl, dl_part, 32)) return SS_ERR_CUDA;
-        if (launch_gemm<Product::kGrad>(p, f32, mt * vt, st) != cudaSuccess) return SS_ERR_CUDA;
+        if (!make_map(&p.s0, dl, 2, Vp, q.tpad, q.dl_parts, q.ld_dl, dl_part, 32)) return SS_ERR_CUDA;
+        if (launch_gemm<Product::kGrad>(p, q.form, mt * vt, st) != cudaSuccess) return SS_ERR_CUDA;
         // dweight: dl and x with the tokens along rows; dhidden: dl with K along columns, weight with K along rows
         char* dw = static_cast<char*>(c.dweight) + v0 * s.dweight_v * es;
-        if (!make_map(&p.a0, dl, 2, Vp, q.tpad, q.parts, q.ld_dl, dl_part, kStep) || !make_map(&p.b0, x, 2, D, q.tpad, q.parts, q.ld_x, x_part, kStep) ||
-            !make_map(&p.a1, dl, 2, Vp, q.tpad, q.parts, q.ld_dl, dl_part, kHalf) || !make_map(&p.b1, wp, 2, D, Vp, q.parts, ld_w, w_part, kStep) ||
+        if (!make_map(&p.a0, dl, 2, Vp, q.tpad, q.dl_parts, q.ld_dl, dl_part, kStep) || !make_map(&p.b0, x, 2, D, q.tpad, q.parts, q.ld_x, x_part, kStep) ||
+            !make_map(&p.a1, dl, 2, Vp, q.tpad, q.dl_parts, q.ld_dl, dl_part, kHalf) || !make_map(&p.b1, wp, 2, D, Vp, q.parts, ld_w, w_part, kStep) ||
             !make_map(&p.s1, p.dx, 4, D, q.tpad, q.splits, q.ld_dx, p.dx_split, 32) ||
             (p.dw_wide && !make_map(&p.s0, dw, es, D, Vp, 1, s.dweight_v, 0, 32)))
             return SS_ERR_CUDA;
         p.add = v0 > 0;
-        if (launch_gemm<Product::kOut>(p, f32, vt * dt + mt * dt * q.splits, st) != cudaSuccess) return SS_ERR_CUDA;
+        if (launch_gemm<Product::kOut>(p, q.form, vt * dt + mt * dt * q.splits, st) != cudaSuccess) return SS_ERR_CUDA;
+        ++p.piece;
     }
     const unsigned rows_grid = static_cast<unsigned>(std::min<int64_t>(T, 8 * sm_count()));
     cudaError_t e;

@@ -11,8 +11,14 @@ namespace selscan {
 
 enum class Product { kLoss, kGrad, kOut };
 
-// Largest finite magnitudes that the operands' scales follow from.
-enum { kRangeX = 0, kRangeW = 1, kRangeG = 2 };
+// What the operands of the products are:
+//   kRaw    bf16 tensors as they are; dl as the sum of two bf16
+//   kHalf   bf16 tensors in fp16, scaled by a power of two (exact), dl in one fp16
+//   kSplit  fp32 tensors, and dl, as sums of two scaled fp16
+enum class Form { kRaw, kHalf, kSplit };
+
+// Largest finite magnitudes that the scales follow from; weight has one for each piece of the vocabulary.
+enum { kRangeX = 0, kRangeG = 1, kRangeW = 2 };
 
 struct XentParams {
     // operands of the products as [part][row][col]; kOut's second product has the maps a1 and b1
@@ -21,7 +27,8 @@ struct XentParams {
     const int* count;           // rows that have a target
     const int* tgt;             // [count] their targets
     int D, v0, Vp;              // the piece: columns v0 .. v0 + Vp of the vocabulary
-    const unsigned int* range;  // [3] bits of the largest magnitudes (scaled operands)
+    const unsigned int* range;  // bits of the largest magnitudes (scaled operands); kRangeW: the first piece's
+    int piece;                  // the piece's number
     unsigned int* err;
     // kLoss
     float2* part;               // [half tile][ld_part] maximum and sum of a row
@@ -53,7 +60,7 @@ struct PrepParams {
     int* rows;                  // [count] row of hidden
     int* tgt;
     unsigned int* err;
-    unsigned int* range;        // [3], zero before xent_range_kernel
+    unsigned int* range;        // zeros before xent_range_kernel
     float* loss_out;            // forward: zeros in rows without a target
     float* lse_out;
     const float* lse;           // backward

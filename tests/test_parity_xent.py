@@ -142,6 +142,30 @@ def test_non_finite_rows_stay_alone(io):
     assert torch.isfinite(d["dhidden"][keep]).all() and torch.isnan(d["dhidden"][7]).all()
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [40, 450])
+@pytest.mark.parametrize("scale", [2.0 ** -60, 2.0 ** -9, 1.5, 2.0 ** 9, 2.0 ** 60])
+def test_magnitudes(io, T, scale):
+    """Operands' scales follow the tensors' sizes: weight, hidden and dloss far from one, by the same pieces."""
+    c = Case(T, 1500, 128, io)
+    c.w, c.h = (c.w.double() * scale).to(DT[io]), (c.h.double() / max(scale, 1.0)).to(DT[io])
+    c.check()
+    c.g = c.g * scale
+    c.check()
+    c.g[::3] *= 2.0 ** -20                                   # weights of tokens far apart
+    c.check()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_rows_of_weight_of_unlike_sizes(io):
+    """Rows of zeros (padding of the vocabulary), small ones and one that outweighs the others."""
+    c = Case(450, 2000, 128, io)
+    c.w[100:200] = 0
+    c.w[200:300] *= 2.0 ** -30
+    c.w[5] *= 8
+    c.check()
+
+
 def test_large_logits():
     """Logits of thousands: the exponentials neither overflow nor lose the row."""
     c = Case(100, 2000, 64, "f32", scale=800.0)
