@@ -45,7 +45,10 @@ namespace {
 constexpr int kTile = 256;                        // rows and columns of a pair's tile
 constexpr int kHalf = kTile / 2;                  // rows of a CTA's operand tiles
 constexpr int kStep = 64;                         // of K per stage
-constexpr int kStages = 6;
+// Stages of operands, and a warp's boxes for what leaves, in 227 KB of shared memory (the loss leaves nothing).
+constexpr int kStagesOf(Product p) { return p == Product::kLoss ? 7 : 5; }
+constexpr int kBoxesOf(Product p) { return p == Product::kLoss ? 0 : 2; }
+constexpr int kMaxStages = 7;
 constexpr uint32_t kOperand = kHalf * kStep * 2;  // bytes of one operand's tile
 constexpr uint32_t kStageBytes = 2 * kOperand;
 constexpr int kEpiWarps = 8;
@@ -86,12 +89,12 @@ struct Pow2x2 {
 };
 
 struct GemmShared {
-    uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
     uint32_t tmem;
     int abort;
 };
 constexpr uint32_t kBox = 32 * 128;                // bytes of a warp's store: 32 rows of 128
-constexpr size_t kGemmSmem = kStages * kStageBytes + kEpiWarps * kBox + sizeof(GemmShared) + 1024;
+constexpr size_t gemm_smem(Product p) { return kStagesOf(p) * kStageBytes + kEpiWarps * kBoxesOf(p) * kBox + sizeof(GemmShared) + 1024; }
 
 // A unit of work: a tile and a range of steps of K (each of them kSegs products of parts).
 struct Unit {
@@ -201,9 +204,11 @@ __device__ __forceinline__ void store_half8(__half* q, int64_t part, const float
 // their own they would be stores of 16 bytes to 32 lines at a time, which took the L1 half of its time beside the
 // operands.  What lies outside the tensor is not written.  ADD: onto what is there.
 template <bool ADD>
-__device__ __forceinline__ void store_box(const CUtensorMap* map, uint8_t* box, const uint32_t (&w)[32], int col, int row, int part) {
+__device__ __forceinline__ void store_box(const CUtensorMap* map, uint8_t* boxes, uint32_t& turn, const uint32_t (&w)[32], int col, int row, int part) {
     const int lane = threadIdx.x % 32;
-    if (lane == 0) tma_store_wait_read();          // the store before has left this memory
+    uint8_t* box = boxes + turn * kBox;
+    turn ^= 1u;
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");     // the store before the last has left this memory
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -219,9 +224,10 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint8_t* box, 
 
 template <Product P, Form F>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xent_gemm_kernel(const __grid_constant__ XentParams p) {
+    constexpr int kStages = kStagesOf(P);
     extern __shared__ uint8_t raw[];
     uint8_t* tiles = raw + (1024 - smem_addr(raw) % 1024) % 1024;
-    GemmShared& sh = *reinterpret_cast<GemmShared*>(tiles + kStages * kStageBytes + kEpiWarps * kBox);
+    GemmShared& sh = *reinterpret_cast<GemmShared*>(tiles + kStages * kStageBytes + kEpiWarps * kBoxesOf(P) * kBox);
     volatile int* abort = &sh.abort;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_ctarank();
@@ -351,7 +357,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
         // ---------------------------------------------------------------- accumulators, by eight warps of each CTA
         const int quarter = warp % 4, half = warp / 4;
         const uint32_t empty0 = peer_smem_addr(&sh.acc_empty[0], 0), empty1 = peer_smem_addr(&sh.acc_empty[1], 0);
-        uint8_t* box = tiles + kStages * kStageBytes + warp * kBox;
+        uint8_t* boxes = tiles + kStages * kStageBytes + warp * kBoxesOf(P) * kBox;     // (two, taken in turn)
+        uint32_t box = 0u;
         int turn = 0;
         bool go = true;
         for (int64_t t = 0, i; (i = nth_unit(work, cluster, clusters, t)) >= 0; ++t) {
@@ -461,8 +468,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                             }
                         }
                     }
-                    store_box<false>(&p.s0, box, hi, col0 + c, row - lane, 0);
-                    if constexpr (kDlParts(F) > 1) store_box<false>(&p.s0, box, lo, col0 + c, row - lane, 1);
+                    store_box<false>(&p.s0, boxes, box, hi, col0 + c, row - lane, 0);
+                    if constexpr (kDlParts(F) > 1) store_box<false>(&p.s0, boxes, box, lo, col0 + c, row - lane, 1);
                 }
             } else {
                 constexpr bool F32 = F == Form::kSplit;
@@ -479,9 +486,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                         uint32_t w[32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(acc[c + j]);
-                        if (!u.job) store_box<false>(&p.s0, box, w, col0 + c, row - lane, 0);
-                        else if (p.add) store_box<true>(&p.s1, box, w, col0 + c, row - lane, u.split);
-                        else store_box<false>(&p.s1, box, w, col0 + c, row - lane, u.split);
+                        if (!u.job) store_box<false>(&p.s0, boxes, box, w, col0 + c, row - lane, 0);
+                        else if (p.add) store_box<true>(&p.s1, boxes, box, w, col0 + c, row - lane, u.split);
+                        else store_box<false>(&p.s1, boxes, box, w, col0 + c, row - lane, u.split);
                     }
                 } else if (!F32 && p.dw_wide) {
 #pragma unroll
@@ -490,7 +497,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                         uint32_t w[32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j) w[j] = pack_bf16(acc[c + 2 * j], acc[c + 2 * j + 1]);
-                        store_box<false>(&p.s0, box, w, col0 + c, row - lane, 0);
+                        store_box<false>(&p.s0, boxes, box, w, col0 + c, row - lane, 0);
                     }
                 } else if (row < p.Vp) {
                     using T = std::conditional_t<F32, float, __nv_bfloat16>;
@@ -611,7 +618,7 @@ __global__ void __launch_bounds__(kPrepThreads) xent_range_kernel(const PrepPara
 }
 
 // The rows that have a target, gathered in order: row i of x is row rows[i] of hidden.  A block has `per` rows of
-// hidden, at most one to a thread, and counts the targets before them itself; a warp packs a row at a time.
+// hidden, at most one to a thread, and counts the targets before them itself.
 template <typename T, bool BWD, bool RAW>
 __global__ void __launch_bounds__(kPrepThreads) xent_gather_kernel(const PrepParams p) {
     constexpr bool F32 = sizeof(T) == 4;
@@ -658,17 +665,18 @@ __global__ void __launch_bounds__(kPrepThreads) xent_gather_kernel(const PrepPar
         }
     }
     __syncthreads();
-    for (int r = warp; r < n; r += kWarps) {
+    const int chunks = (p.D + 255) / 256;          // of a row, one to a warp at a time
+    for (int q = warp; q < n * chunks; q += kWarps) {
+        const int r = q / chunks, c0 = (q - r * chunks) * 256;
         const int64_t t = first + r;
         const int i = to[r];
         if (i >= 0) {
-            const T* src = static_cast<const T*>(p.hidden) + t * p.hidden_t;
-            __half* dst = p.x + static_cast<int64_t>(i) * p.ld_x;
-#pragma unroll 2
-            for (int c = lane * 8; c < p.D; c += 256) pack8<T, RAW>(src, dst, p.x_part, c, p.D, p.wide, scale);
+            if (c0 + lane * 8 < p.D)
+                pack8<T, RAW>(static_cast<const T*>(p.hidden) + t * p.hidden_t, p.x + static_cast<int64_t>(i) * p.ld_x, p.x_part, c0 + lane * 8, p.D,
+                              p.wide, scale);
         } else if constexpr (BWD) {
             T* d = static_cast<T*>(p.dhidden) + t * p.dhidden_t;
-            for (int c = lane; c < p.D; c += 32) d[c] = from_f32<T>(0.f);
+            for (int c = c0 + lane; c < min(c0 + 256, p.D); c += 32) d[c] = from_f32<T>(0.f);
         }
     }
     if (first + n == p.T) {
@@ -705,60 +713,70 @@ __global__ void __launch_bounds__(kPrepThreads) xent_pack_kernel(const T* w, int
     if constexpr (!RAW && !AGAIN) block_max(m, most, range);
 }
 
-// lse and loss from the maxima and sums of the half tiles; a block has 32 rows, a warp a share of the tiles.
-constexpr int kJoinThreads = 1024;
+// lse and loss from the maxima and sums of the half tiles; a block has 8 rows, and 128 threads share a row's.
+constexpr int kJoinThreads = 1024, kJoinRows = 8;
 __global__ void __launch_bounds__(kJoinThreads) xent_join_kernel(const float2* part, int64_t ld, int halves, const int* count, const int* rows,
                                                                  const float* tl, float* loss, float* lse) {
-    constexpr int kWarps = kJoinThreads / 32, U = 16;
-    __shared__ float2 s[kWarps][33];
+    constexpr int kShares = kJoinThreads / kJoinRows, U = 8;
+    __shared__ float2 s[kJoinRows][kJoinThreads / 32];
     wait_for_earlier();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, n = *count;
-    const int row = blockIdx.x * 32 + lane;
+    const int mine = threadIdx.x % kJoinRows, row = blockIdx.x * kJoinRows + mine;
     float m = -INFINITY, sum = 0.f;
     auto join = [&](float2 q) {
         const float b = fmaxf(m, q.x), o = base_of(b);
         sum = sum * ex2((m - o) * kLog2e) + q.y * ex2((q.x - o) * kLog2e);
         m = b;
     };
-    if (blockIdx.x * 32 >= n) return;
-    if (row < n)
-        for (int i = warp; i < halves; i += kWarps * U) {
-            float2 q[U];
+    auto join_lane = [&](int o) { join(make_float2(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, sum, o))); };
+    if (blockIdx.x * kJoinRows >= n) return;
+    for (int i = threadIdx.x / kJoinRows; i < halves; i += kShares * U) {
+        float2 q[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) q[u] = i + u * kWarps < halves ? part[(i + u * kWarps) * ld + row] : make_float2(-INFINITY, 0.f);
+        for (int u = 0; u < U; ++u) q[u] = row < n && i + u * kShares < halves ? part[(i + u * kShares) * ld + row] : make_float2(-INFINITY, 0.f);
 #pragma unroll
-            for (int u = 0; u < U; ++u) join(q[u]);
-        }
-    s[warp][lane] = make_float2(m, sum);
+        for (int u = 0; u < U; ++u) join(q[u]);
+    }
+    join_lane(8);
+    join_lane(16);
+    if (lane < kJoinRows) s[mine][warp] = make_float2(m, sum);
     __syncthreads();
-    // a warp has a row now, a lane a share
-    const float2 q = s[lane][warp];
-    m = q.x;
-    sum = q.y;
+    if (warp >= kJoinRows) return;
+    // a warp has a row now
+    m = s[warp][lane].x;
+    sum = s[warp][lane].y;
 #pragma unroll
-    for (int o = 16; o > 0; o /= 2) join(make_float2(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, sum, o)));
-    const int mine = blockIdx.x * 32 + warp;
-    if (lane == 0 && mine < n) {
+    for (int o = 16; o > 0; o /= 2) join_lane(o);
+    const int i = blockIdx.x * kJoinRows + warp;
+    if (lane == 0 && i < n) {
         const float v = m + logf(sum);
-        const int t = rows[mine];
+        const int t = rows[i];
         lse[t] = v;
-        loss[t] = v - tl[mine];
+        loss[t] = v - tl[i];
     }
 }
 
-// dhidden's rows from their sums.
+// dhidden's rows from their sums; a thread has 4 columns at a time.
 template <typename T>
 __global__ void __launch_bounds__(kPrepThreads) xent_scatter_kernel(const float* dx, int64_t split_stride, int splits, int64_t ld, const int* count,
                                                                     const int* rows, T* dhidden, int64_t stride, int D) {
     wait_for_earlier();
-    const int n = *count;
-    for (int i = blockIdx.x; i < n; i += gridDim.x) {
-        T* out = dhidden + static_cast<int64_t>(rows[i]) * stride;
-        for (int c = threadIdx.x; c < D; c += kPrepThreads) {
-            float v = 0.f;
-            for (int s = 0; s < splits; ++s) v += dx[s * split_stride + i * ld + c];
-            out[c] = from_f32<T>(v);
+    const int n = *count, quads = (D + 3) / 4;
+    for (int64_t q = static_cast<int64_t>(blockIdx.x) * kPrepThreads + threadIdx.x; q < static_cast<int64_t>(n) * quads;
+         q += static_cast<int64_t>(gridDim.x) * kPrepThreads) {
+        const int i = static_cast<int>(q / quads), c = static_cast<int>(q - static_cast<int64_t>(i) * quads) * 4;
+        const float* from = dx + i * ld + c;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int s = 0; s < splits; ++s) {
+            const float4 a = __ldcs(reinterpret_cast<const float4*>(from + s * split_stride));
+            v = make_float4(v.x + a.x, v.y + a.y, v.z + a.z, v.w + a.w);
         }
+        T* out = dhidden + static_cast<int64_t>(rows[i]) * stride + c;
+        const float w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (c + j < D) out[j] = from_f32<T>(w[j]);
     }
 }
 
@@ -910,12 +928,12 @@ cudaError_t launch_gemm_as(const XentParams& p, int64_t units, cudaStream_t stre
     if (e != cudaSuccess) return e;
     int pairs = dev < 64 ? known[dev].load() : 0;
     if (pairs == 0) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kGemmSmem));
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(gemm_smem(P)));
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * sm_count());
         cfg.blockDim = dim3(kGemmThreads);
-        cfg.dynamicSmemBytes = kGemmSmem;
+        cfg.dynamicSmemBytes = gemm_smem(P);
         cudaLaunchAttribute at[1];
         at[0].id = cudaLaunchAttributeClusterDimension;
         at[0].val.clusterDim.x = 2;
@@ -928,7 +946,7 @@ cudaError_t launch_gemm_as(const XentParams& p, int64_t units, cudaStream_t stre
         if (dev < 64) known[dev].store(pairs);
     }
     const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(pairs, std::max<int64_t>(units, 1)));
-    return launch_chained(kern, dim3(grid), dim3(kGemmThreads), kGemmSmem, stream, p);
+    return launch_chained(kern, dim3(grid), dim3(kGemmThreads), gemm_smem(P), stream, p);
 }
 template <Product P>
 cudaError_t launch_gemm(const XentParams& p, Form form, int64_t units, cudaStream_t stream) {
@@ -1025,7 +1043,7 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
     PrepParams g;
     std::memset(&g, 0, sizeof(g));
     g.hidden = c.hidden; g.hidden_t = s.hidden_t; g.targets = c.targets; g.T = T; g.V = V; g.D = static_cast<int>(D);
-    g.per = static_cast<int>(std::min<int64_t>(kPrepThreads, std::max<int64_t>(8, T / 1024)));
+    g.per = static_cast<int>(std::min<int64_t>(kPrepThreads, std::max<int64_t>(1, T / 1024)));
     g.x = x; g.ld_x = q.ld_x; g.x_part = x_part; g.wide = wide(c.hidden, T > 1 ? s.hidden_t : 0);
     g.count = reinterpret_cast<int*>(ws + q.count); g.rows = reinterpret_cast<int*>(ws + q.rows); g.tgt = reinterpret_cast<int*>(ws + q.tgt);
     g.lse = c.lse_in; g.dloss = c.dloss; g.dloss_t = s.dloss_t; g.lse_c = f32_at(q.lse); g.g_c = f32_at(q.g);
@@ -1100,10 +1118,10 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
         if (launch_gemm<Product::kOut>(p, q.form, vt * dt + mt * dt * q.splits, st) != cudaSuccess) return SS_ERR_CUDA;
         ++p.piece;
     }
-    const unsigned rows_grid = static_cast<unsigned>(std::min<int64_t>(T, 8 * sm_count()));
+    const unsigned rows_grid = static_cast<unsigned>(std::min<int64_t>((T * ((D + 3) / 4) + kPrepThreads - 1) / kPrepThreads, 8 * sm_count()));
     cudaError_t e;
     if (!c.bwd)
-        e = launch_chained(xent_join_kernel, dim3(static_cast<unsigned>((T + 31) / 32)), dim3(kJoinThreads), 0, st, p.part, q.tpad,
+        e = launch_chained(xent_join_kernel, dim3(static_cast<unsigned>((T + kJoinRows - 1) / kJoinRows)), dim3(kJoinThreads), 0, st, p.part, q.tpad,
                            static_cast<int>(q.halves), g.count, g.rows, p.tl, c.loss, c.lse);
     else if (f32)
         e = launch_chained(xent_scatter_kernel<float>, dim3(rows_grid), prep, 0, st, p.dx, p.dx_split, p.splits, p.ld_dx, g.count, g.rows,
