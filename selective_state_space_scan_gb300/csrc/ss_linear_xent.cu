@@ -88,13 +88,6 @@ struct Pow2x2 {
     }
 };
 
-struct GemmShared {
-    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
-    uint32_t tmem;
-    int abort;
-};
-constexpr uint32_t kBox = 32 * 128;                // bytes of a warp's store: 32 rows of 128
-constexpr size_t gemm_smem(Product p) { return kStagesOf(p) * kStageBytes + kEpiWarps * kBoxesOf(p) * kBox + sizeof(GemmShared) + 1024; }
 
 // A unit of work: a tile and a range of steps of K (each of them kSegs products of parts).
 struct Unit {
@@ -109,6 +102,15 @@ struct Work {
     int64_t extra;                                // pairs that have one unit of the first job more than the others
     int64_t fill;                                 // units of the second job that each of the others has meanwhile
 };
+struct GemmShared {
+    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+    Work work;                                    // (here and not in registers, which the accumulators take up)
+    int rows, ex, ew, eg;                         // rows that have a target; the operands' scales
+    uint32_t tmem;
+    int abort;
+};
+constexpr uint32_t kBox = 32 * 128;                // bytes of a warp's store: 32 rows of 128
+constexpr size_t gemm_smem(Product p) { return kStagesOf(p) * kStageBytes + kEpiWarps * kBoxesOf(p) * kBox + sizeof(GemmShared) + 1024; }
 template <Product P>
 __device__ __forceinline__ Work make_work(const XentParams& p, int rows, int64_t pairs) {
     Work w = {};
@@ -251,16 +253,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
     tc_fence_after();
     cluster_sync_all();                            // the peer's barriers exist
     const uint32_t tmem = sh.tmem;
-    wait_for_earlier();
-    const int rows = *p.count;
-    const Work work = make_work<P>(p, rows, clusters);
-    int ex = 0, ew = 0, eg = 0;
     constexpr int kTable = F == Form::kSplit ? 0 : 1, kSegsHere = kSegs<P, F>;
-    if constexpr (F != Form::kRaw) {
-        ex = scale_exp(p.range[kRangeX]);
-        ew = weight_exp(p.range[kRangeW + p.piece]);
-        if constexpr (P != Product::kLoss) eg = scale_exp(p.range[kRangeG]);
+    wait_for_earlier();
+    if (threadIdx.x == 0) {
+        sh.rows = *p.count;
+        sh.work = make_work<P>(p, sh.rows, clusters);
+        sh.ex = sh.ew = sh.eg = 0;                 // (operands as they are)
+        if constexpr (F != Form::kRaw) {
+            sh.ex = scale_exp(p.range[kRangeX]);
+            sh.ew = weight_exp(p.range[kRangeW + p.piece]);
+            if constexpr (P != Product::kLoss) sh.eg = scale_exp(p.range[kRangeG]);
+        }
     }
+    __syncthreads();
+    const Work& work = sh.work;
 
     if (warp == kEpiWarps) {
         // ---------------------------------------------------------------- loads, by one thread of each CTA
@@ -373,11 +379,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                 tc_fence_after();
                 const uint32_t at = tmem + (turn & 1) * kAccCols + half * kHalf + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll
-                for (int c = 0; c < kHalf; c += 32) {
-                    uint32_t r[32];
-                    tc_ld32(at + c, r);
+                for (int c = 0; c < kHalf; c += 16) {
+                    uint32_t r[16];
+                    tc_ld16(at + c, r);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
+                    for (int j = 0; j < 16; j += 2) {
                         const float2 v = add2(make_float2(acc[c + j], acc[c + j + 1]), make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])));
                         acc[c + j] = v.x;
                         acc[c + j + 1] = v.y;
@@ -388,11 +394,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                 if (lane == 0) mbar_arrive_peer(turn & 1 ? empty1 : empty0);
             }
             if (!go) break;
+            const int rows = sh.rows;
             const int row = u.m * kTile + static_cast<int>(rank) * kHalf + quarter * 32 + lane;
             const int col0 = u.n * kTile + half * kHalf;
             if constexpr (P == Product::kLoss) {
                 if constexpr (F == Form::kSplit) {
-                    const Pow2x2 f(ex + ew);
+                    const Pow2x2 f(sh.ex + sh.ew);
 #pragma unroll
                     for (int j = 0; j < kHalf; ++j) acc[j] = acc[j] * f.a * f.b;
                 }
@@ -429,9 +436,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                 if (row < rows) p.part[(static_cast<int64_t>(p.tile0 + u.n) * 2 + half) * p.ld_part + row] = make_float2(m, s);
             } else if constexpr (P == Product::kGrad) {
                 const bool ok = row < rows;
-                const float lse = ok ? p.lse[row] : 0.f, g = ok ? (F == Form::kRaw ? p.g[row] : p.g[row] * pow2(-eg)) : 0.f;
+                const float lse = ok ? p.lse[row] : 0.f, g = ok ? (F == Form::kRaw ? p.g[row] : p.g[row] * pow2(-sh.eg)) : 0.f;
                 const int tgt = ok ? p.tgt[row] - p.v0 - col0 : -1;
-                const Pow2x2 f(ex + ew);
+                const Pow2x2 f(sh.ex + sh.ew);
                 const float2 off = splat2(-lse), f2 = splat2(f.a), l2e = splat2(kLog2e), g2 = splat2(g);
                 if (f.b != 1.f) {
 #pragma unroll
@@ -474,7 +481,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
             } else {
                 constexpr bool F32 = F == Form::kSplit;
                 if constexpr (F != Form::kRaw) {
-                    const Pow2x2 f(eg + (u.job ? ew : ex));
+                    const Pow2x2 f(sh.eg + (u.job ? sh.ew : sh.ex));
 #pragma unroll
                     for (int j = 0; j < kHalf; ++j) acc[j] = acc[j] * f.a * f.b;
                 }

@@ -30,6 +30,17 @@ __device__ __forceinline__ void pair_dealloc(uint32_t addr, uint32_t cols) {  //
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
 }
 
+// 16 columns of a warp's 32 lanes (see tc_ld32).
+__device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+        " tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+}
+
 // TMA tile into this CTA's shared memory, completing on a barrier of either CTA (`bar`: its address in the
 // cluster's window, from peer_smem_addr).
 __device__ __forceinline__ void pair_tma_load(void* dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2) {
