@@ -823,7 +823,7 @@ struct Layout {
 // Time of one launch of both products over a piece, in steps of K, when dhidden's are cut in `splits`: units as
 // nth_unit hands them out, each some steps longer for its end.
 int64_t out_cost(int64_t T, int64_t D, int64_t Vp, int64_t segs, int64_t splits, int64_t pairs) {
-    constexpr int64_t kEnd = 6;
+    constexpr int64_t kEnd = 4;
     const int64_t dt = (D + kTile - 1) / kTile;
     const int64_t len[2] = {(T + kStep - 1) / kStep * segs, ((Vp + kStep - 1) / kStep + splits - 1) / splits * segs};
     const int64_t n[2] = {(Vp + kTile - 1) / kTile * dt, (T + kTile - 1) / kTile * dt * splits};
