@@ -6,7 +6,8 @@
 //
 // A stream of three elements per step and channel: what counts is how much of it is on its way.  A thread has 2
 // channels (a packed pair) and a segment of steps; TMA brings the steps into a ring in shared memory (four stages of
-// 8 KB a CTA, 7 CTAs an SM), as loads into registers stayed behind at a third of that (4 x 8192 x 5120 bf16: 315 us).
+// 8 KB a CTA, 6 CTAs an SM).  4 x 8192 x 5120 bf16: 175 us, 5.8 TB/s, 0.85 of the copy rate (3 stages and 8 CTAs 177, 6 and 4
+// 173; loads into registers, the next steps' ahead, 315); 8 x 2048 x 1536 fp32: 56 us, 0.80; 45 steps: 6 us and 3 for the sums.
 // It runs three steps past its segment, whose g belong to its last outputs.  The weight's gradients are sums in
 // registers; every thread leaves its own in the workspace (a row of it per segment) and a second kernel adds the
 // rows up in the same order every time.  Layouts that TMA does not take go by plain loads.

@@ -5,10 +5,12 @@
 //
 // The vocabulary is the traffic, and it is read once: a row is shared out to the CTAs of a cluster so that each
 // keeps its slice (64 KB) in shared memory from the running maximum and sum to the gradient.  Bulk copies bring it,
-// three CTAs to an SM, so that an SM has some 190 KB under way or in use: a CTA's chain (entries, row, the cluster's
-// exchange, stores) is some 5 us long, and slices of 32 KB in registers left it at 0.44 of the copy rate.  (What
-// of a longer row does not fit is read again from L2.)  An entry's values lie in shared memory as well; their
-// columns get their gradient after the row's stream, rounded once, duplicates summed.
+// three CTAs to an SM, so that an SM has some 190 KB under way or in use while its CTAs are at different points of their
+// chain (entries, row, exchange of the sums, stores: some 12 us).  4096 rows of 128000 bf16: 390 us, 5.1 TB/s, 0.76 of
+// the copy rate.  Measured besides: slices of 32 KB in registers 663, of 32 KB in shared memory 438, clusters that
+// take rows in turn with the next one on its way 522, the cluster's own barrier for the exchange 428 (it waits for
+// stores).  What of a longer row does not fit is read again from L2.  An entry's values lie in shared memory as well;
+// their columns get their gradient after the row's stream, rounded once, duplicates summed.
 #include <cuda_runtime.h>
 
 #include <algorithm>
