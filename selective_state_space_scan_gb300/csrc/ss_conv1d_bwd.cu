@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) ss_conv1d_bwd_kernel(c
     __shared__ __align__(128) T tile[kStages][2][kTile];
     __shared__ uint64_t full[kStages];
     __shared__ int abort_flag;
+    let_next_start();                              // (the sums' kernel: it waits for this one's end)
     const Place q = place_of(p, true);
     const int tid = threadIdx.x, c0 = q.d0 - 2 * tid, n = (q.end - q.t0 + U - 1) / U;
     auto issue = [&](int i) {                      // (steps and channels outside the tensor are zeros)
@@ -211,13 +212,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) ss_conv1d_bwd_kernel(c
         }
         if (tid == 0 && i + kStages < n) issue(i + kStages);
     }
-    let_next_start();
     c.leave(p, q);
 }
 
 template <typename T, bool SILU>
 __global__ void __launch_bounds__(kThreads) ss_conv1d_bwd_plain_kernel(const ConvBwdParams p) {
     constexpr int U = 4;                           // steps whose loads are issued together
+    let_next_start();
     const Place q = place_of(p, false);
     if (!q.one) return;                            // (an ended thread lets the next kernel start as well)
     Pair<T, SILU> c;
@@ -249,7 +250,6 @@ __global__ void __launch_bounds__(kThreads) ss_conv1d_bwd_plain_kernel(const Con
             }
         }
     }
-    let_next_start();
     c.leave(p, q);
 }
 

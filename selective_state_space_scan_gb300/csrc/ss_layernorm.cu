@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(512) layernorm_bwd_kernel(const LnParams p) {
     const Cols<VEC> c{p.D, static_cast<int>(blockDim.x), static_cast<int>(threadIdx.x)};
     ColsRaw<TIO, VEC> rdy[K];
     ColsRaw<TR, VEC> rr[K], rdr[K];
+    let_next_start();                              // (the sums' kernel: it waits for this one's end)
     float next_mean, next_rstd;
     auto load_row = [&](int64_t row) {
         const TIO* dy = static_cast<const TIO*>(p.x) + row * p.x_r;
@@ -259,7 +260,6 @@ __global__ void __launch_bounds__(512) layernorm_bwd_kernel(const LnParams p) {
             if (dres) store_cols<TR, VEC>(dres, c, k, a[k]);
         }
     }
-    let_next_start();
     float* mine = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.D;
 #pragma unroll
     for (int k = 0; k < K; ++k)

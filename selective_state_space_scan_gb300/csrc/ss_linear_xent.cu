@@ -374,6 +374,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
         bool go = true;
         for (int64_t t = 0, i; (i = nth_unit(work, cluster, clusters, t)) >= 0; ++t) {
             const Unit u = unit_of<P>(work, i);
+            const int rows = sh.rows;
+            const int row = u.m * kTile + static_cast<int>(rank) * kHalf + quarter * 32 + lane;
+            const int col0 = u.n * kTile + half * kHalf;
+            // what the row's end needs is on its way meanwhile
+            int tgt = -1;
+            float lse = 0.f, g = 0.f;
+            if (P != Product::kOut && row < rows) {
+                tgt = p.tgt[row] - p.v0 - col0;
+                if constexpr (P == Product::kGrad) {
+                    lse = p.lse[row];
+                    g = p.g[row];
+                }
+            }
             float acc[kHalf];                      // a thread has half a row of the tile
 #pragma unroll
             for (int j = 0; j < kHalf; ++j) acc[j] = 0.f;
@@ -399,9 +412,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                 if (lane == 0) mbar_arrive_peer(turn & 1 ? empty1 : empty0);
             }
             if (!go) break;
-            const int rows = sh.rows;
-            const int row = u.m * kTile + static_cast<int>(rank) * kHalf + quarter * 32 + lane;
-            const int col0 = u.n * kTile + half * kHalf;
             if constexpr (P == Product::kLoss) {
                 if constexpr (F == Form::kSplit) {
                     const Pow2x2 f(sh.ex + sh.ew);
@@ -409,7 +419,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                     for (int j = 0; j < kHalf; ++j) acc[j] = acc[j] * f.a * f.b;
                 }
                 float m = -INFINITY, s = 0.f;
-                const int tgt = row < rows ? p.tgt[row] - p.v0 - col0 : -1;
 #pragma unroll
                 for (int c = 0; c < kHalf; c += 32) {
                     const int n = p.Vp - col0 - c;
@@ -440,9 +449,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                 }
                 if (row < rows) p.part[(static_cast<int64_t>(p.tile0 + u.n) * 2 + half) * p.ld_part + row] = make_float2(m, s);
             } else if constexpr (P == Product::kGrad) {
-                const bool ok = row < rows;
-                const float lse = ok ? p.lse[row] : 0.f, g = ok ? (F == Form::kRaw ? p.g[row] : p.g[row] * pow2(-sh.eg)) : 0.f;
-                const int tgt = ok ? p.tgt[row] - p.v0 - col0 : -1;
+                const bool ok = row < rows, all_ok = __all_sync(0xffffffffu, ok);
+                if constexpr (F != Form::kRaw) g *= pow2(-sh.eg);
                 const Pow2x2 f(sh.ex + sh.ew);
                 const float2 off = splat2(-lse), f2 = splat2(f.a), l2e = splat2(kLog2e), g2 = splat2(g);
                 if (f.b != 1.f) {
@@ -469,7 +477,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             e[j] = mul2(e[j], g2);
-                            if (!ok) e[j] = splat2(0.f);
+                            if (!all_ok && !ok) e[j] = splat2(0.f);      // (a row past the last may hold anything)
                             if constexpr (F == Form::kRaw) {
                                 hi[q / 2 + j] = pack_bf16(e[j].x, e[j].y);
                                 lo[q / 2 + j] = pack_rest(e[j], hi[q / 2 + j]);
