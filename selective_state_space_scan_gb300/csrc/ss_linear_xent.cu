@@ -1100,6 +1100,7 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
     p.lse = g.lse_c; p.g = g.g_c;
     p.dw = c.dweight; p.ld_dw = s.dweight_v; p.dw_wide = c.bwd && wide(c.dweight, s.dweight_v);
     p.dx = f32_at(q.dx); p.ld_dx = q.ld_dx; p.dx_split = q.tpad * q.ld_dx; p.splits = static_cast<int>(q.splits);
+    const int64_t rows = round_up(T, kStep);
     const int64_t mt = (T + kTile - 1) / kTile, dt = (D + kTile - 1) / kTile;
     for (int64_t v0 = 0; v0 < V; v0 += q.piece) {
         const int64_t Vp = std::min(q.piece, V - v0), vt = (Vp + kTile - 1) / kTile;
@@ -1122,8 +1123,9 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
         }
         p.v0 = static_cast<int>(v0);
         p.Vp = static_cast<int>(Vp);
-        // logits: rows of x and of weight, K along the columns
-        if (!make_map(&p.a0, x, 2, D, q.tpad, q.parts, q.ld_x, x_part, kHalf) || !make_map(&p.b0, wp, 2, D, Vp, q.parts, ld_w, w_part, kHalf))
+        // logits: rows of x and of weight, K along the columns.  (The maps have T rows up to a step of K, not whole
+        // tiles of them: what is behind costs no traffic, which for few tokens would be most of it.)
+        if (!make_map(&p.a0, x, 2, D, rows, q.parts, q.ld_x, x_part, kHalf) || !make_map(&p.b0, wp, 2, D, Vp, q.parts, ld_w, w_part, kHalf))
             return SS_ERR_CUDA;
         if (!c.bwd) {
             if (launch_gemm<Product::kLoss>(p, q.form, mt * vt, st) != cudaSuccess) return SS_ERR_CUDA;
@@ -1131,13 +1133,13 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
             ++p.piece;
             continue;
         }
-        if (!make_map(&p.s0, dl, 2, Vp, q.tpad, q.dl_parts, q.ld_dl, dl_part, 32)) return SS_ERR_CUDA;
+        if (!make_map(&p.s0, dl, 2, Vp, rows, q.dl_parts, q.ld_dl, dl_part, 32)) return SS_ERR_CUDA;
         if (launch_gemm<Product::kGrad>(p, q.form, mt * vt, st) != cudaSuccess) return SS_ERR_CUDA;
         // dweight: dl and x with the tokens along rows; dhidden: dl with K along columns, weight with K along rows
         char* dw = static_cast<char*>(c.dweight) + v0 * s.dweight_v * es;
-        if (!make_map(&p.a0, dl, 2, Vp, q.tpad, q.dl_parts, q.ld_dl, dl_part, kStep) || !make_map(&p.b0, x, 2, D, q.tpad, q.parts, q.ld_x, x_part, kStep) ||
-            !make_map(&p.a1, dl, 2, Vp, q.tpad, q.dl_parts, q.ld_dl, dl_part, kHalf) || !make_map(&p.b1, wp, 2, D, Vp, q.parts, ld_w, w_part, kStep) ||
-            !make_map(&p.s1, p.dx, 4, D, q.tpad, q.splits, q.ld_dx, p.dx_split, 32) ||
+        if (!make_map(&p.a0, dl, 2, Vp, rows, q.dl_parts, q.ld_dl, dl_part, kStep) || !make_map(&p.b0, x, 2, D, rows, q.parts, q.ld_x, x_part, kStep) ||
+            !make_map(&p.a1, dl, 2, Vp, rows, q.dl_parts, q.ld_dl, dl_part, kHalf) || !make_map(&p.b1, wp, 2, D, Vp, q.parts, ld_w, w_part, kStep) ||
+            !make_map(&p.s1, p.dx, 4, D, rows, q.splits, q.ld_dx, p.dx_split, 32) ||
             (p.dw_wide && !make_map(&p.s0, dw, es, D, Vp, 1, s.dweight_v, 0, 32)))
             return SS_ERR_CUDA;
         p.add = v0 > 0;
