@@ -255,18 +255,20 @@ __global__ void __launch_bounds__(kThreads) ss_conv1d_bwd_plain_kernel(const Con
 
 // Steps per thread for batch · ceil(L / seg) · nbd blocks when `slots` are resident at once: the length whose
 // waves take the least time, a block taking seg + kSetup steps' worth (the three steps past its end, the
-// weights, and the sums' way out).
-constexpr int kSetup = 10;
+// weights, and the sums' way out).  For a number of waves the most segments that fit are the best, so only those are
+// looked at (looking at every number of segments took 27 us of the host's time for 32768 steps of 768 channels).
+constexpr int kSetup = 10, kMoreWaves = 8;
 int segment_steps(int64_t batch, int64_t L, int64_t nbd, int64_t slots) {
+    const int64_t per = batch * nbd, first = (per + slots - 1) / slots;
     int64_t best = L, best_cost = -1;
-    for (int64_t segs = 1; segs <= std::max<int64_t>(L / kSegMin, 1); ++segs) {
-        const int64_t seg = (L + segs - 1) / segs, blocks = batch * ((L + seg - 1) / seg) * nbd;
+    for (int64_t waves = first; waves < first + kMoreWaves; ++waves) {
+        const int64_t segs = std::min(waves * slots / per, std::max<int64_t>(L / kSegMin, 1));
+        const int64_t seg = (L + segs - 1) / segs, blocks = per * ((L + seg - 1) / seg);
         const int64_t cost = (blocks + slots - 1) / slots * (seg + kSetup);
         if (best_cost < 0 || cost < best_cost) {
             best_cost = cost;
             best = seg;
         }
-        if (blocks > 8 * slots) break;
     }
     return static_cast<int>(best);
 }
