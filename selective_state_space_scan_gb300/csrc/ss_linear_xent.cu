@@ -71,6 +71,8 @@ template <Product P, Form F> constexpr int kChain = F == Form::kSplit ? 4 : P ==
 template <Product P, Form F> constexpr int kSegs = F == Form::kSplit ? 3 : F == Form::kRaw && P == Product::kOut ? 2 : 1;
 __constant__ int8_t kPartA[2][3] = {{0, 1, 0}, {1, 0, 0}};
 __constant__ int8_t kPartB[2][3] = {{1, 0, 0}, {0, 0, 0}};
+// Those of dhidden's when dl's two parts are in the rows of a pair's two CTAs: one for each part of weight, the small one first.
+template <Form F> constexpr int kSegsPaired = F == Form::kSplit ? 2 : 1;
 constexpr int kDlParts(Form f) { return f == Form::kHalf ? 1 : 2; }
 
 // Exponent n of the power of two that a tensor's values are divided by, from the bits of its largest finite one: what
@@ -117,7 +119,7 @@ struct GemmShared {
 };
 constexpr uint32_t kBox = 32 * 128;                // bytes of a warp's store: 32 rows of 128
 constexpr size_t gemm_smem(Product p) { return kStagesOf(p) * kStageBytes + kEpiWarps * kBoxesOf(p) * kBox + sizeof(GemmShared) + 1024; }
-template <Product P>
+template <Product P, Form F>
 __device__ __forceinline__ Work make_work(const XentParams& p, int rows, int64_t pairs) {
     Work w = {};
     const int dt = (p.D + kTile - 1) / kTile, vt = (p.Vp + kTile - 1) / kTile, rt = (rows + kTile - 1) / kTile;
@@ -135,13 +137,13 @@ __device__ __forceinline__ Work make_work(const XentParams& p, int rows, int64_t
     w.steps0 = (rows + kStep - 1) / kStep;
     w.steps1 = (p.Vp + kStep - 1) / kStep;
     w.per = (w.steps1 + p.splits - 1) / p.splits;
-    w.first = w.per > w.steps0 ? 1 : 0;           // the longer units first, so that the shorter ones fill up
+    const int l0 = w.steps0 * kSegs<P, F>, l1 = w.per * (p.paired ? kSegsPaired<F> : kSegs<P, F>);
+    w.first = l1 > l0 ? 1 : 0;                    // the longer units first, so that the shorter ones fill up
     const int64_t a = static_cast<int64_t>(vt) * dt, b = static_cast<int64_t>(rt) * dt * p.splits;
     w.n0 = w.first ? b : a;
     w.total = a + b;
     w.extra = w.n0 % pairs;
-    const int short_one = w.first ? w.steps0 : w.per, long_one = w.first ? w.per : w.steps0;
-    w.fill = w.extra > 0 ? long_one / max(short_one, 1) : 0;
+    w.fill = w.extra > 0 ? max(l0, l1) / max(min(l0, l1), 1) : 0;
     return w;
 }
 // The i-th unit of a pair of CTAs, or -1: units of the first job in turn, then those of the second, of which the
@@ -186,6 +188,12 @@ __device__ __forceinline__ Unit unit_of(const Work& w, int64_t i) {
     u.k0 = u.job ? u.split * w.per : 0;
     u.k1 = u.job ? min(u.k0 + w.per, w.steps1) : w.steps0;
     return u;
+}
+
+// Whether a unit's tile has dl's high part in one CTA's rows and its low part in the other's (each a slice of sums).
+template <Product P, Form F>
+__device__ __forceinline__ bool is_paired(const XentParams& p, const Unit& u) {
+    return P == Product::kOut && F != Form::kHalf && u.job && p.paired;
 }
 
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
@@ -263,7 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
     wait_for_earlier();
     if (threadIdx.x == 0) {
         sh.rows = *p.count;
-        sh.work = make_work<P>(p, sh.rows, clusters);
+        sh.work = make_work<P, F>(p, sh.rows, clusters);
         sh.ex = sh.ew = sh.eg = 0;                 // (operands as they are)
         if constexpr (F != Form::kRaw) {
             sh.ex = scale_exp(p.range[kRangeX]);
@@ -288,11 +296,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                 const CUtensorMap* mb = u.job ? &p.b1 : &p.b0;
                 // dweight: both operands have K (the tokens) along rows; dhidden: weight has K (the vocabulary) along rows
                 const bool a_mn = P == Product::kOut && u.job == 0, b_mn = P == Product::kOut;
-                const int am = u.m * kTile + static_cast<int>(rank) * kHalf, bn = u.n * kTile + static_cast<int>(rank) * kHalf;
+                const bool both = is_paired<P, F>(p, u);
+                const int am = both ? 0 : u.m * kTile + static_cast<int>(rank) * kHalf, bn = u.n * kTile + static_cast<int>(rank) * kHalf;
+                const int segs = both ? kSegsPaired<F> : kSegsHere;
                 bool go = true;
                 for (int kc = u.k0; kc < u.k1 && go; kc += kChain<P, F>)
-                    for (int seg = 0; seg < kSegsHere && go; ++seg) {
-                        const int pa = kSegsHere > 1 ? kPartA[kTable][seg] : 0, pb = kSegsHere > 1 ? kPartB[kTable][seg] : 0;
+                    for (int seg = 0; seg < segs && go; ++seg) {
+                        const int pa = both ? static_cast<int>(rank) : kSegsHere > 1 ? kPartA[kTable][seg] : 0;
+                        const int pb = both ? segs - 1 - seg : kSegsHere > 1 ? kPartB[kTable][seg] : 0;
                         for (int k = kc; k < min(kc + kChain<P, F>, u.k1); ++k) {
                             go = mbar_wait_bounded(&sh.empty[st], ph ^ 1, abort, p.err);
                             if (!go) break;
@@ -344,7 +355,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                 const uint32_t la = a_mn ? kOperand / 2 : 16, lb = b_mn ? kOperand / 2 : 16, ka = a_mn ? 2048 : 32, kb = b_mn ? 2048 : 32;
                 for (int kc = u.k0; kc < u.k1 && go; kc += kChain<P, F>, ++turn) {
                     const uint32_t d = tmem + (turn & 1) * kAccCols;
-                    const int n = (min(kc + kChain<P, F>, u.k1) - kc) * kSegsHere;
+                    const int n = (min(kc + kChain<P, F>, u.k1) - kc) * (is_paired<P, F>(p, u) ? kSegsPaired<F> : kSegsHere);
                     go = mbar_wait_bounded(&sh.acc_empty[turn & 1], ((turn >> 1) & 1) ^ 1, abort, p.err);
                     tc_fence_after();
                     for (int k = 0; k < n && go; ++k) {
@@ -501,6 +512,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                 }
                 if (u.job || (F32 && p.dw_wide)) {
                     // rows of 32 floats
+                    const bool both = is_paired<P, F>(p, u);
+                    const int row0 = both ? quarter * 32 : row - lane, slice = both ? 2 * u.split + static_cast<int>(rank) : u.split;
 #pragma unroll
                     for (int c = 0; c < kHalf; c += 32) {
                         if (col0 + c >= p.D) break;
@@ -508,8 +521,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
 #pragma unroll
                         for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(acc[c + j]);
                         if (!u.job) store_box<false>(&p.s0, boxes, box, w, col0 + c, row - lane, 0);
-                        else if (p.add) store_box<true>(&p.s1, boxes, box, w, col0 + c, row - lane, u.split);
-                        else store_box<false>(&p.s1, boxes, box, w, col0 + c, row - lane, u.split);
+                        else if (p.add) store_box<true>(&p.s1, boxes, box, w, col0 + c, row0, slice);
+                        else store_box<false>(&p.s1, boxes, box, w, col0 + c, row0, slice);
                     }
                 } else if (!F32 && p.dw_wide) {
 #pragma unroll
@@ -833,18 +846,19 @@ int sm_count() {
 
 // Where everything lies in the workspace.
 struct Layout {
-    int64_t parts, dl_parts, segs, ld_x, tpad, piece, pieces, splits, ld_dl, ld_dx, halves;
+    int64_t parts, dl_parts, segs, ld_x, tpad, piece, pieces, splits, slices, ld_dl, ld_dx, halves;
     Form form;
     bool packed;                                  // weight, piece by piece
+    bool paired;                                  // dhidden: dl's two parts as the rows of a pair's two CTAs
     size_t count, range, rows, tgt, lse, g, tl, part, x, w, dl, dx, total;
 };
 
 // Time of one launch of both products over a piece, in steps of K, when dhidden's are cut in `splits`: units as
 // nth_unit hands them out, each some steps longer for its end.
-int64_t out_cost(int64_t T, int64_t D, int64_t Vp, int64_t segs, int64_t splits, int64_t pairs) {
+int64_t out_cost(int64_t T, int64_t D, int64_t Vp, int64_t segs, int64_t segs1, bool paired, int64_t splits, int64_t pairs) {
     constexpr int64_t kEnd = 4;
     const int64_t dt = (D + kTile - 1) / kTile;
-    const int64_t len[2] = {(T + kStep - 1) / kStep * segs, ((Vp + kStep - 1) / kStep + splits - 1) / splits * segs};
+    const int64_t len[2] = {(T + kStep - 1) / kStep * segs, ((Vp + kStep - 1) / kStep + splits - 1) / splits * segs1};
     const int64_t n[2] = {(Vp + kTile - 1) / kTile * dt, (T + kTile - 1) / kTile * dt * splits};
     const int first = len[1] > len[0] ? 1 : 0;
     const int64_t a = n[first], b = n[1 - first], la = len[first] + kEnd, lb = len[1 - first] + kEnd;
@@ -854,7 +868,7 @@ int64_t out_cost(int64_t T, int64_t D, int64_t Vp, int64_t segs, int64_t splits,
     const int64_t with_extra = (a / pairs + (extra ? 1 : 0)) * la + (rounds - (extra && rest <= others ? 1 : 0)) * lb;
     const int64_t without = a / pairs * la + ((filled + others - 1) / others + rounds) * lb;
     // a slice of sums more: its bytes out and in again, some 2 MB of them to a step's time (0.3 us at 6.8 TB/s)
-    return std::max(with_extra, without) + splits * T * D * 8 / (2 << 20);
+    return std::max(with_extra, without) + splits * (paired ? 2 : 1) * T * D * 8 / (2 << 20);
 }
 
 Layout layout(int64_t T, int64_t V, int64_t D, bool f32, bool in_place, bool bwd) {
@@ -865,6 +879,9 @@ Layout layout(int64_t T, int64_t V, int64_t D, bool f32, bool in_place, bool bwd
     q.parts = f32 ? 2 : 1;
     q.dl_parts = kDlParts(q.form);
     q.segs = f32 ? kSegs<Product::kOut, Form::kSplit> : q.form == Form::kRaw ? kSegs<Product::kOut, Form::kRaw> : 1;
+    // (the low part would take another pass over weight's tiles: backward of 64 tokens, 2048 x 128000 bf16 429 us, 357
+    // paired, fp32 1175 and 1074; 128 tokens, 768 x 50257 bf16 93 and 88)
+    q.paired = bwd && q.form != Form::kHalf && T <= kHalf;
     q.ld_x = round_up(D, 8);
     q.tpad = round_up(T, kTile);
     const int64_t per_col = std::max(bwd ? q.tpad * 2 * q.dl_parts : 0, packed ? q.ld_x * 2 * q.parts : 0);
@@ -881,16 +898,17 @@ Layout layout(int64_t T, int64_t V, int64_t D, bool f32, bool in_place, bool bwd
     q.ld_dx = round_up(D, 4);
     q.splits = 1;
     if (bwd) {
-        const int64_t pairs = sm_count() / 2;
+        const int64_t pairs = sm_count() / 2, segs1 = !q.paired ? q.segs : f32 ? kSegsPaired<Form::kSplit> : kSegsPaired<Form::kRaw>;
         int64_t best = -1;
         for (int64_t s = 1; s <= kMaxSplits && (s == 1 || (q.piece / kStep / s >= kMinSteps && s * q.tpad * q.ld_dx * 4 <= kPieceBytes)); ++s) {
-            const int64_t c = out_cost(T, D, q.piece, q.segs, s, pairs);
+            const int64_t c = out_cost(T, D, q.piece, q.segs, segs1, q.paired, s, pairs);
             if (best < 0 || c < best) {
                 best = c;
                 q.splits = s;
             }
         }
     }
+    q.slices = q.splits * (q.paired ? 2 : 1);
     size_t at = 0;
     auto take = [&](int64_t bytes) {
         const size_t o = at;
@@ -912,7 +930,7 @@ Layout layout(int64_t T, int64_t V, int64_t D, bool f32, bool in_place, bool bwd
     if (packed) q.w = take(2 * q.parts * q.piece * q.ld_x);
     if (bwd) {
         q.dl = take(2 * q.dl_parts * q.tpad * q.ld_dl);
-        q.dx = take(4 * q.splits * q.tpad * q.ld_dx);
+        q.dx = take(4 * q.slices * q.tpad * q.ld_dx);
     }
     q.total = at;
     return q;
@@ -1099,7 +1117,7 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
     p.part = reinterpret_cast<float2*>(ws + q.part); p.ld_part = q.tpad; p.tl = f32_at(q.tl);
     p.lse = g.lse_c; p.g = g.g_c;
     p.dw = c.dweight; p.ld_dw = s.dweight_v; p.dw_wide = c.bwd && wide(c.dweight, s.dweight_v);
-    p.dx = f32_at(q.dx); p.ld_dx = q.ld_dx; p.dx_split = q.tpad * q.ld_dx; p.splits = static_cast<int>(q.splits);
+    p.dx = f32_at(q.dx); p.ld_dx = q.ld_dx; p.dx_split = q.tpad * q.ld_dx; p.splits = static_cast<int>(q.splits); p.paired = q.paired;
     const int64_t rows = round_up(T, kStep);
     const int64_t mt = (T + kTile - 1) / kTile, dt = (D + kTile - 1) / kTile;
     for (int64_t v0 = 0; v0 < V; v0 += q.piece) {
@@ -1139,7 +1157,7 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
         char* dw = static_cast<char*>(c.dweight) + v0 * s.dweight_v * es;
         if (!make_map(&p.a0, dl, 2, Vp, rows, q.dl_parts, q.ld_dl, dl_part, kStep) || !make_map(&p.b0, x, 2, D, rows, q.parts, q.ld_x, x_part, kStep) ||
             !make_map(&p.a1, dl, 2, Vp, rows, q.dl_parts, q.ld_dl, dl_part, kHalf) || !make_map(&p.b1, wp, 2, D, Vp, q.parts, ld_w, w_part, kStep) ||
-            !make_map(&p.s1, p.dx, 4, D, rows, q.splits, q.ld_dx, p.dx_split, 32) ||
+            !make_map(&p.s1, p.dx, 4, D, rows, q.slices, q.ld_dx, p.dx_split, 32) ||
             (p.dw_wide && !make_map(&p.s0, dw, es, D, Vp, 1, s.dweight_v, 0, 32)))
             return SS_ERR_CUDA;
         p.add = v0 > 0;
@@ -1152,10 +1170,10 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
         e = launch_chained(xent_join_kernel, dim3(static_cast<unsigned>((T + kJoinRows - 1) / kJoinRows)), dim3(kJoinThreads), 0, st, p.part, q.tpad,
                            static_cast<int>(q.halves), g.count, g.rows, p.tl, c.loss, c.lse);
     else if (f32)
-        e = launch_chained(xent_scatter_kernel<float>, dim3(rows_grid), prep, 0, st, p.dx, p.dx_split, p.splits, p.ld_dx, g.count, g.rows,
+        e = launch_chained(xent_scatter_kernel<float>, dim3(rows_grid), prep, 0, st, p.dx, p.dx_split, static_cast<int>(q.slices), p.ld_dx, g.count, g.rows,
                            static_cast<float*>(c.dhidden), s.dhidden_t, p.D);
     else
-        e = launch_chained(xent_scatter_kernel<__nv_bfloat16>, dim3(rows_grid), prep, 0, st, p.dx, p.dx_split, p.splits, p.ld_dx, g.count, g.rows,
+        e = launch_chained(xent_scatter_kernel<__nv_bfloat16>, dim3(rows_grid), prep, 0, st, p.dx, p.dx_split, static_cast<int>(q.slices), p.ld_dx, g.count, g.rows,
                            static_cast<__nv_bfloat16*>(c.dhidden), s.dhidden_t, p.D);
     return e == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }

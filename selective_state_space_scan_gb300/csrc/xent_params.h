@@ -42,9 +42,10 @@ struct XentParams {
     void* dw;
     int64_t ld_dw;
     bool dw_wide;               // rows begin on 16-byte boundaries: stored by s0
-    float* dx;                  // [split][row][ld_dx]
+    float* dx;                  // [slice][row][ld_dx]
     int64_t ld_dx, dx_split;
-    int splits;
+    int splits;                 // slices of K that dhidden is summed in (paired: each of them twice, of dl's parts)
+    bool paired;                // dl's high part is in one CTA's rows of a tile, its low part in the other's
     bool add;                   // dx has the earlier pieces' sums
 };
 
