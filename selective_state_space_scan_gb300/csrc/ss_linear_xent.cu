@@ -106,10 +106,12 @@ struct Unit {
 // dhidden (rows: the tokens) in slices of K.
 struct Work {
     int mt0, mt1, nt, steps0, steps1, per, first;
-    int64_t n0, total;                            // units of the job that is first, and of both
-    int64_t extra;                                // pairs that have one unit of the first job more than the others
-    int64_t fill;                                 // units of the second job that each of the others has meanwhile
+    int n0, total;                                // units of the job that is first, and of both (fewer than 2^31: the host sees to it)
+    int full;                                     // of the first job that every pair has
+    int extra;                                    // pairs that have one unit of the first job more than the others
+    int fill, filled;                             // units of the second job that each of the others has meanwhile, and all of these
 };
+
 struct GemmShared {
     uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
     Work work;                                    // (here and not in registers, which the accumulators take up)
@@ -120,14 +122,15 @@ struct GemmShared {
 constexpr uint32_t kBox = 32 * 128;                // bytes of a warp's store: 32 rows of 128
 constexpr size_t gemm_smem(Product p) { return kStagesOf(p) * kStageBytes + kEpiWarps * kBoxesOf(p) * kBox + sizeof(GemmShared) + 1024; }
 template <Product P, Form F>
-__device__ __forceinline__ Work make_work(const XentParams& p, int rows, int64_t pairs) {
+__device__ __forceinline__ Work make_work(const XentParams& p, int rows, int pairs) {
     Work w = {};
     const int dt = (p.D + kTile - 1) / kTile, vt = (p.Vp + kTile - 1) / kTile, rt = (rows + kTile - 1) / kTile;
     if (P != Product::kOut) {
         w.mt0 = rt;
         w.nt = vt;
         w.steps0 = (p.D + kStep - 1) / kStep;
-        w.n0 = w.total = static_cast<int64_t>(rt) * vt;
+        w.n0 = w.total = rt * vt;
+        w.full = w.n0 / pairs;
         w.extra = w.n0 % pairs;
         return w;
     }
@@ -139,36 +142,39 @@ __device__ __forceinline__ Work make_work(const XentParams& p, int rows, int64_t
     w.per = (w.steps1 + p.splits - 1) / p.splits;
     const int l0 = w.steps0 * kSegs<P, F>, l1 = w.per * (p.paired ? kSegsPaired<F> : kSegs<P, F>);
     w.first = l1 > l0 ? 1 : 0;                    // the longer units first, so that the shorter ones fill up
-    const int64_t a = static_cast<int64_t>(vt) * dt, b = static_cast<int64_t>(rt) * dt * p.splits;
+    const int a = vt * dt, b = rt * dt * p.splits;
     w.n0 = w.first ? b : a;
     w.total = a + b;
+    w.full = w.n0 / pairs;
     w.extra = w.n0 % pairs;
     w.fill = w.extra > 0 ? max(l0, l1) / max(min(l0, l1), 1) : 0;
+    w.filled = static_cast<int>(min(static_cast<int64_t>(w.fill) * (pairs - w.extra), static_cast<int64_t>(w.total - w.n0)));
     return w;
 }
 // The i-th unit of a pair of CTAs, or -1: units of the first job in turn, then those of the second, of which the
 // pairs that have one of the first less get as many more as that one's length allows.
-__device__ __forceinline__ int64_t nth_unit(const Work& w, int64_t pair, int64_t pairs, int64_t i) {
-    const int64_t full = w.n0 / pairs, n = full + (pair < w.extra ? 1 : 0);
+__device__ __forceinline__ int nth_unit(const Work& w, int pair, int pairs, int i) {
+    const int n = w.full + (pair < w.extra ? 1 : 0);
     if (i < n) return pair + i * pairs;
     i -= n;
-    const int64_t others = pairs - w.extra, filled = min(w.fill * others, w.total - w.n0);
-    int64_t at;
-    if (pair >= w.extra && i < w.fill && (pair - w.extra) + i * others < filled) {
-        at = (pair - w.extra) + i * others;
+    const int others = pairs - w.extra;
+    int at;
+    if (pair < w.extra) {
+        at = w.filled + others + pair + i * pairs;
+    } else if (i < w.fill && pair - w.extra + i * others < w.filled) {
+        at = pair - w.extra + i * others;
     } else {
-        if (pair >= w.extra) i -= (filled - (pair - w.extra) + others - 1) / others;
-        at = filled + (pair >= w.extra ? pair - w.extra : others + pair) + i * pairs;
+        i -= (w.filled - (pair - w.extra) + others - 1) / others;
+        at = w.filled + pair - w.extra + i * pairs;
     }
     return at < w.total - w.n0 ? w.n0 + at : -1;
 }
 template <Product P>
-__device__ __forceinline__ Unit unit_of(const Work& w, int64_t i) {
+__device__ __forceinline__ Unit unit_of(const Work& w, int i) {
     Unit u;
     if (P != Product::kOut) {
         // the row tiles of a group take each tile of the vocabulary at the same time: it is read once
-        const int64_t per_group = static_cast<int64_t>(kGroup) * w.nt;
-        const int g = static_cast<int>(i / per_group), r = static_cast<int>(i - g * per_group);
+        const int per_group = kGroup * w.nt, g = i / per_group, r = i - g * per_group;
         const int size = min(kGroup, w.mt0 - g * kGroup);
         u.job = 0;
         u.m = g * kGroup + r % size;
@@ -179,12 +185,11 @@ __device__ __forceinline__ Unit unit_of(const Work& w, int64_t i) {
         return u;
     }
     u.job = i < w.n0 ? w.first : 1 - w.first;
-    const int64_t at = i < w.n0 ? i : i - w.n0;
-    const int64_t r = at / w.nt;
-    u.n = static_cast<int>(at - r * w.nt);
+    const int at = i < w.n0 ? i : i - w.n0, r = at / w.nt;
+    u.n = at - r * w.nt;
     const int mt = u.job ? w.mt1 : w.mt0;
-    u.split = u.job ? static_cast<int>(r / mt) : 0;
-    u.m = static_cast<int>(r - static_cast<int64_t>(u.split) * mt);
+    u.split = u.job ? r / mt : 0;
+    u.m = r - u.split * mt;
     u.k0 = u.job ? u.split * w.per : 0;
     u.k1 = u.job ? min(u.k0 + w.per, w.steps1) : w.steps0;
     return u;
@@ -219,6 +224,12 @@ __device__ __forceinline__ void store_half8(__half* q, int64_t part, const float
 // A warp's 32 rows of 128 bytes (a lane has a row) to a tensor, by way of its own part of shared memory: as rows of
 // their own they would be stores of 16 bytes to 32 lines at a time, which took the L1 half of its time beside the
 // operands.  What lies outside the tensor is not written.  ADD: onto what is there.
+__device__ __forceinline__ void fill_box(uint8_t* box, const uint32_t (&w)[32]) {
+    const int lane = threadIdx.x % 32;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        store16(box + tc_chunk(lane, j), make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
+}
 template <bool ADD>
 __device__ __forceinline__ void store_box(const CUtensorMap* map, uint8_t* boxes, uint32_t& turn, const uint32_t (&w)[32], int col, int row, int part) {
     const int lane = threadIdx.x % 32;
@@ -226,9 +237,7 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint8_t* boxes
     turn ^= 1u;
     if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");     // the store before the last has left this memory
     __syncwarp();
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        store16(box + tc_chunk(lane, j), make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
+    fill_box(box, w);
     tma_store_fence();
     __syncwarp();
     if (lane == 0) {
@@ -247,7 +256,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
     volatile int* abort = &sh.abort;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_ctarank();
-    const int64_t cluster = blockIdx.x / 2, clusters = gridDim.x / 2;
+    const int cluster = blockIdx.x / 2, clusters = gridDim.x / 2;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -290,7 +299,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
             for (int i = 0; i < kStages; ++i) full0[i] = peer_smem_addr(&sh.full[i], 0);
             int st = 0;
             uint32_t ph = 0;
-            for (int64_t t = 0, i; (i = nth_unit(work, cluster, clusters, t)) >= 0 && !*abort; ++t) {
+            for (int t = 0, i; (i = nth_unit(work, cluster, clusters, t)) >= 0 && !*abort; ++t) {
                 const Unit u = unit_of<P>(work, i);
                 const CUtensorMap* ma = u.job ? &p.a1 : &p.a0;
                 const CUtensorMap* mb = u.job ? &p.b1 : &p.b0;
@@ -347,7 +356,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
             uint32_t ph = 0;
             int turn = 0;
             bool go = true;
-            for (int64_t t = 0, i; go && (i = nth_unit(work, cluster, clusters, t)) >= 0; ++t) {
+            for (int t = 0, i; go && (i = nth_unit(work, cluster, clusters, t)) >= 0; ++t) {
                 const Unit u = unit_of<P>(work, i);
                 const bool a_mn = P == Product::kOut && u.job == 0, b_mn = P == Product::kOut;
                 constexpr uint32_t kBf16 = 1u << 7 | 1u << 10;                          // operand types (else fp16)
@@ -384,7 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
         uint32_t box = 0u;
         int turn = 0;
         bool go = true;
-        for (int64_t t = 0, i; (i = nth_unit(work, cluster, clusters, t)) >= 0; ++t) {
+        for (int t = 0, i; (i = nth_unit(work, cluster, clusters, t)) >= 0; ++t) {
             const Unit u = unit_of<P>(work, i);
             const int rows = sh.rows;
             const int row = u.m * kTile + static_cast<int>(rank) * kHalf + quarter * 32 + lane;
@@ -525,13 +534,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                         else store_box<false>(&p.s1, boxes, box, w, col0 + c, row0, slice);
                     }
                 } else if (!F32 && p.dw_wide) {
+                    // both boxes at once: few tokens make this the whole of a unit's time
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    __syncwarp();
 #pragma unroll
                     for (int c = 0; c < kHalf; c += 64) {
-                        if (col0 + c >= p.D) break;
                         uint32_t w[32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j) w[j] = pack_bf16(acc[c + 2 * j], acc[c + 2 * j + 1]);
-                        store_box<false>(&p.s0, boxes, box, w, col0 + c, row - lane, 0);
+                        fill_box(boxes + c / 64 * kBox, w);
+                    }
+                    tma_store_fence();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (col0 < p.D) tma_store_3d(&p.s0, boxes, col0, row, 0);
+                        if (col0 + 64 < p.D) tma_store_3d(&p.s0, boxes + kBox, col0 + 64, row, 0);
+                        tma_store_commit();
                     }
                 } else if (row < p.Vp) {
                     using T = std::conditional_t<F32, float, __nv_bfloat16>;
@@ -868,7 +886,7 @@ int64_t out_cost(int64_t T, int64_t D, int64_t Vp, int64_t segs, int64_t segs1, 
     const int64_t with_extra = (a / pairs + (extra ? 1 : 0)) * la + (rounds - (extra && rest <= others ? 1 : 0)) * lb;
     const int64_t without = a / pairs * la + ((filled + others - 1) / others + rounds) * lb;
     // a slice of sums more: its bytes out and in again, some 2 MB of them to a step's time (0.3 us at 6.8 TB/s)
-    return std::max(with_extra, without) + splits * (paired ? 2 : 1) * T * D * 8 / (2 << 20);
+    return std::max(with_extra, without) + splits * (paired ? 2 : 1) * round_up(T, kStep) * D * 8 / (2 << 20);
 }
 
 Layout layout(int64_t T, int64_t V, int64_t D, bool f32, bool in_place, bool bwd) {
