@@ -793,7 +793,7 @@ typedef struct {
  *   column twice: their p add up.  A row without weight has a loss of 0 and its logits are not read.
  *   A row with a NaN, or with a logit or entry of +inf, or with logits of -inf alone, has a NaN loss; a
  *   logit of -inf under an entry of some weight an infinite one.
- *   V in 1..SS_DISTILL_MAX_V, K in 0..SS_DISTILL_MAX_K, temperature > 0 and finite.  Sums are fp32.
+ *   V in 1..SS_DISTILL_MAX_V, K in 0..SS_DISTILL_MAX_K, temperature in 1e-30 .. 1e30.  Sums are fp32.
  */
 ss_status ss_distill(const void* logits, const int32_t* ids, const void* teacher, float* loss,
                      int64_t rows, int64_t V, int64_t K, float temperature,

@@ -409,7 +409,7 @@ cudaError_t launch(const DistillParams& p, int cluster, cudaStream_t stream) {
 
 ss_status distill(const float* dloss, const void* logits, const int32_t* ids, const void* teacher, float* loss, void* dlogits, bool grad,
                   int64_t rows, int64_t V, int64_t K, float temperature, const ss_distill_strides* strides, void* stream) {
-    if (rows < 0 || V < 1 || K < 0 || !(temperature > 0.f) || !(temperature < INFINITY)) return SS_ERR_INVALID_ARG;
+    if (rows < 0 || V < 1 || K < 0 || !(temperature >= 1e-30f && temperature <= 1e30f)) return SS_ERR_INVALID_ARG;      // (1 / τ is a normal float)
     if (V > SS_DISTILL_MAX_V || K > SS_DISTILL_MAX_K || rows > INT32_MAX / kMaxCluster) return SS_ERR_UNSUPPORTED;
     ss_distill_strides s;
     if (strides) {

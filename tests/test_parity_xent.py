@@ -81,6 +81,19 @@ def test_pieces_of_the_vocabulary():
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 31, 64, 65, 127, 128, 129, 255])
+def test_few_tokens(io, T):
+    """About 128 tokens the shape of dhidden's product changes: both sides of it, sums in several slices of K."""
+    Case(T, 9001, 320, io, ignored=0.0).check()
+    Case(T, 9001, 320, io, ignored=0.5).check()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_few_tokens_in_pieces_of_the_vocabulary(io):
+    Case(20, 530000, 16, io).check()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
 @pytest.mark.parametrize("pad", [1, 8])
 def test_strides(io, pad):
     c = Case(130, 700, 64, io, pad=pad)

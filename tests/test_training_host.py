@@ -92,6 +92,14 @@ def test_distill_refuses_on_host():
         assert call() == 4 and call(K=0, ids=None, t=None) == 4 and grad() == 4
 
 
+@pytest.mark.parametrize("tau,status", [(1e-31, 1), (1e-39, 1), (1e31, 1), (1e-30, 4), (1e30, 4)])
+def test_distill_refuses_temperatures_without_a_normal_inverse(tau, status):
+    if status == 4 and not _no_gpu():
+        pytest.skip("the pointers are no memory")
+    assert ss.lib().ss_distill(FAKE, FAKE, FAKE, FAKE, 2, 10, 3, tau, None, None) == status
+    assert ss.lib().ss_distill_grad(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 2, 10, 3, tau, None, None) == status
+
+
 def test_linear_xent_refuses_on_host():
     size = ss.lib().ss_linear_xent_workspace_size
 
