@@ -430,7 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_peer(turn & 1 ? empty1 : empty0);
+                if (lane == 0) pair_arrive(turn & 1 ? empty1 : empty0);
             }
             if (!go) break;
             if constexpr (P == Product::kLoss) {

@@ -41,6 +41,12 @@ __device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t (&r)[16]) {
         : "memory");
 }
 
+// One arrival on a barrier of either CTA (its address from peer_smem_addr) after tc_fence_before.  Relaxed: what it
+// hands on is tensor memory, which that fence orders; a release would wait for the thread's stores to memory as well.
+__device__ __forceinline__ void pair_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // TMA tile into this CTA's shared memory, completing on a barrier of either CTA (`bar`: its address in the
 // cluster's window, from peer_smem_addr).
 __device__ __forceinline__ void pair_tma_load(void* dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2) {
