@@ -50,16 +50,17 @@ namespace {
 constexpr int kTile = 256;                        // rows and columns of a pair's tile
 constexpr int kHalf = kTile / 2;                  // rows of a CTA's operand tiles
 constexpr int kStep = 64;                         // of K per stage
-// Stages of operands, and a warp's boxes for what leaves, in 227 KB of shared memory (the loss leaves nothing).
-constexpr int kStagesOf(Product p) { return p == Product::kLoss ? 7 : 5; }
-constexpr int kBoxesOf(Product p) { return p == Product::kLoss ? 0 : 2; }
+// Stages of operands, and a warp's boxes for what leaves, in 227 KB of shared memory.  The loss leaves nothing; dl for few
+// tokens leaves little of what is read, and the more is on its way the better.
+constexpr int kBoxesOf(Product p, Form f) { return p == Product::kLoss ? 0 : p == Product::kGrad && f == Form::kRaw ? 1 : 2; }
+constexpr int kStagesOf(Product p, Form f) { return 7 - kBoxesOf(p, f); }
 constexpr int kMaxStages = 7;
 constexpr uint32_t kOperand = kHalf * kStep * 2;  // bytes of one operand's tile
 constexpr uint32_t kStageBytes = 2 * kOperand;
 constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = (kEpiWarps + 2) * 32;
-// Tiles of rows that share a sweep over the vocabulary (8191 tokens, 2560 x 50257: 16 of them 1.67 ms, 8 or 32 1.70).
-constexpr int kGroup = 16;
+// Tiles of rows that share a sweep over the vocabulary (8191 tokens, 2560 x 50257: 8 of them 1.29 ms, 16 1.25, 32, all, 1.235).
+constexpr int kGroup = 32;
 constexpr uint32_t kAccCols = 256;
 // Steps of K that one accumulator takes before its sums go into registers.  The tensor core cuts each addition of
 // 16 products off at 2^-23 of the sum instead of rounding it, so a long chain is off by its length times half of
@@ -120,7 +121,9 @@ struct GemmShared {
     int abort;
 };
 constexpr uint32_t kBox = 32 * 128;                // bytes of a warp's store: 32 rows of 128
-constexpr size_t gemm_smem(Product p) { return kStagesOf(p) * kStageBytes + kEpiWarps * kBoxesOf(p) * kBox + sizeof(GemmShared) + 1024; }
+constexpr size_t gemm_smem(Product p, Form f) {
+    return kStagesOf(p, f) * kStageBytes + kEpiWarps * kBoxesOf(p, f) * kBox + sizeof(GemmShared) + 1024;
+}
 template <Product P, Form F>
 __device__ __forceinline__ Work make_work(const XentParams& p, int rows, int pairs) {
     Work w = {};
@@ -230,12 +233,12 @@ __device__ __forceinline__ void fill_box(uint8_t* box, const uint32_t (&w)[32]) 
     for (int j = 0; j < 8; ++j)
         store16(box + tc_chunk(lane, j), make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
 }
-template <bool ADD>
+template <bool ADD, int BOXES>
 __device__ __forceinline__ void store_box(const CUtensorMap* map, uint8_t* boxes, uint32_t& turn, const uint32_t (&w)[32], int col, int row, int part) {
     const int lane = threadIdx.x % 32;
     uint8_t* box = boxes + turn * kBox;
-    turn ^= 1u;
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");     // the store before the last has left this memory
+    if (BOXES > 1) turn ^= 1u;
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(BOXES - 1) : "memory");      // the box's last store has left this memory
     __syncwarp();
     fill_box(box, w);
     tma_store_fence();
@@ -249,10 +252,10 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint8_t* boxes
 
 template <Product P, Form F>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xent_gemm_kernel(const __grid_constant__ XentParams p) {
-    constexpr int kStages = kStagesOf(P);
+    constexpr int kStages = kStagesOf(P, F), kBoxes = kBoxesOf(P, F);
     extern __shared__ uint8_t raw[];
     uint8_t* tiles = raw + (1024 - smem_addr(raw) % 1024) % 1024;
-    GemmShared& sh = *reinterpret_cast<GemmShared*>(tiles + kStages * kStageBytes + kEpiWarps * kBoxesOf(P) * kBox);
+    GemmShared& sh = *reinterpret_cast<GemmShared*>(tiles + kStages * kStageBytes + kEpiWarps * kBoxes * kBox);
     volatile int* abort = &sh.abort;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_ctarank();
@@ -389,7 +392,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
         // ---------------------------------------------------------------- accumulators, by eight warps of each CTA
         const int quarter = warp % 4, half = warp / 4;
         const uint32_t empty0 = peer_smem_addr(&sh.acc_empty[0], 0), empty1 = peer_smem_addr(&sh.acc_empty[1], 0);
-        uint8_t* boxes = tiles + kStages * kStageBytes + warp * kBoxesOf(P) * kBox;     // (two, taken in turn)
+        uint8_t* boxes = tiles + kStages * kStageBytes + warp * kBoxes * kBox;     // (taken in turn)
         uint32_t box = 0u;
         int turn = 0;
         bool go = true;
@@ -509,8 +512,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                             }
                         }
                     }
-                    store_box<false>(&p.s0, boxes, box, hi, col0 + c, row - lane, 0);
-                    if constexpr (kDlParts(F) > 1) store_box<false>(&p.s0, boxes, box, lo, col0 + c, row - lane, 1);
+                    store_box<false, kBoxes>(&p.s0, boxes, box, hi, col0 + c, row - lane, 0);
+                    if constexpr (kDlParts(F) > 1) store_box<false, kBoxes>(&p.s0, boxes, box, lo, col0 + c, row - lane, 1);
                 }
             } else {
                 constexpr bool F32 = F == Form::kSplit;
@@ -529,9 +532,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                         uint32_t w[32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(acc[c + j]);
-                        if (!u.job) store_box<false>(&p.s0, boxes, box, w, col0 + c, row - lane, 0);
-                        else if (p.add) store_box<true>(&p.s1, boxes, box, w, col0 + c, row0, slice);
-                        else store_box<false>(&p.s1, boxes, box, w, col0 + c, row0, slice);
+                        if (!u.job) store_box<false, kBoxes>(&p.s0, boxes, box, w, col0 + c, row - lane, 0);
+                        else if (p.add) store_box<true, kBoxes>(&p.s1, boxes, box, w, col0 + c, row0, slice);
+                        else store_box<false, kBoxes>(&p.s1, boxes, box, w, col0 + c, row0, slice);
                     }
                 } else if (!F32 && p.dw_wide) {
                     // both boxes at once: few tokens make this the whole of a unit's time
@@ -990,12 +993,12 @@ cudaError_t launch_gemm_as(const XentParams& p, int64_t units, cudaStream_t stre
     if (e != cudaSuccess) return e;
     int pairs = dev < 64 ? known[dev].load() : 0;
     if (pairs == 0) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(gemm_smem(P)));
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(gemm_smem(P, F)));
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * sm_count());
         cfg.blockDim = dim3(kGemmThreads);
-        cfg.dynamicSmemBytes = gemm_smem(P);
+        cfg.dynamicSmemBytes = gemm_smem(P, F);
         cudaLaunchAttribute at[1];
         at[0].id = cudaLaunchAttributeClusterDimension;
         at[0].val.clusterDim.x = 2;
@@ -1008,7 +1011,7 @@ cudaError_t launch_gemm_as(const XentParams& p, int64_t units, cudaStream_t stre
         if (dev < 64) known[dev].store(pairs);
     }
     const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(pairs, std::max<int64_t>(units, 1)));
-    return launch_chained(kern, dim3(grid), dim3(kGemmThreads), gemm_smem(P), stream, p);
+    return launch_chained(kern, dim3(grid), dim3(kGemmThreads), gemm_smem(P, F), stream, p);
 }
 template <Product P>
 cudaError_t launch_gemm(const XentParams& p, Form form, int64_t units, cudaStream_t stream) {
