@@ -22,8 +22,8 @@
 // the other of two accumulators meanwhile and send results off by TMA.  Measured alone, against 1888 TFLOP/s of a
 // library product: the loss of 8191 tokens, 2560 x 50257, 1.14 ms (1850 TFLOP/s); for 4096 tokens, 2048 x 128000, the
 // loss 1.17 ms (1830), dl 1.17 (1830), both products over it 2.42 (1770).  Behind one another they run at the power
-// limit, some 10% slower.  With few tokens weight's traffic is the bound: the loss of 64 tokens, 2048 x 128000, 99 us (5.3
-// TB/s).  Tiles of 256 x 256 by one CTA each would read twice as much from L2 (some 28 TB/s); stores by the threads
+// limit, some 8% slower.  With few tokens weight's traffic is the bound: 64 tokens, 2048 x 128000, loss 91 us (5.8 TB/s), dl
+// 101, dhidden 83 (6.3), but dweight 131 (524 MB out), whose tiles of one step of K are the chain from accumulator to store.  Tiles of 256 x 256 by one CTA each would read twice as much from L2 (some 28 TB/s); stores by the threads
 // that hold the sums cost 8%, accumulators in local memory (an indexed choice among them) 30%.
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
@@ -96,7 +96,6 @@ struct Pow2x2 {
         b = pow2(n - h);
     }
 };
-
 
 // A unit of work: a tile and a range of steps of K (each of them kSegs products of parts).
 struct Unit {
@@ -843,14 +842,14 @@ using host::meet;
 using host::Range;
 using host::range3;
 
-// Bytes of dl (and of a packed piece of weight) at a time: 4096 tokens, 2048 x 128000 take 5.10 ms with 128 MB, 5.06 with
-// 256, 5.00 with 512 and 4.99 with 2 GB (one piece).  At least kMinPiece columns, however many tokens: below, a piece's
+// Bytes of dl (and of a packed piece of weight) at a time: 4096 tokens, 2048 x 128000 take 4.89 ms with 128 MB, 4.78 with
+// 256, 4.77 with 512 and 4.72 with 2 GB (one piece).  At least kMinPiece columns, however many tokens: below, a piece's
 // sums of dhidden, read and written again, cost as much as its products.
 constexpr int64_t kPieceBytes = 512 << 20;
 constexpr int64_t kMinPiece = 4096;
 constexpr int64_t kMaxSplits = 32;
 // Tokens up to which the backward pass takes bf16 operands as they are.  2048 x 128000, us as they are and in fp16:
-// 64 tokens 457 and 560, 256 tokens 533 and 541, 512 tokens 913 and 760; 768 x 50257: 99 and 113, 115 and 120, 183 and 147.
+// 64 tokens 325 and 468, 256 tokens 513 and 533, 512 tokens 886 and 736; 768 x 50257: 77 and 104, 105 and 113, 173 and 146.
 constexpr int64_t kRawTokens = 256;
 constexpr int64_t kMinSteps = 16;                 // of K to a slice of dhidden's sums
 
