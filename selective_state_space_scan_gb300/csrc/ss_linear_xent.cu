@@ -19,12 +19,13 @@
 // bf16 would take six).
 //
 // One persistent CTA pair per two SMs: a warp that loads (TMA, stages of 2 x 16 KB), one that issues, eight that empty
-// the other of two accumulators meanwhile and send results off by TMA.  Measured alone, against 1888 TFLOP/s of a
-// library product: the loss of 8191 tokens, 2560 x 50257, 1.14 ms (1850 TFLOP/s); for 4096 tokens, 2048 x 128000, the
-// loss 1.17 ms (1830), dl 1.17 (1830), both products over it 2.42 (1770).  Behind one another they run at the power
-// limit, some 8% slower.  With few tokens weight's traffic is the bound: 64 tokens, 2048 x 128000, loss 91 us (5.8 TB/s), dl
-// 101, dhidden 83 (6.3), but dweight 131 (524 MB out), whose tiles of one step of K are the chain from accumulator to store.  Tiles of 256 x 256 by one CTA each would read twice as much from L2 (some 28 TB/s); stores by the threads
-// that hold the sums cost 8%, accumulators in local memory (an indexed choice among them) 30%.
+// the other of two accumulators meanwhile and send results off by TMA.  Launches by themselves, against 1888 TFLOP/s of a
+// library product: the loss of 8191 tokens, 2560 x 50257, 1.07 ms (1980 TFLOP/s); for 3482 tokens, 2048 x 64000 (a piece),
+// dl 0.50 ms (1840), both products over it 1.01 (1810).  Behind one another they run at the power limit, some 15% slower.
+// With few tokens weight's traffic is the bound: 64 tokens, 2048 x 128000, loss 91 us (5.8 TB/s), dl 101, dhidden 83 (6.3),
+// but dweight 131 (524 MB out), whose tiles of one step of K are the chain from accumulator to store.  Tiles of 256 x 256
+// by one CTA each would read twice as much from L2 (some 28 TB/s); stores by the threads that hold the sums cost 8%,
+// accumulators in local memory (an indexed choice among them) 30%.
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
