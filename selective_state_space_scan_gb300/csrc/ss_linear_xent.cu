@@ -537,7 +537,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                         else store_box<false, kBoxes>(&p.s1, boxes, box, w, col0 + c, row0, slice);
                     }
                 } else if (!F32 && p.dw_wide) {
-                    // both boxes at once: few tokens make this the whole of a unit's time
+                    // Both boxes are filled at once: few tokens make this the whole of a unit's time.  Each is a group
+                    // of its own, box 0 the older one, as store_box counts them: the dhidden unit that may follow
+                    // takes box 0 when one group is still pending.
                     if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                     __syncwarp();
 #pragma unroll
@@ -551,9 +553,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                     __syncwarp();
                     if (lane == 0) {
                         if (col0 < p.D) tma_store_3d(&p.s0, boxes, col0, row, 0);
+                        tma_store_commit();
                         if (col0 + 64 < p.D) tma_store_3d(&p.s0, boxes + kBox, col0 + 64, row, 0);
                         tma_store_commit();
                     }
+                    box = 0u;
                 } else if (row < p.Vp) {
                     using T = std::conditional_t<F32, float, __nv_bfloat16>;
                     T* out = static_cast<T*>(p.dw) + static_cast<int64_t>(p.v0 + row) * p.ld_dw + col0;
