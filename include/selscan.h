@@ -758,8 +758,10 @@ ss_status ss_linear_xent(const void* hidden, const void* weight, const int32_t* 
  *   workspace           256-byte aligned, ss_linear_xent_workspace_size(tokens, V, D, io_dtype, 1) bytes
  * Rows without a target have a dhidden of zero and no part in dweight, whatever their hidden, lse and dloss.
  * The logits are computed again, a piece of the vocabulary at a time.  Operands, dl among them, are fp16 scaled by a
- * power of two per tensor, one for bf16 tensors (dl to 11 bits) and two for fp32 ones.  Deterministic.  tokens == 0 sets
- * dweight to zero.  Outputs must not overlap anything else.
+ * power of two, one for bf16 tensors (dl to 11 bits) and two for fp32 ones (22 bits).  The power is the tensor's; dl's is the
+ * token's, from its dloss, so that a token's dhidden is as exact however small its dloss (down to 2^-112) beside the others'.
+ * dl is kept down to 2^-39 of the token's dloss; dweight takes hidden · dloss down to 2^-38 of the largest of either.
+ * Deterministic.  tokens == 0 sets dweight to zero.  Outputs must not overlap anything else.
  */
 ss_status ss_linear_xent_bwd(const float* dloss, const void* hidden, const void* weight,
                              const int32_t* targets, const float* lse, void* dhidden, void* dweight,

@@ -13,7 +13,9 @@
 // Operands.  bf16 logits of the forward pass: as they are.  The backward pass takes bf16 tensors in fp16 as a rule, scaled
 // by one power of two per tensor so that the largest value lies below 2^15: a bf16 value is exact there down to 2^-31 of
 // the largest, and dl has 11 bits instead of bf16's 8 (in bf16 its rounding would add to the gradients' error as much as
-// their own does: 2.9e-3 instead of 1.7e-3).  With few tokens, where the traffic is the bound, it takes them as they
+// their own does: 2.9e-3 instead of 1.7e-3).  dl's power of two is its row's, from the row's dloss, and the rows of hidden
+// that dweight sums over have the rest of it: one power for all would leave a token of dloss 2^-20 beside 1 with no more than
+// a bit of its softmax at 128000 columns.  With few tokens, where the traffic is the bound, it takes them as they
 // are and dl as the sum of two bf16: half more products, but weight is not copied.  A float32 value is the sum of two
 // scaled fp16 (22 bits), and a product the three products of these that count (K three times as long; three parts of
 // bf16 would take six).
@@ -63,6 +65,7 @@ constexpr int kGemmThreads = (kEpiWarps + 2) * 32;
 // Tiles of rows that share a sweep over the vocabulary (8191 tokens, 2560 x 50257: 8 of them 1.29 ms, 16 1.25, 32, all, 1.235).
 constexpr int kGroup = 32;
 constexpr uint32_t kAccCols = 256;
+constexpr unsigned int kInfBits = 0x7f800000u;
 // Steps of K that one accumulator takes before its sums go into registers.  The tensor core cuts each addition of
 // 16 products off at 2^-23 of the sum instead of rounding it, so a long chain is off by its length times half of
 // that, to one side: 560 additions gave a dhidden off by 1e-5, 64 in a row 1e-6.  The registers' own additions
@@ -81,6 +84,13 @@ constexpr int kDlParts(Form f) { return f == Form::kHalf ? 1 : 2; }
 // is left is below 2^15.  2^n and 2^-n are normal floats.
 __device__ __forceinline__ int scale_exp(unsigned int bits) { return min(max(static_cast<int>(bits >> 23) - 127 - 14, -126), 126); }
 __device__ __forceinline__ float pow2(int n) { return __int_as_float((n + 127) << 23); }
+// dl's, a row's own: its dloss sets how large it is, and one dloss may be a small part of another.  dweight sums over
+// the rows, so the rows of hidden that it takes are scaled by what a row's exponent lacks to `most`, that of the largest
+// finite dloss (a dloss that is not finite counts as that one).
+__device__ __forceinline__ int row_exp(float g, int most) { return min(scale_exp(__float_as_uint(g) & 0x7fffffffu), most); }
+// Whether every row's is the largest one's, as with one dloss for all (rows of no dloss aside, whose dl is zero): dweight
+// takes hidden as the logits do then (4096 tokens, 2048 x 128000: 0.8% less than with rows of its own).
+__device__ __forceinline__ bool one_exp(const unsigned int* range) { return scale_exp(kInfBits - range[kRangeL]) >= scale_exp(range[kRangeG]); }
 // weight's, which is packed before its largest value is known: that of values below 2^7, unless they turn out larger or
 // all below 2^-4 (they are packed again then).
 constexpr int kGuess = -7;
@@ -117,6 +127,7 @@ struct GemmShared {
     uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
     Work work;                                    // (here and not in registers, which the accumulators take up)
     int rows, ex, ew, eg;                         // rows that have a target; the operands' scales
+    bool one;                                     // dl has one scale (see one_exp)
     uint32_t tmem;
     int abort;
 };
@@ -285,10 +296,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
         sh.rows = *p.count;
         sh.work = make_work<P, F>(p, sh.rows, clusters);
         sh.ex = sh.ew = sh.eg = 0;                 // (operands as they are)
+        sh.one = true;
         if constexpr (F != Form::kRaw) {
             sh.ex = scale_exp(p.range[kRangeX]);
             sh.ew = weight_exp(p.range[kRangeW + p.piece]);
             if constexpr (P != Product::kLoss) sh.eg = scale_exp(p.range[kRangeG]);
+            if constexpr (P == Product::kOut) sh.one = one_exp(p.range);
         }
     }
     __syncthreads();
@@ -305,7 +318,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
             for (int t = 0, i; (i = nth_unit(work, cluster, clusters, t)) >= 0 && !*abort; ++t) {
                 const Unit u = unit_of<P>(work, i);
                 const CUtensorMap* ma = u.job ? &p.a1 : &p.a0;
-                const CUtensorMap* mb = u.job ? &p.b1 : &p.b0;
+                const CUtensorMap* mb = u.job ? &p.b1 : P == Product::kOut && F != Form::kRaw && !sh.one ? &p.b2 : &p.b0;
                 // dweight: both operands have K (the tokens) along rows; dhidden: weight has K (the vocabulary) along rows
                 const bool a_mn = P == Product::kOut && u.job == 0, b_mn = P == Product::kOut;
                 const bool both = is_paired<P, F>(p, u);
@@ -411,6 +424,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                     g = p.g[row];
                 }
             }
+            if constexpr (P == Product::kOut && F != Form::kRaw) {
+                const int at = is_paired<P, F>(p, u) ? quarter * 32 + lane : row;
+                if (u.job && at < rows) g = p.g[at];
+            }
             float acc[kHalf];                      // a thread has half a row of the tile
 #pragma unroll
             for (int j = 0; j < kHalf; ++j) acc[j] = 0.f;
@@ -474,7 +491,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                 if (row < rows) p.part[(static_cast<int64_t>(p.tile0 + u.n) * 2 + half) * p.ld_part + row] = make_float2(m, s);
             } else if constexpr (P == Product::kGrad) {
                 const bool ok = row < rows, all_ok = __all_sync(0xffffffffu, ok);
-                if constexpr (F != Form::kRaw) g *= pow2(-sh.eg);
+                if constexpr (F != Form::kRaw) g *= pow2(-row_exp(g, sh.eg));
                 const Pow2x2 f(sh.ex + sh.ew);
                 const float2 off = splat2(-lse), f2 = splat2(f.a), l2e = splat2(kLog2e), g2 = splat2(g);
                 if (f.b != 1.f) {
@@ -518,7 +535,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
             } else {
                 constexpr bool F32 = F == Form::kSplit;
                 if constexpr (F != Form::kRaw) {
-                    const Pow2x2 f(sh.eg + (u.job ? sh.ew : sh.ex));
+                    const Pow2x2 f(u.job ? row_exp(g, sh.eg) + sh.ew : sh.eg + sh.ex);
 #pragma unroll
                     for (int j = 0; j < kHalf; ++j) acc[j] = acc[j] * f.a * f.b;
                 }
@@ -584,9 +601,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
 constexpr int kPrepThreads = 256;
 
 // Columns [c, c + 8) of a row as an operand: bf16 as it is (RAW), or fp16 times `scale`, in two parts for fp32.
-// Columns of D and more are zero.
+// Columns of D and more are zero.  `also`: the same times `shift`, another power of two.
 template <typename T, bool RAW>
-__device__ __forceinline__ void pack8(const T* row, __half* out, int64_t part, int c, int D, bool wide, float scale, unsigned int* most = nullptr) {
+__device__ __forceinline__ void pack8(const T* row, __half* out, int64_t part, int c, int D, bool wide, float scale, unsigned int* most = nullptr,
+                                      __half* also = nullptr, float shift = 1.f) {
     float v[8];
     if (wide && c + 8 <= D) {
         if constexpr (sizeof(T) == 2) {
@@ -616,20 +634,25 @@ __device__ __forceinline__ void pack8(const T* row, __half* out, int64_t part, i
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const unsigned int bits = __float_as_uint(v[i]) & 0x7fffffffu;
-                *most = max(*most, bits < 0x7f800000u ? bits : 0u);
+                *most = max(*most, bits < kInfBits ? bits : 0u);
             }
         }
         float2 f[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[i] = make_float2(v[2 * i] * scale, v[2 * i + 1] * scale);
         store_half8<sizeof(T) == 4>(out + c, part, f);
+        if (also) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], splat2(shift));
+            store_half8<sizeof(T) == 4>(also + c, part, f);
+        }
     }
 }
 
 // Magnitudes as bits, whose order is the floats': the larger of m and v's, if that is finite.
 __device__ __forceinline__ unsigned int max_finite(unsigned int m, float v) {
     const unsigned int bits = __float_as_uint(v) & 0x7fffffffu;
-    return max(m, bits < 0x7f800000u ? bits : 0u);
+    return max(m, bits < kInfBits ? bits : 0u);
 }
 // The block's largest to *out.
 __device__ __forceinline__ void block_max(unsigned int m, unsigned int* part, unsigned int* out) {
@@ -643,13 +666,14 @@ __device__ __forceinline__ void block_max(unsigned int m, unsigned int* part, un
     __syncthreads();
 }
 
-// Largest finite magnitudes of hidden's rows with a target and of their dloss; a warp has a row at a time.
+// Largest finite magnitudes of hidden's rows with a target and of their dloss, and the smallest one of dloss but zero; a warp
+// has a row at a time.
 template <typename T>
 __global__ void __launch_bounds__(kPrepThreads) xent_range_kernel(const PrepParams p) {
     __shared__ unsigned int part[kPrepThreads / 32];
     constexpr int kWarps = kPrepThreads / 32, N = 16 / sizeof(T), U = 4;
     const int lane = threadIdx.x % 32, vecs = p.wide ? p.D / N : 0;
-    unsigned int m = 0u, g = 0u;
+    unsigned int m = 0u, g = 0u, l = 0u;
     let_next_start();
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32; t < p.T; t += static_cast<int64_t>(gridDim.x) * kWarps) {
         const int v = p.targets[t];
@@ -670,10 +694,15 @@ __global__ void __launch_bounds__(kPrepThreads) xent_range_kernel(const PrepPara
             }
         }
         for (int c = vecs * N + lane; c < p.D; c += 32) m = max_finite(m, to_f32<T>(row[c]));
-        if (p.dloss && lane == 0) g = max_finite(g, p.dloss[t * p.dloss_t]);
+        if (p.dloss && lane == 0) {
+            const unsigned int one = max_finite(0u, p.dloss[t * p.dloss_t]);
+            g = max(g, one);
+            if (one) l = max(l, kInfBits - one);
+        }
     }
     block_max(m, part, &p.range[kRangeX]);
     block_max(g, part, &p.range[kRangeG]);
+    block_max(l, part, &p.range[kRangeL]);
 }
 
 // The rows that have a target, gathered in order: row i of x is row rows[i] of hidden.  A block has `per` rows of
@@ -682,10 +711,14 @@ template <typename T, bool BWD, bool RAW>
 __global__ void __launch_bounds__(kPrepThreads) xent_gather_kernel(const PrepParams p) {
     constexpr bool F32 = sizeof(T) == 4;
     constexpr int kWarps = kPrepThreads / 32;
+    constexpr bool kScaled = BWD && !RAW;
     __shared__ int before[kWarps], own[kWarps], to[kPrepThreads];
+    __shared__ float shift[kScaled ? kPrepThreads : 1];
+    bool own_rows = false;                         // dweight takes rows of its own
     let_next_start();
     if constexpr (!RAW) wait_for_earlier();        // (else it is the call's first)
     const float scale = RAW ? 1.f : pow2(-scale_exp(p.range[kRangeX]));
+    if constexpr (kScaled) own_rows = !one_exp(p.range);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * p.per;
     const int n = static_cast<int>(min(static_cast<int64_t>(p.per), p.T - first));
@@ -713,8 +746,13 @@ __global__ void __launch_bounds__(kPrepThreads) xent_gather_kernel(const PrepPar
         p.rows[at] = static_cast<int>(t);
         p.tgt[at] = mine;
         if constexpr (BWD) {
+            const float g = p.dloss[t * p.dloss_t];
             p.lse_c[at] = p.lse[t];
-            p.g_c[at] = p.dloss[t * p.dloss_t];
+            p.g_c[at] = g;
+            if constexpr (kScaled) {
+                const int most = scale_exp(p.range[kRangeG]);
+                shift[threadIdx.x] = pow2(max(row_exp(g, most) - most, -126));
+            }
         }
     } else if (static_cast<int>(threadIdx.x) < n) {
         to[threadIdx.x] = -1;
@@ -732,7 +770,7 @@ __global__ void __launch_bounds__(kPrepThreads) xent_gather_kernel(const PrepPar
         if (i >= 0) {
             if (c0 + lane * 8 < p.D)
                 pack8<T, RAW>(static_cast<const T*>(p.hidden) + t * p.hidden_t, p.x + static_cast<int64_t>(i) * p.ld_x, p.x_part, c0 + lane * 8, p.D,
-                              p.wide, scale);
+                              p.wide, scale, nullptr, own_rows ? p.xg + static_cast<int64_t>(i) * p.ld_x : nullptr, own_rows ? shift[r] : 1.f);
         } else if constexpr (BWD) {
             T* d = static_cast<T*>(p.dhidden) + t * p.dhidden_t;
             for (int c = c0 + lane; c < min(c0 + 256, p.D); c += 32) d[c] = from_f32<T>(0.f);
@@ -741,11 +779,12 @@ __global__ void __launch_bounds__(kPrepThreads) xent_gather_kernel(const PrepPar
     if (first + n == p.T) {
         if (threadIdx.x == 0) *p.count = total;
         // the rest of the last step of K over the tokens counts for nothing, but must be finite
+        __half* x = own_rows ? p.xg : p.x;
         const int end = (total + kStep - 1) / kStep * kStep, vecs = static_cast<int>(p.ld_x / 8);
         if (BWD)
             for (int q = 0; q < (F32 ? 2 : 1); ++q)
                 for (int i = threadIdx.x; i < (end - total) * vecs; i += kPrepThreads)
-                    store16(p.x + q * p.x_part + (total + i / vecs) * p.ld_x + i % vecs * 8, make_uint4(0u, 0u, 0u, 0u));
+                    store16(x + q * p.x_part + (total + i / vecs) * p.ld_x + i % vecs * 8, make_uint4(0u, 0u, 0u, 0u));
     }
 }
 
@@ -875,7 +914,7 @@ struct Layout {
     Form form;
     bool packed;                                  // weight, piece by piece
     bool paired;                                  // dhidden: dl's two parts as the rows of a pair's two CTAs
-    size_t count, range, rows, tgt, lse, g, tl, part, x, w, dl, dx, total;
+    size_t count, range, rows, tgt, lse, g, tl, part, x, xg, w, dl, dx, total;
 };
 
 // Time of one launch of both products over a piece, in steps of K, when dhidden's are cut in `splits`: units as
@@ -952,6 +991,7 @@ Layout layout(int64_t T, int64_t V, int64_t D, bool f32, bool in_place, bool bwd
         q.part = take(8 * q.tpad * q.halves);
     }
     q.x = take(2 * q.parts * q.tpad * q.ld_x);
+    if (bwd && q.form != Form::kRaw) q.xg = take(2 * q.parts * q.tpad * q.ld_x);
     if (packed) q.w = take(2 * q.parts * q.piece * q.ld_x);
     if (bwd) {
         q.dl = take(2 * q.dl_parts * q.tpad * q.ld_dl);
@@ -1104,6 +1144,7 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
     char* ws = static_cast<char*>(workspace);
     auto f32_at = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
     __half* x = reinterpret_cast<__half*>(ws + q.x);
+    __half* xg = reinterpret_cast<__half*>(ws + q.xg);
     __half* w = reinterpret_cast<__half*>(ws + q.w);
     __half* dl = reinterpret_cast<__half*>(ws + q.dl);
     const int64_t x_part = q.tpad * q.ld_x, w_part = q.piece * q.ld_x, dl_part = q.tpad * q.ld_dl;
@@ -1113,7 +1154,7 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
     std::memset(&g, 0, sizeof(g));
     g.hidden = c.hidden; g.hidden_t = s.hidden_t; g.targets = c.targets; g.T = T; g.V = V; g.D = static_cast<int>(D);
     g.per = static_cast<int>(std::min<int64_t>(kPrepThreads, std::max<int64_t>(1, T / 1024)));
-    g.x = x; g.ld_x = q.ld_x; g.x_part = x_part; g.wide = wide(c.hidden, T > 1 ? s.hidden_t : 0);
+    g.x = x; g.xg = xg; g.ld_x = q.ld_x; g.x_part = x_part; g.wide = wide(c.hidden, T > 1 ? s.hidden_t : 0);
     g.count = reinterpret_cast<int*>(ws + q.count); g.rows = reinterpret_cast<int*>(ws + q.rows); g.tgt = reinterpret_cast<int*>(ws + q.tgt);
     g.lse = c.lse_in; g.dloss = c.dloss; g.dloss_t = s.dloss_t; g.lse_c = f32_at(q.lse); g.g_c = f32_at(q.g);
     g.dhidden = c.dhidden; g.dhidden_t = s.dhidden_t; g.loss_out = c.loss; g.lse_out = c.lse;
@@ -1181,6 +1222,7 @@ ss_status xent(const Call& c, int64_t T, int64_t V, int64_t D, const ss_xent_str
         // dweight: dl and x with the tokens along rows; dhidden: dl with K along columns, weight with K along rows
         char* dw = static_cast<char*>(c.dweight) + v0 * s.dweight_v * es;
         if (!make_map(&p.a0, dl, 2, Vp, rows, q.dl_parts, q.ld_dl, dl_part, kStep) || !make_map(&p.b0, x, 2, D, rows, q.parts, q.ld_x, x_part, kStep) ||
+            (!raw && !make_map(&p.b2, xg, 2, D, rows, q.parts, q.ld_x, x_part, kStep)) ||
             !make_map(&p.a1, dl, 2, Vp, rows, q.dl_parts, q.ld_dl, dl_part, kHalf) || !make_map(&p.b1, wp, 2, D, Vp, q.parts, ld_w, w_part, kStep) ||
             !make_map(&p.s1, p.dx, 4, D, rows, q.slices, q.ld_dx, p.dx_split, 32) ||
             (p.dw_wide && !make_map(&p.s0, dw, es, D, Vp, 1, s.dweight_v, 0, 32)))

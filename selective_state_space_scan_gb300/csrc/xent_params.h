@@ -18,11 +18,13 @@ enum class Product { kLoss, kGrad, kOut };
 enum class Form { kRaw, kHalf, kSplit };
 
 // Largest finite magnitudes that the scales follow from; weight has one for each piece of the vocabulary.
-enum { kRangeX = 0, kRangeG = 1, kRangeW = 2 };
+// kRangeL: the smallest one of dloss but zero, as its distance from infinity's bits.
+enum { kRangeX = 0, kRangeG = 1, kRangeL = 2, kRangeW = 3 };
 
 struct XentParams {
     // operands of the products as [part][row][col]; kOut's second product has the maps a1 and b1
     CUtensorMap a0, b0, a1, b1;
+    CUtensorMap b2;             // kOut: hidden with the rows' shares of dloss, for dweight where these are unlike
     CUtensorMap s0, s1;         // where results go: dl (kGrad), dweight's rows of the piece and dhidden's sums (kOut)
     const int* count;           // rows that have a target
     const int* tgt;             // [count] their targets
@@ -56,6 +58,7 @@ struct PrepParams {
     int D, per;
     bool wide;                  // rows of hidden begin on 16-byte boundaries
     __half* x;                  // [part][row][ld_x] (bf16 where the operands are raw)
+    __half* xg;                 // backward, scaled operands: the same times the rows' shares of the largest dloss, where these are unlike
     int64_t ld_x, x_part;
     int* count;
     int* rows;                  // [count] row of hidden
