@@ -8,7 +8,8 @@
 namespace selscan {
 namespace {
 
-__global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restrict__ part, int n, int64_t ld, int cols, int split,
+// (part is not restrict: the kernel before still writes it when this one comes up)
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float* part, int n, int64_t ld, int cols, int split,
                                                           float* out0, float* out1) {
     __shared__ float s[32][33];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, j = blockIdx.x * 32 + lane;
