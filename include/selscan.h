@@ -742,7 +742,8 @@ typedef struct {
  *                       word and is none either.
  *   workspace           256-byte aligned, ss_linear_xent_workspace_size(tokens, V, D, io_dtype, 0) bytes
  * Sums are fp32.  Products take bf16 operands as they are and fp32 ones as sums of two fp16, scaled by a power
- * of two per tensor (22 bits, and 2^-39 of the tensor's largest finite value at least).  A row with a NaN or an infinity has a NaN or infinite loss, without effect on others.
+ * of two per tensor: 22 bits, and to 2^-39 of the largest finite value of hidden, to 2^-28 of weight's (2^-39 where that
+ * is below 2^-4 or 2^7 and above).  A row with a NaN or an infinity has a NaN or infinite loss, without effect on others.
  * tokens, V and D up to SS_XENT_MAX_*.  strides NULL: fp32, contiguous.
  */
 ss_status ss_linear_xent(const void* hidden, const void* weight, const int32_t* targets, float* loss,
@@ -758,7 +759,8 @@ ss_status ss_linear_xent(const void* hidden, const void* weight, const int32_t* 
  *   workspace           256-byte aligned, ss_linear_xent_workspace_size(tokens, V, D, io_dtype, 1) bytes
  * Rows without a target have a dhidden of zero and no part in dweight, whatever their hidden, lse and dloss.
  * The logits are computed again, a piece of the vocabulary at a time.  Operands, dl among them, are fp16 scaled by a
- * power of two, one for bf16 tensors (dl to 11 bits) and two for fp32 ones (22 bits).  The power is the tensor's; dl's is the
+ * power of two, one for bf16 tensors (dl to 11 bits; up to 256 tokens bf16 as it is, and dl as two) and two for fp32 ones
+ * (22 bits), all of them to the same parts of the tensor's largest value as above.  The power is the tensor's; dl's is the
  * token's, from its dloss, so that a token's dhidden is as exact however small its dloss (down to 2^-112) beside the others'.
  * dl is kept down to 2^-39 of the token's dloss; dweight takes hidden · dloss down to 2^-38 of the largest of either.
  * Deterministic.  tokens == 0 sets dweight to zero.  Outputs must not overlap anything else.

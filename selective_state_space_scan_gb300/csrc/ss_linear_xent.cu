@@ -11,8 +11,7 @@
 //              kPieceBytes of it), then both products over it in one launch: dweight's rows of the piece, whole, and
 //              dhidden as sums in fp32 that grow from piece to piece
 // Operands.  bf16 logits of the forward pass: as they are.  The backward pass takes bf16 tensors in fp16 as a rule, scaled
-// by one power of two per tensor so that the largest value lies below 2^15: a bf16 value is exact there down to 2^-31 of
-// the largest, and dl has 11 bits instead of bf16's 8 (in bf16 its rounding would add to the gradients' error as much as
+// by one power of two per tensor so that the largest value lies below 2^15, and dl has 11 bits instead of bf16's 8 (in bf16 its rounding would add to the gradients' error as much as
 // their own does: 2.9e-3 instead of 1.7e-3).  dl's power of two is its row's, from the row's dloss, and the rows of hidden
 // that dweight sums over have the rest of it: one power for all would leave a token of dloss 2^-20 beside 1 with no more than
 // a bit of its softmax at 128000 columns.  With few tokens, where the traffic is the bound, it takes them as they
@@ -93,6 +92,9 @@ __device__ __forceinline__ int row_exp(float g, int most) { return min(scale_exp
 __device__ __forceinline__ bool one_exp(const unsigned int* range) { return scale_exp(kInfBits - range[kRangeL]) >= scale_exp(range[kRangeG]); }
 // weight's, which is packed before its largest value is known: that of values below 2^7, unless they turn out larger or
 // all below 2^-4 (they are packed again then).
+// What is kept: fp16 ends at steps of 2^-24, so a tensor scaled by its own largest value (2^14 and more) is off by 2^-39 of
+// that at most, and bf16 is exact down to 2^-31 of it; weights scaled by the guess (the largest 2^3 or more) by 2^-28, and
+// exact down to 2^-20.
 constexpr int kGuess = -7;
 __device__ __forceinline__ int weight_exp(unsigned int bits) {
     const int e = static_cast<int>(bits >> 23) - 127;

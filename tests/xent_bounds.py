@@ -21,8 +21,9 @@ def _abs_product(a, b):
     return 1.01 * torch.matmul(a.abs().float(), b.abs().float()).double()
 
 
-def gradients(h, w, t, g):
-    """The definition in doubles: dict of dhidden, dweight and their bounds (rows without a target: zeros)."""
+def gradients(h, w, t, g, w_kept=2.0 ** -28):
+    """The definition in doubles: dict of dhidden, dweight and their bounds (rows without a target: zeros).  w_kept: what
+    weights are off by besides, as a part of the largest."""
     T, D = h.shape
     f32 = h.dtype is torch.float32
     u = 2.0 ** -22 if f32 else 2.0 ** -11 if T > 256 else 2.0 ** -16
@@ -35,7 +36,7 @@ def gradients(h, w, t, g):
     dw, bw = torch.zeros_like(wd), torch.zeros_like(wd)
     steps = D / 16 * (6 if f32 else 1) + 16
     q_all = 4 * steps * 2.0 ** -23 * hd.norm(dim=1) * wd.norm(dim=1).max() + 2.0 ** -20
-    w_floor = 2.0 ** -28 * float(wd.abs().max())
+    w_floor = w_kept * float(wd.abs().max())
     x_most, g_most = (float(hd[rows].abs().max()), float(gd[rows].abs().max())) if len(rows) else (0.0, 0.0)
     for i in range(0, len(rows), CHUNK):
         r = rows[i:i + CHUNK]
