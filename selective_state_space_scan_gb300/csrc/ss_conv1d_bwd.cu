@@ -10,7 +10,9 @@
 // 173; loads into registers, the next steps' ahead, 315); 8 x 2048 x 1536 fp32: 56 us, 0.80; 45 steps: 6 us and 3 for the sums.
 // It runs three steps past its segment, whose g belong to its last outputs.  The weight's gradients are sums in
 // registers; every thread leaves its own in the workspace (a row of it per segment) and a second kernel adds the
-// rows up in the same order every time.  Layouts that TMA does not take go by plain loads.
+// rows up in the same order every time.  Layouts that TMA does not take (rows or bases off 16 bytes) go by plain loads of
+// single elements: 4 x 8192 x 5119 bf16 437 us, 0.34 of the copy rate; 5120 with x one element off 340; 8 x 2048 x 1535 fp32
+// 65 us, 0.69.
 #include <cuda_runtime.h>
 
 #include <algorithm>

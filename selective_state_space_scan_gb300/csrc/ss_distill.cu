@@ -5,9 +5,12 @@
 //
 // The vocabulary is the traffic, and it is read once: a row is shared out to the CTAs of a cluster so that each
 // keeps its slice (64 KB) in shared memory from the running maximum and sum to the gradient.  Bulk copies bring it,
-// three CTAs to an SM, so that an SM has some 190 KB under way or in use while its CTAs are at different points of their
+// three CTAs to an SM while a slice has no more than 64256 bytes (the entries' arrays take 12.5 KB besides; larger ones
+// leave two), so that an SM has some 190 KB under way or in use while its CTAs are at different points of their
 // chain (entries, row, exchange of the sums, stores: some 11 us), and each CTA has a later one's slice fetched into L2.
-// 4096 rows of 128000 bf16: 352 us, 5.7 TB/s, 0.84 of the copy rate.  Measured besides: without the fetch ahead 370 (one
+// 4096 rows with 64 entries each, bf16: 128000 columns 376 us, 0.82 of the copy rate; 129280 502 and 131072 484, 0.62 and 0.65,
+// as 65536 (0.64) and other slices of 64 KB; 2048 rows of 64000 and of 65536 fp32: 184 and 234 us.
+// With a tenth of the rows without entries 352 us, 5.7 TB/s, 0.84.  Measured besides: without the fetch ahead 370 (one
 // CTA of an SM further 361, four 414), slices of 32 KB in registers 663, of 32 KB in shared memory 438 (against 390 then),
 // clusters that take rows in turn with the next one on its way 522, the cluster's own barrier for the exchange 428 (it
 // waits for stores).  What of a longer row does not fit is read again from L2.  An entry's values lie in shared memory as

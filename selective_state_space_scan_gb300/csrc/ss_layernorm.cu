@@ -11,6 +11,8 @@
 // leaves its own in the workspace and a second kernel adds them up, in the same order every time.
 // 32768 rows of 2560, bf16 with an fp32 residual: forward 147 us for 1.0 GB, backward 197 us for 1.34 GB, both at the
 // copy rate, the sums 5 us.  64 rows of 768: 3.5 us each, the launch and a few trips to memory.
+// Rows or bases off 16 bytes, and widths that are no whole runs, are read and written by single elements: 32768 rows of 2559
+// 325 and 318 us (2560 through the binding 156 and 209); bf16 alone, without a residual, 261 and 276 (105 and 136).
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -578,6 +578,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) xen
                     }
                     box = 0u;
                 } else if (row < p.Vp) {
+                    // (rows off 16 bytes, which TMA does not store: a lane has a row, element by element.  64 tokens,
+                    // 2047 x 128000: the backward pass 3.5 ms in bf16 and 2.8 in fp32, against 0.32 and 1.0 at 2048)
                     using T = std::conditional_t<F32, float, __nv_bfloat16>;
                     T* out = static_cast<T*>(p.dw) + static_cast<int64_t>(p.v0 + row) * p.ld_dw + col0;
 #pragma unroll
