@@ -11,13 +11,13 @@
 //              kPieceBytes of it), then both products over it in one launch: dweight's rows of the piece, whole, and
 //              dhidden as sums in fp32 that grow from piece to piece
 // Operands.  bf16 logits of the forward pass: as they are.  The backward pass takes bf16 tensors in fp16 as a rule, scaled
-// by one power of two per tensor so that the largest value lies below 2^15, and dl has 11 bits instead of bf16's 8 (in bf16 its rounding would add to the gradients' error as much as
-// their own does: 2.9e-3 instead of 1.7e-3).  dl's power of two is its row's, from the row's dloss, and the rows of hidden
-// that dweight sums over have the rest of it: one power for all would leave a token of dloss 2^-20 beside 1 with no more than
-// a bit of its softmax at 128000 columns.  With few tokens, where the traffic is the bound, it takes them as they
-// are and dl as the sum of two bf16: half more products, but weight is not copied.  A float32 value is the sum of two
-// scaled fp16 (22 bits), and a product the three products of these that count (K three times as long; three parts of
-// bf16 would take six).
+// by one power of two per tensor so that the largest value lies below 2^15, and dl has 11 bits instead of bf16's 8 (in bf16
+// its rounding would add to the gradients' error as much as their own does: 2.9e-3 instead of 1.7e-3).  dl's power of two is
+// its row's, from the row's dloss, and the rows of hidden that dweight sums over have the rest of it: one power for all would
+// leave a token of dloss 2^-20 beside 1 with no more than a bit of its softmax at 128000 columns.  With few tokens, where the
+// traffic is the bound, it takes bf16 tensors as they are and dl as the sum of two bf16: half more products, but weight is
+// not copied.  A float32 value is the sum of two scaled fp16 (22 bits), and a product the three products of these that count
+// (K three times as long; three parts of bf16 would take six).
 //
 // One persistent CTA pair per two SMs: a warp that loads (TMA, stages of 2 x 16 KB), one that issues, eight that empty
 // the other of two accumulators meanwhile and send results off by TMA.  Launches by themselves, against 1888 TFLOP/s of a
