@@ -85,3 +85,26 @@ def test_a_dloss_that_is_not_finite_stays_in_its_row(io, bad):
     got = ss.ss_linear_xent_bwd(dloss, h, w, t, lse)["dhidden"]
     keep = torch.arange(300) != 7
     assert torch.equal(got[keep], want[keep]) and not torch.isfinite(got[7]).any()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_replayed_with_another_kind_of_dloss(io):
+    """Captured while dloss is one value, replayed with values far apart, and back: what dweight takes follows the device's values."""
+    dt = torch.bfloat16 if io == "bf16" else torch.float32
+    g = torch.Generator("cuda").manual_seed(8)
+    h, w = torch.randn(400, 96, generator=g, device="cuda").to(dt), (0.2 * torch.randn(1500, 96, generator=g, device="cuda")).to(dt)
+    t = torch.randint(-1, 1500, (400,), generator=g, device="cuda", dtype=torch.int32)
+    one = torch.full((400,), 0.25, device="cuda")
+    apart = torch.exp2(-30 * torch.rand(400, generator=g, device="cuda"))
+    loss, lse = ss.ss_linear_xent(h, w, t)
+    want = [ss.ss_linear_xent_bwd(v, h, w, t, lse) for v in (one, apart)]
+    dloss = one.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = ss.ss_linear_xent_bwd(dloss, h, w, t, lse)
+    for k in (0, 1, 1, 0):
+        dloss.copy_((one, apart)[k])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got["dhidden"], want[k]["dhidden"]) and torch.equal(got["dweight"], want[k]["dweight"])
